@@ -151,7 +151,8 @@ enum lowbit_dtype {
   LOWBIT_I8 = 3,    /* int8 with a float scale: value = scale * q             */
   LOWBIT_SIGN1 = 4, /* packed sign bits, K/8 bytes per row, bit k%8 of byte
                        k/8 (LSB first); bit 1 means -alpha, 0 means +alpha     */
-  LOWBIT_I32 = 5    /* int32 output of the exact integer paths               */
+  LOWBIT_I32 = 5,   /* int32 output of the exact integer paths               */
+  LOWBIT_MXFP4 = 6  /* packed MXFP4 activations (lowbit_gemm_mxfp4 only)     */
 };
 
 /* ABI version of the loaded library (LOWBIT_ABI_VERSION).  Library
@@ -384,6 +385,145 @@ int lowbit_rotate_act(int64_t M, int64_t K, const uint16_t* X_bf16, const int8_t
  * beside the decode kernels.  src 16-byte aligned, out 4-byte aligned.
  * Errors: E_NULL, E_SHAPE, E_ALIGN, E_HIP. */
 int lowbit_hbm_read_probe(const void* src, int64_t bytes, uint32_t* out, void* stream);
+
+/* =====================  MXFP4  ===========================================
+ * Matrices in the OCP microscaling format MXFP4: every 32 consecutive values
+ * of a row share one power of two 2^e (E8M0: the byte e + 127; 255 is NaN)
+ * and each value is an e2m1 code (bit 3 the sign, magnitudes 0, 0.5, 1, 1.5,
+ * 2, 3, 4, 6), 4.25 bits a value.  Not from the pages: the 4-bit format that
+ * gfx950's matrix cores take directly, for the layers that one or two bits
+ * lose too much of, with lowbit_gemm's meaning of W, X and Y.
+ *
+ * Packed layout.  Rows in row-blocks of 16 (NB = ceil(rows/16)), k in groups
+ * of 128 (G = ceil(K/128)), groups in quads (GQ = ceil(G/4)); lane L = r + 16 q
+ * owns row r = n % 16 and block q of a group, k = 128 g + 32 q + i.
+ *   code byte  ((rb * G + g) * 64 + L) * 16 + i/2 holds values i (low nibble)
+ *              and i + 1 for even i;                       NB * G * 1024 bytes
+ *   scale byte ((rb * GQ + g/4) * 64 + L) * 4 + g % 4;    NB * GQ * 256 bytes
+ * Padding rows, blocks and groups hold codes 0 and scale 127.
+ * ====================================================================== */
+
+/* Bytes of the packed code and scale buffers of a rows x K matrix (K a
+ * positive multiple of 32; rows, K <= 2^30, rows * K <= 2^38).  Host-only.
+ * Errors: E_NULL, E_SHAPE. */
+int lowbit_mxfp4_bytes(int64_t rows, int64_t K, size_t* code_bytes, size_t* scale_bytes);
+
+/* Row-major MXFP4 (codes [rows][K/2], two values a byte with the even k in the
+ * low nibble; scales [rows][K/32]) into the packed layout, every byte of it
+ * (padding included).  codes, pcodes and pscales 16-byte aligned.
+ * Errors: E_NULL, E_SHAPE, E_ALIGN, E_HIP. */
+int lowbit_pack_mxfp4(int64_t rows, int64_t K, const uint8_t* codes, const uint8_t* scales,
+                      void* pcodes, void* pscales, void* stream);
+
+/* Quantizes X [rows][K] (x_dtype F32 or BF16, rows x_stride elements apart)
+ * into the packed layout: per block a = max |x|, e = max(floor(log2 a) - 2,
+ * -127), codes x / 2^e rounded to nearest even and limited to 6; a zero block
+ * has e = -127; a block that holds an infinity or a NaN has scale 255 and
+ * codes 0, so every product that reads it is NaN.  values, if not NULL,
+ * receives what the codes stand for, [rows][K] in x_dtype.  Weights (once) and
+ * activations (per call) alike.  X, pcodes, pscales, values 16-byte aligned,
+ * x_stride >= K and rows 16-byte aligned.
+ * Errors: E_NULL, E_UNSUPPORTED, E_SHAPE, E_ALIGN, E_HIP. */
+int lowbit_quantize_mxfp4(int64_t rows, int64_t K, int x_dtype, const void* X, int64_t x_stride,
+                          void* pcodes, void* pscales, void* values, void* stream);
+
+/* Y[m][n] = sum_k W[n][k] X[m][k], W MXFP4, for any M >= 1 (one token to
+ * whole prompts), fp32 accumulation, Y [M][N] in y_dtype F32 or BF16.
+ *   x_dtype BF16: X bf16, rows x_stride elements apart (>= K, a multiple of
+ *     8); the products of each pair are exact in fp32.  Weights below 2^-126
+ *     in magnitude may count as 0.
+ *   x_dtype MXFP4: X packed codes and x_pscales its packed scales
+ *     (lowbit_quantize_mxfp4 of the M x K activations); x_stride ignored.
+ * Uses no workspace.  All pointers 16-byte aligned.  N <= 2^26,
+ * ceil(M/128) * ceil(N/128) <= 2^23.
+ * Errors: E_NULL, E_UNSUPPORTED, E_SHAPE, E_ALIGN, E_HIP. */
+int lowbit_gemm_mxfp4(int64_t M, int64_t N, int64_t K, const void* pcodes, const void* pscales,
+                      int x_dtype, const void* X, int64_t x_stride, const void* x_pscales, int y_dtype,
+                      void* Y, void* stream);
+
+/* =====================  8-bit paged cache and attention  ==================
+ * Between the q/k/v and the o product of a layer ([XH] section "ローカル27Bを
+ * 阻む第一の壁：「1語生成するたびに全身を運び直す」": what a token re-reads):
+ * keys and values as e4m3 codes in pages of 16, 32, 64 or 128 tokens, one
+ * power of two per page and head for the keys and one for the values (bytes
+ * e + 127).  Head sizes 64, 128, 256.
+ *   k_codes  [n_pages][kv_heads][page_tokens][head_dim]
+ *   v_codes  [n_pages][kv_heads][head_dim][page_tokens]   (transposed)
+ *   k_scales, v_scales  [n_pages][kv_heads]
+ * All memory is the caller's. */
+typedef struct lowbit_kv8 {
+  int64_t n_pages;
+  int page_tokens, kv_heads, head_dim;
+  void* k_codes;      /* 16-byte aligned */
+  void* v_codes;      /* 16-byte aligned */
+  uint8_t* k_scales;
+  uint8_t* v_scales;
+} lowbit_kv8;
+
+/* The sequences of one call.  Sequence b holds kv_lens[b] tokens, the call's
+ * new ones last; token t lies in page page_table[b][t /
+ * page_tokens].  Its new tokens are rows q_starts[b] .. q_starts[b + 1] - 1 of
+ * the queries (keys, values); q_starts NULL: max_q rows each, in order.
+ * max_q and max_kv bound the new tokens and the lengths of any one sequence;
+ * they size the launch, so keep them close.  The arrays are read on the
+ * device when the call runs (a graph's replay sees their new contents).  What
+ * they hold can not lead a kernel outside the buffers: lengths are cut to
+ * max_kv, rows to total_q and max_q, and tokens in a page whose index is not
+ * in 0 .. n_pages - 1 are not written and not seen, counted in *bad_pages
+ * (device int32, atomically added, once or more for each; not cleared; NULL
+ * to skip).  A sequence may be empty (length 0 or no new tokens). */
+typedef struct lowbit_kv8_batch {
+  int64_t n_seqs;
+  const int32_t* page_table; /* device [n_seqs][table_width] */
+  int64_t table_width;
+  const int32_t* kv_lens;    /* device [n_seqs] */
+  const int32_t* q_starts;   /* device [n_seqs + 1], or NULL */
+  int64_t total_q;           /* rows in all (q_starts NULL: n_seqs * max_q) */
+  int64_t max_q;
+  int64_t max_kv;            /* at most table_width * page_tokens */
+  int32_t* bad_pages;        /* device, or NULL */
+} lowbit_kv8_batch;
+
+/* Writes the new tokens' keys and values (dtype BF16 or F32, [total_q]
+ * [kv_heads][head_dim] with tokens k_stride / v_stride elements apart, so they
+ * may lie in a fused projection's output) into the cache.  Per page and head:
+ * e(a) = the smallest e >= -127 with a <= 448 2^e, a the largest finite
+ * magnitude of the page's new tokens; a page that already holds tokens of the
+ * sequence keeps e = max(e_old, e(a)), and where that rises its earlier codes
+ * are rescaled (times 2^(e_old - e), rounded to nearest even: exact above
+ * e4m3's subnormal range).  code = x / 2^e to nearest even, infinities to
+ * +-448, NaN to NaN.  Bytes behind a sequence's last token stay as they were.
+ * A page that receives tokens must belong to one sequence of the batch (full
+ * pages may be shared by any number).  Writing the same tokens again changes
+ * nothing.  K, V 16-byte aligned, rows 16-byte aligned.
+ * Errors: E_NULL, E_UNSUPPORTED (dtype, page_tokens, head_dim), E_SHAPE,
+ * E_ALIGN, E_HIP. */
+int lowbit_kv8_append(const lowbit_kv8* cache, const lowbit_kv8_batch* batch, int dtype, const void* K,
+                      const void* V, int64_t k_stride, int64_t v_stride, void* stream);
+
+/* O = softmax(softmax_scale Q K^T) V over the cache: query row i of sequence b
+ * stands at position p = kv_lens[b] - (new tokens) + i and sees tokens
+ * j < kv_lens[b] with j <= p (causal != 0) and j > p - window (window > 0).
+ * Q [total_q][q_heads][head_dim] bf16, q_heads a multiple of kv_heads (head h
+ * reads key head h / (q_heads / kv_heads)), tokens q_stride elements apart; O
+ * likewise, o_stride apart.  lse, if not NULL, receives [total_q][q_heads] the
+ * natural logarithm of the softmax sum.  A row that sees no token gets O = 0
+ * and lse = -infinity; what lies in tokens a row does not see (NaN codes too)
+ * does not reach it.  With causal == 0 the cache may hold another sequence (an
+ * encoder's states) of its own length.  Weights times 2^e enter the second
+ * product rounded to bf16; sums and statistics are fp32.  Results do not
+ * depend on the order in which workgroups run.  Rows of sequences behind the
+ * last q_starts entry are not written.
+ * Q, O 16-byte aligned, strides multiples of 8.  Uses the stream's workspace
+ * (lowbit_attention_kv8_workspace bytes) as lowbit_gemv does; reserve it
+ * before a capture.
+ * Errors: E_NULL, E_UNSUPPORTED (page_tokens, head_dim, softmax_scale not
+ * finite), E_SHAPE, E_ALIGN, E_NOMEM, E_HIP. */
+int lowbit_attention_kv8(const lowbit_kv8* cache, const lowbit_kv8_batch* batch, int64_t q_heads,
+                         const uint16_t* Q_bf16, int64_t q_stride, float softmax_scale, int causal,
+                         int64_t window, uint16_t* O_bf16, int64_t o_stride, float* lse, void* stream);
+int lowbit_attention_kv8_workspace(const lowbit_kv8* cache, const lowbit_kv8_batch* batch, int64_t q_heads,
+                                   size_t* bytes);
 
 #ifdef __cplusplus
 }

@@ -9,7 +9,8 @@ CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_lib")
 OBJ_DIR = os.path.join(OUT_DIR, "obj")
 LIB = os.path.join(OUT_DIR, "liblowbit.so")
-SOURCES = ["api.cpp", "pack.hip", "stage.hip", "gemv.hip", "gemm.hip", "probe.hip", "quant.hip"]
+SOURCES = ["api.cpp", "pack.hip", "stage.hip", "gemv.hip", "gemm.hip", "probe.hip", "quant.hip",
+           "mx.hip", "mx_gemm.hip", "kv8.hip", "attn.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

@@ -10,6 +10,7 @@
 
 #include "../../include/lowbit.h"
 #include "common.hpp"
+#include "kv8.hpp"
 
 using namespace lowbit;
 
@@ -472,3 +473,179 @@ int lowbit_rotate_act(int64_t M, int64_t K, const uint16_t* X_bf16, const int8_t
   return hip_status(launch_rotate_act(M, K, X_bf16, signs, X_rot, (hipStream_t)stream));
 }
 
+
+// ------------------------------------------------ MXFP4 and the 8-bit cache
+
+namespace {
+
+// rows x K of an MXFP4 matrix: sizes far from overflow and within one grid
+bool mx_shape_ok(int64_t rows, int64_t K) {
+  return rows >= 1 && K >= kMxBlock && K % kMxBlock == 0 && rows <= (int64_t(1) << 30) &&
+         K <= (int64_t(1) << 30) && rows <= (int64_t(1) << 38) / K;
+}
+
+}  // namespace
+
+int lowbit_mxfp4_bytes(int64_t rows, int64_t K, size_t* code_bytes, size_t* scale_bytes) {
+  if (!code_bytes || !scale_bytes) return LOWBIT_E_NULL;
+  if (!mx_shape_ok(rows, K)) return LOWBIT_E_SHAPE;
+  *code_bytes = (size_t)(cdiv(rows, 16) * mx_groups(K) * 1024);
+  *scale_bytes = (size_t)(cdiv(rows, 16) * mx_quads(K) * 256);
+  return LOWBIT_OK;
+}
+
+int lowbit_pack_mxfp4(int64_t rows, int64_t K, const uint8_t* codes, const uint8_t* scales, void* pcodes,
+                      void* pscales, void* stream) {
+  if (!codes || !scales || !pcodes || !pscales) return LOWBIT_E_NULL;
+  if (!mx_shape_ok(rows, K)) return LOWBIT_E_SHAPE;
+  if (!aligned(codes, 16) || !aligned(pcodes, 16) || !aligned(pscales, 16)) return LOWBIT_E_ALIGN;
+  return hip_status(launch_pack_mxfp4(rows, K, codes, scales, pcodes, pscales, (hipStream_t)stream));
+}
+
+int lowbit_quantize_mxfp4(int64_t rows, int64_t K, int x_dtype, const void* X, int64_t x_stride, void* pcodes,
+                          void* pscales, void* values, void* stream) {
+  if (!X || !pcodes || !pscales) return LOWBIT_E_NULL;
+  if (x_dtype != LOWBIT_F32 && x_dtype != LOWBIT_BF16) return LOWBIT_E_UNSUPPORTED;
+  if (!mx_shape_ok(rows, K)) return LOWBIT_E_SHAPE;
+  if (x_stride < K || x_stride > (int64_t(1) << 40)) return LOWBIT_E_SHAPE;
+  const bool f32 = x_dtype == LOWBIT_F32;
+  if (!aligned(X, 16) || x_stride % (f32 ? 4 : 8) != 0 || !aligned(pcodes, 16) || !aligned(pscales, 16) ||
+      (values && !aligned(values, 16)))
+    return LOWBIT_E_ALIGN;
+  return hip_status(
+      launch_quantize_mxfp4(rows, K, f32, X, x_stride, pcodes, pscales, values, (hipStream_t)stream));
+}
+
+int lowbit_gemm_mxfp4(int64_t M, int64_t N, int64_t K, const void* pcodes, const void* pscales, int x_dtype,
+                      const void* X, int64_t x_stride, const void* x_pscales, int y_dtype, void* Y,
+                      void* stream) {
+  if (!pcodes || !pscales || !X || !Y) return LOWBIT_E_NULL;
+  if (x_dtype != LOWBIT_BF16 && x_dtype != LOWBIT_MXFP4) return LOWBIT_E_UNSUPPORTED;
+  if (y_dtype != LOWBIT_F32 && y_dtype != LOWBIT_BF16) return LOWBIT_E_UNSUPPORTED;
+  const bool x4 = x_dtype == LOWBIT_MXFP4;
+  if (x4 && !x_pscales) return LOWBIT_E_NULL;
+  if (!mx_shape_ok(N, K) || !mx_shape_ok(M, K) || N > (int64_t(1) << 26)) return LOWBIT_E_SHAPE;
+  if (cdiv(M, 128) * cdiv(N, 128) > (int64_t(1) << 23)) return LOWBIT_E_SHAPE;
+  if (!x4 && (x_stride < K || x_stride > (int64_t(1) << 40))) return LOWBIT_E_SHAPE;
+  if (!aligned(pcodes, 16) || !aligned(pscales, 16) || !aligned(X, 16) || !aligned(Y, 16) ||
+      (x4 && !aligned(x_pscales, 16)) || (!x4 && x_stride % 8 != 0))
+    return LOWBIT_E_ALIGN;
+  MxGemmArgs g;
+  g.M = M;
+  g.N = N;
+  g.K = K;
+  g.ld = x4 ? 0 : x_stride;
+  g.pcodes = pcodes;
+  g.pscales = pscales;
+  g.x4 = x4;
+  g.x = X;
+  g.x_pscales = x_pscales;
+  g.ykind = y_dtype;
+  g.y = Y;
+  return hip_status(launch_gemm_mxfp4(g, (hipStream_t)stream));
+}
+
+namespace {
+
+// checks of a cache and a batch, and the kernels' view of them
+int kv8_check(const lowbit_kv8* c, const lowbit_kv8_batch* b, KvArgs* out) {
+  if (!c || !b) return LOWBIT_E_NULL;
+  if (!c->k_codes || !c->v_codes || !c->k_scales || !c->v_scales || !b->page_table || !b->kv_lens)
+    return LOWBIT_E_NULL;
+  int lp = -1;
+  for (int i = 4; i <= 7; i++)
+    if (c->page_tokens == 1 << i) lp = i;
+  if (lp < 0 || (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256)) return LOWBIT_E_UNSUPPORTED;
+  if (c->kv_heads < 1 || c->kv_heads > 4096 || c->n_pages < 1 || c->n_pages > INT32_MAX) return LOWBIT_E_SHAPE;
+  if (b->n_seqs < 1 || b->n_seqs > (1 << 20) || b->table_width < 1 || b->table_width > (1 << 26))
+    return LOWBIT_E_SHAPE;
+  if (b->total_q < 1 || b->total_q > (1 << 30) || b->max_q < 1 || b->max_q > b->total_q) return LOWBIT_E_SHAPE;
+  if (!b->q_starts && b->total_q != b->n_seqs * b->max_q) return LOWBIT_E_SHAPE;
+  if (b->max_kv < 1 || b->max_kv > (1 << 30) || b->max_kv > b->table_width * c->page_tokens) return LOWBIT_E_SHAPE;
+  if (!aligned(c->k_codes, 16) || !aligned(c->v_codes, 16) || !aligned(b->page_table, 4) ||
+      !aligned(b->kv_lens, 4) || (b->q_starts && !aligned(b->q_starts, 4)) ||
+      (b->bad_pages && !aligned(b->bad_pages, 4)))
+    return LOWBIT_E_ALIGN;
+  out->n_pages = c->n_pages;
+  out->H = c->kv_heads;
+  out->D = c->head_dim;
+  out->lp = lp;
+  out->kc = (uint8_t*)c->k_codes;
+  out->vc = (uint8_t*)c->v_codes;
+  out->ks = c->k_scales;
+  out->vs = c->v_scales;
+  out->n_seqs = b->n_seqs;
+  out->table = b->page_table;
+  out->width = b->table_width;
+  out->lens = b->kv_lens;
+  out->starts = b->q_starts;
+  out->total_q = b->total_q;
+  out->max_q = b->max_q;
+  out->max_kv = b->max_kv;
+  out->bad = b->bad_pages;
+  return LOWBIT_OK;
+}
+
+}  // namespace
+
+int lowbit_kv8_append(const lowbit_kv8* cache, const lowbit_kv8_batch* batch, int dtype, const void* K,
+                      const void* V, int64_t k_stride, int64_t v_stride, void* stream) {
+  if (!K || !V) return LOWBIT_E_NULL;
+  KvArgs a;
+  const int rc = kv8_check(cache, batch, &a);
+  if (rc) return rc;
+  if (dtype != LOWBIT_F32 && dtype != LOWBIT_BF16) return LOWBIT_E_UNSUPPORTED;
+  const int64_t row = (int64_t)a.H * a.D, most = int64_t(1) << 40;
+  if (k_stride < row || v_stride < row || k_stride > most || v_stride > most) return LOWBIT_E_SHAPE;
+  if (a.n_seqs * kv8_span(a) * a.H > (1 << 23)) return LOWBIT_E_SHAPE;
+  const int step = dtype == LOWBIT_F32 ? 4 : 8;
+  if (!aligned(K, 16) || !aligned(V, 16) || k_stride % step != 0 || v_stride % step != 0) return LOWBIT_E_ALIGN;
+  return hip_status(launch_kv8_append(a, dtype == LOWBIT_F32, K, V, k_stride, v_stride, (hipStream_t)stream));
+}
+
+int lowbit_attention_kv8_workspace(const lowbit_kv8* cache, const lowbit_kv8_batch* batch, int64_t q_heads,
+                                   size_t* bytes) {
+  if (!bytes) return LOWBIT_E_NULL;
+  *bytes = 0;
+  KvArgs a;
+  const int rc = kv8_check(cache, batch, &a);
+  if (rc) return rc;
+  if (q_heads < 1 || q_heads > (1 << 16) || q_heads % a.H != 0) return LOWBIT_E_SHAPE;
+  *bytes = attention_workspace_bytes(a.D, a.H, a.n_seqs, a.max_q, a.max_kv, q_heads / a.H);
+  return LOWBIT_OK;
+}
+
+int lowbit_attention_kv8(const lowbit_kv8* cache, const lowbit_kv8_batch* batch, int64_t q_heads,
+                         const uint16_t* Q_bf16, int64_t q_stride, float softmax_scale, int causal,
+                         int64_t window, uint16_t* O_bf16, int64_t o_stride, float* lse, void* stream) {
+  if (!Q_bf16 || !O_bf16) return LOWBIT_E_NULL;
+  AttnArgs a;
+  const int rc = kv8_check(cache, batch, &a.kv);
+  if (rc) return rc;
+  if (q_heads < 1 || q_heads > (1 << 16) || q_heads % a.kv.H != 0) return LOWBIT_E_SHAPE;
+  const int64_t row = q_heads * a.kv.D, most = int64_t(1) << 40;
+  if (q_stride < row || o_stride < row || q_stride > most || o_stride > most) return LOWBIT_E_SHAPE;
+  if (!(softmax_scale - softmax_scale == 0.0f)) return LOWBIT_E_UNSUPPORTED;  // infinite or NaN
+  if (window < 0) return LOWBIT_E_SHAPE;
+  a.G = q_heads / a.kv.H;
+  if (a.kv.max_q * a.G > (1 << 30) ||
+      attention_blocks(a.kv.D, a.kv.H, a.kv.n_seqs, a.kv.max_q, a.kv.max_kv, a.G) > (1 << 22))
+    return LOWBIT_E_SHAPE;
+  if (!aligned(Q_bf16, 16) || !aligned(O_bf16, 16) || q_stride % 8 != 0 || o_stride % 8 != 0 ||
+      (lse && !aligned(lse, 4)))
+    return LOWBIT_E_ALIGN;
+  a.Hq = q_heads;
+  a.q = Q_bf16;
+  a.q_stride = q_stride;
+  a.scale2 = softmax_scale * 1.4426950408889634f;
+  a.causal = causal ? 1 : 0;
+  a.window = window > (1 << 30) ? 0 : (int)window;  // wider than any sequence
+  a.o = O_bf16;
+  a.o_stride = o_stride;
+  a.lse = lse;
+  void* ws = nullptr;
+  const int r2 = workspace((hipStream_t)stream,
+                           attention_workspace_bytes(a.kv.D, a.kv.H, a.kv.n_seqs, a.kv.max_q, a.kv.max_kv, a.G), &ws);
+  if (r2) return r2;
+  return hip_status(launch_attention(a, ws, (hipStream_t)stream));
+}

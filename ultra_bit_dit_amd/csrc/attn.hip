@@ -1,0 +1,479 @@
+// Attention over the paged 8-bit cache: O = softmax(scale Q K^T) V with
+// K = 2^ek codes, V = 2^ev codes, per page and head.
+//
+// Rows.  The queries of one sequence that share a key / value head are one
+// matrix of R = n G rows (n new tokens, G = query heads per key head): row
+// rho is token rho / G, head h G + rho % G.
+//
+// Products run as v_mfma_f32_16x16x32_bf16 on codes widened to bf16 (exact,
+// v_cvt_scalef32_pk_bf16_fp8), fp32 accumulation.  S^T = K Q^T puts a query
+// row in lane n = L % 16 and tokens in the lane's registers; with the tile's
+// token of row 4 g + j of tile t chosen as 16 g + 4 t + j, lane group
+// g = L / 16 holds 16 consecutive tokens, which is what the B operand of
+// O^T = V^T P^T needs: no exchange between the products, 16 tokens of one
+// row of V are one 16-byte load, and (pages hold 16 tokens or more) one
+// exponent ek and ev per lane and step.  p 2^ev is rounded to bf16 (relative
+// error 2^-9 of each weight, the same size as the output's own rounding);
+// statistics, sums and O stay in fp32.
+#include <hip/hip_runtime.h>
+
+#include "kv8.hpp"
+
+namespace lowbit {
+namespace {
+
+constexpr int kUnit = 64;  // tokens of one step of a wave
+constexpr float kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ v8bf bf16x8_of_e4m3(uint32_t w0, uint32_t w1) {
+  union {
+    v2bf h[4];
+    v8bf v;
+  } r;
+  r.h[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, 1.0f, false);
+  r.h[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, 1.0f, true);
+  r.h[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, 1.0f, false);
+  r.h[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, 1.0f, true);
+  return r.v;
+}
+__device__ __forceinline__ float pow2_byte(uint32_t b) {
+  return __uint_as_float(b ? b << 23 : 0x00400000u);  // byte 255: infinity, which no append writes
+}
+__device__ __forceinline__ v4f mfma(const v8bf& a, const v8bf& b, const v4f& c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+// bytes of w that are e4m3 NaN codes (0x7F or 0xFF): bit 7 of each
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
+  return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+}
+// mask of the bytes of a word whose index e in 0..3 has lo <= e < hi
+__device__ __forceinline__ uint32_t byte_range(int lo, int hi) {
+  lo = lo < 0 ? 0 : lo > 4 ? 4 : lo;
+  hi = hi < 0 ? 0 : hi > 4 ? 4 : hi;
+  if (hi <= lo) return 0u;
+  const uint32_t up = hi == 4 ? 0xFFFFFFFFu : (1u << (8 * hi)) - 1u;
+  return up & ~((1u << (8 * lo)) - 1u);  // lo < 4 here
+}
+
+// Few rows: one workgroup of WAVES waves per (sequence, key head, 16 NC rows,
+// split of the tokens); the waves take 64-token steps in turn and every wave
+// reads the codes it needs straight from the cache into registers.
+// Eight waves a compute unit where a wave fits 256 registers, else four.
+constexpr int dec_waves(int D, int NC) { return D * NC >= 256 ? 4 : 8; }
+constexpr int kChunkUnit = 8 * kUnit;  // a split is whole turns of up to eight waves
+
+template <int D, int NC>
+__global__ __launch_bounds__(64 * dec_waves(D, NC)) void attn_decode(AttnArgs a) {
+  constexpr int DC = D / 64, DT = D / 16, kDecWaves = dec_waves(D, NC);
+  __shared__ __attribute__((aligned(16))) float lo_[kDecWaves / 2][NC * 16 * D];  // partial O of half the waves
+  __shared__ float lm_[kDecWaves][NC * 16], ll_[kDecWaves][NC * 16];
+  __shared__ uint32_t s_last;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n = lane & 15, g = lane >> 4;
+  const int64_t bid = blockIdx.x;
+  const int sp = (int)(bid % a.S);
+  const int64_t tile = bid / a.S;
+  const int h = (int)(tile % a.kv.H);
+  const int64_t rt = (tile / a.kv.H) % a.RT, b = tile / a.kv.H / a.RT;
+  const SeqSpan s = seq_span(a.kv, b);
+  const int64_t R = (int64_t)s.n * a.G;
+  const int64_t rho0 = rt * 16 * NC;
+  if (rho0 >= R) return;
+  const int len = s.len, first = len - s.n;  // position of the first new token
+  const int P = 1 << a.kv.lp;
+
+  // visible tokens of this lane's rows: [vlo, vhi)
+  int vlo[NC], vhi[NC];
+  int hi_max = 0, hi_min = len, lo_min = 0, lo_max = 0;
+  {
+    const int64_t rlast = rho0 + 16 * NC - 1 < R ? rho0 + 16 * NC - 1 : R - 1;
+    const int p0 = first + (int)(rho0 / a.G), p1 = first + (int)(rlast / a.G);
+    hi_max = a.causal ? min(len, p1 + 1) : len;
+    hi_min = a.causal ? min(len, p0 + 1) : len;
+    hi_max = max(hi_max, 0);
+    hi_min = max(hi_min, 0);
+    if (a.window > 0) {
+      lo_min = max(0, p0 - a.window + 1);
+      lo_max = max(0, p1 - a.window + 1);
+    }
+  }
+  int64_t rho[NC];
+#pragma unroll
+  for (int c = 0; c < NC; c++) {
+    rho[c] = rho0 + 16 * c + n;
+    const int64_t rc = rho[c] < R ? rho[c] : R - 1;
+    const int p = first + (int)(rc / a.G);
+    vhi[c] = a.causal ? min(len, p + 1) : len;
+    vlo[c] = a.window > 0 ? max(0, p - a.window + 1) : 0;
+  }
+  const int64_t t0 = (int64_t)(lo_min / kUnit) * kUnit + sp * a.chunk;  // tokens of this split
+  const int64_t t1 = t0 + a.chunk < hi_max ? t0 + a.chunk : hi_max;
+  const int u0 = (int)(t0 / kUnit), u1 = t1 > t0 ? (int)((t1 + kUnit - 1) / kUnit) : u0;
+  const int n_splits = hi_max > lo_min ? (int)((hi_max - (int64_t)(lo_min / kUnit) * kUnit + a.chunk - 1) / a.chunk) : 1;
+  if (sp >= n_splits) return;
+
+  // Q: lane (n, g) holds dims 64 c + 16 g + 8 e .. + 7 of its row
+  v8bf qf[NC][DC][2];
+#pragma unroll
+  for (int c = 0; c < NC; c++) {
+    const int64_t rc = rho[c] < R ? rho[c] : R - 1;
+    const uint16_t* qp = a.q + (s.row0 + rc / a.G) * a.q_stride + (h * a.G + rc % a.G) * D + 16 * g;
+#pragma unroll
+    for (int d = 0; d < DC; d++) {
+      qf[c][d][0] = __builtin_bit_cast(v8bf, *(const mx_u4*)(qp + 64 * d));
+      qf[c][d][1] = __builtin_bit_cast(v8bf, *(const mx_u4*)(qp + 64 * d + 8));
+    }
+  }
+
+  v4f o[NC][DT];
+  float m[NC], l[NC];
+#pragma unroll
+  for (int c = 0; c < NC; c++) {
+    m[c] = -INFINITY;
+    l[c] = 0.f;
+#pragma unroll
+    for (int d = 0; d < DT; d++) o[c][d] = v4f{0.f, 0.f, 0.f, 0.f};
+  }
+
+  const int32_t* table = a.kv.table + b * a.kv.width;
+  const int64_t page_bytes = ((int64_t)D << a.kv.lp);
+  // page of the 16 tokens from t on; -1 where there are none or the entry is unusable
+  auto page_at = [&](int t) -> int64_t {
+    if (t >= hi_max) return -1;
+    const int64_t pg = table[t >> a.kv.lp];
+    return pg >= 0 && pg < a.kv.n_pages ? pg : -2;
+  };
+  mx_u4 kr[4][DC], vr[DT];
+  int64_t pgv = -1;
+  auto load_k = [&](int u) {
+    const int tk = u * kUnit + 16 * (n >> 2);
+    const int64_t pg = page_at(tk);
+    const uint8_t* kb = a.kv.kc + ((pg < 0 ? 0 : pg) * a.kv.H + h) * page_bytes +
+                        (int64_t)((tk & (P - 1)) + (n & 3)) * D + 16 * g;
+#pragma unroll
+    for (int t = 0; t < 4; t++)
+#pragma unroll
+      for (int d = 0; d < DC; d++) kr[t][d] = *(const mx_u4*)(kb + 4 * t * D + 64 * d);
+  };
+  auto load_v = [&](int u) {
+    const int tv = u * kUnit + 16 * g;
+    pgv = page_at(tv);
+    const uint8_t* vb = a.kv.vc + ((pgv < 0 ? 0 : pgv) * a.kv.H + h) * page_bytes + (int64_t)n * P + (tv & (P - 1));
+#pragma unroll
+    for (int d = 0; d < DT; d++) vr[d] = *(const mx_u4*)(vb + (int64_t)16 * d * P);
+  };
+
+  int u = u0 + wave;
+  if (u < u1) {
+    load_k(u);
+    load_v(u);
+  }
+  for (; u < u1; u += kDecWaves) {
+    const int64_t ph = (pgv < 0 ? 0 : pgv) * a.kv.H + h;
+    const bool gone = pgv < 0;  // none of this lane's 16 tokens can be read
+    const float sk = pow2_byte(a.kv.ks[ph]) * a.scale2, sv = pow2_byte(a.kv.vs[ph]);
+    if (pgv == -2 && n == 0 && a.kv.bad) atomicAdd(a.kv.bad, 1);
+    const int T = u * kUnit;
+    const bool part = T + kUnit > hi_min || T < lo_max || __any(gone);
+    // scores of tokens T + 16 g + 4 t + j
+    v4f sc[NC][4];
+#pragma unroll
+    for (int t = 0; t < 4; t++) {
+#pragma unroll
+      for (int c = 0; c < NC; c++) sc[c][t] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int d = 0; d < DC; d++) {
+        const v8bf k0 = bf16x8_of_e4m3(kr[t][d].x, kr[t][d].y), k1 = bf16x8_of_e4m3(kr[t][d].z, kr[t][d].w);
+#pragma unroll
+        for (int c = 0; c < NC; c++) {
+          sc[c][t] = mfma(k0, qf[c][d][0], sc[c][t]);
+          sc[c][t] = mfma(k1, qf[c][d][1], sc[c][t]);
+        }
+      }
+    }
+    if (u + kDecWaves < u1) load_k(u + kDecWaves);
+    v8bf pf[NC][2];
+    uint32_t seen[NC];  // bit e: token 16 g + e is visible to the lane's row
+#pragma unroll
+    for (int c = 0; c < NC; c++) {
+      float mx = -INFINITY;
+      seen[c] = 0xFFFFu;
+      if (part) {
+        seen[c] = 0;
+#pragma unroll
+        for (int e = 0; e < 16; e++) {
+          const int tok = T + 16 * g + e;
+          const bool see = tok >= vlo[c] && tok < vhi[c] && !gone;
+          seen[c] |= see ? 1u << e : 0u;
+          sc[c][e >> 2][e & 3] = see ? sc[c][e >> 2][e & 3] * sk : -INFINITY;
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 16; e++) sc[c][e >> 2][e & 3] *= sk;
+      }
+#pragma unroll
+      for (int e = 0; e < 16; e++) mx = fmaxf(mx, sc[c][e >> 2][e & 3]);
+      mx = fmaxf(mx, __shfl_xor(mx, 16));
+      mx = fmaxf(mx, __shfl_xor(mx, 32));
+      const float mn = fmaxf(m[c], mx);
+      const float mu = mn == -INFINITY ? 0.f : mn;
+      const float al = __builtin_amdgcn_exp2f(m[c] - mu);  // first tokens: 2^-inf = 0
+      m[c] = mn;
+      l[c] *= al;
+#pragma unroll
+      for (int d = 0; d < DT; d++)
+#pragma unroll
+        for (int e = 0; e < 4; e++) o[c][d][e] *= al;
+      float p[16];
+#pragma unroll
+      for (int e = 0; e < 16; e++) {
+        p[e] = __builtin_amdgcn_exp2f(sc[c][e >> 2][e & 3] - mu);
+        l[c] += p[e];
+      }
+#pragma unroll
+      for (int e = 0; e < 16; e++) pf[c][e >> 3][e & 7] = (__bf16)(p[e] * (seen[c] ? sv : 0.f));
+    }
+    if (part) {
+      // Tokens no row sees: their codes may be anything, so they become 0.
+      // A NaN code of a token that only some rows see must reach those rows
+      // alone: it becomes 0 too and is put back below.
+      uint32_t nans = 0;
+      const int lo = (gone ? 16 : lo_min - (T + 16 * g)), hi = hi_max - (T + 16 * g);
+      const uint32_t k0 = byte_range(lo, hi), k1 = byte_range(lo - 4, hi - 4);
+      const uint32_t k2 = byte_range(lo - 8, hi - 8), k3 = byte_range(lo - 12, hi - 12);
+#pragma unroll
+      for (int d = 0; d < DT; d++) {
+        vr[d].x &= k0;
+        vr[d].y &= k1;
+        vr[d].z &= k2;
+        vr[d].w &= k3;
+        nans |= nan_bytes(vr[d].x) | nan_bytes(vr[d].y) | nan_bytes(vr[d].z) | nan_bytes(vr[d].w);
+      }
+      if (__any(nans != 0)) {
+        v8bf vis[NC][2];
+#pragma unroll
+        for (int c = 0; c < NC; c++)
+#pragma unroll
+          for (int e = 0; e < 16; e++) vis[c][e >> 3][e & 7] = (__bf16)((seen[c] >> e) & 1u ? 1.0f : 0.0f);
+#pragma unroll
+        for (int d = 0; d < DT; d++) {
+          v8bf isn[2];
+#pragma unroll
+          for (int e = 0; e < 16; e++) {
+            const uint32_t w = (&vr[d])[0][e >> 2];
+            isn[e >> 3][e & 7] = (__bf16)((nan_bytes(w) >> (8 * (e & 3) + 7)) & 1u ? 1.0f : 0.0f);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; i++) vr[d][i] &= ~((nan_bytes(vr[d][i]) >> 7) * 0xFFu);
+#pragma unroll
+          for (int c = 0; c < NC; c++) {
+            v4f hit = v4f{0.f, 0.f, 0.f, 0.f};
+            hit = mfma(isn[0], vis[c][0], hit);
+            hit = mfma(isn[1], vis[c][1], hit);
+#pragma unroll
+            for (int e = 0; e < 4; e++)
+              if (hit[e] > 0.f) o[c][d][e] = __uint_as_float(0x7FC00000u);
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int d = 0; d < DT; d++) {
+      const v8bf v0 = bf16x8_of_e4m3(vr[d].x, vr[d].y), v1 = bf16x8_of_e4m3(vr[d].z, vr[d].w);
+#pragma unroll
+      for (int c = 0; c < NC; c++) {
+        o[c][d] = mfma(v0, pf[c][0], o[c][d]);
+        o[c][d] = mfma(v1, pf[c][1], o[c][d]);
+      }
+    }
+    if (u + kDecWaves < u1) load_v(u + kDecWaves);
+  }
+
+  // ---- the waves' results: common maximum, then O added in the order of the waves
+#pragma unroll
+  for (int c = 0; c < NC; c++) {
+    l[c] += __shfl_xor(l[c], 16);
+    l[c] += __shfl_xor(l[c], 32);
+    if (g == 0) {
+      lm_[wave][16 * c + n] = m[c];
+      ll_[wave][16 * c + n] = l[c];
+    }
+  }
+  __syncthreads();
+  float f[NC], mt[NC], lt[NC];
+#pragma unroll
+  for (int c = 0; c < NC; c++) {
+    mt[c] = -INFINITY;
+    lt[c] = 0.f;
+#pragma unroll
+    for (int w = 0; w < kDecWaves; w++) mt[c] = fmaxf(mt[c], lm_[w][16 * c + n]);
+    const float mu = mt[c] == -INFINITY ? 0.f : mt[c];
+#pragma unroll
+    for (int w = 0; w < kDecWaves; w++) lt[c] += ll_[w][16 * c + n] * __builtin_amdgcn_exp2f(lm_[w][16 * c + n] - mu);
+    f[c] = __builtin_amdgcn_exp2f(m[c] - mu);
+#pragma unroll
+    for (int d = 0; d < DT; d++)
+#pragma unroll
+      for (int e = 0; e < 4; e++) o[c][d][e] *= f[c];
+  }
+  // a tree over the waves: the upper half hands its O to the lower half
+#pragma unroll
+  for (int half = kDecWaves / 2; half >= 1; half >>= 1) {
+    if (wave >= half && wave < 2 * half) {
+#pragma unroll
+      for (int c = 0; c < NC; c++)
+#pragma unroll
+        for (int d = 0; d < DT; d++) *(v4f*)&lo_[wave - half][((c * DT + d) * 64 + lane) * 4] = o[c][d];
+    }
+    __syncthreads();
+    if (wave < half) {
+#pragma unroll
+      for (int c = 0; c < NC; c++)
+#pragma unroll
+        for (int d = 0; d < DT; d++) {
+          const v4f v = *(const v4f*)&lo_[wave][((c * DT + d) * 64 + lane) * 4];
+#pragma unroll
+          for (int e = 0; e < 4; e++) o[c][d][e] += v[e];
+        }
+    }
+    __syncthreads();
+  }
+
+  if (n_splits == 1) {
+    if (wave == 0) {
+#pragma unroll
+      for (int c = 0; c < NC; c++) {
+        if (rho[c] >= R) continue;
+        const float inv = lt[c] > 0.f || lt[c] != lt[c] ? 1.0f / lt[c] : 0.f;
+        const int64_t tok = s.row0 + rho[c] / a.G, hd = h * a.G + rho[c] % a.G;
+        uint16_t* op = a.o + tok * a.o_stride + hd * D + 4 * g;
+#pragma unroll
+        for (int d = 0; d < DT; d++) {
+          uint2 w;
+          w.x = bf16_bits(o[c][d][0] * inv) | (bf16_bits(o[c][d][1] * inv) << 16);
+          w.y = bf16_bits(o[c][d][2] * inv) | (bf16_bits(o[c][d][3] * inv) << 16);
+          *(uint2*)(op + 16 * d) = w;
+        }
+        if (a.lse && g == 0) a.lse[tok * a.Hq + hd] = lt[c] == 0.f ? -INFINITY : (mt[c] + __builtin_amdgcn_logf(lt[c])) * kLn2;
+      }
+    }
+    return;
+  }
+
+  // ---- several splits: results to the workspace with device-coherent
+  // stores that complete before the arrival is counted; the last workgroup
+  // to arrive joins them in the order of the splits
+  const int rows = (int)(R - rho0 < 16 * NC ? R - rho0 : 16 * NC);
+  constexpr int PR = D + 2;  // floats of one row: O, m, l
+  float* tp = a.part + tile * (int64_t)a.S * 16 * NC * PR;
+  if (wave == 0) {
+    float* mine = tp + (int64_t)sp * 16 * NC * PR;
+#pragma unroll
+    for (int c = 0; c < NC; c++) {
+      if (16 * c + n < rows) {
+        float* row = mine + (16 * c + n) * PR;
+#pragma unroll
+        for (int d = 0; d < DT; d++)
+#pragma unroll
+          for (int e = 0; e < 4; e++)
+            __hip_atomic_store(row + 16 * d + 4 * g + e, o[c][d][e], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        if (g == 0) {
+          __hip_atomic_store(row + D, mt[c], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+          __hip_atomic_store(row + D + 1, lt[c], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+      }
+    }
+    __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    if (lane == 0) s_last = __hip_atomic_fetch_add(a.cnt + tile, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  __syncthreads();
+  if (s_last != (uint32_t)n_splits - 1) return;
+  if (threadIdx.x == 0) __hip_atomic_store(a.cnt + tile, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  constexpr int D4 = D / 4;
+  for (int i = threadIdx.x; i < rows * D4; i += 64 * kDecWaves) {
+    const int r = i / D4, d = (i % D4) * 4;
+    const float* row = tp + r * PR;
+    float mm = -INFINITY;
+    for (int k = 0; k < n_splits; k++)
+      mm = fmaxf(mm, __hip_atomic_load(row + (int64_t)k * 16 * NC * PR + D, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+    const float mu = mm == -INFINITY ? 0.f : mm;
+    float L = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int k = 0; k < n_splits; k++) {
+      const float* rk = row + (int64_t)k * 16 * NC * PR;
+      const float w = __builtin_amdgcn_exp2f(__hip_atomic_load(rk + D, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) - mu);
+      L += w * __hip_atomic_load(rk + D + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+      for (int e = 0; e < 4; e++)
+        acc[e] += w * __hip_atomic_load(rk + d + e, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    const float inv = L > 0.f || L != L ? 1.0f / L : 0.f;
+    const int64_t rr = rho0 + r, tok = s.row0 + rr / a.G, hd = h * a.G + rr % a.G;
+    uint2 w;
+    w.x = bf16_bits(acc[0] * inv) | (bf16_bits(acc[1] * inv) << 16);
+    w.y = bf16_bits(acc[2] * inv) | (bf16_bits(acc[3] * inv) << 16);
+    *(uint2*)(a.o + tok * a.o_stride + hd * D + d) = w;
+    if (a.lse && d == 0) a.lse[tok * a.Hq + hd] = L == 0.f ? -INFINITY : (mm + __builtin_amdgcn_logf(L)) * kLn2;
+  }
+}
+
+struct Plan {
+  int nc, S;
+  int64_t RT, tiles, chunk;
+};
+
+Plan plan_decode(int D, int H, int64_t n_seqs, int64_t max_q, int64_t max_kv, int64_t G) {
+  Plan p;
+  const int64_t R = max_q * G;
+  p.nc = R > 16 && D <= 128 ? 2 : 1;  // wider heads: the registers of 16 rows
+  p.RT = cdiv(R, 16 * p.nc);
+  p.tiles = n_seqs * H * p.RT;
+  // tokens of one split: about 1024 workgroups in all, at least one step for
+  // each wave, at most 64 splits to join
+  int64_t S = p.tiles >= 1024 ? 1 : cdiv(1024, p.tiles);
+  S = S < 64 ? S : 64;
+  const int64_t per = cdiv(cdiv(max_kv, S), kChunkUnit) * kChunkUnit;
+  p.chunk = per;
+  p.S = (int)cdiv(max_kv + kUnit, per);
+  if (p.tiles > kMaxRowGroups || p.S < 1) {
+    p.S = 1;
+    p.chunk = cdiv(max_kv + kUnit, kUnit) * kUnit;
+  }
+  return p;
+}
+
+}  // namespace
+
+int64_t attention_blocks(int D, int H, int64_t n_seqs, int64_t max_q, int64_t max_kv, int64_t G) {
+  const Plan p = plan_decode(D, H, n_seqs, max_q, max_kv, G);
+  return p.tiles * p.S;
+}
+
+size_t attention_workspace_bytes(int D, int H, int64_t n_seqs, int64_t max_q, int64_t max_kv, int64_t G) {
+  const Plan p = plan_decode(D, H, n_seqs, max_q, max_kv, G);
+  if (p.S == 1) return kCounterBytes;
+  return (size_t)kCounterBytes + (size_t)(p.tiles * p.S * 16 * p.nc * (D + 2)) * 4;
+}
+
+hipError_t launch_attention(AttnArgs a, void* ws, hipStream_t s) {
+  const Plan p = plan_decode(a.kv.D, a.kv.H, a.kv.n_seqs, a.kv.max_q, a.kv.max_kv, a.G);
+  a.RT = p.RT;
+  a.S = p.S;
+  a.chunk = p.chunk;
+  a.cnt = (uint32_t*)ws + 16;
+  a.part = (float*)((uint8_t*)ws + kCounterBytes);
+  const dim3 grid((unsigned)(p.tiles * p.S));
+#define LOWBIT_DEC(DD, NN) \
+  hipLaunchKernelGGL((attn_decode<DD, NN>), grid, dim3(64 * dec_waves(DD, NN)), 0, s, a)
+  if (p.nc == 1) {
+    if (a.kv.D == 64) LOWBIT_DEC(64, 1);
+    else if (a.kv.D == 128) LOWBIT_DEC(128, 1);
+    else LOWBIT_DEC(256, 1);
+  } else {
+    if (a.kv.D == 64) LOWBIT_DEC(64, 2);
+    else LOWBIT_DEC(128, 2);
+  }
+#undef LOWBIT_DEC
+  return hipGetLastError();
+}
+
+}  // namespace lowbit

@@ -150,4 +150,33 @@ hipError_t launch_quantize_weights(int fmt, int64_t N, int64_t K, const uint16_t
 hipError_t launch_rotate_act(int64_t M, int64_t K, const uint16_t* X, const int8_t* signs,
                              float* Xr, hipStream_t s);
 
+// ---- MXFP4 (mx.hip, mx_gemm.hip) and the 8-bit cache (kv8.hip)
+
+hipError_t launch_quantize_mxfp4(int64_t rows, int64_t K, bool f32, const void* X, int64_t ld,
+                                 void* pcodes, void* pscales, void* values, hipStream_t s);
+hipError_t launch_pack_mxfp4(int64_t rows, int64_t K, const uint8_t* codes, const uint8_t* scales,
+                             void* pcodes, void* pscales, hipStream_t s);
+
+struct MxGemmArgs {
+  int64_t M, N, K, ld;      // ld: elements between rows of a bf16 X
+  const void* pcodes;
+  const void* pscales;
+  bool x4;                  // X is MXFP4 (x, x_pscales), else bf16
+  const void* x;
+  const void* x_pscales;
+  int ykind;                // YK_F32 / YK_BF16
+  void* y;                  // [M][N]
+};
+hipError_t launch_gemm_mxfp4(const MxGemmArgs& a, hipStream_t s);
+
+struct KvArgs;
+struct AttnArgs;
+int64_t kv8_span(const KvArgs& a);  // pages one sequence's new tokens can touch
+hipError_t launch_kv8_append(const KvArgs& a, bool f32, const void* K, const void* V, int64_t k_stride,
+                             int64_t v_stride, hipStream_t s);
+// workgroups of an attention launch, and its workspace (counters included)
+int64_t attention_blocks(int D, int H, int64_t n_seqs, int64_t max_q, int64_t max_kv, int64_t G);
+size_t attention_workspace_bytes(int D, int H, int64_t n_seqs, int64_t max_q, int64_t max_kv, int64_t G);
+hipError_t launch_attention(AttnArgs a, void* ws, hipStream_t s);
+
 }  // namespace lowbit
