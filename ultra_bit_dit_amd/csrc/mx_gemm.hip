@@ -12,6 +12,8 @@
 // word j takes X[m][128 g + 32 q + 8 j .. + 7] from lane m + 16 q.
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "mx.hpp"
 
 namespace lowbit {
@@ -183,6 +185,198 @@ void launch_small(const MxArgs& a, int ykind, hipStream_t s) {
     hipLaunchKernelGGL((mx_small<X4, MT, RB, YK_BF16>), grid, dim3(64 * W), lds, s, a);
 }
 
+// ------------------------------------------------------------ many rows of X
+// Workgroup tiles of 16 RN rows of W by 16 RM rows of X.  Codes, activations
+// and exponents reach LDS as direct global -> LDS copies into a ring of group
+// buffers; one counter of a wave's copies orders them, so each group waits
+// exactly for its own (the later groups' stay in flight) and one barrier a
+// group keeps the ring.  W is operand A (rows n) and X operand B (columns m):
+// a lane then holds four consecutive n of one output row.
+typedef __attribute__((address_space(3))) uint8_t lds_u8;
+
+// s_waitcnt immediate: vmcnt n, lgkmcnt and expcnt at their maxima
+constexpr int vm_wait(int n) { return (n & 15) | ((n >> 4) << 14) | 0xF70; }
+
+__device__ __forceinline__ void copy16(const uint8_t* src, lds_u8* dst) {
+  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
+                                   (__attribute__((address_space(3))) void*)dst, 16, 0, 0);
+}
+template <int N>
+__device__ __forceinline__ void wait_copies_and_meet() {
+  __asm__ volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(vm_wait(N));
+  __builtin_amdgcn_s_barrier();
+  __asm__ volatile("" ::: "memory");
+}
+
+// Tile of workgroup bid: each XCD (bid % 8) takes a contiguous run of tiles,
+// in bands of 8 row tiles of X with those running fastest, so that the
+// workgroups of an XCD share both operands in its L2.
+__device__ __forceinline__ void tile_of(int64_t bid, int64_t MT, int64_t NT, int64_t* mt, int64_t* nt) {
+  const int64_t T = MT * NT, per = T / 8, rem = T % 8, x = bid % 8, i = bid / 8;
+  const int64_t t = x * per + (x < rem ? x : rem) + i;
+  const int64_t band = t / (8 * NT), left = MT - band * 8, w = left < 8 ? left : 8, r = t - band * 8 * NT;
+  *mt = band * 8 + r % w;
+  *nt = r / w;
+}
+
+template <int YK, int JN, int IM>
+__device__ __forceinline__ void store_tile(const MxArgs& a, const v4f (&acc)[JN][IM], int64_t n0, int64_t m0, int lane) {
+  const int r = lane & 15, q = lane >> 4;
+#pragma unroll
+  for (int i = 0; i < IM; i++) {
+    const int64_t m = m0 + 16 * i + r;
+    if (m >= a.M) continue;
+#pragma unroll
+    for (int j = 0; j < JN; j++) {
+      const int64_t n = n0 + 16 * j + 4 * q;
+      const v4f v = acc[j][i];
+      if (a.N % 4 == 0 && n + 3 < a.N) {
+        if constexpr (YK == YK_F32) {
+          *(v4f*)((float*)a.y + m * a.N + n) = v;
+        } else {
+          uint2 w;
+          w.x = bf16_bits(v[0]) | (bf16_bits(v[1]) << 16);
+          w.y = bf16_bits(v[2]) | (bf16_bits(v[3]) << 16);
+          *(uint2*)((uint16_t*)a.y + m * a.N + n) = w;
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; e++)
+          if (n + e < a.N) store_y<YK>(a.y, m * a.N + n + e, v[e]);
+      }
+    }
+  }
+}
+
+// X MXFP4.  WN x WM waves, each JN row-blocks of W by IM of X.
+template <int WN, int WM, int JN, int IM, int YK>
+__global__ __launch_bounds__(64 * WN * WM) void mx_gemm4(MxArgs a, int64_t MT, int64_t NT) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  constexpr int RN = WN * JN, RM = WM * IM, R = RN + RM, WAVES = WN * WM, CP = R / WAVES;
+  static_assert(R % WAVES == 0 && R / 4 == WAVES, "one scale copy and CP code copies per wave");
+  // four group buffers; the first also holds the quad's exponents.  (Separate
+  // objects, and no more of them: the compiler keeps apart the copies in flight
+  // to four LDS objects and would wait for every copy before any read of a fifth.)
+  __shared__ __attribute__((aligned(16))) uint8_t b0[R * 1280], b1[R * 1024], b2[R * 1024], b3[R * 1024];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wn = wave % WN, wm = wave / WN;
+  int64_t mt, nt;
+  tile_of(blockIdx.x, MT, NT, &mt, &nt);
+  const int G = (int)a.G, GQ = (int)a.GQ;
+
+  // this wave's code pieces: row-blocks CP wave .. of the tile's R (W first)
+  const uint8_t* src[CP];
+#pragma unroll
+  for (int i = 0; i < CP; i++) {
+    const int p = CP * wave + i;
+    int64_t rb = p < RN ? nt * RN + p : mt * RM + (p - RN);
+    const int64_t last = p < RN ? a.NB - 1 : a.MB - 1;
+    rb = rb < last ? rb : last;
+    src[i] = (p < RN ? a.wc : a.x) + rb * a.G * 1024 + 16 * lane;
+  }
+  // and four row-blocks' exponents
+  const uint8_t* ssrc;
+  {
+    const int p = 4 * wave + (lane >> 4);
+    int64_t rb = p < RN ? nt * RN + p : mt * RM + (p - RN);
+    const int64_t last = p < RN ? a.NB - 1 : a.MB - 1;
+    rb = rb < last ? rb : last;
+    ssrc = (p < RN ? a.ws : a.xs) + rb * a.GQ * 256 + 16 * (lane & 15);
+  }
+  auto copy_group = [&](int g, uint8_t* buf) {
+    const int64_t off = (int64_t)(g < G ? g : G - 1) * 1024;
+#pragma unroll
+    for (int i = 0; i < CP; i++) copy16(src[i] + off, (lds_u8*)buf + (CP * wave + i) * 1024);
+    __builtin_amdgcn_sched_barrier(0);  // issued before the phase's products, not behind them
+  };
+  auto copy_scales = [&](int gq) {
+    copy16(ssrc + (int64_t)(gq < GQ ? gq : GQ - 1) * 256, (lds_u8*)b0 + R * 1024 + wave * 1024);
+  };
+
+  v4f acc[JN][IM];
+#pragma unroll
+  for (int j = 0; j < JN; j++)
+#pragma unroll
+    for (int i = 0; i < IM; i++) acc[j][i] = v4f{0.f, 0.f, 0.f, 0.f};
+  uint32_t sw[JN], sx[IM];
+
+  copy_scales(0);
+  copy_group(0, b0);
+  __asm__ volatile("" ::: "memory");  // the waits below count the copies of each phase
+  copy_group(1, b1);
+  __asm__ volatile("" ::: "memory");
+  copy_group(2, b2);
+
+  auto compute = [&](auto tt, const uint8_t* buf) {
+    constexpr int T = decltype(tt)::value;
+    const uint8_t* pw = buf + wn * JN * 1024 + 16 * lane;
+    const uint8_t* px = buf + (RN + wm * IM) * 1024 + 16 * lane;
+    mx_u4 w[JN], x[IM];
+#pragma unroll
+    for (int j = 0; j < JN; j++) w[j] = *(const mx_u4*)(pw + j * 1024);
+#pragma unroll
+    for (int i = 0; i < IM; i++) x[i] = *(const mx_u4*)(px + i * 1024);
+#pragma unroll
+    for (int i = 0; i < IM; i++)
+#pragma unroll
+      for (int j = 0; j < JN; j++) acc[j][i] = mfma_mx<T>(w[j], x[i], acc[j][i], sw[j], sx[i]);
+  };
+  auto scales = [&]() {
+    const uint8_t* buf = b0 + R * 1024 + 4 * lane;
+#pragma unroll
+    for (int j = 0; j < JN; j++) sw[j] = *(const uint32_t*)(buf + (wn * JN + j) * 256);
+#pragma unroll
+    for (int i = 0; i < IM; i++) sx[i] = *(const uint32_t*)(buf + (RN + wm * IM + i) * 256);
+  };
+  // Per quad, groups g .. g + 3 in buffers 0 .. 3.  Each phase waits until the
+  // copies issued three phases ago are complete (the counts are those of the
+  // two phases between), meets the other waves, which have then read the
+  // previous buffer, and refills that one.  The next quad's exponents travel
+  // with its first group, after every wave has read this quad's.
+  auto phase0 = [&](int g) {
+    wait_copies_and_meet<2 * CP>();
+    copy_group(g + 3, b3);
+    scales();
+    compute(std::integral_constant<int, 0>{}, b0);
+  };
+  auto phase1 = [&](int g) {
+    wait_copies_and_meet<2 * CP>();
+    copy_group(g + 4, b0);
+    copy_scales(g / 4 + 1);
+    compute(std::integral_constant<int, 1>{}, b1);
+  };
+  auto phase2 = [&](int g) {
+    wait_copies_and_meet<2 * CP + 1>();
+    copy_group(g + 5, b1);
+    compute(std::integral_constant<int, 2>{}, b2);
+  };
+  const int full = G & ~3;
+  for (int g = 0; g < full; g += 4) {
+    phase0(g);
+    phase1(g);
+    phase2(g);
+    wait_copies_and_meet<2 * CP + 1>();
+    copy_group(g + 6, b2);
+    compute(std::integral_constant<int, 3>{}, b3);
+  }
+  if (full < G) phase0(full);
+  if (full + 1 < G) phase1(full);
+  if (full + 2 < G) phase2(full);
+  // no copy may still be on its way to LDS when the workgroup ends
+  __builtin_amdgcn_s_waitcnt(vm_wait(0));
+  store_tile<YK, JN, IM>(a, acc, (nt * RN + wn * JN) * 16, (mt * RM + wm * IM) * 16, lane);
+#endif
+}
+
+template <int WN, int WM, int JN, int IM>
+void launch_tile4(const MxArgs& a, int ykind, hipStream_t s) {
+  const int64_t NT = cdiv(a.NB, WN * JN), MT = cdiv(a.MB, WM * IM);
+  const dim3 grid((unsigned)(NT * MT)), block(64 * WN * WM);
+  if (ykind == YK_F32) hipLaunchKernelGGL((mx_gemm4<WN, WM, JN, IM, YK_F32>), grid, block, 0, s, a, MT, NT);
+  else hipLaunchKernelGGL((mx_gemm4<WN, WM, JN, IM, YK_BF16>), grid, block, 0, s, a, MT, NT);
+}
+
 }  // namespace
 
 hipError_t launch_gemm_mxfp4(const MxGemmArgs& g, hipStream_t s) {
@@ -200,7 +394,10 @@ hipError_t launch_gemm_mxfp4(const MxGemmArgs& g, hipStream_t s) {
   a.GQ = mx_quads(g.K);
   a.NB = cdiv(g.N, 16);
   a.MB = cdiv(g.M, 16);
-  if (g.x4) launch_small<true, 1, 1>(a, g.ykind, s);
+  if (g.x4 && a.M > 64) {
+    if (cdiv(a.NB, 16) * cdiv(a.MB, 16) >= 256) launch_tile4<4, 2, 4, 8>(a, g.ykind, s);
+    else launch_tile4<2, 2, 4, 4>(a, g.ykind, s);
+  } else if (g.x4) launch_small<true, 1, 1>(a, g.ykind, s);
   else launch_small<false, 1, 1>(a, g.ykind, s);
   return hipGetLastError();
 }
