@@ -377,6 +377,156 @@ void launch_tile4(const MxArgs& a, int ykind, hipStream_t s) {
   else hipLaunchKernelGGL((mx_gemm4<WN, WM, JN, IM, YK_BF16>), grid, block, 0, s, a, MT, NT);
 }
 
+// X bf16.  WN x WM waves, each JN row-blocks of W by IM of X; two group
+// buffers, the next group's copies in flight while one is multiplied (2048
+// cycles of MFMA per SIMD, longer than a copy takes).  A row of X is 256 bytes
+// of a group; its 16-byte chunk c lies at place c ^ (row % 16), so that the 16
+// rows of an operand read fall on different banks.  Chunks past K come from a
+// block of zeros: the codes there are 0, but 0 times what follows a row of X
+// need not be.
+[[maybe_unused]] __device__ const mx_u4 mx_zeros[16] = {};
+
+template <int WN, int WM, int JN, int IM, int YK>
+__global__ __launch_bounds__(64 * WN * WM) void mx_gemm16(MxArgs a, int64_t MT, int64_t NT) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  constexpr int RN = WN * JN, RM = WM * IM, WAVES = WN * WM;
+  constexpr int CW = RN / WAVES, CX = 4 * RM / WAVES;  // code and X copies of a wave (1 KiB each)
+  constexpr int CS = (RN / 4 + WAVES - 1) / WAVES;     // exponent copies, waves below RN / 4
+  static_assert(CW * WAVES == RN && CX * WAVES == 4 * RM && CS == 1, "whole copies per wave");
+  constexpr int XB = RM * 4096, CB = RN * 1024;
+  __shared__ __attribute__((aligned(16))) uint8_t b0[XB + CB + RN * 256], b1[XB + CB];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wn = wave % WN, wm = wave / WN, r = lane & 15, q = lane >> 4;
+  int64_t mt, nt;
+  tile_of(blockIdx.x, MT, NT, &mt, &nt);
+  const int G = (int)a.G, GQ = (int)a.GQ;
+
+  const uint8_t* wsrc[CW];
+#pragma unroll
+  for (int i = 0; i < CW; i++) {
+    int64_t rb = nt * RN + CW * wave + i;
+    rb = rb < a.NB - 1 ? rb : a.NB - 1;
+    wsrc[i] = a.wc + rb * a.G * 1024 + 16 * lane;
+  }
+  // piece p of X: rows 4 p .. 4 p + 3; lane: row lane / 16, place lane % 16
+  const uint8_t* xsrc[CX];
+  int xk[CX];  // first k of the lane's chunk
+#pragma unroll
+  for (int i = 0; i < CX; i++) {
+    const int row = 4 * (CX * wave + i) + (lane >> 4);
+    int64_t m = mt * RM * 16 + row;
+    m = m < a.M - 1 ? m : a.M - 1;
+    xk[i] = 8 * ((lane & 15) ^ (row & 15));
+    xsrc[i] = a.x + (m * a.ld + xk[i]) * 2;
+  }
+  const uint8_t* ssrc;
+  {
+    int64_t rb = nt * RN + 4 * wave + (lane >> 4);
+    rb = rb < a.NB - 1 ? rb : a.NB - 1;
+    ssrc = a.ws + rb * a.GQ * 256 + 16 * (lane & 15);
+  }
+  const uint8_t* zeros = (const uint8_t*)mx_zeros;
+  auto copy_group = [&](int g, uint8_t* buf) {
+    g = g < G ? g : G - 1;
+    const int left = (int)(a.K - (int64_t)g * 128 < 128 ? a.K - (int64_t)g * 128 : 128);
+#pragma unroll
+    for (int i = 0; i < CX; i++)
+      copy16(xk[i] < left ? xsrc[i] + (int64_t)g * 256 : zeros, (lds_u8*)buf + (CX * wave + i) * 1024);
+#pragma unroll
+    for (int i = 0; i < CW; i++) copy16(wsrc[i] + (int64_t)g * 1024, (lds_u8*)buf + XB + (CW * wave + i) * 1024);
+  };
+  auto copy_scales = [&](int gq) {
+    if (4 * wave < RN) copy16(ssrc + (int64_t)(gq < GQ ? gq : GQ - 1) * 256, (lds_u8*)b0 + XB + CB + wave * 1024);
+  };
+
+  v4f acc[JN][IM];
+#pragma unroll
+  for (int j = 0; j < JN; j++)
+#pragma unroll
+    for (int i = 0; i < IM; i++) acc[j][i] = v4f{0.f, 0.f, 0.f, 0.f};
+  uint32_t sw[JN];
+
+  auto compute = [&](auto tt, const uint8_t* buf) {
+    constexpr int T = decltype(tt)::value;
+    const uint8_t* pw = buf + XB + wn * JN * 1024 + 16 * lane;
+    const uint8_t* px = buf + wm * IM * 4096 + r * 256;
+    mx_u4 w[JN];
+    float s[JN];
+#pragma unroll
+    for (int j = 0; j < JN; j++) {
+      w[j] = *(const mx_u4*)(pw + j * 1024);
+      s[j] = scale_float(sw[j], T);
+    }
+#pragma unroll
+    for (int h = 0; h < 4; h++) {
+      v8bf x[IM], b[JN];
+      const int at = ((4 * q + h) ^ r) * 16;
+#pragma unroll
+      for (int i = 0; i < IM; i++) x[i] = *(const v8bf*)(px + i * 4096 + at);
+#pragma unroll
+      for (int j = 0; j < JN; j++) b[j] = bf16x8(w[j][h], s[j]);
+#pragma unroll
+      for (int i = 0; i < IM; i++)
+#pragma unroll
+        for (int j = 0; j < JN; j++)
+          acc[j][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j], x[i], acc[j][i], 0, 0, 0);
+    }
+  };
+  auto scales = [&]() {
+#pragma unroll
+    for (int j = 0; j < JN; j++) sw[j] = *(const uint32_t*)(b0 + XB + CB + (wn * JN + j) * 256 + 4 * lane);
+  };
+  // Each phase waits for its group (the only copies in flight), meets the
+  // other waves, which have then read the other buffer, and refills that one.
+  // The next quad's exponents travel behind every wave's read of this quad's.
+  auto phase0 = [&](int g) {
+    wait_copies_and_meet<0>();
+    copy_group(g + 1, b1);
+    __builtin_amdgcn_sched_barrier(0);
+    scales();
+    compute(std::integral_constant<int, 0>{}, b0);
+  };
+  auto phase1 = [&](int g) {
+    wait_copies_and_meet<0>();
+    copy_group(g + 2, b0);
+    copy_scales(g / 4 + 1);
+    __builtin_amdgcn_sched_barrier(0);
+    compute(std::integral_constant<int, 1>{}, b1);
+  };
+  auto phase2 = [&](int g) {
+    wait_copies_and_meet<0>();
+    copy_group(g + 3, b1);
+    __builtin_amdgcn_sched_barrier(0);
+    compute(std::integral_constant<int, 2>{}, b0);
+  };
+  copy_group(0, b0);
+  copy_scales(0);
+  const int full = G & ~3;
+  for (int g = 0; g < full; g += 4) {
+    phase0(g);
+    phase1(g);
+    phase2(g);
+    wait_copies_and_meet<0>();
+    copy_group(g + 4, b0);
+    __builtin_amdgcn_sched_barrier(0);
+    compute(std::integral_constant<int, 3>{}, b1);
+  }
+  if (full < G) phase0(full);
+  if (full + 1 < G) phase1(full);
+  if (full + 2 < G) phase2(full);
+  __builtin_amdgcn_s_waitcnt(vm_wait(0));
+  store_tile<YK, JN, IM>(a, acc, (nt * RN + wn * JN) * 16, (mt * RM + wm * IM) * 16, lane);
+#endif
+}
+
+template <int WN, int WM, int JN, int IM>
+void launch_tile16(const MxArgs& a, int ykind, hipStream_t s) {
+  const int64_t NT = cdiv(a.NB, WN * JN), MT = cdiv(a.MB, WM * IM);
+  const dim3 grid((unsigned)(NT * MT)), block(64 * WN * WM);
+  if (ykind == YK_F32) hipLaunchKernelGGL((mx_gemm16<WN, WM, JN, IM, YK_F32>), grid, block, 0, s, a, MT, NT);
+  else hipLaunchKernelGGL((mx_gemm16<WN, WM, JN, IM, YK_BF16>), grid, block, 0, s, a, MT, NT);
+}
+
 }  // namespace
 
 hipError_t launch_gemm_mxfp4(const MxGemmArgs& g, hipStream_t s) {
@@ -398,6 +548,7 @@ hipError_t launch_gemm_mxfp4(const MxGemmArgs& g, hipStream_t s) {
     if (cdiv(a.NB, 16) * cdiv(a.MB, 16) >= 256) launch_tile4<4, 2, 4, 8>(a, g.ykind, s);
     else launch_tile4<2, 2, 4, 4>(a, g.ykind, s);
   } else if (g.x4) launch_small<true, 1, 1>(a, g.ykind, s);
+  else if (a.M > 64) launch_tile16<4, 2, 4, 4>(a, g.ykind, s);
   else launch_small<false, 1, 1>(a, g.ykind, s);
   return hipGetLastError();
 }
