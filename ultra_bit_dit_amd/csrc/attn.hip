@@ -25,15 +25,16 @@ namespace {
 constexpr int kUnit = 64;  // tokens of one step of a wave
 constexpr float kLn2 = 0.6931471805599453f;
 
-__device__ __forceinline__ v8bf bf16x8_of_e4m3(uint32_t w0, uint32_t w1) {
+// eight codes times the power of two s as bf16 (exact: four significant bits)
+__device__ __forceinline__ v8bf bf16x8_of_e4m3(uint32_t w0, uint32_t w1, float s) {
   union {
     v2bf h[4];
     v8bf v;
   } r;
-  r.h[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, 1.0f, false);
-  r.h[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, 1.0f, true);
-  r.h[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, 1.0f, false);
-  r.h[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, 1.0f, true);
+  r.h[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, s, false);
+  r.h[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, s, true);
+  r.h[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, s, false);
+  r.h[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, s, true);
   return r.v;
 }
 __device__ __forceinline__ float pow2_byte(uint32_t b) {
@@ -145,22 +146,25 @@ __global__ __launch_bounds__(64 * dec_waves(D, NC)) void attn_decode(AttnArgs a)
   };
   mx_u4 kr[4][DC], vr[DT];
   int64_t pgv = -1;
+  uint32_t kb = 0, vb = 0;  // exponent bytes of the lane's keys and values
   auto load_k = [&](int u) {
     const int tk = u * kUnit + 16 * (n >> 2);
-    const int64_t pg = page_at(tk);
-    const uint8_t* kb = a.kv.kc + ((pg < 0 ? 0 : pg) * a.kv.H + h) * page_bytes +
-                        (int64_t)((tk & (P - 1)) + (n & 3)) * D + 16 * g;
+    const int64_t pg = page_at(tk), ph = (pg < 0 ? 0 : pg) * a.kv.H + h;
+    const uint8_t* kp = a.kv.kc + ph * page_bytes + (int64_t)((tk & (P - 1)) + (n & 3)) * D + 16 * g;
+    kb = a.kv.ks[ph];
 #pragma unroll
     for (int t = 0; t < 4; t++)
 #pragma unroll
-      for (int d = 0; d < DC; d++) kr[t][d] = *(const mx_u4*)(kb + 4 * t * D + 64 * d);
+      for (int d = 0; d < DC; d++) kr[t][d] = *(const mx_u4*)(kp + 4 * t * D + 64 * d);
   };
   auto load_v = [&](int u) {
     const int tv = u * kUnit + 16 * g;
     pgv = page_at(tv);
-    const uint8_t* vb = a.kv.vc + ((pgv < 0 ? 0 : pgv) * a.kv.H + h) * page_bytes + (int64_t)n * P + (tv & (P - 1));
+    const int64_t ph = (pgv < 0 ? 0 : pgv) * a.kv.H + h;
+    const uint8_t* vp = a.kv.vc + ph * page_bytes + (int64_t)n * P + (tv & (P - 1));
+    vb = a.kv.vs[ph];
 #pragma unroll
-    for (int d = 0; d < DT; d++) vr[d] = *(const mx_u4*)(vb + (int64_t)16 * d * P);
+    for (int d = 0; d < DT; d++) vr[d] = *(const mx_u4*)(vp + (int64_t)16 * d * P);
   };
 
   int u = u0 + wave;
@@ -169,9 +173,8 @@ __global__ __launch_bounds__(64 * dec_waves(D, NC)) void attn_decode(AttnArgs a)
     load_v(u);
   }
   for (; u < u1; u += kDecWaves) {
-    const int64_t ph = (pgv < 0 ? 0 : pgv) * a.kv.H + h;
     const bool gone = pgv < 0;  // none of this lane's 16 tokens can be read
-    const float sk = pow2_byte(a.kv.ks[ph]) * a.scale2, sv = pow2_byte(a.kv.vs[ph]);
+    const float sk = pow2_byte(kb), sv = gone ? 0.f : pow2_byte(vb);
     if (pgv == -2 && n == 0 && a.kv.bad) atomicAdd(a.kv.bad, 1);
     const int T = u * kUnit;
     const bool part = T + kUnit > hi_min || T < lo_max || __any(gone);
@@ -183,7 +186,7 @@ __global__ __launch_bounds__(64 * dec_waves(D, NC)) void attn_decode(AttnArgs a)
       for (int c = 0; c < NC; c++) sc[c][t] = v4f{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int d = 0; d < DC; d++) {
-        const v8bf k0 = bf16x8_of_e4m3(kr[t][d].x, kr[t][d].y), k1 = bf16x8_of_e4m3(kr[t][d].z, kr[t][d].w);
+        const v8bf k0 = bf16x8_of_e4m3(kr[t][d].x, kr[t][d].y, sk), k1 = bf16x8_of_e4m3(kr[t][d].z, kr[t][d].w, sk);
 #pragma unroll
         for (int c = 0; c < NC; c++) {
           sc[c][t] = mfma(k0, qf[c][d][0], sc[c][t]);
@@ -205,11 +208,11 @@ __global__ __launch_bounds__(64 * dec_waves(D, NC)) void attn_decode(AttnArgs a)
           const int tok = T + 16 * g + e;
           const bool see = tok >= vlo[c] && tok < vhi[c] && !gone;
           seen[c] |= see ? 1u << e : 0u;
-          sc[c][e >> 2][e & 3] = see ? sc[c][e >> 2][e & 3] * sk : -INFINITY;
+          sc[c][e >> 2][e & 3] = see ? sc[c][e >> 2][e & 3] * a.scale2 : -INFINITY;
         }
       } else {
 #pragma unroll
-        for (int e = 0; e < 16; e++) sc[c][e >> 2][e & 3] *= sk;
+        for (int e = 0; e < 16; e++) sc[c][e >> 2][e & 3] *= a.scale2;
       }
 #pragma unroll
       for (int e = 0; e < 16; e++) mx = fmaxf(mx, sc[c][e >> 2][e & 3]);
@@ -231,7 +234,7 @@ __global__ __launch_bounds__(64 * dec_waves(D, NC)) void attn_decode(AttnArgs a)
         l[c] += p[e];
       }
 #pragma unroll
-      for (int e = 0; e < 16; e++) pf[c][e >> 3][e & 7] = (__bf16)(p[e] * (seen[c] ? sv : 0.f));
+      for (int e = 0; e < 16; e++) pf[c][e >> 3][e & 7] = (__bf16)p[e];
     }
     if (part) {
       // Tokens no row sees: their codes may be anything, so they become 0.
@@ -279,7 +282,7 @@ __global__ __launch_bounds__(64 * dec_waves(D, NC)) void attn_decode(AttnArgs a)
     }
 #pragma unroll
     for (int d = 0; d < DT; d++) {
-      const v8bf v0 = bf16x8_of_e4m3(vr[d].x, vr[d].y), v1 = bf16x8_of_e4m3(vr[d].z, vr[d].w);
+      const v8bf v0 = bf16x8_of_e4m3(vr[d].x, vr[d].y, sv), v1 = bf16x8_of_e4m3(vr[d].z, vr[d].w, sv);
 #pragma unroll
       for (int c = 0; c < NC; c++) {
         o[c][d] = mfma(v0, pf[c][0], o[c][d]);
@@ -416,14 +419,313 @@ __global__ __launch_bounds__(64 * dec_waves(D, NC)) void attn_decode(AttnArgs a)
   }
 }
 
+// ------------------------------------------------------------- many rows
+// One workgroup per (sequence, key head, 16 NC WAVES rows).  A step's keys and
+// values (64 tokens) are widened to bf16 once for all waves, while the
+// previous step is multiplied, and lie in LDS as whole MFMA operands: 1 KiB
+// per 16 rows x 32 k, lane (i, g)'s 16 bytes at place 4 i + (g + i / 4) % 4,
+// which spreads both the writes (neighbouring lanes: one row, all g) and the
+// reads (neighbouring lanes: one g, all rows) over the banks.
+template <int D, int NC, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void attn_prompt(AttnArgs a) {
+  constexpr int DS = D / 32, DT = D / 16, KP = D / (16 * WAVES);
+  static_assert(KP * 16 * WAVES == D, "whole 16-byte pieces per thread");
+  constexpr int KB = 4 * DS * 1024, VB = DT * 2048;
+  __shared__ __attribute__((aligned(16))) uint8_t kv_[2][KB + VB];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int n = lane & 15, g = lane >> 4;
+  // pairs (sequence, head) run fastest, so that an XCD (bid % 8) keeps few of
+  // them in its L2; the last, longest row tiles start first
+  const int64_t pairs = a.kv.n_seqs * a.kv.H, bid = blockIdx.x, pair = bid % pairs;
+  const int64_t rt = a.RT - 1 - bid / pairs, b = pair / a.kv.H;
+  const int h = (int)(pair % a.kv.H);
+  const SeqSpan s = seq_span(a.kv, b);
+  const int64_t R = (int64_t)s.n * a.G, wg0 = rt * 16 * NC * WAVES;
+  if (wg0 >= R) return;
+  const int len = s.len, first = len - s.n, P = 1 << a.kv.lp;
+
+  // what rows [r0, r1) see between them: some of them [lo, hi), all of them [lo_all, hi_all)
+  auto range = [&](int64_t r0, int64_t r1, int* lo, int* hi, int* lo_all, int* hi_all) {
+    r0 = r0 < R - 1 ? r0 : R - 1;
+    r1 = r1 < R ? r1 : R;
+    const int p0 = first + (int)(r0 / a.G), p1 = first + (int)((r1 - 1) / a.G);
+    *hi = a.causal ? max(0, min(len, p1 + 1)) : len;
+    *hi_all = a.causal ? max(0, min(len, p0 + 1)) : len;
+    *lo = a.window > 0 ? max(0, p0 - a.window + 1) : 0;
+    *lo_all = a.window > 0 ? max(0, p1 - a.window + 1) : 0;
+  };
+  int wlo, whi, wlo_all, whi_all, lo_min, hi_max, lo_all, hi_all;
+  const int64_t rho0 = wg0 + wave * 16 * NC;
+  range(wg0, wg0 + 16 * NC * WAVES, &lo_min, &hi_max, &lo_all, &hi_all);
+  range(rho0, rho0 + 16 * NC, &wlo, &whi, &wlo_all, &whi_all);
+  whi = __builtin_amdgcn_readfirstlane(rho0 < R ? whi : 0);
+  int64_t rho[NC];
+  int vlo[NC], vhi[NC];
+  v8bf qf[NC][DS];
+#pragma unroll
+  for (int c = 0; c < NC; c++) {
+    rho[c] = rho0 + 16 * c + n;
+    const int64_t rc = rho[c] < R ? rho[c] : R - 1;
+    const int p = first + (int)(rc / a.G);
+    vhi[c] = a.causal ? min(len, p + 1) : len;
+    vlo[c] = a.window > 0 ? max(0, p - a.window + 1) : 0;
+    const uint16_t* qp = a.q + (s.row0 + rc / a.G) * a.q_stride + (h * a.G + rc % a.G) * D + 16 * g;
+#pragma unroll
+    for (int d = 0; d < DS; d++) {  // dims 64 (d / 2) + 16 g + 8 (d % 2) .. + 7
+      mx_u4 w = *(const mx_u4*)(qp + 64 * (d >> 1) + 8 * (d & 1));
+      if (a.scale2 < 0.f) w ^= 0x80008000u;  // (-q) k |scale|: the maximum below wants a scale >= 0
+      qf[c][d] = __builtin_bit_cast(v8bf, w);
+    }
+  }
+  const float scale = fabsf(a.scale2);
+  v4f o[NC][DT];
+  float m[NC], l[NC];
+  uint64_t nanned[NC];  // bit 4 d + e: o[c][d][e] meets a NaN value
+#pragma unroll
+  for (int c = 0; c < NC; c++) {
+    m[c] = -INFINITY;
+    l[c] = 0.f;
+    nanned[c] = 0;
+#pragma unroll
+    for (int d = 0; d < DT; d++) o[c][d] = v4f{0.f, 0.f, 0.f, 0.f};
+  }
+
+  const int u0 = lo_min / kUnit, u1 = (hi_max + kUnit - 1) / kUnit;
+  const int32_t* table = a.kv.table + b * a.kv.width;
+  const int64_t page_bytes = (int64_t)D << a.kv.lp;
+  // page of 16 tokens: lanes with lane % 4 = x hold that of tokens 64 u + 16 x ..
+  auto pages = [&](int u) -> int {
+    const int t = u * kUnit + 16 * (lane & 3);
+    if (t >= hi_max) return -1;
+    const int pg = table[t >> a.kv.lp];
+    return pg >= 0 && pg < a.kv.n_pages ? pg : -2;
+  };
+  // this thread's pieces of a step.  Keys: 16 dims of a token; values: 16 tokens of a dim
+  mx_u4 kr[KP], vr[KP];
+  uint32_t kb[KP], vb;
+  int vpage;
+  auto fetch = [&](int u, int pg) {
+#pragma unroll
+    for (int i = 0; i < KP; i++) {
+      const int x = tid + 64 * WAVES * i, tok = x / (D / 16), dim = (x % (D / 16)) * 16;
+      const int pk = __shfl(pg, tok >> 4);
+      const int64_t ph = (int64_t)(pk < 0 ? 0 : pk) * a.kv.H + h;
+      kr[i] = *(const mx_u4*)(a.kv.kc + ph * page_bytes + ((u * kUnit + tok) & (P - 1)) * D + dim);
+      kb[i] = a.kv.ks[ph];
+    }
+    vpage = pg;  // tid % 4 = lane % 4
+    const int64_t ph = (int64_t)(pg < 0 ? 0 : pg) * a.kv.H + h;
+    const uint8_t* vp = a.kv.vc + ph * page_bytes + ((u * kUnit + 16 * (tid & 3)) & (P - 1));
+    vb = a.kv.vs[ph];
+#pragma unroll
+    for (int i = 0; i < KP; i++) vr[i] = *(const mx_u4*)(vp + (int64_t)((tid >> 2) + 16 * WAVES * i) * P);
+  };
+  // widened and written to a buffer; whether NaN codes were put aside
+  auto stage = [&](int u, uint8_t* buf, bool part) -> bool {
+    bool nans = false;
+#pragma unroll
+    for (int i = 0; i < KP; i++) {
+      const int x = tid + 64 * WAVES * i, tok = x / (D / 16), c16 = x % (D / 16);
+      // token 16 g' + 4 t + j is row 4 g' + j of tile t; dims 16 c16 ..: operands 2 (c16 / 4) + half, group c16 % 4
+      const int t = (tok & 15) >> 2, row = 4 * (tok >> 4) + (tok & 3), gg = c16 & 3;
+      uint8_t* w = buf + ((t * DS + 2 * (c16 >> 2)) * 64 + 4 * row + ((gg + (row >> 2)) & 3)) * 16;
+      const float sc = pow2_byte(kb[i]);
+      *(v8bf*)w = bf16x8_of_e4m3(kr[i].x, kr[i].y, sc);
+      *(v8bf*)(w + 1024) = bf16x8_of_e4m3(kr[i].z, kr[i].w, sc);
+    }
+    const float sc = pow2_byte(vb);
+    const int gg = tid & 3, T = u * kUnit + 16 * gg;
+    uint32_t keep[4];
+    if (part) {
+      const int lo = vpage < 0 ? 16 : lo_min - T, hi = hi_max - T;
+#pragma unroll
+      for (int e = 0; e < 4; e++) keep[e] = byte_range(lo - 4 * e, hi - 4 * e);
+    }
+#pragma unroll
+    for (int i = 0; i < KP; i++) {
+      const int d = (tid >> 2) + 16 * WAVES * i, row = d & 15;
+      if (part) {
+        // codes of tokens no row sees become 0; NaN codes too, and are put
+        // back behind the products for the rows that see them
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+          vr[i][e] &= keep[e];
+          const uint32_t nb = nan_bytes(vr[i][e]);
+          nans |= nb != 0;
+          vr[i][e] &= ~((nb >> 7) * 0xFFu);
+        }
+      }
+      uint8_t* w = buf + KB + ((d >> 4) * 128 + 4 * row + ((gg + (row >> 2)) & 3)) * 16;
+      *(v8bf*)w = bf16x8_of_e4m3(vr[i].x, vr[i].y, vpage < 0 ? 0.f : sc);
+      *(v8bf*)(w + 1024) = bf16x8_of_e4m3(vr[i].z, vr[i].w, vpage < 0 ? 0.f : sc);
+    }
+    return nans;
+  };
+  // tokens some row of the workgroup does not see, or that cannot be read
+  auto partial = [&](int u, int pg) { return u * kUnit + kUnit > hi_all || u * kUnit < lo_all || __any(pg < 0); };
+  auto count_bad = [&](int pg) {
+    if (pg == -2 && wave == 0 && lane < 4 && a.kv.bad) atomicAdd(a.kv.bad, 1);
+  };
+
+  int pg0 = u0 < u1 ? pages(u0) : -1, pg1 = u0 + 1 < u1 ? pages(u0 + 1) : -1;
+  bool part = false, nan_now = false;
+  if (u0 < u1) {
+    fetch(u0, pg0);
+    part = partial(u0, pg0);
+    const bool nn = stage(u0, kv_[0], part);
+    if (part) nan_now = __syncthreads_or(nn);
+    else __syncthreads();
+  }
+  for (int u = u0; u < u1; u++) {
+    const uint8_t* buf = kv_[(u - u0) & 1];
+    const bool more = u + 1 < u1;
+    const int pg2 = u + 2 < u1 ? pages(u + 2) : -1;
+    if (more) fetch(u + 1, pg1);
+    const int T = u * kUnit;
+    if (T < whi && T + kUnit > wlo) {
+      const int at = (4 * n + ((g + (n >> 2)) & 3)) * 16;
+      v4f sc[NC][4];
+#pragma unroll
+      for (int t = 0; t < 4; t++) {
+#pragma unroll
+        for (int c = 0; c < NC; c++) sc[c][t] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int d = 0; d < DS; d++) {
+          const v8bf k = *(const v8bf*)(buf + (t * DS + d) * 1024 + at);
+#pragma unroll
+          for (int c = 0; c < NC; c++) sc[c][t] = mfma(k, qf[c][d], sc[c][t]);
+        }
+      }
+      const bool mask = T + kUnit > whi_all || T < wlo_all || (part && __any(pg0 < 0));
+      const int page = mask ? __shfl(pg0, g) : 0;  // of the lane's 16 tokens
+      v8bf pf[NC][2];
+#pragma unroll
+      for (int c = 0; c < NC; c++) {
+        uint32_t seen = 0xFFFFu;
+        if (mask) {
+          const int lo = page < 0 ? 16 : vlo[c] - (T + 16 * g), hi = vhi[c] - (T + 16 * g);
+          const uint32_t up = hi >= 16 ? 0xFFFFu : hi <= 0 ? 0u : (1u << hi) - 1u;
+          seen = lo >= 16 ? 0u : lo <= 0 ? up : up & ~((1u << lo) - 1u);
+#pragma unroll
+          for (int e = 0; e < 16; e++) sc[c][e >> 2][e & 3] = (seen >> e) & 1u ? sc[c][e >> 2][e & 3] : -INFINITY;
+        }
+        float mx = -INFINITY;
+#pragma unroll
+        for (int e = 0; e < 16; e++) mx = fmaxf(mx, sc[c][e >> 2][e & 3]);
+        mx = fmaxf(mx, __shfl_xor(mx, 16));
+        mx = fmaxf(mx, __shfl_xor(mx, 32));
+        mx = mx == -INFINITY ? mx : mx * scale;
+        const float mn = fmaxf(m[c], mx), mu = mn == -INFINITY ? 0.f : mn;
+        if (__any(mn != m[c])) {
+          const float al = __builtin_amdgcn_exp2f(m[c] - mu);  // first tokens: 2^-inf = 0
+          m[c] = mn;
+          l[c] *= al;
+#pragma unroll
+          for (int d = 0; d < DT; d++)
+#pragma unroll
+            for (int e = 0; e < 4; e++) o[c][d][e] *= al;
+        }
+        float sum = 0.f;
+#pragma unroll
+        for (int e = 0; e < 16; e++) {
+          float p = __builtin_amdgcn_exp2f(fmaf(sc[c][e >> 2][e & 3], scale, -mu));
+          if (mask) p = (seen >> e) & 1u ? p : 0.f;
+          sum += p;
+          pf[c][e >> 3][e & 7] = (__bf16)p;
+        }
+        l[c] += sum;
+      }
+      if (nan_now) {
+        // rare: a NaN code among tokens that not every row of the workgroup sees
+        const int vp = __shfl(pg0, g);
+        const uint8_t* vc = a.kv.vc + ((int64_t)(vp < 0 ? 0 : vp) * a.kv.H + h) * page_bytes + ((T + 16 * g) & (P - 1));
+#pragma unroll 1
+        for (int d = 0; d < DT; d++) {
+          const mx_u4 w = *(const mx_u4*)(vc + (int64_t)(16 * d + n) * P);
+          v8bf isn[2];
+#pragma unroll
+          for (int e = 0; e < 16; e++)
+            isn[e >> 3][e & 7] = (__bf16)(vp >= 0 && ((nan_bytes(w[e >> 2]) >> (8 * (e & 3) + 7)) & 1u) ? 1.f : 0.f);
+#pragma unroll
+          for (int c = 0; c < NC; c++) {
+            v8bf vis[2];
+#pragma unroll
+            for (int e = 0; e < 16; e++) {
+              const int tok = T + 16 * g + e;
+              vis[e >> 3][e & 7] = (__bf16)(tok >= vlo[c] && tok < vhi[c] ? 1.f : 0.f);
+            }
+            v4f hit = v4f{0.f, 0.f, 0.f, 0.f};
+            hit = mfma(isn[0], vis[0], hit);
+            hit = mfma(isn[1], vis[1], hit);
+#pragma unroll
+            for (int e = 0; e < 4; e++) nanned[c] |= hit[e] > 0.f ? uint64_t(1) << (4 * d + e) : 0;
+          }
+        }
+      }
+#pragma unroll
+      for (int d = 0; d < DT; d++) {
+        const v8bf v0 = *(const v8bf*)(buf + KB + d * 2048 + at), v1 = *(const v8bf*)(buf + KB + d * 2048 + 1024 + at);
+#pragma unroll
+        for (int c = 0; c < NC; c++) {
+          o[c][d] = mfma(v0, pf[c][0], o[c][d]);
+          o[c][d] = mfma(v1, pf[c][1], o[c][d]);
+        }
+      }
+    }
+    if (part) count_bad(pg0);
+    pg0 = pg1;
+    pg1 = pg2;
+    if (more) {
+      part = partial(u + 1, pg0);
+      const bool nn = stage(u + 1, kv_[(u + 1 - u0) & 1], part);
+      if (part) nan_now = __syncthreads_or(nn);
+      else {
+        nan_now = false;
+        __syncthreads();
+      }
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < NC; c++) {
+    l[c] += __shfl_xor(l[c], 16);
+    l[c] += __shfl_xor(l[c], 32);
+    if (rho[c] >= R) continue;
+    const float inv = l[c] > 0.f || l[c] != l[c] ? 1.0f / l[c] : 0.f;
+    const int64_t tok = s.row0 + rho[c] / a.G, hd = h * a.G + rho[c] % a.G;
+    uint16_t* op = a.o + tok * a.o_stride + hd * D + 4 * g;
+#pragma unroll
+    for (int d = 0; d < DT; d++) {
+#pragma unroll
+      for (int e = 0; e < 4; e++)
+        if ((nanned[c] >> (4 * d + e)) & 1) o[c][d][e] = __uint_as_float(0x7FC00000u);
+      uint2 w;
+      w.x = bf16_bits(o[c][d][0] * inv) | (bf16_bits(o[c][d][1] * inv) << 16);
+      w.y = bf16_bits(o[c][d][2] * inv) | (bf16_bits(o[c][d][3] * inv) << 16);
+      *(uint2*)(op + 16 * d) = w;
+    }
+    if (a.lse && g == 0) a.lse[tok * a.Hq + hd] = l[c] == 0.f ? -INFINITY : (m[c] + __builtin_amdgcn_logf(l[c])) * kLn2;
+  }
+}
+
 struct Plan {
-  int nc, S;
+  int nc, S;          // nc 0: attn_prompt
   int64_t RT, tiles, chunk;
 };
+
+constexpr int64_t kPromptRows = 128;
+constexpr int prompt_rows(int D) { return D == 256 ? 128 : 256; }
 
 Plan plan_decode(int D, int H, int64_t n_seqs, int64_t max_q, int64_t max_kv, int64_t G) {
   Plan p;
   const int64_t R = max_q * G;
+  if (R >= kPromptRows) {
+    p.nc = 0;
+    p.S = 1;
+    p.RT = cdiv(R, prompt_rows(D));
+    p.tiles = n_seqs * H * p.RT;
+    p.chunk = 0;
+    return p;
+  }
   p.nc = R > 16 && D <= 128 ? 2 : 1;  // wider heads: the registers of 16 rows
   p.RT = cdiv(R, 16 * p.nc);
   p.tiles = n_seqs * H * p.RT;
@@ -462,6 +764,12 @@ hipError_t launch_attention(AttnArgs a, void* ws, hipStream_t s) {
   a.cnt = (uint32_t*)ws + 16;
   a.part = (float*)((uint8_t*)ws + kCounterBytes);
   const dim3 grid((unsigned)(p.tiles * p.S));
+  if (p.nc == 0) {
+    if (a.kv.D == 64) hipLaunchKernelGGL((attn_prompt<64, 4, 4>), grid, dim3(256), 0, s, a);
+    else if (a.kv.D == 128) hipLaunchKernelGGL((attn_prompt<128, 2, 8>), grid, dim3(512), 0, s, a);
+    else hipLaunchKernelGGL((attn_prompt<256, 2, 4>), grid, dim3(256), 0, s, a);
+    return hipGetLastError();
+  }
 #define LOWBIT_DEC(DD, NN) \
   hipLaunchKernelGGL((attn_decode<DD, NN>), grid, dim3(64 * dec_waves(DD, NN)), 0, s, a)
   if (p.nc == 1) {
