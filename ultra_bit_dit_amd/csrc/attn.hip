@@ -43,6 +43,14 @@ __device__ __forceinline__ float pow2_byte(uint32_t b) {
 __device__ __forceinline__ v4f mfma(const v8bf& a, const v8bf& b, const v4f& c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
+// maximum over the four lanes of a row (n, n + 16, n + 32, n + 48): the swaps
+// leave one of each pair in either result
+__device__ __forceinline__ float group_max(float x) {
+  const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  x = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  const auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
 // bytes of w that are e4m3 NaN codes (0x7F or 0xFF): bit 7 of each
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
   return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
@@ -216,9 +224,7 @@ __global__ __launch_bounds__(64 * dec_waves(D, NC)) void attn_decode(AttnArgs a)
       }
 #pragma unroll
       for (int e = 0; e < 16; e++) mx = fmaxf(mx, sc[c][e >> 2][e & 3]);
-      mx = fmaxf(mx, __shfl_xor(mx, 16));
-      mx = fmaxf(mx, __shfl_xor(mx, 32));
-      const float mn = fmaxf(m[c], mx);
+      const float mn = fmaxf(m[c], group_max(mx));
       const float mu = mn == -INFINITY ? 0.f : mn;
       const float al = __builtin_amdgcn_exp2f(m[c] - mu);  // first tokens: 2^-inf = 0
       m[c] = mn;
@@ -459,6 +465,7 @@ __global__ __launch_bounds__(64 * WAVES) void attn_prompt(AttnArgs a) {
   range(wg0, wg0 + 16 * NC * WAVES, &lo_min, &hi_max, &lo_all, &hi_all);
   range(rho0, rho0 + 16 * NC, &wlo, &whi, &wlo_all, &whi_all);
   whi = __builtin_amdgcn_readfirstlane(rho0 < R ? whi : 0);
+  const bool none = fabsf(a.scale2) < 0x1p-126f;  // all scores 0
   int64_t rho[NC];
   int vlo[NC], vhi[NC];
   v8bf qf[NC][DS];
@@ -473,11 +480,13 @@ __global__ __launch_bounds__(64 * WAVES) void attn_prompt(AttnArgs a) {
 #pragma unroll
     for (int d = 0; d < DS; d++) {  // dims 64 (d / 2) + 16 g + 8 (d % 2) .. + 7
       mx_u4 w = *(const mx_u4*)(qp + 64 * (d >> 1) + 8 * (d & 1));
-      if (a.scale2 < 0.f) w ^= 0x80008000u;  // (-q) k |scale|: the maximum below wants a scale >= 0
+      // the maximum and the mask's -infinity below want a positive scale
+      if (a.scale2 < 0.f) w ^= 0x80008000u;
+      if (none) w &= 0x80008000u;
       qf[c][d] = __builtin_bit_cast(v8bf, w);
     }
   }
-  const float scale = fabsf(a.scale2);
+  const float scale = none ? 1.f : fabsf(a.scale2);
   v4f o[NC][DT];
   float m[NC], l[NC];
   uint64_t nanned[NC];  // bit 4 d + e: o[c][d][e] meets a NaN value
@@ -492,7 +501,6 @@ __global__ __launch_bounds__(64 * WAVES) void attn_prompt(AttnArgs a) {
 
   const int u0 = lo_min / kUnit, u1 = (hi_max + kUnit - 1) / kUnit;
   const int32_t* table = a.kv.table + b * a.kv.width;
-  const int64_t page_bytes = (int64_t)D << a.kv.lp;
   // page of 16 tokens: lanes with lane % 4 = x hold that of tokens 64 u + 16 x ..
   auto pages = [&](int u) -> int {
     const int t = u * kUnit + 16 * (lane & 3);
@@ -500,25 +508,33 @@ __global__ __launch_bounds__(64 * WAVES) void attn_prompt(AttnArgs a) {
     const int pg = table[t >> a.kv.lp];
     return pg >= 0 && pg < a.kv.n_pages ? pg : -2;
   };
-  // this thread's pieces of a step.  Keys: 16 dims of a token; values: 16 tokens of a dim
+  // This thread's pieces of a step.  Keys: 16 dims of a token; values: 16
+  // tokens of a dim.  A wave's keys lie in one group of 16 tokens.
   mx_u4 kr[KP], vr[KP];
   uint32_t kb[KP], vb;
   int vpage;
+  constexpr int kTokenPieces = D / 16;
+  const int sh = a.kv.lp + (D == 64 ? 6 : D == 128 ? 7 : 8);  // log2 of a page's bytes of one head
+  const int tok0 = tid / kTokenPieces, dim0 = (tid % kTokenPieces) * 16;
+  const uint32_t vat = (uint32_t)(tid >> 2) * P + ((16 * (tid & 3)) & (P - 1));
   auto fetch = [&](int u, int pg) {
+    const int in = (u * kUnit) & (P - 1);  // the step's place in a larger page
 #pragma unroll
     for (int i = 0; i < KP; i++) {
-      const int x = tid + 64 * WAVES * i, tok = x / (D / 16), dim = (x % (D / 16)) * 16;
-      const int pk = __shfl(pg, tok >> 4);
+      const int tok = tok0 + (64 * WAVES / kTokenPieces) * i;
+      const int grp = __builtin_amdgcn_readfirstlane(tok >> 4);
+      const int pk = __builtin_amdgcn_readlane(pg, grp);
       const int64_t ph = (int64_t)(pk < 0 ? 0 : pk) * a.kv.H + h;
-      kr[i] = *(const mx_u4*)(a.kv.kc + ph * page_bytes + ((u * kUnit + tok) & (P - 1)) * D + dim);
+      const uint8_t* kp = a.kv.kc + (ph << sh) + in * D;
+      kr[i] = *(const mx_u4*)(kp + (uint32_t)((tok & (P - 1)) * D + dim0));
       kb[i] = a.kv.ks[ph];
     }
     vpage = pg;  // tid % 4 = lane % 4
     const int64_t ph = (int64_t)(pg < 0 ? 0 : pg) * a.kv.H + h;
-    const uint8_t* vp = a.kv.vc + ph * page_bytes + ((u * kUnit + 16 * (tid & 3)) & (P - 1));
+    const uint8_t* vp = a.kv.vc + (ph << sh) + in + vat;
     vb = a.kv.vs[ph];
 #pragma unroll
-    for (int i = 0; i < KP; i++) vr[i] = *(const mx_u4*)(vp + (int64_t)((tid >> 2) + 16 * WAVES * i) * P);
+    for (int i = 0; i < KP; i++) vr[i] = *(const mx_u4*)(vp + (uint32_t)(16 * WAVES * i * P));
   };
   // widened and written to a buffer; whether NaN codes were put aside
   auto stage = [&](int u, uint8_t* buf, bool part) -> bool {
@@ -612,11 +628,11 @@ __global__ __launch_bounds__(64 * WAVES) void attn_prompt(AttnArgs a) {
         float mx = -INFINITY;
 #pragma unroll
         for (int e = 0; e < 16; e++) mx = fmaxf(mx, sc[c][e >> 2][e & 3]);
-        mx = fmaxf(mx, __shfl_xor(mx, 16));
-        mx = fmaxf(mx, __shfl_xor(mx, 32));
-        mx = mx == -INFINITY ? mx : mx * scale;
-        const float mn = fmaxf(m[c], mx), mu = mn == -INFINITY ? 0.f : mn;
-        if (__any(mn != m[c])) {
+        mx = group_max(mx) * scale;
+        // The maximum in use may lag by up to 2^8 (weights up to 256 lose no
+        // precision), so O is rescaled in few of the steps.
+        if (__any(mx > m[c] + 8.f)) {
+          const float mn = fmaxf(m[c], mx), mu = mn == -INFINITY ? 0.f : mn;
           const float al = __builtin_amdgcn_exp2f(m[c] - mu);  // first tokens: 2^-inf = 0
           m[c] = mn;
           l[c] *= al;
@@ -625,11 +641,11 @@ __global__ __launch_bounds__(64 * WAVES) void attn_prompt(AttnArgs a) {
 #pragma unroll
             for (int e = 0; e < 4; e++) o[c][d][e] *= al;
         }
+        const float mu = m[c] == -INFINITY ? 0.f : m[c];
         float sum = 0.f;
 #pragma unroll
         for (int e = 0; e < 16; e++) {
-          float p = __builtin_amdgcn_exp2f(fmaf(sc[c][e >> 2][e & 3], scale, -mu));
-          if (mask) p = (seen >> e) & 1u ? p : 0.f;
+          const float p = __builtin_amdgcn_exp2f(fmaf(sc[c][e >> 2][e & 3], scale, -mu));  // masked: 2^-inf = 0
           sum += p;
           pf[c][e >> 3][e & 7] = (__bf16)p;
         }
@@ -638,7 +654,7 @@ __global__ __launch_bounds__(64 * WAVES) void attn_prompt(AttnArgs a) {
       if (nan_now) {
         // rare: a NaN code among tokens that not every row of the workgroup sees
         const int vp = __shfl(pg0, g);
-        const uint8_t* vc = a.kv.vc + ((int64_t)(vp < 0 ? 0 : vp) * a.kv.H + h) * page_bytes + ((T + 16 * g) & (P - 1));
+        const uint8_t* vc = a.kv.vc + (((int64_t)(vp < 0 ? 0 : vp) * a.kv.H + h) << sh) + ((T + 16 * g) & (P - 1));
 #pragma unroll 1
         for (int d = 0; d < DT; d++) {
           const mx_u4 w = *(const mx_u4*)(vc + (int64_t)(16 * d + n) * P);
