@@ -64,9 +64,47 @@ __device__ __forceinline__ uint32_t byte_range(int lo, int hi) {
   return up & ~((1u << (8 * lo)) - 1u);  // lo < 4 here
 }
 
+// The work item of index k when sequence b has count(b) of them, in the order
+// of the sequences: sets b and its item, or returns false past the last one.
+// Workgroups are numbered over the items that exist (the host only knows
+// bounds): empty ones between full ones would not be spread evenly, as
+// workgroups go to the shader engines in turn whether or not they have work.
+// Every wave finds it for itself, 64 sequences at a time.
+template <class Count>
+__device__ __forceinline__ bool find_item(int64_t n_seqs, int64_t k, Count count, int64_t* b, int64_t* item) {
+  const int lane = threadIdx.x & 63;
+  for (int64_t b0 = 0; b0 < n_seqs; b0 += 64) {
+    const int mine = b0 + lane < n_seqs ? (int)count(b0 + lane) : 0;
+    int sum = mine;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int v = __shfl_up(sum, d);
+      sum += lane >= d ? v : 0;
+    }
+    const uint64_t past = __ballot((int64_t)sum > k);
+    if (past) {
+      const int l = __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)past) - 1);
+      *b = b0 + l;
+      *item = k - (__builtin_amdgcn_readlane(sum, l) - __builtin_amdgcn_readlane(mine, l));
+      return true;
+    }
+    k -= __builtin_amdgcn_readlane(sum, 63);
+  }
+  return false;
+}
+
 // Few rows: one workgroup of WAVES waves per (sequence, key head, 16 NC rows,
 // split of the tokens); the waves take 64-token steps in turn and every wave
 // reads the codes it needs straight from the cache into registers.
+// Splits that cover what any row of a sequence sees (at least one).
+__device__ __forceinline__ int splits_of(const AttnArgs& a, int len, int n) {
+  if (a.S == 1) return 1;
+  int64_t most = len;
+  if (a.window > 0 && a.causal) most = min<int64_t>(most, (int64_t)a.window + n);
+  const int64_t k = (most + kUnit - 1 + a.chunk - 1) / a.chunk;
+  return k < 1 ? 1 : (int)k;
+}
+
 // Eight waves a compute unit where a wave fits 256 registers, else four.
 constexpr int dec_waves(int D, int NC) { return D * NC >= 256 ? 4 : 8; }
 constexpr int kChunkUnit = 8 * kUnit;  // a split is whole turns of up to eight waves
@@ -80,14 +118,19 @@ __global__ __launch_bounds__(64 * dec_waves(D, NC)) void attn_decode(AttnArgs a)
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 15, g = lane >> 4;
   const int64_t bid = blockIdx.x;
-  const int sp = (int)(bid % a.S);
-  const int64_t tile = bid / a.S;
-  const int h = (int)(tile % a.kv.H);
-  const int64_t rt = (tile / a.kv.H) % a.RT, b = tile / a.kv.H / a.RT;
+  const int h = (int)(bid % a.kv.H);
+  int64_t b, item;
+  const bool some = find_item(a.kv.n_seqs, bid / a.kv.H, [&](int64_t i) {
+    const SeqSpan t = seq_span(a.kv, i);
+    const int64_t tiles = (t.n * a.G + 16 * NC - 1) / (16 * NC);
+    return tiles * splits_of(a, t.len, t.n);
+  }, &b, &item);
+  if (!some) return;
   const SeqSpan s = seq_span(a.kv, b);
+  const int splits = splits_of(a, s.len, s.n), sp = (int)(item % splits);
+  const int64_t rt = item / splits, tile = (b * a.kv.H + h) * a.RT + rt;
   const int64_t R = (int64_t)s.n * a.G;
   const int64_t rho0 = rt * 16 * NC;
-  if (rho0 >= R) return;
   const int len = s.len, first = len - s.n;  // position of the first new token
   const int P = 1 << a.kv.lp;
 
@@ -440,14 +483,16 @@ __global__ __launch_bounds__(64 * WAVES) void attn_prompt(AttnArgs a) {
   __shared__ __attribute__((aligned(16))) uint8_t kv_[2][KB + VB];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n = lane & 15, g = lane >> 4;
-  // pairs (sequence, head) run fastest, so that an XCD (bid % 8) keeps few of
-  // them in its L2; the last, longest row tiles start first
-  const int64_t pairs = a.kv.n_seqs * a.kv.H, bid = blockIdx.x, pair = bid % pairs;
-  const int64_t rt = a.RT - 1 - bid / pairs, b = pair / a.kv.H;
-  const int h = (int)(pair % a.kv.H);
+  // heads run fastest, so that an XCD (bid % 8) keeps few of them in its L2;
+  // the last, longest row tiles of a sequence start first
+  constexpr int ROWS = 16 * NC * WAVES;
+  const int64_t bid = blockIdx.x;
+  const int h = (int)(bid % a.kv.H);
+  int64_t b, item;
+  auto tiles = [&](int64_t i) { return (seq_span(a.kv, i).n * a.G + ROWS - 1) / ROWS; };
+  if (!find_item(a.kv.n_seqs, bid / a.kv.H, tiles, &b, &item)) return;
   const SeqSpan s = seq_span(a.kv, b);
-  const int64_t R = (int64_t)s.n * a.G, wg0 = rt * 16 * NC * WAVES;
-  if (wg0 >= R) return;
+  const int64_t R = (int64_t)s.n * a.G, wg0 = ((R + ROWS - 1) / ROWS - 1 - item) * ROWS;
   const int len = s.len, first = len - s.n, P = 1 << a.kv.lp;
 
   // what rows [r0, r1) see between them: some of them [lo, hi), all of them [lo_all, hi_all)
@@ -601,16 +646,29 @@ __global__ __launch_bounds__(64 * WAVES) void attn_prompt(AttnArgs a) {
     if (T < whi && T + kUnit > wlo) {
       const int at = (4 * n + ((g + (n >> 2)) & 3)) * 16;
       v4f sc[NC][4];
+      // operands are read one tile ahead of their products
+      v8bf kf[2][DS], vf[2][4];
+      auto read_k = [&](int t) {
+#pragma unroll
+        for (int d = 0; d < DS; d++) kf[t & 1][d] = *(const v8bf*)(buf + (t * DS + d) * 1024 + at);
+      };
+      auto read_v = [&](int d) {  // two tiles of 16 dims
+#pragma unroll
+        for (int e = 0; e < 4; e++) vf[(d >> 1) & 1][e] = *(const v8bf*)(buf + KB + d * 2048 + e * 1024 + at);
+      };
+      read_k(0);
 #pragma unroll
       for (int t = 0; t < 4; t++) {
+        if (t < 3) read_k(t + 1);
+        else read_v(0);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int c = 0; c < NC; c++) sc[c][t] = v4f{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int d = 0; d < DS; d++) {
-          const v8bf k = *(const v8bf*)(buf + (t * DS + d) * 1024 + at);
+        for (int d = 0; d < DS; d++)
 #pragma unroll
-          for (int c = 0; c < NC; c++) sc[c][t] = mfma(k, qf[c][d], sc[c][t]);
-        }
+          for (int c = 0; c < NC; c++) sc[c][t] = mfma(kf[t & 1][d], qf[c][d], sc[c][t]);
+        __builtin_amdgcn_sched_barrier(0);
       }
       const bool mask = T + kUnit > whi_all || T < wlo_all || (part && __any(pg0 < 0));
       const int page = mask ? __shfl(pg0, g) : 0;  // of the lane's 16 tokens
@@ -642,14 +700,14 @@ __global__ __launch_bounds__(64 * WAVES) void attn_prompt(AttnArgs a) {
             for (int e = 0; e < 4; e++) o[c][d][e] *= al;
         }
         const float mu = m[c] == -INFINITY ? 0.f : m[c];
-        float sum = 0.f;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int e = 0; e < 16; e++) {
           const float p = __builtin_amdgcn_exp2f(fmaf(sc[c][e >> 2][e & 3], scale, -mu));  // masked: 2^-inf = 0
-          sum += p;
+          sum[e & 3] += p;
           pf[c][e >> 3][e & 7] = (__bf16)p;
         }
-        l[c] += sum;
+        l[c] += (sum[0] + sum[1]) + (sum[2] + sum[3]);
       }
       if (nan_now) {
         // rare: a NaN code among tokens that not every row of the workgroup sees
@@ -679,13 +737,14 @@ __global__ __launch_bounds__(64 * WAVES) void attn_prompt(AttnArgs a) {
         }
       }
 #pragma unroll
-      for (int d = 0; d < DT; d++) {
-        const v8bf v0 = *(const v8bf*)(buf + KB + d * 2048 + at), v1 = *(const v8bf*)(buf + KB + d * 2048 + 1024 + at);
+      for (int d = 0; d < DT; d += 2) {
+        if (d + 2 < DT) read_v(d + 2);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int c = 0; c < NC; c++) {
-          o[c][d] = mfma(v0, pf[c][0], o[c][d]);
-          o[c][d] = mfma(v1, pf[c][1], o[c][d]);
-        }
+        for (int e = 0; e < 4; e++)
+#pragma unroll
+          for (int c = 0; c < NC; c++) o[c][d + (e >> 1)] = mfma(vf[(d >> 1) & 1][e], pf[c][e & 1], o[c][d + (e >> 1)]);
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
     if (part) count_bad(pg0);
@@ -726,12 +785,13 @@ __global__ __launch_bounds__(64 * WAVES) void attn_prompt(AttnArgs a) {
 struct Plan {
   int nc, S;          // nc 0: attn_prompt
   int64_t RT, tiles, chunk;
+  int64_t blocks;     // workgroups: a bound on the work items
 };
 
 constexpr int64_t kPromptRows = 128;
 constexpr int prompt_rows(int D) { return D == 256 ? 128 : 256; }
 
-Plan plan_decode(int D, int H, int64_t n_seqs, int64_t max_q, int64_t max_kv, int64_t G) {
+Plan plan_decode(int D, int H, int64_t n_seqs, int64_t total_q, int64_t max_q, int64_t max_kv, int64_t G) {
   Plan p;
   const int64_t R = max_q * G;
   if (R >= kPromptRows) {
@@ -740,6 +800,7 @@ Plan plan_decode(int D, int H, int64_t n_seqs, int64_t max_q, int64_t max_kv, in
     p.RT = cdiv(R, prompt_rows(D));
     p.tiles = n_seqs * H * p.RT;
     p.chunk = 0;
+    p.blocks = H * min(n_seqs * p.RT, total_q * G / prompt_rows(D) + n_seqs);
     return p;
   }
   p.nc = R > 16 && D <= 128 ? 2 : 1;  // wider heads: the registers of 16 rows
@@ -756,30 +817,33 @@ Plan plan_decode(int D, int H, int64_t n_seqs, int64_t max_q, int64_t max_kv, in
     p.S = 1;
     p.chunk = cdiv(max_kv + kUnit, kUnit) * kUnit;
   }
+  // every item that any contents of the device arrays can name: a split that
+  // did not run would leave its tile's arrivals uncounted
+  p.blocks = p.tiles * p.S;
   return p;
 }
 
 }  // namespace
 
-int64_t attention_blocks(int D, int H, int64_t n_seqs, int64_t max_q, int64_t max_kv, int64_t G) {
-  const Plan p = plan_decode(D, H, n_seqs, max_q, max_kv, G);
-  return p.tiles * p.S;
+int64_t attention_blocks(int D, int H, int64_t n_seqs, int64_t total_q, int64_t max_q, int64_t max_kv, int64_t G) {
+  const Plan p = plan_decode(D, H, n_seqs, total_q, max_q, max_kv, G);
+  return p.blocks;
 }
 
-size_t attention_workspace_bytes(int D, int H, int64_t n_seqs, int64_t max_q, int64_t max_kv, int64_t G) {
-  const Plan p = plan_decode(D, H, n_seqs, max_q, max_kv, G);
+size_t attention_workspace_bytes(int D, int H, int64_t n_seqs, int64_t total_q, int64_t max_q, int64_t max_kv, int64_t G) {
+  const Plan p = plan_decode(D, H, n_seqs, total_q, max_q, max_kv, G);
   if (p.S == 1) return kCounterBytes;
   return (size_t)kCounterBytes + (size_t)(p.tiles * p.S * 16 * p.nc * (D + 2)) * 4;
 }
 
 hipError_t launch_attention(AttnArgs a, void* ws, hipStream_t s) {
-  const Plan p = plan_decode(a.kv.D, a.kv.H, a.kv.n_seqs, a.kv.max_q, a.kv.max_kv, a.G);
+  const Plan p = plan_decode(a.kv.D, a.kv.H, a.kv.n_seqs, a.kv.total_q, a.kv.max_q, a.kv.max_kv, a.G);
   a.RT = p.RT;
   a.S = p.S;
   a.chunk = p.chunk;
   a.cnt = (uint32_t*)ws + 16;
   a.part = (float*)((uint8_t*)ws + kCounterBytes);
-  const dim3 grid((unsigned)(p.tiles * p.S));
+  const dim3 grid((unsigned)p.blocks);
   if (p.nc == 0) {
     if (a.kv.D == 64) hipLaunchKernelGGL((attn_prompt<64, 4, 4>), grid, dim3(256), 0, s, a);
     else if (a.kv.D == 128) hipLaunchKernelGGL((attn_prompt<128, 2, 8>), grid, dim3(512), 0, s, a);
