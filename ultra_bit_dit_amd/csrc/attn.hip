@@ -64,75 +64,133 @@ __device__ __forceinline__ uint32_t byte_range(int lo, int hi) {
   return up & ~((1u << (8 * lo)) - 1u);  // lo < 4 here
 }
 
-// The work item of index k when sequence b has count(b) of them, in the order
-// of the sequences: sets b and its item, or returns false past the last one.
-// Workgroups are numbered over the items that exist (the host only knows
-// bounds): empty ones between full ones would not be spread evenly, as
+// Work items numbered in the order of the sequences, sequence b having
+// count(b) of them: each thread sums a run of sequences, one scan joins them.
+// Workgroups are numbered over the work that exists (the host only knows
+// bounds): empty workgroups between full ones would not be spread evenly, as
 // workgroups go to the shader engines in turn whether or not they have work.
-// Every wave finds it for itself, 64 sequences at a time.
-template <class Count>
-__device__ __forceinline__ bool find_item(int64_t n_seqs, int64_t k, Count count, int64_t* b, int64_t* item) {
-  const int lane = threadIdx.x & 63;
-  for (int64_t b0 = 0; b0 < n_seqs; b0 += 64) {
-    const int mine = b0 + lane < n_seqs ? (int)count(b0 + lane) : 0;
-    int sum = mine;
+template <int THREADS, class Count>
+struct ItemScan {
+  Count count;
+  int64_t n_seqs, per, first, mine, total;  // this thread's run: its first item and their number
+  int64_t* lds;                             // [THREADS / 64 + 2]
+
+  __device__ __forceinline__ ItemScan(int64_t n, Count c, int64_t* mem) : count(c), n_seqs(n), lds(mem) {
+    const int tid = threadIdx.x, lane = tid & 63;
+    per = (n_seqs + THREADS - 1) / THREADS;
+    mine = 0;
+    for (int64_t b = tid * per; b < min(n_seqs, (tid + 1) * per); b++) mine += count(b);
+    int64_t sum = mine;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
-      const int v = __shfl_up(sum, d);
+      const int64_t v = __shfl_up((long long)sum, d);
       sum += lane >= d ? v : 0;
     }
-    const uint64_t past = __ballot((int64_t)sum > k);
-    if (past) {
-      const int l = __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)past) - 1);
-      *b = b0 + l;
-      *item = k - (__builtin_amdgcn_readlane(sum, l) - __builtin_amdgcn_readlane(mine, l));
-      return true;
+    if (lane == 63) lds[tid >> 6] = sum;
+    __syncthreads();
+    int64_t before = 0;
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 64; w++) {
+      before += w < (tid >> 6) ? lds[w] : 0;
+      total += lds[w];
     }
-    k -= __builtin_amdgcn_readlane(sum, 63);
+    first = before + sum - mine;
   }
-  return false;
+  // sequence and item in it of index k < total (the whole workgroup calls it)
+  __device__ __forceinline__ void find(int64_t k, int64_t* b, int64_t* item) {
+    if (k >= first && k < first + mine) {
+      int64_t i = threadIdx.x * per, left = k - first;
+      for (;; i++) {
+        const int64_t c = count(i);
+        if (left < c) break;
+        left -= c;
+      }
+      lds[THREADS / 64] = i;
+      lds[THREADS / 64 + 1] = left;
+    }
+    __syncthreads();
+    *b = uniform64(lds[THREADS / 64]);
+    *item = uniform64(lds[THREADS / 64 + 1]);
+    __syncthreads();
+  }
+};
+
+// Few rows.  A tile is 16 NC rows of one sequence and key head, its work the
+// 64-token steps any of them sees.  A fixed number of workgroups take equal,
+// contiguous shares of all steps of all tiles; a workgroup's waves take the
+// steps of a tile in turn, and every wave reads the codes it needs straight
+// from the cache into registers.  A tile that lies in several shares is joined
+// by the workgroup that ends last.
+constexpr int kJoinLoads = 8;   // results of a pair of outputs read at once
+constexpr int kMaxJoin = 32;    // results joined by one workgroup: shares of a tile <= kMaxJoin^2
+constexpr int kMaxShares = 512;
+
+// two floats, device-coherent
+__device__ __forceinline__ void put2(float* p, float x, float y) {
+  __hip_atomic_store((uint64_t*)p, (uint64_t)__float_as_uint(x) | ((uint64_t)__float_as_uint(y) << 32),
+                     __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ float2 get2(const float* p) {
+  const uint64_t v = __hip_atomic_load((const uint64_t*)p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  return make_float2(__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32)));
 }
 
-// Few rows: one workgroup of WAVES waves per (sequence, key head, 16 NC rows,
-// split of the tokens); the waves take 64-token steps in turn and every wave
-// reads the codes it needs straight from the cache into registers.
-// Splits that cover what any row of a sequence sees (at least one).
-__device__ __forceinline__ int splits_of(const AttnArgs& a, int len, int n) {
-  if (a.S == 1) return 1;
-  int64_t most = len;
-  if (a.window > 0 && a.causal) most = min<int64_t>(most, (int64_t)a.window + n);
-  const int64_t k = (most + kUnit - 1 + a.chunk - 1) / a.chunk;
-  return k < 1 ? 1 : (int)k;
-}
-
-// Eight waves a compute unit where a wave fits 256 registers, else four.
-constexpr int dec_waves(int D, int NC) { return D * NC >= 256 ? 4 : 8; }
-constexpr int kChunkUnit = 8 * kUnit;  // a split is whole turns of up to eight waves
+// Four waves, so that two workgroups share a compute unit where a wave fits
+// 256 registers and one starts or ends while the other reads.
+constexpr int kDecWaves = 4;
 
 template <int D, int NC>
-__global__ __launch_bounds__(64 * dec_waves(D, NC)) void attn_decode(AttnArgs a) {
-  constexpr int DC = D / 64, DT = D / 16, kDecWaves = dec_waves(D, NC);
+__global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_decode(AttnArgs a) {
+  constexpr int DC = D / 64, DT = D / 16;
   __shared__ __attribute__((aligned(16))) float lo_[kDecWaves / 2][NC * 16 * D];  // partial O of half the waves
   __shared__ float lm_[kDecWaves][NC * 16], ll_[kDecWaves][NC * 16];
+  __shared__ int64_t scan_[kDecWaves + 2];
   __shared__ uint32_t s_last;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 15, g = lane >> 4;
-  const int64_t bid = blockIdx.x;
-  const int h = (int)(bid % a.kv.H);
-  int64_t b, item;
-  const bool some = find_item(a.kv.n_seqs, bid / a.kv.H, [&](int64_t i) {
+  const int P = 1 << a.kv.lp;
+  // steps of one tile of a sequence (at least one, which writes its rows), and its tiles
+  auto steps_of = [&](const SeqSpan& t) -> int64_t {
+    int64_t most = t.len;
+    if (a.window > 0 && a.causal) most = min(most, (int64_t)a.window + t.n + kUnit);
+    return max((most + kUnit - 1) / kUnit, (int64_t)1);
+  };
+  auto tiles_of = [&](const SeqSpan& t) -> int64_t { return (t.n * a.G + 16 * NC - 1) / (16 * NC); };
+  auto work_of = [&](int64_t i) -> int64_t {
     const SeqSpan t = seq_span(a.kv, i);
-    const int64_t tiles = (t.n * a.G + 16 * NC - 1) / (16 * NC);
-    return tiles * splits_of(a, t.len, t.n);
-  }, &b, &item);
-  if (!some) return;
-  const SeqSpan s = seq_span(a.kv, b);
-  const int splits = splits_of(a, s.len, s.n), sp = (int)(item % splits);
-  const int64_t rt = item / splits, tile = (b * a.kv.H + h) * a.RT + rt;
+    return tiles_of(t) * steps_of(t);
+  };
+  ItemScan<64 * kDecWaves, decltype(work_of)> scan(a.kv.n_seqs, work_of, scan_);
+  const int64_t per_head = scan.total, total = per_head * a.kv.H;
+  // Shares: one for each four steps (one a wave), as many as tiles if that is
+  // more, at most the launch's workgroups.
+  const int64_t want = max(total / kDecWaves, min(total, a.tiles));
+  const int64_t shares = max(min(want, (int64_t)gridDim.x), (int64_t)1);
+  // neighbouring shares on one XCD (bid % 8) where every workgroup has one
+  const int64_t per_xcd = gridDim.x / 8, bid = blockIdx.x;
+  const int64_t share = shares == (int64_t)gridDim.x ? (bid % 8) * per_xcd + bid / 8 : bid;
+  if (share >= shares) return;
+  int64_t x = total * share / shares;
+  const int64_t x_end = total * (share + 1) / shares;
+  if (x >= x_end) return;
+  int h = (int)(x / per_head);
+  int64_t b, item;
+  scan.find(x % per_head, &b, &item);
+  SeqSpan s = seq_span(a.kv, b);
+  int64_t steps = steps_of(s), tiles = tiles_of(s);
+  int64_t rt = item / steps;
+  int at = (int)(item % steps);  // first step of this share in the tile
+  for (;;) {
+  const int64_t x0 = x - at;     // the tile's first step among all
+  const int count = (int)min(steps - at, x_end - x);
+  // shares that hold steps of this tile
+  const int64_t share0 = ((x0 + 1) * shares + total - 1) / total - 1;
+  const int64_t share1 = ((x0 + steps) * shares + total - 1) / total - 1;
+  const int n_parts = (int)(share1 - share0 + 1);
   const int64_t R = (int64_t)s.n * a.G;
   const int64_t rho0 = rt * 16 * NC;
   const int len = s.len, first = len - s.n;  // position of the first new token
-  const int P = 1 << a.kv.lp;
 
   // visible tokens of this lane's rows: [vlo, vhi)
   int vlo[NC], vhi[NC];
@@ -158,11 +216,7 @@ __global__ __launch_bounds__(64 * dec_waves(D, NC)) void attn_decode(AttnArgs a)
     vhi[c] = a.causal ? min(len, p + 1) : len;
     vlo[c] = a.window > 0 ? max(0, p - a.window + 1) : 0;
   }
-  const int64_t t0 = (int64_t)(lo_min / kUnit) * kUnit + sp * a.chunk;  // tokens of this split
-  const int64_t t1 = t0 + a.chunk < hi_max ? t0 + a.chunk : hi_max;
-  const int u0 = (int)(t0 / kUnit), u1 = t1 > t0 ? (int)((t1 + kUnit - 1) / kUnit) : u0;
-  const int n_splits = hi_max > lo_min ? (int)((hi_max - (int64_t)(lo_min / kUnit) * kUnit + a.chunk - 1) / a.chunk) : 1;
-  if (sp >= n_splits) return;
+  const int u0 = lo_min / kUnit + at, u1 = min(lo_min / kUnit + at + count, (hi_max + kUnit - 1) / kUnit);
 
   // Q: lane (n, g) holds dims 64 c + 16 g + 8 e .. + 7 of its row
   v8bf qf[NC][DC][2];
@@ -190,17 +244,21 @@ __global__ __launch_bounds__(64 * dec_waves(D, NC)) void attn_decode(AttnArgs a)
   const int32_t* table = a.kv.table + b * a.kv.width;
   const int64_t page_bytes = ((int64_t)D << a.kv.lp);
   // page of the 16 tokens from t on; -1 where there are none or the entry is unusable
-  auto page_at = [&](int t) -> int64_t {
+  auto page_at = [&](int t) -> int {
     if (t >= hi_max) return -1;
-    const int64_t pg = table[t >> a.kv.lp];
+    const int pg = table[t >> a.kv.lp];
     return pg >= 0 && pg < a.kv.n_pages ? pg : -2;
   };
   mx_u4 kr[4][DC], vr[DT];
-  int64_t pgv = -1;
-  uint32_t kb = 0, vb = 0;  // exponent bytes of the lane's keys and values
+  int pgv = -1, pkn = -1, pvn = -1;  // pages: of this step's values, of the next step's keys and values
+  uint32_t kb = 0, vb = 0;           // exponent bytes of the lane's keys and values
+  auto next_pages = [&](int u) {
+    pkn = page_at(u * kUnit + 16 * (n >> 2));
+    pvn = page_at(u * kUnit + 16 * g);
+  };
   auto load_k = [&](int u) {
     const int tk = u * kUnit + 16 * (n >> 2);
-    const int64_t pg = page_at(tk), ph = (pg < 0 ? 0 : pg) * a.kv.H + h;
+    const int64_t ph = (int64_t)(pkn < 0 ? 0 : pkn) * a.kv.H + h;
     const uint8_t* kp = a.kv.kc + ph * page_bytes + (int64_t)((tk & (P - 1)) + (n & 3)) * D + 16 * g;
     kb = a.kv.ks[ph];
 #pragma unroll
@@ -208,20 +266,25 @@ __global__ __launch_bounds__(64 * dec_waves(D, NC)) void attn_decode(AttnArgs a)
 #pragma unroll
       for (int d = 0; d < DC; d++) kr[t][d] = *(const mx_u4*)(kp + 4 * t * D + 64 * d);
   };
-  auto load_v = [&](int u) {
+  auto load_v = [&](int u, int pg) {
     const int tv = u * kUnit + 16 * g;
-    pgv = page_at(tv);
-    const int64_t ph = (pgv < 0 ? 0 : pgv) * a.kv.H + h;
+    pgv = pg;
+    const int64_t ph = (int64_t)(pg < 0 ? 0 : pg) * a.kv.H + h;
     const uint8_t* vp = a.kv.vc + ph * page_bytes + (int64_t)n * P + (tv & (P - 1));
     vb = a.kv.vs[ph];
 #pragma unroll
     for (int d = 0; d < DT; d++) vr[d] = *(const mx_u4*)(vp + (int64_t)16 * d * P);
   };
 
-  int u = u0 + wave;
+  // Loads in flight at any time: the next keys behind the scores of this step,
+  // the next values behind its second product; page numbers a step earlier.
+  int u = u0 + wave, pvu = -1;
   if (u < u1) {
+    next_pages(u);
+    pvu = pvn;
     load_k(u);
-    load_v(u);
+    if (u + kDecWaves < u1) next_pages(u + kDecWaves);
+    load_v(u, pvu);
   }
   for (; u < u1; u += kDecWaves) {
     const bool gone = pgv < 0;  // none of this lane's 16 tokens can be read
@@ -245,7 +308,11 @@ __global__ __launch_bounds__(64 * dec_waves(D, NC)) void attn_decode(AttnArgs a)
         }
       }
     }
-    if (u + kDecWaves < u1) load_k(u + kDecWaves);
+    if (u + kDecWaves < u1) {
+      load_k(u + kDecWaves);
+      pvu = pvn;
+      if (u + 2 * kDecWaves < u1) next_pages(u + 2 * kDecWaves);
+    }
     v8bf pf[NC][2];
     uint32_t seen[NC];  // bit e: token 16 g + e is visible to the lane's row
 #pragma unroll
@@ -338,7 +405,7 @@ __global__ __launch_bounds__(64 * dec_waves(D, NC)) void attn_decode(AttnArgs a)
         o[c][d] = mfma(v1, pf[c][1], o[c][d]);
       }
     }
-    if (u + kDecWaves < u1) load_v(u + kDecWaves);
+    if (u + kDecWaves < u1) load_v(u + kDecWaves, pvu);
   }
 
   // ---- the waves' results: common maximum, then O added in the order of the waves
@@ -391,7 +458,7 @@ __global__ __launch_bounds__(64 * dec_waves(D, NC)) void attn_decode(AttnArgs a)
     __syncthreads();
   }
 
-  if (n_splits == 1) {
+  if (n_parts == 1) {
     if (wave == 0) {
 #pragma unroll
       for (int c = 0; c < NC; c++) {
@@ -409,62 +476,135 @@ __global__ __launch_bounds__(64 * dec_waves(D, NC)) void attn_decode(AttnArgs a)
         if (a.lse && g == 0) a.lse[tok * a.Hq + hd] = lt[c] == 0.f ? -INFINITY : (mt[c] + __builtin_amdgcn_logf(lt[c])) * kLn2;
       }
     }
-    return;
-  }
+  } else {
 
-  // ---- several splits: results to the workspace with device-coherent
-  // stores that complete before the arrival is counted; the last workgroup
-  // to arrive joins them in the order of the splits
+  // ---- Several shares: results to the workspace with device-coherent stores
+  // that complete before the arrival is counted.  A share has at most two
+  // such tiles, so it has two places: 2 share for a tile that began in an
+  // earlier one, 2 share + 1 for one that goes on.  Results are joined in the
+  // order of the shares in groups, by the last of a group to arrive, then the
+  // groups by the last of them: one workgroup reading every result of a long
+  // context would take longer than reading the context.
   const int rows = (int)(R - rho0 < 16 * NC ? R - rho0 : 16 * NC);
-  constexpr int PR = D + 2;  // floats of one row: O, m, l
-  float* tp = a.part + tile * (int64_t)a.S * 16 * NC * PR;
+  constexpr int PR = D + 2;                      // floats of one row: O, m, l
+  constexpr int64_t PS = (int64_t)16 * NC * PR;  // of one place
+  const int group = n_parts <= 64 ? 8 : kMaxJoin, groups = (n_parts + group - 1) / group;
+  const int part_no = (int)(share - share0), grp = part_no / group;
+  const int in_group = min(group, n_parts - grp * group);
+  auto place = [&](int i) -> int64_t { return 2 * (share0 + i) + (i == 0 ? 1 : 0); };
+  float* joined = a.part + 2 * (int64_t)kMaxShares * PS;  // a group's result, at the place of its first share
+  uint32_t* group_cnt = a.cnt + place(grp * group);
+  uint32_t* tile_cnt = a.cnt + 2 * kMaxShares + share0;
   if (wave == 0) {
-    float* mine = tp + (int64_t)sp * 16 * NC * PR;
+    float* mine = a.part + place(part_no) * PS;
 #pragma unroll
     for (int c = 0; c < NC; c++) {
       if (16 * c + n < rows) {
         float* row = mine + (16 * c + n) * PR;
 #pragma unroll
-        for (int d = 0; d < DT; d++)
-#pragma unroll
-          for (int e = 0; e < 4; e++)
-            __hip_atomic_store(row + 16 * d + 4 * g + e, o[c][d][e], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        if (g == 0) {
-          __hip_atomic_store(row + D, mt[c], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-          __hip_atomic_store(row + D + 1, lt[c], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        for (int d = 0; d < DT; d++) {
+          put2(row + 16 * d + 4 * g, o[c][d][0], o[c][d][1]);
+          put2(row + 16 * d + 4 * g + 2, o[c][d][2], o[c][d][3]);
         }
+        if (g == 0) put2(row + D, mt[c], lt[c]);
       }
     }
     __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    if (lane == 0) s_last = __hip_atomic_fetch_add(a.cnt + tile, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (lane == 0) s_last = __hip_atomic_fetch_add(group_cnt, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
   __syncthreads();
-  if (s_last != (uint32_t)n_splits - 1) return;
-  if (threadIdx.x == 0) __hip_atomic_store(a.cnt + tile, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  constexpr int D4 = D / 4;
-  for (int i = threadIdx.x; i < rows * D4; i += 64 * kDecWaves) {
-    const int r = i / D4, d = (i % D4) * 4;
-    const float* row = tp + r * PR;
-    float mm = -INFINITY;
-    for (int k = 0; k < n_splits; k++)
-      mm = fmaxf(mm, __hip_atomic_load(row + (int64_t)k * 16 * NC * PR + D, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
-    const float mu = mm == -INFINITY ? 0.f : mm;
-    float L = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int k = 0; k < n_splits; k++) {
-      const float* rk = row + (int64_t)k * 16 * NC * PR;
-      const float w = __builtin_amdgcn_exp2f(__hip_atomic_load(rk + D, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) - mu);
-      L += w * __hip_atomic_load(rk + D + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-#pragma unroll
-      for (int e = 0; e < 4; e++)
-        acc[e] += w * __hip_atomic_load(rk + d + e, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  // in the LDS of the waves' results: [row][kMaxJoin] maxima, then weights; sums; joined m and l
+  float* jw = &lo_[0][0];
+  float* js = jw + 16 * NC * kMaxJoin;
+  float* jm = js + 16 * NC * kMaxJoin;
+  float* jl = jm + 16 * NC;
+  static_assert(16 * NC * (2 * kMaxJoin + 2) <= (kDecWaves / 2) * 16 * NC * D, "fits the waves' O");
+  // joins the results at from(0 .. count - 1); each pair of outputs goes to put(row, dim, O, O)
+  auto join = [&](auto&& from, int count, auto&& put) {
+    for (int i = threadIdx.x; i < rows * count; i += 64 * kDecWaves) {
+      const int r = i / count, k = i % count;
+      const float2 v = get2(from(k) + r * PR + D);
+      jw[r * kMaxJoin + k] = v.x;
+      js[r * kMaxJoin + k] = v.y;
     }
-    const float inv = L > 0.f || L != L ? 1.0f / L : 0.f;
+    __syncthreads();
+    if (threadIdx.x < rows) {
+      const int r = threadIdx.x;
+      float mm = -INFINITY, L = 0.f;
+      for (int k = 0; k < count; k++) mm = fmaxf(mm, jw[r * kMaxJoin + k]);
+      const float mu = mm == -INFINITY ? 0.f : mm;
+      for (int k = 0; k < count; k++) {
+        const float w = __builtin_amdgcn_exp2f(jw[r * kMaxJoin + k] - mu);
+        L += w * js[r * kMaxJoin + k];
+        jw[r * kMaxJoin + k] = w;
+      }
+      jm[r] = mm;
+      jl[r] = L;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < rows * (D / 2); i += 64 * kDecWaves) {
+      const int r = i / (D / 2), d = (i % (D / 2)) * 2;
+      float px = 0.f, py = 0.f;
+      for (int k0 = 0; k0 < count; k0 += kJoinLoads) {
+        float2 v[kJoinLoads];
+#pragma unroll
+        for (int k = 0; k < kJoinLoads; k++)
+          v[k] = k0 + k < count ? get2(from(k0 + k) + r * PR + d) : make_float2(0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < kJoinLoads; k++) {
+          const float w = k0 + k < count ? jw[r * kMaxJoin + k0 + k] : 0.f;
+          px += w * v[k].x;
+          py += w * v[k].y;
+        }
+      }
+      put(r, d, px, py);
+    }
+  };
+  auto finish = [&](int r, int d, float px, float py) {
+    const float L = jl[r], inv = L > 0.f || L != L ? 1.0f / L : 0.f;
     const int64_t rr = rho0 + r, tok = s.row0 + rr / a.G, hd = h * a.G + rr % a.G;
-    uint2 w;
-    w.x = bf16_bits(acc[0] * inv) | (bf16_bits(acc[1] * inv) << 16);
-    w.y = bf16_bits(acc[2] * inv) | (bf16_bits(acc[3] * inv) << 16);
-    *(uint2*)(a.o + tok * a.o_stride + hd * D + d) = w;
-    if (a.lse && d == 0) a.lse[tok * a.Hq + hd] = L == 0.f ? -INFINITY : (mm + __builtin_amdgcn_logf(L)) * kLn2;
+    *(uint32_t*)(a.o + tok * a.o_stride + hd * D + d) = bf16_bits(px * inv) | (bf16_bits(py * inv) << 16);
+    if (a.lse && d == 0) a.lse[tok * a.Hq + hd] = L == 0.f ? -INFINITY : (jm[r] + __builtin_amdgcn_logf(L)) * kLn2;
+  };
+  auto part_of_group = [&](int k) -> const float* { return a.part + place(grp * group + k) * PS; };
+  if (s_last == (uint32_t)in_group - 1) {
+    if (threadIdx.x == 0) __hip_atomic_store(group_cnt, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (groups == 1) {
+      join(part_of_group, n_parts, finish);
+    } else {
+      float* mine = joined + place(grp * group) * PS;
+      join(part_of_group, in_group, [&](int r, int d, float px, float py) {
+        put2(mine + r * PR + d, px, py);
+        if (d == 0) put2(mine + r * PR + D, jm[r], jl[r]);
+      });
+      __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      __syncthreads();  // every wave's stores are complete
+      if (threadIdx.x == 0) s_last = __hip_atomic_fetch_add(tile_cnt, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      __syncthreads();
+      if (s_last == (uint32_t)groups - 1) {
+        if (threadIdx.x == 0) __hip_atomic_store(tile_cnt, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        join([&](int k) -> const float* { return joined + place(k * group) * PS; }, groups, finish);
+      }
+    }
+  }
+  }
+  // ---- the share's next tile
+  x += count;
+  if (x >= x_end) return;
+  __syncthreads();  // the LDS is free again
+  at = 0;
+  if (++rt == tiles) {
+    rt = 0;
+    do {
+      if (++b == a.kv.n_seqs) {
+        b = 0;
+        h++;
+      }
+      s = seq_span(a.kv, b);
+      tiles = tiles_of(s);
+    } while (tiles == 0);  // some sequence has tiles, as x < total
+    steps = steps_of(s);
+  }
   }
 }
 
@@ -489,8 +629,11 @@ __global__ __launch_bounds__(64 * WAVES) void attn_prompt(AttnArgs a) {
   const int64_t bid = blockIdx.x;
   const int h = (int)(bid % a.kv.H);
   int64_t b, item;
-  auto tiles = [&](int64_t i) { return (seq_span(a.kv, i).n * a.G + ROWS - 1) / ROWS; };
-  if (!find_item(a.kv.n_seqs, bid / a.kv.H, tiles, &b, &item)) return;
+  auto tiles = [&](int64_t i) -> int64_t { return (seq_span(a.kv, i).n * a.G + ROWS - 1) / ROWS; };
+  __shared__ int64_t scan_[WAVES + 2];
+  ItemScan<64 * WAVES, decltype(tiles)> scan(a.kv.n_seqs, tiles, scan_);
+  if (bid / a.kv.H >= scan.total) return;
+  scan.find(bid / a.kv.H, &b, &item);
   const SeqSpan s = seq_span(a.kv, b);
   const int64_t R = (int64_t)s.n * a.G, wg0 = ((R + ROWS - 1) / ROWS - 1 - item) * ROWS;
   const int len = s.len, first = len - s.n, P = 1 << a.kv.lp;
@@ -783,64 +926,44 @@ __global__ __launch_bounds__(64 * WAVES) void attn_prompt(AttnArgs a) {
 }
 
 struct Plan {
-  int nc, S;          // nc 0: attn_prompt
-  int64_t RT, tiles, chunk;
-  int64_t blocks;     // workgroups: a bound on the work items
+  int nc;             // column tiles of a decode tile; 0: attn_prompt
+  int64_t tiles;      // a bound
+  int64_t blocks;
 };
 
 constexpr int64_t kPromptRows = 128;
 constexpr int prompt_rows(int D) { return D == 256 ? 128 : 256; }
 
-Plan plan_decode(int D, int H, int64_t n_seqs, int64_t total_q, int64_t max_q, int64_t max_kv, int64_t G) {
+Plan plan_attention(int D, int H, int64_t n_seqs, int64_t total_q, int64_t max_q, int64_t G) {
   Plan p;
   const int64_t R = max_q * G;
   if (R >= kPromptRows) {
     p.nc = 0;
-    p.S = 1;
-    p.RT = cdiv(R, prompt_rows(D));
-    p.tiles = n_seqs * H * p.RT;
-    p.chunk = 0;
-    p.blocks = H * min(n_seqs * p.RT, total_q * G / prompt_rows(D) + n_seqs);
+    p.tiles = n_seqs * H * cdiv(R, prompt_rows(D));
+    p.blocks = min(p.tiles, H * (total_q * G / prompt_rows(D) + n_seqs));
     return p;
   }
   p.nc = R > 16 && D <= 128 ? 2 : 1;  // wider heads: the registers of 16 rows
-  p.RT = cdiv(R, 16 * p.nc);
-  p.tiles = n_seqs * H * p.RT;
-  // tokens of one split: about 1024 workgroups in all, at least one step for
-  // each wave, at most 64 splits to join
-  int64_t S = p.tiles >= 1024 ? 1 : cdiv(1024, p.tiles);
-  S = S < 64 ? S : 64;
-  const int64_t per = cdiv(cdiv(max_kv, S), kChunkUnit) * kChunkUnit;
-  p.chunk = per;
-  p.S = (int)cdiv(max_kv + kUnit, per);
-  if (p.tiles > kMaxRowGroups || p.S < 1) {
-    p.S = 1;
-    p.chunk = cdiv(max_kv + kUnit, kUnit) * kUnit;
-  }
-  // every item that any contents of the device arrays can name: a split that
-  // did not run would leave its tile's arrivals uncounted
-  p.blocks = p.tiles * p.S;
+  p.tiles = n_seqs * H * cdiv(R, 16 * p.nc);
+  p.blocks = D == 256 ? kMaxShares / 2 : kMaxShares;  // what the chip holds at once
   return p;
 }
 
 }  // namespace
 
-int64_t attention_blocks(int D, int H, int64_t n_seqs, int64_t total_q, int64_t max_q, int64_t max_kv, int64_t G) {
-  const Plan p = plan_decode(D, H, n_seqs, total_q, max_q, max_kv, G);
-  return p.blocks;
+int64_t attention_blocks(int D, int H, int64_t n_seqs, int64_t total_q, int64_t max_q, int64_t G) {
+  return plan_attention(D, H, n_seqs, total_q, max_q, G).blocks;
 }
 
-size_t attention_workspace_bytes(int D, int H, int64_t n_seqs, int64_t total_q, int64_t max_q, int64_t max_kv, int64_t G) {
-  const Plan p = plan_decode(D, H, n_seqs, total_q, max_q, max_kv, G);
-  if (p.S == 1) return kCounterBytes;
-  return (size_t)kCounterBytes + (size_t)(p.tiles * p.S * 16 * p.nc * (D + 2)) * 4;
+size_t attention_workspace_bytes(int D, int H, int64_t n_seqs, int64_t total_q, int64_t max_q, int64_t G) {
+  const Plan p = plan_attention(D, H, n_seqs, total_q, max_q, G);
+  if (p.nc == 0) return 0;
+  return (size_t)kCounterBytes + (size_t)4 * kMaxShares * 16 * p.nc * (D + 2) * 4;
 }
 
 hipError_t launch_attention(AttnArgs a, void* ws, hipStream_t s) {
-  const Plan p = plan_decode(a.kv.D, a.kv.H, a.kv.n_seqs, a.kv.total_q, a.kv.max_q, a.kv.max_kv, a.G);
-  a.RT = p.RT;
-  a.S = p.S;
-  a.chunk = p.chunk;
+  const Plan p = plan_attention(a.kv.D, a.kv.H, a.kv.n_seqs, a.kv.total_q, a.kv.max_q, a.G);
+  a.tiles = p.tiles;
   a.cnt = (uint32_t*)ws + 16;
   a.part = (float*)((uint8_t*)ws + kCounterBytes);
   const dim3 grid((unsigned)p.blocks);
@@ -851,7 +974,7 @@ hipError_t launch_attention(AttnArgs a, void* ws, hipStream_t s) {
     return hipGetLastError();
   }
 #define LOWBIT_DEC(DD, NN) \
-  hipLaunchKernelGGL((attn_decode<DD, NN>), grid, dim3(64 * dec_waves(DD, NN)), 0, s, a)
+  hipLaunchKernelGGL((attn_decode<DD, NN>), grid, dim3(64 * kDecWaves), 0, s, a)
   if (p.nc == 1) {
     if (a.kv.D == 64) LOWBIT_DEC(64, 1);
     else if (a.kv.D == 128) LOWBIT_DEC(128, 1);

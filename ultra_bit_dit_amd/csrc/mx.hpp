@@ -22,6 +22,12 @@ constexpr uint32_t kMxUnitScale = 127;  // 2^0: the exponent byte of padding
 __host__ __device__ inline int64_t mx_groups(int64_t K) { return (K + 127) / 128; }
 __host__ __device__ inline int64_t mx_quads(int64_t K) { return (K + 511) / 512; }
 
+__device__ __forceinline__ int64_t uniform64(int64_t v) {
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)((uint64_t)v >> 32));
+  return (int64_t)(((uint64_t)hi << 32) | lo);
+}
+
 // fp32 -> bf16 bits, round to nearest even, NaN kept
 __device__ __forceinline__ uint32_t bf16_bits(float f) {
   const uint32_t u = __float_as_uint(f);
