@@ -7,6 +7,7 @@ no fallback.
 """
 import ctypes
 import os
+import struct
 import sys
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -256,22 +257,50 @@ def rotate_act(X, signs, stream=None):
     return Xr
 
 
-# ---- MXFP4
+# ---- MXFP4 and the 8-bit cache.  Single tokens take a few microseconds on the
+# device, so these wrappers check with plain comparisons and pass addresses and
+# packed structs straight to the library.
+
+_torch = None     # set by the first call
+_FLOAT = {}       # torch type -> lowbit_dtype of the float inputs
+_fast = None      # the same exports with address-only prototypes
+_PACK_KV8 = struct.Struct("@qiiiPPPP").pack        # lowbit_kv8
+_PACK_BATCH = struct.Struct("@qPqPPqqqP").pack     # lowbit_kv8_batch
 
 
-def _on(device, *tensors):
-    """Every given tensor lies on `device`, which has to be the current one (calls run there)."""
+class _Fast:
+    def __init__(self):
+        L, vp, i64, i32 = lib(), ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
+        for name, types in (
+                ("lowbit_quantize_mxfp4", [i64, i64, i32, vp, i64, vp, vp, vp, vp]),
+                ("lowbit_gemm_mxfp4", [i64, i64, i64, vp, vp, i32, vp, i64, vp, i32, vp, vp]),
+                ("lowbit_kv8_append", [vp, vp, i32, vp, vp, i64, i64, vp]),
+                ("lowbit_attention_kv8", [vp, vp, i64, vp, i64, ctypes.c_float, i32, i64, vp, i64, vp, vp])):
+            f = L[name]  # a function object of its own
+            f.argtypes, f.restype = types, i32
+            setattr(self, name[7:], f)
+
+
+def _load():
+    global _torch, _fast
     import torch
-    if device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors on {device}, but the current device is cuda:{torch.cuda.current_device()}")
+    _FLOAT.update({torch.bfloat16: BF16, torch.float32: F32})
+    _fast = _Fast()
+    _torch = torch
+    return torch
+
+
+def _device(T, dev, *tensors):
+    """The given tensors lie on GPU `dev`, the current one (calls run there)."""
     for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError(f"tensors on {device} and {t.device} in one call")
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensors on {t.device} and GPU {dev} in one call")
+    if dev < 0 or dev != T._C._cuda_getDevice():
+        raise ValueError(f"tensors on device {dev}: calls take tensors of the current GPU")
 
 
-def _want(cond, what):
-    if not cond:
-        raise ValueError(what)
+def _raw_stream(T, dev, stream):
+    return T._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def _mx_sizes(rows, K):
@@ -296,26 +325,26 @@ def empty_mxfp4(rows, K, device="cuda"):
             torch.empty(sb, dtype=torch.uint8, device=device))
 
 
-def _mx_packed(codes, scales, rows, K, what):
-    import torch
+def _mx_packed(T, codes, scales, rows, K, what):
     cb, sb = _mx_sizes(rows, K)
-    _want(codes.dtype == torch.uint8 and scales.dtype == torch.uint8 and codes.numel() == cb
-          and scales.numel() == sb and codes.is_contiguous() and scales.is_contiguous(),
-          f"{what}: packed MXFP4 buffers of a {rows} x {K} matrix are {cb} and {sb} contiguous uint8")
+    u8 = T.uint8
+    if (codes.dtype != u8 or scales.dtype != u8 or codes.numel() != cb or scales.numel() != sb
+            or not codes.is_contiguous() or not scales.is_contiguous()):
+        raise ValueError(f"{what}: packed MXFP4 buffers of a {rows} x {K} matrix are {cb} and {sb} contiguous uint8")
 
 
 def pack_mxfp4(codes, scales, pcodes=None, pscales=None, stream=None):
     """Row-major MXFP4 (uint8 codes [rows][K/2], scales [rows][K/32]) -> packed buffers
     (see lowbit_pack_mxfp4)."""
-    import torch
+    T = _torch or _load()
     rows, K = codes.shape[0], 2 * codes.shape[1]
-    _want(codes.dtype == torch.uint8 and scales.dtype == torch.uint8 and tuple(scales.shape) == (rows, K // 32)
-          and codes.is_contiguous() and scales.is_contiguous(),
-          "pack_mxfp4: contiguous uint8 codes [rows][K/2] and scales [rows][K/32]")
+    if (codes.dtype != T.uint8 or scales.dtype != T.uint8 or tuple(scales.shape) != (rows, K // 32)
+            or not codes.is_contiguous() or not scales.is_contiguous()):
+        raise ValueError("pack_mxfp4: contiguous uint8 codes [rows][K/2] and scales [rows][K/32]")
     if pcodes is None:
         pcodes, pscales = empty_mxfp4(rows, K, codes.device)
-    _mx_packed(pcodes, pscales, rows, K, "pack_mxfp4")
-    _on(codes.device, scales, pcodes, pscales)
+    _mx_packed(T, pcodes, pscales, rows, K, "pack_mxfp4")
+    _device(T, codes.get_device(), scales, pcodes, pscales)
     _check("lowbit_pack_mxfp4", lib().lowbit_pack_mxfp4(rows, K, _ptr(codes), _ptr(scales), _ptr(pcodes),
                                                         _ptr(pscales), _stream(stream)))
     return pcodes, pscales
@@ -325,59 +354,58 @@ def quantize_mxfp4(X, values=False, pcodes=None, pscales=None, stream=None):
     """X [rows][K] (bf16 or fp32, rows may be strided) -> packed (codes, scales);
     values=True (or a tensor): and the numbers they stand for, in X's type (see
     lowbit_quantize_mxfp4)."""
-    import torch
-    _want(X.dim() == 2 and X.stride(1) == 1, "quantize_mxfp4: X is [rows][K] with contiguous rows")
+    T = _torch or _load()
+    if X.dim() != 2 or X.stride(1) != 1 or X.dtype not in _FLOAT:
+        raise ValueError("quantize_mxfp4: X is bf16 or fp32 [rows][K] with contiguous rows")
     rows, K = X.shape
+    dev = X.get_device()
     if pcodes is None:
-        pcodes, pscales = empty_mxfp4(rows, K, X.device)
-    _mx_packed(pcodes, pscales, rows, K, "quantize_mxfp4")
+        cb, sb = _mx_sizes(rows, K)
+        pcodes = T.empty(cb, dtype=T.uint8, device=X.device)
+        pscales = T.empty(sb, dtype=T.uint8, device=X.device)
+        _device(T, dev)
+    else:
+        _mx_packed(T, pcodes, pscales, rows, K, "quantize_mxfp4")
+        _device(T, dev, pcodes, pscales)
     vals = None
-    if values is not False and values is not None:
-        vals = torch.empty((rows, K), dtype=X.dtype, device=X.device) if values is True else values
-        _want(tuple(vals.shape) == (rows, K) and vals.dtype == X.dtype and vals.is_contiguous(),
-              "quantize_mxfp4: values is contiguous, of X's shape and type")
-    _on(X.device, pcodes, pscales, vals)
-    _check("lowbit_quantize_mxfp4",
-           lib().lowbit_quantize_mxfp4(rows, K, _xfloat(X), _ptr(X), max(X.stride(0), K), _ptr(pcodes),
-                                       _ptr(pscales), _ptr(vals), _stream(stream)))
+    if values is True:
+        vals = T.empty((rows, K), dtype=X.dtype, device=X.device)
+    elif values is not False and values is not None:
+        vals = values
+        if vals.shape != X.shape or vals.dtype != X.dtype or not vals.is_contiguous() or vals.get_device() != dev:
+            raise ValueError("quantize_mxfp4: values is contiguous, of X's shape, type and device")
+    rc = _fast.quantize_mxfp4(rows, K, _FLOAT[X.dtype], X.data_ptr(), X.stride(0) if rows > 1 else K,
+                              pcodes.data_ptr(), pscales.data_ptr(), None if vals is None else vals.data_ptr(),
+                              _raw_stream(T, dev, stream))
+    if rc:
+        raise LowbitError("lowbit_quantize_mxfp4", rc)
     return (pcodes, pscales) if vals is None else (pcodes, pscales, vals)
-
-
-def _xfloat(x):
-    import torch
-    if x.dtype == torch.bfloat16:
-        return BF16
-    if x.dtype == torch.float32:
-        return F32
-    raise ValueError(f"bf16 or fp32 expected, got {x.dtype}")
 
 
 def gemm_mxfp4(M, N, K, pcodes, pscales, X, x_scales=None, y_dtype=F32, Y=None, stream=None):
     """Y[m][n] = sum_k W[n][k] X[m][k] with MXFP4 weights (see lowbit_gemm_mxfp4): X is
     bf16 [M][K] (rows may be strided), or with x_scales the packed MXFP4 codes of
     the activations."""
-    import torch
-    _mx_packed(pcodes, pscales, N, K, "gemm_mxfp4: weights")
+    T = _torch or _load()
+    _mx_packed(T, pcodes, pscales, N, K, "gemm_mxfp4: weights")
+    dev = pcodes.get_device()
     if x_scales is not None:
-        _mx_packed(X, x_scales, M, K, "gemm_mxfp4: activations")
-        xd, ld = MXFP4, 0
+        _mx_packed(T, X, x_scales, M, K, "gemm_mxfp4: activations")
+        xd, ld, xs = MXFP4, 0, x_scales.data_ptr()
     else:
-        _want(X.dtype == torch.bfloat16 and tuple(X.shape) == (M, K) and X.stride(1) == 1,
-              "gemm_mxfp4: X is bf16 [M][K] with contiguous rows, or packed codes with x_scales")
-        xd, ld = BF16, max(X.stride(0), K)
+        if X.dtype != T.bfloat16 or X.shape != (M, K) or X.stride(1) != 1:
+            raise ValueError("gemm_mxfp4: X is bf16 [M][K] with contiguous rows, or packed codes with x_scales")
+        xd, ld, xs = BF16, X.stride(0) if M > 1 else K, None
     if Y is None:
-        Y = torch.empty((M, N), dtype=_ytorch(y_dtype), device=pcodes.device)
-    else:
-        _want(tuple(Y.shape) == (M, N) and Y.dtype == _ytorch(y_dtype) and Y.is_contiguous(),
-              "gemm_mxfp4: Y is contiguous [M][N] of y_dtype")
-    _on(pcodes.device, pscales, X, x_scales, Y)
-    _check("lowbit_gemm_mxfp4",
-           lib().lowbit_gemm_mxfp4(M, N, K, _ptr(pcodes), _ptr(pscales), xd, _ptr(X), ld, _ptr(x_scales),
-                                   y_dtype, _ptr(Y), _stream(stream)))
+        Y = T.empty((M, N), dtype=T.float32 if y_dtype == F32 else _ytorch(y_dtype), device=pcodes.device)
+    elif Y.shape != (M, N) or Y.dtype != _ytorch(y_dtype) or not Y.is_contiguous():
+        raise ValueError("gemm_mxfp4: Y is contiguous [M][N] of y_dtype")
+    _device(T, dev, pscales, X, x_scales, Y)
+    rc = _fast.gemm_mxfp4(M, N, K, pcodes.data_ptr(), pscales.data_ptr(), xd, X.data_ptr(), ld, xs, y_dtype,
+                          Y.data_ptr(), _raw_stream(T, dev, stream))
+    if rc:
+        raise LowbitError("lowbit_gemm_mxfp4", rc)
     return Y
-
-
-# ---- 8-bit paged cache
 
 
 def empty_kv8(n_pages, page_tokens, kv_heads, head_dim, device="cuda"):
@@ -390,49 +418,55 @@ def empty_kv8(n_pages, page_tokens, kv_heads, head_dim, device="cuda"):
     return k.view(torch.float8_e4m3fn), v.view(torch.float8_e4m3fn), s[0], s[1]
 
 
-def _kv8(cache, page_table, kv_lens, q_starts, total_q, max_q, max_kv, bad_pages):
-    import torch
+def _kv8(T, cache, page_table, kv_lens, q_starts, total_q, max_q, max_kv, bad_pages):
+    """Checked and packed lowbit_kv8 and lowbit_kv8_batch, and the tensors' device."""
     kc, vc, ks, vs = cache
-    _want(kc.dim() == 4 and vc.dim() == 4 and kc.element_size() == 1 and vc.element_size() == 1,
-          "cache: 8-bit codes [pages][heads][tokens][dim] and [pages][heads][dim][tokens]")
     n, H, P, D = kc.shape
-    _want(tuple(vc.shape) == (n, H, D, P) and tuple(ks.shape) == (n, H) and tuple(vs.shape) == (n, H)
-          and ks.dtype == torch.uint8 and vs.dtype == torch.uint8,
-          "cache: v_codes [pages][heads][dim][tokens] and uint8 scales [pages][heads] of the same sizes")
-    _want(kc.is_contiguous() and vc.is_contiguous() and ks.is_contiguous() and vs.is_contiguous(),
-          "cache: contiguous tensors")
-    i32 = torch.int32
-    _want(page_table.dim() == 2 and page_table.dtype == i32 and page_table.is_contiguous(),
-          "page_table: contiguous int32 [sequences][pages]")
-    B = page_table.shape[0]
-    _want(kv_lens.dtype == i32 and tuple(kv_lens.shape) == (B,) and kv_lens.is_contiguous(),
-          "kv_lens: contiguous int32 [sequences]")
+    if vc.shape != (n, H, D, P) or kc.element_size() != 1 or vc.element_size() != 1:
+        raise ValueError("cache: 8-bit codes k [pages][heads][tokens][dim] and v [pages][heads][dim][tokens]")
+    if ks.shape != (n, H) or vs.shape != (n, H) or ks.dtype != T.uint8 or vs.dtype != T.uint8:
+        raise ValueError("cache: uint8 scales [pages][heads]")
+    if not (kc.is_contiguous() and vc.is_contiguous() and ks.is_contiguous() and vs.is_contiguous()):
+        raise ValueError("cache: contiguous tensors")
+    B, width = page_table.shape
+    i32 = T.int32
+    if page_table.dtype != i32 or not page_table.is_contiguous():
+        raise ValueError("page_table: contiguous int32 [sequences][pages]")
+    if kv_lens.dtype != i32 or kv_lens.shape != (B,) or not kv_lens.is_contiguous():
+        raise ValueError("kv_lens: contiguous int32 [sequences]")
+    dev = kc.get_device()
+    starts = bad = 0
     if q_starts is None:
-        _want(B > 0 and total_q % B == 0, "without q_starts every sequence has the same number of new tokens")
+        if B < 1 or total_q % B:
+            raise ValueError("without q_starts every sequence has the same number of new tokens")
         if max_q is None:
             max_q = total_q // B
     else:
-        _want(q_starts.dtype == i32 and tuple(q_starts.shape) == (B + 1,) and q_starts.is_contiguous(),
-              "q_starts: contiguous int32 [sequences + 1]")
+        if q_starts.dtype != i32 or q_starts.shape != (B + 1,) or not q_starts.is_contiguous():
+            raise ValueError("q_starts: contiguous int32 [sequences + 1]")
+        starts = q_starts.data_ptr()
         if max_q is None:
             max_q = total_q
     if max_kv is None:
-        max_kv = page_table.shape[1] * P
+        max_kv = width * P
     if bad_pages is not None:
-        _want(bad_pages.dtype == i32 and bad_pages.numel() >= 1, "bad_pages: int32")
-    _on(kc.device, vc, ks, vs, page_table, kv_lens, q_starts, bad_pages)
-    c = Kv8(n, P, H, D, kc.data_ptr(), vc.data_ptr(), ks.data_ptr(), vs.data_ptr())
-    b = Kv8Batch(B, page_table.data_ptr(), page_table.shape[1], kv_lens.data_ptr(),
-                 None if q_starts is None else q_starts.data_ptr(), total_q, max_q, max_kv,
-                 None if bad_pages is None else bad_pages.data_ptr())
-    return c, b
+        if bad_pages.dtype != i32 or bad_pages.numel() < 1:
+            raise ValueError("bad_pages: int32")
+        bad = bad_pages.data_ptr()
+    _device(T, dev, vc, ks, vs, page_table, kv_lens, q_starts, bad_pages)
+    return (_PACK_KV8(n, P, H, D, kc.data_ptr(), vc.data_ptr(), ks.data_ptr(), vs.data_ptr()),
+            _PACK_BATCH(B, page_table.data_ptr(), width, kv_lens.data_ptr(), starts, total_q, max_q, max_kv, bad), dev)
 
 
 def _heads(x, H, D, what):
     """Token stride of a [tokens][heads][dim] tensor whose heads are contiguous."""
-    _want(x.dim() == 3 and x.shape[2] == D and (H is None or x.shape[1] == H) and x.stride(2) == 1
-          and (x.stride(1) == D or x.shape[1] == 1), f"{what}: [tokens][heads][{D}] with contiguous heads")
-    return max(x.stride(0), x.shape[1] * D)
+    shape = x.shape
+    if len(shape) != 3 or shape[2] != D or shape[1] != H:
+        raise ValueError(f"{what}: [tokens][{H}][{D}] expected, got {list(shape)}")
+    s0, s1, s2 = x.stride()
+    if s2 != 1 or (s1 != D and H != 1):
+        raise ValueError(f"{what}: a token's heads have to be contiguous")
+    return s0 if shape[0] > 1 else H * D
 
 
 def kv8_append(cache, page_table, kv_lens, K, V, q_starts=None, max_q=None, max_kv=None, bad_pages=None,
@@ -440,48 +474,60 @@ def kv8_append(cache, page_table, kv_lens, K, V, q_starts=None, max_q=None, max_
     """Write new keys and values [tokens][kv_heads][dim] (bf16 or fp32, tokens may be strided) into the
     cache (see lowbit_kv8_append).  kv_lens counts them already; q_starts None: every sequence has
     tokens / sequences new ones."""
-    H, D = cache[0].shape[1], cache[0].shape[3]
+    T = _torch or _load()
+    _, H, _, D = cache[0].shape
     ks, vs = _heads(K, H, D, "K"), _heads(V, H, D, "V")
-    _want(K.shape[0] == V.shape[0] and K.dtype == V.dtype, "K and V: the same tokens and type")
-    c, b = _kv8(cache, page_table, kv_lens, q_starts, K.shape[0], max_q, max_kv, bad_pages)
-    _on(cache[0].device, K, V)
-    _check("lowbit_kv8_append", lib().lowbit_kv8_append(c, b, _xfloat(K), _ptr(K), _ptr(V), ks, vs,
-                                                        _stream(stream)))
+    if K.shape[0] != V.shape[0] or K.dtype != V.dtype or K.dtype not in _FLOAT:
+        raise ValueError("K and V: the same tokens and type, bf16 or fp32")
+    c, b, dev = _kv8(T, cache, page_table, kv_lens, q_starts, K.shape[0], max_q, max_kv, bad_pages)
+    if K.get_device() != dev or V.get_device() != dev:
+        raise ValueError("K and V lie on another device than the cache")
+    rc = _fast.kv8_append(c, b, _FLOAT[K.dtype], K.data_ptr(), V.data_ptr(), ks, vs, _raw_stream(T, dev, stream))
+    if rc:
+        raise LowbitError("lowbit_kv8_append", rc)
 
 
 def attention_kv8(Q, cache, page_table, kv_lens, q_starts=None, max_q=None, max_kv=None, softmax_scale=None,
                   causal=True, window=0, O=None, lse=None, return_lse=False, bad_pages=None, stream=None):
     """Attention of bf16 queries [tokens][q_heads][dim] (tokens may be strided) over the cache (see
     lowbit_attention_kv8); softmax_scale None: 1 / sqrt(dim).  Returns O, or (O, lse) with return_lse."""
-    import torch
+    T = _torch or _load()
     D = cache[0].shape[3]
-    qs = _heads(Q, None, D, "Q")
-    T, Hq = Q.shape[0], Q.shape[1]
-    _want(Q.dtype == torch.bfloat16, f"Q: bf16 expected, got {Q.dtype}")
-    c, b = _kv8(cache, page_table, kv_lens, q_starts, T, max_q, max_kv, bad_pages)
+    if Q.dim() != 3 or Q.dtype != T.bfloat16:
+        raise ValueError("Q: bf16 [tokens][q_heads][dim]")
+    tokens, Hq, _ = Q.shape
+    qs = _heads(Q, Hq, D, "Q")
+    c, b, dev = _kv8(T, cache, page_table, kv_lens, q_starts, tokens, max_q, max_kv, bad_pages)
     if O is None:
-        O = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=Q.device)
+        O = T.empty((tokens, Hq, D), dtype=T.bfloat16, device=Q.device)
+        os = Hq * D
     else:
-        _want(tuple(O.shape) == (T, Hq, D) and O.dtype == torch.bfloat16, "O: bf16 of Q's shape")
-    if return_lse and lse is None:
-        lse = torch.empty((T, Hq), dtype=torch.float32, device=Q.device)
-    if lse is not None:
-        _want(tuple(lse.shape) == (T, Hq) and lse.dtype == torch.float32 and lse.is_contiguous(),
-              "lse: contiguous fp32 [tokens][q_heads]")
-    _on(cache[0].device, Q, O, lse)
-    _check("lowbit_attention_kv8",
-           lib().lowbit_attention_kv8(c, b, Hq, _ptr(Q), qs, float(D ** -0.5 if softmax_scale is None else softmax_scale),
-                                      int(bool(causal)), int(window), _ptr(O), _heads(O, Hq, D, "O"), _ptr(lse),
-                                      _stream(stream)))
+        if O.shape != Q.shape or O.dtype != T.bfloat16 or O.get_device() != dev:
+            raise ValueError("O: bf16 of Q's shape, on its device")
+        os = _heads(O, Hq, D, "O")
+    if lse is None:
+        if return_lse:
+            lse = T.empty((tokens, Hq), dtype=T.float32, device=Q.device)
+    elif lse.shape != (tokens, Hq) or lse.dtype != T.float32 or not lse.is_contiguous() or lse.get_device() != dev:
+        raise ValueError("lse: contiguous fp32 [tokens][q_heads] on Q's device")
+    if Q.get_device() != dev:
+        raise ValueError("Q lies on another device than the cache")
+    rc = _fast.attention_kv8(c, b, Hq, Q.data_ptr(), qs, D ** -0.5 if softmax_scale is None else softmax_scale,
+                             1 if causal else 0, window, O.data_ptr(), os, None if lse is None else lse.data_ptr(),
+                             _raw_stream(T, dev, stream))
+    if rc:
+        raise LowbitError("lowbit_attention_kv8", rc)
     return (O, lse) if return_lse else O
 
 
 def attention_kv8_workspace(cache, page_table, kv_lens, q_heads, total_q, q_starts=None, max_q=None, max_kv=None):
     """Workspace bytes lowbit_attention_kv8 needs for these arguments (reserve before a capture)."""
-    c, b = _kv8(cache, page_table, kv_lens, q_starts, total_q, max_q, max_kv, None)
+    T = _torch or _load()
+    c, b, _ = _kv8(T, cache, page_table, kv_lens, q_starts, total_q, max_q, max_kv, None)
     n = ctypes.c_size_t()
     _check("lowbit_attention_kv8_workspace",
-           lib().lowbit_attention_kv8_workspace(c, b, q_heads, ctypes.byref(n)))
+           lib().lowbit_attention_kv8_workspace(Kv8.from_buffer_copy(c), Kv8Batch.from_buffer_copy(b), q_heads,
+                                                ctypes.byref(n)))
     return n.value
 
 
