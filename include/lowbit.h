@@ -434,12 +434,16 @@ int lowbit_quantize_mxfp4(int64_t rows, int64_t K, int x_dtype, const void* X, i
  *     in magnitude may count as 0.
  *   x_dtype MXFP4: X packed codes and x_pscales its packed scales
  *     (lowbit_quantize_mxfp4 of the M x K activations); x_stride ignored.
- * Uses no workspace.  All pointers 16-byte aligned.  N <= 2^26,
- * ceil(M/128) * ceil(N/128) <= 2^23.
- * Errors: E_NULL, E_UNSUPPORTED, E_SHAPE, E_ALIGN, E_HIP. */
+ * All pointers 16-byte aligned.  N <= 2^26, ceil(M/128) * ceil(N/128) <= 2^23.
+ * Sums are added in a fixed order: repeated calls give the same bits.  Uses
+ * the stream's workspace as lowbit_gemm does where K is split over workgroups
+ * (lowbit_gemm_mxfp4_workspace: its bytes, 0 where none; reserve it before a
+ * capture).
+ * Errors: E_NULL, E_UNSUPPORTED, E_SHAPE, E_ALIGN, E_NOMEM, E_HIP. */
 int lowbit_gemm_mxfp4(int64_t M, int64_t N, int64_t K, const void* pcodes, const void* pscales,
                       int x_dtype, const void* X, int64_t x_stride, const void* x_pscales, int y_dtype,
                       void* Y, void* stream);
+int lowbit_gemm_mxfp4_workspace(int64_t M, int64_t N, int64_t K, int x_dtype, size_t* bytes);
 
 /* =====================  8-bit paged cache and attention  ==================
  * Between the q/k/v and the o product of a layer ([XH] section "ローカル27Bを

@@ -542,7 +542,24 @@ int lowbit_gemm_mxfp4(int64_t M, int64_t N, int64_t K, const void* pcodes, const
   g.x_pscales = x_pscales;
   g.ykind = y_dtype;
   g.y = Y;
+  g.ws = nullptr;
+  const size_t need = gemm_mxfp4_workspace_bytes(x4, M, N, K);
+  if (need) {
+    const int rc = workspace((hipStream_t)stream, need, &g.ws);
+    if (rc) return rc;
+  }
   return hip_status(launch_gemm_mxfp4(g, (hipStream_t)stream));
+}
+
+int lowbit_gemm_mxfp4_workspace(int64_t M, int64_t N, int64_t K, int x_dtype, size_t* bytes) {
+  if (!bytes) return LOWBIT_E_NULL;
+  *bytes = 0;
+  if (x_dtype != LOWBIT_BF16 && x_dtype != LOWBIT_MXFP4) return LOWBIT_E_UNSUPPORTED;
+  if (!mx_shape_ok(N, K) || !mx_shape_ok(M, K) || N > (int64_t(1) << 26) ||
+      cdiv(M, 128) * cdiv(N, 128) > (int64_t(1) << 23))
+    return LOWBIT_E_SHAPE;
+  *bytes = gemm_mxfp4_workspace_bytes(x_dtype == LOWBIT_MXFP4, M, N, K);
+  return LOWBIT_OK;
 }
 
 namespace {

@@ -166,7 +166,9 @@ struct MxGemmArgs {
   const void* x_pscales;
   int ykind;                // YK_F32 / YK_BF16
   void* y;                  // [M][N]
+  void* ws;                 // workspace (counters first), or NULL if it needs none
 };
+size_t gemm_mxfp4_workspace_bytes(bool x4, int64_t M, int64_t N, int64_t K);
 hipError_t launch_gemm_mxfp4(const MxGemmArgs& a, hipStream_t s);
 
 struct KvArgs;

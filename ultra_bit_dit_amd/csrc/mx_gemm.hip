@@ -27,6 +27,10 @@ struct MxArgs {
   const uint8_t* xs;         // packed MXFP4 exponents of X
   void* y;
   int64_t G, GQ, NB, MB;     // groups, quads, row-blocks of W and of X
+  int64_t MT, NT;            // tiles of X rows and of W rows
+  int KS;                    // splits of K
+  float* part;               // partial tiles of the splits
+  uint32_t* cnt;             // arrivals per tile
 };
 
 template <int T>
@@ -59,130 +63,169 @@ __device__ __forceinline__ void store_y(void* y, int64_t i, float v) {
 }
 
 // ---------------------------------------------------------- few rows of X
-// One workgroup of up to 16 waves per (RB row-blocks of W, 16 MT rows of X);
-// the waves split the quads of K, each issues a whole quad's loads at once,
-// and the partial tiles are added over the waves in a fixed order.
+// Up to 16 rows: one workgroup per RB row-blocks of W whose waves split the
+// quads of K.  A wave loads a quad's codes a quad ahead, straight to registers;
+// bf16 rows of X reach the wave's own LDS as direct copies of 1 KiB (a row of
+// a quad), with the 16-byte chunk c of row r at place c ^ r so that an
+// operand's 16 rows fall on different banks.  The partial tiles are added over
+// the waves in a fixed order.
 constexpr int kSmallWaves = 12;
+constexpr int64_t kSmallRows = 16;
+constexpr int64_t kPairBlocks = 1024;  // two row-blocks a workgroup from here on
+constexpr int kSmallLds = 128 * 1024;  // of bf16 rows of X
+typedef __attribute__((address_space(3))) uint8_t lds_u8;
 
-template <bool X4, int MT, int RB, int YK>
+__device__ __forceinline__ void copy16(const uint8_t* src, lds_u8* dst) {
+  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
+                                   (__attribute__((address_space(3))) void*)dst, 16, 0, 0);
+}
+
+[[maybe_unused]] __device__ const mx_u4 mx_zeros[16] = {};
+
+template <bool X4, int RB>
+struct SmallQuad {
+  mx_u4 w[RB][4];
+  uint32_t ws[RB];
+  mx_u4 x[X4 ? 4 : 1];  // MXFP4 rows: one row-block
+  uint32_t xs;
+};
+
+template <bool X4, int RB>
+__device__ __forceinline__ void load_small(const MxArgs& a, int64_t rb0, int64_t gq, int lane, SmallQuad<X4, RB>& o) {
+  // groups past the last one read it again: their codes are cleared below
+#pragma unroll
+  for (int j = 0; j < RB; j++) {
+    const int64_t rb = rb0 + j < a.NB ? rb0 + j : a.NB - 1;
+    const uint8_t* src = a.wc + rb * a.G * 1024 + 16 * lane;
+#pragma unroll
+    for (int t = 0; t < 4; t++)
+      o.w[j][t] = __builtin_nontemporal_load((const mx_u4*)(src + min(4 * gq + t, a.G - 1) * 1024));
+    o.ws[j] = *(const uint32_t*)(a.ws + ((rb * a.GQ + gq) * 64 + lane) * 4);
+  }
+  if constexpr (X4) {
+#pragma unroll
+    for (int t = 0; t < 4; t++) o.x[t] = *(const mx_u4*)(a.x + (min(4 * gq + t, a.G - 1) * 64 + lane) * 16);
+    o.xs = *(const uint32_t*)(a.xs + (gq * 64 + lane) * 4);
+  }
+}
+
+template <bool X4, int RB, int YK>
 __global__ __launch_bounds__(64 * kSmallWaves) void mx_small(MxArgs a) {
-  extern __shared__ __attribute__((aligned(16))) float red[];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, W = blockDim.x >> 6;
-  const int r = lane & 15, q = lane >> 4;
-  const int64_t rb0 = (int64_t)blockIdx.x * RB, mb0 = (int64_t)blockIdx.y * MT;
-  v4f acc[MT][RB];
+#if defined(__HIP_DEVICE_COMPILE__)
+  extern __shared__ __attribute__((aligned(16))) uint8_t mem[];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), W = blockDim.x >> 6;
+  const int r = lane & 15, q = lane >> 4, rows = (int)a.M;
+  const int64_t rb0 = (int64_t)blockIdx.x * RB;
+  uint8_t* xw = mem + wave * rows * 1024;
+  v4f acc[RB][2];  // two chains each
 #pragma unroll
-  for (int i = 0; i < MT; i++)
+  for (int j = 0; j < RB; j++) acc[j][0] = acc[j][1] = v4f{0.f, 0.f, 0.f, 0.f};
+  const uint8_t* zeros = (const uint8_t*)mx_zeros;
+  auto copy_x = [&](int64_t gq) {
+    for (int m = 0; m < rows; m++) {
+      const int64_t k = gq * 512 + 8 * (lane ^ m);
+      copy16(k < a.K ? a.x + (m * a.ld + k) * 2 : zeros, (lds_u8*)xw + m * 1024);
+    }
+  };
+  const int mrow = r < rows ? r : rows - 1;  // rows of the operand past the last one repeat it
+  SmallQuad<X4, RB> cur, next;
+  int64_t gq = wave;
+  if (gq < a.GQ) {
+    if constexpr (!X4) copy_x(gq);
+    load_small<X4, RB>(a, rb0, gq, lane, cur);
+  }
+  for (; gq < a.GQ; gq += W) {
+    const bool more = gq + W < a.GQ;
+    // This quad's copies of X are the last loads issued: all are awaited here,
+    // and the next quad's codes are loaded behind the first read.
+    v8bf xf[2][4];
+    auto read_x = [&](int t) {
 #pragma unroll
-    for (int j = 0; j < RB; j++) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
-
-  for (int64_t gq = wave; gq < a.GQ; gq += W) {
-    mx_u4 wc[RB][4];
-    uint32_t wsc[RB];
+      for (int h = 0; h < 4; h++)
+        xf[t & 1][h] = *(const v8bf*)(xw + mrow * 1024 + (((16 * t + 4 * q + h) ^ mrow) * 16));
+    };
+    if constexpr (!X4) {
+      __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      read_x(0);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if (more) load_small<X4, RB>(a, rb0, gq + W, lane, next);
+    if (4 * gq + 3 >= a.G) {
 #pragma unroll
-    for (int j = 0; j < RB; j++) {
-      const int64_t rb = rb0 + j < a.NB ? rb0 + j : a.NB - 1;
+      for (int t = 1; t < 4; t++)
+        if (4 * gq + t >= a.G) {
 #pragma unroll
-      for (int t = 0; t < 4; t++) {
-        const int64_t g = 4 * gq + t;
-        wc[j][t] = mx_u4{0, 0, 0, 0};
-        if (g < a.G)
-          wc[j][t] = __builtin_nontemporal_load((const mx_u4*)(a.wc + ((rb * a.G + g) * 64 + lane) * 16));
-      }
-      wsc[j] = *(const uint32_t*)(a.ws + ((rb * a.GQ + gq) * 64 + lane) * 4);
+          for (int j = 0; j < RB; j++) cur.w[j][t] = mx_u4{0, 0, 0, 0};
+        }
     }
     if constexpr (X4) {
 #pragma unroll
-      for (int i = 0; i < MT; i++) {
-        const int64_t mb = mb0 + i < a.MB ? mb0 + i : a.MB - 1;
-        const uint32_t xsc = *(const uint32_t*)(a.xs + ((mb * a.GQ + gq) * 64 + lane) * 4);
-        mx_u4 xc[4];
-#pragma unroll
-        for (int t = 0; t < 4; t++) {
-          const int64_t g = 4 * gq + t;
-          xc[t] = mx_u4{0, 0, 0, 0};
-          if (g < a.G) xc[t] = *(const mx_u4*)(a.x + ((mb * a.G + g) * 64 + lane) * 16);
-        }
-#pragma unroll
-        for (int j = 0; j < RB; j++) {
-          acc[i][j] = mfma_mx<0>(xc[0], wc[j][0], acc[i][j], xsc, wsc[j]);
-          acc[i][j] = mfma_mx<1>(xc[1], wc[j][1], acc[i][j], xsc, wsc[j]);
-          acc[i][j] = mfma_mx<2>(xc[2], wc[j][2], acc[i][j], xsc, wsc[j]);
-          acc[i][j] = mfma_mx<3>(xc[3], wc[j][3], acc[i][j], xsc, wsc[j]);
-        }
+      for (int j = 0; j < RB; j++) {
+        acc[j][0] = mfma_mx<0>(cur.x[0], cur.w[j][0], acc[j][0], cur.xs, cur.ws[j]);
+        acc[j][1] = mfma_mx<1>(cur.x[1], cur.w[j][1], acc[j][1], cur.xs, cur.ws[j]);
+        acc[j][0] = mfma_mx<2>(cur.x[2], cur.w[j][2], acc[j][0], cur.xs, cur.ws[j]);
+        acc[j][1] = mfma_mx<3>(cur.x[3], cur.w[j][3], acc[j][1], cur.xs, cur.ws[j]);
       }
     } else {
 #pragma unroll
       for (int t = 0; t < 4; t++) {
-        const int64_t k = gq * 512 + 128 * t + 32 * q;
-        mx_u4 xv[MT][4];
+        if (t < 3) read_x(t + 1);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int i = 0; i < MT; i++) {
-          const int64_t m = (mb0 + i) * 16 + r;
+        for (int h = 0; h < 4; h++)
 #pragma unroll
-          for (int h = 0; h < 4; h++) xv[i][h] = mx_u4{0, 0, 0, 0};
-          // rows of the tile are independent: only the lanes of real rows load
-          if (m < a.M && k < a.K) {
-            const mx_u4* src = (const mx_u4*)(a.x + (m * a.ld + k) * 2);
-#pragma unroll
-            for (int h = 0; h < 4; h++) xv[i][h] = src[h];
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < RB; j++) {
-          const float s = scale_float(wsc[j], t);
-#pragma unroll
-          for (int h = 0; h < 4; h++) {
-            const v8bf b = bf16x8(wc[j][t][h], s);
-#pragma unroll
-            for (int i = 0; i < MT; i++)
-              acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, xv[i][h]), b,
-                                                                  acc[i][j], 0, 0, 0);
-          }
-        }
+          for (int j = 0; j < RB; j++)
+            acc[j][h & 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                xf[t & 1][h], bf16x8(cur.w[j][t][h], scale_float(cur.ws[j], t)), acc[j][h & 1], 0, 0, 0);
+      }
+      if (more) {
+        __asm__ volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // this quad's rows have been read
+        copy_x(gq + W);
       }
     }
+    if (more) cur = next;
   }
   // partial tiles to LDS, then added over the waves in order
-  constexpr int TILES = MT * RB;
-#pragma unroll
-  for (int i = 0; i < MT; i++)
-#pragma unroll
-    for (int j = 0; j < RB; j++) *(v4f*)(red + ((wave * TILES + i * RB + j) * 64 + lane) * 4) = acc[i][j];
   __syncthreads();
-  for (int it = threadIdx.x; it < TILES * 64; it += blockDim.x) {
+  float* red = (float*)mem;
+#pragma unroll
+  for (int j = 0; j < RB; j++) {
+    v4f v;
+#pragma unroll
+    for (int e = 0; e < 4; e++) v[e] = acc[j][0][e] + acc[j][1][e];
+    *(v4f*)(red + ((wave * RB + j) * 64 + lane) * 4) = v;
+  }
+  __syncthreads();
+  for (int it = threadIdx.x; it < RB * 64; it += blockDim.x) {
     v4f s = *(const v4f*)(red + it * 4);
     for (int w = 1; w < W; w++) {
-      const v4f v = *(const v4f*)(red + (w * TILES * 64 + it) * 4);
+      const v4f v = *(const v4f*)(red + (w * RB * 64 + it) * 4);
 #pragma unroll
       for (int e = 0; e < 4; e++) s[e] += v[e];
     }
-    const int tile = it >> 6, l = it & 63;
-    const int64_t n = (rb0 + tile % RB) * 16 + (l & 15);
+    const int l = it & 63;
+    const int64_t n = (rb0 + (it >> 6)) * 16 + (l & 15);
     if (n < a.N) {
 #pragma unroll
       for (int e = 0; e < 4; e++) {
-        const int64_t m = (mb0 + tile / RB) * 16 + 4 * (l >> 4) + e;
+        const int64_t m = 4 * (l >> 4) + e;
         if (m < a.M) store_y<YK>(a.y, m * a.N + n, s[e]);
       }
     }
   }
+#endif
 }
 
-int small_waves(int64_t GQ) {
-  const int64_t rounds = cdiv(GQ, kSmallWaves);
-  return (int)cdiv(GQ, rounds);
-}
-
-template <bool X4, int MT, int RB>
+template <bool X4, int RB>
 void launch_small(const MxArgs& a, int ykind, hipStream_t s) {
-  const int W = small_waves(a.GQ);
-  const dim3 grid((unsigned)cdiv(a.NB, RB), (unsigned)cdiv(cdiv(a.M, 16), MT));
-  const size_t lds = (size_t)W * MT * RB * 1024;
+  const int64_t most = X4 ? kSmallWaves : min((int64_t)kSmallWaves, (int64_t)(kSmallLds / 1024 / a.M));
+  const int W = (int)cdiv(a.GQ, cdiv(a.GQ, most));
+  const dim3 grid((unsigned)cdiv(a.NB, RB));
+  const size_t lds = (size_t)W * max((int64_t)RB, X4 ? 0 : a.M) * 1024;
   if (ykind == YK_F32)
-    hipLaunchKernelGGL((mx_small<X4, MT, RB, YK_F32>), grid, dim3(64 * W), lds, s, a);
+    hipLaunchKernelGGL((mx_small<X4, RB, YK_F32>), grid, dim3(64 * W), lds, s, a);
   else
-    hipLaunchKernelGGL((mx_small<X4, MT, RB, YK_BF16>), grid, dim3(64 * W), lds, s, a);
+    hipLaunchKernelGGL((mx_small<X4, RB, YK_BF16>), grid, dim3(64 * W), lds, s, a);
 }
 
 // ------------------------------------------------------------ many rows of X
@@ -192,15 +235,9 @@ void launch_small(const MxArgs& a, int ykind, hipStream_t s) {
 // exactly for its own (the later groups' stay in flight) and one barrier a
 // group keeps the ring.  W is operand A (rows n) and X operand B (columns m):
 // a lane then holds four consecutive n of one output row.
-typedef __attribute__((address_space(3))) uint8_t lds_u8;
-
 // s_waitcnt immediate: vmcnt n, lgkmcnt and expcnt at their maxima
 constexpr int vm_wait(int n) { return (n & 15) | ((n >> 4) << 14) | 0xF70; }
 
-__device__ __forceinline__ void copy16(const uint8_t* src, lds_u8* dst) {
-  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
-                                   (__attribute__((address_space(3))) void*)dst, 16, 0, 0);
-}
 template <int N>
 __device__ __forceinline__ void wait_copies_and_meet() {
   __asm__ volatile("" ::: "memory");
@@ -249,9 +286,61 @@ __device__ __forceinline__ void store_tile(const MxArgs& a, const v4f (&acc)[JN]
   }
 }
 
+// Splits of K: the tile's partial sums go to the workspace with
+// device-coherent stores that complete before the arrival is counted; the last
+// split to arrive adds them in the order of the splits and stores the tile.
+// Returns whether this workgroup does.
+template <int WAVES, int JN, int IM>
+__device__ __forceinline__ bool add_splits(const MxArgs& a, v4f (&acc)[JN][IM], int64_t tile, int ks, uint32_t* s_last) {
+  constexpr int64_t LANES = 64 * WAVES, TILE = LANES * JN * IM * 2;  // in pairs of floats
+  uint64_t* base = (uint64_t*)a.part + tile * a.KS * TILE + threadIdx.x;
+  uint64_t* mine = base + ks * TILE;
+#pragma unroll
+  for (int j = 0; j < JN; j++)
+#pragma unroll
+    for (int i = 0; i < IM; i++)
+#pragma unroll
+      for (int e = 0; e < 2; e++)
+        __hip_atomic_store(mine + ((j * IM + i) * 2 + e) * LANES,
+                           (uint64_t)__float_as_uint(acc[j][i][2 * e]) | ((uint64_t)__float_as_uint(acc[j][i][2 * e + 1]) << 32),
+                           __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
+  if (threadIdx.x == 0)
+    *s_last = __hip_atomic_fetch_add(a.cnt + tile, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  __syncthreads();
+  if (*s_last != (uint32_t)a.KS - 1) return false;
+  if (threadIdx.x == 0) __hip_atomic_store(a.cnt + tile, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+  for (int j = 0; j < JN; j++) {
+    v4f sum[IM];
+#pragma unroll
+    for (int i = 0; i < IM; i++) sum[i] = v4f{0.f, 0.f, 0.f, 0.f};
+    for (int k = 0; k < a.KS; k++) {
+      uint64_t v[IM][2];
+#pragma unroll
+      for (int i = 0; i < IM; i++)
+#pragma unroll
+        for (int e = 0; e < 2; e++)
+          v[i][e] = __hip_atomic_load(base + k * TILE + ((j * IM + i) * 2 + e) * LANES, __ATOMIC_RELAXED,
+                                      __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+      for (int i = 0; i < IM; i++)
+#pragma unroll
+        for (int e = 0; e < 2; e++) {
+          sum[i][2 * e] += __uint_as_float((uint32_t)v[i][e]);
+          sum[i][2 * e + 1] += __uint_as_float((uint32_t)(v[i][e] >> 32));
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < IM; i++) acc[j][i] = sum[i];
+  }
+  return true;
+}
+
 // X MXFP4.  WN x WM waves, each JN row-blocks of W by IM of X.
 template <int WN, int WM, int JN, int IM, int YK>
-__global__ __launch_bounds__(64 * WN * WM) void mx_gemm4(MxArgs a, int64_t MT, int64_t NT) {
+__global__ __launch_bounds__(64 * WN * WM) void mx_gemm4(MxArgs a) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int RN = WN * JN, RM = WM * IM, R = RN + RM, WAVES = WN * WM, CP = R / WAVES;
   static_assert(R % WAVES == 0 && R / 4 == WAVES, "one scale copy and CP code copies per wave");
@@ -262,8 +351,12 @@ __global__ __launch_bounds__(64 * WN * WM) void mx_gemm4(MxArgs a, int64_t MT, i
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wn = wave % WN, wm = wave / WN;
   int64_t mt, nt;
-  tile_of(blockIdx.x, MT, NT, &mt, &nt);
-  const int G = (int)a.G, GQ = (int)a.GQ;
+  const int64_t tiles = a.MT * a.NT, tile = blockIdx.x % tiles;
+  const int ks = (int)(blockIdx.x / tiles);
+  tile_of(tile, a.MT, a.NT, &mt, &nt);
+  // quads of this split; G: the end of its groups
+  const int Q0 = (int)(a.GQ * ks / a.KS), GQ = (int)(a.GQ * (ks + 1) / a.KS);
+  const int G0 = 4 * Q0, G = min(4 * GQ, (int)a.G);
 
   // this wave's code pieces: row-blocks CP wave .. of the tile's R (W first)
   const uint8_t* src[CP];
@@ -301,12 +394,12 @@ __global__ __launch_bounds__(64 * WN * WM) void mx_gemm4(MxArgs a, int64_t MT, i
     for (int i = 0; i < IM; i++) acc[j][i] = v4f{0.f, 0.f, 0.f, 0.f};
   uint32_t sw[JN], sx[IM];
 
-  copy_scales(0);
-  copy_group(0, b0);
+  copy_scales(Q0);
+  copy_group(G0, b0);
   __asm__ volatile("" ::: "memory");  // the waits below count the copies of each phase
-  copy_group(1, b1);
+  copy_group(G0 + 1, b1);
   __asm__ volatile("" ::: "memory");
-  copy_group(2, b2);
+  copy_group(G0 + 2, b2);
 
   auto compute = [&](auto tt, const uint8_t* buf) {
     constexpr int T = decltype(tt)::value;
@@ -352,7 +445,7 @@ __global__ __launch_bounds__(64 * WN * WM) void mx_gemm4(MxArgs a, int64_t MT, i
     compute(std::integral_constant<int, 2>{}, b2);
   };
   const int full = G & ~3;
-  for (int g = 0; g < full; g += 4) {
+  for (int g = G0; g < full; g += 4) {
     phase0(g);
     phase1(g);
     phase2(g);
@@ -365,16 +458,12 @@ __global__ __launch_bounds__(64 * WN * WM) void mx_gemm4(MxArgs a, int64_t MT, i
   if (full + 2 < G) phase2(full);
   // no copy may still be on its way to LDS when the workgroup ends
   __builtin_amdgcn_s_waitcnt(vm_wait(0));
+  if (a.KS > 1) {
+    __shared__ uint32_t s_last;
+    if (!add_splits<WN * WM, JN, IM>(a, acc, tile, ks, &s_last)) return;
+  }
   store_tile<YK, JN, IM>(a, acc, (nt * RN + wn * JN) * 16, (mt * RM + wm * IM) * 16, lane);
 #endif
-}
-
-template <int WN, int WM, int JN, int IM>
-void launch_tile4(const MxArgs& a, int ykind, hipStream_t s) {
-  const int64_t NT = cdiv(a.NB, WN * JN), MT = cdiv(a.MB, WM * IM);
-  const dim3 grid((unsigned)(NT * MT)), block(64 * WN * WM);
-  if (ykind == YK_F32) hipLaunchKernelGGL((mx_gemm4<WN, WM, JN, IM, YK_F32>), grid, block, 0, s, a, MT, NT);
-  else hipLaunchKernelGGL((mx_gemm4<WN, WM, JN, IM, YK_BF16>), grid, block, 0, s, a, MT, NT);
 }
 
 // X bf16.  WN x WM waves, each JN row-blocks of W by IM of X; two group
@@ -384,10 +473,8 @@ void launch_tile4(const MxArgs& a, int ykind, hipStream_t s) {
 // rows of an operand read fall on different banks.  Chunks past K come from a
 // block of zeros: the codes there are 0, but 0 times what follows a row of X
 // need not be.
-[[maybe_unused]] __device__ const mx_u4 mx_zeros[16] = {};
-
 template <int WN, int WM, int JN, int IM, int YK>
-__global__ __launch_bounds__(64 * WN * WM) void mx_gemm16(MxArgs a, int64_t MT, int64_t NT) {
+__global__ __launch_bounds__(64 * WN * WM) void mx_gemm16(MxArgs a) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int RN = WN * JN, RM = WM * IM, WAVES = WN * WM;
   constexpr int CW = RN / WAVES, CX = 4 * RM / WAVES;  // code and X copies of a wave (1 KiB each)
@@ -398,8 +485,12 @@ __global__ __launch_bounds__(64 * WN * WM) void mx_gemm16(MxArgs a, int64_t MT, 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wn = wave % WN, wm = wave / WN, r = lane & 15, q = lane >> 4;
   int64_t mt, nt;
-  tile_of(blockIdx.x, MT, NT, &mt, &nt);
-  const int G = (int)a.G, GQ = (int)a.GQ;
+  const int64_t tiles = a.MT * a.NT, tile = blockIdx.x % tiles;
+  const int ks = (int)(blockIdx.x / tiles);
+  tile_of(tile, a.MT, a.NT, &mt, &nt);
+  // quads of this split; G: the end of its groups
+  const int Q0 = (int)(a.GQ * ks / a.KS), GQ = (int)(a.GQ * (ks + 1) / a.KS);
+  const int G0 = 4 * Q0, G = min(4 * GQ, (int)a.G);
 
   const uint8_t* wsrc[CW];
 #pragma unroll
@@ -499,10 +590,10 @@ __global__ __launch_bounds__(64 * WN * WM) void mx_gemm16(MxArgs a, int64_t MT, 
     __builtin_amdgcn_sched_barrier(0);
     compute(std::integral_constant<int, 2>{}, b0);
   };
-  copy_group(0, b0);
-  copy_scales(0);
+  copy_group(G0, b0);
+  copy_scales(Q0);
   const int full = G & ~3;
-  for (int g = 0; g < full; g += 4) {
+  for (int g = G0; g < full; g += 4) {
     phase0(g);
     phase1(g);
     phase2(g);
@@ -515,22 +606,91 @@ __global__ __launch_bounds__(64 * WN * WM) void mx_gemm16(MxArgs a, int64_t MT, 
   if (full + 1 < G) phase1(full);
   if (full + 2 < G) phase2(full);
   __builtin_amdgcn_s_waitcnt(vm_wait(0));
+  if (a.KS > 1) {
+    __shared__ uint32_t s_last;
+    if (!add_splits<WN * WM, JN, IM>(a, acc, tile, ks, &s_last)) return;
+  }
   store_tile<YK, JN, IM>(a, acc, (nt * RN + wn * JN) * 16, (mt * RM + wm * IM) * 16, lane);
 #endif
 }
 
+// Tile shapes, in row-blocks of X and of W.
+struct Shape {
+  int rm, rn;
+};
+constexpr Shape kBig4{16, 16}, kSmall4{8, 8}, kBig16{8, 16}, kSmall16{4, 8};
+
+// What runs a product: few rows (small), or tiles of a shape with K in KS
+// splits.
+struct Plan {
+  bool small;
+  bool big;
+  int64_t MT, NT;
+  int KS;
+  size_t part_bytes;
+};
+
+// Cost in cycles of a launch of T tiles in KS splits: rounds over the chip's
+// slots, each the split's groups and a fixed start and end, and the last
+// arrival's reading of the other splits.
+double tile_cost(int64_t T, int KS, int64_t G, int slots, double group, double fixed, double join) {
+  const double rounds = (double)cdiv(T * KS, slots);
+  return rounds * ((double)cdiv(G, KS) * group + fixed) + (KS > 1 ? fixed + KS * join : 0.0);
+}
+
+Plan plan_gemm(bool x4, int64_t M, int64_t N, int64_t K) {
+  Plan p{};
+  if (M <= kSmallRows) {
+    p.small = true;
+    return p;
+  }
+  const int64_t MB = cdiv(M, 16), NB = cdiv(N, 16), G = mx_groups(K), GQ = mx_quads(K);
+  double best = 0;
+  for (int big = 0; big < 2; big++) {
+    const Shape sh = x4 ? (big ? kBig4 : kSmall4) : (big ? kBig16 : kSmall16);
+    const int64_t MT = cdiv(MB, sh.rm), NT = cdiv(NB, sh.rn), T = MT * NT;
+    const int slots = big ? 256 : 512;
+    // cycles of a group on a busy compute unit (small: two workgroups share it)
+    const double group = x4 ? (big ? 1300.0 : 900.0) : (big ? 2800.0 : 1500.0);
+    for (int KS = 1; KS <= 16; KS *= 2) {
+      if (KS > 1 && (GQ < 2 * KS || T * KS > 4 * slots || T > kMaxRowGroups)) break;
+      const double c = tile_cost(T, KS, G, slots, group, 6000.0, 40.0 * sh.rm * sh.rn / 16);
+      if (best == 0 || c < best) {
+        best = c;
+        p.big = big;
+        p.MT = MT;
+        p.NT = NT;
+        p.KS = KS;
+        p.part_bytes = KS > 1 ? (size_t)(T * KS * sh.rm * sh.rn) * 1024 : 0;
+      }
+    }
+  }
+  return p;
+}
+
+template <int WN, int WM, int JN, int IM>
+void launch_tile4(const MxArgs& a, int ykind, hipStream_t s) {
+  const dim3 grid((unsigned)(a.NT * a.MT * a.KS)), block(64 * WN * WM);
+  if (ykind == YK_F32) hipLaunchKernelGGL((mx_gemm4<WN, WM, JN, IM, YK_F32>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((mx_gemm4<WN, WM, JN, IM, YK_BF16>), grid, block, 0, s, a);
+}
 template <int WN, int WM, int JN, int IM>
 void launch_tile16(const MxArgs& a, int ykind, hipStream_t s) {
-  const int64_t NT = cdiv(a.NB, WN * JN), MT = cdiv(a.MB, WM * IM);
-  const dim3 grid((unsigned)(NT * MT)), block(64 * WN * WM);
-  if (ykind == YK_F32) hipLaunchKernelGGL((mx_gemm16<WN, WM, JN, IM, YK_F32>), grid, block, 0, s, a, MT, NT);
-  else hipLaunchKernelGGL((mx_gemm16<WN, WM, JN, IM, YK_BF16>), grid, block, 0, s, a, MT, NT);
+  const dim3 grid((unsigned)(a.NT * a.MT * a.KS)), block(64 * WN * WM);
+  if (ykind == YK_F32) hipLaunchKernelGGL((mx_gemm16<WN, WM, JN, IM, YK_F32>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((mx_gemm16<WN, WM, JN, IM, YK_BF16>), grid, block, 0, s, a);
 }
 
 }  // namespace
 
+size_t gemm_mxfp4_workspace_bytes(bool x4, int64_t M, int64_t N, int64_t K) {
+  const Plan p = plan_gemm(x4, M, N, K);
+  return p.part_bytes ? (size_t)kCounterBytes + p.part_bytes : 0;
+}
+
 hipError_t launch_gemm_mxfp4(const MxGemmArgs& g, hipStream_t s) {
-  MxArgs a;
+  const Plan p = plan_gemm(g.x4, g.M, g.N, g.K);
+  MxArgs a{};
   a.M = g.M;
   a.N = g.N;
   a.K = g.K;
@@ -544,12 +704,23 @@ hipError_t launch_gemm_mxfp4(const MxGemmArgs& g, hipStream_t s) {
   a.GQ = mx_quads(g.K);
   a.NB = cdiv(g.N, 16);
   a.MB = cdiv(g.M, 16);
-  if (g.x4 && a.M > 64) {
-    if (cdiv(a.NB, 16) * cdiv(a.MB, 16) >= 256) launch_tile4<4, 2, 4, 8>(a, g.ykind, s);
+  a.MT = p.MT;
+  a.NT = p.NT;
+  a.KS = p.KS;
+  if (p.part_bytes) {
+    a.cnt = (uint32_t*)g.ws + 16;
+    a.part = (float*)((uint8_t*)g.ws + kCounterBytes);
+  }
+  if (p.small) {
+    if (g.x4) a.NB >= kPairBlocks ? launch_small<true, 2>(a, g.ykind, s) : launch_small<true, 1>(a, g.ykind, s);
+    else a.NB >= kPairBlocks ? launch_small<false, 2>(a, g.ykind, s) : launch_small<false, 1>(a, g.ykind, s);
+  } else if (g.x4) {
+    if (p.big) launch_tile4<4, 2, 4, 8>(a, g.ykind, s);
     else launch_tile4<2, 2, 4, 4>(a, g.ykind, s);
-  } else if (g.x4) launch_small<true, 1, 1>(a, g.ykind, s);
-  else if (a.M > 64) launch_tile16<4, 2, 4, 4>(a, g.ykind, s);
-  else launch_small<false, 1, 1>(a, g.ykind, s);
+  } else {
+    if (p.big) launch_tile16<4, 2, 4, 4>(a, g.ykind, s);
+    else launch_tile16<4, 1, 2, 4>(a, g.ykind, s);
+  }
   return hipGetLastError();
 }
 

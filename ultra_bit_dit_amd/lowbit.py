@@ -26,7 +26,7 @@ EXPORTS = ("lowbit_abi_version", "lowbit_status_str", "lowbit_packed_bytes", "lo
            "lowbit_chain_create", "lowbit_chain_create_rows", "lowbit_chain_run", "lowbit_chain_status",
            "lowbit_chain_destroy",
            "lowbit_hbm_read_probe", "lowbit_quantize_weights", "lowbit_rotate_act",
-           "lowbit_mxfp4_bytes", "lowbit_pack_mxfp4", "lowbit_quantize_mxfp4", "lowbit_gemm_mxfp4",
+           "lowbit_mxfp4_bytes", "lowbit_pack_mxfp4", "lowbit_quantize_mxfp4", "lowbit_gemm_mxfp4", "lowbit_gemm_mxfp4_workspace",
            "lowbit_kv8_append", "lowbit_attention_kv8", "lowbit_attention_kv8_workspace")
 
 
@@ -98,6 +98,7 @@ def lib():
         L.lowbit_pack_mxfp4.argtypes = [i64, i64, vp, vp, vp, vp, vp]
         L.lowbit_quantize_mxfp4.argtypes = [i64, i64, i32, vp, i64, vp, vp, vp, vp]
         L.lowbit_gemm_mxfp4.argtypes = [i64, i64, i64, vp, vp, i32, vp, i64, vp, i32, vp, vp]
+        L.lowbit_gemm_mxfp4_workspace.argtypes = [i64, i64, i64, i32, szp]
         L.lowbit_kv8_append.argtypes = [kvp, kbp, i32, vp, vp, i64, i64, vp]
         L.lowbit_attention_kv8.argtypes = [kvp, kbp, i64, vp, i64, ctypes.c_float, i32, i64, vp, i64, vp, vp]
         L.lowbit_attention_kv8_workspace.argtypes = [kvp, kbp, i64, szp]
@@ -406,6 +407,14 @@ def gemm_mxfp4(M, N, K, pcodes, pscales, X, x_scales=None, y_dtype=F32, Y=None, 
     if rc:
         raise LowbitError("lowbit_gemm_mxfp4", rc)
     return Y
+
+
+def gemm_mxfp4_workspace(M, N, K, x_dtype):
+    """Workspace bytes lowbit_gemm_mxfp4 needs for these arguments (BF16 or MXFP4 activations)."""
+    n = ctypes.c_size_t()
+    _check("lowbit_gemm_mxfp4_workspace",
+           lib().lowbit_gemm_mxfp4_workspace(M, N, K, x_dtype, ctypes.byref(n)))
+    return n.value
 
 
 def empty_kv8(n_pages, page_tokens, kv_heads, head_dim, device="cuda"):
