@@ -28,7 +28,7 @@ struct MxArgs {
   void* y;
   int64_t G, GQ, NB, MB;     // groups, quads, row-blocks of W and of X
   int64_t MT, NT;            // tiles of X rows and of W rows
-  int KS;                    // splits of K
+  uint32_t KS;               // splits of K
   float* part;               // partial tiles of the splits
   uint32_t* cnt;             // arrivals per tile
 };
@@ -63,16 +63,15 @@ __device__ __forceinline__ void store_y(void* y, int64_t i, float v) {
 }
 
 // ---------------------------------------------------------- few rows of X
-// Up to 16 rows: one workgroup per RB row-blocks of W whose waves split the
-// quads of K.  A wave loads a quad's codes a quad ahead, straight to registers;
+// Up to 16 rows: workgroups per row-block of W (RB of them) and split of K,
+// whose waves take the quads in turn.  A wave loads a quad's codes a quad ahead, straight to registers;
 // bf16 rows of X reach the wave's own LDS as direct copies of 1 KiB (a row of
 // a quad), with the 16-byte chunk c of row r at place c ^ r so that an
 // operand's 16 rows fall on different banks.  The partial tiles are added over
 // the waves in a fixed order.
-constexpr int kSmallWaves = 12;
+constexpr int kSmallWaves = 8;
 constexpr int64_t kSmallRows = 16;
-constexpr int64_t kPairBlocks = 1024;  // two row-blocks a workgroup from here on
-constexpr int kSmallLds = 128 * 1024;  // of bf16 rows of X
+constexpr int kSmallSplits = 8;
 typedef __attribute__((address_space(3))) uint8_t lds_u8;
 
 __device__ __forceinline__ void copy16(const uint8_t* src, lds_u8* dst) {
@@ -109,13 +108,46 @@ __device__ __forceinline__ void load_small(const MxArgs& a, int64_t rb0, int64_t
   }
 }
 
+// four floats, device-coherent
+__device__ __forceinline__ void put_pairs(float* p, const v4f& v) {
+#pragma unroll
+  for (int e = 0; e < 2; e++)
+    __hip_atomic_store((uint64_t*)p + e,
+                       (uint64_t)__float_as_uint(v[2 * e]) | ((uint64_t)__float_as_uint(v[2 * e + 1]) << 32),
+                       __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ v4f get_pairs(const float* p) {
+  v4f v;
+#pragma unroll
+  for (int e = 0; e < 2; e++) {
+    const uint64_t u = __hip_atomic_load((const uint64_t*)p + e, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    v[2 * e] = __uint_as_float((uint32_t)u);
+    v[2 * e + 1] = __uint_as_float((uint32_t)(u >> 32));
+  }
+  return v;
+}
+
+// lane l's four outputs of a 16 x 16 tile (rows m = 4 (l / 16) .., column n = l % 16)
+template <int YK>
+__device__ __forceinline__ void store_small(const MxArgs& a, const v4f& s, int64_t rb, int l) {
+  const int64_t n = rb * 16 + (l & 15);
+  if (n >= a.N) return;
+#pragma unroll
+  for (int e = 0; e < 4; e++) {
+    const int64_t m = 4 * (l >> 4) + e;
+    if (m < a.M) store_y<YK>(a.y, m * a.N + n, s[e]);
+  }
+}
+
 template <bool X4, int RB, int YK>
 __global__ __launch_bounds__(64 * kSmallWaves) void mx_small(MxArgs a) {
 #if defined(__HIP_DEVICE_COMPILE__)
   extern __shared__ __attribute__((aligned(16))) uint8_t mem[];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), W = blockDim.x >> 6;
   const int r = lane & 15, q = lane >> 4, rows = (int)a.M;
-  const int64_t rb0 = (int64_t)blockIdx.x * RB;
+  const int64_t blk = blockIdx.x, rb0 = blk * RB;
+  const uint32_t ks = blockIdx.y, quads = (uint32_t)a.GQ;
+  const int64_t q0 = quads * ks / a.KS, q1 = quads * (ks + 1) / a.KS;  // quads of this split
   uint8_t* xw = mem + wave * rows * 1024;
   v4f acc[RB][2];  // two chains each
 #pragma unroll
@@ -129,13 +161,13 @@ __global__ __launch_bounds__(64 * kSmallWaves) void mx_small(MxArgs a) {
   };
   const int mrow = r < rows ? r : rows - 1;  // rows of the operand past the last one repeat it
   SmallQuad<X4, RB> cur, next;
-  int64_t gq = wave;
-  if (gq < a.GQ) {
+  int64_t gq = q0 + wave;
+  if (gq < q1) {
     if constexpr (!X4) copy_x(gq);
     load_small<X4, RB>(a, rb0, gq, lane, cur);
   }
-  for (; gq < a.GQ; gq += W) {
-    const bool more = gq + W < a.GQ;
+  for (; gq < q1; gq += W) {
+    const bool more = gq + W < q1;
     // This quad's copies of X are the last loads issued: all are awaited here,
     // and the next quad's codes are loaded behind the first read.
     v8bf xf[2][4];
@@ -196,6 +228,7 @@ __global__ __launch_bounds__(64 * kSmallWaves) void mx_small(MxArgs a) {
     *(v4f*)(red + ((wave * RB + j) * 64 + lane) * 4) = v;
   }
   __syncthreads();
+  // an item is a lane of a tile; a workgroup of one wave takes RB rounds
   for (int it = threadIdx.x; it < RB * 64; it += blockDim.x) {
     v4f s = *(const v4f*)(red + it * 4);
     for (int w = 1; w < W; w++) {
@@ -203,29 +236,63 @@ __global__ __launch_bounds__(64 * kSmallWaves) void mx_small(MxArgs a) {
 #pragma unroll
       for (int e = 0; e < 4; e++) s[e] += v[e];
     }
-    const int l = it & 63;
-    const int64_t n = (rb0 + (it >> 6)) * 16 + (l & 15);
-    if (n < a.N) {
-#pragma unroll
-      for (int e = 0; e < 4; e++) {
-        const int64_t m = 4 * (l >> 4) + e;
-        if (m < a.M) store_y<YK>(a.y, m * a.N + n, s[e]);
-      }
+    if (a.KS == 1) {
+      store_small<YK>(a, s, rb0 + (it >> 6), it & 63);
+    } else {
+      put_pairs(a.part + (((int64_t)ks * a.NT + blk) * RB * 64 + it) * 4, s);
     }
+  }
+  if (a.KS == 1) return;
+  // Splits of K: the last to arrive adds the partial tiles in their order.
+  __shared__ uint32_t s_last;
+  __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
+  if (threadIdx.x == 0) s_last = __hip_atomic_fetch_add(a.cnt + blk, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  __syncthreads();
+  if (s_last != a.KS - 1) return;
+  if (threadIdx.x == 0) __hip_atomic_store(a.cnt + blk, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  for (int it = threadIdx.x; it < RB * 64; it += blockDim.x) {
+    v4f v[kSmallSplits];
+#pragma unroll
+    for (int k = 0; k < kSmallSplits; k++)
+      v[k] = k < (int)a.KS ? get_pairs(a.part + (((int64_t)k * a.NT + blk) * RB * 64 + it) * 4) : v4f{0.f, 0.f, 0.f, 0.f};
+    v4f s = v[0];
+#pragma unroll
+    for (int k = 1; k < kSmallSplits; k++)
+#pragma unroll
+      for (int e = 0; e < 4; e++) s[e] += v[k][e];
+    store_small<YK>(a, s, rb0 + (it >> 6), it & 63);
   }
 #endif
 }
 
-template <bool X4, int RB>
-void launch_small(const MxArgs& a, int ykind, hipStream_t s) {
-  const int64_t most = X4 ? kSmallWaves : min((int64_t)kSmallWaves, (int64_t)(kSmallLds / 1024 / a.M));
-  const int W = (int)cdiv(a.GQ, cdiv(a.GQ, most));
-  const dim3 grid((unsigned)cdiv(a.NB, RB));
-  const size_t lds = (size_t)W * max((int64_t)RB, X4 ? 0 : a.M) * 1024;
+// Waves W of a workgroup and splits KS of K for NB row-blocks, GQ quads and M
+// rows of X.  Four waves where the row-blocks alone fill the chip's 16 waves a
+// compute unit, so that several workgroups share one and one starts while
+// another ends (1 x 34816 x 5120: 21 us, 24 with 5 to 10 waves), else eight
+// (1 x 5120 x 5120: 5.5 us, 6.4 with four or ten), fewer where three workgroups'
+// rows of X would not fit the LDS.  K is split over workgroups where even so
+// few waves run long: a join costs about 2.5 us, a wave's quad 1.25 (5 rows,
+// 700 x 17408: 6.4 us, 8.5 without).
+void plan_small(bool x4, int64_t M, int64_t NB, int64_t GQ, int* W_, int* KS_) {
+  int64_t W = NB >= 640 ? 4 : 8;
+  if (!x4) W = max((int64_t)1, min(W, 48 / M));
+  W = cdiv(GQ, cdiv(GQ, W));
+  int64_t KS = 1;
+  const int64_t turns = cdiv(GQ, W);
+  if (turns >= 4 && NB * W < 1024) KS = min(min((int64_t)kSmallSplits, turns), 4096 / (NB * W));
+  *W_ = (int)W;
+  *KS_ = (int)KS;
+}
+
+template <bool X4>
+void launch_small(const MxArgs& a, int W, int ykind, hipStream_t s) {
+  const dim3 grid((unsigned)a.NT, (unsigned)a.KS);
+  const size_t lds = (size_t)W * max((int64_t)1, X4 ? 0 : a.M) * 1024;
   if (ykind == YK_F32)
-    hipLaunchKernelGGL((mx_small<X4, RB, YK_F32>), grid, dim3(64 * W), lds, s, a);
+    hipLaunchKernelGGL((mx_small<X4, 1, YK_F32>), grid, dim3(64 * W), lds, s, a);
   else
-    hipLaunchKernelGGL((mx_small<X4, RB, YK_BF16>), grid, dim3(64 * W), lds, s, a);
+    hipLaunchKernelGGL((mx_small<X4, 1, YK_BF16>), grid, dim3(64 * W), lds, s, a);
 }
 
 // ------------------------------------------------------------ many rows of X
@@ -249,93 +316,81 @@ __device__ __forceinline__ void wait_copies_and_meet() {
 // Tile of workgroup bid: each XCD (bid % 8) takes a contiguous run of tiles,
 // in bands of 8 row tiles of X with those running fastest, so that the
 // workgroups of an XCD share both operands in its L2.
-__device__ __forceinline__ void tile_of(int64_t bid, int64_t MT, int64_t NT, int64_t* mt, int64_t* nt) {
-  const int64_t T = MT * NT, per = T / 8, rem = T % 8, x = bid % 8, i = bid / 8;
-  const int64_t t = x * per + (x < rem ? x : rem) + i;
-  const int64_t band = t / (8 * NT), left = MT - band * 8, w = left < 8 ? left : 8, r = t - band * 8 * NT;
+__device__ __forceinline__ void tile_of(uint32_t bid, uint32_t MT, uint32_t NT, int64_t* mt, int64_t* nt) {
+  const uint32_t T = MT * NT, per = T / 8, rem = T % 8, x = bid % 8, i = bid / 8;
+  const uint32_t t = x * per + (x < rem ? x : rem) + i;
+  const uint32_t band = t / (8 * NT), left = MT - band * 8, w = left < 8 ? left : 8, r = t - band * 8 * NT;
   *mt = band * 8 + r % w;
   *nt = r / w;
 }
 
-template <int YK, int JN, int IM>
-__device__ __forceinline__ void store_tile(const MxArgs& a, const v4f (&acc)[JN][IM], int64_t n0, int64_t m0, int lane) {
-  const int r = lane & 15, q = lane >> 4;
+// four consecutive outputs of row m from column n on
+template <int YK>
+__device__ __forceinline__ void store_quad(const MxArgs& a, int64_t m, int64_t n, const v4f& v) {
+  if (a.N % 4 == 0 && n + 3 < a.N) {
+    if constexpr (YK == YK_F32) {
+      *(v4f*)((float*)a.y + m * a.N + n) = v;
+    } else {
+      uint2 w;
+      w.x = bf16_bits(v[0]) | (bf16_bits(v[1]) << 16);
+      w.y = bf16_bits(v[2]) | (bf16_bits(v[3]) << 16);
+      *(uint2*)((uint16_t*)a.y + m * a.N + n) = w;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; e++)
+      if (n + e < a.N) store_y<YK>(a.y, m * a.N + n + e, v[e]);
+  }
+}
+
+// A wave's part of a tile: to Y, or with K split over workgroups to the
+// workspace, [split][tile][part of a wave][thread], for mx_reduce to add.
+template <int YK, int THREADS, int JN, int IM>
+__device__ __forceinline__ void store_tile(const MxArgs& a, const v4f (&acc)[JN][IM], int64_t n0, int64_t m0, int64_t tile,
+                                           uint32_t ks) {
+  const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+  if (a.KS > 1) {
+    v4f* p = (v4f*)a.part + ((int64_t)ks * a.MT * a.NT + tile) * (JN * IM * THREADS) + threadIdx.x;
+#pragma unroll
+    for (int j = 0; j < JN; j++)
+#pragma unroll
+      for (int i = 0; i < IM; i++) p[(j * IM + i) * THREADS] = acc[j][i];
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < IM; i++) {
     const int64_t m = m0 + 16 * i + r;
     if (m >= a.M) continue;
 #pragma unroll
-    for (int j = 0; j < JN; j++) {
-      const int64_t n = n0 + 16 * j + 4 * q;
-      const v4f v = acc[j][i];
-      if (a.N % 4 == 0 && n + 3 < a.N) {
-        if constexpr (YK == YK_F32) {
-          *(v4f*)((float*)a.y + m * a.N + n) = v;
-        } else {
-          uint2 w;
-          w.x = bf16_bits(v[0]) | (bf16_bits(v[1]) << 16);
-          w.y = bf16_bits(v[2]) | (bf16_bits(v[3]) << 16);
-          *(uint2*)((uint16_t*)a.y + m * a.N + n) = w;
-        }
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; e++)
-          if (n + e < a.N) store_y<YK>(a.y, m * a.N + n + e, v[e]);
-      }
-    }
+    for (int j = 0; j < JN; j++) store_quad<YK>(a, m, n0 + 16 * j + 4 * q, acc[j][i]);
   }
 }
 
-// Splits of K: the tile's partial sums go to the workspace with
-// device-coherent stores that complete before the arrival is counted; the last
-// split to arrive adds them in the order of the splits and stores the tile.
-// Returns whether this workgroup does.
-template <int WAVES, int JN, int IM>
-__device__ __forceinline__ bool add_splits(const MxArgs& a, v4f (&acc)[JN][IM], int64_t tile, int ks, uint32_t* s_last) {
-  constexpr int64_t LANES = 64 * WAVES, TILE = LANES * JN * IM * 2;  // in pairs of floats
-  uint64_t* base = (uint64_t*)a.part + tile * a.KS * TILE + threadIdx.x;
-  uint64_t* mine = base + ks * TILE;
+// The splits of K added in their order, four outputs a thread.  (The last
+// split to arrive adding the others' tiles was slower: one workgroup reads
+// KS tiles at 30 GB/s, 300 x 700 x 17408 in eight splits 12 us.)
+template <int WN, int WM, int JN, int IM, int YK>
+__global__ __launch_bounds__(256) void mx_reduce(MxArgs a) {
+  constexpr int THREADS = 64 * WN * WM, PARTS = JN * IM;
+  static_assert(THREADS % 256 == 0, "a block lies in one part of a tile");
+  const uint32_t blk = blockIdx.x, per_tile = PARTS * THREADS / 256;
+  const uint32_t tile = blk / per_tile, in = blk % per_tile, part = in / (THREADS / 256);
+  const int tid = (in % (THREADS / 256)) * 256 + threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  int64_t mt, nt;
+  tile_of(tile, (uint32_t)a.MT, (uint32_t)a.NT, &mt, &nt);
+  const int wn = wave % WN, wm = wave / WN, j = part / IM, i = part % IM;
+  const int64_t n = (nt * WN * JN + wn * JN + j) * 16 + 4 * (lane >> 4);
+  const int64_t m = (mt * WM * IM + wm * IM + i) * 16 + (lane & 15);
+  if (m >= a.M || n >= a.N) return;
+  const int64_t step = a.MT * a.NT * (int64_t)(PARTS * THREADS);
+  const v4f* p = (const v4f*)a.part + ((int64_t)tile * PARTS + part) * THREADS + tid;
+  v4f s = p[0];
+  for (uint32_t k = 1; k < a.KS; k++) {
+    const v4f v = p[k * step];
 #pragma unroll
-  for (int j = 0; j < JN; j++)
-#pragma unroll
-    for (int i = 0; i < IM; i++)
-#pragma unroll
-      for (int e = 0; e < 2; e++)
-        __hip_atomic_store(mine + ((j * IM + i) * 2 + e) * LANES,
-                           (uint64_t)__float_as_uint(acc[j][i][2 * e]) | ((uint64_t)__float_as_uint(acc[j][i][2 * e + 1]) << 32),
-                           __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
-  __syncthreads();
-  if (threadIdx.x == 0)
-    *s_last = __hip_atomic_fetch_add(a.cnt + tile, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  __syncthreads();
-  if (*s_last != (uint32_t)a.KS - 1) return false;
-  if (threadIdx.x == 0) __hip_atomic_store(a.cnt + tile, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-#pragma unroll
-  for (int j = 0; j < JN; j++) {
-    v4f sum[IM];
-#pragma unroll
-    for (int i = 0; i < IM; i++) sum[i] = v4f{0.f, 0.f, 0.f, 0.f};
-    for (int k = 0; k < a.KS; k++) {
-      uint64_t v[IM][2];
-#pragma unroll
-      for (int i = 0; i < IM; i++)
-#pragma unroll
-        for (int e = 0; e < 2; e++)
-          v[i][e] = __hip_atomic_load(base + k * TILE + ((j * IM + i) * 2 + e) * LANES, __ATOMIC_RELAXED,
-                                      __HIP_MEMORY_SCOPE_AGENT);
-#pragma unroll
-      for (int i = 0; i < IM; i++)
-#pragma unroll
-        for (int e = 0; e < 2; e++) {
-          sum[i][2 * e] += __uint_as_float((uint32_t)v[i][e]);
-          sum[i][2 * e + 1] += __uint_as_float((uint32_t)(v[i][e] >> 32));
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < IM; i++) acc[j][i] = sum[i];
+    for (int e = 0; e < 4; e++) s[e] += v[e];
   }
-  return true;
+  store_quad<YK>(a, m, n, s);
 }
 
 // X MXFP4.  WN x WM waves, each JN row-blocks of W by IM of X.
@@ -351,11 +406,11 @@ __global__ __launch_bounds__(64 * WN * WM) void mx_gemm4(MxArgs a) {
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wn = wave % WN, wm = wave / WN;
   int64_t mt, nt;
-  const int64_t tiles = a.MT * a.NT, tile = blockIdx.x % tiles;
-  const int ks = (int)(blockIdx.x / tiles);
-  tile_of(tile, a.MT, a.NT, &mt, &nt);
+  const int64_t tile = blockIdx.x;
+  const uint32_t ks = blockIdx.y, quads = (uint32_t)a.GQ;
+  tile_of(blockIdx.x, (uint32_t)a.MT, (uint32_t)a.NT, &mt, &nt);
   // quads of this split; G: the end of its groups
-  const int Q0 = (int)(a.GQ * ks / a.KS), GQ = (int)(a.GQ * (ks + 1) / a.KS);
+  const int Q0 = (int)(quads * ks / a.KS), GQ = (int)(quads * (ks + 1) / a.KS);
   const int G0 = 4 * Q0, G = min(4 * GQ, (int)a.G);
 
   // this wave's code pieces: row-blocks CP wave .. of the tile's R (W first)
@@ -458,38 +513,37 @@ __global__ __launch_bounds__(64 * WN * WM) void mx_gemm4(MxArgs a) {
   if (full + 2 < G) phase2(full);
   // no copy may still be on its way to LDS when the workgroup ends
   __builtin_amdgcn_s_waitcnt(vm_wait(0));
-  if (a.KS > 1) {
-    __shared__ uint32_t s_last;
-    if (!add_splits<WN * WM, JN, IM>(a, acc, tile, ks, &s_last)) return;
-  }
-  store_tile<YK, JN, IM>(a, acc, (nt * RN + wn * JN) * 16, (mt * RM + wm * IM) * 16, lane);
+  store_tile<YK, 64 * WAVES, JN, IM>(a, acc, (nt * RN + wn * JN) * 16, (mt * RM + wm * IM) * 16, tile, ks);
 #endif
 }
 
-// X bf16.  WN x WM waves, each JN row-blocks of W by IM of X; two group
-// buffers, the next group's copies in flight while one is multiplied (2048
-// cycles of MFMA per SIMD, longer than a copy takes).  A row of X is 256 bytes
+// X bf16.  WN x WM waves, each JN row-blocks of W by IM of X.  RING 2: two
+// group buffers, the next group's copies in flight while one is multiplied
+// (large tiles: 2048 cycles of MFMA per SIMD, longer than a copy takes).  RING
+// 4: copies three groups ahead, for tiles that are multiplied faster than that.  A row of X is 256 bytes
 // of a group; its 16-byte chunk c lies at place c ^ (row % 16), so that the 16
 // rows of an operand read fall on different banks.  Chunks past K come from a
 // block of zeros: the codes there are 0, but 0 times what follows a row of X
 // need not be.
-template <int WN, int WM, int JN, int IM, int YK>
+template <int WN, int WM, int JN, int IM, int RING, int YK>
 __global__ __launch_bounds__(64 * WN * WM) void mx_gemm16(MxArgs a) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int RN = WN * JN, RM = WM * IM, WAVES = WN * WM;
   constexpr int CW = RN / WAVES, CX = 4 * RM / WAVES;  // code and X copies of a wave (1 KiB each)
-  constexpr int CS = (RN / 4 + WAVES - 1) / WAVES;     // exponent copies, waves below RN / 4
-  static_assert(CW * WAVES == RN && CX * WAVES == 4 * RM && CS == 1, "whole copies per wave");
+  constexpr int CP = CW + CX;
+  static_assert(CW * WAVES == RN && CX * WAVES == 4 * RM && RN / 4 <= WAVES, "whole copies per wave");
+  static_assert(RING == 2 || RING == 4, "buffers of a quad's groups in turn");
   constexpr int XB = RM * 4096, CB = RN * 1024;
   __shared__ __attribute__((aligned(16))) uint8_t b0[XB + CB + RN * 256], b1[XB + CB];
+  __shared__ __attribute__((aligned(16))) uint8_t b2[RING == 4 ? XB + CB : 16], b3[RING == 4 ? XB + CB : 16];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wn = wave % WN, wm = wave / WN, r = lane & 15, q = lane >> 4;
   int64_t mt, nt;
-  const int64_t tiles = a.MT * a.NT, tile = blockIdx.x % tiles;
-  const int ks = (int)(blockIdx.x / tiles);
-  tile_of(tile, a.MT, a.NT, &mt, &nt);
+  const int64_t tile = blockIdx.x;
+  const uint32_t ks = blockIdx.y, quads = (uint32_t)a.GQ;
+  tile_of(blockIdx.x, (uint32_t)a.MT, (uint32_t)a.NT, &mt, &nt);
   // quads of this split; G: the end of its groups
-  const int Q0 = (int)(a.GQ * ks / a.KS), GQ = (int)(a.GQ * (ks + 1) / a.KS);
+  const int Q0 = (int)(quads * ks / a.KS), GQ = (int)(quads * (ks + 1) / a.KS);
   const int G0 = 4 * Q0, G = min(4 * GQ, (int)a.G);
 
   const uint8_t* wsrc[CW];
@@ -510,9 +564,12 @@ __global__ __launch_bounds__(64 * WN * WM) void mx_gemm16(MxArgs a) {
     xk[i] = 8 * ((lane & 15) ^ (row & 15));
     xsrc[i] = a.x + (m * a.ld + xk[i]) * 2;
   }
+  // four row-blocks' exponents; waves past RN / 4 repeat another's copy, so
+  // that all count the same copies
+  const int sp = wave % (RN / 4);
   const uint8_t* ssrc;
   {
-    int64_t rb = nt * RN + 4 * wave + (lane >> 4);
+    int64_t rb = nt * RN + 4 * sp + (lane >> 4);
     rb = rb < a.NB - 1 ? rb : a.NB - 1;
     ssrc = a.ws + rb * a.GQ * 256 + 16 * (lane & 15);
   }
@@ -527,7 +584,7 @@ __global__ __launch_bounds__(64 * WN * WM) void mx_gemm16(MxArgs a) {
     for (int i = 0; i < CW; i++) copy16(wsrc[i] + (int64_t)g * 1024, (lds_u8*)buf + XB + (CW * wave + i) * 1024);
   };
   auto copy_scales = [&](int gq) {
-    if (4 * wave < RN) copy16(ssrc + (int64_t)(gq < GQ ? gq : GQ - 1) * 256, (lds_u8*)b0 + XB + CB + wave * 1024);
+    copy16(ssrc + (int64_t)(gq < GQ ? gq : GQ - 1) * 256, (lds_u8*)b0 + XB + CB + sp * 1024);
   };
 
   v4f acc[JN][IM];
@@ -567,50 +624,88 @@ __global__ __launch_bounds__(64 * WN * WM) void mx_gemm16(MxArgs a) {
 #pragma unroll
     for (int j = 0; j < JN; j++) sw[j] = *(const uint32_t*)(b0 + XB + CB + (wn * JN + j) * 256 + 4 * lane);
   };
-  // Each phase waits for its group (the only copies in flight), meets the
-  // other waves, which have then read the other buffer, and refills that one.
-  // The next quad's exponents travel behind every wave's read of this quad's.
-  auto phase0 = [&](int g) {
-    wait_copies_and_meet<0>();
-    copy_group(g + 1, b1);
-    __builtin_amdgcn_sched_barrier(0);
-    scales();
-    compute(std::integral_constant<int, 0>{}, b0);
-  };
-  auto phase1 = [&](int g) {
-    wait_copies_and_meet<0>();
-    copy_group(g + 2, b0);
-    copy_scales(g / 4 + 1);
-    __builtin_amdgcn_sched_barrier(0);
-    compute(std::integral_constant<int, 1>{}, b1);
-  };
-  auto phase2 = [&](int g) {
-    wait_copies_and_meet<0>();
-    copy_group(g + 3, b1);
-    __builtin_amdgcn_sched_barrier(0);
-    compute(std::integral_constant<int, 2>{}, b0);
-  };
-  copy_group(G0, b0);
-  copy_scales(Q0);
   const int full = G & ~3;
-  for (int g = G0; g < full; g += 4) {
-    phase0(g);
-    phase1(g);
-    phase2(g);
-    wait_copies_and_meet<0>();
-    copy_group(g + 4, b0);
-    __builtin_amdgcn_sched_barrier(0);
-    compute(std::integral_constant<int, 3>{}, b1);
+  if constexpr (RING == 2) {
+    // Each phase waits for its group (the only copies in flight), meets the
+    // other waves, which have then read the other buffer, and refills that one.
+    // The next quad's exponents travel behind every wave's read of this quad's.
+    auto phase0 = [&](int g) {
+      wait_copies_and_meet<0>();
+      copy_group(g + 1, b1);
+      __builtin_amdgcn_sched_barrier(0);
+      scales();
+      compute(std::integral_constant<int, 0>{}, b0);
+    };
+    auto phase1 = [&](int g) {
+      wait_copies_and_meet<0>();
+      copy_group(g + 2, b0);
+      copy_scales(g / 4 + 1);
+      __builtin_amdgcn_sched_barrier(0);
+      compute(std::integral_constant<int, 1>{}, b1);
+    };
+    auto phase2 = [&](int g) {
+      wait_copies_and_meet<0>();
+      copy_group(g + 3, b1);
+      __builtin_amdgcn_sched_barrier(0);
+      compute(std::integral_constant<int, 2>{}, b0);
+    };
+    copy_group(G0, b0);
+    copy_scales(Q0);
+    for (int g = G0; g < full; g += 4) {
+      phase0(g);
+      phase1(g);
+      phase2(g);
+      wait_copies_and_meet<0>();
+      copy_group(g + 4, b0);
+      __builtin_amdgcn_sched_barrier(0);
+      compute(std::integral_constant<int, 3>{}, b1);
+    }
+    if (full < G) phase0(full);
+    if (full + 1 < G) phase1(full);
+    if (full + 2 < G) phase2(full);
+  } else {
+    // as mx_gemm4's phases: each waits for the copies issued three phases ago
+    auto phase0 = [&](int g) {
+      wait_copies_and_meet<2 * CP>();
+      copy_group(g + 3, b3);
+      __builtin_amdgcn_sched_barrier(0);
+      scales();
+      compute(std::integral_constant<int, 0>{}, b0);
+    };
+    auto phase1 = [&](int g) {
+      wait_copies_and_meet<2 * CP>();
+      copy_group(g + 4, b0);
+      copy_scales(g / 4 + 1);
+      __builtin_amdgcn_sched_barrier(0);
+      compute(std::integral_constant<int, 1>{}, b1);
+    };
+    auto phase2 = [&](int g) {
+      wait_copies_and_meet<2 * CP + 1>();
+      copy_group(g + 5, b1);
+      __builtin_amdgcn_sched_barrier(0);
+      compute(std::integral_constant<int, 2>{}, b2);
+    };
+    copy_scales(Q0);
+    copy_group(G0, b0);
+    __asm__ volatile("" ::: "memory");  // the waits count the copies of each phase
+    copy_group(G0 + 1, b1);
+    __asm__ volatile("" ::: "memory");
+    copy_group(G0 + 2, b2);
+    for (int g = G0; g < full; g += 4) {
+      phase0(g);
+      phase1(g);
+      phase2(g);
+      wait_copies_and_meet<2 * CP + 1>();
+      copy_group(g + 6, b2);
+      __builtin_amdgcn_sched_barrier(0);
+      compute(std::integral_constant<int, 3>{}, b3);
+    }
+    if (full < G) phase0(full);
+    if (full + 1 < G) phase1(full);
+    if (full + 2 < G) phase2(full);
   }
-  if (full < G) phase0(full);
-  if (full + 1 < G) phase1(full);
-  if (full + 2 < G) phase2(full);
   __builtin_amdgcn_s_waitcnt(vm_wait(0));
-  if (a.KS > 1) {
-    __shared__ uint32_t s_last;
-    if (!add_splits<WN * WM, JN, IM>(a, acc, tile, ks, &s_last)) return;
-  }
-  store_tile<YK, JN, IM>(a, acc, (nt * RN + wn * JN) * 16, (mt * RM + wm * IM) * 16, lane);
+  store_tile<YK, 64 * WAVES, JN, IM>(a, acc, (nt * RN + wn * JN) * 16, (mt * RM + wm * IM) * 16, tile, ks);
 #endif
 }
 
@@ -625,36 +720,37 @@ constexpr Shape kBig4{16, 16}, kSmall4{8, 8}, kBig16{8, 16}, kSmall16{4, 8};
 struct Plan {
   bool small;
   bool big;
-  int64_t MT, NT;
-  int KS;
+  int64_t MT, NT;     // small: NT row-blocks of W
+  int KS, W;          // W: waves of a workgroup of few rows
   size_t part_bytes;
 };
-
-// Cost in cycles of a launch of T tiles in KS splits: rounds over the chip's
-// slots, each the split's groups and a fixed start and end, and the last
-// arrival's reading of the other splits.
-double tile_cost(int64_t T, int KS, int64_t G, int slots, double group, double fixed, double join) {
-  const double rounds = (double)cdiv(T * KS, slots);
-  return rounds * ((double)cdiv(G, KS) * group + fixed) + (KS > 1 ? fixed + KS * join : 0.0);
-}
 
 Plan plan_gemm(bool x4, int64_t M, int64_t N, int64_t K) {
   Plan p{};
   if (M <= kSmallRows) {
     p.small = true;
+    p.NT = cdiv(N, 16);
+    plan_small(x4, M, p.NT, mx_quads(K), &p.W, &p.KS);
+    p.part_bytes = p.KS > 1 ? (size_t)(p.NT * p.KS) * 1024 : 0;
     return p;
   }
-  const int64_t MB = cdiv(M, 16), NB = cdiv(N, 16), G = mx_groups(K), GQ = mx_quads(K);
+  const int64_t MB = cdiv(M, 16), NB = cdiv(N, 16), GQ = mx_quads(K);
+  // Microseconds of each choice: rounds over the chip, a round the groups of a
+  // split (`busy` where all compute units work, `idle` for few tiles; both
+  // measured) and its start and end; a split adds a launch and the partial
+  // tiles' way to memory and back.
   double best = 0;
   for (int big = 0; big < 2; big++) {
     const Shape sh = x4 ? (big ? kBig4 : kSmall4) : (big ? kBig16 : kSmall16);
     const int64_t MT = cdiv(MB, sh.rm), NT = cdiv(NB, sh.rn), T = MT * NT;
-    const int slots = big ? 256 : 512;
-    // cycles of a group on a busy compute unit (small: two workgroups share it)
-    const double group = x4 ? (big ? 1300.0 : 900.0) : (big ? 2800.0 : 1500.0);
+    const int per_cu = x4 && !big ? 2 : 1;
+    const double busy = x4 ? (big ? 1.0 : 0.6) : (big ? 1.53 : 0.51), idle = x4 ? (big ? 0.65 : 0.29) : (big ? 1.28 : 0.47);
     for (int KS = 1; KS <= 16; KS *= 2) {
-      if (KS > 1 && (GQ < 2 * KS || T * KS > 4 * slots || T > kMaxRowGroups)) break;
-      const double c = tile_cost(T, KS, G, slots, group, 6000.0, 40.0 * sh.rm * sh.rn / 16);
+      if (KS > 1 && (GQ < 2 * KS || T * KS > 1024)) break;
+      const double load = (double)(T * KS) / 256, groups = (double)cdiv(GQ, KS) * 4;
+      const double rounds = load <= per_cu ? 1.0 : (double)cdiv(T * KS, 256 * per_cu);
+      const double group = load <= 1 ? idle + (busy - idle) * load * (per_cu == 1 ? 1.0 : 0.5) : busy;
+      const double c = rounds * (groups * group + 2.5) + (KS > 1 ? 3.0 + (double)(T * KS) * sh.rm * sh.rn * 2048e-6 / 4.0 : 0.0);
       if (best == 0 || c < best) {
         best = c;
         p.big = big;
@@ -669,16 +765,25 @@ Plan plan_gemm(bool x4, int64_t M, int64_t N, int64_t K) {
 }
 
 template <int WN, int WM, int JN, int IM>
+void launch_reduce(const MxArgs& a, int ykind, hipStream_t s) {
+  const dim3 grid((unsigned)(a.MT * a.NT * JN * IM * WN * WM / 4));
+  if (ykind == YK_F32) hipLaunchKernelGGL((mx_reduce<WN, WM, JN, IM, YK_F32>), grid, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((mx_reduce<WN, WM, JN, IM, YK_BF16>), grid, dim3(256), 0, s, a);
+}
+
+template <int WN, int WM, int JN, int IM>
 void launch_tile4(const MxArgs& a, int ykind, hipStream_t s) {
-  const dim3 grid((unsigned)(a.NT * a.MT * a.KS)), block(64 * WN * WM);
+  const dim3 grid((unsigned)(a.NT * a.MT), (unsigned)a.KS), block(64 * WN * WM);
   if (ykind == YK_F32) hipLaunchKernelGGL((mx_gemm4<WN, WM, JN, IM, YK_F32>), grid, block, 0, s, a);
   else hipLaunchKernelGGL((mx_gemm4<WN, WM, JN, IM, YK_BF16>), grid, block, 0, s, a);
+  if (a.KS > 1) launch_reduce<WN, WM, JN, IM>(a, ykind, s);
 }
-template <int WN, int WM, int JN, int IM>
+template <int WN, int WM, int JN, int IM, int RING>
 void launch_tile16(const MxArgs& a, int ykind, hipStream_t s) {
-  const dim3 grid((unsigned)(a.NT * a.MT * a.KS)), block(64 * WN * WM);
-  if (ykind == YK_F32) hipLaunchKernelGGL((mx_gemm16<WN, WM, JN, IM, YK_F32>), grid, block, 0, s, a);
-  else hipLaunchKernelGGL((mx_gemm16<WN, WM, JN, IM, YK_BF16>), grid, block, 0, s, a);
+  const dim3 grid((unsigned)(a.NT * a.MT), (unsigned)a.KS), block(64 * WN * WM);
+  if (ykind == YK_F32) hipLaunchKernelGGL((mx_gemm16<WN, WM, JN, IM, RING, YK_F32>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((mx_gemm16<WN, WM, JN, IM, RING, YK_BF16>), grid, block, 0, s, a);
+  if (a.KS > 1) launch_reduce<WN, WM, JN, IM>(a, ykind, s);
 }
 
 }  // namespace
@@ -712,14 +817,14 @@ hipError_t launch_gemm_mxfp4(const MxGemmArgs& g, hipStream_t s) {
     a.part = (float*)((uint8_t*)g.ws + kCounterBytes);
   }
   if (p.small) {
-    if (g.x4) a.NB >= kPairBlocks ? launch_small<true, 2>(a, g.ykind, s) : launch_small<true, 1>(a, g.ykind, s);
-    else a.NB >= kPairBlocks ? launch_small<false, 2>(a, g.ykind, s) : launch_small<false, 1>(a, g.ykind, s);
+    if (g.x4) launch_small<true>(a, p.W, g.ykind, s);
+    else launch_small<false>(a, p.W, g.ykind, s);
   } else if (g.x4) {
     if (p.big) launch_tile4<4, 2, 4, 8>(a, g.ykind, s);
     else launch_tile4<2, 2, 4, 4>(a, g.ykind, s);
   } else {
-    if (p.big) launch_tile16<4, 2, 4, 4>(a, g.ykind, s);
-    else launch_tile16<4, 1, 2, 4>(a, g.ykind, s);
+    if (p.big) launch_tile16<4, 2, 4, 4, 2>(a, g.ykind, s);
+    else launch_tile16<4, 2, 2, 2, 4>(a, g.ykind, s);
   }
   return hipGetLastError();
 }
