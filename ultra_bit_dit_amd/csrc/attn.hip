@@ -610,17 +610,16 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
 
 // ------------------------------------------------------------- many rows
 // One workgroup per (sequence, key head, 16 NC WAVES rows).  A step's keys and
-// values (64 tokens) are widened to bf16 once for all waves, while the
-// previous step is multiplied, and lie in LDS as whole MFMA operands: 1 KiB
-// per 16 rows x 32 k, lane (i, g)'s 16 bytes at place 4 i + (g + i / 4) % 4,
-// which spreads both the writes (neighbouring lanes: one row, all g) and the
-// reads (neighbouring lanes: one g, all rows) over the banks.
+// values (64 tokens) are widened to bf16 once for all waves and lie in LDS as
+// whole MFMA operands, 1 KiB per 16 rows x 32 k in the order of the lanes:
+// writes and reads without bank conflicts.
 template <int D, int NC, int WAVES>
-__global__ __launch_bounds__(64 * WAVES) void attn_prompt(AttnArgs a) {
-  constexpr int DS = D / 32, DT = D / 16, KP = D / (16 * WAVES);
-  static_assert(KP * 16 * WAVES == D, "whole 16-byte pieces per thread");
-  constexpr int KB = 4 * DS * 1024, VB = DT * 2048;
-  __shared__ __attribute__((aligned(16))) uint8_t kv_[2][KB + VB];
+__global__ __launch_bounds__(64 * WAVES, 2) void attn_prompt(AttnArgs a) {
+  constexpr int DS = D / 32, DT = D / 16, HALF = 32 * WAVES, SP = 4 * D / HALF;
+  static_assert(SP * HALF == 4 * D, "whole 16-byte pieces per thread");
+  __shared__ __attribute__((aligned(16))) uint8_t k_[2][4 * DS * 1024], v_[2][DT * 2048];
+  __shared__ int nan_at_[4];  // steps whose values hold NaN codes that were put aside
+  const bool keys = __builtin_amdgcn_readfirstlane((int)threadIdx.x) < HALF;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n = lane & 15, g = lane >> 4;
   // heads run fastest, so that an XCD (bid % 8) keeps few of them in its L2;
@@ -689,219 +688,234 @@ __global__ __launch_bounds__(64 * WAVES) void attn_prompt(AttnArgs a) {
 
   const int u0 = lo_min / kUnit, u1 = (hi_max + kUnit - 1) / kUnit;
   const int32_t* table = a.kv.table + b * a.kv.width;
-  // page of 16 tokens: lanes with lane % 4 = x hold that of tokens 64 u + 16 x ..
+  // Page of the 16 tokens that the lane stages from: tokens 64 u + 16 x .. with
+  // x = row / 4 of the keys' operand, x = group of the values'.
+  const int stage_group = keys ? (lane >> 2) & 3 : g;
   auto pages = [&](int u) -> int {
-    const int t = u * kUnit + 16 * (lane & 3);
+    const int t = u * kUnit + 16 * stage_group;
     if (t >= hi_max) return -1;
     const int pg = table[t >> a.kv.lp];
     return pg >= 0 && pg < a.kv.n_pages ? pg : -2;
   };
-  // This thread's pieces of a step.  Keys: 16 dims of a token; values: 16
-  // tokens of a dim.  A wave's keys lie in one group of 16 tokens.
-  mx_u4 kr[KP], vr[KP];
-  uint32_t kb[KP], vb;
-  int vpage;
-  constexpr int kTokenPieces = D / 16;
+  // This thread's 16-byte pieces of a step: of the keys for the first half of
+  // the waves (wave t: the rows of tile t, piece i: dims 64 i + 16 g ..), of the
+  // values for the second (16 tokens of dim 16 (t + 4 i) + n).  A wave's piece
+  // makes two whole operands, lane by lane.
+  mx_u4 raw[SP];
+  uint32_t eb = 0;
   const int sh = a.kv.lp + (D == 64 ? 6 : D == 128 ? 7 : 8);  // log2 of a page's bytes of one head
-  const int tok0 = tid / kTokenPieces, dim0 = (tid % kTokenPieces) * 16;
-  const uint32_t vat = (uint32_t)(tid >> 2) * P + ((16 * (tid & 3)) & (P - 1));
+  const int w4 = wave & (WAVES / 2 - 1);
+  // row 4 g' + j of tile t is token 16 g' + 4 t + j
+  const int tok = 16 * stage_group + 4 * w4 + (lane & 3);
+  const uint32_t kat = (uint32_t)((tok & (P - 1)) * D + 16 * g);
+  const uint32_t vat = (uint32_t)((16 * w4 + n) * P + ((16 * g) & (P - 1)));
   auto fetch = [&](int u, int pg) {
-    const int in = (u * kUnit) & (P - 1);  // the step's place in a larger page
-#pragma unroll
-    for (int i = 0; i < KP; i++) {
-      const int tok = tok0 + (64 * WAVES / kTokenPieces) * i;
-      const int grp = __builtin_amdgcn_readfirstlane(tok >> 4);
-      const int pk = __builtin_amdgcn_readlane(pg, grp);
-      const int64_t ph = (int64_t)(pk < 0 ? 0 : pk) * a.kv.H + h;
-      const uint8_t* kp = a.kv.kc + (ph << sh) + in * D;
-      kr[i] = *(const mx_u4*)(kp + (uint32_t)((tok & (P - 1)) * D + dim0));
-      kb[i] = a.kv.ks[ph];
-    }
-    vpage = pg;  // tid % 4 = lane % 4
+    const uint32_t in = (u * kUnit) & (P - 1);  // the step's place in a larger page
     const int64_t ph = (int64_t)(pg < 0 ? 0 : pg) * a.kv.H + h;
-    const uint8_t* vp = a.kv.vc + (ph << sh) + in + vat;
-    vb = a.kv.vs[ph];
+    if (keys) {
+      const uint8_t* kp = a.kv.kc + (ph << sh) + (kat + in * D);
+      eb = a.kv.ks[ph];
 #pragma unroll
-    for (int i = 0; i < KP; i++) vr[i] = *(const mx_u4*)(vp + (uint32_t)(16 * WAVES * i * P));
-  };
-  // widened and written to a buffer; whether NaN codes were put aside
-  auto stage = [&](int u, uint8_t* buf, bool part) -> bool {
-    bool nans = false;
+      for (int i = 0; i < SP; i++) raw[i] = *(const mx_u4*)(kp + 64 * i);
+    } else {
+      const uint8_t* vp = a.kv.vc + (ph << sh) + (vat + in);
+      eb = a.kv.vs[ph];
 #pragma unroll
-    for (int i = 0; i < KP; i++) {
-      const int x = tid + 64 * WAVES * i, tok = x / (D / 16), c16 = x % (D / 16);
-      // token 16 g' + 4 t + j is row 4 g' + j of tile t; dims 16 c16 ..: operands 2 (c16 / 4) + half, group c16 % 4
-      const int t = (tok & 15) >> 2, row = 4 * (tok >> 4) + (tok & 3), gg = c16 & 3;
-      uint8_t* w = buf + ((t * DS + 2 * (c16 >> 2)) * 64 + 4 * row + ((gg + (row >> 2)) & 3)) * 16;
-      const float sc = pow2_byte(kb[i]);
-      *(v8bf*)w = bf16x8_of_e4m3(kr[i].x, kr[i].y, sc);
-      *(v8bf*)(w + 1024) = bf16x8_of_e4m3(kr[i].z, kr[i].w, sc);
+      for (int i = 0; i < SP; i++) raw[i] = *(const mx_u4*)(vp + (uint32_t)(64 * i * P));
     }
-    const float sc = pow2_byte(vb);
-    const int gg = tid & 3, T = u * kUnit + 16 * gg;
-    uint32_t keep[4];
-    if (part) {
-      const int lo = vpage < 0 ? 16 : lo_min - T, hi = hi_max - T;
-#pragma unroll
-      for (int e = 0; e < 4; e++) keep[e] = byte_range(lo - 4 * e, hi - 4 * e);
-    }
-#pragma unroll
-    for (int i = 0; i < KP; i++) {
-      const int d = (tid >> 2) + 16 * WAVES * i, row = d & 15;
-      if (part) {
-        // codes of tokens no row sees become 0; NaN codes too, and are put
-        // back behind the products for the rows that see them
-#pragma unroll
-        for (int e = 0; e < 4; e++) {
-          vr[i][e] &= keep[e];
-          const uint32_t nb = nan_bytes(vr[i][e]);
-          nans |= nb != 0;
-          vr[i][e] &= ~((nb >> 7) * 0xFFu);
-        }
-      }
-      uint8_t* w = buf + KB + ((d >> 4) * 128 + 4 * row + ((gg + (row >> 2)) & 3)) * 16;
-      *(v8bf*)w = bf16x8_of_e4m3(vr[i].x, vr[i].y, vpage < 0 ? 0.f : sc);
-      *(v8bf*)(w + 1024) = bf16x8_of_e4m3(vr[i].z, vr[i].w, vpage < 0 ? 0.f : sc);
-    }
-    return nans;
   };
   // tokens some row of the workgroup does not see, or that cannot be read
   auto partial = [&](int u, int pg) { return u * kUnit + kUnit > hi_all || u * kUnit < lo_all || __any(pg < 0); };
-  auto count_bad = [&](int pg) {
-    if (pg == -2 && wave == 0 && lane < 4 && a.kv.bad) atomicAdd(a.kv.bad, 1);
+  // widened and written to the step's buffer
+  auto stage = [&](int u, int pg) {
+    if (keys) {
+      const float sc = pow2_byte(eb);
+      uint8_t* w = k_[(u - u0) & 1] + w4 * DS * 1024 + 16 * lane;
+#pragma unroll
+      for (int i = 0; i < SP; i++) {
+        *(v8bf*)(w + 2 * i * 1024) = bf16x8_of_e4m3(raw[i].x, raw[i].y, sc);
+        *(v8bf*)(w + (2 * i + 1) * 1024) = bf16x8_of_e4m3(raw[i].z, raw[i].w, sc);
+      }
+    } else {
+      const bool part = partial(u, pg);
+      const float sc = pg < 0 ? 0.f : pow2_byte(eb);
+      if (part) {
+        // codes of tokens no row sees become 0; NaN codes too, and are put
+        // back beside the products for the rows that see them
+        const int T = u * kUnit + 16 * g, lo = pg < 0 ? 16 : lo_min - T, hi = hi_max - T;
+        uint32_t nans = 0;
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+          const uint32_t keep = byte_range(lo - 4 * e, hi - 4 * e);
+#pragma unroll
+          for (int i = 0; i < SP; i++) {
+            raw[i][e] &= keep;
+            const uint32_t nb = nan_bytes(raw[i][e]);
+            nans |= nb;
+            raw[i][e] &= ~((nb >> 7) * 0xFFu);
+          }
+        }
+        if (nans) nan_at_[u & 3] = u;
+        if (pg == -2 && w4 == 0 && n == 0 && a.kv.bad) atomicAdd(a.kv.bad, 1);
+      }
+      uint8_t* w = v_[(u - u0) & 1] + w4 * 2048 + 16 * lane;
+#pragma unroll
+      for (int i = 0; i < SP; i++) {
+        *(v8bf*)(w + i * 8192) = bf16x8_of_e4m3(raw[i].x, raw[i].y, sc);
+        *(v8bf*)(w + i * 8192 + 1024) = bf16x8_of_e4m3(raw[i].z, raw[i].w, sc);
+      }
+    }
+  };
+  auto meet = [&]() {  // LDS reads and writes are done; loads stay in flight
+    __asm__ volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    __asm__ volatile("" ::: "memory");
   };
 
+  const int at = 16 * lane;
+  v4f sc[NC][4];
+  v8bf pf[NC][2];
+  auto sees = [&](int u) { return u * kUnit < whi && u * kUnit + kUnit > wlo; };
+  // scores of step u
+  auto scores = [&](int u) {
+    const uint8_t* buf = k_[(u - u0) & 1];
+    v8bf kf[2][DS];  // two tiles, so that four chains of products alternate
+#pragma unroll
+    for (int t = 0; t < 4; t += 2) {
+#pragma unroll
+      for (int d = 0; d < DS; d++)
+#pragma unroll
+        for (int e = 0; e < 2; e++) kf[e][d] = *(const v8bf*)(buf + ((t + e) * DS + d) * 1024 + at);
+#pragma unroll
+      for (int e = 0; e < 2; e++)
+#pragma unroll
+        for (int c = 0; c < NC; c++) sc[c][t + e] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int d = 0; d < DS; d++)
+#pragma unroll
+        for (int e = 0; e < 2; e++)
+#pragma unroll
+          for (int c = 0; c < NC; c++) sc[c][t + e] = mfma(kf[e][d], qf[c][d], sc[c][t + e]);
+    }
+  };
+  // O += P V of step u
+  auto weigh = [&](int u) {
+    const uint8_t* buf = v_[(u - u0) & 1];
+    if (nan_at_[u & 3] == u) {
+      // rare: a NaN code among tokens that not every row of the workgroup sees
+      const int T = u * kUnit, vp = __shfl(pages(u), keys ? 4 * g : lane);
+      const uint8_t* vc = a.kv.vc + (((int64_t)(vp < 0 ? 0 : vp) * a.kv.H + h) << sh) + ((T + 16 * g) & (P - 1));
+#pragma unroll 1
+      for (int d = 0; d < DT; d++) {
+        const mx_u4 w = *(const mx_u4*)(vc + (int64_t)(16 * d + n) * P);
+        v8bf isn[2];
+#pragma unroll
+        for (int e = 0; e < 16; e++)
+          isn[e >> 3][e & 7] = (__bf16)(vp >= 0 && ((nan_bytes(w[e >> 2]) >> (8 * (e & 3) + 7)) & 1u) ? 1.f : 0.f);
+#pragma unroll
+        for (int c = 0; c < NC; c++) {
+          v8bf vis[2];
+#pragma unroll
+          for (int e = 0; e < 16; e++) {
+            const int tok = T + 16 * g + e;
+            vis[e >> 3][e & 7] = (__bf16)(tok >= vlo[c] && tok < vhi[c] ? 1.f : 0.f);
+          }
+          v4f hit = v4f{0.f, 0.f, 0.f, 0.f};
+          hit = mfma(isn[0], vis[0], hit);
+          hit = mfma(isn[1], vis[1], hit);
+#pragma unroll
+          for (int e = 0; e < 4; e++) nanned[c] |= hit[e] > 0.f ? uint64_t(1) << (4 * d + e) : 0;
+        }
+      }
+    }
+    v8bf vf[2][4];
+    auto read_v = [&](int d) {  // two tiles of 16 dims
+#pragma unroll
+      for (int e = 0; e < 4; e++) vf[(d >> 1) & 1][e] = *(const v8bf*)(buf + d * 2048 + e * 1024 + at);
+    };
+    read_v(0);
+#pragma unroll
+    for (int d = 0; d < DT; d += 2) {
+      if (d + 2 < DT) read_v(d + 2);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int f = 0; f < 2; f++)
+#pragma unroll
+        for (int e = f; e < 4; e += 2)
+#pragma unroll
+          for (int c = 0; c < NC; c++) o[c][d + (e >> 1)] = mfma(vf[(d >> 1) & 1][e], pf[c][f], o[c][d + (e >> 1)]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  // weights of step u from its scores
+  auto softmax = [&](int u, int pg) {
+    const int T = u * kUnit;
+    const bool mask = T + kUnit > whi_all || T < wlo_all || __any(pg < 0);
+    const int page = mask ? __shfl(pg, keys ? 4 * g : lane) : 0;  // of the lane's 16 tokens
+#pragma unroll
+    for (int c = 0; c < NC; c++) {
+      if (mask) {
+        const int lo = page < 0 ? 16 : vlo[c] - (T + 16 * g), hi = vhi[c] - (T + 16 * g);
+        const uint32_t up = hi >= 16 ? 0xFFFFu : hi <= 0 ? 0u : (1u << hi) - 1u;
+        const uint32_t seen = lo >= 16 ? 0u : lo <= 0 ? up : up & ~((1u << lo) - 1u);
+#pragma unroll
+        for (int e = 0; e < 16; e++) sc[c][e >> 2][e & 3] = (seen >> e) & 1u ? sc[c][e >> 2][e & 3] : -INFINITY;
+      }
+      float mx = -INFINITY;
+#pragma unroll
+      for (int e = 0; e < 16; e++) mx = fmaxf(mx, sc[c][e >> 2][e & 3]);
+      mx = group_max(mx) * scale;
+      // The maximum in use may lag by up to 2^8 (weights up to 256 lose no
+      // precision), so O is rescaled in few of the steps.
+      if (__any(mx > m[c] + 8.f)) {
+        const float mn = fmaxf(m[c], mx), mu = mn == -INFINITY ? 0.f : mn;
+        const float al = __builtin_amdgcn_exp2f(m[c] - mu);  // first tokens: 2^-inf = 0
+        m[c] = mn;
+        l[c] *= al;
+#pragma unroll
+        for (int d = 0; d < DT; d++)
+#pragma unroll
+          for (int e = 0; e < 4; e++) o[c][d][e] *= al;
+      }
+      const float mu = m[c] == -INFINITY ? 0.f : m[c];
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int e = 0; e < 16; e++) {
+        const float p = __builtin_amdgcn_exp2f(fmaf(sc[c][e >> 2][e & 3], scale, -mu));  // masked: 2^-inf = 0
+        sum[e & 3] += p;
+        pf[c][e >> 3][e & 7] = (__bf16)p;
+      }
+      l[c] += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+    }
+  };
+
+  // Two phases a step: products (scores of step u, weighted values of u - 1),
+  // then softmax and staging.  The second half of the waves runs one phase
+  // behind the first, so that on every SIMD one wave multiplies while another
+  // computes weights.  The first half stages the keys of u + 1, read from its
+  // next phase on; the second the values of u + 1, read two steps on; either
+  // buffer's last reader is a phase before.
+  if (tid < 4) nan_at_[tid] = -1;
+  __syncthreads();
   int pg0 = u0 < u1 ? pages(u0) : -1, pg1 = u0 + 1 < u1 ? pages(u0 + 1) : -1;
-  bool part = false, nan_now = false;
   if (u0 < u1) {
     fetch(u0, pg0);
-    part = partial(u0, pg0);
-    const bool nn = stage(u0, kv_[0], part);
-    if (part) nan_now = __syncthreads_or(nn);
-    else __syncthreads();
+    stage(u0, pg0);
   }
-  for (int u = u0; u < u1; u++) {
-    const uint8_t* buf = kv_[(u - u0) & 1];
+  meet();
+  if (!keys) meet();
+  for (int u = u0; u <= u1; u++) {
     const bool more = u + 1 < u1;
     const int pg2 = u + 2 < u1 ? pages(u + 2) : -1;
     if (more) fetch(u + 1, pg1);
-    const int T = u * kUnit;
-    if (T < whi && T + kUnit > wlo) {
-      const int at = (4 * n + ((g + (n >> 2)) & 3)) * 16;
-      v4f sc[NC][4];
-      // operands are read one tile ahead of their products
-      v8bf kf[2][DS], vf[2][4];
-      auto read_k = [&](int t) {
-#pragma unroll
-        for (int d = 0; d < DS; d++) kf[t & 1][d] = *(const v8bf*)(buf + (t * DS + d) * 1024 + at);
-      };
-      auto read_v = [&](int d) {  // two tiles of 16 dims
-#pragma unroll
-        for (int e = 0; e < 4; e++) vf[(d >> 1) & 1][e] = *(const v8bf*)(buf + KB + d * 2048 + e * 1024 + at);
-      };
-      read_k(0);
-#pragma unroll
-      for (int t = 0; t < 4; t++) {
-        if (t < 3) read_k(t + 1);
-        else read_v(0);
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int c = 0; c < NC; c++) sc[c][t] = v4f{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int d = 0; d < DS; d++)
-#pragma unroll
-          for (int c = 0; c < NC; c++) sc[c][t] = mfma(kf[t & 1][d], qf[c][d], sc[c][t]);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      const bool mask = T + kUnit > whi_all || T < wlo_all || (part && __any(pg0 < 0));
-      const int page = mask ? __shfl(pg0, g) : 0;  // of the lane's 16 tokens
-      v8bf pf[NC][2];
-#pragma unroll
-      for (int c = 0; c < NC; c++) {
-        uint32_t seen = 0xFFFFu;
-        if (mask) {
-          const int lo = page < 0 ? 16 : vlo[c] - (T + 16 * g), hi = vhi[c] - (T + 16 * g);
-          const uint32_t up = hi >= 16 ? 0xFFFFu : hi <= 0 ? 0u : (1u << hi) - 1u;
-          seen = lo >= 16 ? 0u : lo <= 0 ? up : up & ~((1u << lo) - 1u);
-#pragma unroll
-          for (int e = 0; e < 16; e++) sc[c][e >> 2][e & 3] = (seen >> e) & 1u ? sc[c][e >> 2][e & 3] : -INFINITY;
-        }
-        float mx = -INFINITY;
-#pragma unroll
-        for (int e = 0; e < 16; e++) mx = fmaxf(mx, sc[c][e >> 2][e & 3]);
-        mx = group_max(mx) * scale;
-        // The maximum in use may lag by up to 2^8 (weights up to 256 lose no
-        // precision), so O is rescaled in few of the steps.
-        if (__any(mx > m[c] + 8.f)) {
-          const float mn = fmaxf(m[c], mx), mu = mn == -INFINITY ? 0.f : mn;
-          const float al = __builtin_amdgcn_exp2f(m[c] - mu);  // first tokens: 2^-inf = 0
-          m[c] = mn;
-          l[c] *= al;
-#pragma unroll
-          for (int d = 0; d < DT; d++)
-#pragma unroll
-            for (int e = 0; e < 4; e++) o[c][d][e] *= al;
-        }
-        const float mu = m[c] == -INFINITY ? 0.f : m[c];
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int e = 0; e < 16; e++) {
-          const float p = __builtin_amdgcn_exp2f(fmaf(sc[c][e >> 2][e & 3], scale, -mu));  // masked: 2^-inf = 0
-          sum[e & 3] += p;
-          pf[c][e >> 3][e & 7] = (__bf16)p;
-        }
-        l[c] += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-      }
-      if (nan_now) {
-        // rare: a NaN code among tokens that not every row of the workgroup sees
-        const int vp = __shfl(pg0, g);
-        const uint8_t* vc = a.kv.vc + (((int64_t)(vp < 0 ? 0 : vp) * a.kv.H + h) << sh) + ((T + 16 * g) & (P - 1));
-#pragma unroll 1
-        for (int d = 0; d < DT; d++) {
-          const mx_u4 w = *(const mx_u4*)(vc + (int64_t)(16 * d + n) * P);
-          v8bf isn[2];
-#pragma unroll
-          for (int e = 0; e < 16; e++)
-            isn[e >> 3][e & 7] = (__bf16)(vp >= 0 && ((nan_bytes(w[e >> 2]) >> (8 * (e & 3) + 7)) & 1u) ? 1.f : 0.f);
-#pragma unroll
-          for (int c = 0; c < NC; c++) {
-            v8bf vis[2];
-#pragma unroll
-            for (int e = 0; e < 16; e++) {
-              const int tok = T + 16 * g + e;
-              vis[e >> 3][e & 7] = (__bf16)(tok >= vlo[c] && tok < vhi[c] ? 1.f : 0.f);
-            }
-            v4f hit = v4f{0.f, 0.f, 0.f, 0.f};
-            hit = mfma(isn[0], vis[0], hit);
-            hit = mfma(isn[1], vis[1], hit);
-#pragma unroll
-            for (int e = 0; e < 4; e++) nanned[c] |= hit[e] > 0.f ? uint64_t(1) << (4 * d + e) : 0;
-          }
-        }
-      }
-#pragma unroll
-      for (int d = 0; d < DT; d += 2) {
-        if (d + 2 < DT) read_v(d + 2);
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int e = 0; e < 4; e++)
-#pragma unroll
-          for (int c = 0; c < NC; c++) o[c][d + (e >> 1)] = mfma(vf[(d >> 1) & 1][e], pf[c][e & 1], o[c][d + (e >> 1)]);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-    }
-    if (part) count_bad(pg0);
+    if (u < u1 && sees(u)) scores(u);
+    if (u > u0 && sees(u - 1)) weigh(u - 1);
+    meet();
+    if (u < u1 && sees(u)) softmax(u, pg0);
+    if (more) stage(u + 1, pg1);
     pg0 = pg1;
     pg1 = pg2;
-    if (more) {
-      part = partial(u + 1, pg0);
-      const bool nn = stage(u + 1, kv_[(u + 1 - u0) & 1], part);
-      if (part) nan_now = __syncthreads_or(nn);
-      else {
-        nan_now = false;
-        __syncthreads();
-      }
-    }
+    if (keys || u < u1) meet();
   }
 #pragma unroll
   for (int c = 0; c < NC; c++) {
@@ -932,7 +946,28 @@ struct Plan {
 };
 
 constexpr int64_t kPromptRows = 128;
-constexpr int prompt_rows(int D) { return D == 256 ? 128 : 256; }
+#ifndef T64
+#define T64 512
+#endif
+#ifndef T128
+#define T128 512
+#endif
+#ifndef T256
+#define T256 512
+#endif
+#ifndef V64
+#define V64 64, 2, 8
+#define R64 256
+#endif
+#ifndef V128
+#define V128 128, 2, 8
+#define R128 256
+#endif
+#ifndef V256
+#define V256 256, 1, 8
+#define R256 128
+#endif
+constexpr int prompt_rows(int D) { return D == 64 ? R64 : D == 128 ? R128 : R256; }
 
 Plan plan_attention(int D, int H, int64_t n_seqs, int64_t total_q, int64_t max_q, int64_t G) {
   Plan p;
@@ -968,9 +1003,9 @@ hipError_t launch_attention(AttnArgs a, void* ws, hipStream_t s) {
   a.part = (float*)((uint8_t*)ws + kCounterBytes);
   const dim3 grid((unsigned)p.blocks);
   if (p.nc == 0) {
-    if (a.kv.D == 64) hipLaunchKernelGGL((attn_prompt<64, 4, 4>), grid, dim3(256), 0, s, a);
-    else if (a.kv.D == 128) hipLaunchKernelGGL((attn_prompt<128, 2, 8>), grid, dim3(512), 0, s, a);
-    else hipLaunchKernelGGL((attn_prompt<256, 2, 4>), grid, dim3(256), 0, s, a);
+    if (a.kv.D == 64) hipLaunchKernelGGL((attn_prompt<V64>), grid, dim3(T64), 0, s, a);
+    else if (a.kv.D == 128) hipLaunchKernelGGL((attn_prompt<V128>), grid, dim3(T128), 0, s, a);
+    else hipLaunchKernelGGL((attn_prompt<V256>), grid, dim3(T256), 0, s, a);
     return hipGetLastError();
   }
 #define LOWBIT_DEC(DD, NN) \
