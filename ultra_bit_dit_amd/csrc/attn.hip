@@ -64,6 +64,13 @@ __device__ __forceinline__ uint32_t byte_range(int lo, int hi) {
   return up & ~((1u << (8 * lo)) - 1u);  // lo < 4 here
 }
 
+// a / b, a >= 0, b > 0: numbers are small but for the longest batches, and a
+// 64-bit division takes some 150 instructions
+__device__ __forceinline__ int64_t quot(int64_t a, int64_t b) {
+  if (__builtin_expect((((uint64_t)a | (uint64_t)b) >> 32) == 0, 1)) return (uint32_t)a / (uint32_t)b;
+  return a / b;
+}
+
 // Work items numbered in the order of the sequences, sequence b having
 // count(b) of them: each thread sums a run of sequences, one scan joins them.
 // Workgroups are numbered over the work that exists (the host only knows
@@ -75,30 +82,44 @@ struct ItemScan {
   int64_t n_seqs, per, first, mine, total;  // this thread's run: its first item and their number
   int64_t* lds;                             // [THREADS / 64 + 2]
 
+  // a batch of at most 64: every wave by itself, sequence b in lane b
+  __device__ __forceinline__ bool few() const { return n_seqs <= 64; }
+
   __device__ __forceinline__ ItemScan(int64_t n, Count c, int64_t* mem) : count(c), n_seqs(n), lds(mem) {
-    const int tid = threadIdx.x, lane = tid & 63;
-    per = (n_seqs + THREADS - 1) / THREADS;
+    const int tid = threadIdx.x, lane = tid & 63, run = few() ? lane : tid;
+    per = few() ? 1 : (n_seqs + THREADS - 1) / THREADS;
     mine = 0;
-    for (int64_t b = tid * per; b < min(n_seqs, (tid + 1) * per); b++) mine += count(b);
+    for (int64_t b = run * per; b < min(n_seqs, (run + 1) * per); b++) mine += count(b);
     int64_t sum = mine;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
+      if (few() && d >= n_seqs) break;
       const int64_t v = __shfl_up((long long)sum, d);
       sum += lane >= d ? v : 0;
     }
-    if (lane == 63) lds[tid >> 6] = sum;
-    __syncthreads();
     int64_t before = 0;
-    total = 0;
+    if (few()) {
+      total = uniform64(__shfl((long long)sum, (int)n_seqs - 1));
+    } else {
+      if (lane == 63) lds[tid >> 6] = sum;
+      __syncthreads();
+      total = 0;
 #pragma unroll
-    for (int w = 0; w < THREADS / 64; w++) {
-      before += w < (tid >> 6) ? lds[w] : 0;
-      total += lds[w];
+      for (int w = 0; w < THREADS / 64; w++) {
+        before += w < (tid >> 6) ? lds[w] : 0;
+        total += lds[w];
+      }
     }
     first = before + sum - mine;
   }
   // sequence and item in it of index k < total (the whole workgroup calls it)
   __device__ __forceinline__ void find(int64_t k, int64_t* b, int64_t* item) {
+    if (few()) {
+      const int at = __builtin_ctzll(__ballot(k >= first && k < first + mine));
+      *b = at;
+      *item = k - uniform64(__shfl((long long)first, at));
+      return;
+    }
     if (k >= first && k < first + mine) {
       int64_t i = threadIdx.x * per, left = k - first;
       for (;; i++) {
@@ -117,11 +138,14 @@ struct ItemScan {
 };
 
 // Few rows.  A tile is 16 NC rows of one sequence and key head, its work the
-// 64-token steps any of them sees.  A fixed number of workgroups take equal,
-// contiguous shares of all steps of all tiles; a workgroup's waves take the
-// steps of a tile in turn, and every wave reads the codes it needs straight
-// from the cache into registers.  A tile that lies in several shares is joined
-// by the workgroup that ends last.
+// blocks of 256 tokens (a step of 64 for each of the four waves) that any of
+// them sees.  A fixed number of workgroups take equal, contiguous shares of all
+// blocks of all tiles, or one block each where there are no more blocks; every
+// wave reads the codes it needs straight from the cache into registers.  A tile
+// that lies in several shares is joined by the workgroup that ends last.
+// (Shares of single steps, which often had the end of one tile and the start of
+// the next: 4 x 4 tokens in contexts of 777 23.1 us, with blocks 14.0 us; one
+// token in 16000, D = 256, 28.1 and 23.4 us.)
 constexpr int kJoinLoads = 8;   // results of a pair of outputs read at once
 constexpr int kMaxJoin = 32;    // results joined by one workgroup: shares of a tile <= kMaxJoin^2
 constexpr int kMaxShares = 512;
@@ -139,6 +163,7 @@ __device__ __forceinline__ float2 get2(const float* p) {
 // Four waves, so that two workgroups share a compute unit where a wave fits
 // 256 registers and one starts or ends while the other reads.
 constexpr int kDecWaves = 4;
+constexpr int kBlock = kUnit * kDecWaves;  // tokens of a block: a step of every wave
 
 template <int D, int NC>
 __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_decode(AttnArgs a) {
@@ -150,43 +175,42 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 15, g = lane >> 4;
   const int P = 1 << a.kv.lp;
-  // steps of one tile of a sequence (at least one, which writes its rows), and its tiles
-  auto steps_of = [&](const SeqSpan& t) -> int64_t {
+  // blocks of one tile of a sequence (at least one, which writes its rows), and its tiles
+  auto blocks_of = [&](const SeqSpan& t) -> int64_t {
     int64_t most = t.len;
     if (a.window > 0 && a.causal) most = min(most, (int64_t)a.window + t.n + kUnit);
-    return max((most + kUnit - 1) / kUnit, (int64_t)1);
+    return max((most + kBlock - 1) / kBlock, (int64_t)1);
   };
   auto tiles_of = [&](const SeqSpan& t) -> int64_t { return (t.n * a.G + 16 * NC - 1) / (16 * NC); };
   auto work_of = [&](int64_t i) -> int64_t {
     const SeqSpan t = seq_span(a.kv, i);
-    return tiles_of(t) * steps_of(t);
+    return tiles_of(t) * blocks_of(t);
   };
   ItemScan<64 * kDecWaves, decltype(work_of)> scan(a.kv.n_seqs, work_of, scan_);
   const int64_t per_head = scan.total, total = per_head * a.kv.H;
-  // Shares: one for each four steps (one a wave), as many as tiles if that is
-  // more, at most the launch's workgroups.
-  const int64_t want = max(total / kDecWaves, min(total, a.tiles));
-  const int64_t shares = max(min(want, (int64_t)gridDim.x), (int64_t)1);
+  // Shares: one for each block while there are workgroups for that, so that none
+  // has parts of two tiles, which it would have to begin and join in turn
+  const int64_t shares = max(min(total, (int64_t)gridDim.x), (int64_t)1);
   // neighbouring shares on one XCD (bid % 8) where every workgroup has one
   const int64_t per_xcd = gridDim.x / 8, bid = blockIdx.x;
   const int64_t share = shares == (int64_t)gridDim.x ? (bid % 8) * per_xcd + bid / 8 : bid;
   if (share >= shares) return;
-  int64_t x = total * share / shares;
-  const int64_t x_end = total * (share + 1) / shares;
+  int64_t x = quot(total * share, shares);
+  const int64_t x_end = quot(total * (share + 1), shares);
   if (x >= x_end) return;
-  int h = (int)(x / per_head);
+  int h = (int)quot(x, per_head);
   int64_t b, item;
-  scan.find(x % per_head, &b, &item);
+  scan.find(x - h * per_head, &b, &item);
   SeqSpan s = seq_span(a.kv, b);
-  int64_t steps = steps_of(s), tiles = tiles_of(s);
-  int64_t rt = item / steps;
-  int at = (int)(item % steps);  // first step of this share in the tile
+  int64_t blocks = blocks_of(s), tiles = tiles_of(s);
+  int64_t rt = quot(item, blocks);
+  int at = (int)(item - rt * blocks);  // first block of this share in the tile
   for (;;) {
-  const int64_t x0 = x - at;     // the tile's first step among all
-  const int count = (int)min(steps - at, x_end - x);
-  // shares that hold steps of this tile
-  const int64_t share0 = ((x0 + 1) * shares + total - 1) / total - 1;
-  const int64_t share1 = ((x0 + steps) * shares + total - 1) / total - 1;
+  const int64_t x0 = x - at;     // the tile's first block among all
+  const int count = (int)min(blocks - at, x_end - x);
+  // shares that hold blocks of this tile
+  const int64_t share0 = quot((x0 + 1) * shares + total - 1, total) - 1;
+  const int64_t share1 = quot((x0 + blocks) * shares + total - 1, total) - 1;
   const int n_parts = (int)(share1 - share0 + 1);
   const int64_t R = (int64_t)s.n * a.G;
   const int64_t rho0 = rt * 16 * NC;
@@ -216,7 +240,7 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
     vhi[c] = a.causal ? min(len, p + 1) : len;
     vlo[c] = a.window > 0 ? max(0, p - a.window + 1) : 0;
   }
-  const int u0 = lo_min / kUnit + at, u1 = min(lo_min / kUnit + at + count, (hi_max + kUnit - 1) / kUnit);
+  const int u0 = lo_min / kUnit + kDecWaves * at, u1 = min(u0 + kDecWaves * count, (hi_max + kUnit - 1) / kUnit);
 
   // Q: lane (n, g) holds dims 64 c + 16 g + 8 e .. + 7 of its row
   v8bf qf[NC][DC][2];
@@ -603,7 +627,7 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
       s = seq_span(a.kv, b);
       tiles = tiles_of(s);
     } while (tiles == 0);  // some sequence has tiles, as x < total
-    steps = steps_of(s);
+    blocks = blocks_of(s);
   }
   }
 }
@@ -939,47 +963,400 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attn_prompt(AttnArgs a) {
   }
 }
 
+// The same for heads of 64 and 128 with 32 x 32 x 16 products: half the operand
+// reads for a product, one row a lane, and products and multiply-adds of two
+// waves of a SIMD overlap better (side by side they took 1 / 1.92 of their
+// times' sum, with 16 x 16 x 32 products 1 / 1.66).  Row 8 x + 4 h + j of a tile
+// of 32 tokens is token 16 h + 4 x + j, so that lane half h holds 16
+// consecutive tokens.  2 prompts of 4096 in 4096 tokens, 40 heads over 8, all
+// pairs: D = 128 801 -> 753 us; what bounds it is the clock that products of
+// such data leave (with the reads of LDS or the weights' exponentials taken out
+// it takes 97% of the time).  D = 64, causal: 342 us with 16 x 16 products, 315 us
+// with 8 waves, 266 us with 4 waves and three workgroups a compute unit (the
+// exponentials bound it, and more waves hide their latency).
+template <int D, int NC, int WAVES, int OCC>
+__global__ __launch_bounds__(64 * WAVES, OCC) void attn_prompt32(AttnArgs a) {
+  constexpr int DS = D / 16, DT = D / 32, HALF = 32 * WAVES, SP = 4 * D / HALF, PS = WAVES / 4;
+  static_assert(SP * HALF == 4 * D, "whole 16-byte pieces per thread");
+  constexpr int KB = 2 * DS * 1024, VB = 4 * DT * 1024;  // bytes of a step's operands
+  constexpr int OUT = 2 * D + 16;                        // a row of O on its way out, padded against bank conflicts
+  __shared__ __attribute__((aligned(16))) uint8_t lds_[2 * (KB + VB) > 32 * NC * WAVES * OUT ? 2 * (KB + VB) : 32 * NC * WAVES * OUT];
+  // steps whose values hold NaN codes that were put aside; that name pages that cannot be read
+  __shared__ int nan_at_[4], bad_at_[4];
+  const bool keys = __builtin_amdgcn_readfirstlane((int)threadIdx.x) < HALF;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int n = lane & 31, hf = lane >> 5;
+  constexpr int ROWS = 32 * NC * WAVES;
+  const uint32_t G = (uint32_t)a.G, H = (uint32_t)a.kv.H, tile_at = blockIdx.x / H;
+  const int h = (int)(blockIdx.x - tile_at * H);
+  int64_t b, item;
+  auto tiles = [&](int64_t i) -> int64_t { return (seq_span(a.kv, i).n * a.G + ROWS - 1) / ROWS; };
+  __shared__ int64_t scan_[WAVES + 2];
+  ItemScan<64 * WAVES, decltype(tiles)> scan(a.kv.n_seqs, tiles, scan_);
+  if (tile_at >= scan.total) return;
+  scan.find(tile_at, &b, &item);
+  const SeqSpan s = seq_span(a.kv, b);
+  // rows count to less than 2^31 (checked at the entry)
+  const int R = s.n * (int)G, wg0 = (R - 1) / ROWS * ROWS - (int)item * ROWS;
+  const int len = s.len, first = len - s.n, P = 1 << a.kv.lp;
+
+  // what rows [r0, r1) see between them: some of them [lo, hi), all of them [lo_all, hi_all)
+  auto range = [&](int r0, int r1, int* lo, int* hi, int* lo_all, int* hi_all) {
+    r0 = r0 < R - 1 ? r0 : R - 1;
+    r1 = r1 < R ? r1 : R;
+    const int p0 = first + (int)((uint32_t)r0 / G), p1 = first + (int)((uint32_t)(r1 - 1) / G);
+    *hi = a.causal ? max(0, min(len, p1 + 1)) : len;
+    *hi_all = a.causal ? max(0, min(len, p0 + 1)) : len;
+    *lo = a.window > 0 ? max(0, p0 - a.window + 1) : 0;
+    *lo_all = a.window > 0 ? max(0, p1 - a.window + 1) : 0;
+  };
+  int wlo, whi, wlo_all, whi_all, lo_min, hi_max, lo_all, hi_all;
+  const int rho0 = wg0 + wave * 32 * NC;
+  range(wg0, wg0 + ROWS, &lo_min, &hi_max, &lo_all, &hi_all);
+  range(rho0, rho0 + 32 * NC, &wlo, &whi, &wlo_all, &whi_all);
+  whi = __builtin_amdgcn_readfirstlane(rho0 < R ? whi : 0);
+  const bool none = fabsf(a.scale2) < 0x1p-126f;  // all scores 0
+  int rho[NC], vlo[NC], vhi[NC];
+  v8bf qf[NC][DS];
+#pragma unroll
+  for (int c = 0; c < NC; c++) {
+    rho[c] = rho0 + 32 * c + n;
+    const uint32_t rc = rho[c] < R ? rho[c] : R - 1, at = rc / G;
+    const int p = first + (int)at;
+    vhi[c] = a.causal ? min(len, p + 1) : len;
+    vlo[c] = a.window > 0 ? max(0, p - a.window + 1) : 0;
+    const uint16_t* qp = a.q + (s.row0 + at) * a.q_stride + ((int64_t)h * G + (rc - at * G)) * D + 8 * hf;
+#pragma unroll
+    for (int d = 0; d < DS; d++) qf[c][d] = __builtin_bit_cast(v8bf, *(const mx_u4*)(qp + 16 * d));  // dims 16 d + 8 h .. + 7
+  }
+  const float scale = none ? 1.f : fabsf(a.scale2);
+  v16f o[NC][DT];
+  float m[NC], l[NC];
+  uint64_t nanned[NC];  // bit 16 d + e: o[c][d][e] meets a NaN value
+#pragma unroll
+  for (int c = 0; c < NC; c++) {
+    m[c] = -INFINITY;
+    l[c] = 0.f;
+    nanned[c] = 0;
+#pragma unroll
+    for (int d = 0; d < DT; d++)
+#pragma unroll
+      for (int e = 0; e < 16; e++) o[c][d][e] = 0.f;
+  }
+
+  const int u0 = lo_min / kUnit, u1 = (hi_max + kUnit - 1) / kUnit;
+  const int32_t* table = a.kv.table + b * a.kv.width;
+  // This thread's 16-byte pieces of a step.  Keys (first half of the waves,
+  // tile w4 % 2): 16 dims 16 (2 (w4 / 2 + 2 i) + h) .. of the token of row n.
+  // Values (second half): 16 tokens of dim 32 (w4 / 2 + 2 i) + n, tokens
+  // 32 (w4 % 2) + 16 h ...  A piece of values is two operands lane by lane, of
+  // keys the two halves of one.
+  const int w4 = wave & (WAVES / 2 - 1), tile = w4 & 1;
+  const int stage_group = 2 * tile + (keys ? (lane >> 2) & 1 : hf);  // of 16 tokens
+  auto pages = [&](int u) -> int {
+    const int t = u * kUnit + 16 * stage_group;
+    if (t >= hi_max) return -1;
+    const int pg = table[t >> a.kv.lp];
+    return pg >= 0 && pg < a.kv.n_pages ? pg : -2;
+  };
+  mx_u4 raw[SP];
+  uint32_t eb = 0;
+  const int sh = a.kv.lp + (D == 64 ? 6 : 7);  // log2 of a page's bytes of one head
+  const int tok = 16 * stage_group + 4 * (n >> 3) + (n & 3);
+  const uint32_t kat = (uint32_t)((tok & (P - 1)) * D + 32 * (w4 >> 1) + 16 * hf);
+  const uint32_t vat = (uint32_t)((32 * (w4 >> 1) + n) * P + ((16 * stage_group) & (P - 1)));
+  auto fetch = [&](int u, int pg) {
+    const uint32_t in = (u * kUnit) & (P - 1);  // the step's place in a larger page
+    const int64_t ph = (int64_t)(pg < 0 ? 0 : pg) * a.kv.H + h;
+    if (keys) {
+      const uint8_t* kp = a.kv.kc + (ph << sh) + (kat + in * D);
+      eb = a.kv.ks[ph];
+#pragma unroll
+      for (int i = 0; i < SP; i++) raw[i] = *(const mx_u4*)(kp + 32 * PS * i);
+    } else {
+      const uint8_t* vp = a.kv.vc + (ph << sh) + (vat + in);
+      eb = a.kv.vs[ph];
+#pragma unroll
+      for (int i = 0; i < SP; i++) raw[i] = *(const mx_u4*)(vp + (uint32_t)(32 * PS * i * P));
+    }
+  };
+  // tokens some row of the workgroup does not see, or that cannot be read
+  auto partial = [&](int u, int pg) { return u * kUnit + kUnit > hi_all || u * kUnit < lo_all || __any(pg < 0); };
+  // widened and written to the step's buffer
+  auto stage = [&](int u, int pg) {
+    if (keys) {
+      const float sc = pow2_byte(eb);
+      // operand (tile, 16-dim block x): lane (n, half of the dims)
+      uint8_t* w = lds_ + ((u - u0) & 1) * KB + (tile * DS + 2 * (w4 >> 1) + hf) * 1024 + 16 * n;
+#pragma unroll
+      for (int i = 0; i < SP; i++) {
+        *(v8bf*)(w + 2 * PS * i * 1024) = bf16x8_of_e4m3(raw[i].x, raw[i].y, sc);
+        *(v8bf*)(w + 2 * PS * i * 1024 + 512) = bf16x8_of_e4m3(raw[i].z, raw[i].w, sc);
+      }
+    } else {
+      const bool part = partial(u, pg);
+      const float sc = pg < 0 ? 0.f : pow2_byte(eb);
+      if (part) {
+        // codes of tokens no row sees become 0; NaN codes too, and are put
+        // back beside the products for the rows that see them
+        const int T = u * kUnit + 16 * stage_group, lo = pg < 0 ? 16 : lo_min - T, hi = hi_max - T;
+        uint32_t nans = 0;
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+          const uint32_t keep = byte_range(lo - 4 * e, hi - 4 * e);
+#pragma unroll
+          for (int i = 0; i < SP; i++) {
+            raw[i][e] &= keep;
+            const uint32_t nb = nan_bytes(raw[i][e]);
+            nans |= nb;
+            raw[i][e] &= ~((nb >> 7) * 0xFFu);
+          }
+        }
+        if (nans) nan_at_[u & 3] = u;
+        if (pg == -2) bad_at_[u & 3] = u;
+        if (pg == -2 && w4 < 2 && n == 0 && a.kv.bad) atomicAdd(a.kv.bad, 1);
+      }
+      // operand (16-token block x of 4: tile, 8 tokens; 32-dim tile): lane (n, h)
+      uint8_t* w = lds_ + 2 * KB + ((u - u0) & 1) * VB + (2 * tile * DT + (w4 >> 1)) * 1024 + 16 * lane;
+#pragma unroll
+      for (int i = 0; i < SP; i++) {
+        *(v8bf*)(w + PS * i * 1024) = bf16x8_of_e4m3(raw[i].x, raw[i].y, sc);
+        *(v8bf*)(w + (PS * i + DT) * 1024) = bf16x8_of_e4m3(raw[i].z, raw[i].w, sc);
+      }
+    }
+  };
+  auto meet = [&]() {  // LDS reads and writes are done; loads stay in flight
+    __asm__ volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    __asm__ volatile("" ::: "memory");
+  };
+
+  v16f sc[NC][2];
+  v8bf pf[NC][4];  // weights of 8 tokens: tile, first or second eight of the lane's 16
+  auto sees = [&](int u) { return u * kUnit < whi && u * kUnit + kUnit > wlo; };
+  auto mul = [](const v8bf& x, const v8bf& y, const v16f& z) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, y, z, 0, 0, 0);
+  };
+  // A product phase is a run of stages of four operands, read a stage ahead (two
+  // ahead: 3% slower):
+  // the scores of step u, then the weighted values of step u - 1.
+  constexpr int KST = DS / 2, VST = DT;
+  v8bf f[2][4];
+  auto read_stage = [&](int st, const uint8_t* kb, const uint8_t* vb) {
+#pragma unroll
+    for (int e = 0; e < 4; e++) {
+      if (st < KST) f[st & 1][e] = *(const v8bf*)(kb + ((e & 1) * DS + 2 * st + (e >> 1)) * 1024 + 16 * lane);
+      else f[st & 1][e] = *(const v8bf*)(vb + (4 * (st - KST) + e) * 1024 + 16 * lane);
+    }
+  };
+  auto multiply_stage = [&](int st) {
+#pragma unroll
+    for (int e = 0; e < 4; e++)
+#pragma unroll
+      for (int c = 0; c < NC; c++) {
+        if (st < KST) {  // tile e % 2, dims 16 (2 st + e / 2) ..
+          sc[c][e & 1] = mul(f[st & 1][e], qf[c][2 * st + (e >> 1)], sc[c][e & 1]);
+        } else {         // operand 4 (st - KST) + e: tokens / DT, dims % DT
+          const int i = 4 * (st - KST) + e;
+          o[c][i % DT] = mul(f[st & 1][e], pf[c][i / DT], o[c][i % DT]);
+        }
+      }
+  };
+  auto products = [&](auto from, auto to, const uint8_t* kb, const uint8_t* vb) {
+    constexpr int F = decltype(from)::value, E = decltype(to)::value;
+    if constexpr (F == 0) {
+#pragma unroll
+      for (int c = 0; c < NC; c++)
+#pragma unroll
+        for (int t = 0; t < 2; t++)
+#pragma unroll
+          for (int e = 0; e < 16; e++) sc[c][t][e] = 0.f;
+    }
+    read_stage(F, kb, vb);
+#pragma unroll
+    for (int st = F; st < E; st++) {
+      if (st + 1 < E) read_stage(st + 1, kb, vb);
+      __builtin_amdgcn_sched_barrier(0);
+      multiply_stage(st);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  // rare: step u holds a NaN code among tokens that not every row of the workgroup sees
+  auto mark_nans = [&](int u) {
+#pragma unroll 1
+    for (int t = 0; t < 2; t++) {
+      const int T = u * kUnit + 32 * t + 16 * hf;
+      int pg = T < hi_max ? table[T >> a.kv.lp] : -1;
+      pg = pg >= 0 && pg < a.kv.n_pages ? pg : -1;
+      const uint8_t* vc = a.kv.vc + (((int64_t)(pg < 0 ? 0 : pg) * a.kv.H + h) << sh) + (T & (P - 1));
+#pragma unroll 1
+      for (int d = 0; d < DT; d++) {
+        const mx_u4 w = *(const mx_u4*)(vc + (int64_t)(32 * d + n) * P);
+        v8bf isn[2];
+#pragma unroll
+        for (int e = 0; e < 16; e++)
+          isn[e >> 3][e & 7] = (__bf16)(pg >= 0 && ((nan_bytes(w[e >> 2]) >> (8 * (e & 3) + 7)) & 1u) ? 1.f : 0.f);
+#pragma unroll
+        for (int c = 0; c < NC; c++) {
+          v8bf vis[2];
+#pragma unroll
+          for (int e = 0; e < 16; e++)
+            vis[e >> 3][e & 7] = (__bf16)(T + e >= vlo[c] && T + e < vhi[c] ? 1.f : 0.f);
+          v16f hit;
+#pragma unroll
+          for (int e = 0; e < 16; e++) hit[e] = 0.f;
+          hit = mul(isn[0], vis[0], hit);
+          hit = mul(isn[1], vis[1], hit);
+#pragma unroll
+          for (int e = 0; e < 16; e++) nanned[c] |= hit[e] > 0.f ? uint64_t(1) << (16 * d + e) : 0;
+        }
+      }
+    }
+  };
+  // weights of step u from its scores
+  auto softmax = [&](int u) {
+    const int T = u * kUnit;
+    bool mask = T + kUnit > whi_all || T < wlo_all;
+    int unread = 0;  // tiles whose 16 tokens of the lane cannot be read
+    if (bad_at_[u & 3] == u) {
+      mask = true;
+#pragma unroll
+      for (int t = 0; t < 2; t++) {
+        const int at = T + 32 * t + 16 * hf;
+        const int pg = at < hi_max ? table[at >> a.kv.lp] : -1;
+        unread |= pg >= 0 && pg < a.kv.n_pages ? 0 : 1 << t;
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < NC; c++) {
+      if (mask) {
+#pragma unroll
+        for (int t = 0; t < 2; t++) {
+          const int at = T + 32 * t + 16 * hf;
+          const int lo = (unread >> t) & 1 ? 16 : vlo[c] - at, hi = vhi[c] - at;
+          const uint32_t up = hi >= 16 ? 0xFFFFu : hi <= 0 ? 0u : (1u << hi) - 1u;
+          const uint32_t seen = lo >= 16 ? 0u : lo <= 0 ? up : up & ~((1u << lo) - 1u);
+#pragma unroll
+          for (int e = 0; e < 16; e++) sc[c][t][e] = (seen >> e) & 1u ? sc[c][t][e] : -INFINITY;
+        }
+      }
+      float mx = -INFINITY;
+#pragma unroll
+      for (int e = 0; e < 32; e++) mx = fmaxf(mx, sc[c][e >> 4][e & 15]);
+      const auto sw = __builtin_amdgcn_permlane32_swap(__float_as_uint(mx), __float_as_uint(mx), false, false);
+      mx = fmaxf(__uint_as_float(sw[0]), __uint_as_float(sw[1])) * scale;
+      // The maximum in use may lag by up to 2^8 (weights up to 256 lose no
+      // precision), so O is rescaled in few of the steps.
+      if (__any(mx > m[c] + 8.f)) {
+        const float mn = fmaxf(m[c], mx), mu = mn == -INFINITY ? 0.f : mn;
+        const float al = __builtin_amdgcn_exp2f(m[c] - mu);  // first tokens: 2^-inf = 0
+        m[c] = mn;
+        l[c] *= al;
+#pragma unroll
+        for (int d = 0; d < DT; d++)
+#pragma unroll
+          for (int e = 0; e < 16; e++) o[c][d][e] *= al;
+      }
+      const float mu = m[c] == -INFINITY ? 0.f : m[c];
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int e = 0; e < 32; e++) {
+        const float p = __builtin_amdgcn_exp2f(fmaf(sc[c][e >> 4][e & 15], scale, -mu));  // masked: 2^-inf = 0
+        sum[e & 3] += p;
+        pf[c][e >> 3][e & 7] = (__bf16)p;
+      }
+      l[c] += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+    }
+  };
+
+  // the phases of attn_prompt
+  if (tid < 4) nan_at_[tid] = bad_at_[tid] = -1;
+  __syncthreads();
+  int pg0 = u0 < u1 ? pages(u0) : -1, pg1 = u0 + 1 < u1 ? pages(u0 + 1) : -1;
+  if (u0 < u1) fetch(u0, pg0);
+  // the maximum and the mask's -infinity want a positive scale
+  const uint32_t flip = a.scale2 < 0.f ? 0x80008000u : 0u, keep = none ? 0x80008000u : ~0u;
+#pragma unroll
+  for (int c = 0; c < NC; c++)
+#pragma unroll
+    for (int d = 0; d < DS; d++)
+      qf[c][d] = __builtin_bit_cast(v8bf, (__builtin_bit_cast(mx_u4, qf[c][d]) ^ flip) & keep);
+  if (u0 < u1) stage(u0, pg0);
+  meet();
+  if (!keys) meet();
+  for (int u = u0; u <= u1; u++) {
+    const bool more = u + 1 < u1;
+    const int pg2 = u + 2 < u1 ? pages(u + 2) : -1;
+    if (more) fetch(u + 1, pg1);
+    {
+      const bool s_now = u < u1 && sees(u), w_now = u > u0 && sees(u - 1);
+      const uint8_t *kb = lds_ + ((u - u0) & 1) * KB, *vb = lds_ + 2 * KB + ((u - u0 + 1) & 1) * VB;
+      using First = std::integral_constant<int, 0>;
+      using Middle = std::integral_constant<int, KST>;
+      using Last = std::integral_constant<int, KST + VST>;
+      if (w_now && nan_at_[(u - 1) & 3] == u - 1) mark_nans(u - 1);
+      if (s_now) products(First{}, Middle{}, kb, vb);
+      if (w_now) products(Middle{}, Last{}, kb, vb);
+    }
+    meet();
+    if (u < u1 && sees(u)) softmax(u);
+    if (more) stage(u + 1, pg1);
+    pg1 = pg2;
+    if (keys || u < u1) meet();
+  }
+  // through LDS, so that a row's stores lie side by side: a wave's rows are its own
+  __syncthreads();
+  uint8_t* out = lds_ + wave * (32 * NC * OUT);
+#pragma unroll
+  for (int c = 0; c < NC; c++) {
+    l[c] += __shfl_xor(l[c], 32);
+    const float inv = l[c] > 0.f || l[c] != l[c] ? 1.0f / l[c] : 0.f;
+#pragma unroll
+    for (int d = 0; d < DT; d++)
+#pragma unroll
+      for (int x = 0; x < 4; x++) {  // dims 32 d + 8 x + 4 h .. + 3
+        float y[4];
+#pragma unroll
+        for (int e = 0; e < 4; e++)
+          y[e] = (nanned[c] >> (16 * d + 4 * x + e)) & 1 ? __uint_as_float(0x7FC00000u) : o[c][d][4 * x + e] * inv;
+        uint2 w;
+        w.x = bf16_bits(y[0]) | (bf16_bits(y[1]) << 16);
+        w.y = bf16_bits(y[2]) | (bf16_bits(y[3]) << 16);
+        *(uint2*)(out + (32 * c + n) * OUT + 64 * d + 16 * x + 8 * hf) = w;
+      }
+    if (a.lse && hf == 0 && rho[c] < R) {
+      const uint32_t at = (uint32_t)rho[c] / G;
+      a.lse[(s.row0 + at) * a.Hq + (int64_t)h * G + (rho[c] - at * G)] =
+          l[c] == 0.f ? -INFINITY : (m[c] + __builtin_amdgcn_logf(l[c])) * kLn2;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NC * D / 16; i++) {
+    const int row = (i * 64 + lane) / (D / 8), d = 8 * (lane % (D / 8));
+    const uint32_t rc = rho0 + row, at = rc / G;
+    const mx_u4 w = *(const mx_u4*)(out + row * OUT + 2 * d);
+    if (rc < (uint32_t)R) *(mx_u4*)(a.o + (s.row0 + at) * a.o_stride + ((int64_t)h * G + (rc - at * G)) * D + d) = w;
+  }
+}
+
 struct Plan {
   int nc;             // column tiles of a decode tile; 0: attn_prompt
-  int64_t tiles;      // a bound
   int64_t blocks;
 };
 
 constexpr int64_t kPromptRows = 128;
-#ifndef T64
-#define T64 512
-#endif
-#ifndef T128
-#define T128 512
-#endif
-#ifndef T256
-#define T256 512
-#endif
-#ifndef V64
-#define V64 64, 2, 8
-#define R64 256
-#endif
-#ifndef V128
-#define V128 128, 2, 8
-#define R128 256
-#endif
-#ifndef V256
-#define V256 256, 1, 8
-#define R256 128
-#endif
-constexpr int prompt_rows(int D) { return D == 64 ? R64 : D == 128 ? R128 : R256; }
+// rows of a workgroup
+constexpr int prompt_rows(int D) { return D == 128 ? 256 : 128; }
 
 Plan plan_attention(int D, int H, int64_t n_seqs, int64_t total_q, int64_t max_q, int64_t G) {
   Plan p;
   const int64_t R = max_q * G;
   if (R >= kPromptRows) {
     p.nc = 0;
-    p.tiles = n_seqs * H * cdiv(R, prompt_rows(D));
-    p.blocks = min(p.tiles, H * (total_q * G / prompt_rows(D) + n_seqs));
+    p.blocks = min(n_seqs * H * cdiv(R, prompt_rows(D)), H * (total_q * G / prompt_rows(D) + n_seqs));
     return p;
   }
   p.nc = R > 16 && D <= 128 ? 2 : 1;  // wider heads: the registers of 16 rows
-  p.tiles = n_seqs * H * cdiv(R, 16 * p.nc);
   p.blocks = D == 256 ? kMaxShares / 2 : kMaxShares;  // what the chip holds at once
   return p;
 }
@@ -998,14 +1375,13 @@ size_t attention_workspace_bytes(int D, int H, int64_t n_seqs, int64_t total_q, 
 
 hipError_t launch_attention(AttnArgs a, void* ws, hipStream_t s) {
   const Plan p = plan_attention(a.kv.D, a.kv.H, a.kv.n_seqs, a.kv.total_q, a.kv.max_q, a.G);
-  a.tiles = p.tiles;
   a.cnt = (uint32_t*)ws + 16;
   a.part = (float*)((uint8_t*)ws + kCounterBytes);
   const dim3 grid((unsigned)p.blocks);
   if (p.nc == 0) {
-    if (a.kv.D == 64) hipLaunchKernelGGL((attn_prompt<V64>), grid, dim3(T64), 0, s, a);
-    else if (a.kv.D == 128) hipLaunchKernelGGL((attn_prompt<V128>), grid, dim3(T128), 0, s, a);
-    else hipLaunchKernelGGL((attn_prompt<V256>), grid, dim3(T256), 0, s, a);
+    if (a.kv.D == 64) hipLaunchKernelGGL((attn_prompt32<64, 1, 4, 3>), grid, dim3(256), 0, s, a);
+    else if (a.kv.D == 128) hipLaunchKernelGGL((attn_prompt32<128, 1, 8, 2>), grid, dim3(512), 0, s, a);
+    else hipLaunchKernelGGL((attn_prompt<256, 1, 8>), grid, dim3(512), 0, s, a);
     return hipGetLastError();
   }
 #define LOWBIT_DEC(DD, NN) \
