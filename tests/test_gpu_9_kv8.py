@@ -261,6 +261,80 @@ def test_long_context_splits(D, P):
     attend(c, lens, [1, 1, 1], 3, 4, window=2000)
 
 
+@pytest.mark.parametrize("D,H,G,P", [(64, 2, 4, 16), (128, 2, 5, 64), (256, 1, 4, 128)])
+@pytest.mark.parametrize("causal,window", [(True, 0), (True, 900), (False, 0)])
+def test_prompt_parts(D, H, G, P, causal, window):
+    """Chunks of rows against contexts long enough to be cut into parts."""
+    lens, new = [5003, 1300, 40, 0], [33, 40, 40, 3]
+    print(f"parts D={D} G={G} P={P} causal={causal} window={window}", flush=True)
+    c = Cache(lens, P, H, D, seed=12)
+    fill(c, lens, 13)
+    starts = np.concatenate([[0], np.cumsum(new)])
+    size = lb.attention_kv8_workspace(c.gpu, c.tables(), i32(lens), H * G, int(starts[-1]), q_starts=i32(starts),
+                                      max_q=max(new))
+    assert size > 4 * 128 * (D + 2) * 4  # holds more than one part's rows
+    q, O, lse = attend(c, lens, new, G, 14, causal=causal, window=window)
+    for _ in range(2):
+        O2, l2 = lb.attention_kv8(q, c.gpu, c.tables(), i32(lens), q_starts=i32(starts), max_q=max(new),
+                                  causal=causal, window=window, return_lse=True)
+        assert torch.equal(O, O2) and torch.equal(lse, l2)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("T", [300, 3000])
+def test_unreadable_pages_and_nan_in_chunks(T, D):
+    """Pages that cannot be read in the middle of many rows' context, and a NaN
+    value that half of the rows see."""
+    P, H, G, n = 32, 2, 2, 70
+    print(f"unreadable pages T={T} D={D}", flush=True)
+    c = Cache([T], P, H, D, seed=18)
+    fill(c, [T], 16)
+    keep = c.table.copy()
+    gone = np.isin(np.arange(T) // P, (2, 5))
+    c.table[0, 2], c.table[0, 5] = c.gpu[0].shape[0] + 7, -1
+    at = T - n // 2
+    c.gpu[1].view(torch.uint8)[int(c.table[0, at // P]), 1, 5, at % P] = 0x7F
+    bad = torch.zeros(1, dtype=torch.int32, device="cuda")
+    q = torch.randn(n, H * G, D, device="cuda").bfloat16()
+    O = f64(lb.attention_kv8(q, c.gpu, c.tables(), i32([T]), bad_pages=bad))
+    assert int(bad) >= 2
+    c.table = keep
+    K, V = c.read(0, T)
+    for i in range(n):
+        see = ~gone & (np.arange(T) <= T - n + i)
+        o, _, A, eps = R.attention(f64(q[i:i + 1]), K[see], V[see], int(see.sum()) - 1, D ** -0.5, True, 0)
+        want = np.zeros((H * G, D), bool)
+        want[G:, 5] = T - n + i >= at
+        nan = np.isnan(O[i])
+        assert np.array_equal(nan, want), i
+        assert np.all((np.abs(O[i] - o[0]) <= R.attention_tolerance(o, A, eps, T)[0]) | want), i
+
+
+def test_one_tile_in_very_many_shares():
+    """One key head and a context that more than 64 workgroups share: joined in groups of many."""
+    T, P, D = 40000, 64, 64
+    print("one tile, many shares", flush=True)
+    c = Cache([T], P, 1, D, seed=22)
+    fill(c, [T], 23)
+    attend(c, [T], [1], 2, 24)
+    attend(c, [T], [3], 1, 25, window=33000)
+
+
+@pytest.mark.parametrize("D,G,big", [(64, 2, 3), (128, 1, 130)])
+def test_many_sequences(D, G, big):
+    """More sequences than threads that number them, empty ones among them; in
+    the second case some are prompts."""
+    g = np.random.default_rng(31)
+    B, P, H = 700, 16, 1
+    print(f"many sequences D={D} big={big}", flush=True)
+    new = g.integers(0, 3, B)
+    new[[5, 300, B - 1]] = big
+    lens = np.where(g.random(B) < 0.2, 0, new + g.integers(0, 40, B))
+    c = Cache(list(lens), P, H, D, seed=32)
+    fill(c, list(map(int, lens)), 33)
+    attend(c, list(map(int, lens)), list(map(int, new)), G, 34)
+
+
 def test_rows_that_see_nothing():
     """Length 0, more new tokens than the sequence holds, and rows behind the last sequence."""
     print("empty rows", flush=True)
@@ -435,6 +509,40 @@ def test_decode_step_in_a_graph():
             c.append(b, lens[b] - 1, f64(K)[b:b + 1], f64(V)[b:b + 1])
         c.check(f"replay {i}")
         compare(c, q, O, lse, lens, [0, 1, 2])
+
+
+def test_chunk_in_parts_in_a_graph():
+    """A chunk of rows against a long context, captured and replayed as the
+    context grows, with eager calls of the same kind between."""
+    P, H, D, G, n = 64, 1, 128, 4, 40
+    print("graph of parts", flush=True)
+    T = 4000
+    c = Cache([T + 64], P, H, D, seed=43)
+    fill(c, [T], 44)
+    table, dl = c.tables(), i32([T])
+    q = torch.zeros(n, H * G, D, device="cuda", dtype=torch.bfloat16)
+    O, lse = torch.empty_like(q), torch.empty(n, H * G, device="cuda")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    lb.reserve_workspace(lb.attention_kv8_workspace(c.gpu, table, dl, H * G, n), s)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        lb.attention_kv8(q, c.gpu, table, dl, O=O, lse=lse)
+    for i in range(3):
+        K, V = tokens(1, H, D, 100 + i), tokens(1, H, D, 200 + i)
+        T += 1
+        dl.copy_(i32([T]))
+        lb.kv8_append(c.gpu, table, dl, K, V)
+        c.append(0, T - 1, f64(K), f64(V))
+        q.copy_(torch.randn(n, H * G, D, device="cuda"))
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            graph.replay()
+            e = lb.attention_kv8(q, c.gpu, table, dl)
+        torch.cuda.synchronize()
+        assert torch.equal(e, O)
+        compare(c, q, O, lse, [T], [0, n])
 
 
 def test_two_streams_at_once():

@@ -628,7 +628,7 @@ int lowbit_attention_kv8_workspace(const lowbit_kv8* cache, const lowbit_kv8_bat
   const int rc = kv8_check(cache, batch, &a);
   if (rc) return rc;
   if (q_heads < 1 || q_heads > (1 << 16) || q_heads % a.H != 0) return LOWBIT_E_SHAPE;
-  *bytes = attention_workspace_bytes(a.D, a.H, a.n_seqs, a.total_q, a.max_q, q_heads / a.H);
+  *bytes = attention_workspace_bytes(a, q_heads / a.H);
   return LOWBIT_OK;
 }
 
@@ -646,7 +646,7 @@ int lowbit_attention_kv8(const lowbit_kv8* cache, const lowbit_kv8_batch* batch,
   if (window < 0) return LOWBIT_E_SHAPE;
   a.G = q_heads / a.kv.H;
   if (a.kv.max_q * a.G > (1 << 30) ||
-      attention_blocks(a.kv.D, a.kv.H, a.kv.n_seqs, a.kv.total_q, a.kv.max_q, a.G) > (1 << 22))
+      attention_blocks(a.kv, a.G) > (1 << 22))
     return LOWBIT_E_SHAPE;
   if (!aligned(Q_bf16, 16) || !aligned(O_bf16, 16) || q_stride % 8 != 0 || o_stride % 8 != 0 ||
       (lse && !aligned(lse, 4)))
@@ -660,7 +660,7 @@ int lowbit_attention_kv8(const lowbit_kv8* cache, const lowbit_kv8_batch* batch,
   a.o = O_bf16;
   a.o_stride = o_stride;
   a.lse = lse;
-  const size_t need = attention_workspace_bytes(a.kv.D, a.kv.H, a.kv.n_seqs, a.kv.total_q, a.kv.max_q, a.G);
+  const size_t need = attention_workspace_bytes(a.kv, a.G);
   void* ws = nullptr;
   if (need) {
     const int r2 = workspace((hipStream_t)stream, need, &ws);

@@ -637,6 +637,19 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
 // values (64 tokens) are widened to bf16 once for all waves and lie in LDS as
 // whole MFMA operands, 1 KiB per 16 rows x 32 k in the order of the lanes:
 // writes and reads without bank conflicts.
+// Where the tiles do not fill the chip, a tile's steps are cut into parts, one
+// workgroup each, whose results attn_join puts together.
+//
+// A part's results lie in rows of kPartPad floats more than D: sums of O
+// (before the division), maximum (of base 2), sum of weights.
+constexpr int kPartPad = 4;
+// steps [u0, u1) of part k of n
+__device__ __forceinline__ void part_steps(int k, int n, int* u0, int* u1) {
+  const int each = (*u1 - *u0) / n, more = (*u1 - *u0) - each * n;
+  *u0 += each * k + min(k, more);
+  *u1 = *u0 + each + (k < more ? 1 : 0);
+}
+
 template <int D, int NC, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, 2) void attn_prompt(AttnArgs a) {
   constexpr int DS = D / 32, DT = D / 16, HALF = 32 * WAVES, SP = 4 * D / HALF;
@@ -649,45 +662,45 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attn_prompt(AttnArgs a) {
   // heads run fastest, so that an XCD (bid % 8) keeps few of them in its L2;
   // the last, longest row tiles of a sequence start first
   constexpr int ROWS = 16 * NC * WAVES;
-  const int64_t bid = blockIdx.x;
-  const int h = (int)(bid % a.kv.H);
+  const uint32_t G = (uint32_t)a.G, H = (uint32_t)a.kv.H, at_part = blockIdx.x / H, tile_at = at_part / (uint32_t)a.parts;
+  const int h = (int)(blockIdx.x - at_part * H), part = (int)(at_part - tile_at * a.parts);
   int64_t b, item;
   auto tiles = [&](int64_t i) -> int64_t { return (seq_span(a.kv, i).n * a.G + ROWS - 1) / ROWS; };
   __shared__ int64_t scan_[WAVES + 2];
   ItemScan<64 * WAVES, decltype(tiles)> scan(a.kv.n_seqs, tiles, scan_);
-  if (bid / a.kv.H >= scan.total) return;
-  scan.find(bid / a.kv.H, &b, &item);
+  if (tile_at >= scan.total) return;
+  scan.find(tile_at, &b, &item);
   const SeqSpan s = seq_span(a.kv, b);
-  const int64_t R = (int64_t)s.n * a.G, wg0 = ((R + ROWS - 1) / ROWS - 1 - item) * ROWS;
+  // rows count to less than 2^31 (checked at the entry)
+  const int R = s.n * (int)G, wg0 = (R - 1) / ROWS * ROWS - (int)item * ROWS;
   const int len = s.len, first = len - s.n, P = 1 << a.kv.lp;
 
   // what rows [r0, r1) see between them: some of them [lo, hi), all of them [lo_all, hi_all)
-  auto range = [&](int64_t r0, int64_t r1, int* lo, int* hi, int* lo_all, int* hi_all) {
+  auto range = [&](int r0, int r1, int* lo, int* hi, int* lo_all, int* hi_all) {
     r0 = r0 < R - 1 ? r0 : R - 1;
     r1 = r1 < R ? r1 : R;
-    const int p0 = first + (int)(r0 / a.G), p1 = first + (int)((r1 - 1) / a.G);
+    const int p0 = first + (int)((uint32_t)r0 / G), p1 = first + (int)((uint32_t)(r1 - 1) / G);
     *hi = a.causal ? max(0, min(len, p1 + 1)) : len;
     *hi_all = a.causal ? max(0, min(len, p0 + 1)) : len;
     *lo = a.window > 0 ? max(0, p0 - a.window + 1) : 0;
     *lo_all = a.window > 0 ? max(0, p1 - a.window + 1) : 0;
   };
   int wlo, whi, wlo_all, whi_all, lo_min, hi_max, lo_all, hi_all;
-  const int64_t rho0 = wg0 + wave * 16 * NC;
+  const int rho0 = wg0 + wave * 16 * NC;
   range(wg0, wg0 + 16 * NC * WAVES, &lo_min, &hi_max, &lo_all, &hi_all);
   range(rho0, rho0 + 16 * NC, &wlo, &whi, &wlo_all, &whi_all);
   whi = __builtin_amdgcn_readfirstlane(rho0 < R ? whi : 0);
   const bool none = fabsf(a.scale2) < 0x1p-126f;  // all scores 0
-  int64_t rho[NC];
-  int vlo[NC], vhi[NC];
+  int rho[NC], vlo[NC], vhi[NC];
   v8bf qf[NC][DS];
 #pragma unroll
   for (int c = 0; c < NC; c++) {
     rho[c] = rho0 + 16 * c + n;
-    const int64_t rc = rho[c] < R ? rho[c] : R - 1;
-    const int p = first + (int)(rc / a.G);
+    const uint32_t rc = rho[c] < R ? rho[c] : R - 1, at = rc / G;
+    const int p = first + (int)at;
     vhi[c] = a.causal ? min(len, p + 1) : len;
     vlo[c] = a.window > 0 ? max(0, p - a.window + 1) : 0;
-    const uint16_t* qp = a.q + (s.row0 + rc / a.G) * a.q_stride + (h * a.G + rc % a.G) * D + 16 * g;
+    const uint16_t* qp = a.q + (s.row0 + at) * a.q_stride + ((int64_t)h * G + (rc - at * G)) * D + 16 * g;
 #pragma unroll
     for (int d = 0; d < DS; d++) {  // dims 64 (d / 2) + 16 g + 8 (d % 2) .. + 7
       mx_u4 w = *(const mx_u4*)(qp + 64 * (d >> 1) + 8 * (d & 1));
@@ -710,7 +723,8 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attn_prompt(AttnArgs a) {
     for (int d = 0; d < DT; d++) o[c][d] = v4f{0.f, 0.f, 0.f, 0.f};
   }
 
-  const int u0 = lo_min / kUnit, u1 = (hi_max + kUnit - 1) / kUnit;
+  int u0 = lo_min / kUnit, u1 = (hi_max + kUnit - 1) / kUnit;
+  part_steps(part, a.parts, &u0, &u1);
   const int32_t* table = a.kv.table + b * a.kv.width;
   // Page of the 16 tokens that the lane stages from: tokens 64 u + 16 x .. with
   // x = row / 4 of the keys' operand, x = group of the values'.
@@ -946,20 +960,30 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attn_prompt(AttnArgs a) {
     l[c] += __shfl_xor(l[c], 16);
     l[c] += __shfl_xor(l[c], 32);
     if (rho[c] >= R) continue;
-    const float inv = l[c] > 0.f || l[c] != l[c] ? 1.0f / l[c] : 0.f;
-    const int64_t tok = s.row0 + rho[c] / a.G, hd = h * a.G + rho[c] % a.G;
-    uint16_t* op = a.o + tok * a.o_stride + hd * D + 4 * g;
 #pragma unroll
-    for (int d = 0; d < DT; d++) {
+    for (int d = 0; d < DT; d++)
 #pragma unroll
       for (int e = 0; e < 4; e++)
         if ((nanned[c] >> (4 * d + e)) & 1) o[c][d][e] = __uint_as_float(0x7FC00000u);
+    if (a.parts > 1) {
+      float* pp = a.part + ((int64_t)blockIdx.x * ROWS + (rho[c] - wg0)) * (D + kPartPad);
+#pragma unroll
+      for (int d = 0; d < DT; d++) *(v4f*)(pp + 16 * d + 4 * g) = o[c][d];
+      if (g == 0) *(float2*)(pp + D) = make_float2(m[c], l[c]);
+      continue;
+    }
+    const float inv = l[c] > 0.f || l[c] != l[c] ? 1.0f / l[c] : 0.f;
+    const uint32_t tok = (uint32_t)rho[c] / G;
+    const int64_t row = s.row0 + tok, hd = (int64_t)h * G + (rho[c] - tok * G);
+    uint16_t* op = a.o + row * a.o_stride + hd * D + 4 * g;
+#pragma unroll
+    for (int d = 0; d < DT; d++) {
       uint2 w;
       w.x = bf16_bits(o[c][d][0] * inv) | (bf16_bits(o[c][d][1] * inv) << 16);
       w.y = bf16_bits(o[c][d][2] * inv) | (bf16_bits(o[c][d][3] * inv) << 16);
       *(uint2*)(op + 16 * d) = w;
     }
-    if (a.lse && g == 0) a.lse[tok * a.Hq + hd] = l[c] == 0.f ? -INFINITY : (m[c] + __builtin_amdgcn_logf(l[c])) * kLn2;
+    if (a.lse && g == 0) a.lse[row * a.Hq + hd] = l[c] == 0.f ? -INFINITY : (m[c] + __builtin_amdgcn_logf(l[c])) * kLn2;
   }
 }
 
@@ -987,8 +1011,8 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void attn_prompt32(AttnArgs a) {
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n = lane & 31, hf = lane >> 5;
   constexpr int ROWS = 32 * NC * WAVES;
-  const uint32_t G = (uint32_t)a.G, H = (uint32_t)a.kv.H, tile_at = blockIdx.x / H;
-  const int h = (int)(blockIdx.x - tile_at * H);
+  const uint32_t G = (uint32_t)a.G, H = (uint32_t)a.kv.H, at_part = blockIdx.x / H, tile_at = at_part / (uint32_t)a.parts;
+  const int h = (int)(blockIdx.x - at_part * H), part = (int)(at_part - tile_at * a.parts);
   int64_t b, item;
   auto tiles = [&](int64_t i) -> int64_t { return (seq_span(a.kv, i).n * a.G + ROWS - 1) / ROWS; };
   __shared__ int64_t scan_[WAVES + 2];
@@ -1044,7 +1068,8 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void attn_prompt32(AttnArgs a) {
       for (int e = 0; e < 16; e++) o[c][d][e] = 0.f;
   }
 
-  const int u0 = lo_min / kUnit, u1 = (hi_max + kUnit - 1) / kUnit;
+  int u0 = lo_min / kUnit, u1 = (hi_max + kUnit - 1) / kUnit;
+  part_steps(part, a.parts, &u0, &u1);
   const int32_t* table = a.kv.table + b * a.kv.width;
   // This thread's 16-byte pieces of a step.  Keys (first half of the waves,
   // tile w4 % 2): 16 dims 16 (2 (w4 / 2 + 2 i) + h) .. of the token of row n.
@@ -1304,6 +1329,26 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void attn_prompt32(AttnArgs a) {
     pg1 = pg2;
     if (keys || u < u1) meet();
   }
+  if (a.parts > 1) {
+#pragma unroll
+    for (int c = 0; c < NC; c++) {
+      l[c] += __shfl_xor(l[c], 32);
+      if (rho[c] >= R) continue;
+      float* pp = a.part + ((int64_t)blockIdx.x * ROWS + (rho[c] - wg0)) * (D + kPartPad);
+#pragma unroll
+      for (int d = 0; d < DT; d++)
+#pragma unroll
+        for (int x = 0; x < 4; x++) {
+          v4f y;
+#pragma unroll
+          for (int e = 0; e < 4; e++)
+            y[e] = (nanned[c] >> (16 * d + 4 * x + e)) & 1 ? __uint_as_float(0x7FC00000u) : o[c][d][4 * x + e];
+          *(v4f*)(pp + 32 * d + 8 * x + 4 * hf) = y;
+        }
+      if (hf == 0) *(float2*)(pp + D) = make_float2(m[c], l[c]);
+    }
+    return;
+  }
   // through LDS, so that a row's stores lie side by side: a wave's rows are its own
   __syncthreads();
   uint8_t* out = lds_ + wave * (32 * NC * OUT);
@@ -1339,49 +1384,118 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void attn_prompt32(AttnArgs a) {
   }
 }
 
+// Results of the parts of a tile: O = sum 2^(m_k - M) O_k / sum 2^(m_k - M) l_k,
+// M the largest m_k, in the order of the parts.  One thread for four dims of a
+// row, rows of ROWS as the tile's workgroups have them.
+template <int D, int ROWS>
+__global__ __launch_bounds__(256) void attn_join(AttnArgs a) {
+  constexpr int T4 = D / 4, AHEAD = 8;
+  const uint32_t G = (uint32_t)a.G, H = (uint32_t)a.kv.H, tile_at = blockIdx.x / H, h = blockIdx.x - tile_at * H;
+  auto tiles = [&](int64_t i) -> int64_t { return (seq_span(a.kv, i).n * a.G + ROWS - 1) / ROWS; };
+  __shared__ int64_t scan_[256 / 64 + 2];
+  ItemScan<256, decltype(tiles)> scan(a.kv.n_seqs, tiles, scan_);
+  if (tile_at >= scan.total) return;
+  int64_t b, item;
+  scan.find(tile_at, &b, &item);
+  const SeqSpan s = seq_span(a.kv, b);
+  const int R = s.n * (int)G, wg0 = (R - 1) / ROWS * ROWS - (int)item * ROWS;
+  const int at = blockIdx.y * 256 + threadIdx.x, r = at / T4, d = at % T4 * 4;
+  if (wg0 + r >= R) return;
+  const int64_t step = (int64_t)H * ROWS * (D + kPartPad);  // to the next part
+  const float* p = a.part + (((int64_t)tile_at * a.parts * H + h) * ROWS + r) * (D + kPartPad);
+  float M = -INFINITY, L = 0.f;
+  v4f o = v4f{0.f, 0.f, 0.f, 0.f};
+  for (int k = 0; k < a.parts; k += AHEAD) {
+    v4f po[AHEAD];
+    float2 ml[AHEAD];
+#pragma unroll
+    for (int e = 0; e < AHEAD; e++) {
+      const float* q = p + min(k + e, a.parts - 1) * step;
+      po[e] = *(const v4f*)(q + d);
+      ml[e] = *(const float2*)(q + D);
+    }
+    float mx = M;
+#pragma unroll
+    for (int e = 0; e < AHEAD; e++) mx = fmaxf(mx, ml[e].x);
+    const float mu = mx == -INFINITY ? 0.f : mx, al = __builtin_amdgcn_exp2f(M - mu);
+    M = mx;
+    L *= al;
+#pragma unroll
+    for (int c = 0; c < 4; c++) o[c] *= al;
+#pragma unroll
+    for (int e = 0; e < AHEAD; e++) {
+      if (k + e >= a.parts) break;
+      const float w = __builtin_amdgcn_exp2f(ml[e].x - mu);
+      L += w * ml[e].y;
+#pragma unroll
+      for (int c = 0; c < 4; c++) o[c] += w * po[e][c];
+    }
+  }
+  const float inv = L > 0.f || L != L ? 1.0f / L : 0.f;
+  const uint32_t rc = wg0 + r, tok = rc / G;
+  const int64_t row = s.row0 + tok, hd = (int64_t)h * G + (rc - tok * G);
+  uint2 w;
+  w.x = bf16_bits(o[0] * inv) | (bf16_bits(o[1] * inv) << 16);
+  w.y = bf16_bits(o[2] * inv) | (bf16_bits(o[3] * inv) << 16);
+  *(uint2*)(a.o + row * a.o_stride + hd * D + d) = w;
+  if (a.lse && d == 0) a.lse[row * a.Hq + hd] = L == 0.f ? -INFINITY : (M + __builtin_amdgcn_logf(L)) * kLn2;
+}
+
 struct Plan {
   int nc;             // column tiles of a decode tile; 0: attn_prompt
+  int parts;          // of a prompt tile's steps
   int64_t blocks;
 };
 
 constexpr int64_t kPromptRows = 128;
-// rows of a workgroup
+// rows of a workgroup, workgroups that the chip holds at once
 constexpr int prompt_rows(int D) { return D == 128 ? 256 : 128; }
+constexpr int prompt_slots(int D) { return D == 64 ? 768 : 256; }
 
-Plan plan_attention(int D, int H, int64_t n_seqs, int64_t total_q, int64_t max_q, int64_t G) {
+// window: 0 where rows see everything before them or more
+Plan plan_attention(const KvArgs& kv, int64_t G, int64_t window) {
   Plan p;
-  const int64_t R = max_q * G;
+  const int64_t R = kv.max_q * G, rows = prompt_rows(kv.D), slots = prompt_slots(kv.D);
+  p.parts = 1;
   if (R >= kPromptRows) {
     p.nc = 0;
-    p.blocks = min(n_seqs * H * cdiv(R, prompt_rows(D)), H * (total_q * G / prompt_rows(D) + n_seqs));
+    p.blocks = min(kv.n_seqs * kv.H * cdiv(R, rows), kv.H * (kv.total_q * G / rows + kv.n_seqs));
+    // a part has eight steps or more: the join costs what some four take
+    const int64_t most = window > 0 ? min((int64_t)kv.max_kv, window + rows / G + 2) : kv.max_kv;
+    p.parts = (int)max(min(slots / p.blocks, most / (8 * kUnit)), (int64_t)1);
     return p;
   }
-  p.nc = R > 16 && D <= 128 ? 2 : 1;  // wider heads: the registers of 16 rows
-  p.blocks = D == 256 ? kMaxShares / 2 : kMaxShares;  // what the chip holds at once
+  p.nc = R > 16 && kv.D <= 128 ? 2 : 1;  // wider heads: the registers of 16 rows
+  p.blocks = kv.D == 256 ? kMaxShares / 2 : kMaxShares;  // what the chip holds at once
   return p;
 }
 
 }  // namespace
 
-int64_t attention_blocks(int D, int H, int64_t n_seqs, int64_t total_q, int64_t max_q, int64_t G) {
-  return plan_attention(D, H, n_seqs, total_q, max_q, G).blocks;
-}
+int64_t attention_blocks(const KvArgs& kv, int64_t G) { return plan_attention(kv, G, 0).blocks; }
 
-size_t attention_workspace_bytes(int D, int H, int64_t n_seqs, int64_t total_q, int64_t max_q, int64_t G) {
-  const Plan p = plan_attention(D, H, n_seqs, total_q, max_q, G);
-  if (p.nc == 0) return 0;
-  return (size_t)kCounterBytes + (size_t)4 * kMaxShares * 16 * p.nc * (D + 2) * 4;
+size_t attention_workspace_bytes(const KvArgs& kv, int64_t G) {
+  const Plan p = plan_attention(kv, G, 0);  // a window takes no more
+  if (p.nc > 0) return (size_t)kCounterBytes + (size_t)4 * kMaxShares * 16 * p.nc * (kv.D + 2) * 4;
+  if (p.parts == 1) return 0;
+  return (size_t)kCounterBytes + (size_t)(p.blocks * p.parts * prompt_rows(kv.D)) * (kv.D + kPartPad) * 4;
 }
 
 hipError_t launch_attention(AttnArgs a, void* ws, hipStream_t s) {
-  const Plan p = plan_attention(a.kv.D, a.kv.H, a.kv.n_seqs, a.kv.total_q, a.kv.max_q, a.G);
+  const Plan p = plan_attention(a.kv, a.G, a.causal ? a.window : 0);
   a.cnt = (uint32_t*)ws + 16;
   a.part = (float*)((uint8_t*)ws + kCounterBytes);
-  const dim3 grid((unsigned)p.blocks);
+  a.parts = p.parts;
+  const dim3 grid((unsigned)(p.blocks * p.parts));
   if (p.nc == 0) {
     if (a.kv.D == 64) hipLaunchKernelGGL((attn_prompt32<64, 1, 4, 3>), grid, dim3(256), 0, s, a);
     else if (a.kv.D == 128) hipLaunchKernelGGL((attn_prompt32<128, 1, 8, 2>), grid, dim3(512), 0, s, a);
     else hipLaunchKernelGGL((attn_prompt<256, 1, 8>), grid, dim3(512), 0, s, a);
+    if (p.parts == 1) return hipGetLastError();
+    const dim3 join((unsigned)p.blocks, (unsigned)(prompt_rows(a.kv.D) * a.kv.D / 4 / 256));
+    if (a.kv.D == 64) hipLaunchKernelGGL((attn_join<64, prompt_rows(64)>), join, dim3(256), 0, s, a);
+    else if (a.kv.D == 128) hipLaunchKernelGGL((attn_join<128, prompt_rows(128)>), join, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((attn_join<256, prompt_rows(256)>), join, dim3(256), 0, s, a);
     return hipGetLastError();
   }
 #define LOWBIT_DEC(DD, NN) \

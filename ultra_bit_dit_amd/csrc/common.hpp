@@ -177,8 +177,8 @@ int64_t kv8_span(const KvArgs& a);  // pages one sequence's new tokens can touch
 hipError_t launch_kv8_append(const KvArgs& a, bool f32, const void* K, const void* V, int64_t k_stride,
                              int64_t v_stride, hipStream_t s);
 // workgroups of an attention launch, and its workspace (counters included; 0: none)
-int64_t attention_blocks(int D, int H, int64_t n_seqs, int64_t total_q, int64_t max_q, int64_t G);
-size_t attention_workspace_bytes(int D, int H, int64_t n_seqs, int64_t total_q, int64_t max_q, int64_t G);
+int64_t attention_blocks(const KvArgs& kv, int64_t G);
+size_t attention_workspace_bytes(const KvArgs& kv, int64_t G);
 hipError_t launch_attention(AttnArgs a, void* ws, hipStream_t s);
 
 }  // namespace lowbit

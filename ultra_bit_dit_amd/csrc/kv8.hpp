@@ -60,7 +60,8 @@ struct AttnArgs {
   uint16_t* o;               // bf16, o_stride elements between tokens
   int64_t o_stride;
   float* lse;                // [total_q][Hq] or NULL
-  float* part;               // results of shares: two places each, then of their groups
+  float* part;               // results of shares: two places each, then of their groups; or of a tile's parts
+  int parts;                 // of a prompt tile
   uint32_t* cnt;             // arrivals: of a group (by the place of its first share), then of a tile
 };
 
