@@ -310,6 +310,38 @@ def test_unreadable_pages_and_nan_in_chunks(T, D):
         assert np.all((np.abs(O[i] - o[0]) <= R.attention_tolerance(o, A, eps, T)[0]) | want), i
 
 
+@pytest.mark.parametrize("D,P", [(64, 16), (128, 32), (256, 64)])
+@pytest.mark.parametrize("causal,window", [(True, 0), (True, 130), (False, 0)])
+def test_up_to_32_rows_behind_a_wide_table(D, P, causal, window):
+    """17 to 32 rows a head in calls whose bound on the length is large; table
+    entries behind a sequence's pages are anything.  A NaN value in the last
+    tokens reaches the rows that see it."""
+    lens, new, H, G = [700, 131, 9, 64], [5, 4, 5, 1], 2, 6
+    print(f"wide table D={D} P={P} causal={causal} window={window}", flush=True)
+    c = Cache(lens, P, H, D, seed=52)
+    fill(c, lens, 53)
+    wide = torch.full((len(lens), 40000 // P), -77, dtype=torch.int32, device="cuda")
+    wide[:, :c.width] = c.tables()
+    starts = np.concatenate([[0], np.cumsum(new)])
+    g = torch.Generator(device="cuda").manual_seed(54)
+    q = torch.randn(int(starts[-1]), H * G, D, device="cuda", generator=g).bfloat16()
+
+    def run():
+        return lb.attention_kv8(q, c.gpu, wide, i32(lens), q_starts=i32(starts), max_q=5, causal=causal,
+                                window=window, return_lse=True)
+
+    O, lse = run()
+    compare(c, q, O, lse, lens, starts, causal=causal, window=window)
+    t = lens[0] - 3
+    c.gpu[1].view(torch.uint8)[int(c.table[0, t // P]), 1, 7, t % P] = 0xFF
+    O2, lse2 = run()
+    want = torch.zeros_like(O, dtype=torch.bool)
+    for i in range(5):
+        want[i, G:, 7] = not causal or lens[0] - 5 + i >= t
+    assert torch.equal(torch.isnan(O2), want)
+    assert torch.equal(torch.where(want, O, O2), O) and torch.equal(lse, lse2)
+
+
 def test_one_tile_in_very_many_shares():
     """One key head and a context that more than 64 workgroups share: joined in groups of many."""
     T, P, D = 40000, 64, 64

@@ -1447,7 +1447,20 @@ struct Plan {
   int64_t blocks;
 };
 
-constexpr int64_t kPromptRows = 128;
+// Few rows or many.  A wave of attn_decode has 16 rows (32 for D = 64 and 128, in
+// twice the registers) and every tile reads the cache again; attn_prompt reads
+// it once for all rows but widens it for 128 or 256 of them and joins by another
+// launch.  us, attn_decode / attn_prompt, 32 heads over 8 (D = 256: 24 over 4):
+//   D = 128, 40 rows, 1 x 4096 29 / 21, 1 x 32768 66 / 44, 64 x 600 72 / 49
+//   D = 128, 20 rows, 1 x 4096 23 / 21, 16 x 2048 43 / 36, 1 x 32768 49 / 42,
+//            64 x 600 41 / 48, 64 x 2048 76 / 113, 1 x 131071 91 / 112
+//   D = 128, 16 rows, 1 x 4096 19 / 21, 16 x 2048 25 / 36
+//   D = 64,  80 rows, 16 x 2048 35 / 29; 40 rows 25 / 25; 20 rows 20 / 22
+//   D = 256, 18 rows, 1 x 8192 30 / 27, 16 x 2048 36 / 28, 64 x 2048 95 / 70
+bool many_rows(const KvArgs& kv, int64_t R) {
+  if (kv.D == 128 && R > 16 && kv.n_seqs * kv.H * cdiv(kv.max_kv, kUnit) <= 4096) return true;
+  return R > (kv.D == 256 ? 16 : 32);
+}
 // rows of a workgroup, workgroups that the chip holds at once
 constexpr int prompt_rows(int D) { return D == 128 ? 256 : 128; }
 constexpr int prompt_slots(int D) { return D == 64 ? 768 : 256; }
@@ -1457,7 +1470,7 @@ Plan plan_attention(const KvArgs& kv, int64_t G, int64_t window) {
   Plan p;
   const int64_t R = kv.max_q * G, rows = prompt_rows(kv.D), slots = prompt_slots(kv.D);
   p.parts = 1;
-  if (R >= kPromptRows) {
+  if (many_rows(kv, R)) {
     p.nc = 0;
     p.blocks = min(kv.n_seqs * kv.H * cdiv(R, rows), kv.H * (kv.total_q * G / rows + kv.n_seqs));
     // a part has eight steps or more: the join costs what some four take
