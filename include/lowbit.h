@@ -43,18 +43,19 @@
  * point waits for the GPU except lowbit_chain_status, lowbit_chain_destroy
  * and lowbit_release_workspaces, which say so.
  *
- * Streams, workspaces and graphs.  lowbit_gemv and lowbit_gemm use a device
- * workspace that the library owns, one per (device, stream).  Calls on one
- * stream are ordered and share it; calls on different streams never share
- * one.  A call that needs more than its stream's workspace holds allocates a
+ * Streams, workspaces and graphs.  lowbit_gemv, lowbit_gemm, lowbit_gemm_mxfp4
+ * and lowbit_attention_kv8 use a device workspace that the library owns, one
+ * per (device, stream).  Calls on one stream are ordered and share it; calls on
+ * different streams never share one.  A call that needs more than its stream's workspace holds allocates a
  * larger one (hipMalloc, which may synchronize the device as HIP does) and
  * keeps the smaller one allocated until lowbit_release_workspaces, because
  * kernels already queued, and graphs captured earlier, may still use it; no
  * call waits on the stream.  A stream that is being captured into a HIP graph
  * cannot grow its workspace: such a call returns LOWBIT_E_NOMEM, so reserve
  * the workspace first (lowbit_workspace_bytes + lowbit_reserve_workspace, or
- * one eager call of the largest captured product on that stream).  A captured
- * graph keeps the workspace address it was captured with; replaying it is
+ * one eager call of the largest captured product on that stream;
+ * lowbit_gemm_mxfp4_workspace and lowbit_attention_kv8_workspace for those).
+ * A captured graph keeps the workspace address it was captured with; replaying it is
  * valid until lowbit_release_workspaces.  Replays of graphs captured on one
  * stream must run in order on one stream (they share its workspace).  The
  * kernels leave the workspace's counters as they found them, so a replay
@@ -129,7 +130,8 @@ extern "C" {
 enum lowbit_status {
   LOWBIT_OK = 0,
   LOWBIT_E_NULL = -1,        /* a required pointer is NULL                    */
-  LOWBIT_E_SHAPE = -2,       /* K % 128 != 0, N/M/K < 1, or size overflow     */
+  LOWBIT_E_SHAPE = -2,       /* K % 128 != 0 (MXFP4: % 32), a size < 1 or too
+                                large                                         */
   LOWBIT_E_ALIGN = -3,       /* pointer not aligned as documented             */
   LOWBIT_E_UNSUPPORTED = -4, /* format / dtype combination not provided       */
   LOWBIT_E_BADCODE = -5,     /* reserved for callers that check the flag     */
@@ -422,7 +424,7 @@ int lowbit_pack_mxfp4(int64_t rows, int64_t K, const uint8_t* codes, const uint8
  * codes 0, so every product that reads it is NaN.  values, if not NULL,
  * receives what the codes stand for, [rows][K] in x_dtype.  Weights (once) and
  * activations (per call) alike.  X, pcodes, pscales, values 16-byte aligned,
- * x_stride >= K and rows 16-byte aligned.
+ * x_stride >= K and rows 16-byte aligned; the buffers do not overlap.
  * Errors: E_NULL, E_UNSUPPORTED, E_SHAPE, E_ALIGN, E_HIP. */
 int lowbit_quantize_mxfp4(int64_t rows, int64_t K, int x_dtype, const void* X, int64_t x_stride,
                           void* pcodes, void* pscales, void* values, void* stream);
@@ -497,9 +499,12 @@ typedef struct lowbit_kv8_batch {
  * are rescaled (times 2^(e_old - e), rounded to nearest even: exact above
  * e4m3's subnormal range).  code = x / 2^e to nearest even, infinities to
  * +-448, NaN to NaN.  Bytes behind a sequence's last token stay as they were.
- * A page that receives tokens must belong to one sequence of the batch (full
- * pages may be shared by any number).  Writing the same tokens again changes
- * nothing.  K, V 16-byte aligned, rows 16-byte aligned.
+ * A page that receives tokens must belong to one sequence of the batch and
+ * stand in its table once (full pages may be shared by any number).  New tokens
+ * that lie before the sequence's start (more of them than kv_lens) are not
+ * written.  Writing the same tokens again changes nothing.  K, V 16-byte
+ * aligned, rows 16-byte aligned; n_seqs * kv_heads * (pages that max_q tokens
+ * can touch) <= 2^23.
  * Errors: E_NULL, E_UNSUPPORTED (dtype, page_tokens, head_dim), E_SHAPE,
  * E_ALIGN, E_HIP. */
 int lowbit_kv8_append(const lowbit_kv8* cache, const lowbit_kv8_batch* batch, int dtype, const void* K,
@@ -512,12 +517,17 @@ int lowbit_kv8_append(const lowbit_kv8* cache, const lowbit_kv8_batch* batch, in
  * reads key head h / (q_heads / kv_heads)), tokens q_stride elements apart; O
  * likewise, o_stride apart.  lse, if not NULL, receives [total_q][q_heads] the
  * natural logarithm of the softmax sum.  A row that sees no token gets O = 0
- * and lse = -infinity; what lies in tokens a row does not see (NaN codes too)
+ * and lse = -infinity (so does one whose scores are all -infinity, which takes
+ * an infinity in Q); what lies in tokens a row does not see (NaN codes too)
  * does not reach it.  With causal == 0 the cache may hold another sequence (an
  * encoder's states) of its own length.  Weights times 2^e enter the second
  * product rounded to bf16; sums and statistics are fp32.  Results do not
  * depend on the order in which workgroups run.  Rows of sequences behind the
  * last q_starts entry are not written.
+ * One call runs one kernel for all its sequences, chosen by max_q * q_heads /
+ * kv_heads and max_kv: long contexts with single tokens and prompts of many
+ * rows are faster as two calls, each with a max_q of its own.
+ * max_q * q_heads / kv_heads <= 2^30; O does not overlap Q or the cache.
  * Q, O 16-byte aligned, strides multiples of 8.  Uses the stream's workspace
  * (lowbit_attention_kv8_workspace bytes) as lowbit_gemv does; reserve it
  * before a capture.

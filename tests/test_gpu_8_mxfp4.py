@@ -199,3 +199,65 @@ def test_stream_and_graph():
         _, _, xv = lb.quantize_mxfp4(x, values=True)
         check_product(y4, wv, f64(xv), K, False, f"replay {i}")
         check_product(y16, wv, f64(x), K, False, f"replay {i}")
+
+
+def test_split_products_in_a_graph():
+    """Products whose K is split over workgroups, captured with a reserved
+    workspace and replayed, with eager ones on the stream between."""
+    K, cases = 17408, ((3, 48, False), (40, 130, False), (70, 100, True))
+    print("graph of split products", flush=True)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    work = []
+    for M, N, x4 in cases:
+        size = lb.gemm_mxfp4_workspace(M, N, K, lb.MXFP4 if x4 else lb.BF16)
+        assert size > 4 * M * N  # more than one sum for each output
+        lb.reserve_workspace(size, s)
+        wc, ws, x, _, wv, _ = product_case(M, N, K, 7, False)
+        work.append((M, N, x4, wc, ws, x, wv, torch.empty(M, N, device="cuda"), *lb.empty_mxfp4(M, K)))
+
+    def step():
+        for M, N, x4, wc, ws, x, _, y, pc, ps in work:
+            if x4:
+                lb.quantize_mxfp4(x, pcodes=pc, pscales=ps)
+                lb.gemm_mxfp4(M, N, K, wc, ws, pc, x_scales=ps, Y=y)
+            else:
+                lb.gemm_mxfp4(M, N, K, wc, ws, x, Y=y)
+
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        step()
+    for i in range(3):
+        for M, *_, x, _, _, _, _ in work:
+            x.copy_(device(values(M, K, 60 + i), torch.bfloat16))
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            graph.replay()
+            first = [w[7].clone() for w in work]
+            step()
+        torch.cuda.synchronize()
+        for (M, N, x4, _, _, x, wv, y, _, _), g in zip(work, first):
+            assert torch.equal(y, g)
+            xv = lb.quantize_mxfp4(x, values=True)[2] if x4 else x
+            check_product(g, wv, f64(xv), K, False, f"replay {i}")
+
+
+def test_capture_without_a_workspace_is_refused():
+    """A stream that is being captured cannot grow its workspace: E_NOMEM, and nothing is recorded."""
+    M, N, K = 40, 130, 17408
+    print("capture without workspace", flush=True)
+    wc, ws, x, _, _, _ = product_case(M, N, K, 8, False)
+    y = torch.full((M, N), 7.0, device="cuda")
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    lb.release_workspaces()  # the stream may have been another test's
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        y.add_(1.0)
+        with pytest.raises(lb.LowbitError) as e:
+            lb.gemm_mxfp4(M, N, K, wc, ws, x, Y=y)
+        assert e.value.status == lb.E_NOMEM
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.all(y == 8.0)

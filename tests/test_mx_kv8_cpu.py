@@ -61,6 +61,20 @@ def test_mxfp4_refusals():
     assert L.lowbit_gemm(1, 1, 16, 128, A16, A16, lb.MXFP4, A16, None, lb.F32, A16, None) == lb.E_UNSUPPORTED
 
 
+def test_product_workspace():
+    """Host-only: its refusals, and that K is split only where tiles are few."""
+    L = lb.lib()
+    n = ctypes.c_size_t(5)
+    f = L.lowbit_gemm_mxfp4_workspace
+    assert f(1, 16, 32, lb.BF16, None) == lb.E_NULL
+    for bad in ((0, 16, 32), (1, 0, 32), (1, 16, 0), (1, 16, 48), (1, (1 << 26) + 1, 32), (1 << 30, 1 << 20, 32)):
+        n.value = 5
+        assert f(*bad, lb.BF16, ctypes.byref(n)) == lb.E_SHAPE and n.value == 0
+    assert f(1, 16, 32, lb.F32, ctypes.byref(n)) == lb.E_UNSUPPORTED
+    assert lb.gemm_mxfp4_workspace(40, 130, 17408, lb.BF16) > 0
+    assert lb.gemm_mxfp4_workspace(4096, 16384, 5120, lb.BF16) == 0
+
+
 def kv(**over):
     c = dict(n_pages=4, page_tokens=16, kv_heads=2, head_dim=64, k_codes=0x10000, v_codes=0x20000, k_scales=0x30000,
              v_scales=0x40000)
