@@ -302,8 +302,9 @@ void launch_small(const MxArgs& a, int W, int ykind, hipStream_t s) {
 // exactly for its own (the later groups' stay in flight) and one barrier a
 // group keeps the ring.  W is operand A (rows n) and X operand B (columns m):
 // a lane then holds four consecutive n of one output row.
-// s_waitcnt immediate: vmcnt n, lgkmcnt and expcnt at their maxima
-constexpr int vm_wait(int n) { return (n & 15) | ((n >> 4) << 14) | 0xF70; }
+// s_waitcnt immediate: vmcnt n; lgkmcnt 0, so that a wave has what it read of a
+// buffer before another refills it; expcnt at its maximum
+constexpr int vm_wait(int n) { return (n & 15) | ((n >> 4) << 14) | 0x70; }
 
 template <int N>
 __device__ __forceinline__ void wait_copies_and_meet() {
