@@ -206,429 +206,428 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
   int64_t rt = quot(item, blocks);
   int at = (int)(item - rt * blocks);  // first block of this share in the tile
   for (;;) {
-  const int64_t x0 = x - at;     // the tile's first block among all
-  const int count = (int)min(blocks - at, x_end - x);
-  // shares that hold blocks of this tile
-  const int64_t share0 = quot((x0 + 1) * shares + total - 1, total) - 1;
-  const int64_t share1 = quot((x0 + blocks) * shares + total - 1, total) - 1;
-  const int n_parts = (int)(share1 - share0 + 1);
-  const int64_t R = (int64_t)s.n * a.G;
-  const int64_t rho0 = rt * 16 * NC;
-  const int len = s.len, first = len - s.n;  // position of the first new token
+    const int64_t x0 = x - at;     // the tile's first block among all
+    const int count = (int)min(blocks - at, x_end - x);
+    // shares that hold blocks of this tile
+    const int64_t share0 = quot((x0 + 1) * shares + total - 1, total) - 1;
+    const int64_t share1 = quot((x0 + blocks) * shares + total - 1, total) - 1;
+    const int n_parts = (int)(share1 - share0 + 1);
+    const int64_t R = (int64_t)s.n * a.G;
+    const int64_t rho0 = rt * 16 * NC;
+    const int len = s.len, first = len - s.n;  // position of the first new token
 
-  // visible tokens of this lane's rows: [vlo, vhi)
-  int vlo[NC], vhi[NC];
-  int hi_max = 0, hi_min = len, lo_min = 0, lo_max = 0;
-  {
-    const int64_t rlast = rho0 + 16 * NC - 1 < R ? rho0 + 16 * NC - 1 : R - 1;
-    const int p0 = first + (int)(rho0 / a.G), p1 = first + (int)(rlast / a.G);
-    hi_max = a.causal ? min(len, p1 + 1) : len;
-    hi_min = a.causal ? min(len, p0 + 1) : len;
-    hi_max = max(hi_max, 0);
-    hi_min = max(hi_min, 0);
-    if (a.window > 0) {
-      lo_min = max(0, p0 - a.window + 1);
-      lo_max = max(0, p1 - a.window + 1);
-    }
-  }
-  int64_t rho[NC];
-#pragma unroll
-  for (int c = 0; c < NC; c++) {
-    rho[c] = rho0 + 16 * c + n;
-    const int64_t rc = rho[c] < R ? rho[c] : R - 1;
-    const int p = first + (int)(rc / a.G);
-    vhi[c] = a.causal ? min(len, p + 1) : len;
-    vlo[c] = a.window > 0 ? max(0, p - a.window + 1) : 0;
-  }
-  const int u0 = lo_min / kUnit + kDecWaves * at, u1 = min(u0 + kDecWaves * count, (hi_max + kUnit - 1) / kUnit);
-
-  // Q: lane (n, g) holds dims 64 c + 16 g + 8 e .. + 7 of its row
-  v8bf qf[NC][DC][2];
-#pragma unroll
-  for (int c = 0; c < NC; c++) {
-    const int64_t rc = rho[c] < R ? rho[c] : R - 1;
-    const uint16_t* qp = a.q + (s.row0 + rc / a.G) * a.q_stride + (h * a.G + rc % a.G) * D + 16 * g;
-#pragma unroll
-    for (int d = 0; d < DC; d++) {
-      qf[c][d][0] = __builtin_bit_cast(v8bf, *(const mx_u4*)(qp + 64 * d));
-      qf[c][d][1] = __builtin_bit_cast(v8bf, *(const mx_u4*)(qp + 64 * d + 8));
-    }
-  }
-
-  v4f o[NC][DT];
-  float m[NC], l[NC];
-#pragma unroll
-  for (int c = 0; c < NC; c++) {
-    m[c] = -INFINITY;
-    l[c] = 0.f;
-#pragma unroll
-    for (int d = 0; d < DT; d++) o[c][d] = v4f{0.f, 0.f, 0.f, 0.f};
-  }
-
-  const int32_t* table = a.kv.table + b * a.kv.width;
-  const int64_t page_bytes = ((int64_t)D << a.kv.lp);
-  // page of the 16 tokens from t on; -1 where there are none or the entry is unusable
-  auto page_at = [&](int t) -> int {
-    if (t >= hi_max) return -1;
-    const int pg = table[t >> a.kv.lp];
-    return pg >= 0 && pg < a.kv.n_pages ? pg : -2;
-  };
-  mx_u4 kr[4][DC], vr[DT];
-  int pgv = -1, pkn = -1, pvn = -1;  // pages: of this step's values, of the next step's keys and values
-  uint32_t kb = 0, vb = 0;           // exponent bytes of the lane's keys and values
-  auto next_pages = [&](int u) {
-    pkn = page_at(u * kUnit + 16 * (n >> 2));
-    pvn = page_at(u * kUnit + 16 * g);
-  };
-  auto load_k = [&](int u) {
-    const int tk = u * kUnit + 16 * (n >> 2);
-    const int64_t ph = (int64_t)(pkn < 0 ? 0 : pkn) * a.kv.H + h;
-    const uint8_t* kp = a.kv.kc + ph * page_bytes + (int64_t)((tk & (P - 1)) + (n & 3)) * D + 16 * g;
-    kb = a.kv.ks[ph];
-#pragma unroll
-    for (int t = 0; t < 4; t++)
-#pragma unroll
-      for (int d = 0; d < DC; d++) kr[t][d] = *(const mx_u4*)(kp + 4 * t * D + 64 * d);
-  };
-  auto load_v = [&](int u, int pg) {
-    const int tv = u * kUnit + 16 * g;
-    pgv = pg;
-    const int64_t ph = (int64_t)(pg < 0 ? 0 : pg) * a.kv.H + h;
-    const uint8_t* vp = a.kv.vc + ph * page_bytes + (int64_t)n * P + (tv & (P - 1));
-    vb = a.kv.vs[ph];
-#pragma unroll
-    for (int d = 0; d < DT; d++) vr[d] = *(const mx_u4*)(vp + (int64_t)16 * d * P);
-  };
-
-  // Loads in flight at any time: the next keys behind the scores of this step,
-  // the next values behind its second product; page numbers a step earlier.
-  int u = u0 + wave, pvu = -1;
-  if (u < u1) {
-    next_pages(u);
-    pvu = pvn;
-    load_k(u);
-    if (u + kDecWaves < u1) next_pages(u + kDecWaves);
-    load_v(u, pvu);
-  }
-  for (; u < u1; u += kDecWaves) {
-    const bool gone = pgv < 0;  // none of this lane's 16 tokens can be read
-    const float sk = pow2_byte(kb), sv = gone ? 0.f : pow2_byte(vb);
-    if (pgv == -2 && n == 0 && a.kv.bad) atomicAdd(a.kv.bad, 1);
-    const int T = u * kUnit;
-    const bool part = T + kUnit > hi_min || T < lo_max || __any(gone);
-    // scores of tokens T + 16 g + 4 t + j
-    v4f sc[NC][4];
-#pragma unroll
-    for (int t = 0; t < 4; t++) {
-#pragma unroll
-      for (int c = 0; c < NC; c++) sc[c][t] = v4f{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int d = 0; d < DC; d++) {
-        const v8bf k0 = bf16x8_of_e4m3(kr[t][d].x, kr[t][d].y, sk), k1 = bf16x8_of_e4m3(kr[t][d].z, kr[t][d].w, sk);
-#pragma unroll
-        for (int c = 0; c < NC; c++) {
-          sc[c][t] = mfma(k0, qf[c][d][0], sc[c][t]);
-          sc[c][t] = mfma(k1, qf[c][d][1], sc[c][t]);
-        }
+    // visible tokens of this lane's rows: [vlo, vhi)
+    int vlo[NC], vhi[NC];
+    int hi_max = 0, hi_min = len, lo_min = 0, lo_max = 0;
+    {
+      const int64_t rlast = rho0 + 16 * NC - 1 < R ? rho0 + 16 * NC - 1 : R - 1;
+      const int p0 = first + (int)(rho0 / a.G), p1 = first + (int)(rlast / a.G);
+      hi_max = a.causal ? min(len, p1 + 1) : len;
+      hi_min = a.causal ? min(len, p0 + 1) : len;
+      hi_max = max(hi_max, 0);
+      hi_min = max(hi_min, 0);
+      if (a.window > 0) {
+        lo_min = max(0, p0 - a.window + 1);
+        lo_max = max(0, p1 - a.window + 1);
       }
     }
-    if (u + kDecWaves < u1) {
-      load_k(u + kDecWaves);
-      pvu = pvn;
-      if (u + 2 * kDecWaves < u1) next_pages(u + 2 * kDecWaves);
-    }
-    v8bf pf[NC][2];
-    uint32_t seen[NC];  // bit e: token 16 g + e is visible to the lane's row
+    int64_t rho[NC];
 #pragma unroll
     for (int c = 0; c < NC; c++) {
-      float mx = -INFINITY;
-      seen[c] = 0xFFFFu;
-      if (part) {
-        seen[c] = 0;
+      rho[c] = rho0 + 16 * c + n;
+      const int64_t rc = rho[c] < R ? rho[c] : R - 1;
+      const int p = first + (int)(rc / a.G);
+      vhi[c] = a.causal ? min(len, p + 1) : len;
+      vlo[c] = a.window > 0 ? max(0, p - a.window + 1) : 0;
+    }
+    const int u0 = lo_min / kUnit + kDecWaves * at, u1 = min(u0 + kDecWaves * count, (hi_max + kUnit - 1) / kUnit);
+
+    // Q: lane (n, g) holds dims 64 c + 16 g + 8 e .. + 7 of its row
+    v8bf qf[NC][DC][2];
+#pragma unroll
+    for (int c = 0; c < NC; c++) {
+      const int64_t rc = rho[c] < R ? rho[c] : R - 1;
+      const uint16_t* qp = a.q + (s.row0 + rc / a.G) * a.q_stride + (h * a.G + rc % a.G) * D + 16 * g;
+#pragma unroll
+      for (int d = 0; d < DC; d++) {
+        qf[c][d][0] = __builtin_bit_cast(v8bf, *(const mx_u4*)(qp + 64 * d));
+        qf[c][d][1] = __builtin_bit_cast(v8bf, *(const mx_u4*)(qp + 64 * d + 8));
+      }
+    }
+
+    v4f o[NC][DT];
+    float m[NC], l[NC];
+#pragma unroll
+    for (int c = 0; c < NC; c++) {
+      m[c] = -INFINITY;
+      l[c] = 0.f;
+#pragma unroll
+      for (int d = 0; d < DT; d++) o[c][d] = v4f{0.f, 0.f, 0.f, 0.f};
+    }
+
+    const int32_t* table = a.kv.table + b * a.kv.width;
+    const int64_t page_bytes = ((int64_t)D << a.kv.lp);
+    // page of the 16 tokens from t on; -1 where there are none or the entry is unusable
+    auto page_at = [&](int t) -> int {
+      if (t >= hi_max) return -1;
+      const int pg = table[t >> a.kv.lp];
+      return pg >= 0 && pg < a.kv.n_pages ? pg : -2;
+    };
+    mx_u4 kr[4][DC], vr[DT];
+    int pgv = -1, pkn = -1, pvn = -1;  // pages: of this step's values, of the next step's keys and values
+    uint32_t kb = 0, vb = 0;           // exponent bytes of the lane's keys and values
+    auto next_pages = [&](int u) {
+      pkn = page_at(u * kUnit + 16 * (n >> 2));
+      pvn = page_at(u * kUnit + 16 * g);
+    };
+    auto load_k = [&](int u) {
+      const int tk = u * kUnit + 16 * (n >> 2);
+      const int64_t ph = (int64_t)(pkn < 0 ? 0 : pkn) * a.kv.H + h;
+      const uint8_t* kp = a.kv.kc + ph * page_bytes + (int64_t)((tk & (P - 1)) + (n & 3)) * D + 16 * g;
+      kb = a.kv.ks[ph];
+#pragma unroll
+      for (int t = 0; t < 4; t++)
+#pragma unroll
+        for (int d = 0; d < DC; d++) kr[t][d] = *(const mx_u4*)(kp + 4 * t * D + 64 * d);
+    };
+    auto load_v = [&](int u, int pg) {
+      const int tv = u * kUnit + 16 * g;
+      pgv = pg;
+      const int64_t ph = (int64_t)(pg < 0 ? 0 : pg) * a.kv.H + h;
+      const uint8_t* vp = a.kv.vc + ph * page_bytes + (int64_t)n * P + (tv & (P - 1));
+      vb = a.kv.vs[ph];
+#pragma unroll
+      for (int d = 0; d < DT; d++) vr[d] = *(const mx_u4*)(vp + (int64_t)16 * d * P);
+    };
+
+    // Loads in flight at any time: the next keys behind the scores of this step,
+    // the next values behind its second product; page numbers a step earlier.
+    int u = u0 + wave, pvu = -1;
+    if (u < u1) {
+      next_pages(u);
+      pvu = pvn;
+      load_k(u);
+      if (u + kDecWaves < u1) next_pages(u + kDecWaves);
+      load_v(u, pvu);
+    }
+    for (; u < u1; u += kDecWaves) {
+      const bool gone = pgv < 0;  // none of this lane's 16 tokens can be read
+      const float sk = pow2_byte(kb), sv = gone ? 0.f : pow2_byte(vb);
+      if (pgv == -2 && n == 0 && a.kv.bad) atomicAdd(a.kv.bad, 1);
+      const int T = u * kUnit;
+      const bool part = T + kUnit > hi_min || T < lo_max || __any(gone);
+      // scores of tokens T + 16 g + 4 t + j
+      v4f sc[NC][4];
+#pragma unroll
+      for (int t = 0; t < 4; t++) {
+#pragma unroll
+        for (int c = 0; c < NC; c++) sc[c][t] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int d = 0; d < DC; d++) {
+          const v8bf k0 = bf16x8_of_e4m3(kr[t][d].x, kr[t][d].y, sk), k1 = bf16x8_of_e4m3(kr[t][d].z, kr[t][d].w, sk);
+#pragma unroll
+          for (int c = 0; c < NC; c++) {
+            sc[c][t] = mfma(k0, qf[c][d][0], sc[c][t]);
+            sc[c][t] = mfma(k1, qf[c][d][1], sc[c][t]);
+          }
+        }
+      }
+      if (u + kDecWaves < u1) {
+        load_k(u + kDecWaves);
+        pvu = pvn;
+        if (u + 2 * kDecWaves < u1) next_pages(u + 2 * kDecWaves);
+      }
+      v8bf pf[NC][2];
+      uint32_t seen[NC];  // bit e: token 16 g + e is visible to the lane's row
+#pragma unroll
+      for (int c = 0; c < NC; c++) {
+        float mx = -INFINITY;
+        seen[c] = 0xFFFFu;
+        if (part) {
+          seen[c] = 0;
+#pragma unroll
+          for (int e = 0; e < 16; e++) {
+            const int tok = T + 16 * g + e;
+            const bool see = tok >= vlo[c] && tok < vhi[c] && !gone;
+            seen[c] |= see ? 1u << e : 0u;
+            sc[c][e >> 2][e & 3] = see ? sc[c][e >> 2][e & 3] * a.scale2 : -INFINITY;
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 16; e++) sc[c][e >> 2][e & 3] *= a.scale2;
+        }
+#pragma unroll
+        for (int e = 0; e < 16; e++) mx = fmaxf(mx, sc[c][e >> 2][e & 3]);
+        const float mn = fmaxf(m[c], group_max(mx));
+        const float mu = mn == -INFINITY ? 0.f : mn;
+        const float al = __builtin_amdgcn_exp2f(m[c] - mu);  // first tokens: 2^-inf = 0
+        m[c] = mn;
+        l[c] *= al;
+#pragma unroll
+        for (int d = 0; d < DT; d++)
+#pragma unroll
+          for (int e = 0; e < 4; e++) o[c][d][e] *= al;
+        float p[16];
 #pragma unroll
         for (int e = 0; e < 16; e++) {
-          const int tok = T + 16 * g + e;
-          const bool see = tok >= vlo[c] && tok < vhi[c] && !gone;
-          seen[c] |= see ? 1u << e : 0u;
-          sc[c][e >> 2][e & 3] = see ? sc[c][e >> 2][e & 3] * a.scale2 : -INFINITY;
+          p[e] = __builtin_amdgcn_exp2f(sc[c][e >> 2][e & 3] - mu);
+          l[c] += p[e];
         }
-      } else {
 #pragma unroll
-        for (int e = 0; e < 16; e++) sc[c][e >> 2][e & 3] *= a.scale2;
+        for (int e = 0; e < 16; e++) pf[c][e >> 3][e & 7] = (__bf16)p[e];
+      }
+      if (part) {
+        // Tokens no row sees: their codes may be anything, so they become 0.
+        // A NaN code of a token that only some rows see must reach those rows
+        // alone: it becomes 0 too and is put back below.
+        uint32_t nans = 0;
+        const int lo = (gone ? 16 : lo_min - (T + 16 * g)), hi = hi_max - (T + 16 * g);
+        const uint32_t k0 = byte_range(lo, hi), k1 = byte_range(lo - 4, hi - 4);
+        const uint32_t k2 = byte_range(lo - 8, hi - 8), k3 = byte_range(lo - 12, hi - 12);
+#pragma unroll
+        for (int d = 0; d < DT; d++) {
+          vr[d].x &= k0;
+          vr[d].y &= k1;
+          vr[d].z &= k2;
+          vr[d].w &= k3;
+          nans |= nan_bytes(vr[d].x) | nan_bytes(vr[d].y) | nan_bytes(vr[d].z) | nan_bytes(vr[d].w);
+        }
+        if (__any(nans != 0)) {
+          v8bf vis[NC][2];
+#pragma unroll
+          for (int c = 0; c < NC; c++)
+#pragma unroll
+            for (int e = 0; e < 16; e++) vis[c][e >> 3][e & 7] = (__bf16)((seen[c] >> e) & 1u ? 1.0f : 0.0f);
+#pragma unroll
+          for (int d = 0; d < DT; d++) {
+            v8bf isn[2];
+#pragma unroll
+            for (int e = 0; e < 16; e++) {
+              const uint32_t w = (&vr[d])[0][e >> 2];
+              isn[e >> 3][e & 7] = (__bf16)((nan_bytes(w) >> (8 * (e & 3) + 7)) & 1u ? 1.0f : 0.0f);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; i++) vr[d][i] &= ~((nan_bytes(vr[d][i]) >> 7) * 0xFFu);
+#pragma unroll
+            for (int c = 0; c < NC; c++) {
+              v4f hit = v4f{0.f, 0.f, 0.f, 0.f};
+              hit = mfma(isn[0], vis[c][0], hit);
+              hit = mfma(isn[1], vis[c][1], hit);
+#pragma unroll
+              for (int e = 0; e < 4; e++)
+                if (hit[e] > 0.f) o[c][d][e] = __uint_as_float(0x7FC00000u);
+            }
+          }
+        }
       }
 #pragma unroll
-      for (int e = 0; e < 16; e++) mx = fmaxf(mx, sc[c][e >> 2][e & 3]);
-      const float mn = fmaxf(m[c], group_max(mx));
-      const float mu = mn == -INFINITY ? 0.f : mn;
-      const float al = __builtin_amdgcn_exp2f(m[c] - mu);  // first tokens: 2^-inf = 0
-      m[c] = mn;
-      l[c] *= al;
+      for (int d = 0; d < DT; d++) {
+        const v8bf v0 = bf16x8_of_e4m3(vr[d].x, vr[d].y, sv), v1 = bf16x8_of_e4m3(vr[d].z, vr[d].w, sv);
+#pragma unroll
+        for (int c = 0; c < NC; c++) {
+          o[c][d] = mfma(v0, pf[c][0], o[c][d]);
+          o[c][d] = mfma(v1, pf[c][1], o[c][d]);
+        }
+      }
+      if (u + kDecWaves < u1) load_v(u + kDecWaves, pvu);
+    }
+
+    // ---- the waves' results: common maximum, then O added in the order of the waves
+#pragma unroll
+    for (int c = 0; c < NC; c++) {
+      l[c] += __shfl_xor(l[c], 16);
+      l[c] += __shfl_xor(l[c], 32);
+      if (g == 0) {
+        lm_[wave][16 * c + n] = m[c];
+        ll_[wave][16 * c + n] = l[c];
+      }
+    }
+    __syncthreads();
+    float f[NC], mt[NC], lt[NC];
+#pragma unroll
+    for (int c = 0; c < NC; c++) {
+      mt[c] = -INFINITY;
+      lt[c] = 0.f;
+#pragma unroll
+      for (int w = 0; w < kDecWaves; w++) mt[c] = fmaxf(mt[c], lm_[w][16 * c + n]);
+      const float mu = mt[c] == -INFINITY ? 0.f : mt[c];
+#pragma unroll
+      for (int w = 0; w < kDecWaves; w++) lt[c] += ll_[w][16 * c + n] * __builtin_amdgcn_exp2f(lm_[w][16 * c + n] - mu);
+      f[c] = __builtin_amdgcn_exp2f(m[c] - mu);
 #pragma unroll
       for (int d = 0; d < DT; d++)
 #pragma unroll
-        for (int e = 0; e < 4; e++) o[c][d][e] *= al;
-      float p[16];
-#pragma unroll
-      for (int e = 0; e < 16; e++) {
-        p[e] = __builtin_amdgcn_exp2f(sc[c][e >> 2][e & 3] - mu);
-        l[c] += p[e];
-      }
-#pragma unroll
-      for (int e = 0; e < 16; e++) pf[c][e >> 3][e & 7] = (__bf16)p[e];
+        for (int e = 0; e < 4; e++) o[c][d][e] *= f[c];
     }
-    if (part) {
-      // Tokens no row sees: their codes may be anything, so they become 0.
-      // A NaN code of a token that only some rows see must reach those rows
-      // alone: it becomes 0 too and is put back below.
-      uint32_t nans = 0;
-      const int lo = (gone ? 16 : lo_min - (T + 16 * g)), hi = hi_max - (T + 16 * g);
-      const uint32_t k0 = byte_range(lo, hi), k1 = byte_range(lo - 4, hi - 4);
-      const uint32_t k2 = byte_range(lo - 8, hi - 8), k3 = byte_range(lo - 12, hi - 12);
+    // a tree over the waves: the upper half hands its O to the lower half
 #pragma unroll
-      for (int d = 0; d < DT; d++) {
-        vr[d].x &= k0;
-        vr[d].y &= k1;
-        vr[d].z &= k2;
-        vr[d].w &= k3;
-        nans |= nan_bytes(vr[d].x) | nan_bytes(vr[d].y) | nan_bytes(vr[d].z) | nan_bytes(vr[d].w);
-      }
-      if (__any(nans != 0)) {
-        v8bf vis[NC][2];
+    for (int half = kDecWaves / 2; half >= 1; half >>= 1) {
+      if (wave >= half && wave < 2 * half) {
 #pragma unroll
         for (int c = 0; c < NC; c++)
 #pragma unroll
-          for (int e = 0; e < 16; e++) vis[c][e >> 3][e & 7] = (__bf16)((seen[c] >> e) & 1u ? 1.0f : 0.0f);
-#pragma unroll
-        for (int d = 0; d < DT; d++) {
-          v8bf isn[2];
-#pragma unroll
-          for (int e = 0; e < 16; e++) {
-            const uint32_t w = (&vr[d])[0][e >> 2];
-            isn[e >> 3][e & 7] = (__bf16)((nan_bytes(w) >> (8 * (e & 3) + 7)) & 1u ? 1.0f : 0.0f);
-          }
-#pragma unroll
-          for (int i = 0; i < 4; i++) vr[d][i] &= ~((nan_bytes(vr[d][i]) >> 7) * 0xFFu);
-#pragma unroll
-          for (int c = 0; c < NC; c++) {
-            v4f hit = v4f{0.f, 0.f, 0.f, 0.f};
-            hit = mfma(isn[0], vis[c][0], hit);
-            hit = mfma(isn[1], vis[c][1], hit);
-#pragma unroll
-            for (int e = 0; e < 4; e++)
-              if (hit[e] > 0.f) o[c][d][e] = __uint_as_float(0x7FC00000u);
-          }
-        }
+          for (int d = 0; d < DT; d++) *(v4f*)&lo_[wave - half][((c * DT + d) * 64 + lane) * 4] = o[c][d];
       }
-    }
-#pragma unroll
-    for (int d = 0; d < DT; d++) {
-      const v8bf v0 = bf16x8_of_e4m3(vr[d].x, vr[d].y, sv), v1 = bf16x8_of_e4m3(vr[d].z, vr[d].w, sv);
-#pragma unroll
-      for (int c = 0; c < NC; c++) {
-        o[c][d] = mfma(v0, pf[c][0], o[c][d]);
-        o[c][d] = mfma(v1, pf[c][1], o[c][d]);
-      }
-    }
-    if (u + kDecWaves < u1) load_v(u + kDecWaves, pvu);
-  }
-
-  // ---- the waves' results: common maximum, then O added in the order of the waves
-#pragma unroll
-  for (int c = 0; c < NC; c++) {
-    l[c] += __shfl_xor(l[c], 16);
-    l[c] += __shfl_xor(l[c], 32);
-    if (g == 0) {
-      lm_[wave][16 * c + n] = m[c];
-      ll_[wave][16 * c + n] = l[c];
-    }
-  }
-  __syncthreads();
-  float f[NC], mt[NC], lt[NC];
-#pragma unroll
-  for (int c = 0; c < NC; c++) {
-    mt[c] = -INFINITY;
-    lt[c] = 0.f;
-#pragma unroll
-    for (int w = 0; w < kDecWaves; w++) mt[c] = fmaxf(mt[c], lm_[w][16 * c + n]);
-    const float mu = mt[c] == -INFINITY ? 0.f : mt[c];
-#pragma unroll
-    for (int w = 0; w < kDecWaves; w++) lt[c] += ll_[w][16 * c + n] * __builtin_amdgcn_exp2f(lm_[w][16 * c + n] - mu);
-    f[c] = __builtin_amdgcn_exp2f(m[c] - mu);
-#pragma unroll
-    for (int d = 0; d < DT; d++)
-#pragma unroll
-      for (int e = 0; e < 4; e++) o[c][d][e] *= f[c];
-  }
-  // a tree over the waves: the upper half hands its O to the lower half
-#pragma unroll
-  for (int half = kDecWaves / 2; half >= 1; half >>= 1) {
-    if (wave >= half && wave < 2 * half) {
-#pragma unroll
-      for (int c = 0; c < NC; c++)
-#pragma unroll
-        for (int d = 0; d < DT; d++) *(v4f*)&lo_[wave - half][((c * DT + d) * 64 + lane) * 4] = o[c][d];
-    }
-    __syncthreads();
-    if (wave < half) {
-#pragma unroll
-      for (int c = 0; c < NC; c++)
-#pragma unroll
-        for (int d = 0; d < DT; d++) {
-          const v4f v = *(const v4f*)&lo_[wave][((c * DT + d) * 64 + lane) * 4];
-#pragma unroll
-          for (int e = 0; e < 4; e++) o[c][d][e] += v[e];
-        }
-    }
-    __syncthreads();
-  }
-
-  if (n_parts == 1) {
-    if (wave == 0) {
-#pragma unroll
-      for (int c = 0; c < NC; c++) {
-        if (rho[c] >= R) continue;
-        const float inv = lt[c] > 0.f || lt[c] != lt[c] ? 1.0f / lt[c] : 0.f;
-        const int64_t tok = s.row0 + rho[c] / a.G, hd = h * a.G + rho[c] % a.G;
-        uint16_t* op = a.o + tok * a.o_stride + hd * D + 4 * g;
-#pragma unroll
-        for (int d = 0; d < DT; d++) {
-          uint2 w;
-          w.x = bf16_bits(o[c][d][0] * inv) | (bf16_bits(o[c][d][1] * inv) << 16);
-          w.y = bf16_bits(o[c][d][2] * inv) | (bf16_bits(o[c][d][3] * inv) << 16);
-          *(uint2*)(op + 16 * d) = w;
-        }
-        if (a.lse && g == 0) a.lse[tok * a.Hq + hd] = lt[c] == 0.f ? -INFINITY : (mt[c] + __builtin_amdgcn_logf(lt[c])) * kLn2;
-      }
-    }
-  } else {
-
-  // ---- Several shares: results to the workspace with device-coherent stores
-  // that complete before the arrival is counted.  A share has at most two
-  // such tiles, so it has two places: 2 share for a tile that began in an
-  // earlier one, 2 share + 1 for one that goes on.  Results are joined in the
-  // order of the shares in groups, by the last of a group to arrive, then the
-  // groups by the last of them: one workgroup reading every result of a long
-  // context would take longer than reading the context.
-  const int rows = (int)(R - rho0 < 16 * NC ? R - rho0 : 16 * NC);
-  constexpr int PR = D + 2;                      // floats of one row: O, m, l
-  constexpr int64_t PS = (int64_t)16 * NC * PR;  // of one place
-  const int group = n_parts <= 64 ? 8 : kMaxJoin, groups = (n_parts + group - 1) / group;
-  const int part_no = (int)(share - share0), grp = part_no / group;
-  const int in_group = min(group, n_parts - grp * group);
-  auto place = [&](int i) -> int64_t { return 2 * (share0 + i) + (i == 0 ? 1 : 0); };
-  float* joined = a.part + 2 * (int64_t)kMaxShares * PS;  // a group's result, at the place of its first share
-  uint32_t* group_cnt = a.cnt + place(grp * group);
-  uint32_t* tile_cnt = a.cnt + 2 * kMaxShares + share0;
-  if (wave == 0) {
-    float* mine = a.part + place(part_no) * PS;
-#pragma unroll
-    for (int c = 0; c < NC; c++) {
-      if (16 * c + n < rows) {
-        float* row = mine + (16 * c + n) * PR;
-#pragma unroll
-        for (int d = 0; d < DT; d++) {
-          put2(row + 16 * d + 4 * g, o[c][d][0], o[c][d][1]);
-          put2(row + 16 * d + 4 * g + 2, o[c][d][2], o[c][d][3]);
-        }
-        if (g == 0) put2(row + D, mt[c], lt[c]);
-      }
-    }
-    __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    if (lane == 0) s_last = __hip_atomic_fetch_add(group_cnt, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  }
-  __syncthreads();
-  // in the LDS of the waves' results: [row][kMaxJoin] maxima, then weights; sums; joined m and l
-  float* jw = &lo_[0][0];
-  float* js = jw + 16 * NC * kMaxJoin;
-  float* jm = js + 16 * NC * kMaxJoin;
-  float* jl = jm + 16 * NC;
-  static_assert(16 * NC * (2 * kMaxJoin + 2) <= (kDecWaves / 2) * 16 * NC * D, "fits the waves' O");
-  // joins the results at from(0 .. count - 1); each pair of outputs goes to put(row, dim, O, O)
-  auto join = [&](auto&& from, int count, auto&& put) {
-    for (int i = threadIdx.x; i < rows * count; i += 64 * kDecWaves) {
-      const int r = i / count, k = i % count;
-      const float2 v = get2(from(k) + r * PR + D);
-      jw[r * kMaxJoin + k] = v.x;
-      js[r * kMaxJoin + k] = v.y;
-    }
-    __syncthreads();
-    if (threadIdx.x < rows) {
-      const int r = threadIdx.x;
-      float mm = -INFINITY, L = 0.f;
-      for (int k = 0; k < count; k++) mm = fmaxf(mm, jw[r * kMaxJoin + k]);
-      const float mu = mm == -INFINITY ? 0.f : mm;
-      for (int k = 0; k < count; k++) {
-        const float w = __builtin_amdgcn_exp2f(jw[r * kMaxJoin + k] - mu);
-        L += w * js[r * kMaxJoin + k];
-        jw[r * kMaxJoin + k] = w;
-      }
-      jm[r] = mm;
-      jl[r] = L;
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < rows * (D / 2); i += 64 * kDecWaves) {
-      const int r = i / (D / 2), d = (i % (D / 2)) * 2;
-      float px = 0.f, py = 0.f;
-      for (int k0 = 0; k0 < count; k0 += kJoinLoads) {
-        float2 v[kJoinLoads];
-#pragma unroll
-        for (int k = 0; k < kJoinLoads; k++)
-          v[k] = k0 + k < count ? get2(from(k0 + k) + r * PR + d) : make_float2(0.f, 0.f);
-#pragma unroll
-        for (int k = 0; k < kJoinLoads; k++) {
-          const float w = k0 + k < count ? jw[r * kMaxJoin + k0 + k] : 0.f;
-          px += w * v[k].x;
-          py += w * v[k].y;
-        }
-      }
-      put(r, d, px, py);
-    }
-  };
-  auto finish = [&](int r, int d, float px, float py) {
-    const float L = jl[r], inv = L > 0.f || L != L ? 1.0f / L : 0.f;
-    const int64_t rr = rho0 + r, tok = s.row0 + rr / a.G, hd = h * a.G + rr % a.G;
-    *(uint32_t*)(a.o + tok * a.o_stride + hd * D + d) = bf16_bits(px * inv) | (bf16_bits(py * inv) << 16);
-    if (a.lse && d == 0) a.lse[tok * a.Hq + hd] = L == 0.f ? -INFINITY : (jm[r] + __builtin_amdgcn_logf(L)) * kLn2;
-  };
-  auto part_of_group = [&](int k) -> const float* { return a.part + place(grp * group + k) * PS; };
-  if (s_last == (uint32_t)in_group - 1) {
-    if (threadIdx.x == 0) __hip_atomic_store(group_cnt, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    if (groups == 1) {
-      join(part_of_group, n_parts, finish);
-    } else {
-      float* mine = joined + place(grp * group) * PS;
-      join(part_of_group, in_group, [&](int r, int d, float px, float py) {
-        put2(mine + r * PR + d, px, py);
-        if (d == 0) put2(mine + r * PR + D, jm[r], jl[r]);
-      });
-      __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
-      __syncthreads();  // every wave's stores are complete
-      if (threadIdx.x == 0) s_last = __hip_atomic_fetch_add(tile_cnt, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       __syncthreads();
-      if (s_last == (uint32_t)groups - 1) {
-        if (threadIdx.x == 0) __hip_atomic_store(tile_cnt, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        join([&](int k) -> const float* { return joined + place(k * group) * PS; }, groups, finish);
+      if (wave < half) {
+#pragma unroll
+        for (int c = 0; c < NC; c++)
+#pragma unroll
+          for (int d = 0; d < DT; d++) {
+            const v4f v = *(const v4f*)&lo_[wave][((c * DT + d) * 64 + lane) * 4];
+#pragma unroll
+            for (int e = 0; e < 4; e++) o[c][d][e] += v[e];
+          }
+      }
+      __syncthreads();
+    }
+
+    if (n_parts == 1) {
+      if (wave == 0) {
+#pragma unroll
+        for (int c = 0; c < NC; c++) {
+          if (rho[c] >= R) continue;
+          const float inv = lt[c] > 0.f || lt[c] != lt[c] ? 1.0f / lt[c] : 0.f;
+          const int64_t tok = s.row0 + rho[c] / a.G, hd = h * a.G + rho[c] % a.G;
+          uint16_t* op = a.o + tok * a.o_stride + hd * D + 4 * g;
+#pragma unroll
+          for (int d = 0; d < DT; d++) {
+            uint2 w;
+            w.x = bf16_bits(o[c][d][0] * inv) | (bf16_bits(o[c][d][1] * inv) << 16);
+            w.y = bf16_bits(o[c][d][2] * inv) | (bf16_bits(o[c][d][3] * inv) << 16);
+            *(uint2*)(op + 16 * d) = w;
+          }
+          if (a.lse && g == 0) a.lse[tok * a.Hq + hd] = lt[c] == 0.f ? -INFINITY : (mt[c] + __builtin_amdgcn_logf(lt[c])) * kLn2;
+        }
+      }
+    } else {
+      // ---- Several shares: results to the workspace with device-coherent stores
+      // that complete before the arrival is counted.  A share has at most two
+      // such tiles, so it has two places: 2 share for a tile that began in an
+      // earlier one, 2 share + 1 for one that goes on.  Results are joined in the
+      // order of the shares in groups, by the last of a group to arrive, then the
+      // groups by the last of them: one workgroup reading every result of a long
+      // context would take longer than reading the context.
+      const int rows = (int)(R - rho0 < 16 * NC ? R - rho0 : 16 * NC);
+      constexpr int PR = D + 2;                      // floats of one row: O, m, l
+      constexpr int64_t PS = (int64_t)16 * NC * PR;  // of one place
+      const int group = n_parts <= 64 ? 8 : kMaxJoin, groups = (n_parts + group - 1) / group;
+      const int part_no = (int)(share - share0), grp = part_no / group;
+      const int in_group = min(group, n_parts - grp * group);
+      auto place = [&](int i) -> int64_t { return 2 * (share0 + i) + (i == 0 ? 1 : 0); };
+      float* joined = a.part + 2 * (int64_t)kMaxShares * PS;  // a group's result, at the place of its first share
+      uint32_t* group_cnt = a.cnt + place(grp * group);
+      uint32_t* tile_cnt = a.cnt + 2 * kMaxShares + share0;
+      if (wave == 0) {
+        float* mine = a.part + place(part_no) * PS;
+#pragma unroll
+        for (int c = 0; c < NC; c++) {
+          if (16 * c + n < rows) {
+            float* row = mine + (16 * c + n) * PR;
+#pragma unroll
+            for (int d = 0; d < DT; d++) {
+              put2(row + 16 * d + 4 * g, o[c][d][0], o[c][d][1]);
+              put2(row + 16 * d + 4 * g + 2, o[c][d][2], o[c][d][3]);
+            }
+            if (g == 0) put2(row + D, mt[c], lt[c]);
+          }
+        }
+        __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        if (lane == 0) s_last = __hip_atomic_fetch_add(group_cnt, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      }
+      __syncthreads();
+      // in the LDS of the waves' results: [row][kMaxJoin] maxima, then weights; sums; joined m and l
+      float* jw = &lo_[0][0];
+      float* js = jw + 16 * NC * kMaxJoin;
+      float* jm = js + 16 * NC * kMaxJoin;
+      float* jl = jm + 16 * NC;
+      static_assert(16 * NC * (2 * kMaxJoin + 2) <= (kDecWaves / 2) * 16 * NC * D, "fits the waves' O");
+      // joins the results at from(0 .. count - 1); each pair of outputs goes to put(row, dim, O, O)
+      auto join = [&](auto&& from, int count, auto&& put) {
+        for (int i = threadIdx.x; i < rows * count; i += 64 * kDecWaves) {
+          const int r = i / count, k = i % count;
+          const float2 v = get2(from(k) + r * PR + D);
+          jw[r * kMaxJoin + k] = v.x;
+          js[r * kMaxJoin + k] = v.y;
+        }
+        __syncthreads();
+        if (threadIdx.x < rows) {
+          const int r = threadIdx.x;
+          float mm = -INFINITY, L = 0.f;
+          for (int k = 0; k < count; k++) mm = fmaxf(mm, jw[r * kMaxJoin + k]);
+          const float mu = mm == -INFINITY ? 0.f : mm;
+          for (int k = 0; k < count; k++) {
+            const float w = __builtin_amdgcn_exp2f(jw[r * kMaxJoin + k] - mu);
+            L += w * js[r * kMaxJoin + k];
+            jw[r * kMaxJoin + k] = w;
+          }
+          jm[r] = mm;
+          jl[r] = L;
+        }
+        __syncthreads();
+        for (int i = threadIdx.x; i < rows * (D / 2); i += 64 * kDecWaves) {
+          const int r = i / (D / 2), d = (i % (D / 2)) * 2;
+          float px = 0.f, py = 0.f;
+          for (int k0 = 0; k0 < count; k0 += kJoinLoads) {
+            float2 v[kJoinLoads];
+#pragma unroll
+            for (int k = 0; k < kJoinLoads; k++)
+              v[k] = k0 + k < count ? get2(from(k0 + k) + r * PR + d) : make_float2(0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < kJoinLoads; k++) {
+              const float w = k0 + k < count ? jw[r * kMaxJoin + k0 + k] : 0.f;
+              px += w * v[k].x;
+              py += w * v[k].y;
+            }
+          }
+          put(r, d, px, py);
+        }
+      };
+      auto finish = [&](int r, int d, float px, float py) {
+        const float L = jl[r], inv = L > 0.f || L != L ? 1.0f / L : 0.f;
+        const int64_t rr = rho0 + r, tok = s.row0 + rr / a.G, hd = h * a.G + rr % a.G;
+        *(uint32_t*)(a.o + tok * a.o_stride + hd * D + d) = bf16_bits(px * inv) | (bf16_bits(py * inv) << 16);
+        if (a.lse && d == 0) a.lse[tok * a.Hq + hd] = L == 0.f ? -INFINITY : (jm[r] + __builtin_amdgcn_logf(L)) * kLn2;
+      };
+      auto part_of_group = [&](int k) -> const float* { return a.part + place(grp * group + k) * PS; };
+      if (s_last == (uint32_t)in_group - 1) {
+        if (threadIdx.x == 0) __hip_atomic_store(group_cnt, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        if (groups == 1) {
+          join(part_of_group, n_parts, finish);
+        } else {
+          float* mine = joined + place(grp * group) * PS;
+          join(part_of_group, in_group, [&](int r, int d, float px, float py) {
+            put2(mine + r * PR + d, px, py);
+            if (d == 0) put2(mine + r * PR + D, jm[r], jl[r]);
+          });
+          __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
+          __syncthreads();  // every wave's stores are complete
+          if (threadIdx.x == 0) s_last = __hip_atomic_fetch_add(tile_cnt, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+          __syncthreads();
+          if (s_last == (uint32_t)groups - 1) {
+            if (threadIdx.x == 0) __hip_atomic_store(tile_cnt, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            join([&](int k) -> const float* { return joined + place(k * group) * PS; }, groups, finish);
+          }
+        }
       }
     }
-  }
-  }
-  // ---- the share's next tile
-  x += count;
-  if (x >= x_end) return;
-  __syncthreads();  // the LDS is free again
-  at = 0;
-  if (++rt == tiles) {
-    rt = 0;
-    do {
-      if (++b == a.kv.n_seqs) {
-        b = 0;
-        h++;
-      }
-      s = seq_span(a.kv, b);
-      tiles = tiles_of(s);
-    } while (tiles == 0);  // some sequence has tiles, as x < total
-    blocks = blocks_of(s);
-  }
+    // ---- the share's next tile
+    x += count;
+    if (x >= x_end) return;
+    __syncthreads();  // the LDS is free again
+    at = 0;
+    if (++rt == tiles) {
+      rt = 0;
+      do {
+        if (++b == a.kv.n_seqs) {
+          b = 0;
+          h++;
+        }
+        s = seq_span(a.kv, b);
+        tiles = tiles_of(s);
+      } while (tiles == 0);  // some sequence has tiles, as x < total
+      blocks = blocks_of(s);
+    }
   }
 }
 

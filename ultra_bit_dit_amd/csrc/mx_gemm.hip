@@ -63,12 +63,14 @@ __device__ __forceinline__ void store_y(void* y, int64_t i, float v) {
 }
 
 // ---------------------------------------------------------- few rows of X
-// Up to 16 rows: workgroups per row-block of W (RB of them) and split of K,
-// whose waves take the quads in turn.  A wave loads a quad's codes a quad ahead, straight to registers;
-// bf16 rows of X reach the wave's own LDS as direct copies of 1 KiB (a row of
-// a quad), with the 16-byte chunk c of row r at place c ^ r so that an
+// Up to 16 rows: a workgroup per row-block of W and split of K, whose waves take
+// the quads in turn.  A wave loads a quad's codes a quad ahead, straight to
+// registers; bf16 rows of X reach the wave's own LDS as direct copies of 1 KiB
+// (a row of a quad), with the 16-byte chunk c of row r at place c ^ r so that an
 // operand's 16 rows fall on different banks.  The partial tiles are added over
-// the waves in a fixed order.
+// the waves in a fixed order.  1 x 5120 x 5120 5.5 us on the GPU (14 MB of
+// codes), 5 x 5120 x 17408 15.7 us (47 MB, 3.0 TB/s): what bounds the longer one
+// is widening the codes, 64 conversions a wave and quad beside 16 products.
 constexpr int kSmallWaves = 8;
 constexpr int64_t kSmallRows = 16;
 constexpr int kSmallSplits = 8;
@@ -81,26 +83,22 @@ __device__ __forceinline__ void copy16(const uint8_t* src, lds_u8* dst) {
 
 [[maybe_unused]] __device__ const mx_u4 mx_zeros[16] = {};
 
-template <bool X4, int RB>
+template <bool X4>
 struct SmallQuad {
-  mx_u4 w[RB][4];
-  uint32_t ws[RB];
+  mx_u4 w[4];
+  uint32_t ws;
   mx_u4 x[X4 ? 4 : 1];  // MXFP4 rows: one row-block
   uint32_t xs;
 };
 
-template <bool X4, int RB>
-__device__ __forceinline__ void load_small(const MxArgs& a, int64_t rb0, int64_t gq, int lane, SmallQuad<X4, RB>& o) {
+template <bool X4>
+__device__ __forceinline__ void load_small(const MxArgs& a, int64_t rb, int64_t gq, int lane, SmallQuad<X4>& o) {
   // groups past the last one read it again: their codes are cleared below
+  const uint8_t* src = a.wc + rb * a.G * 1024 + 16 * lane;
 #pragma unroll
-  for (int j = 0; j < RB; j++) {
-    const int64_t rb = rb0 + j < a.NB ? rb0 + j : a.NB - 1;
-    const uint8_t* src = a.wc + rb * a.G * 1024 + 16 * lane;
-#pragma unroll
-    for (int t = 0; t < 4; t++)
-      o.w[j][t] = __builtin_nontemporal_load((const mx_u4*)(src + min(4 * gq + t, a.G - 1) * 1024));
-    o.ws[j] = *(const uint32_t*)(a.ws + ((rb * a.GQ + gq) * 64 + lane) * 4);
-  }
+  for (int t = 0; t < 4; t++)
+    o.w[t] = __builtin_nontemporal_load((const mx_u4*)(src + min(4 * gq + t, a.G - 1) * 1024));
+  o.ws = *(const uint32_t*)(a.ws + ((rb * a.GQ + gq) * 64 + lane) * 4);
   if constexpr (X4) {
 #pragma unroll
     for (int t = 0; t < 4; t++) o.x[t] = *(const mx_u4*)(a.x + (min(4 * gq + t, a.G - 1) * 64 + lane) * 16);
@@ -139,19 +137,17 @@ __device__ __forceinline__ void store_small(const MxArgs& a, const v4f& s, int64
   }
 }
 
-template <bool X4, int RB, int YK>
+template <bool X4, int YK>
 __global__ __launch_bounds__(64 * kSmallWaves) void mx_small(MxArgs a) {
 #if defined(__HIP_DEVICE_COMPILE__)
   extern __shared__ __attribute__((aligned(16))) uint8_t mem[];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), W = blockDim.x >> 6;
   const int r = lane & 15, q = lane >> 4, rows = (int)a.M;
-  const int64_t blk = blockIdx.x, rb0 = blk * RB;
+  const int64_t rb = blockIdx.x;
   const uint32_t ks = blockIdx.y, quads = (uint32_t)a.GQ;
   const int64_t q0 = quads * ks / a.KS, q1 = quads * (ks + 1) / a.KS;  // quads of this split
   uint8_t* xw = mem + wave * rows * 1024;
-  v4f acc[RB][2];  // two chains each
-#pragma unroll
-  for (int j = 0; j < RB; j++) acc[j][0] = acc[j][1] = v4f{0.f, 0.f, 0.f, 0.f};
+  v4f acc[2] = {};  // two chains
   const uint8_t* zeros = (const uint8_t*)mx_zeros;
   auto copy_x = [&](int64_t gq) {
     for (int m = 0; m < rows; m++) {
@@ -160,11 +156,11 @@ __global__ __launch_bounds__(64 * kSmallWaves) void mx_small(MxArgs a) {
     }
   };
   const int mrow = r < rows ? r : rows - 1;  // rows of the operand past the last one repeat it
-  SmallQuad<X4, RB> cur, next;
+  SmallQuad<X4> cur, next;
   int64_t gq = q0 + wave;
   if (gq < q1) {
     if constexpr (!X4) copy_x(gq);
-    load_small<X4, RB>(a, rb0, gq, lane, cur);
+    load_small<X4>(a, rb, gq, lane, cur);
   }
   for (; gq < q1; gq += W) {
     const bool more = gq + W < q1;
@@ -181,23 +177,17 @@ __global__ __launch_bounds__(64 * kSmallWaves) void mx_small(MxArgs a) {
       read_x(0);
       __builtin_amdgcn_sched_barrier(0);
     }
-    if (more) load_small<X4, RB>(a, rb0, gq + W, lane, next);
+    if (more) load_small<X4>(a, rb, gq + W, lane, next);
     if (4 * gq + 3 >= a.G) {
 #pragma unroll
       for (int t = 1; t < 4; t++)
-        if (4 * gq + t >= a.G) {
-#pragma unroll
-          for (int j = 0; j < RB; j++) cur.w[j][t] = mx_u4{0, 0, 0, 0};
-        }
+        if (4 * gq + t >= a.G) cur.w[t] = mx_u4{0, 0, 0, 0};
     }
     if constexpr (X4) {
-#pragma unroll
-      for (int j = 0; j < RB; j++) {
-        acc[j][0] = mfma_mx<0>(cur.x[0], cur.w[j][0], acc[j][0], cur.xs, cur.ws[j]);
-        acc[j][1] = mfma_mx<1>(cur.x[1], cur.w[j][1], acc[j][1], cur.xs, cur.ws[j]);
-        acc[j][0] = mfma_mx<2>(cur.x[2], cur.w[j][2], acc[j][0], cur.xs, cur.ws[j]);
-        acc[j][1] = mfma_mx<3>(cur.x[3], cur.w[j][3], acc[j][1], cur.xs, cur.ws[j]);
-      }
+      acc[0] = mfma_mx<0>(cur.x[0], cur.w[0], acc[0], cur.xs, cur.ws);
+      acc[1] = mfma_mx<1>(cur.x[1], cur.w[1], acc[1], cur.xs, cur.ws);
+      acc[0] = mfma_mx<2>(cur.x[2], cur.w[2], acc[0], cur.xs, cur.ws);
+      acc[1] = mfma_mx<3>(cur.x[3], cur.w[3], acc[1], cur.xs, cur.ws);
     } else {
 #pragma unroll
       for (int t = 0; t < 4; t++) {
@@ -205,10 +195,8 @@ __global__ __launch_bounds__(64 * kSmallWaves) void mx_small(MxArgs a) {
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int h = 0; h < 4; h++)
-#pragma unroll
-          for (int j = 0; j < RB; j++)
-            acc[j][h & 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                xf[t & 1][h], bf16x8(cur.w[j][t][h], scale_float(cur.ws[j], t)), acc[j][h & 1], 0, 0, 0);
+          acc[h & 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+              xf[t & 1][h], bf16x8(cur.w[t][h], scale_float(cur.ws, t)), acc[h & 1], 0, 0, 0);
       }
       if (more) {
         __asm__ volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // this quad's rows have been read
@@ -221,48 +209,36 @@ __global__ __launch_bounds__(64 * kSmallWaves) void mx_small(MxArgs a) {
   __syncthreads();
   float* red = (float*)mem;
 #pragma unroll
-  for (int j = 0; j < RB; j++) {
-    v4f v;
-#pragma unroll
-    for (int e = 0; e < 4; e++) v[e] = acc[j][0][e] + acc[j][1][e];
-    *(v4f*)(red + ((wave * RB + j) * 64 + lane) * 4) = v;
-  }
+  for (int e = 0; e < 4; e++) acc[0][e] += acc[1][e];
+  *(v4f*)(red + (wave * 64 + lane) * 4) = acc[0];
   __syncthreads();
-  // an item is a lane of a tile; a workgroup of one wave takes RB rounds
-  for (int it = threadIdx.x; it < RB * 64; it += blockDim.x) {
-    v4f s = *(const v4f*)(red + it * 4);
+  if (wave == 0) {
+    v4f s = *(const v4f*)(red + lane * 4);
     for (int w = 1; w < W; w++) {
-      const v4f v = *(const v4f*)(red + (w * RB * 64 + it) * 4);
+      const v4f v = *(const v4f*)(red + (w * 64 + lane) * 4);
 #pragma unroll
       for (int e = 0; e < 4; e++) s[e] += v[e];
     }
-    if (a.KS == 1) {
-      store_small<YK>(a, s, rb0 + (it >> 6), it & 63);
-    } else {
-      put_pairs(a.part + (((int64_t)ks * a.NT + blk) * RB * 64 + it) * 4, s);
-    }
+    if (a.KS == 1) store_small<YK>(a, s, rb, lane);
+    else put_pairs(a.part + (((int64_t)ks * a.NT + rb) * 64 + lane) * 4, s);
   }
-  if (a.KS == 1) return;
+  if (a.KS == 1 || wave != 0) return;
   // Splits of K: the last to arrive adds the partial tiles in their order.
-  __shared__ uint32_t s_last;
   __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
-  __syncthreads();
-  if (threadIdx.x == 0) s_last = __hip_atomic_fetch_add(a.cnt + blk, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  __syncthreads();
-  if (s_last != a.KS - 1) return;
-  if (threadIdx.x == 0) __hip_atomic_store(a.cnt + blk, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  for (int it = threadIdx.x; it < RB * 64; it += blockDim.x) {
-    v4f v[kSmallSplits];
+  uint32_t arrived = 0;
+  if (lane == 0) arrived = __hip_atomic_fetch_add(a.cnt + rb, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  if (__builtin_amdgcn_readfirstlane((int)arrived) != (int)a.KS - 1) return;
+  if (lane == 0) __hip_atomic_store(a.cnt + rb, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  v4f v[kSmallSplits];
 #pragma unroll
-    for (int k = 0; k < kSmallSplits; k++)
-      v[k] = k < (int)a.KS ? get_pairs(a.part + (((int64_t)k * a.NT + blk) * RB * 64 + it) * 4) : v4f{0.f, 0.f, 0.f, 0.f};
-    v4f s = v[0];
+  for (int k = 0; k < kSmallSplits; k++)
+    v[k] = k < (int)a.KS ? get_pairs(a.part + (((int64_t)k * a.NT + rb) * 64 + lane) * 4) : v4f{0.f, 0.f, 0.f, 0.f};
+  v4f s = v[0];
 #pragma unroll
-    for (int k = 1; k < kSmallSplits; k++)
+  for (int k = 1; k < kSmallSplits; k++)
 #pragma unroll
-      for (int e = 0; e < 4; e++) s[e] += v[k][e];
-    store_small<YK>(a, s, rb0 + (it >> 6), it & 63);
-  }
+    for (int e = 0; e < 4; e++) s[e] += v[k][e];
+  store_small<YK>(a, s, rb, lane);
 #endif
 }
 
@@ -290,9 +266,9 @@ void launch_small(const MxArgs& a, int W, int ykind, hipStream_t s) {
   const dim3 grid((unsigned)a.NT, (unsigned)a.KS);
   const size_t lds = (size_t)W * max((int64_t)1, X4 ? 0 : a.M) * 1024;
   if (ykind == YK_F32)
-    hipLaunchKernelGGL((mx_small<X4, 1, YK_F32>), grid, dim3(64 * W), lds, s, a);
+    hipLaunchKernelGGL((mx_small<X4, YK_F32>), grid, dim3(64 * W), lds, s, a);
   else
-    hipLaunchKernelGGL((mx_small<X4, 1, YK_BF16>), grid, dim3(64 * W), lds, s, a);
+    hipLaunchKernelGGL((mx_small<X4, YK_BF16>), grid, dim3(64 * W), lds, s, a);
 }
 
 // ------------------------------------------------------------ many rows of X
