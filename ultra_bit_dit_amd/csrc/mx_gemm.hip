@@ -69,8 +69,9 @@ __device__ __forceinline__ void store_y(void* y, int64_t i, float v) {
 // (a row of a quad), with the 16-byte chunk c of row r at place c ^ r so that an
 // operand's 16 rows fall on different banks.  The partial tiles are added over
 // the waves in a fixed order.  1 x 5120 x 5120 5.5 us on the GPU (14 MB of
-// codes), 5 x 5120 x 17408 15.7 us (47 MB, 3.0 TB/s): what bounds the longer one
-// is widening the codes, 64 conversions a wave and quad beside 16 products.
+// codes), 5 x 5120 x 17408 15.2 us (47 MB, 3.1 TB/s: 320 workgroups on 256 compute
+// units; with MXFP4 rows, so without widening the codes, 15.0), 1 x 34816 x 5120
+// 21 us (4.5 TB/s).
 constexpr int kSmallWaves = 8;
 constexpr int64_t kSmallRows = 16;
 constexpr int kSmallSplits = 8;
@@ -245,15 +246,16 @@ __global__ __launch_bounds__(64 * kSmallWaves) void mx_small(MxArgs a) {
 // Waves W of a workgroup and splits KS of K for NB row-blocks, GQ quads and M
 // rows of X.  Four waves where the row-blocks alone fill the chip's 16 waves a
 // compute unit, so that several workgroups share one and one starts while
-// another ends (1 x 34816 x 5120: 21 us, 24 with 5 to 10 waves), else eight
-// (1 x 5120 x 5120: 5.5 us, 6.4 with four or ten), fewer where three workgroups'
-// rows of X would not fit the LDS.  K is split over workgroups where even so
+// another ends (1 x 34816 x 5120: 21 us, 24 with 5 to 10 waves; 5 x 10240 x 5120:
+// 9.6 us, 10.5 with eight), else eight (1 x 5120 x 5120: 5.5 us, 6.4 with four or
+// ten; 5 x 2560 x 10240: 7.3 us with eight, 7.8 with seven that have equal turns,
+// 9.8 with four), fewer where three workgroups' rows of X would not fit the LDS.  K is split over workgroups where even so
 // few waves run long: a join costs about 2.5 us, a wave's quad 1.25 (5 rows,
 // 700 x 17408: 6.4 us, 8.5 without).
 void plan_small(bool x4, int64_t M, int64_t NB, int64_t GQ, int* W_, int* KS_) {
   int64_t W = NB >= 640 ? 4 : 8;
   if (!x4) W = max((int64_t)1, min(W, 48 / M));
-  W = cdiv(GQ, cdiv(GQ, W));
+  W = min(W, GQ);
   int64_t KS = 1;
   const int64_t turns = cdiv(GQ, W);
   if (turns >= 4 && NB * W < 1024) KS = min(min((int64_t)kSmallSplits, turns), 4096 / (NB * W));
