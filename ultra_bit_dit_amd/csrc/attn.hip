@@ -267,22 +267,23 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
 
     const int32_t* table = a.kv.table + b * a.kv.width;
     const int64_t page_bytes = ((int64_t)D << a.kv.lp);
-    // page of the 16 tokens from t on; -1 where there are none or the entry is unusable
-    auto page_at = [&](int t) -> int {
-      if (t >= hi_max) return -1;
-      const int pg = table[t >> a.kv.lp];
-      return pg >= 0 && pg < a.kv.n_pages ? pg : -2;
+    // Entry of the 16 tokens from t on, and the page it names: -1 where there are
+    // none, -2 where it is unusable.  (Looked at when the page is needed: looked at
+    // when read, it would be waited for, and every load before it.)
+    auto entry_at = [&](int t) -> int { return table[min(t, hi_max - 1) >> a.kv.lp]; };
+    auto page_of = [&](int t, int entry) -> int {
+      return t >= hi_max ? -1 : entry >= 0 && entry < (int)a.kv.n_pages ? entry : -2;
     };
     mx_u4 kr[4][DC], vr[DT];
-    int pgv = -1, pkn = -1, pvn = -1;  // pages: of this step's values, of the next step's keys and values
+    int pgv = -1, pkn = 0, pvn = 0;  // this step's values' page, the next step's keys' and values' entries
     uint32_t kb = 0, vb = 0;           // exponent bytes of the lane's keys and values
     auto next_pages = [&](int u) {
-      pkn = page_at(u * kUnit + 16 * (n >> 2));
-      pvn = page_at(u * kUnit + 16 * g);
+      pkn = entry_at(u * kUnit + 16 * (n >> 2));
+      pvn = entry_at(u * kUnit + 16 * g);
     };
     auto load_k = [&](int u) {
       const int tk = u * kUnit + 16 * (n >> 2);
-      const int64_t ph = (int64_t)(pkn < 0 ? 0 : pkn) * a.kv.H + h;
+      const int64_t ph = (int64_t)max(page_of(tk, pkn), 0) * a.kv.H + h;
       const uint8_t* kp = a.kv.kc + ph * page_bytes + (int64_t)((tk & (P - 1)) + (n & 3)) * D + 16 * g;
       kb = a.kv.ks[ph];
 #pragma unroll
@@ -290,10 +291,10 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
 #pragma unroll
         for (int d = 0; d < DC; d++) kr[t][d] = *(const mx_u4*)(kp + 4 * t * D + 64 * d);
     };
-    auto load_v = [&](int u, int pg) {
+    auto load_v = [&](int u, int entry) {
       const int tv = u * kUnit + 16 * g;
-      pgv = pg;
-      const int64_t ph = (int64_t)(pg < 0 ? 0 : pg) * a.kv.H + h;
+      pgv = page_of(tv, entry);
+      const int64_t ph = (int64_t)max(pgv, 0) * a.kv.H + h;
       const uint8_t* vp = a.kv.vc + ph * page_bytes + (int64_t)n * P + (tv & (P - 1));
       vb = a.kv.vs[ph];
 #pragma unroll
@@ -302,7 +303,7 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
 
     // Loads in flight at any time: the next keys behind the scores of this step,
     // the next values behind its second product; page numbers a step earlier.
-    int u = u0 + wave, pvu = -1;
+    int u = u0 + wave, pvu = 0;
     if (u < u1) {
       next_pages(u);
       pvu = pvn;
@@ -728,11 +729,11 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attn_prompt(AttnArgs a) {
   // Page of the 16 tokens that the lane stages from: tokens 64 u + 16 x .. with
   // x = row / 4 of the keys' operand, x = group of the values'.
   const int stage_group = keys ? (lane >> 2) & 3 : g;
-  auto pages = [&](int u) -> int {
-    const int t = u * kUnit + 16 * stage_group;
-    if (t >= hi_max) return -1;
-    const int pg = table[t >> a.kv.lp];
-    return pg >= 0 && pg < a.kv.n_pages ? pg : -2;
+  // their table entry, and the page it names: -1 where there are none, -2 where it
+  // is unusable (looked at a step later: looked at when read, it would be waited for)
+  auto entry_at = [&](int u) -> int { return table[min(u * kUnit + 16 * stage_group, hi_max - 1) >> a.kv.lp]; };
+  auto page_of = [&](int u, int entry) -> int {
+    return u * kUnit + 16 * stage_group >= hi_max ? -1 : entry >= 0 && entry < (int)a.kv.n_pages ? entry : -2;
   };
   // This thread's 16-byte pieces of a step: of the keys for the first half of
   // the waves (wave t: the rows of tile t, piece i: dims 64 i + 16 g ..), of the
@@ -840,7 +841,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attn_prompt(AttnArgs a) {
     const uint8_t* buf = v_[(u - u0) & 1];
     if (nan_at_[u & 3] == u) {
       // rare: a NaN code among tokens that not every row of the workgroup sees
-      const int T = u * kUnit, vp = __shfl(pages(u), keys ? 4 * g : lane);
+      const int T = u * kUnit, vp = __shfl(page_of(u, entry_at(u)), keys ? 4 * g : lane);
       const uint8_t* vc = a.kv.vc + (((int64_t)(vp < 0 ? 0 : vp) * a.kv.H + h) << sh) + ((T + 16 * g) & (P - 1));
 #pragma unroll 1
       for (int d = 0; d < DT; d++) {
@@ -934,7 +935,8 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attn_prompt(AttnArgs a) {
   // buffer's last reader is a phase before.
   if (tid < 4) nan_at_[tid] = -1;
   __syncthreads();
-  int pg0 = u0 < u1 ? pages(u0) : -1, pg1 = u0 + 1 < u1 ? pages(u0 + 1) : -1;
+  const int e0 = u0 < u1 ? entry_at(u0) : -1, e1 = u0 + 1 < u1 ? entry_at(u0 + 1) : -1;
+  int pg0 = page_of(u0, e0), pg1 = page_of(u0 + 1, e1);
   if (u0 < u1) {
     fetch(u0, pg0);
     stage(u0, pg0);
@@ -943,7 +945,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attn_prompt(AttnArgs a) {
   if (!keys) meet();
   for (int u = u0; u <= u1; u++) {
     const bool more = u + 1 < u1;
-    const int pg2 = u + 2 < u1 ? pages(u + 2) : -1;
+    const int e2 = u + 2 < u1 ? entry_at(u + 2) : -1;
     if (more) fetch(u + 1, pg1);
     if (u < u1 && sees(u)) scores(u);
     if (u > u0 && sees(u - 1)) weigh(u - 1);
@@ -951,7 +953,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attn_prompt(AttnArgs a) {
     if (u < u1 && sees(u)) softmax(u, pg0);
     if (more) stage(u + 1, pg1);
     pg0 = pg1;
-    pg1 = pg2;
+    pg1 = page_of(u + 2, e2);
     if (keys || u < u1) meet();
   }
 #pragma unroll
@@ -1077,11 +1079,11 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void attn_prompt32(AttnArgs a) {
   // keys the two halves of one.
   const int w4 = wave & (WAVES / 2 - 1), tile = w4 & 1;
   const int stage_group = 2 * tile + (keys ? (lane >> 2) & 1 : hf);  // of 16 tokens
-  auto pages = [&](int u) -> int {
-    const int t = u * kUnit + 16 * stage_group;
-    if (t >= hi_max) return -1;
-    const int pg = table[t >> a.kv.lp];
-    return pg >= 0 && pg < a.kv.n_pages ? pg : -2;
+  // their table entry, and the page it names: -1 where there are none, -2 where it
+  // is unusable (looked at a step later: looked at when read, it would be waited for)
+  auto entry_at = [&](int u) -> int { return table[min(u * kUnit + 16 * stage_group, hi_max - 1) >> a.kv.lp]; };
+  auto page_of = [&](int u, int entry) -> int {
+    return u * kUnit + 16 * stage_group >= hi_max ? -1 : entry >= 0 && entry < (int)a.kv.n_pages ? entry : -2;
   };
   mx_u4 raw[SP];
   uint32_t eb = 0;
@@ -1296,7 +1298,8 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void attn_prompt32(AttnArgs a) {
   // the phases of attn_prompt
   if (tid < 4) nan_at_[tid] = bad_at_[tid] = -1;
   __syncthreads();
-  int pg0 = u0 < u1 ? pages(u0) : -1, pg1 = u0 + 1 < u1 ? pages(u0 + 1) : -1;
+  const int e0 = u0 < u1 ? entry_at(u0) : -1, e1 = u0 + 1 < u1 ? entry_at(u0 + 1) : -1;
+  int pg0 = page_of(u0, e0), pg1 = page_of(u0 + 1, e1);
   if (u0 < u1) fetch(u0, pg0);
   // the maximum and the mask's -infinity want a positive scale
   const uint32_t flip = a.scale2 < 0.f ? 0x80008000u : 0u, keep = none ? 0x80008000u : ~0u;
@@ -1310,7 +1313,7 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void attn_prompt32(AttnArgs a) {
   if (!keys) meet();
   for (int u = u0; u <= u1; u++) {
     const bool more = u + 1 < u1;
-    const int pg2 = u + 2 < u1 ? pages(u + 2) : -1;
+    const int e2 = u + 2 < u1 ? entry_at(u + 2) : -1;
     if (more) fetch(u + 1, pg1);
     {
       const bool s_now = u < u1 && sees(u), w_now = u > u0 && sees(u - 1);
@@ -1325,7 +1328,7 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void attn_prompt32(AttnArgs a) {
     meet();
     if (u < u1 && sees(u)) softmax(u);
     if (more) stage(u + 1, pg1);
-    pg1 = pg2;
+    pg1 = page_of(u + 2, e2);
     if (keys || u < u1) meet();
   }
   if (a.parts > 1) {

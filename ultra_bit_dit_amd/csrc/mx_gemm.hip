@@ -499,11 +499,13 @@ __global__ __launch_bounds__(64 * WN * WM) void mx_gemm4(MxArgs a) {
 // X bf16.  WN x WM waves, each JN row-blocks of W by IM of X.  RING 2: two
 // group buffers, the next group's copies in flight while one is multiplied
 // (large tiles: 2048 cycles of MFMA per SIMD, longer than a copy takes).  RING
-// 4: copies three groups ahead, for tiles that are multiplied faster than that.  A row of X is 256 bytes
-// of a group; its 16-byte chunk c lies at place c ^ (row % 16), so that the 16
-// rows of an operand read fall on different banks.  Chunks past K come from a
-// block of zeros: the codes there are 0, but 0 times what follows a row of X
-// need not be.
+// 4: copies three groups ahead, for tiles that are multiplied faster than that.
+// A row of X is 256 bytes of a group; its 16-byte chunk c lies at place
+// c ^ (row % 16), so that the 16 rows of an operand read fall on different banks
+// in pairs (places that keep all apart: the same time).  Chunks past K come
+// from a block of zeros: the codes there are 0, but 0 times what follows a row
+// of X need not be.  509 x 15360 x 5120 64 us (1.25 PFLOP/s, the rate of a large
+// bf16 product), 4096 x 5120 x 5120 191 us.
 template <int WN, int WM, int JN, int IM, int RING, int YK>
 __global__ __launch_bounds__(64 * WN * WM) void mx_gemm16(MxArgs a) {
 #if defined(__HIP_DEVICE_COMPILE__)
