@@ -312,12 +312,13 @@ def test_unreadable_pages_and_nan_in_chunks(T, D):
 
 @pytest.mark.parametrize("D,P", [(64, 16), (128, 32), (256, 64)])
 @pytest.mark.parametrize("causal,window", [(True, 0), (True, 130), (False, 0)])
-def test_up_to_32_rows_behind_a_wide_table(D, P, causal, window):
-    """17 to 32 rows a head in calls whose bound on the length is large; table
+@pytest.mark.parametrize("G", [1, 3, 6])
+def test_up_to_32_rows_behind_a_wide_table(D, P, causal, window, G):
+    """5, 15 and 30 rows a head in calls whose bound on the length is large; table
     entries behind a sequence's pages are anything.  A NaN value in the last
     tokens reaches the rows that see it."""
-    lens, new, H, G = [700, 131, 9, 64], [5, 4, 5, 1], 2, 6
-    print(f"wide table D={D} P={P} causal={causal} window={window}", flush=True)
+    lens, new, H = [700, 131, 9, 64], [5, 4, 5, 1], 2
+    print(f"wide table D={D} P={P} G={G} causal={causal} window={window}", flush=True)
     c = Cache(lens, P, H, D, seed=52)
     fill(c, lens, 53)
     wide = torch.full((len(lens), 40000 // P), -77, dtype=torch.int32, device="cuda")
@@ -342,10 +343,11 @@ def test_up_to_32_rows_behind_a_wide_table(D, P, causal, window):
     assert torch.equal(torch.where(want, O, O2), O) and torch.equal(lse, lse2)
 
 
-def test_one_tile_in_very_many_shares():
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_one_tile_in_very_many_shares(D):
     """One key head and a context that more than 64 workgroups share: joined in groups of many."""
-    T, P, D = 40000, 64, 64
-    print("one tile, many shares", flush=True)
+    T, P = 70000, 64
+    print(f"one tile, many shares D={D}", flush=True)
     c = Cache([T], P, 1, D, seed=22)
     fill(c, [T], 23)
     attend(c, [T], [1], 2, 24)

@@ -17,6 +17,8 @@
 // statistics, sums and O stay in fp32.
 #include <hip/hip_runtime.h>
 
+#include <cmath>
+
 #include "kv8.hpp"
 
 namespace lowbit {
@@ -994,11 +996,13 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attn_prompt(AttnArgs a) {
 // times' sum, with 16 x 16 x 32 products 1 / 1.66).  Row 8 x + 4 h + j of a tile
 // of 32 tokens is token 16 h + 4 x + j, so that lane half h holds 16
 // consecutive tokens.  2 prompts of 4096 in 4096 tokens, 40 heads over 8, all
-// pairs: D = 128 801 -> 753 us; what bounds it is the clock that products of
-// such data leave (with the reads of LDS or the weights' exponentials taken out
-// it takes 97% of the time).  D = 64, causal: 342 us with 16 x 16 products, 315 us
-// with 8 waves, 266 us with 4 waves and three workgroups a compute unit (the
-// exponentials bound it, and more waves hide their latency).
+// pairs: D = 128 801 -> 753 us.  4096 rows over 8192 tokens take 1453 us (0.95
+// PFLOP/s) and 1212 us where all codes are 0, so power bounds much of it;
+// products that begin with their operands read ahead across the phases took the
+// same time, and weights without their exponentials 98%.  D = 64, causal: 342 us
+// with 16 x 16 products, 315 us with 8 waves, 266 us with 4 waves and three
+// workgroups a compute unit (the exponentials bound it, and more waves hide
+// their latency).
 template <int D, int NC, int WAVES, int OCC>
 __global__ __launch_bounds__(64 * WAVES, OCC) void attn_prompt32(AttnArgs a) {
   constexpr int DS = D / 16, DT = D / 32, HALF = 32 * WAVES, SP = 4 * D / HALF, PS = WAVES / 4;
@@ -1451,17 +1455,25 @@ struct Plan {
 
 // Few rows or many.  A wave of attn_decode has 16 rows (32 for D = 64 and 128, in
 // twice the registers) and every tile reads the cache again; attn_prompt reads
-// it once for all rows but widens it for 128 or 256 of them and joins by another
-// launch.  us, attn_decode / attn_prompt, 32 heads over 8 (D = 256: 24 over 4):
-//   D = 128, 40 rows, 1 x 4096 29 / 21, 1 x 32768 66 / 44, 64 x 600 72 / 49
-//   D = 128, 20 rows, 1 x 4096 23 / 21, 16 x 2048 43 / 36, 1 x 32768 49 / 42,
-//            64 x 600 41 / 48, 64 x 2048 76 / 113, 1 x 131071 91 / 112
-//   D = 128, 16 rows, 1 x 4096 19 / 21, 16 x 2048 25 / 36
-//   D = 64,  80 rows, 16 x 2048 35 / 29; 40 rows 25 / 25; 20 rows 20 / 22
-//   D = 256, 18 rows, 1 x 8192 30 / 27, 16 x 2048 36 / 28, 64 x 2048 95 / 70
+// it once for all rows, but widens it for 128 or 256 of them and joins its parts
+// by another launch.  So the choice goes by the rows of a head and the steps of
+// all heads.  us, attn_decode / attn_prompt, 32 heads over 8 (D = 256: 24 over 4):
+//   D = 64   4 rows, 1 x 1024 9.4 / 10.3; 16 rows 11.1 / 10.9, 1 x 4096 13.9 / 14.6
+//            20 rows, 1 x 4096 17.4 / 14.6, 16 x 2048 19.4 / 20.8
+//            40 rows, 1 x 4096 19.6 / 14.9, 64 x 2048 53 / 58; 80 rows, 16 x 2048 35 / 29
+//   D = 128  8 rows, 1 x 4096 15.6 / 16.3; 16 rows, 1 x 1024 14.6 / 12.3,
+//            1 x 8192 20.2 / 20.1, 16 x 2048 24 / 35
+//            20 rows, 1 x 4096 23 / 16, 16 x 2048 43 / 36, 64 x 600 40 / 47, 64 x 2048 64 / 109
+//            40 rows, 1 x 32768 66 / 44, 64 x 600 72 / 49
+//   D = 256  6 rows, 1 x 1024 16.4 / 13.9, 8 x 1024 16.8 / 14.8, 32 x 1024 24 / 28, 1 x 16384 22 / 32
+//            18 rows, 1 x 1024 21 / 14, 64 x 2048 93 / 66
 bool many_rows(const KvArgs& kv, int64_t R) {
-  if (kv.D == 128 && R > 16 && kv.n_seqs * kv.H * cdiv(kv.max_kv, kUnit) <= 4096) return true;
-  return R > (kv.D == 256 ? 16 : 32);
+  constexpr int64_t kAny = INT64_MAX;
+  int64_t most;  // steps up to which attn_prompt is the faster one
+  if (kv.D == 64) most = R <= 16 ? 0 : R <= 64 ? 2048 : kAny;
+  else if (kv.D == 128) most = R <= 8 ? 0 : R <= 16 ? 1024 : R <= 32 ? 4096 : kAny;
+  else most = R <= 16 ? 512 : kAny;
+  return kv.n_seqs * kv.H * cdiv(kv.max_kv, kUnit) <= most;
 }
 // rows of a workgroup, workgroups that the chip holds at once
 constexpr int prompt_rows(int D) { return D == 128 ? 256 : 128; }
@@ -1475,9 +1487,12 @@ Plan plan_attention(const KvArgs& kv, int64_t G, int64_t window) {
   if (many_rows(kv, R)) {
     p.nc = 0;
     p.blocks = min(kv.n_seqs * kv.H * cdiv(R, rows), kv.H * (kv.total_q * G / rows + kv.n_seqs));
-    // a part has eight steps or more: the join costs what some four take
+    // A step takes some 1.5 us, a part more to join 0.4: twice the root of the steps
+    // is best (40 tokens of 32 heads over 8, D = 128, in 4096 tokens: 27 us in 32
+    // parts, 22 in 16, 26 in 8; in 1024 tokens 16 us in 8, 19 in 4, 25 in 2).
     const int64_t most = window > 0 ? min((int64_t)kv.max_kv, window + rows / G + 2) : kv.max_kv;
-    p.parts = (int)max(min(slots / p.blocks, most / (8 * kUnit)), (int64_t)1);
+    const int64_t best = (int64_t)(2.0 * sqrt((double)cdiv(most, kUnit)));
+    p.parts = (int)max(min(slots / p.blocks, best), (int64_t)1);
     return p;
   }
   p.nc = R > 16 && kv.D <= 128 ? 2 : 1;  // wider heads: the registers of 16 rows
