@@ -1449,40 +1449,46 @@ __global__ __launch_bounds__(256) void attn_join(AttnArgs a) {
 
 struct Plan {
   int nc;             // column tiles of a decode tile; 0: attn_prompt
-  int parts;          // of a prompt tile's steps
+  int rows;           // of a prompt tile
+  int parts;          // of its steps
   int64_t blocks;
 };
 
-// Few rows or many.  A wave of attn_decode has 16 rows (32 for D = 64 and 128, in
-// twice the registers) and every tile reads the cache again; attn_prompt reads
-// it once for all rows, but widens it for 128 or 256 of them and joins its parts
-// by another launch.  So the choice goes by the rows of a head and the steps of
-// all heads.  us, attn_decode / attn_prompt, 32 heads over 8 (D = 256: 24 over 4):
+// Few rows or many.  A wave of attn_decode has 16 rows (32 for D = 64, in twice
+// the registers) and every tile reads the cache again; attn_prompt reads it once
+// for all rows, but widens it for 128 or 256 of them and joins its parts by
+// another launch.  So the choice goes by the rows of a head and the steps of all
+// heads.  us, attn_decode / attn_prompt, 32 heads over 8 (D = 256: 24 over 4):
 //   D = 64   4 rows, 1 x 1024 9.4 / 10.3; 16 rows 11.1 / 10.9, 1 x 4096 13.9 / 14.6
 //            20 rows, 1 x 4096 17.4 / 14.6, 16 x 2048 19.4 / 20.8
-//            40 rows, 1 x 4096 19.6 / 14.9, 64 x 2048 53 / 58; 80 rows, 16 x 2048 35 / 29
-//   D = 128  8 rows, 1 x 4096 15.6 / 16.3; 16 rows, 1 x 1024 14.6 / 12.3,
-//            1 x 8192 20.2 / 20.1, 16 x 2048 24 / 35
-//            20 rows, 1 x 4096 23 / 16, 16 x 2048 43 / 36, 64 x 600 40 / 47, 64 x 2048 64 / 109
-//            40 rows, 1 x 32768 66 / 44, 64 x 600 72 / 49
+//            40 rows, 1 x 4096 19.6 / 14.9, 64 x 2048 53 / 58, 1 x 32768 26 / 41
+//            80 rows, 16 x 2048 35 / 29
+//   D = 128  8 rows, 1 x 1024 12.7 / 12.2, 1 x 4096 15.6 / 16.6, 8 x 1000 13.2 / 14.1
+//            16 rows, 1 x 1024 14.8 / 12.2, 1 x 8192 20.5 / 20.8, 16 x 2048 24 / 26
+//            20 rows (of 32 a wave), 1 x 4096 23 / 16, 64 x 2048 65 / 64, 1 x 131071 80 / 86
+//            40 rows, 1 x 32768 62 / 47, 64 x 2048 115 / 74
 //   D = 256  6 rows, 1 x 1024 16.4 / 13.9, 8 x 1024 16.8 / 14.8, 32 x 1024 24 / 28, 1 x 16384 22 / 32
 //            18 rows, 1 x 1024 21 / 14, 64 x 2048 93 / 66
 bool many_rows(const KvArgs& kv, int64_t R) {
   constexpr int64_t kAny = INT64_MAX;
   int64_t most;  // steps up to which attn_prompt is the faster one
   if (kv.D == 64) most = R <= 16 ? 0 : R <= 64 ? 2048 : kAny;
-  else if (kv.D == 128) most = R <= 8 ? 0 : R <= 16 ? 1024 : R <= 32 ? 4096 : kAny;
+  else if (kv.D == 128) most = R <= 8 ? 0 : R <= 16 ? 1024 : kAny;
   else most = R <= 16 ? 512 : kAny;
   return kv.n_seqs * kv.H * cdiv(kv.max_kv, kUnit) <= most;
 }
-// rows of a workgroup, workgroups that the chip holds at once
-constexpr int prompt_rows(int D) { return D == 128 ? 256 : 128; }
-constexpr int prompt_slots(int D) { return D == 64 ? 768 : 256; }
+// Rows of a workgroup, and workgroups that the chip holds at once.  D = 128: 256
+// rows, 128 where no sequence has more (two workgroups a compute unit, fewer idle
+// waves; 2 x 4096 in 4096, 40 heads over 8, 411 us with 128 rows and 376 with 256,
+// 16 x 64 in 1024 50 and 42, 16 x 5 in 2048, 32 heads, 26 and 35).
+int prompt_rows(int D, int64_t R) { return D == 128 && R > 128 ? 256 : 128; }
+int prompt_slots(int D, int64_t R) { return D == 64 ? 768 : D == 128 && R <= 128 ? 512 : 256; }
 
 // window: 0 where rows see everything before them or more
 Plan plan_attention(const KvArgs& kv, int64_t G, int64_t window) {
   Plan p;
-  const int64_t R = kv.max_q * G, rows = prompt_rows(kv.D), slots = prompt_slots(kv.D);
+  const int64_t R = kv.max_q * G, rows = prompt_rows(kv.D, R), slots = prompt_slots(kv.D, R);
+  p.rows = (int)rows;
   p.parts = 1;
   if (many_rows(kv, R)) {
     p.nc = 0;
@@ -1495,7 +1501,7 @@ Plan plan_attention(const KvArgs& kv, int64_t G, int64_t window) {
     p.parts = (int)max(min(slots / p.blocks, best), (int64_t)1);
     return p;
   }
-  p.nc = R > 16 && kv.D <= 128 ? 2 : 1;  // wider heads: the registers of 16 rows
+  p.nc = R > 16 && kv.D == 64 ? 2 : 1;  // wider heads: the registers of 16 rows
   p.blocks = kv.D == 256 ? kMaxShares / 2 : kMaxShares;  // what the chip holds at once
   return p;
 }
@@ -1508,7 +1514,7 @@ size_t attention_workspace_bytes(const KvArgs& kv, int64_t G) {
   const Plan p = plan_attention(kv, G, 0);  // a window takes no more
   if (p.nc > 0) return (size_t)kCounterBytes + (size_t)4 * kMaxShares * 16 * p.nc * (kv.D + 2) * 4;
   if (p.parts == 1) return 0;
-  return (size_t)kCounterBytes + (size_t)(p.blocks * p.parts * prompt_rows(kv.D)) * (kv.D + kPartPad) * 4;
+  return (size_t)kCounterBytes + (size_t)(p.blocks * p.parts * p.rows) * (kv.D + kPartPad) * 4;
 }
 
 hipError_t launch_attention(AttnArgs a, void* ws, hipStream_t s) {
@@ -1519,25 +1525,23 @@ hipError_t launch_attention(AttnArgs a, void* ws, hipStream_t s) {
   const dim3 grid((unsigned)(p.blocks * p.parts));
   if (p.nc == 0) {
     if (a.kv.D == 64) hipLaunchKernelGGL((attn_prompt32<64, 1, 4, 3>), grid, dim3(256), 0, s, a);
+    else if (a.kv.D == 128 && p.rows == 128) hipLaunchKernelGGL((attn_prompt32<128, 1, 4, 2>), grid, dim3(256), 0, s, a);
     else if (a.kv.D == 128) hipLaunchKernelGGL((attn_prompt32<128, 1, 8, 2>), grid, dim3(512), 0, s, a);
     else hipLaunchKernelGGL((attn_prompt<256, 1, 8>), grid, dim3(512), 0, s, a);
     if (p.parts == 1) return hipGetLastError();
-    const dim3 join((unsigned)p.blocks, (unsigned)(prompt_rows(a.kv.D) * a.kv.D / 4 / 256));
-    if (a.kv.D == 64) hipLaunchKernelGGL((attn_join<64, prompt_rows(64)>), join, dim3(256), 0, s, a);
-    else if (a.kv.D == 128) hipLaunchKernelGGL((attn_join<128, prompt_rows(128)>), join, dim3(256), 0, s, a);
-    else hipLaunchKernelGGL((attn_join<256, prompt_rows(256)>), join, dim3(256), 0, s, a);
+    const dim3 join((unsigned)p.blocks, (unsigned)(p.rows * a.kv.D / 4 / 256));
+    if (a.kv.D == 64) hipLaunchKernelGGL((attn_join<64, 128>), join, dim3(256), 0, s, a);
+    else if (a.kv.D == 128 && p.rows == 128) hipLaunchKernelGGL((attn_join<128, 128>), join, dim3(256), 0, s, a);
+    else if (a.kv.D == 128) hipLaunchKernelGGL((attn_join<128, 256>), join, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((attn_join<256, 128>), join, dim3(256), 0, s, a);
     return hipGetLastError();
   }
 #define LOWBIT_DEC(DD, NN) \
   hipLaunchKernelGGL((attn_decode<DD, NN>), grid, dim3(64 * kDecWaves), 0, s, a)
-  if (p.nc == 1) {
-    if (a.kv.D == 64) LOWBIT_DEC(64, 1);
-    else if (a.kv.D == 128) LOWBIT_DEC(128, 1);
-    else LOWBIT_DEC(256, 1);
-  } else {
-    if (a.kv.D == 64) LOWBIT_DEC(64, 2);
-    else LOWBIT_DEC(128, 2);
-  }
+  if (a.kv.D == 64 && p.nc == 1) LOWBIT_DEC(64, 1);
+  else if (a.kv.D == 64) LOWBIT_DEC(64, 2);
+  else if (a.kv.D == 128) LOWBIT_DEC(128, 1);
+  else LOWBIT_DEC(256, 1);
 #undef LOWBIT_DEC
   return hipGetLastError();
 }
