@@ -138,6 +138,21 @@ def test_append_and_attention_refusals():
     assert L.lowbit_attention_kv8_workspace(kv(), batch(), 4, ctypes.byref(n)) == lb.OK and n.value > 0
 
 
+def test_attention_sizes_beyond_a_grid():
+    """Numbers of workgroups that 32 bits do not hold are refused, not cut."""
+    L = lb.lib()
+    n = ctypes.c_size_t(5)
+    many = dict(n_seqs=1 << 20, total_q=1 << 29, max_q=1 << 9, q_starts=0x70000)
+    for heads in (4096, 8192):
+        c, b = kv(kv_heads=4096), batch(**many)
+        assert L.lowbit_attention_kv8_workspace(c, b, heads, ctypes.byref(n)) == lb.E_SHAPE and n.value == 0
+        n.value = 5
+        row = heads * 64
+        assert L.lowbit_attention_kv8(c, b, heads, A16, row, 1.0, 1, 0, A16, row, None, None) == lb.E_SHAPE
+    b = batch(n_seqs=1, total_q=1 << 30, max_q=1 << 30, q_starts=0x70000)
+    assert L.lowbit_attention_kv8_workspace(kv(), b, 8, ctypes.byref(n)) == lb.E_SHAPE
+
+
 def test_binding_checks_tensors():
     """The binding refuses wrong shapes, types and layouts before it looks for a device."""
     x = torch.zeros(4, 64, dtype=torch.bfloat16)

@@ -603,6 +603,13 @@ int kv8_check(const lowbit_kv8* c, const lowbit_kv8_batch* b, KvArgs* out) {
   return LOWBIT_OK;
 }
 
+// query heads of a call: whole groups, rows that int counts, one grid
+bool attention_heads_ok(const KvArgs& a, int64_t q_heads) {
+  if (q_heads < 1 || q_heads > (1 << 16) || q_heads % a.H != 0) return false;
+  const int64_t G = q_heads / a.H;
+  return a.max_q * G <= (1 << 30) && attention_blocks(a, G) <= (1 << 22);
+}
+
 }  // namespace
 
 int lowbit_kv8_append(const lowbit_kv8* cache, const lowbit_kv8_batch* batch, int dtype, const void* K,
@@ -627,7 +634,7 @@ int lowbit_attention_kv8_workspace(const lowbit_kv8* cache, const lowbit_kv8_bat
   KvArgs a;
   const int rc = kv8_check(cache, batch, &a);
   if (rc) return rc;
-  if (q_heads < 1 || q_heads > (1 << 16) || q_heads % a.H != 0) return LOWBIT_E_SHAPE;
+  if (!attention_heads_ok(a, q_heads)) return LOWBIT_E_SHAPE;
   *bytes = attention_workspace_bytes(a, q_heads / a.H);
   return LOWBIT_OK;
 }
@@ -639,15 +646,12 @@ int lowbit_attention_kv8(const lowbit_kv8* cache, const lowbit_kv8_batch* batch,
   AttnArgs a;
   const int rc = kv8_check(cache, batch, &a.kv);
   if (rc) return rc;
-  if (q_heads < 1 || q_heads > (1 << 16) || q_heads % a.kv.H != 0) return LOWBIT_E_SHAPE;
+  if (!attention_heads_ok(a.kv, q_heads)) return LOWBIT_E_SHAPE;
   const int64_t row = q_heads * a.kv.D, most = int64_t(1) << 40;
   if (q_stride < row || o_stride < row || q_stride > most || o_stride > most) return LOWBIT_E_SHAPE;
   if (!(softmax_scale - softmax_scale == 0.0f)) return LOWBIT_E_UNSUPPORTED;  // infinite or NaN
   if (window < 0) return LOWBIT_E_SHAPE;
   a.G = q_heads / a.kv.H;
-  if (a.kv.max_q * a.G > (1 << 30) ||
-      attention_blocks(a.kv, a.G) > (1 << 22))
-    return LOWBIT_E_SHAPE;
   if (!aligned(Q_bf16, 16) || !aligned(O_bf16, 16) || q_stride % 8 != 0 || o_stride % 8 != 0 ||
       (lse && !aligned(lse, 4)))
     return LOWBIT_E_ALIGN;

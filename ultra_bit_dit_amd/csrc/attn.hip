@@ -17,6 +17,7 @@
 // statistics, sums and O stay in fp32.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 
 #include "kv8.hpp"
@@ -1492,13 +1493,13 @@ Plan plan_attention(const KvArgs& kv, int64_t G, int64_t window) {
   p.parts = 1;
   if (many_rows(kv, R)) {
     p.nc = 0;
-    p.blocks = min(kv.n_seqs * kv.H * cdiv(R, rows), kv.H * (kv.total_q * G / rows + kv.n_seqs));
+    p.blocks = std::min<int64_t>(kv.n_seqs * kv.H * cdiv(R, rows), kv.H * (kv.total_q * G / rows + kv.n_seqs));
     // A step takes some 1.5 us, a part more to join 0.4: twice the root of the steps
     // is best (40 tokens of 32 heads over 8, D = 128, in 4096 tokens: 27 us in 32
     // parts, 22 in 16, 26 in 8; in 1024 tokens 16 us in 8, 19 in 4, 25 in 2).
-    const int64_t most = window > 0 ? min((int64_t)kv.max_kv, window + rows / G + 2) : kv.max_kv;
+    const int64_t most = window > 0 ? std::min<int64_t>(kv.max_kv, window + rows / G + 2) : kv.max_kv;
     const int64_t best = (int64_t)(2.0 * sqrt((double)cdiv(most, kUnit)));
-    p.parts = (int)max(min(slots / p.blocks, best), (int64_t)1);
+    p.parts = (int)std::max<int64_t>(std::min(slots / p.blocks, best), 1);
     return p;
   }
   p.nc = R > 16 && kv.D == 64 ? 2 : 1;  // wider heads: the registers of 16 rows

@@ -11,6 +11,8 @@
 // (NaN) and codes 0.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+
 #include "mx.hpp"
 
 namespace lowbit {
@@ -186,7 +188,7 @@ hipError_t launch_quantize_mxfp4(int64_t rows, int64_t K, bool f32, const void* 
 hipError_t launch_pack_mxfp4(int64_t rows, int64_t K, const uint8_t* codes, const uint8_t* scales,
                              void* pcodes, void* pscales, hipStream_t s) {
   const int64_t words = cdiv(rows, 16) * mx_quads(K) * 64;
-  const int64_t blocks = min(cdiv(words, 256), (int64_t)16384);
+  const int64_t blocks = std::min<int64_t>(cdiv(words, 256), 16384);
   hipLaunchKernelGGL(pack_mxfp4, dim3((unsigned)blocks), dim3(256), 0, s, rows, K, words, codes, scales,
                      (uint8_t*)pcodes, (uint8_t*)pscales);
   return hipGetLastError();

@@ -12,6 +12,7 @@
 // word j takes X[m][128 g + 32 q + 8 j .. + 7] from lane m + 16 q.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "mx.hpp"
@@ -249,16 +250,16 @@ __global__ __launch_bounds__(64 * kSmallWaves) void mx_small(MxArgs a) {
 // another ends (1 x 34816 x 5120: 21 us, 24 with 5 to 10 waves; 5 x 10240 x 5120:
 // 9.6 us, 10.5 with eight), else eight (1 x 5120 x 5120: 5.5 us, 6.4 with four or
 // ten; 5 x 2560 x 10240: 7.3 us with eight, 7.8 with seven that have equal turns,
-// 9.8 with four), fewer where three workgroups' rows of X would not fit the LDS.  K is split over workgroups where even so
-// few waves run long: a join costs about 2.5 us, a wave's quad 1.25 (5 rows,
-// 700 x 17408: 6.4 us, 8.5 without).
+// 9.8 with four), fewer where three workgroups' rows of X would not fit the LDS.
+// K is split over workgroups where even so few waves run long: a join costs
+// about 2.5 us, a wave's quad 1.25 (5 rows, 700 x 17408: 6.4 us, 8.5 without).
 void plan_small(bool x4, int64_t M, int64_t NB, int64_t GQ, int* W_, int* KS_) {
   int64_t W = NB >= 640 ? 4 : 8;
-  if (!x4) W = max((int64_t)1, min(W, 48 / M));
-  W = min(W, GQ);
+  if (!x4) W = std::max<int64_t>(1, std::min(W, 48 / M));
+  W = std::min(W, GQ);
   int64_t KS = 1;
   const int64_t turns = cdiv(GQ, W);
-  if (turns >= 4 && NB * W < 1024) KS = min(min((int64_t)kSmallSplits, turns), 4096 / (NB * W));
+  if (turns >= 4 && NB * W < 1024) KS = std::min({(int64_t)kSmallSplits, turns, 4096 / (NB * W)});
   *W_ = (int)W;
   *KS_ = (int)KS;
 }
@@ -266,7 +267,7 @@ void plan_small(bool x4, int64_t M, int64_t NB, int64_t GQ, int* W_, int* KS_) {
 template <bool X4>
 void launch_small(const MxArgs& a, int W, int ykind, hipStream_t s) {
   const dim3 grid((unsigned)a.NT, (unsigned)a.KS);
-  const size_t lds = (size_t)W * max((int64_t)1, X4 ? 0 : a.M) * 1024;
+  const size_t lds = (size_t)W * std::max<int64_t>(1, X4 ? 0 : a.M) * 1024;
   if (ykind == YK_F32)
     hipLaunchKernelGGL((mx_small<X4, YK_F32>), grid, dim3(64 * W), lds, s, a);
   else
@@ -700,7 +701,8 @@ constexpr Shape kBig4{16, 16}, kSmall4{8, 8}, kBig16{8, 16}, kSmall16{4, 8};
 // splits.
 struct Plan {
   bool small;
-  bool big;
+  bool big;           // the larger tile
+  bool resident;      // bf16, the smaller tile: two group buffers, three workgroups a compute unit
   int64_t MT, NT;     // small: NT row-blocks of W
   int KS, W;          // W: waves of a workgroup of few rows
   size_t part_bytes;
@@ -721,7 +723,12 @@ Plan plan_gemm(bool x4, int64_t M, int64_t N, int64_t K) {
   // measured) and its start and end; a split adds a launch and the partial
   // tiles' way to memory and back.
   double best = 0;
-  for (int big = 0; big < 2; big++) {
+  // The smaller bf16 tile also comes with two group buffers instead of four: a
+  // group takes 0.7 us alone, but three workgroups share a compute unit at 0.5 us a
+  // group each, so no round is left half empty (64 x 34816 x 5120: 41 us, 49 with
+  // four buffers; 256 x 34816 x 5120: 100 and 121; 64 x 5120 x 17408: 32 and 26).
+  for (int v = 0; v < (x4 ? 2 : 3); v++) {
+    const bool big = v == 1, resident = v == 2;
     const Shape sh = x4 ? (big ? kBig4 : kSmall4) : (big ? kBig16 : kSmall16);
     const int64_t MT = cdiv(MB, sh.rm), NT = cdiv(NB, sh.rn), T = MT * NT;
     const int per_cu = x4 && !big ? 2 : 1;
@@ -729,12 +736,20 @@ Plan plan_gemm(bool x4, int64_t M, int64_t N, int64_t K) {
     for (int KS = 1; KS <= 16; KS *= 2) {
       if (KS > 1 && (GQ < 2 * KS || T * KS > 1024)) break;
       const double load = (double)(T * KS) / 256, groups = (double)cdiv(GQ, KS) * 4;
-      const double rounds = load <= per_cu ? 1.0 : (double)cdiv(T * KS, 256 * per_cu);
-      const double group = load <= 1 ? idle + (busy - idle) * load * (per_cu == 1 ? 1.0 : 0.5) : busy;
-      const double c = rounds * (groups * group + 2.5) + (KS > 1 ? 3.0 + (double)(T * KS) * sh.rm * sh.rn * 2048e-6 / 4.0 : 0.0);
+      const double split = KS > 1 ? 3.0 + (double)(T * KS) * sh.rm * sh.rn * 2048e-6 / 4.0 : 0.0;
+      double c;
+      if (resident) {
+        const double group = 0.5 * (double)cdiv(T * KS, 256);
+        c = groups * (group < 0.7 ? 0.7 : group) + 3.0 + split;
+      } else {
+        const double rounds = load <= per_cu ? 1.0 : (double)cdiv(T * KS, 256 * per_cu);
+        const double group = load <= 1 ? idle + (busy - idle) * load * (per_cu == 1 ? 1.0 : 0.5) : busy;
+        c = rounds * (groups * group + 2.5) + split;
+      }
       if (best == 0 || c < best) {
         best = c;
         p.big = big;
+        p.resident = resident;
         p.MT = MT;
         p.NT = NT;
         p.KS = KS;
@@ -805,6 +820,7 @@ hipError_t launch_gemm_mxfp4(const MxGemmArgs& g, hipStream_t s) {
     else launch_tile4<2, 2, 4, 4>(a, g.ykind, s);
   } else {
     if (p.big) launch_tile16<4, 2, 4, 4, 2>(a, g.ykind, s);
+    else if (p.resident) launch_tile16<4, 2, 2, 2, 2>(a, g.ykind, s);
     else launch_tile16<4, 2, 2, 2, 4>(a, g.ykind, s);
   }
   return hipGetLastError();
