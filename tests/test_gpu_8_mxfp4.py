@@ -115,6 +115,17 @@ def test_product(M, N, K, x4):
         assert torch.equal(y, y2), "two runs differ"
 
 
+@pytest.mark.parametrize("K", [96, 672])
+def test_product_of_more_tiles_than_compute_units(K):
+    """Tiles of 64 rows that share compute units."""
+    M, N = 50, 34800
+    print(f"product {M}x{N}x{K}", flush=True)
+    wc, ws, x, _, wv, xv = product_case(M, N, K, 21, False)
+    for yd in (lb.F32, lb.BF16):
+        y = lb.gemm_mxfp4(M, N, K, wc, ws, x, y_dtype=yd)
+        check_product(y, wv, xv, K, yd == lb.BF16, f"y {yd}")
+
+
 @pytest.mark.parametrize("M", [1, 7, 80, 300])
 def test_product_strided_x(M):
     """Rows of X inside a wider matrix whose other elements are NaN; K ends inside a group."""
