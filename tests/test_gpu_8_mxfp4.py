@@ -180,6 +180,26 @@ def test_product_layer_shape_sampled(M, x4):
     check_product(y[:, at], f64(wv[at]), xv, K, False, f"layer M={M}")
 
 
+@pytest.mark.parametrize("M,N,K,x4", [(2001, 4003, 672, False), (900, 2200, 6176, False), (4001, 4003, 672, True),
+                                      (392, 4290, 16000, True)])
+def test_product_of_large_tiles_sampled(M, N, K, x4):
+    """Sizes with odd ends that take the large tiles, whole K and split; sampled columns against 64 bits."""
+    print(f"large tiles M={M} N={N} K={K} x4={x4}", flush=True)
+    g = torch.Generator(device="cuda").manual_seed(M + N)
+    wc, ws, wv = lb.quantize_mxfp4(torch.randn(N, K, device="cuda", generator=g) * 0.02, values=True)
+    x = torch.randn(M, K, device="cuda", generator=g).bfloat16()
+    xa, xs, xv = x, None, f64(x)
+    if x4:
+        xa, xs, xv = lb.quantize_mxfp4(x, values=True)
+        xv = f64(xv)
+    cols = np.unique(np.r_[0:33, np.random.default_rng(3).choice(N, 60, replace=False), N - 40:N])
+    at = torch.from_numpy(cols).cuda()
+    for yd in (lb.F32, lb.BF16):
+        y = lb.gemm_mxfp4(M, N, K, wc, ws, xa, x_scales=xs, y_dtype=yd)
+        check_product(y[:, at], f64(wv[at]), xv, K, yd == lb.BF16, f"large tiles M={M}")
+        assert bool(torch.isfinite(y.float()).all())
+
+
 def test_stream_and_graph():
     """Quantizing and multiplying on another stream, then captured and replayed
     on new inputs with other work between the replays."""

@@ -117,6 +117,11 @@ def test_append_prompt_then_tokens(P, D, H, dtype):
         c.check(f"token {step} again")
 
 
+@pytest.mark.parametrize("P,D", [(16, 128), (64, 128), (128, 128), (32, 256), (128, 256)])
+def test_append_fp32_wide_heads(P, D):
+    test_append_prompt_then_tokens(P, D, 2, torch.float32)
+
+
 def test_append_strided_empty_and_special():
     """Keys and values inside a fused projection's output; a sequence without new
     tokens, one of length 0; zeros, subnormals, infinities, NaN."""
