@@ -646,6 +646,22 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
 // A part's results lie in rows of kPartPad floats more than D: sums of O
 // (before the division), maximum (of base 2), sum of weights.
 constexpr int kPartPad = 4;
+// Parts of a tile of `steps` steps: at most the launch's, which knows only a
+// bound on the length.  A step takes some 1.5 us, a part more to join 0.4: twice
+// the root of the steps is best (40 tokens of 32 heads over 8, D = 128, in 4096
+// tokens: 27 us in 32 parts, 22 in 16, 26 in 8; in 1024 16 us in 8, 19 in 4, 25
+// in 2; in 1000 with a bound of 131072 36 us without this limit).
+__device__ __forceinline__ int parts_of(int steps, int most) {
+  return max(1, min((int)(2.f * __builtin_amdgcn_sqrtf((float)steps)), most));
+}
+// steps [u0, u1) that rows [r0, r1) of a sequence see some token of
+__device__ __forceinline__ void steps_of_rows(const AttnArgs& a, const SeqSpan& s, int r0, int r1, int* u0, int* u1) {
+  const int first = s.len - s.n, p0 = first + (int)((uint32_t)r0 / (uint32_t)a.G);
+  const int p1 = first + (int)((uint32_t)(r1 - 1) / (uint32_t)a.G);
+  const int hi = a.causal ? max(0, min(s.len, p1 + 1)) : s.len, lo = a.window > 0 ? max(0, p0 - a.window + 1) : 0;
+  *u0 = lo / kUnit;
+  *u1 = (hi + kUnit - 1) / kUnit;
+}
 // steps [u0, u1) of part k of n
 __device__ __forceinline__ void part_steps(int k, int n, int* u0, int* u1) {
   const int each = (*u1 - *u0) / n, more = (*u1 - *u0) - each * n;
@@ -726,8 +742,11 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attn_prompt(AttnArgs a) {
     for (int d = 0; d < DT; d++) o[c][d] = v4f{0.f, 0.f, 0.f, 0.f};
   }
 
-  int u0 = lo_min / kUnit, u1 = (hi_max + kUnit - 1) / kUnit;
-  part_steps(part, a.parts, &u0, &u1);
+  int u0, u1;
+  steps_of_rows(a, s, wg0, min(wg0 + ROWS, R), &u0, &u1);
+  const int parts = parts_of(u1 - u0, a.parts);
+  if (part >= parts) return;
+  part_steps(part, parts, &u0, &u1);
   const int32_t* table = a.kv.table + b * a.kv.width;
   // Page of the 16 tokens that the lane stages from: tokens 64 u + 16 x .. with
   // x = row / 4 of the keys' operand, x = group of the values'.
@@ -969,7 +988,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attn_prompt(AttnArgs a) {
 #pragma unroll
       for (int e = 0; e < 4; e++)
         if ((nanned[c] >> (4 * d + e)) & 1) o[c][d][e] = __uint_as_float(0x7FC00000u);
-    if (a.parts > 1) {
+    if (parts > 1) {
       float* pp = a.part + ((int64_t)blockIdx.x * ROWS + (rho[c] - wg0)) * (D + kPartPad);
 #pragma unroll
       for (int d = 0; d < DT; d++) *(v4f*)(pp + 16 * d + 4 * g) = o[c][d];
@@ -1074,8 +1093,11 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void attn_prompt32(AttnArgs a) {
       for (int e = 0; e < 16; e++) o[c][d][e] = 0.f;
   }
 
-  int u0 = lo_min / kUnit, u1 = (hi_max + kUnit - 1) / kUnit;
-  part_steps(part, a.parts, &u0, &u1);
+  int u0, u1;
+  steps_of_rows(a, s, wg0, min(wg0 + ROWS, R), &u0, &u1);
+  const int parts = parts_of(u1 - u0, a.parts);
+  if (part >= parts) return;
+  part_steps(part, parts, &u0, &u1);
   const int32_t* table = a.kv.table + b * a.kv.width;
   // This thread's 16-byte pieces of a step.  Keys (first half of the waves,
   // tile w4 % 2): 16 dims 16 (2 (w4 / 2 + 2 i) + h) .. of the token of row n.
@@ -1336,7 +1358,7 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void attn_prompt32(AttnArgs a) {
     pg1 = page_of(u + 2, e2);
     if (keys || u < u1) meet();
   }
-  if (a.parts > 1) {
+  if (parts > 1) {
 #pragma unroll
     for (int c = 0; c < NC; c++) {
       l[c] += __shfl_xor(l[c], 32);
@@ -1407,17 +1429,20 @@ __global__ __launch_bounds__(256) void attn_join(AttnArgs a) {
   const SeqSpan s = seq_span(a.kv, b);
   const int R = s.n * (int)G, wg0 = (R - 1) / ROWS * ROWS - (int)item * ROWS;
   const int at = blockIdx.y * 256 + threadIdx.x, r = at / T4, d = at % T4 * 4;
-  if (wg0 + r >= R) return;
+  int u0, u1;
+  steps_of_rows(a, s, wg0, min(wg0 + ROWS, R), &u0, &u1);
+  const int parts = parts_of(u1 - u0, a.parts);
+  if (wg0 + r >= R || parts == 1) return;  // one part: its workgroup has written O
   const int64_t step = (int64_t)H * ROWS * (D + kPartPad);  // to the next part
   const float* p = a.part + (((int64_t)tile_at * a.parts * H + h) * ROWS + r) * (D + kPartPad);
   float M = -INFINITY, L = 0.f;
   v4f o = v4f{0.f, 0.f, 0.f, 0.f};
-  for (int k = 0; k < a.parts; k += AHEAD) {
+  for (int k = 0; k < parts; k += AHEAD) {
     v4f po[AHEAD];
     float2 ml[AHEAD];
 #pragma unroll
     for (int e = 0; e < AHEAD; e++) {
-      const float* q = p + min(k + e, a.parts - 1) * step;
+      const float* q = p + min(k + e, parts - 1) * step;
       po[e] = *(const v4f*)(q + d);
       ml[e] = *(const float2*)(q + D);
     }
@@ -1431,7 +1456,7 @@ __global__ __launch_bounds__(256) void attn_join(AttnArgs a) {
     for (int c = 0; c < 4; c++) o[c] *= al;
 #pragma unroll
     for (int e = 0; e < AHEAD; e++) {
-      if (k + e >= a.parts) break;
+      if (k + e >= parts) break;
       const float w = __builtin_amdgcn_exp2f(ml[e].x - mu);
       L += w * ml[e].y;
 #pragma unroll
@@ -1494,9 +1519,7 @@ Plan plan_attention(const KvArgs& kv, int64_t G, int64_t window) {
   if (many_rows(kv, R)) {
     p.nc = 0;
     p.blocks = std::min<int64_t>(kv.n_seqs * kv.H * cdiv(R, rows), kv.H * (kv.total_q * G / rows + kv.n_seqs));
-    // A step takes some 1.5 us, a part more to join 0.4: twice the root of the steps
-    // is best (40 tokens of 32 heads over 8, D = 128, in 4096 tokens: 27 us in 32
-    // parts, 22 in 16, 26 in 8; in 1024 tokens 16 us in 8, 19 in 4, 25 in 2).
+    // at most as parts_of has them
     const int64_t most = window > 0 ? std::min<int64_t>(kv.max_kv, window + rows / G + 2) : kv.max_kv;
     const int64_t best = (int64_t)(2.0 * sqrt((double)cdiv(most, kUnit)));
     p.parts = (int)std::max<int64_t>(std::min(slots / p.blocks, best), 1);
