@@ -654,20 +654,59 @@ constexpr int kPartPad = 4;
 __device__ __forceinline__ int parts_of(int steps, int most) {
   return max(1, min((int)(2.f * __builtin_amdgcn_sqrtf((float)steps)), most));
 }
-// steps [u0, u1) that rows [r0, r1) of a sequence see some token of
-__device__ __forceinline__ void steps_of_rows(const AttnArgs& a, const SeqSpan& s, int r0, int r1, int* u0, int* u1) {
-  const int first = s.len - s.n, p0 = first + (int)((uint32_t)r0 / (uint32_t)a.G);
-  const int p1 = first + (int)((uint32_t)(r1 - 1) / (uint32_t)a.G);
-  const int hi = a.causal ? max(0, min(s.len, p1 + 1)) : s.len, lo = a.window > 0 ? max(0, p0 - a.window + 1) : 0;
-  *u0 = lo / kUnit;
-  *u1 = (hi + kUnit - 1) / kUnit;
-}
 // steps [u0, u1) of part k of n
 __device__ __forceinline__ void part_steps(int k, int n, int* u0, int* u1) {
   const int each = (*u1 - *u0) / n, more = (*u1 - *u0) - each * n;
   *u0 += each * k + min(k, more);
   *u1 = *u0 + each + (k < more ? 1 : 0);
 }
+
+// tokens that some of a run of rows see, [lo, hi), and that all of them see
+struct Seen {
+  int lo, hi, lo_all, hi_all;
+};
+
+// A tile of ROWS rows of one sequence and key head.
+template <int ROWS>
+struct PromptTile {
+  int64_t b;     // sequence
+  SeqSpan s;
+  int R, wg0;    // rows of the sequence and head (less than 2^31, checked at the entry), first of the tile
+  int first;     // position of the first new token
+  Seen seen;     // by the tile
+  int u0, u1;    // steps of 64 tokens that some row sees
+  int parts;     // they are cut into
+
+  // tile number `at` of a head, all sequences in turn; false behind the last
+  template <int THREADS>
+  __device__ __forceinline__ bool find(const AttnArgs& a, uint32_t at, int64_t* mem) {
+    auto tiles = [&](int64_t i) -> int64_t { return (seq_span(a.kv, i).n * a.G + ROWS - 1) / ROWS; };
+    ItemScan<THREADS, decltype(tiles)> scan(a.kv.n_seqs, tiles, mem);
+    if (at >= scan.total) return false;
+    int64_t item;
+    scan.find(at, &b, &item);
+    s = seq_span(a.kv, b);
+    R = s.n * (int)a.G;
+    wg0 = (R - 1) / ROWS * ROWS - (int)item * ROWS;  // the last, longest tiles of a sequence first
+    first = s.len - s.n;
+    seen = of_rows(a, wg0, wg0 + ROWS);
+    u0 = seen.lo / kUnit;
+    u1 = (seen.hi + kUnit - 1) / kUnit;
+    parts = parts_of(u1 - u0, a.parts);
+    return true;
+  }
+  __device__ __forceinline__ Seen of_rows(const AttnArgs& a, int r0, int r1) const {
+    r0 = r0 < R - 1 ? r0 : R - 1;
+    r1 = r1 < R ? r1 : R;
+    const int p0 = first + (int)((uint32_t)r0 / (uint32_t)a.G), p1 = first + (int)((uint32_t)(r1 - 1) / (uint32_t)a.G);
+    Seen v;
+    v.hi = a.causal ? max(0, min(s.len, p1 + 1)) : s.len;
+    v.hi_all = a.causal ? max(0, min(s.len, p0 + 1)) : s.len;
+    v.lo = a.window > 0 ? max(0, p0 - a.window + 1) : 0;
+    v.lo_all = a.window > 0 ? max(0, p1 - a.window + 1) : 0;
+    return v;
+  }
+};
 
 template <int D, int NC, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, 2) void attn_prompt(AttnArgs a) {
@@ -678,37 +717,19 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attn_prompt(AttnArgs a) {
   const bool keys = __builtin_amdgcn_readfirstlane((int)threadIdx.x) < HALF;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n = lane & 15, g = lane >> 4;
-  // heads run fastest, so that an XCD (bid % 8) keeps few of them in its L2;
-  // the last, longest row tiles of a sequence start first
+  // heads run fastest, so that an XCD (bid % 8) keeps few of them in its L2
   constexpr int ROWS = 16 * NC * WAVES;
   const uint32_t G = (uint32_t)a.G, H = (uint32_t)a.kv.H, at_part = blockIdx.x / H, tile_at = at_part / (uint32_t)a.parts;
   const int h = (int)(blockIdx.x - at_part * H), part = (int)(at_part - tile_at * a.parts);
-  int64_t b, item;
-  auto tiles = [&](int64_t i) -> int64_t { return (seq_span(a.kv, i).n * a.G + ROWS - 1) / ROWS; };
   __shared__ int64_t scan_[WAVES + 2];
-  ItemScan<64 * WAVES, decltype(tiles)> scan(a.kv.n_seqs, tiles, scan_);
-  if (tile_at >= scan.total) return;
-  scan.find(tile_at, &b, &item);
-  const SeqSpan s = seq_span(a.kv, b);
-  // rows count to less than 2^31 (checked at the entry)
-  const int R = s.n * (int)G, wg0 = (R - 1) / ROWS * ROWS - (int)item * ROWS;
-  const int len = s.len, first = len - s.n, P = 1 << a.kv.lp;
-
-  // what rows [r0, r1) see between them: some of them [lo, hi), all of them [lo_all, hi_all)
-  auto range = [&](int r0, int r1, int* lo, int* hi, int* lo_all, int* hi_all) {
-    r0 = r0 < R - 1 ? r0 : R - 1;
-    r1 = r1 < R ? r1 : R;
-    const int p0 = first + (int)((uint32_t)r0 / G), p1 = first + (int)((uint32_t)(r1 - 1) / G);
-    *hi = a.causal ? max(0, min(len, p1 + 1)) : len;
-    *hi_all = a.causal ? max(0, min(len, p0 + 1)) : len;
-    *lo = a.window > 0 ? max(0, p0 - a.window + 1) : 0;
-    *lo_all = a.window > 0 ? max(0, p1 - a.window + 1) : 0;
-  };
-  int wlo, whi, wlo_all, whi_all, lo_min, hi_max, lo_all, hi_all;
-  const int rho0 = wg0 + wave * 16 * NC;
-  range(wg0, wg0 + 16 * NC * WAVES, &lo_min, &hi_max, &lo_all, &hi_all);
-  range(rho0, rho0 + 16 * NC, &wlo, &whi, &wlo_all, &whi_all);
-  whi = __builtin_amdgcn_readfirstlane(rho0 < R ? whi : 0);
+  PromptTile<ROWS> t;
+  if (!t.template find<64 * WAVES>(a, tile_at, scan_) || part >= t.parts) return;
+  const SeqSpan s = t.s;
+  const int R = t.R, wg0 = t.wg0, len = s.len, first = t.first, P = 1 << a.kv.lp, rho0 = wg0 + wave * 16 * NC;
+  const int lo_min = t.seen.lo, hi_max = t.seen.hi, lo_all = t.seen.lo_all, hi_all = t.seen.hi_all;
+  const Seen mine = t.of_rows(a, rho0, rho0 + 16 * NC);  // by this wave's rows
+  const int wlo = mine.lo, wlo_all = mine.lo_all, whi_all = mine.hi_all;
+  const int whi = __builtin_amdgcn_readfirstlane(rho0 < R ? mine.hi : 0);
   const bool none = fabsf(a.scale2) < 0x1p-126f;  // all scores 0
   int rho[NC], vlo[NC], vhi[NC];
   v8bf qf[NC][DS];
@@ -742,12 +763,10 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attn_prompt(AttnArgs a) {
     for (int d = 0; d < DT; d++) o[c][d] = v4f{0.f, 0.f, 0.f, 0.f};
   }
 
-  int u0, u1;
-  steps_of_rows(a, s, wg0, min(wg0 + ROWS, R), &u0, &u1);
-  const int parts = parts_of(u1 - u0, a.parts);
-  if (part >= parts) return;
+  const int parts = t.parts;
+  int u0 = t.u0, u1 = t.u1;
   part_steps(part, parts, &u0, &u1);
-  const int32_t* table = a.kv.table + b * a.kv.width;
+  const int32_t* table = a.kv.table + t.b * a.kv.width;
   // Page of the 16 tokens that the lane stages from: tokens 64 u + 16 x .. with
   // x = row / 4 of the keys' operand, x = group of the values'.
   const int stage_group = keys ? (lane >> 2) & 3 : g;
@@ -1038,32 +1057,15 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void attn_prompt32(AttnArgs a) {
   constexpr int ROWS = 32 * NC * WAVES;
   const uint32_t G = (uint32_t)a.G, H = (uint32_t)a.kv.H, at_part = blockIdx.x / H, tile_at = at_part / (uint32_t)a.parts;
   const int h = (int)(blockIdx.x - at_part * H), part = (int)(at_part - tile_at * a.parts);
-  int64_t b, item;
-  auto tiles = [&](int64_t i) -> int64_t { return (seq_span(a.kv, i).n * a.G + ROWS - 1) / ROWS; };
   __shared__ int64_t scan_[WAVES + 2];
-  ItemScan<64 * WAVES, decltype(tiles)> scan(a.kv.n_seqs, tiles, scan_);
-  if (tile_at >= scan.total) return;
-  scan.find(tile_at, &b, &item);
-  const SeqSpan s = seq_span(a.kv, b);
-  // rows count to less than 2^31 (checked at the entry)
-  const int R = s.n * (int)G, wg0 = (R - 1) / ROWS * ROWS - (int)item * ROWS;
-  const int len = s.len, first = len - s.n, P = 1 << a.kv.lp;
-
-  // what rows [r0, r1) see between them: some of them [lo, hi), all of them [lo_all, hi_all)
-  auto range = [&](int r0, int r1, int* lo, int* hi, int* lo_all, int* hi_all) {
-    r0 = r0 < R - 1 ? r0 : R - 1;
-    r1 = r1 < R ? r1 : R;
-    const int p0 = first + (int)((uint32_t)r0 / G), p1 = first + (int)((uint32_t)(r1 - 1) / G);
-    *hi = a.causal ? max(0, min(len, p1 + 1)) : len;
-    *hi_all = a.causal ? max(0, min(len, p0 + 1)) : len;
-    *lo = a.window > 0 ? max(0, p0 - a.window + 1) : 0;
-    *lo_all = a.window > 0 ? max(0, p1 - a.window + 1) : 0;
-  };
-  int wlo, whi, wlo_all, whi_all, lo_min, hi_max, lo_all, hi_all;
-  const int rho0 = wg0 + wave * 32 * NC;
-  range(wg0, wg0 + ROWS, &lo_min, &hi_max, &lo_all, &hi_all);
-  range(rho0, rho0 + 32 * NC, &wlo, &whi, &wlo_all, &whi_all);
-  whi = __builtin_amdgcn_readfirstlane(rho0 < R ? whi : 0);
+  PromptTile<ROWS> t;
+  if (!t.template find<64 * WAVES>(a, tile_at, scan_) || part >= t.parts) return;
+  const SeqSpan s = t.s;
+  const int R = t.R, wg0 = t.wg0, len = s.len, first = t.first, P = 1 << a.kv.lp, rho0 = wg0 + wave * 32 * NC;
+  const int lo_min = t.seen.lo, hi_max = t.seen.hi, lo_all = t.seen.lo_all, hi_all = t.seen.hi_all;
+  const Seen mine = t.of_rows(a, rho0, rho0 + 32 * NC);  // by this wave's rows
+  const int wlo = mine.lo, wlo_all = mine.lo_all, whi_all = mine.hi_all;
+  const int whi = __builtin_amdgcn_readfirstlane(rho0 < R ? mine.hi : 0);
   const bool none = fabsf(a.scale2) < 0x1p-126f;  // all scores 0
   int rho[NC], vlo[NC], vhi[NC];
   v8bf qf[NC][DS];
@@ -1093,12 +1095,10 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void attn_prompt32(AttnArgs a) {
       for (int e = 0; e < 16; e++) o[c][d][e] = 0.f;
   }
 
-  int u0, u1;
-  steps_of_rows(a, s, wg0, min(wg0 + ROWS, R), &u0, &u1);
-  const int parts = parts_of(u1 - u0, a.parts);
-  if (part >= parts) return;
+  const int parts = t.parts;
+  int u0 = t.u0, u1 = t.u1;
   part_steps(part, parts, &u0, &u1);
-  const int32_t* table = a.kv.table + b * a.kv.width;
+  const int32_t* table = a.kv.table + t.b * a.kv.width;
   // This thread's 16-byte pieces of a step.  Keys (first half of the waves,
   // tile w4 % 2): 16 dims 16 (2 (w4 / 2 + 2 i) + h) .. of the token of row n.
   // Values (second half): 16 tokens of dim 32 (w4 / 2 + 2 i) + n, tokens
@@ -1420,19 +1420,11 @@ template <int D, int ROWS>
 __global__ __launch_bounds__(256) void attn_join(AttnArgs a) {
   constexpr int T4 = D / 4, AHEAD = 8;
   const uint32_t G = (uint32_t)a.G, H = (uint32_t)a.kv.H, tile_at = blockIdx.x / H, h = blockIdx.x - tile_at * H;
-  auto tiles = [&](int64_t i) -> int64_t { return (seq_span(a.kv, i).n * a.G + ROWS - 1) / ROWS; };
   __shared__ int64_t scan_[256 / 64 + 2];
-  ItemScan<256, decltype(tiles)> scan(a.kv.n_seqs, tiles, scan_);
-  if (tile_at >= scan.total) return;
-  int64_t b, item;
-  scan.find(tile_at, &b, &item);
-  const SeqSpan s = seq_span(a.kv, b);
-  const int R = s.n * (int)G, wg0 = (R - 1) / ROWS * ROWS - (int)item * ROWS;
-  const int at = blockIdx.y * 256 + threadIdx.x, r = at / T4, d = at % T4 * 4;
-  int u0, u1;
-  steps_of_rows(a, s, wg0, min(wg0 + ROWS, R), &u0, &u1);
-  const int parts = parts_of(u1 - u0, a.parts);
-  if (wg0 + r >= R || parts == 1) return;  // one part: its workgroup has written O
+  PromptTile<ROWS> t;
+  if (!t.template find<256>(a, tile_at, scan_) || t.parts == 1) return;  // one part: its workgroup has written O
+  const int parts = t.parts, at = blockIdx.y * 256 + threadIdx.x, r = at / T4, d = at % T4 * 4;
+  if (t.wg0 + r >= t.R) return;
   const int64_t step = (int64_t)H * ROWS * (D + kPartPad);  // to the next part
   const float* p = a.part + (((int64_t)tile_at * a.parts * H + h) * ROWS + r) * (D + kPartPad);
   float M = -INFINITY, L = 0.f;
@@ -1464,8 +1456,8 @@ __global__ __launch_bounds__(256) void attn_join(AttnArgs a) {
     }
   }
   const float inv = L > 0.f || L != L ? 1.0f / L : 0.f;
-  const uint32_t rc = wg0 + r, tok = rc / G;
-  const int64_t row = s.row0 + tok, hd = (int64_t)h * G + (rc - tok * G);
+  const uint32_t rc = t.wg0 + r, tok = rc / G;
+  const int64_t row = t.s.row0 + tok, hd = (int64_t)h * G + (rc - tok * G);
   uint2 w;
   w.x = bf16_bits(o[0] * inv) | (bf16_bits(o[1] * inv) << 16);
   w.y = bf16_bits(o[2] * inv) | (bf16_bits(o[3] * inv) << 16);
