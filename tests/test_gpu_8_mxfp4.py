@@ -115,6 +115,12 @@ def test_product(M, N, K, x4):
         assert torch.equal(y, y2), "two runs differ"
 
 
+@pytest.mark.parametrize("M,N,K", [(17, 16, 32), (25, 300, 17408), (31, 33, 544), (32, 700, 5120), (33, 300, 17408)])
+def test_product_of_two_row_blocks(M, N, K):
+    """17 to 32 rows of MXFP4 X, and one more; K whole and split."""
+    test_product(M, N, K, True)
+
+
 @pytest.mark.parametrize("K", [96, 672])
 def test_product_of_more_tiles_than_compute_units(K):
     """Tiles of 64 rows that share compute units."""

@@ -64,17 +64,19 @@ __device__ __forceinline__ void store_y(void* y, int64_t i, float v) {
 }
 
 // ---------------------------------------------------------- few rows of X
-// Up to 16 rows: a workgroup per row-block of W and split of K, whose waves take
-// the quads in turn.  A wave loads a quad's codes a quad ahead, straight to
+// Up to 16 bf16 or 32 MXFP4 rows: a workgroup per row-block of W and split of K,
+// whose waves take the quads in turn.  A wave loads a quad's codes a quad ahead, straight to
 // registers; bf16 rows of X reach the wave's own LDS as direct copies of 1 KiB
 // (a row of a quad), with the 16-byte chunk c of row r at place c ^ r so that an
 // operand's 16 rows fall on different banks.  The partial tiles are added over
 // the waves in a fixed order.  1 x 5120 x 5120 5.5 us on the GPU (14 MB of
 // codes), 5 x 5120 x 17408 15.2 us (47 MB, 3.1 TB/s: 320 workgroups on 256 compute
 // units; with MXFP4 rows, so without widening the codes, 15.0), 1 x 34816 x 5120
-// 21 us (4.5 TB/s).
+// 21 us (4.5 TB/s).  32 MXFP4 rows x 5120 x 5120 8.7 us, x 15360 x 5120 14.3 us, x
+// 700 x 17408 6.8 us (tiles: 12.7, 18.3 and 13.8); 17 bf16 rows here would need
+// two operands' rows in every wave's LDS.
 constexpr int kSmallWaves = 8;
-constexpr int64_t kSmallRows = 16;
+constexpr int64_t kSmallRows = 16, kSmallRows4 = 32;  // bf16, MXFP4 X
 constexpr int kSmallSplits = 8;
 typedef __attribute__((address_space(3))) uint8_t lds_u8;
 
@@ -85,16 +87,17 @@ __device__ __forceinline__ void copy16(const uint8_t* src, lds_u8* dst) {
 
 [[maybe_unused]] __device__ const mx_u4 mx_zeros[16] = {};
 
-template <bool X4>
+// RB: row-blocks of X (MXFP4 rows: up to two)
+template <bool X4, int RB>
 struct SmallQuad {
   mx_u4 w[4];
   uint32_t ws;
-  mx_u4 x[X4 ? 4 : 1];  // MXFP4 rows: one row-block
-  uint32_t xs;
+  mx_u4 x[RB][X4 ? 4 : 1];
+  uint32_t xs[RB];
 };
 
-template <bool X4>
-__device__ __forceinline__ void load_small(const MxArgs& a, int64_t rb, int64_t gq, int lane, SmallQuad<X4>& o) {
+template <bool X4, int RB>
+__device__ __forceinline__ void load_small(const MxArgs& a, int64_t rb, int64_t gq, int lane, SmallQuad<X4, RB>& o) {
   // groups past the last one read it again: their codes are cleared below
   const uint8_t* src = a.wc + rb * a.G * 1024 + 16 * lane;
 #pragma unroll
@@ -103,8 +106,12 @@ __device__ __forceinline__ void load_small(const MxArgs& a, int64_t rb, int64_t 
   o.ws = *(const uint32_t*)(a.ws + ((rb * a.GQ + gq) * 64 + lane) * 4);
   if constexpr (X4) {
 #pragma unroll
-    for (int t = 0; t < 4; t++) o.x[t] = *(const mx_u4*)(a.x + (min(4 * gq + t, a.G - 1) * 64 + lane) * 16);
-    o.xs = *(const uint32_t*)(a.xs + (gq * 64 + lane) * 4);
+    for (int i = 0; i < RB; i++) {
+#pragma unroll
+      for (int t = 0; t < 4; t++)
+        o.x[i][t] = *(const mx_u4*)(a.x + ((i * a.G + min(4 * gq + t, a.G - 1)) * 64 + lane) * 16);
+      o.xs[i] = *(const uint32_t*)(a.xs + ((i * a.GQ + gq) * 64 + lane) * 4);
+    }
   }
 }
 
@@ -127,19 +134,19 @@ __device__ __forceinline__ v4f get_pairs(const float* p) {
   return v;
 }
 
-// lane l's four outputs of a 16 x 16 tile (rows m = 4 (l / 16) .., column n = l % 16)
+// lane l's four outputs of a 16 x 16 tile (rows m = 16 i + 4 (l / 16) .., column n = l % 16)
 template <int YK>
-__device__ __forceinline__ void store_small(const MxArgs& a, const v4f& s, int64_t rb, int l) {
+__device__ __forceinline__ void store_small(const MxArgs& a, const v4f& s, int64_t rb, int i, int l) {
   const int64_t n = rb * 16 + (l & 15);
   if (n >= a.N) return;
 #pragma unroll
   for (int e = 0; e < 4; e++) {
-    const int64_t m = 4 * (l >> 4) + e;
+    const int64_t m = 16 * i + 4 * (l >> 4) + e;
     if (m < a.M) store_y<YK>(a.y, m * a.N + n, s[e]);
   }
 }
 
-template <bool X4, int YK>
+template <bool X4, int RB, int YK>
 __global__ __launch_bounds__(64 * kSmallWaves) void mx_small(MxArgs a) {
 #if defined(__HIP_DEVICE_COMPILE__)
   extern __shared__ __attribute__((aligned(16))) uint8_t mem[];
@@ -149,7 +156,7 @@ __global__ __launch_bounds__(64 * kSmallWaves) void mx_small(MxArgs a) {
   const uint32_t ks = blockIdx.y, quads = (uint32_t)a.GQ;
   const int64_t q0 = quads * ks / a.KS, q1 = quads * (ks + 1) / a.KS;  // quads of this split
   uint8_t* xw = mem + wave * rows * 1024;
-  v4f acc[2] = {};  // two chains
+  v4f acc[RB][2] = {};  // two chains each
   const uint8_t* zeros = (const uint8_t*)mx_zeros;
   auto copy_x = [&](int64_t gq) {
     for (int m = 0; m < rows; m++) {
@@ -158,11 +165,11 @@ __global__ __launch_bounds__(64 * kSmallWaves) void mx_small(MxArgs a) {
     }
   };
   const int mrow = r < rows ? r : rows - 1;  // rows of the operand past the last one repeat it
-  SmallQuad<X4> cur, next;
+  SmallQuad<X4, RB> cur, next;
   int64_t gq = q0 + wave;
   if (gq < q1) {
     if constexpr (!X4) copy_x(gq);
-    load_small<X4>(a, rb, gq, lane, cur);
+    load_small<X4, RB>(a, rb, gq, lane, cur);
   }
   for (; gq < q1; gq += W) {
     const bool more = gq + W < q1;
@@ -179,17 +186,20 @@ __global__ __launch_bounds__(64 * kSmallWaves) void mx_small(MxArgs a) {
       read_x(0);
       __builtin_amdgcn_sched_barrier(0);
     }
-    if (more) load_small<X4>(a, rb, gq + W, lane, next);
+    if (more) load_small<X4, RB>(a, rb, gq + W, lane, next);
     if (4 * gq + 3 >= a.G) {
 #pragma unroll
       for (int t = 1; t < 4; t++)
         if (4 * gq + t >= a.G) cur.w[t] = mx_u4{0, 0, 0, 0};
     }
     if constexpr (X4) {
-      acc[0] = mfma_mx<0>(cur.x[0], cur.w[0], acc[0], cur.xs, cur.ws);
-      acc[1] = mfma_mx<1>(cur.x[1], cur.w[1], acc[1], cur.xs, cur.ws);
-      acc[0] = mfma_mx<2>(cur.x[2], cur.w[2], acc[0], cur.xs, cur.ws);
-      acc[1] = mfma_mx<3>(cur.x[3], cur.w[3], acc[1], cur.xs, cur.ws);
+#pragma unroll
+      for (int i = 0; i < RB; i++) {
+        acc[i][0] = mfma_mx<0>(cur.x[i][0], cur.w[0], acc[i][0], cur.xs[i], cur.ws);
+        acc[i][1] = mfma_mx<1>(cur.x[i][1], cur.w[1], acc[i][1], cur.xs[i], cur.ws);
+        acc[i][0] = mfma_mx<2>(cur.x[i][2], cur.w[2], acc[i][0], cur.xs[i], cur.ws);
+        acc[i][1] = mfma_mx<3>(cur.x[i][3], cur.w[3], acc[i][1], cur.xs[i], cur.ws);
+      }
     } else {
 #pragma unroll
       for (int t = 0; t < 4; t++) {
@@ -197,8 +207,8 @@ __global__ __launch_bounds__(64 * kSmallWaves) void mx_small(MxArgs a) {
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int h = 0; h < 4; h++)
-          acc[h & 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-              xf[t & 1][h], bf16x8(cur.w[t][h], scale_float(cur.ws, t)), acc[h & 1], 0, 0, 0);
+          acc[0][h & 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+              xf[t & 1][h], bf16x8(cur.w[t][h], scale_float(cur.ws, t)), acc[0][h & 1], 0, 0, 0);
       }
       if (more) {
         __asm__ volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // this quad's rows have been read
@@ -211,36 +221,42 @@ __global__ __launch_bounds__(64 * kSmallWaves) void mx_small(MxArgs a) {
   __syncthreads();
   float* red = (float*)mem;
 #pragma unroll
-  for (int e = 0; e < 4; e++) acc[0][e] += acc[1][e];
-  *(v4f*)(red + (wave * 64 + lane) * 4) = acc[0];
+  for (int i = 0; i < RB; i++) {
+#pragma unroll
+    for (int e = 0; e < 4; e++) acc[i][0][e] += acc[i][1][e];
+    *(v4f*)(red + ((wave * RB + i) * 64 + lane) * 4) = acc[i][0];
+  }
   __syncthreads();
-  if (wave == 0) {
-    v4f s = *(const v4f*)(red + lane * 4);
+  for (int i = wave; i < RB; i += W) {  // a wave for each row-block of X
+    v4f s = *(const v4f*)(red + (i * 64 + lane) * 4);
     for (int w = 1; w < W; w++) {
-      const v4f v = *(const v4f*)(red + (w * 64 + lane) * 4);
+      const v4f v = *(const v4f*)(red + ((w * RB + i) * 64 + lane) * 4);
 #pragma unroll
       for (int e = 0; e < 4; e++) s[e] += v[e];
     }
-    if (a.KS == 1) store_small<YK>(a, s, rb, lane);
-    else put_pairs(a.part + (((int64_t)ks * a.NT + rb) * 64 + lane) * 4, s);
+    if (a.KS == 1) {
+      store_small<YK>(a, s, rb, i, lane);
+      continue;
+    }
+    // Splits of K: the last to arrive adds the partial tiles in their order.
+    auto part = [&](int64_t k) -> float* { return a.part + (((k * a.NT + rb) * RB + i) * 64 + lane) * 4; };
+    uint32_t* cnt = a.cnt + rb * RB + i;
+    put_pairs(part(ks), s);
+    __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    uint32_t arrived = 0;
+    if (lane == 0) arrived = __hip_atomic_fetch_add(cnt, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (__builtin_amdgcn_readfirstlane((int)arrived) != (int)a.KS - 1) continue;
+    if (lane == 0) __hip_atomic_store(cnt, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    v4f v[kSmallSplits];
+#pragma unroll
+    for (int k = 0; k < kSmallSplits; k++) v[k] = k < (int)a.KS ? get_pairs(part(k)) : v4f{0.f, 0.f, 0.f, 0.f};
+    s = v[0];
+#pragma unroll
+    for (int k = 1; k < kSmallSplits; k++)
+#pragma unroll
+      for (int e = 0; e < 4; e++) s[e] += v[k][e];
+    store_small<YK>(a, s, rb, i, lane);
   }
-  if (a.KS == 1 || wave != 0) return;
-  // Splits of K: the last to arrive adds the partial tiles in their order.
-  __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
-  uint32_t arrived = 0;
-  if (lane == 0) arrived = __hip_atomic_fetch_add(a.cnt + rb, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  if (__builtin_amdgcn_readfirstlane((int)arrived) != (int)a.KS - 1) return;
-  if (lane == 0) __hip_atomic_store(a.cnt + rb, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  v4f v[kSmallSplits];
-#pragma unroll
-  for (int k = 0; k < kSmallSplits; k++)
-    v[k] = k < (int)a.KS ? get_pairs(a.part + (((int64_t)k * a.NT + rb) * 64 + lane) * 4) : v4f{0.f, 0.f, 0.f, 0.f};
-  v4f s = v[0];
-#pragma unroll
-  for (int k = 1; k < kSmallSplits; k++)
-#pragma unroll
-    for (int e = 0; e < 4; e++) s[e] += v[k][e];
-  store_small<YK>(a, s, rb, lane);
 #endif
 }
 
@@ -264,14 +280,14 @@ void plan_small(bool x4, int64_t M, int64_t NB, int64_t GQ, int* W_, int* KS_) {
   *KS_ = (int)KS;
 }
 
-template <bool X4>
+template <bool X4, int RB>
 void launch_small(const MxArgs& a, int W, int ykind, hipStream_t s) {
   const dim3 grid((unsigned)a.NT, (unsigned)a.KS);
-  const size_t lds = (size_t)W * std::max<int64_t>(1, X4 ? 0 : a.M) * 1024;
+  const size_t lds = (size_t)W * std::max<int64_t>(RB, X4 ? 0 : a.M) * 1024;
   if (ykind == YK_F32)
-    hipLaunchKernelGGL((mx_small<X4, YK_F32>), grid, dim3(64 * W), lds, s, a);
+    hipLaunchKernelGGL((mx_small<X4, RB, YK_F32>), grid, dim3(64 * W), lds, s, a);
   else
-    hipLaunchKernelGGL((mx_small<X4, YK_BF16>), grid, dim3(64 * W), lds, s, a);
+    hipLaunchKernelGGL((mx_small<X4, RB, YK_BF16>), grid, dim3(64 * W), lds, s, a);
 }
 
 // ------------------------------------------------------------ many rows of X
@@ -710,11 +726,11 @@ struct Plan {
 
 Plan plan_gemm(bool x4, int64_t M, int64_t N, int64_t K) {
   Plan p{};
-  if (M <= kSmallRows) {
+  if (M <= (x4 ? kSmallRows4 : kSmallRows)) {
     p.small = true;
     p.NT = cdiv(N, 16);
     plan_small(x4, M, p.NT, mx_quads(K), &p.W, &p.KS);
-    p.part_bytes = p.KS > 1 ? (size_t)(p.NT * p.KS) * 1024 : 0;
+    p.part_bytes = p.KS > 1 ? (size_t)(p.NT * p.KS * cdiv(M, 16)) * 1024 : 0;
     return p;
   }
   const int64_t MB = cdiv(M, 16), NB = cdiv(N, 16), GQ = mx_quads(K);
@@ -813,8 +829,9 @@ hipError_t launch_gemm_mxfp4(const MxGemmArgs& g, hipStream_t s) {
     a.part = (float*)((uint8_t*)g.ws + kCounterBytes);
   }
   if (p.small) {
-    if (g.x4) launch_small<true>(a, p.W, g.ykind, s);
-    else launch_small<false>(a, p.W, g.ykind, s);
+    if (!g.x4) launch_small<false, 1>(a, p.W, g.ykind, s);
+    else if (g.M <= 16) launch_small<true, 1>(a, p.W, g.ykind, s);
+    else launch_small<true, 2>(a, p.W, g.ykind, s);
   } else if (g.x4) {
     if (p.big) launch_tile4<4, 2, 4, 8>(a, g.ykind, s);
     else launch_tile4<2, 2, 4, 4>(a, g.ykind, s);
