@@ -520,7 +520,7 @@ int lowbit_kv8_append(const lowbit_kv8* cache, const lowbit_kv8_batch* batch, in
  * and lse = -infinity (so does one whose scores are all -infinity, which takes
  * an infinity in Q); what lies in tokens a row does not see (NaN codes too)
  * does not reach it.  With causal == 0 the cache may hold another sequence (an
- * encoder's states) of its own length.  Weights times 2^e enter the second
+ * encoder's states) of its own length.  Weights enter the second
  * product rounded to bf16; sums and statistics are fp32.  Results do not
  * depend on the order in which workgroups run.  Rows of sequences behind the
  * last q_starts entry are not written.

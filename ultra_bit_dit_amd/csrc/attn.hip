@@ -12,8 +12,8 @@
 // g = L / 16 holds 16 consecutive tokens, which is what the B operand of
 // O^T = V^T P^T needs: no exchange between the products, 16 tokens of one
 // row of V are one 16-byte load, and (pages hold 16 tokens or more) one
-// exponent ek and ev per lane and step.  p 2^ev is rounded to bf16 (relative
-// error 2^-9 of each weight, the same size as the output's own rounding);
+// exponent ek and ev per lane and step.  Weights are rounded to bf16 (relative
+// error 2^-9 of each, the same size as the output's own rounding);
 // statistics, sums and O stay in fp32.
 #include <hip/hip_runtime.h>
 
@@ -148,7 +148,10 @@ struct ItemScan {
 // that lies in several shares is joined by the workgroup that ends last.
 // (Shares of single steps, which often had the end of one tile and the start of
 // the next: 4 x 4 tokens in contexts of 777 23.1 us, with blocks 14.0 us; one
-// token in 16000, D = 256, 28.1 and 23.4 us.)
+// token in 16000, D = 256, 28.1 and 23.4 us.)  Bound by memory: 32 tokens in
+// ragged contexts up to 16384, 40 heads over 8, D = 128, 135 us (695 MB, 5.1
+// TB/s); one in 131071, 24 heads over 4, D = 256, 58 us (268 MB, 4.6 TB/s); one
+// in 512, 32 heads over 8, 10.7 us: start, one block a workgroup, the join.
 constexpr int kJoinLoads = 8;   // results of a pair of outputs read at once
 constexpr int kMaxJoin = 32;    // results joined by one workgroup: shares of a tile <= kMaxJoin^2
 constexpr int kMaxShares = 512;
@@ -639,7 +642,8 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
 // One workgroup per (sequence, key head, 16 NC WAVES rows).  A step's keys and
 // values (64 tokens) are widened to bf16 once for all waves and lie in LDS as
 // whole MFMA operands, 1 KiB per 16 rows x 32 k in the order of the lanes:
-// writes and reads without bank conflicts.
+// writes and reads without bank conflicts.  2 x 4096 in 4096 tokens, causal, 24
+// heads over 4, D = 256: 593 us (0.70 PFLOP/s).
 // Where the tiles do not fill the chip, a tile's steps are cut into parts, one
 // workgroup each, whose results attn_join puts together.
 //
@@ -1415,7 +1419,8 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void attn_prompt32(AttnArgs a) {
 
 // Results of the parts of a tile: O = sum 2^(m_k - M) O_k / sum 2^(m_k - M) l_k,
 // M the largest m_k, in the order of the parts.  One thread for four dims of a
-// row, rows of ROWS as the tile's workgroups have them.
+// row, rows of ROWS as the tile's workgroups have them.  Eight parts are read at
+// once: the loads' latency bounds it (some 3 us with the launch for 16 parts).
 template <int D, int ROWS>
 __global__ __launch_bounds__(256) void attn_join(AttnArgs a) {
   constexpr int T4 = D / 4, AHEAD = 8;
