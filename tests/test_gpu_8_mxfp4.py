@@ -298,3 +298,48 @@ def test_capture_without_a_workspace_is_refused():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.all(y == 8.0)
+
+
+@pytest.mark.parametrize("M,x4", [(1, False), (3, True), (20, True), (40, False), (40, True)])
+def test_weights_beyond_32_bits(M, x4):
+    """Packed codes of more than 4 GiB: rows from both ends against 64 bits."""
+    N, K = 1_100_005, 8192
+    print(f"large weights M={M} x4={x4}", flush=True)
+    g = torch.Generator(device="cuda").manual_seed(9)
+    wc, ws = lb.empty_mxfp4(N, K)
+    assert wc.numel() > 1 << 32
+    wc.random_(0, 256, generator=g)
+    ws.random_(118, 130, generator=g)
+    x = torch.randn(M, K, device="cuda", generator=g).bfloat16()
+    xa, xs, xv = x, None, f64(x)
+    if x4:
+        xa, xs, xv = lb.quantize_mxfp4(x, values=True)
+        xv = f64(xv)
+    y = lb.gemm_mxfp4(M, N, K, wc, ws, xa, x_scales=xs)
+    rows = np.r_[0:3, 65535:65540, N - 40:N]
+    codes = wc.view(-1, K // 128, 4, 16, 16)
+    scales = ws.view(-1, K // 512, 4, 16, 4)
+    wv = np.empty((len(rows), K))
+    table = np.array([0, 0.5, 1, 1.5, 2, 3, 4, 6, 0, -0.5, -1, -1.5, -2, -3, -4, -6])
+    for i, n in enumerate(rows):
+        c = codes[n // 16, :, :, n % 16].cpu().numpy()                       # [group][q][16]
+        e = scales[n // 16, :, :, n % 16].permute(0, 2, 1).cpu().numpy()     # [quad][group % 4][q]
+        v = table[np.stack([c & 15, c >> 4], -1).reshape(-1, 4, 32)]
+        wv[i] = (v * np.exp2(e.reshape(-1, 4, 1).astype(float) - 127)).reshape(-1)
+    check_product(y[:, torch.from_numpy(rows).cuda()], wv, xv, K, False, f"large weights M={M}")
+
+
+def test_quantize_beyond_32_bits():
+    """More than 2^32 values, and codes of more than 4 GiB: the last rows like those rows alone."""
+    rows, K = (1 << 27) + 77, 32
+    print("large quantization", flush=True)
+    X = torch.empty(rows, K, device="cuda", dtype=torch.bfloat16)
+    X.fill_(1.0)
+    tail = torch.randn(93, K, device="cuda").bfloat16()
+    X[-93:] = tail
+    pc, ps, vals = lb.quantize_mxfp4(X, values=True)
+    # the last 93 rows begin a row-block
+    assert (rows - 93) % 16 == 0 and pc.numel() > 1 << 32
+    c2, s2, v2 = lb.quantize_mxfp4(tail, values=True)
+    assert torch.equal(pc[-c2.numel():], c2) and torch.equal(ps[-s2.numel():], s2) and torch.equal(vals[-93:], v2)
+    assert bool((vals[:1000] == 1).all()) and bool((vals[-1093:-93] == 1).all())
