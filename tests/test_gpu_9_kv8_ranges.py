@@ -1,0 +1,50 @@
+"""The 8-bit cache at the ends of its number ranges: exponents that rise by
+any amount."""
+import numpy as np
+import pytest
+import torch
+
+from ultra_bit_dit_amd import lowbit as lb
+from test_gpu_9_kv8 import Cache, f64, i32
+
+pytestmark = pytest.mark.gpu
+
+
+def check_bits(c, what):
+    """As Cache.check, and the signs of zeros."""
+    c.check(what)
+    for t, m in ((c.gpu[0], c.k), (c.gpu[1], c.v)):
+        by = t.view(torch.uint8).cpu().numpy()
+        assert np.array_equal((by >> 7 == 1) & ~np.isnan(m), np.signbit(m) & ~np.isnan(m)), f"{what}: signs"
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("P,D", [(16, 64), (64, 128), (128, 256)])
+@pytest.mark.parametrize("which", ["k", "v"])
+def test_append_exponent_rises_by_any_amount(P, D, which, dtype):
+    """Earlier tokens all zero, or near 2^-120 (exponent -127), then tokens whose
+    maximum raises the page's exponent by 1 .. 246; the other side rises by one."""
+    H, n = 2, 3
+    lo = P // 2 + 3
+    tops = [(0.0, t) for t in (448.0, 500.0, 896.0, 897.0, 2.0 ** 60, 2.0 ** 99)]
+    tops += [(2.0 ** -120, 448 * 2.0 ** (r - 127)) for r in
+             (0, 1, 9, 17, 18, 100, 125, 126, 127, 128, 129, 140, 191, 192, 246)]
+    B = len(tops)
+    print(f"append far rise {which} P={P} D={D} {dtype}", flush=True)
+    c = Cache([lo + n] * B, P, H, D, seed=P)
+    g = np.random.default_rng(3)
+
+    def side(T, size, far):
+        """[B T][H][D] with the given largest magnitude of each sequence's heads"""
+        x = g.uniform(0.25, 1, (B, T, H, D)) * np.where(g.random((B, T, H, D)) < .5, -1, 1)
+        x[:, 0, :, 5] = 1.0
+        x *= np.array([s[size] for s in tops])[:, None, None, None] if far else 1.0 + size
+        return torch.from_numpy(x.reshape(B * T, H, D).astype(np.float32)).cuda().to(dtype)
+
+    for T, first, size in ((lo, 0, 0), (n, lo, 1)):
+        K, V = side(T, size, which == "k"), side(T, size, which == "v")
+        lb.kv8_append(c.gpu, c.tables(), i32([first + T] * B), K, V)
+        for b in range(B):
+            c.append(b, first, f64(K)[b * T:(b + 1) * T], f64(V)[b * T:(b + 1) * T])
+        check_bits(c, "earlier" if first == 0 else "later")
+    assert {1, 127, 128, 246} <= set((c.ks if which == "k" else c.vs)[c.table[:, 0], 0] + 127)

@@ -59,7 +59,13 @@ __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
   return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, (int)w, true);
 }
 
-// four codes times 2^-shift, rounded again
+// 2^-rise for codes written under an exponent `rise` lower; 0 from 127 on, where
+// even 448 2^-rise rounds to no code (and 2^-rise leaves the exponent field)
+__device__ __forceinline__ float rise_factor(uint32_t rise) {
+  return rise < 127u ? __uint_as_float((127u - rise) << 23) : 0.f;
+}
+
+// four codes times f, rounded again
 __device__ __forceinline__ uint32_t requantize4(uint32_t w, float f) {
   return codes4(__builtin_amdgcn_cvt_f32_fp8((int)w, 0) * f, __builtin_amdgcn_cvt_f32_fp8((int)w, 1) * f,
                 __builtin_amdgcn_cvt_f32_fp8((int)w, 2) * f, __builtin_amdgcn_cvt_f32_fp8((int)w, 3) * f);
@@ -159,14 +165,14 @@ __global__ __launch_bounds__(THREADS) void kv8_append(KvArgs a, int64_t span, co
   }
   // earlier tokens of the page, where its exponent rose
   if (lo > 0 && bk > ok) {
-    const float f = inv_scale(bk - ok + 127);
+    const float f = rise_factor(bk - ok);
     for (int i = tid; i < lo * (D / 4); i += THREADS) {
       uint32_t* w = (uint32_t*)kc + i;
       *w = requantize4(*w, f);
     }
   }
   const bool rise = lo > 0 && bv > ov;
-  const float fv = inv_scale(rise ? bv - ov + 127 : 127);
+  const float fv = rise_factor(rise ? bv - ov : 0u);
   __syncthreads();
   // V rows of the page, four tokens at a time: whole words where all four are
   // written, else byte by byte (tokens behind the last one stay as they were)
