@@ -504,7 +504,8 @@ typedef struct lowbit_kv8_batch {
  * that lie before the sequence's start (more of them than kv_lens) are not
  * written.  Writing the same tokens again changes nothing.  K, V 16-byte
  * aligned, rows 16-byte aligned; n_seqs * kv_heads * (pages that max_q tokens
- * can touch) <= 2^23.
+ * can touch) <= 2^23, below it where page_tokens * head_dim is 16384 and below
+ * 2^22 where it is 32768.
  * Errors: E_NULL, E_UNSUPPORTED (dtype, page_tokens, head_dim), E_SHAPE,
  * E_ALIGN, E_HIP. */
 int lowbit_kv8_append(const lowbit_kv8* cache, const lowbit_kv8_batch* batch, int dtype, const void* K,

@@ -1,0 +1,31 @@
+"""Sizes at the ends of what a launch holds (2^32 - 1 threads), on a machine
+without a GPU: one more is refused with E_SHAPE.  The largest accepted ones
+are shown by the check that comes after the sizes', a misaligned pointer."""
+import pytest
+
+from ultra_bit_dit_amd import lowbit as lb
+from test_mx_kv8_cpu import A4, A16, batch, kv
+
+
+@pytest.mark.parametrize("P,D,most", [(128, 256, 1 << 22), (64, 256, 1 << 23), (128, 128, 1 << 23)])
+def test_append_workgroups(P, D, most):
+    """1024 threads for pages of 32768 elements a head, 512 for 16384."""
+    def call(H):
+        c = kv(page_tokens=P, kv_heads=H, head_dim=D)
+        b = batch(n_seqs=1 << 13, table_width=2, total_q=1 << 13, max_q=1, max_kv=2 * P, q_starts=0x70000)
+        return lb.lib().lowbit_kv8_append(c, b, lb.BF16, A4, A16, H * D, H * D, None)
+
+    H = most >> 13  # max_q = 1 touches one page
+    assert call(H) == lb.E_SHAPE
+    assert call(H - 1) == lb.E_ALIGN
+
+
+def test_append_workgroups_of_small_pages():
+    """The documented bound itself."""
+    def call(n):
+        c = kv(page_tokens=64, kv_heads=1 << 10, head_dim=128)
+        b = batch(n_seqs=n, table_width=2, total_q=n, max_q=1, max_kv=64, q_starts=0x70000)
+        return lb.lib().lowbit_kv8_append(c, b, lb.BF16, A4, A16, 1 << 17, 1 << 17, None)
+
+    assert call(1 << 13) == lb.E_ALIGN
+    assert call((1 << 13) + 1) == lb.E_SHAPE

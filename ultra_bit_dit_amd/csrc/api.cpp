@@ -621,7 +621,7 @@ int lowbit_kv8_append(const lowbit_kv8* cache, const lowbit_kv8_batch* batch, in
   if (dtype != LOWBIT_F32 && dtype != LOWBIT_BF16) return LOWBIT_E_UNSUPPORTED;
   const int64_t row = (int64_t)a.H * a.D, most = int64_t(1) << 40;
   if (k_stride < row || v_stride < row || k_stride > most || v_stride > most) return LOWBIT_E_SHAPE;
-  if (a.n_seqs * kv8_span(a) * a.H > (1 << 23)) return LOWBIT_E_SHAPE;
+  if (!kv8_append_fits(a)) return LOWBIT_E_SHAPE;
   const int step = dtype == LOWBIT_F32 ? 4 : 8;
   if (!aligned(K, 16) || !aligned(V, 16) || k_stride % step != 0 || v_stride % step != 0) return LOWBIT_E_ALIGN;
   return hip_status(launch_kv8_append(a, dtype == LOWBIT_F32, K, V, k_stride, v_stride, (hipStream_t)stream));

@@ -18,6 +18,9 @@ typedef short v8s __attribute__((ext_vector_type(8)));
 
 __host__ __device__ inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// threads of one dimension of a launch, at most
+constexpr int64_t kMaxThreads = UINT32_MAX;
+
 // k offset inside a group of slot i (0..31) of quarter q (0..3): the order in
 // which the fp4 B operand of the 16x16x128 f8f6f4 MFMA consumes k relative
 // to the fp8 A operand (lane = row + 16 * quarter).
@@ -173,7 +176,7 @@ hipError_t launch_gemm_mxfp4(const MxGemmArgs& a, hipStream_t s);
 
 struct KvArgs;
 struct AttnArgs;
-int64_t kv8_span(const KvArgs& a);  // pages one sequence's new tokens can touch
+bool kv8_append_fits(const KvArgs& a);  // one launch holds its workgroups
 hipError_t launch_kv8_append(const KvArgs& a, bool f32, const void* K, const void* V, int64_t k_stride,
                              int64_t v_stride, hipStream_t s);
 // workgroups of an attention launch, and its workspace (counters included; 0: none)

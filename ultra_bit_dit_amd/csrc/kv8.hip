@@ -198,15 +198,20 @@ __global__ __launch_bounds__(THREADS) void kv8_append(KvArgs a, int64_t span, co
   }
 }
 
+// A page of one head in pieces of eight elements, a power of two from 128 to
+// 4096: HOLD of them (1, 2 or 4) to a thread.
+int64_t page_pieces(const KvArgs& a) { return ((int64_t)a.D << a.lp) / 8; }
+int append_threads(int64_t pieces) { return pieces <= 1024 ? 256 : (int)(pieces / 4); }
+
 template <bool F32, int D>
 hipError_t launch_d(const KvArgs& a, int64_t span, const void* K, const void* V, int64_t ks, int64_t vs,
                     hipStream_t s) {
-  const dim3 grid((unsigned)(a.n_seqs * span * a.H));
+  const int64_t pieces = page_pieces(a);
+  const dim3 grid((unsigned)(a.n_seqs * span * a.H)), block((unsigned)append_threads(pieces));
   const size_t lds = (size_t)D * ((1 << a.lp) + 4);
   const uint8_t *k = (const uint8_t*)K, *v = (const uint8_t*)V;
 #define LOWBIT_APPEND(THREADS, HOLD) \
-  hipLaunchKernelGGL((kv8_append<F32, D, THREADS, HOLD>), grid, dim3(THREADS), lds, s, a, span, k, v, ks, vs)
-  const int64_t pieces = ((int64_t)D << a.lp) / 8;  // a power of two from 128 to 4096
+  hipLaunchKernelGGL((kv8_append<F32, D, THREADS, HOLD>), grid, block, lds, s, a, span, k, v, ks, vs)
   if (pieces <= 256) LOWBIT_APPEND(256, 1);
   else if (pieces <= 512) LOWBIT_APPEND(256, 2);
   else if (pieces <= 1024) LOWBIT_APPEND(256, 4);
@@ -219,6 +224,11 @@ hipError_t launch_d(const KvArgs& a, int64_t span, const void* K, const void* V,
 }  // namespace
 
 int64_t kv8_span(const KvArgs& a) { return ((a.max_q + (int64_t(1) << a.lp) - 2) >> a.lp) + 1; }
+
+bool kv8_append_fits(const KvArgs& a) {
+  const int64_t groups = a.n_seqs * kv8_span(a) * a.H;
+  return groups <= (int64_t(1) << 23) && groups * append_threads(page_pieces(a)) <= kMaxThreads;
+}
 
 hipError_t launch_kv8_append(const KvArgs& a, bool f32, const void* K, const void* V, int64_t k_stride,
                              int64_t v_stride, hipStream_t s) {
