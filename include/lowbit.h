@@ -424,7 +424,8 @@ int lowbit_pack_mxfp4(int64_t rows, int64_t K, const uint8_t* codes, const uint8
  * codes 0, so every product that reads it is NaN.  values, if not NULL,
  * receives what the codes stand for, [rows][K] in x_dtype.  Weights (once) and
  * activations (per call) alike.  X, pcodes, pscales, values 16-byte aligned,
- * x_stride >= K and rows 16-byte aligned; the buffers do not overlap.
+ * x_stride >= K and rows 16-byte aligned; the buffers do not overlap.  rows <=
+ * 2^30 - 64.
  * Errors: E_NULL, E_UNSUPPORTED, E_SHAPE, E_ALIGN, E_HIP. */
 int lowbit_quantize_mxfp4(int64_t rows, int64_t K, int x_dtype, const void* X, int64_t x_stride,
                           void* pcodes, void* pscales, void* values, void* stream);

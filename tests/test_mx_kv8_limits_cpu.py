@@ -29,3 +29,14 @@ def test_append_workgroups_of_small_pages():
 
     assert call(1 << 13) == lb.E_ALIGN
     assert call((1 << 13) + 1) == lb.E_SHAPE
+
+
+def test_quantizer_rows():
+    def call(rows, K):
+        return lb.lib().lowbit_quantize_mxfp4(rows, K, lb.BF16, A4, K, A16, A16, None, None)
+
+    for K in (32, 256):
+        assert call(1 << 30, K) == lb.E_SHAPE
+        assert call((1 << 30) - 63, K) == lb.E_SHAPE
+        assert call((1 << 30) - 64, K) == lb.E_ALIGN
+    assert call(1 << 29, 512) == lb.E_ALIGN

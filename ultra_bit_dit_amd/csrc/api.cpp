@@ -478,7 +478,7 @@ int lowbit_rotate_act(int64_t M, int64_t K, const uint16_t* X_bf16, const int8_t
 
 namespace {
 
-// rows x K of an MXFP4 matrix: sizes far from overflow and within one grid
+// rows x K of an MXFP4 matrix: sizes far from overflow
 bool mx_shape_ok(int64_t rows, int64_t K) {
   return rows >= 1 && K >= kMxBlock && K % kMxBlock == 0 && rows <= (int64_t(1) << 30) &&
          K <= (int64_t(1) << 30) && rows <= (int64_t(1) << 38) / K;
@@ -506,7 +506,7 @@ int lowbit_quantize_mxfp4(int64_t rows, int64_t K, int x_dtype, const void* X, i
                           void* pscales, void* values, void* stream) {
   if (!X || !pcodes || !pscales) return LOWBIT_E_NULL;
   if (x_dtype != LOWBIT_F32 && x_dtype != LOWBIT_BF16) return LOWBIT_E_UNSUPPORTED;
-  if (!mx_shape_ok(rows, K)) return LOWBIT_E_SHAPE;
+  if (!mx_shape_ok(rows, K) || !quantize_mxfp4_fits(rows, K)) return LOWBIT_E_SHAPE;
   if (x_stride < K || x_stride > (int64_t(1) << 40)) return LOWBIT_E_SHAPE;
   const bool f32 = x_dtype == LOWBIT_F32;
   if (!aligned(X, 16) || x_stride % (f32 ? 4 : 8) != 0 || !aligned(pcodes, 16) || !aligned(pscales, 16) ||

@@ -155,6 +155,7 @@ hipError_t launch_rotate_act(int64_t M, int64_t K, const uint16_t* X, const int8
 
 // ---- MXFP4 (mx.hip, mx_gemm.hip) and the 8-bit cache (kv8.hip)
 
+bool quantize_mxfp4_fits(int64_t rows, int64_t K);  // one launch holds its workgroups
 hipError_t launch_quantize_mxfp4(int64_t rows, int64_t K, bool f32, const void* X, int64_t ld,
                                  void* pcodes, void* pscales, void* values, hipStream_t s);
 hipError_t launch_pack_mxfp4(int64_t rows, int64_t K, const uint8_t* codes, const uint8_t* scales,

@@ -174,9 +174,15 @@ __global__ __launch_bounds__(256) void pack_mxfp4(int64_t rows, int64_t K, int64
 
 }  // namespace
 
+namespace {
+int64_t quantize_units(int64_t rows, int64_t K) { return cdiv(rows, 16) * mx_quads(K); }
+}  // namespace
+
+bool quantize_mxfp4_fits(int64_t rows, int64_t K) { return cdiv(quantize_units(rows, K), 4) * 256 <= kMaxThreads; }
+
 hipError_t launch_quantize_mxfp4(int64_t rows, int64_t K, bool f32, const void* X, int64_t ld,
                                  void* pcodes, void* pscales, void* values, hipStream_t s) {
-  const int64_t units = cdiv(rows, 16) * mx_quads(K);
+  const int64_t units = quantize_units(rows, K);
   const dim3 grid((unsigned)cdiv(units, 4));
   if (f32)
     hipLaunchKernelGGL(quantize_mxfp4<true>, grid, dim3(256), 0, s, rows, K, ld, units, (const uint8_t*)X,
