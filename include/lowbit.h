@@ -437,7 +437,8 @@ int lowbit_quantize_mxfp4(int64_t rows, int64_t K, int x_dtype, const void* X, i
  *     in magnitude may count as 0.
  *   x_dtype MXFP4: X packed codes and x_pscales its packed scales
  *     (lowbit_quantize_mxfp4 of the M x K activations); x_stride ignored.
- * All pointers 16-byte aligned.  N <= 2^26, ceil(M/128) * ceil(N/128) <= 2^23.
+ * All pointers 16-byte aligned.  N <= 2^26, ceil(M/128) * ceil(N/128) <= 2^23
+ * (BF16 X: < 2^23).
  * Sums are added in a fixed order: repeated calls give the same bits.  Uses
  * the stream's workspace as lowbit_gemm does where K is split over workgroups
  * (lowbit_gemm_mxfp4_workspace: its bytes, 0 where none; reserve it before a

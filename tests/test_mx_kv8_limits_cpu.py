@@ -1,6 +1,8 @@
 """Sizes at the ends of what a launch holds (2^32 - 1 threads), on a machine
 without a GPU: one more is refused with E_SHAPE.  The largest accepted ones
 are shown by the check that comes after the sizes', a misaligned pointer."""
+import ctypes
+
 import pytest
 
 from ultra_bit_dit_amd import lowbit as lb
@@ -40,3 +42,21 @@ def test_quantizer_rows():
         assert call((1 << 30) - 63, K) == lb.E_SHAPE
         assert call((1 << 30) - 64, K) == lb.E_ALIGN
     assert call(1 << 29, 512) == lb.E_ALIGN
+
+
+@pytest.mark.parametrize("x,most", [(lb.BF16, (1 << 30) - 128), (lb.MXFP4, 1 << 30)])
+def test_product_tiles(x, most):
+    """ceil(M/128) ceil(N/128) <= 2^23, with bf16 X (512 threads a tile of 128 rows) < 2^23."""
+    L = lb.lib()
+    n = ctypes.c_size_t()
+
+    def call(M, N):
+        size = L.lowbit_gemm_mxfp4_workspace(M, N, 32, x, ctypes.byref(n))
+        run = L.lowbit_gemm_mxfp4(M, N, 32, A16, A16, x, A4, 32, A16, lb.F32, A16, None)
+        assert (size, run) in ((lb.OK, lb.E_ALIGN), (lb.E_SHAPE, lb.E_SHAPE)), (M, N, size, run)
+        return size
+
+    for M, N in ((most + 1, 16), (most + 1, 128), (1 << 30, 129), (1 << 23, (1 << 14) + 1), (1 << 10, 1 << 27)):
+        assert call(M, N) == lb.E_SHAPE
+    for M, N in ((most, 16), (most, 128), (1 << 29, 16), ((1 << 29) + 1, 100), (128, 1 << 26), (1 << 20, 1 << 16)):
+        assert call(M, N) == lb.OK

@@ -484,6 +484,12 @@ bool mx_shape_ok(int64_t rows, int64_t K) {
          K <= (int64_t(1) << 30) && rows <= (int64_t(1) << 38) / K;
 }
 
+// sizes of an MXFP4 product
+bool product_shape_ok(bool x4, int64_t M, int64_t N, int64_t K) {
+  return mx_shape_ok(N, K) && mx_shape_ok(M, K) && N <= (int64_t(1) << 26) &&
+         cdiv(M, 128) * cdiv(N, 128) <= (int64_t(1) << 23) && gemm_mxfp4_fits(x4, M, N, K);
+}
+
 }  // namespace
 
 int lowbit_mxfp4_bytes(int64_t rows, int64_t K, size_t* code_bytes, size_t* scale_bytes) {
@@ -524,8 +530,7 @@ int lowbit_gemm_mxfp4(int64_t M, int64_t N, int64_t K, const void* pcodes, const
   if (y_dtype != LOWBIT_F32 && y_dtype != LOWBIT_BF16) return LOWBIT_E_UNSUPPORTED;
   const bool x4 = x_dtype == LOWBIT_MXFP4;
   if (x4 && !x_pscales) return LOWBIT_E_NULL;
-  if (!mx_shape_ok(N, K) || !mx_shape_ok(M, K) || N > (int64_t(1) << 26)) return LOWBIT_E_SHAPE;
-  if (cdiv(M, 128) * cdiv(N, 128) > (int64_t(1) << 23)) return LOWBIT_E_SHAPE;
+  if (!product_shape_ok(x4, M, N, K)) return LOWBIT_E_SHAPE;
   if (!x4 && (x_stride < K || x_stride > (int64_t(1) << 40))) return LOWBIT_E_SHAPE;
   if (!aligned(pcodes, 16) || !aligned(pscales, 16) || !aligned(X, 16) || !aligned(Y, 16) ||
       (x4 && !aligned(x_pscales, 16)) || (!x4 && x_stride % 8 != 0))
@@ -555,9 +560,7 @@ int lowbit_gemm_mxfp4_workspace(int64_t M, int64_t N, int64_t K, int x_dtype, si
   if (!bytes) return LOWBIT_E_NULL;
   *bytes = 0;
   if (x_dtype != LOWBIT_BF16 && x_dtype != LOWBIT_MXFP4) return LOWBIT_E_UNSUPPORTED;
-  if (!mx_shape_ok(N, K) || !mx_shape_ok(M, K) || N > (int64_t(1) << 26) ||
-      cdiv(M, 128) * cdiv(N, 128) > (int64_t(1) << 23))
-    return LOWBIT_E_SHAPE;
+  if (!product_shape_ok(x_dtype == LOWBIT_MXFP4, M, N, K)) return LOWBIT_E_SHAPE;
   *bytes = gemm_mxfp4_workspace_bytes(x_dtype == LOWBIT_MXFP4, M, N, K);
   return LOWBIT_OK;
 }

@@ -172,6 +172,7 @@ struct MxGemmArgs {
   void* y;                  // [M][N]
   void* ws;                 // workspace (counters first), or NULL if it needs none
 };
+bool gemm_mxfp4_fits(bool x4, int64_t M, int64_t N, int64_t K);  // a launch holds its workgroups
 size_t gemm_mxfp4_workspace_bytes(bool x4, int64_t M, int64_t N, int64_t K);
 hipError_t launch_gemm_mxfp4(const MxGemmArgs& a, hipStream_t s);
 

@@ -727,6 +727,7 @@ struct Plan {
   size_t part_bytes;
 };
 
+// MT 0: no choice fits a launch
 Plan plan_gemm(bool x4, int64_t M, int64_t N, int64_t K) {
   Plan p{};
   if (M <= (x4 ? kSmallRows4 : kSmallRows)) {
@@ -754,6 +755,7 @@ Plan plan_gemm(bool x4, int64_t M, int64_t N, int64_t K) {
     const double busy = x4 ? (big ? 1.0 : 0.6) : (big ? 1.53 : 0.51), idle = x4 ? (big ? 0.65 : 0.29) : (big ? 1.28 : 0.47);
     for (int KS = 1; KS <= 16; KS *= 2) {
       if (KS > 1 && (GQ < 2 * KS || T * KS > 1024)) break;
+      if (T * (x4 && !big ? 256 : 512) > kMaxThreads) break;  // threads of its launch
       const double load = (double)(T * KS) / 256, groups = (double)cdiv(GQ, KS) * 4;
       const double split = KS > 1 ? 3.0 + (double)(T * KS) * sh.rm * sh.rn * 2048e-6 / 4.0 : 0.0;
       double c;
@@ -802,6 +804,12 @@ void launch_tile16(const MxArgs& a, int ykind, hipStream_t s) {
 }
 
 }  // namespace
+
+bool gemm_mxfp4_fits(bool x4, int64_t M, int64_t N, int64_t K) {
+  if (cdiv(M, 64) * cdiv(N, 128) < (int64_t(1) << 23)) return true;  // so many of the smallest tiles
+  const Plan p = plan_gemm(x4, M, N, K);
+  return p.small || p.MT > 0;
+}
 
 size_t gemm_mxfp4_workspace_bytes(bool x4, int64_t M, int64_t N, int64_t K) {
   const Plan p = plan_gemm(x4, M, N, K);
