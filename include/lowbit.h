@@ -454,7 +454,7 @@ int lowbit_gemm_mxfp4_workspace(int64_t M, int64_t N, int64_t K, int x_dtype, si
  * 阻む第一の壁：「1語生成するたびに全身を運び直す」": what a token re-reads):
  * keys and values as e4m3 codes in pages of 16, 32, 64 or 128 tokens, one
  * power of two per page and head for the keys and one for the values (bytes
- * e + 127).  Head sizes 64, 128, 256.
+ * e + 127, 0 .. 247 where tokens lie).  Head sizes 64, 128, 256.
  *   k_codes  [n_pages][kv_heads][page_tokens][head_dim]
  *   v_codes  [n_pages][kv_heads][head_dim][page_tokens]   (transposed)
  *   k_scales, v_scales  [n_pages][kv_heads]
@@ -500,7 +500,8 @@ typedef struct lowbit_kv8_batch {
  * sequence keeps e = max(e_old, e(a)), and where that rises its earlier codes
  * are rescaled (times 2^(e_old - e), rounded to nearest even: exact above
  * e4m3's subnormal range).  code = x / 2^e to nearest even, infinities to
- * +-448, NaN to NaN.  Bytes behind a sequence's last token stay as they were.
+ * +-448, NaN to NaN; at e = 120, where larger codes would stand for infinities,
+ * codes end at +-240.  Bytes behind a sequence's last token stay as they were.
  * A page that receives tokens must belong to one sequence of the batch and
  * stand in its table once (full pages may be shared by any number).  New tokens
  * that lie before the sequence's start (more of them than kv_lens) are not

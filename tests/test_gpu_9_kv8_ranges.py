@@ -1,11 +1,12 @@
 """The 8-bit cache at the ends of its number ranges: exponents that rise by
-any amount."""
+any amount, the largest finite values."""
 import numpy as np
 import pytest
 import torch
 
+import mx_ref as R
 from ultra_bit_dit_amd import lowbit as lb
-from test_gpu_9_kv8 import Cache, f64, i32
+from test_gpu_9_kv8 import Cache, f64, i32, tokens
 
 pytestmark = pytest.mark.gpu
 
@@ -48,3 +49,39 @@ def test_append_exponent_rises_by_any_amount(P, D, which, dtype):
             c.append(b, first, f64(K)[b * T:(b + 1) * T], f64(V)[b * T:(b + 1) * T])
         check_bits(c, "earlier" if first == 0 else "later")
     assert {1, 127, 128, 246} <= set((c.ks if which == "k" else c.vs)[c.table[:, 0], 0] + 127)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("D,P", [(64, 16), (128, 64), (256, 128)])
+@pytest.mark.parametrize("new", [1, 4, 150])
+def test_largest_finite_values(D, P, new, dtype):
+    """Values near the largest finite number stay finite in the cache (at e = 120 codes
+    end at 240) and, in tokens a row does not see, do not reach it."""
+    H, G, T = 1, 2, 170
+    print(f"largest values D={D} P={P} new={new} {dtype}", flush=True)
+    c = Cache([T], P, H, D, seed=2)
+    K, V = tokens(T, H, D, 5, dtype), tokens(T, H, D, 6, dtype)
+    top = torch.finfo(dtype).max
+    at = T - (new + 1) // 2          # half of the rows see it
+    V[at, 0, 3], V[at, 0, 4], V[at, 0, 5] = top, -top, float("inf")
+    K[at, 0, 7], K[at, 0, 8] = top, -float("inf")
+    lb.kv8_append(c.gpu, c.tables(), i32([T]), K, V)
+    kc, vc, ks, vs = c.gpu
+    pg, s = int(c.table[0, at // P]), at % P
+    assert int(vs[pg, 0]) == 247 and int(ks[pg, 0]) == 247
+    c.fresh()  # the cache as it is, in 64 bits
+    K64, V64 = c.read(0, T)
+    q = torch.randn(new, H * G, D, device="cuda").bfloat16()
+    q[:, :, 7:9] = 0                 # the large keys do not take part in the scores
+    O, lse = lb.attention_kv8(q, c.gpu, c.tables(), i32([T]), return_lse=True)
+    o, l, A, eps = R.attention(f64(q), K64, V64, T - new, D ** -0.5, True, 0)
+    got = f64(O)
+    hidden = np.arange(T - new, T) < at
+    tol = R.attention_tolerance(o, A, eps, T)
+    assert np.isfinite(got[hidden]).all()
+    assert np.all(np.abs(got - o)[hidden] <= tol[hidden])
+    rest = np.ones(D, bool)
+    rest[3:6] = False
+    assert np.all(np.abs(got - o)[~hidden][..., rest] <= tol[~hidden][..., rest])
+    assert vc[pg, 0, 3:6, s].float().tolist() == [240, -240, 240]
+    assert kc[pg, 0, s, 7:9].float().tolist() == [240, -240]

@@ -7,8 +7,8 @@
 // where it rises the earlier codes are multiplied by 2^(e_old - e) and
 // rounded again (exact unless a code falls below e4m3's normal range).
 // code = x / 2^e rounded to nearest even; an infinity becomes +-448, a NaN
-// the NaN code.  x / 2^e is exact in fp32, so codes and exponents do not
-// depend on the order of anything.
+// the NaN code; at e = 120 codes end at 240 (top_code).  x / 2^e is exact in
+// fp32, so codes and exponents do not depend on the order of anything.
 //
 // One workgroup per (sequence, page that receives tokens, head): it owns the
 // page's codes and exponents of that head, keys and values.  The new elements
@@ -34,8 +34,13 @@ __device__ __forceinline__ uint32_t page_byte(uint32_t a) {
   const int e = (int)(a >> 23) - 8 + ((a & 0x7FFFFFu) > 0x600000u ? 1 : 0);
   return e > 0 ? (uint32_t)e : 0u;
 }
-__device__ __forceinline__ float clamp448(float v) {
-  return fabsf(v) > 448.0f ? copysignf(448.0f, v) : v;  // NaN passes
+// The largest code of a page: 448, and where 448 2^e would lie beyond the finite
+// numbers (byte 247, values of 1.75 2^127 and more) the one that stands for
+// 1.875 2^127.  (Infinities in the cache would reach rows that do not see them, as 0
+// times them.)
+__device__ __forceinline__ float top_code(uint32_t byte) { return byte < 247u ? 448.0f : 240.0f; }
+__device__ __forceinline__ float clamp_code(float v, float top) {
+  return fabsf(v) > top ? copysignf(top, v) : v;  // NaN passes
 }
 // 2^-(byte - 127)
 __device__ __forceinline__ float inv_scale(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
@@ -142,7 +147,7 @@ __global__ __launch_bounds__(THREADS) void kv8_append(KvArgs a, int64_t span, co
     bk = max(bk, ok);
     bv = max(bv, ov);
   }
-  const float ik = inv_scale(bk), iv = inv_scale(bv);
+  const float ik = inv_scale(bk), iv = inv_scale(bv), tk = top_code(bk), tv = top_code(bv);
   uint8_t* kc = a.kc + ph * P * D;
   uint8_t* vc = a.vc + ph * P * D;
 #pragma unroll
@@ -152,8 +157,8 @@ __global__ __launch_bounds__(THREADS) void kv8_append(KvArgs a, int64_t span, co
     float x[8], y[8];
 #pragma unroll
     for (int e = 0; e < 8; e++) {
-      x[e] = clamp448(hk[c][e] * ik);
-      y[e] = clamp448(hv[c][e] * iv);
+      x[e] = clamp_code(hk[c][e] * ik, tk);
+      y[e] = clamp_code(hv[c][e] * iv, tv);
     }
     *(uint2*)(kc + t * D + d) = make_uint2(codes4(x[0], x[1], x[2], x[3]), codes4(x[4], x[5], x[6], x[7]));
     const uint32_t w0 = codes4(y[0], y[1], y[2], y[3]), w1 = codes4(y[4], y[5], y[6], y[7]);
