@@ -1,12 +1,12 @@
 """The 8-bit cache at the ends of its number ranges: exponents that rise by
-any amount, the largest finite values."""
+any amount, the largest finite values, scales of zero."""
 import numpy as np
 import pytest
 import torch
 
 import mx_ref as R
 from ultra_bit_dit_amd import lowbit as lb
-from test_gpu_9_kv8 import Cache, f64, i32, tokens
+from test_gpu_9_kv8 import Cache, f64, fill, i32, tokens
 
 pytestmark = pytest.mark.gpu
 
@@ -85,3 +85,28 @@ def test_largest_finite_values(D, P, new, dtype):
     assert np.all(np.abs(got - o)[~hidden][..., rest] <= tol[~hidden][..., rest])
     assert vc[pg, 0, 3:6, s].float().tolist() == [240, -240, 240]
     assert kc[pg, 0, s, 7:9].float().tolist() == [240, -240]
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("new", [1, 150])
+@pytest.mark.parametrize("scale", [0.0, -0.0])
+def test_scale_of_zero_keeps_nan_and_infinity(D, new, scale):
+    """0 times a NaN or an infinity of Q is NaN: such a row is NaN, the others
+    are the mean of what they see."""
+    P, H, G, T = 32, 1, 2, 200
+    print(f"scale {scale} D={D} new={new}", flush=True)
+    c = Cache([T], P, H, D, seed=4)
+    fill(c, [T], 6)
+    q = torch.randn(new, H * G, D, device="cuda").bfloat16()
+    bad = np.zeros((new, H * G), bool)
+    for r, h, v in ((0, 0, float("nan")), (new - 1, 1, float("inf")), (new // 2, 0, float("-inf"))):
+        q[r, h, 9] = v
+        bad[r, h] = True
+    O, lse = lb.attention_kv8(q, c.gpu, c.tables(), i32([T]), softmax_scale=scale, return_lse=True)
+    assert np.array_equal(np.isnan(f64(O)).all(2), bad) and np.array_equal(np.isnan(f64(O)).any(2), bad)
+    assert np.array_equal(np.isnan(f64(lse)), bad)
+    K, V = c.read(0, T)
+    clean = torch.where(torch.isfinite(q), q, torch.zeros_like(q))
+    o, l, A, eps = R.attention(f64(clean), K, V, T - new, scale, True, 0)
+    assert np.all((np.abs(f64(O) - o) <= R.attention_tolerance(o, A, eps, T))[~bad])
+    assert np.all((np.abs(f64(lse) - l) <= R.lse_tolerance(l, eps, T))[~bad])

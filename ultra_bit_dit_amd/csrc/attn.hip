@@ -54,6 +54,16 @@ __device__ __forceinline__ float group_max(float x) {
   const auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
   return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
 }
+// eight bf16 numbers times 0: infinities and NaN become NaN
+__device__ __forceinline__ mx_u4 zero_or_nan(mx_u4 w) {
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    const uint32_t lo = (w[i] & 0x7F80u) == 0x7F80u ? 0x7FC0u : 0u;
+    const uint32_t hi = (w[i] & 0x7F800000u) == 0x7F800000u ? 0x7FC00000u : 0u;
+    w[i] = (w[i] & 0x80008000u) | lo | hi;
+  }
+  return w;
+}
 // bytes of w that are e4m3 NaN codes (0x7F or 0xFF): bit 7 of each
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
   return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
@@ -734,7 +744,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attn_prompt(AttnArgs a) {
   const Seen mine = t.of_rows(a, rho0, rho0 + 16 * NC);  // by this wave's rows
   const int wlo = mine.lo, wlo_all = mine.lo_all, whi_all = mine.hi_all;
   const int whi = __builtin_amdgcn_readfirstlane(rho0 < R ? mine.hi : 0);
-  const bool none = fabsf(a.scale2) < 0x1p-126f;  // all scores 0
+  const bool none = fabsf(a.scale2) < 0x1p-126f;  // all scores 0, or NaN
   int rho[NC], vlo[NC], vhi[NC];
   v8bf qf[NC][DS];
 #pragma unroll
@@ -750,7 +760,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attn_prompt(AttnArgs a) {
       mx_u4 w = *(const mx_u4*)(qp + 64 * (d >> 1) + 8 * (d & 1));
       // the maximum and the mask's -infinity below want a positive scale
       if (a.scale2 < 0.f) w ^= 0x80008000u;
-      if (none) w &= 0x80008000u;
+      if (none) w = zero_or_nan(w);
       qf[c][d] = __builtin_bit_cast(v8bf, w);
     }
   }
@@ -1070,7 +1080,7 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void attn_prompt32(AttnArgs a) {
   const Seen mine = t.of_rows(a, rho0, rho0 + 32 * NC);  // by this wave's rows
   const int wlo = mine.lo, wlo_all = mine.lo_all, whi_all = mine.hi_all;
   const int whi = __builtin_amdgcn_readfirstlane(rho0 < R ? mine.hi : 0);
-  const bool none = fabsf(a.scale2) < 0x1p-126f;  // all scores 0
+  const bool none = fabsf(a.scale2) < 0x1p-126f;  // all scores 0, or NaN
   int rho[NC], vlo[NC], vhi[NC];
   v8bf qf[NC][DS];
 #pragma unroll
@@ -1333,12 +1343,15 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void attn_prompt32(AttnArgs a) {
   int pg0 = page_of(u0, e0), pg1 = page_of(u0 + 1, e1);
   if (u0 < u1) fetch(u0, pg0);
   // the maximum and the mask's -infinity want a positive scale
-  const uint32_t flip = a.scale2 < 0.f ? 0x80008000u : 0u, keep = none ? 0x80008000u : ~0u;
+  const uint32_t flip = a.scale2 < 0.f ? 0x80008000u : 0u;
 #pragma unroll
   for (int c = 0; c < NC; c++)
 #pragma unroll
-    for (int d = 0; d < DS; d++)
-      qf[c][d] = __builtin_bit_cast(v8bf, (__builtin_bit_cast(mx_u4, qf[c][d]) ^ flip) & keep);
+    for (int d = 0; d < DS; d++) {
+      mx_u4 w = __builtin_bit_cast(mx_u4, qf[c][d]) ^ flip;
+      if (none) w = zero_or_nan(w);
+      qf[c][d] = __builtin_bit_cast(v8bf, w);
+    }
   if (u0 < u1) stage(u0, pg0);
   meet();
   if (!keys) meet();
