@@ -1,5 +1,6 @@
 """The 8-bit cache at the ends of its number ranges: exponents that rise by
-any amount, the largest finite values, scales of zero."""
+any amount, the largest finite values, scales of zero
+and next to it."""
 import numpy as np
 import pytest
 import torch
@@ -110,3 +111,28 @@ def test_scale_of_zero_keeps_nan_and_infinity(D, new, scale):
     o, l, A, eps = R.attention(f64(clean), K, V, T - new, scale, True, 0)
     assert np.all((np.abs(f64(O) - o) <= R.attention_tolerance(o, A, eps, T))[~bad])
     assert np.all((np.abs(f64(lse) - l) <= R.lse_tolerance(l, eps, T))[~bad])
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("new", [1, 150])
+@pytest.mark.parametrize("scale", [2.0 ** -127, -2.0 ** -127])
+def test_subnormal_scale(D, new, scale):
+    """A scale below the normal numbers against keys and queries near 2^62 still weighs."""
+    P, H, G, T = 32, 1, 2, 200
+    print(f"scale {scale} D={D} new={new}", flush=True)
+    c = Cache([T], P, H, D, seed=4)
+    K, V = tokens(T, H, D, 7), tokens(T, H, D, 8)
+    K = (K.float().sign() * 2.0 ** 60).bfloat16()
+    lb.kv8_append(c.gpu, c.tables(), i32([T]), K, V)
+    c.append(0, 0, f64(K), f64(V))
+    q = (torch.randn(new, H * G, D, device="cuda").clamp(-3, 3) * 2.0 ** 63).bfloat16()
+    q[:, :, 20:] = 0  # |q k| <= 20 * 3 * 2^123: below 2^128.95, and below 2^128 for sums this far from all alike
+    O, lse = lb.attention_kv8(q, c.gpu, c.tables(), i32([T]), softmax_scale=scale, return_lse=True)
+    K64, V64 = c.read(0, T)
+    o, l, A, eps = R.attention(f64(q), K64, V64, T - new, scale, True, 0)
+    s = np.einsum("ihd,jd->ihj", f64(q), K64[:, 0]) * scale
+    assert 0.5 < np.abs(s).max() < 1.9  # scores that matter, sums below 2^128
+    # scale log2(e) is rounded to a multiple of 2^-149, half a step: 2^-23 of it, and the scores with it
+    eps = eps + 2.0 ** -22 * np.abs(s).max()
+    assert np.all(np.abs(f64(O) - o) <= R.attention_tolerance(o, A, eps, T))
+    assert np.all(np.abs(f64(lse) - l) <= R.lse_tolerance(l, eps, T))

@@ -744,7 +744,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attn_prompt(AttnArgs a) {
   const Seen mine = t.of_rows(a, rho0, rho0 + 16 * NC);  // by this wave's rows
   const int wlo = mine.lo, wlo_all = mine.lo_all, whi_all = mine.hi_all;
   const int whi = __builtin_amdgcn_readfirstlane(rho0 < R ? mine.hi : 0);
-  const bool none = fabsf(a.scale2) < 0x1p-126f;  // all scores 0, or NaN
+  const bool none = a.scale2 == 0.f;  // all scores 0, or NaN
   int rho[NC], vlo[NC], vhi[NC];
   v8bf qf[NC][DS];
 #pragma unroll
@@ -1080,7 +1080,7 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void attn_prompt32(AttnArgs a) {
   const Seen mine = t.of_rows(a, rho0, rho0 + 32 * NC);  // by this wave's rows
   const int wlo = mine.lo, wlo_all = mine.lo_all, whi_all = mine.hi_all;
   const int whi = __builtin_amdgcn_readfirstlane(rho0 < R ? mine.hi : 0);
-  const bool none = fabsf(a.scale2) < 0x1p-126f;  // all scores 0, or NaN
+  const bool none = a.scale2 == 0.f;  // all scores 0, or NaN
   int rho[NC], vlo[NC], vhi[NC];
   v8bf qf[NC][DS];
 #pragma unroll
