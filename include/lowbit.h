@@ -535,8 +535,8 @@ int lowbit_kv8_append(const lowbit_kv8* cache, const lowbit_kv8_batch* batch, in
  * Q, O 16-byte aligned, strides multiples of 8.  Uses the stream's workspace
  * (lowbit_attention_kv8_workspace bytes) as lowbit_gemv does; reserve it
  * before a capture.
- * Errors: E_NULL, E_UNSUPPORTED (page_tokens, head_dim, softmax_scale not
- * finite), E_SHAPE, E_ALIGN, E_NOMEM, E_HIP. */
+ * Errors: E_NULL, E_UNSUPPORTED (page_tokens, head_dim, softmax_scale
+ * log2(e) not finite), E_SHAPE, E_ALIGN, E_NOMEM, E_HIP. */
 int lowbit_attention_kv8(const lowbit_kv8* cache, const lowbit_kv8_batch* batch, int64_t q_heads,
                          const uint16_t* Q_bf16, int64_t q_stride, float softmax_scale, int causal,
                          int64_t window, uint16_t* O_bf16, int64_t o_stride, float* lse, void* stream);

@@ -60,3 +60,11 @@ def test_product_tiles(x, most):
         assert call(M, N) == lb.E_SHAPE
     for M, N in ((most, 16), (most, 128), (1 << 29, 16), ((1 << 29) + 1, 100), (128, 1 << 26), (1 << 20, 1 << 16)):
         assert call(M, N) == lb.OK
+
+
+@pytest.mark.parametrize("scale,status", [(2.35e38, lb.E_ALIGN), (2.37e38, lb.E_UNSUPPORTED), (-2.37e38, lb.E_UNSUPPORTED),
+                                          (3.4e38, lb.E_UNSUPPORTED)])
+def test_scale_whose_base_2_form_is_infinite(scale, status):
+    """scale log2(e) has to be finite, as 0 times it has to be 0."""
+    f = lb.lib().lowbit_attention_kv8
+    assert f(kv(), batch(), 4, A4, 256, scale, 1, 0, A16, 256, None, None) == status

@@ -652,7 +652,8 @@ int lowbit_attention_kv8(const lowbit_kv8* cache, const lowbit_kv8_batch* batch,
   if (!attention_heads_ok(a.kv, q_heads)) return LOWBIT_E_SHAPE;
   const int64_t row = q_heads * a.kv.D, most = int64_t(1) << 40;
   if (q_stride < row || o_stride < row || q_stride > most || o_stride > most) return LOWBIT_E_SHAPE;
-  if (!(softmax_scale - softmax_scale == 0.0f)) return LOWBIT_E_UNSUPPORTED;  // infinite or NaN
+  a.scale2 = softmax_scale * 1.4426950408889634f;
+  if (!(a.scale2 - a.scale2 == 0.0f)) return LOWBIT_E_UNSUPPORTED;  // infinite or NaN
   if (window < 0) return LOWBIT_E_SHAPE;
   a.G = q_heads / a.kv.H;
   if (!aligned(Q_bf16, 16) || !aligned(O_bf16, 16) || q_stride % 8 != 0 || o_stride % 8 != 0 ||
@@ -661,7 +662,6 @@ int lowbit_attention_kv8(const lowbit_kv8* cache, const lowbit_kv8_batch* batch,
   a.Hq = q_heads;
   a.q = Q_bf16;
   a.q_stride = q_stride;
-  a.scale2 = softmax_scale * 1.4426950408889634f;
   a.causal = causal ? 1 : 0;
   a.window = window > (1 << 30) ? 0 : (int)window;  // wider than any sequence
   a.o = O_bf16;
