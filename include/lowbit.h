@@ -524,10 +524,12 @@ int lowbit_kv8_append(const lowbit_kv8* cache, const lowbit_kv8_batch* batch, in
  * and lse = -infinity (so does one whose scores are all -infinity, which takes
  * an infinity in Q); what lies in tokens a row does not see (NaN codes too)
  * does not reach it.  With causal == 0 the cache may hold another sequence (an
- * encoder's states) of its own length.  Weights enter the second
- * product rounded to bf16; sums and statistics are fp32.  Results do not
- * depend on the order in which workgroups run.  Rows of sequences behind the
- * last q_starts entry are not written.
+ * encoder's states) of its own length.  Sums and
+ * statistics are fp32.  Weights enter the second product as bf16: in two terms
+ * (16 bits) in calls of few rows a sequence and key head, such as single
+ * tokens, rounded once (8 bits, as O) in calls of many.  Results do not depend
+ * on the order in which workgroups run.  Rows of sequences behind the last
+ * q_starts entry are not written.
  * One call runs one kernel for all its sequences, chosen by max_q * q_heads /
  * kv_heads and max_kv: long contexts with single tokens and prompts of many
  * rows are faster as two calls, each with a max_q of its own.

@@ -1,6 +1,6 @@
 """The 8-bit cache at the ends of its number ranges: exponents that rise by
 any amount, the largest finite values, scales of zero
-and next to it."""
+and next to it, and how finely attention with few rows weighs."""
 import numpy as np
 import pytest
 import torch
@@ -136,3 +136,40 @@ def test_subnormal_scale(D, new, scale):
     eps = eps + 2.0 ** -22 * np.abs(s).max()
     assert np.all(np.abs(f64(O) - o) <= R.attention_tolerance(o, A, eps, T))
     assert np.all(np.abs(f64(lse) - l) <= R.lse_tolerance(l, eps, T))
+
+
+@pytest.mark.parametrize("D,G", [(64, 4), (64, 20), (128, 4), (128, 16), (256, 6)])
+@pytest.mark.parametrize("lens", [[16] * 9, [16, 4000, 14, 2, 900]])
+def test_single_tokens_are_weighed_finely(D, G, lens):
+    """Values that cancel in pairs of keys that are nearly alike: what is left is
+    the difference of their weights, far below one weight's half step of bf16.
+    Weights enter the second product in two bf16 terms, so a weight is off by at
+    most 2^-8 of 2^-8."""
+    P, H = 16, 2
+    print(f"weights D={D} G={G} lens={lens}", flush=True)
+    c = Cache(lens, P, H, D, seed=9)
+    B, most = len(lens), max(lens)
+    g = np.random.default_rng(D + G)
+    K = np.zeros((B, most, H, D))
+    for b, n in enumerate(lens):
+        base = g.standard_normal((n // 2, H, D)) * 0.1
+        K[b, :n] = np.repeat(base, 2, 0) + g.standard_normal((n, H, D)) * 0.02
+    V = np.where(np.arange(most) % 2 == 0, 1.0, -1.0)[None, :, None, None] * np.ones((B, 1, H, D))
+    starts = np.concatenate([[0], np.cumsum(lens)])
+    flat = lambda x: torch.from_numpy(np.concatenate([x[b, :n] for b, n in enumerate(lens)]).astype(np.float32)).cuda()
+    Kt, Vt = flat(K), flat(V)
+    lb.kv8_append(c.gpu, c.tables(), i32(lens), Kt, Vt, q_starts=i32(starts), max_q=most)
+    for b, n in enumerate(lens):
+        c.append(b, 0, f64(Kt)[starts[b]:starts[b + 1]], f64(Vt)[starts[b]:starts[b + 1]])
+    q = torch.randn(B, H * G, D, device="cuda", generator=torch.Generator(device="cuda").manual_seed(G)).bfloat16()
+    wide = torch.full((B, 40000 // P), -77, dtype=torch.int32, device="cuda")  # a loose bound: the kernel of few rows
+    wide[:, :c.width] = c.tables()
+    O = f64(lb.attention_kv8(q, c.gpu, wide, i32(lens)))
+    for b, n in enumerate(lens):
+        K64, V64 = c.read(b, n)
+        o, _, A, eps = R.attention(f64(q[b:b + 1]), K64, V64, n - 1, D ** -0.5, True, 0)
+        # scores off by eps, a weight by 2^-16 (and 2^-126 where a term is subnormal), n of them
+        # added in fp32, one rounding of the output
+        tol = (2.5 * eps[..., None] + 2.0 ** -16 * 1.01 + (n + 64) * 2.0 ** -22) * A + 2.0 ** -8 * np.abs(o) + n * 2.0 ** -126
+        bad = ~(np.abs(O[b] - o[0]) <= tol[0])
+        assert not bad.any(), f"sequence {b}: {int(bad.sum())} of {bad.size} off, {O[b][bad][0]} for {o[0][bad][0]} +- {tol[0][bad][0]}"

@@ -12,9 +12,14 @@
 // g = L / 16 holds 16 consecutive tokens, which is what the B operand of
 // O^T = V^T P^T needs: no exchange between the products, 16 tokens of one
 // row of V are one 16-byte load, and (pages hold 16 tokens or more) one
-// exponent ek and ev per lane and step.  Weights are rounded to bf16 (relative
-// error 2^-9 of each, the same size as the output's own rounding);
-// statistics, sums and O stay in fp32.
+// exponent ek and ev per lane and step.  Statistics, sums and O stay in fp32.
+// Weights become bf16 for the second product: with few rows, where memory is the
+// bound, in two terms, what the first leaves being the second (off by 2^-16 at
+// most; 0.2 to 0.4 us a call more than one term, 1% of long ones, 5% with 32 rows a
+// wave: 16 x 5 tokens in 2048, D = 64, 19.2 -> 20.1 us); with many rows, where the
+// products are, rounded once (off by 2^-8 at most, the output's own rounding): a
+// second term would take 2 x 4096 rows, 40 heads over 8, D = 128, from 383 to 497 us
+// and attn_prompt32<64> out of its registers (221 -> 511 us).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -354,7 +359,7 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
         pvu = pvn;
         if (u + 2 * kDecWaves < u1) next_pages(u + 2 * kDecWaves);
       }
-      v8bf pf[NC][2];
+      v8bf pf[NC][2][2];  // weights in two bf16 terms
       uint32_t seen[NC];  // bit e: token 16 g + e is visible to the lane's row
 #pragma unroll
       for (int c = 0; c < NC; c++) {
@@ -391,7 +396,11 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
           l[c] += p[e];
         }
 #pragma unroll
-        for (int e = 0; e < 16; e++) pf[c][e >> 3][e & 7] = (__bf16)p[e];
+        for (int e = 0; e < 16; e++) {
+          const __bf16 hi = (__bf16)p[e];
+          pf[c][e >> 3][0][e & 7] = hi;
+          pf[c][e >> 3][1][e & 7] = (__bf16)(p[e] - (float)hi);
+        }
       }
       if (part) {
         // Tokens no row sees: their codes may be anything, so they become 0.
@@ -442,8 +451,11 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
         const v8bf v0 = bf16x8_of_e4m3(vr[d].x, vr[d].y, sv), v1 = bf16x8_of_e4m3(vr[d].z, vr[d].w, sv);
 #pragma unroll
         for (int c = 0; c < NC; c++) {
-          o[c][d] = mfma(v0, pf[c][0], o[c][d]);
-          o[c][d] = mfma(v1, pf[c][1], o[c][d]);
+#pragma unroll
+          for (int t = 0; t < 2; t++) {
+            o[c][d] = mfma(v0, pf[c][0][t], o[c][d]);
+            o[c][d] = mfma(v1, pf[c][1][t], o[c][d]);
+          }
         }
       }
       if (u + kDecWaves < u1) load_v(u + kDecWaves, pvu);
