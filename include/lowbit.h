@@ -434,7 +434,8 @@ int lowbit_quantize_mxfp4(int64_t rows, int64_t K, int x_dtype, const void* X, i
  * whole prompts), fp32 accumulation, Y [M][N] in y_dtype F32 or BF16.
  *   x_dtype BF16: X bf16, rows x_stride elements apart (>= K, a multiple of
  *     8); the products of each pair are exact in fp32.  Weights below 2^-126
- *     in magnitude may count as 0.
+ *     in magnitude may count as 0, of 2^128 and more (bytes 253, 254, which
+ *     lowbit_quantize_mxfp4 does not write) as infinities.
  *   x_dtype MXFP4: X packed codes and x_pscales its packed scales
  *     (lowbit_quantize_mxfp4 of the M x K activations); x_stride ignored.
  * All pointers 16-byte aligned.  N <= 2^26, ceil(M/128) * ceil(N/128) <= 2^23

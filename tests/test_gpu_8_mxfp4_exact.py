@@ -2,11 +2,9 @@
 whole numbers of a common step and small enough that every partial sum, in any
 order, is a multiple of that step below 2^24 of it.  A sum held or joined in
 fewer bits anywhere on the way shows."""
-import numpy as np
 import pytest
 import torch
 
-import mx_ref as R
 from ultra_bit_dit_amd import lowbit as lb
 
 pytestmark = pytest.mark.gpu
@@ -91,3 +89,18 @@ def test_exponents_of_both_operands_at_the_ends(M, N, K):
         xc, xs, xv = operand(M, K, spread(M, K, x, x, g), g)
         y = lb.gemm_mxfp4(M, N, K, wc, ws, xc, x_scales=xs)
         assert torch.equal(y.double(), xv @ wv.t().contiguous()), (w, x)
+
+
+@pytest.mark.parametrize("M,N,K", [(3, 16, 96), (90, 200, 672), (300, 600, 672)])
+def test_largest_exponents_with_bf16_x(M, N, K):
+    """Bytes 253 and 254, codes whose values are below 2^128: counted exactly."""
+    g = torch.Generator(device="cuda").manual_seed(M)
+    for byte, top in ((253, 6), (254, 4)):  # magnitudes below 4, below 2
+        print(f"byte {byte} M={M} N={N} K={K}", flush=True)
+        codes = torch.randint(0, top, (N, K), generator=g, device="cuda", dtype=torch.uint8)
+        codes |= torch.randint(0, 2, (N, K), generator=g, device="cuda", dtype=torch.uint8) << 3
+        wc, ws = lb.pack_mxfp4((codes[:, 0::2] | (codes[:, 1::2] << 4)).contiguous(), spread(N, K, byte, byte, g))
+        wv = TABLE.cuda()[codes.long()] * 2.0 ** (byte - 127)
+        xv = torch.randint(-8, 9, (M, K), generator=g, device="cuda").double() * 2.0 ** -60
+        y = lb.gemm_mxfp4(M, N, K, wc, ws, xv.bfloat16())
+        assert torch.equal(y.double(), xv @ wv.t().contiguous())
