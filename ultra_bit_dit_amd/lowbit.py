@@ -304,6 +304,15 @@ def _raw_stream(T, dev, stream):
     return T._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
+def _empty(T, shape, dtype, device, stream):
+    """An output of a call on `stream`: memory of that stream, which no work still queued
+    on the current one uses."""
+    if stream is None:
+        return T.empty(shape, dtype=dtype, device=device)
+    with T.cuda.stream(stream):
+        return T.empty(shape, dtype=dtype, device=device)
+
+
 def _mx_sizes(rows, K):
     if rows < 1 or K < 32 or K % 32:
         raise LowbitError("lowbit_mxfp4_bytes", E_SHAPE)
@@ -343,9 +352,12 @@ def pack_mxfp4(codes, scales, pcodes=None, pscales=None, stream=None):
             or not codes.is_contiguous() or not scales.is_contiguous()):
         raise ValueError("pack_mxfp4: contiguous uint8 codes [rows][K/2] and scales [rows][K/32]")
     if pcodes is None:
-        pcodes, pscales = empty_mxfp4(rows, K, codes.device)
-    _mx_packed(T, pcodes, pscales, rows, K, "pack_mxfp4")
-    _device(T, codes.get_device(), scales, pcodes, pscales)
+        sizes = _mx_sizes(rows, K)
+        _device(T, codes.get_device(), scales)
+        pcodes, pscales = (_empty(T, n, T.uint8, codes.device, stream) for n in sizes)
+    else:
+        _mx_packed(T, pcodes, pscales, rows, K, "pack_mxfp4")
+        _device(T, codes.get_device(), scales, pcodes, pscales)
     _check("lowbit_pack_mxfp4", lib().lowbit_pack_mxfp4(rows, K, _ptr(codes), _ptr(scales), _ptr(pcodes),
                                                         _ptr(pscales), _stream(stream)))
     return pcodes, pscales
@@ -362,15 +374,15 @@ def quantize_mxfp4(X, values=False, pcodes=None, pscales=None, stream=None):
     dev = X.get_device()
     if pcodes is None:
         cb, sb = _mx_sizes(rows, K)
-        pcodes = T.empty(cb, dtype=T.uint8, device=X.device)
-        pscales = T.empty(sb, dtype=T.uint8, device=X.device)
         _device(T, dev)
+        pcodes = _empty(T, cb, T.uint8, X.device, stream)
+        pscales = _empty(T, sb, T.uint8, X.device, stream)
     else:
         _mx_packed(T, pcodes, pscales, rows, K, "quantize_mxfp4")
         _device(T, dev, pcodes, pscales)
     vals = None
     if values is True:
-        vals = T.empty((rows, K), dtype=X.dtype, device=X.device)
+        vals = _empty(T, (rows, K), X.dtype, X.device, stream)
     elif values is not False and values is not None:
         vals = values
         if vals.shape != X.shape or vals.dtype != X.dtype or not vals.is_contiguous() or vals.get_device() != dev:
@@ -397,11 +409,11 @@ def gemm_mxfp4(M, N, K, pcodes, pscales, X, x_scales=None, y_dtype=F32, Y=None, 
         if X.dtype != T.bfloat16 or X.shape != (M, K) or X.stride(1) != 1:
             raise ValueError("gemm_mxfp4: X is bf16 [M][K] with contiguous rows, or packed codes with x_scales")
         xd, ld, xs = BF16, X.stride(0) if M > 1 else K, None
-    if Y is None:
-        Y = T.empty((M, N), dtype=T.float32 if y_dtype == F32 else _ytorch(y_dtype), device=pcodes.device)
-    elif Y.shape != (M, N) or Y.dtype != _ytorch(y_dtype) or not Y.is_contiguous():
+    if Y is not None and (Y.shape != (M, N) or Y.dtype != _ytorch(y_dtype) or not Y.is_contiguous()):
         raise ValueError("gemm_mxfp4: Y is contiguous [M][N] of y_dtype")
     _device(T, dev, pscales, X, x_scales, Y)
+    if Y is None:
+        Y = _empty(T, (M, N), T.float32 if y_dtype == F32 else _ytorch(y_dtype), pcodes.device, stream)
     rc = _fast.gemm_mxfp4(M, N, K, pcodes.data_ptr(), pscales.data_ptr(), xd, X.data_ptr(), ld, xs, y_dtype,
                           Y.data_ptr(), _raw_stream(T, dev, stream))
     if rc:
@@ -508,7 +520,7 @@ def attention_kv8(Q, cache, page_table, kv_lens, q_starts=None, max_q=None, max_
     qs = _heads(Q, Hq, D, "Q")
     c, b, dev = _kv8(T, cache, page_table, kv_lens, q_starts, tokens, max_q, max_kv, bad_pages)
     if O is None:
-        O = T.empty((tokens, Hq, D), dtype=T.bfloat16, device=Q.device)
+        O = _empty(T, (tokens, Hq, D), T.bfloat16, Q.device, stream)
         os = Hq * D
     else:
         if O.shape != Q.shape or O.dtype != T.bfloat16 or O.get_device() != dev:
@@ -516,7 +528,7 @@ def attention_kv8(Q, cache, page_table, kv_lens, q_starts=None, max_q=None, max_
         os = _heads(O, Hq, D, "O")
     if lse is None:
         if return_lse:
-            lse = T.empty((tokens, Hq), dtype=T.float32, device=Q.device)
+            lse = _empty(T, (tokens, Hq), T.float32, Q.device, stream)
     elif lse.shape != (tokens, Hq) or lse.dtype != T.float32 or not lse.is_contiguous() or lse.get_device() != dev:
         raise ValueError("lse: contiguous fp32 [tokens][q_heads] on Q's device")
     if Q.get_device() != dev:
