@@ -1,6 +1,6 @@
 """Calls on a stream that is not the current one: what the binding allocates
 belongs to the call's stream, so work queued on the current stream that still
-uses freed memory cannot write into it."""
+uses freed memory cannot write into it; a stream of another device is refused."""
 import pytest
 import torch
 
@@ -54,3 +54,26 @@ def test_outputs_belong_to_the_calls_stream(make):
     torch.cuda.synchronize()
     for g, w in zip(got, want):
         assert torch.equal(g.view(torch.uint8), w.view(torch.uint8)), make.__name__
+
+
+class OtherDevice:
+    cuda_stream, device_index = 0, 1
+
+
+@pytest.mark.parametrize("make", [quantize, product, packed, attention])
+def test_stream_of_another_device_is_refused(make):
+    print(f"{make.__name__} on a stream of another device", flush=True)
+    call = make(None)
+    with pytest.raises(ValueError):
+        call(stream=OtherDevice())
+
+
+def test_append_on_a_stream_of_another_device_is_refused():
+    print("append on a stream of another device", flush=True)
+    c = Cache([20], 16, 2, 64, seed=1)
+    k = torch.randn(20, 2, 64, device="cuda").bfloat16()
+    before = [t.clone() for t in c.gpu]
+    with pytest.raises(ValueError):
+        lb.kv8_append(c.gpu, c.tables(), i32([20]), k, k, stream=OtherDevice())
+    torch.cuda.synchronize()
+    assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(before, c.gpu))

@@ -300,8 +300,14 @@ def _device(T, dev, *tensors):
         raise ValueError(f"tensors on device {dev}: calls take tensors of the current GPU")
 
 
+def _of_device(stream, dev):
+    if stream.device_index != dev:
+        raise ValueError(f"a stream of GPU {stream.device_index} for tensors of GPU {dev}")
+    return stream
+
+
 def _raw_stream(T, dev, stream):
-    return T._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    return T._C._cuda_getCurrentRawStream(dev) if stream is None else _of_device(stream, dev).cuda_stream
 
 
 def _empty(T, shape, dtype, device, stream):
@@ -309,7 +315,7 @@ def _empty(T, shape, dtype, device, stream):
     on the current one uses."""
     if stream is None:
         return T.empty(shape, dtype=dtype, device=device)
-    with T.cuda.stream(stream):
+    with T.cuda.stream(_of_device(stream, device.index)):
         return T.empty(shape, dtype=dtype, device=device)
 
 
@@ -358,8 +364,8 @@ def pack_mxfp4(codes, scales, pcodes=None, pscales=None, stream=None):
     else:
         _mx_packed(T, pcodes, pscales, rows, K, "pack_mxfp4")
         _device(T, codes.get_device(), scales, pcodes, pscales)
-    _check("lowbit_pack_mxfp4", lib().lowbit_pack_mxfp4(rows, K, _ptr(codes), _ptr(scales), _ptr(pcodes),
-                                                        _ptr(pscales), _stream(stream)))
+    _check("lowbit_pack_mxfp4", lib().lowbit_pack_mxfp4(rows, K, _ptr(codes), _ptr(scales), _ptr(pcodes), _ptr(pscales),
+                                                        _raw_stream(T, codes.get_device(), stream)))
     return pcodes, pscales
 
 
