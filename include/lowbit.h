@@ -534,7 +534,9 @@ int lowbit_kv8_append(const lowbit_kv8* cache, const lowbit_kv8_batch* batch, in
  * One call runs one kernel for all its sequences, chosen by max_q * q_heads /
  * kv_heads and max_kv: long contexts with single tokens and prompts of many
  * rows are faster as two calls, each with a max_q of its own.
- * max_q * q_heads / kv_heads <= 2^30; O does not overlap Q or the cache.
+ * max_q * q_heads / kv_heads <= 2^30, and n_seqs * kv_heads * ceil(max_q *
+ * q_heads / kv_heads / 128) <= 2^22 (calls of few rows: any).  O does not overlap
+ * Q or the cache.  Keys and values below 2^-126 in magnitude may count as 0.
  * Q, O 16-byte aligned, strides multiples of 8.  Uses the stream's workspace
  * (lowbit_attention_kv8_workspace bytes) as lowbit_gemv does; reserve it
  * before a capture.

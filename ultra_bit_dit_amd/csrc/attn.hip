@@ -165,8 +165,10 @@ struct ItemScan {
 // the next: 4 x 4 tokens in contexts of 777 23.1 us, with blocks 14.0 us; one
 // token in 16000, D = 256, 28.1 and 23.4 us.)  Bound by memory: 32 tokens in
 // ragged contexts up to 16384, 40 heads over 8, D = 128, 135 us (695 MB, 5.1
-// TB/s); one in 131071, 24 heads over 4, D = 256, 58 us (268 MB, 4.6 TB/s); one
-// in 512, 32 heads over 8, 10.7 us: start, one block a workgroup, the join.
+// TB/s); one in 131071, 24 heads over 4, D = 256, 65 us (268 MB, 4.1 TB/s; 57 us
+// where the same cache was read just before and part of it lies in the last-level
+// cache); 64 in 8192, 16 heads over 4, D = 64, 58 us (268 MB, 4.6 TB/s); one in 512,
+// 32 heads over 8, 10.9 us: start, one block a workgroup, the join.
 constexpr int kJoinLoads = 8;   // results of a pair of outputs read at once
 constexpr int kMaxJoin = 32;    // results joined by one workgroup: shares of a tile <= kMaxJoin^2
 constexpr int kMaxShares = 512;
@@ -182,7 +184,9 @@ __device__ __forceinline__ float2 get2(const float* p) {
 }
 
 // Four waves, so that two workgroups share a compute unit where a wave fits
-// 256 registers and one starts or ends while the other reads.
+// 256 registers and one starts or ends while the other reads.  D = 128 fills them:
+// one is spilled, written before the first tile and read back behind a tile's
+// steps; some 110 scalars of every variant lie in lanes of vector registers.
 constexpr int kDecWaves = 4;
 constexpr int kBlock = kUnit * kDecWaves;  // tokens of a block: a step of every wave
 
@@ -1066,8 +1070,10 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attn_prompt(AttnArgs a) {
 // products that begin with their operands read ahead across the phases took the
 // same time, and weights without their exponentials 98%.  D = 64, causal: 342 us
 // with 16 x 16 products, 315 us with 8 waves, 266 us with 4 waves and three
-// workgroups a compute unit (the exponentials bound it, and more waves hide
-// their latency).
+// workgroups a compute unit: more waves hide latency.  Its products keep the MFMA
+// busy in 24% of the cycles, LDS is active in 20%; vector instructions take 47% at
+// four cycles each and the exponentials' quarter rate some 17% more (2 x 4096 in
+// 4096, 32 heads over 8: 226 us).  One register is spilled.
 template <int D, int NC, int WAVES, int OCC>
 __global__ __launch_bounds__(64 * WAVES, OCC) void attn_prompt32(AttnArgs a) {
   constexpr int DS = D / 16, DT = D / 32, HALF = 32 * WAVES, SP = 4 * D / HALF, PS = WAVES / 4;
@@ -1507,6 +1513,7 @@ struct Plan {
 // for all rows, but widens it for 128 or 256 of them and joins its parts by
 // another launch.  So the choice goes by the rows of a head and the steps of all
 // heads.  us, attn_decode / attn_prompt, 32 heads over 8 (D = 256: 24 over 4):
+// (attn_decode with one bf16 term of the weights; the second takes 0.2 to 0.4 us more)
 //   D = 64   4 rows, 1 x 1024 9.4 / 10.3; 16 rows 11.1 / 10.9, 1 x 4096 13.9 / 14.6
 //            20 rows, 1 x 4096 17.4 / 14.6, 16 x 2048 19.4 / 20.8
 //            40 rows, 1 x 4096 19.6 / 14.9, 64 x 2048 53 / 58, 1 x 32768 26 / 41

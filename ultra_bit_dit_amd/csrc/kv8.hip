@@ -17,7 +17,7 @@
 // heads of 128: bf16 into pages of 16 20.2 us (75 MB: 3.7 TB/s; reading twice
 // 26.0 us), of 64 19.1 (24.2), fp32 23.8 us (5.3 TB/s; 35.9); 4 heads of 256 into
 // pages of 128 26.4 us (49.4).  Loads in a chain (length, page, elements) bound the
-// small pages and one token a sequence (64 of them: 6.7 us).
+// small pages and one token a sequence (64 of them: 7.0 us).
 #include <hip/hip_runtime.h>
 
 #include "kv8.hpp"

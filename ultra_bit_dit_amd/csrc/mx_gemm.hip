@@ -390,9 +390,10 @@ __global__ __launch_bounds__(256) void mx_reduce(MxArgs a) {
 }
 
 // X MXFP4.  WN x WM waves, each JN row-blocks of W by IM of X.  256 x 256 tiles:
-// a group's 96 KiB of LDS reads (768 cycles) stay behind its products (1024);
-// 128 x 128 where those would leave compute units idle.  4608 x 34816 x 5120 430
-// us (3.8 PFLOP/s): products are 44% of the cycles at the 2.0 GHz that they leave.
+// a group is 96 KiB of LDS reads and 1024 cycles of products on each SIMD, one after
+// the other as all waves leave one barrier together; 128 x 128 where those would
+// leave compute units idle.  4608 x 34816 x 5120 430 us (3.8 PFLOP/s) back to back:
+// the MFMA is busy in 44% of the cycles, at 2.0 GHz.
 template <int WN, int WM, int JN, int IM, int YK>
 __global__ __launch_bounds__(64 * WN * WM) void mx_gemm4(MxArgs a) {
 #if defined(__HIP_DEVICE_COMPILE__)

@@ -500,7 +500,9 @@ def kv8_append(cache, page_table, kv_lens, K, V, q_starts=None, max_q=None, max_
                stream=None):
     """Write new keys and values [tokens][kv_heads][dim] (bf16 or fp32, tokens may be strided) into the
     cache (see lowbit_kv8_append).  kv_lens counts them already; q_starts None: every sequence has
-    tokens / sequences new ones."""
+    tokens / sequences new ones.  max_q and max_kv bound one sequence's new tokens and length and size
+    the launch: without them, with q_starts, all the tokens (pass max_q for a batch of sequences), and
+    the whole page table."""
     T = _torch or _load()
     _, H, _, D = cache[0].shape
     ks, vs = _heads(K, H, D, "K"), _heads(V, H, D, "V")
@@ -517,7 +519,10 @@ def kv8_append(cache, page_table, kv_lens, K, V, q_starts=None, max_q=None, max_
 def attention_kv8(Q, cache, page_table, kv_lens, q_starts=None, max_q=None, max_kv=None, softmax_scale=None,
                   causal=True, window=0, O=None, lse=None, return_lse=False, bad_pages=None, stream=None):
     """Attention of bf16 queries [tokens][q_heads][dim] (tokens may be strided) over the cache (see
-    lowbit_attention_kv8); softmax_scale None: 1 / sqrt(dim).  Returns O, or (O, lse) with return_lse."""
+    lowbit_attention_kv8); softmax_scale None: 1 / sqrt(dim).  Returns O, or (O, lse) with return_lse.
+    max_q and max_kv bound one sequence's new tokens and length; they size the launch and choose its
+    kernel.  Without them, with q_starts, max_q is all the tokens: single tokens of many sequences
+    passed so run as prompts; max_kv is the whole page table."""
     T = _torch or _load()
     D = cache[0].shape[3]
     if Q.dim() != 3 or Q.dtype != T.bfloat16:
