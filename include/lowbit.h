@@ -548,6 +548,102 @@ int lowbit_attention_kv8(const lowbit_kv8* cache, const lowbit_kv8_batch* batch,
 int lowbit_attention_kv8_workspace(const lowbit_kv8* cache, const lowbit_kv8_batch* batch, int64_t q_heads,
                                    size_t* bytes);
 
+/* =====================  heads of queries and keys  ========================
+ * Between a fused q/k/v product and lowbit_kv8_append / lowbit_attention_kv8
+ * (or a diffusion transformer's attention): each head's norm and its rotation
+ * by the token's position, in one pass over queries and keys. */
+typedef struct lowbit_rope {
+  int64_t tokens;
+  int head_dim;             /* D, a multiple of 8, at most 256 */
+  int n_pairs;              /* rotated pairs, a multiple of 4, 2 n_pairs <= D; 0: no rotation */
+  int adjacent;             /* 0: pairs (i, i + n_pairs), else (2 i, 2 i + 1), of the first 2 n_pairs dims */
+  int n_axes;               /* at least 1 */
+  const int32_t* positions; /* device [n_axes][pos_stride], of any sign */
+  int64_t pos_stride;       /* at least tokens (n_axes = 1: ignored) */
+  const double* freqs;      /* device [n_pairs], radians for one step of the position */
+  const int32_t* pair_axis; /* device [n_pairs], each pair's axis; NULL: axis 0.  A pair whose axis
+                               is not in 0 .. n_axes - 1 is not rotated */
+} lowbit_rope;
+
+/* For every token and head x of Q [tokens][q_heads][D] and K [tokens][kv_heads]
+ * [D] (x_dtype F32 or BF16): y = x w / sqrt(mean of x^2 + eps) with w =
+ * q_weight / k_weight [D] (fp32; NULL: y = x, w of 1 + v is the caller's to
+ * add); then each pair (a, b) becomes (a cos t - b sin t, b cos t + a sin t),
+ * t = positions[axis][token] freqs[pair], reduced in fp64 (exact enough for any
+ * position).  Everything else is fp32 (squares beyond its range overflow),
+ * rounded once to y_dtype F32 or BF16.  Q, K and the outputs lie with tokens
+ * the given strides (in elements) apart, heads contiguous: a fused projection's
+ * output as it is.  Q_out may be Q and K_out may be K where x_dtype = y_dtype
+ * and the strides agree; otherwise outputs overlap nothing.  K NULL (kv_heads 0):
+ * queries alone.
+ * Several axes (time, height, width): each pair turns by one of them.
+ * All of Q, K, Q_out, K_out 16-byte aligned, strides multiples of 8; freqs 8 bytes,
+ * positions, pair_axis and weights 4.  tokens <= 2^30, q_heads, kv_heads <= 2^16.
+ * eps finite, >= 0.
+ * Errors: E_NULL, E_UNSUPPORTED (types, head_dim, n_pairs, eps), E_SHAPE, E_ALIGN,
+ * E_HIP. */
+int lowbit_qk_norm_rope(const lowbit_rope* rope, int x_dtype, const void* Q, int64_t q_heads, int64_t q_stride,
+                        const float* q_weight, const void* K, int64_t kv_heads, int64_t k_stride,
+                        const float* k_weight, float eps, int y_dtype, void* Q_out, int64_t qo_stride, void* K_out,
+                        int64_t ko_stride, void* stream);
+
+/* =====================  pages of the cache  ===============================
+ * Who holds which page, decided on the device, so that a step whose new
+ * sequences are chosen there (beams, samples) needs no copy to the host.
+ * A sequence of n tokens holds the first ceil(n / page_tokens) pages of its
+ * table row.  refs [n_pages] counts the holders of each page (a store of prompts
+ * may hold pages too); 0: free.  The caches of one call are a model's layers:
+ * the same n_pages and page_tokens, one set of tables for all (heads and sizes
+ * of head may differ).  Arrays are int32 on the device; the library keeps
+ * nothing between calls, and results do not depend on the order in which
+ * workgroups run. */
+
+/* The next batch from this one: new sequence i takes over parents[i]'s tokens
+ * (0 .. n_seqs - 1; any other number: none) and gets room for grow[i] tokens
+ * more (grow NULL: max_grow each; cut to 0 .. max_grow).  new_lens[i] counts them
+ * already, as lowbit_kv8_append and lowbit_attention_kv8 want it.  Sequences with
+ * several children are forked, those with one go on, those with none are freed.
+ *   - Pages are shared.  A partly filled one that new tokens will be written to
+ *     stays with the first of the children that will, if nobody else holds it;
+ *     every other one gets a copy (codes and exponents, of all layers).
+ *   - Copies and further pages are the free ones (after the old batch's pages
+ *     were given back) in ascending order, for the children in turn.
+ *   - new_refs = refs without the old batch's holders, with the new one's.
+ *   - new_table rows end with -1 behind their pages.  A page number outside
+ *     0 .. n_pages - 1 in a row becomes -1 and counts for nobody.
+ * Where pages do not suffice, *failed is the number that lacks (else 0), no page
+ * is written, and the other outputs do not stand: the inputs do.  A child that
+ * has more than new_width pages, or 2^30 tokens, is cut to them.
+ * n_seqs 0 (nothing yet: parents are none) and n_new 0 (everything freed) are
+ * fine, their arrays may be NULL.  Outputs overlap no input; new_refs 16-byte
+ * aligned.  n_pages <= 2^26; n_seqs, n_new <= 2^20; table widths <= 2^26; max_grow <= 2^30, n_new
+ * (max_grow / page_tokens + 2) <= 2^30, n_new * ceil(new_width / 1024) < 2^24 - 2048;
+ * n_caches <= 4096.  One workgroup plans: time grows with n_new and with the
+ * entries of the sequences that do not go on as one.  Uses the stream's workspace
+ * (lowbit_kv8_fork_workspace bytes); reserve it before a capture.
+ * Errors: E_NULL, E_UNSUPPORTED (page_tokens, head_dim), E_SHAPE, E_ALIGN, E_NOMEM,
+ * E_HIP. */
+int lowbit_kv8_fork(const lowbit_kv8* caches, int64_t n_caches, int64_t n_seqs, const int32_t* page_table,
+                    int64_t table_width, const int32_t* kv_lens, const int32_t* refs, int64_t n_new,
+                    const int32_t* parents, const int32_t* grow, int64_t max_grow, int32_t* new_table,
+                    int64_t new_width, int32_t* new_lens, int32_t* new_refs, int32_t* failed, void* stream);
+int lowbit_kv8_fork_workspace(int64_t n_pages, int page_tokens, int64_t n_seqs, int64_t n_new, int64_t max_grow,
+                              size_t* bytes);
+
+/* Closes the cache up: with *live pages in use (refs > 0), the k-th page in use
+ * at or behind *live moves to the k-th free page before it, so that the pages
+ * from *live on are free (in all layers).  remap [n_pages] receives where each
+ * page is now (-1: it was free), for tables that are not in the call; new_table
+ * is page_table so rewritten (-1 behind a sequence's pages), new_refs the counts.
+ * n_seqs may be 0 (the tables then NULL).  Outputs overlap no input.  Limits as
+ * lowbit_kv8_fork, and ceil(n_pages / 1024) + n_seqs * ceil(table_width / 1024) <
+ * 2^24 - 2048.  Uses the stream's workspace (lowbit_kv8_compact_workspace bytes).
+ * Errors as lowbit_kv8_fork. */
+int lowbit_kv8_compact(const lowbit_kv8* caches, int64_t n_caches, int64_t n_seqs, const int32_t* page_table,
+                       int64_t table_width, const int32_t* kv_lens, const int32_t* refs, int32_t* new_table,
+                       int32_t* new_refs, int32_t* remap, int32_t* live, void* stream);
+int lowbit_kv8_compact_workspace(int64_t n_pages, size_t* bytes);
+
 #ifdef __cplusplus
 }
 #endif

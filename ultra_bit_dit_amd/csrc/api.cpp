@@ -675,3 +675,208 @@ int lowbit_attention_kv8(const lowbit_kv8* cache, const lowbit_kv8_batch* batch,
   }
   return hip_status(launch_attention(a, ws, (hipStream_t)stream));
 }
+
+// ------------------------------------------- heads of queries and keys; pages
+
+int lowbit_qk_norm_rope(const lowbit_rope* rope, int x_dtype, const void* Q, int64_t q_heads, int64_t q_stride,
+                        const float* q_weight, const void* K, int64_t kv_heads, int64_t k_stride,
+                        const float* k_weight, float eps, int y_dtype, void* Q_out, int64_t qo_stride, void* K_out,
+                        int64_t ko_stride, void* stream) {
+  if (!rope || !Q || !Q_out || (kv_heads != 0 && (!K || !K_out))) return LOWBIT_E_NULL;
+  const lowbit_rope& r = *rope;
+  if (r.n_pairs != 0 && (!r.positions || !r.freqs)) return LOWBIT_E_NULL;
+  for (int t : {x_dtype, y_dtype})
+    if (t != LOWBIT_F32 && t != LOWBIT_BF16) return LOWBIT_E_UNSUPPORTED;
+  if (r.head_dim < 8 || r.head_dim > 256 || r.head_dim % 8 != 0) return LOWBIT_E_UNSUPPORTED;
+  if (r.n_pairs < 0 || r.n_pairs % 4 != 0 || 2 * (int64_t)r.n_pairs > r.head_dim) return LOWBIT_E_UNSUPPORTED;
+  if (!(eps >= 0.f) || !(eps - eps == 0.f)) return LOWBIT_E_UNSUPPORTED;
+  if (r.tokens < 1 || r.tokens > (1 << 30) || r.n_axes < 1 || r.n_axes > (1 << 16)) return LOWBIT_E_SHAPE;
+  const int64_t most = int64_t(1) << 40;
+  if (r.n_axes > 1 && r.n_pairs != 0 && (r.pos_stride < r.tokens || r.pos_stride > most)) return LOWBIT_E_SHAPE;
+  if (q_heads < 1 || q_heads > (1 << 16) || kv_heads < 0 || kv_heads > (1 << 16)) return LOWBIT_E_SHAPE;
+  auto bad_stride = [&](int64_t stride, int64_t heads) { return stride < heads * r.head_dim || stride > most; };
+  if (bad_stride(q_stride, q_heads) || bad_stride(qo_stride, q_heads)) return LOWBIT_E_SHAPE;
+  if (kv_heads && (bad_stride(k_stride, kv_heads) || bad_stride(ko_stride, kv_heads))) return LOWBIT_E_SHAPE;
+  if (!aligned(Q, 16) || !aligned(Q_out, 16) || q_stride % 8 != 0 || qo_stride % 8 != 0) return LOWBIT_E_ALIGN;
+  if (kv_heads && (!aligned(K, 16) || !aligned(K_out, 16) || k_stride % 8 != 0 || ko_stride % 8 != 0))
+    return LOWBIT_E_ALIGN;
+  if (r.n_pairs && (!aligned(r.positions, 4) || !aligned(r.freqs, 8) || (r.pair_axis && !aligned(r.pair_axis, 4))))
+    return LOWBIT_E_ALIGN;
+  if ((q_weight && !aligned(q_weight, 4)) || (k_weight && !aligned(k_weight, 4))) return LOWBIT_E_ALIGN;
+  RopeArgs a;
+  a.tokens = r.tokens;
+  a.D = r.head_dim;
+  a.pairs = r.n_pairs;
+  a.adjacent = r.adjacent ? 1 : 0;
+  a.axes = r.n_axes;
+  a.Hq = (int)q_heads;
+  a.Hk = (int)kv_heads;
+  a.pos = r.positions;
+  a.pos_stride = r.n_axes > 1 ? r.pos_stride : 0;
+  a.freqs = r.freqs;
+  a.pair_axis = r.pair_axis;
+  a.eps = eps;
+  a.inv_d = 1.0f / r.head_dim;
+  a.qw = q_weight;
+  a.kw = k_weight;
+  a.q = Q;
+  a.k = K;
+  a.qo = Q_out;
+  a.ko = K_out;
+  a.q_stride = q_stride;
+  a.k_stride = kv_heads ? k_stride : 0;
+  a.qo_stride = qo_stride;
+  a.ko_stride = kv_heads ? ko_stride : 0;
+  return hip_status(launch_qk_norm_rope(a, x_dtype == LOWBIT_F32, y_dtype == LOWBIT_F32, (hipStream_t)stream));
+}
+
+namespace {
+
+constexpr int64_t kMaxCachePages = int64_t(1) << 26, kMaxWidth = int64_t(1) << 26, kMaxCaches = 4096;
+
+int log2_page(int page_tokens) {
+  for (int i = 4; i <= 7; i++)
+    if (page_tokens == 1 << i) return i;
+  return -1;
+}
+
+// checks of a model's caches (its layers), which share pages and tables
+int caches_check(const lowbit_kv8* c, int64_t n, std::vector<KvLayer>* out) {
+  if (!c) return LOWBIT_E_NULL;
+  if (n < 1 || n > kMaxCaches) return LOWBIT_E_SHAPE;
+  for (int64_t i = 0; i < n; i++) {
+    if (!c[i].k_codes || !c[i].v_codes || !c[i].k_scales || !c[i].v_scales) return LOWBIT_E_NULL;
+    if (log2_page(c[i].page_tokens) < 0 || (c[i].head_dim != 64 && c[i].head_dim != 128 && c[i].head_dim != 256))
+      return LOWBIT_E_UNSUPPORTED;
+    if (c[i].n_pages < 1 || c[i].n_pages > kMaxCachePages || c[i].kv_heads < 1 || c[i].kv_heads > 4096)
+      return LOWBIT_E_SHAPE;
+    if (c[i].n_pages != c[0].n_pages || c[i].page_tokens != c[0].page_tokens) return LOWBIT_E_SHAPE;
+    if (!aligned(c[i].k_codes, 16) || !aligned(c[i].v_codes, 16)) return LOWBIT_E_ALIGN;
+    out->push_back(KvLayer{c[i].kv_heads, c[i].head_dim, (uint8_t*)c[i].k_codes, (uint8_t*)c[i].v_codes, c[i].k_scales,
+                           c[i].v_scales});
+  }
+  return LOWBIT_OK;
+}
+
+bool fork_sizes_ok(int64_t n_pages, int page_tokens, int64_t n_seqs, int64_t n_new, int64_t max_grow) {
+  return n_pages >= 1 && n_pages <= kMaxCachePages && n_seqs >= 0 && n_seqs <= (1 << 20) && n_new >= 0 &&
+         n_new <= (1 << 20) && max_grow >= 0 && max_grow <= (1 << 30) &&
+         n_new * (max_grow / page_tokens + 2) <= (1 << 30);
+}
+bool table_ok(int64_t n_seqs, int64_t width) {
+  return n_seqs == 0 || (width >= 1 && width <= kMaxWidth);
+}
+
+// runs f; C++ exceptions (of the host's memory) do not leave the library
+template <class F>
+int no_throw(F&& f) {
+  try {
+    return f();
+  } catch (...) {
+    return LOWBIT_E_NOMEM;
+  }
+}
+
+}  // namespace
+
+int lowbit_kv8_fork_workspace(int64_t n_pages, int page_tokens, int64_t n_seqs, int64_t n_new, int64_t max_grow,
+                              size_t* bytes) {
+  if (!bytes) return LOWBIT_E_NULL;
+  *bytes = 0;
+  if (log2_page(page_tokens) < 0) return LOWBIT_E_UNSUPPORTED;
+  if (!fork_sizes_ok(n_pages, page_tokens, n_seqs, n_new, max_grow)) return LOWBIT_E_SHAPE;
+  ForkArgs a = {};
+  a.n_pages = n_pages;
+  a.lp = log2_page(page_tokens);
+  a.n_seqs = n_seqs;
+  a.n_new = n_new;
+  a.max_grow = max_grow;
+  *bytes = fork_workspace_bytes(a);
+  return LOWBIT_OK;
+}
+
+int lowbit_kv8_fork(const lowbit_kv8* caches, int64_t n_caches, int64_t n_seqs, const int32_t* page_table,
+                    int64_t table_width, const int32_t* kv_lens, const int32_t* refs, int64_t n_new,
+                    const int32_t* parents, const int32_t* grow, int64_t max_grow, int32_t* new_table,
+                    int64_t new_width, int32_t* new_lens, int32_t* new_refs, int32_t* failed, void* stream) {
+  return no_throw([&]() -> int {
+    std::vector<KvLayer> layers;
+    const int rc = caches_check(caches, n_caches, &layers);
+    if (rc) return rc;
+    if (!refs || !new_refs || !failed) return LOWBIT_E_NULL;
+    if (n_seqs != 0 && (!page_table || !kv_lens)) return LOWBIT_E_NULL;
+    if (n_new != 0 && (!parents || !new_table || !new_lens)) return LOWBIT_E_NULL;
+    const int P = caches[0].page_tokens;
+    if (!fork_sizes_ok(caches[0].n_pages, P, n_seqs, n_new, max_grow)) return LOWBIT_E_SHAPE;
+    if (!table_ok(n_seqs, table_width) || !table_ok(n_new, new_width)) return LOWBIT_E_SHAPE;
+    for (const void* p : {(const void*)page_table, (const void*)kv_lens, (const void*)refs, (const void*)parents,
+                          (const void*)grow, (const void*)new_table, (const void*)new_lens, (const void*)failed})
+      if (!aligned(p, 4)) return LOWBIT_E_ALIGN;
+    if (!aligned(new_refs, 16)) return LOWBIT_E_ALIGN;
+    ForkArgs a = {};
+    a.n_pages = caches[0].n_pages;
+    a.lp = log2_page(P);
+    a.n_seqs = n_seqs;
+    a.width = n_seqs ? table_width : 1;
+    a.table = page_table;
+    a.lens = kv_lens;
+    a.refs = refs;
+    a.n_new = n_new;
+    a.new_width = n_new ? new_width : 1;
+    a.max_grow = max_grow;
+    a.parents = parents;
+    a.grow = grow;
+    a.new_table = new_table;
+    a.new_lens = new_lens;
+    a.new_refs = new_refs;
+    a.failed = failed;
+    if (!fork_fits(a)) return LOWBIT_E_SHAPE;
+    void* ws = nullptr;
+    const int r2 = workspace((hipStream_t)stream, fork_workspace_bytes(a), &ws);
+    if (r2) return r2;
+    return hip_status(launch_fork(a, layers.data(), n_caches, ws, (hipStream_t)stream));
+  });
+}
+
+int lowbit_kv8_compact_workspace(int64_t n_pages, size_t* bytes) {
+  if (!bytes) return LOWBIT_E_NULL;
+  *bytes = 0;
+  if (n_pages < 1 || n_pages > kMaxCachePages) return LOWBIT_E_SHAPE;
+  CompactArgs a = {};
+  a.n_pages = n_pages;
+  *bytes = compact_workspace_bytes(a);
+  return LOWBIT_OK;
+}
+
+int lowbit_kv8_compact(const lowbit_kv8* caches, int64_t n_caches, int64_t n_seqs, const int32_t* page_table,
+                       int64_t table_width, const int32_t* kv_lens, const int32_t* refs, int32_t* new_table,
+                       int32_t* new_refs, int32_t* remap, int32_t* live, void* stream) {
+  return no_throw([&]() -> int {
+    std::vector<KvLayer> layers;
+    const int rc = caches_check(caches, n_caches, &layers);
+    if (rc) return rc;
+    if (!refs || !new_refs || !remap || !live) return LOWBIT_E_NULL;
+    if (n_seqs != 0 && (!page_table || !kv_lens || !new_table)) return LOWBIT_E_NULL;
+    if (n_seqs < 0 || n_seqs > (1 << 20) || !table_ok(n_seqs, table_width)) return LOWBIT_E_SHAPE;
+    for (const void* p : {(const void*)page_table, (const void*)kv_lens, (const void*)refs, (const void*)new_table,
+                          (const void*)new_refs, (const void*)remap, (const void*)live})
+      if (!aligned(p, 4)) return LOWBIT_E_ALIGN;
+    CompactArgs a = {};
+    a.n_pages = caches[0].n_pages;
+    a.lp = log2_page(caches[0].page_tokens);
+    a.n_seqs = n_seqs;
+    a.width = n_seqs ? table_width : 1;
+    a.table = page_table;
+    a.lens = kv_lens;
+    a.refs = refs;
+    a.new_table = new_table;
+    a.new_refs = new_refs;
+    a.remap = remap;
+    a.live = live;
+    if (!compact_fits(a)) return LOWBIT_E_SHAPE;
+    void* ws = nullptr;
+    const int r2 = workspace((hipStream_t)stream, compact_workspace_bytes(a), &ws);
+    if (r2) return r2;
+    return hip_status(launch_compact(a, layers.data(), n_caches, ws, (hipStream_t)stream));
+  });
+}

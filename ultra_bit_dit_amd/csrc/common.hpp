@@ -176,6 +176,36 @@ bool gemm_mxfp4_fits(bool x4, int64_t M, int64_t N, int64_t K);  // a launch hol
 size_t gemm_mxfp4_workspace_bytes(bool x4, int64_t M, int64_t N, int64_t K);
 hipError_t launch_gemm_mxfp4(const MxGemmArgs& a, hipStream_t s);
 
+// Head norms and rotation (rope.hip)
+struct RopeArgs {
+  int64_t tokens;
+  int D, pairs, adjacent, axes, Hq, Hk;
+  const int32_t* pos;        // [axes][pos_stride]
+  int64_t pos_stride;
+  const double* freqs;       // [pairs]
+  const int32_t* pair_axis;  // [pairs], or NULL: axis 0
+  float eps, inv_d;
+  const float* qw;           // [D] or NULL: no norm
+  const float* kw;
+  const void* q;             // [tokens][Hq][D], strides in elements between tokens
+  const void* k;
+  void* qo;
+  void* ko;
+  int64_t q_stride, k_stride, qo_stride, ko_stride;
+};
+hipError_t launch_qk_norm_rope(const RopeArgs& a, bool f32, bool out32, hipStream_t s);
+
+// Pages of the 8-bit cache (pages.hip); the workspaces count the counters in
+struct KvLayer;
+struct ForkArgs;
+struct CompactArgs;
+bool fork_fits(const ForkArgs& a);  // one launch holds its workgroups
+bool compact_fits(const CompactArgs& a);
+size_t fork_workspace_bytes(ForkArgs a);
+size_t compact_workspace_bytes(CompactArgs a);
+hipError_t launch_fork(ForkArgs a, const KvLayer* caches, int64_t n_caches, void* ws, hipStream_t s);
+hipError_t launch_compact(CompactArgs a, const KvLayer* caches, int64_t n_caches, void* ws, hipStream_t s);
+
 struct KvArgs;
 struct AttnArgs;
 bool kv8_append_fits(const KvArgs& a);  // one launch holds its workgroups

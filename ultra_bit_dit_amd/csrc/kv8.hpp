@@ -50,6 +50,53 @@ __device__ __forceinline__ SeqSpan seq_span(const KvArgs& a, int64_t b) {
   return s;
 }
 
+// One layer's cache, as page moves see it.
+struct KvLayer {
+  int H, D;
+  uint8_t *kc, *vc, *ks, *vs;
+};
+struct ForkArgs {
+  int64_t n_pages;
+  int lp;                    // log2 of a page's tokens
+  int64_t n_seqs, width;
+  const int32_t* table;      // [n_seqs][width]
+  const int32_t* lens;       // [n_seqs]
+  const int32_t* refs;       // [n_pages] holders of each page
+  int64_t n_new, new_width, max_grow;
+  const int32_t* parents;    // [n_new]
+  const int32_t* grow;       // [n_new] tokens to come, or NULL: max_grow each
+  int32_t* new_table;        // [n_new][new_width]
+  int32_t* new_lens;         // [n_new]
+  int32_t* new_refs;         // [n_pages]
+  int32_t* failed;           // pages that were not found
+  // workspace
+  int* children;             // [n_seqs]
+  int* first;                // [n_pages] the first child that will write to the page, and how many will:
+  int* writers;              // [n_pages] set for those pages only
+  int* fresh;                // free pages, for the children in turn
+  int64_t* start;            // [n_new] twice the place of a child's first one there, and 1 if that is a copy
+  int *src, *dst;            // copies: a page, and the place of the one it is copied to
+  int* n_copies;
+  int64_t* found;            // pages in `fresh`
+};
+struct CompactArgs {
+  int64_t n_pages;
+  int lp;
+  int64_t n_seqs, width;
+  const int32_t* table;
+  const int32_t* lens;
+  const int32_t* refs;
+  int32_t* new_table;
+  int32_t* new_refs;
+  int32_t* remap;            // [n_pages]
+  int32_t* live;             // pages in use
+  // workspace
+  int* count;                // pages in use in each chunk
+  int* place;                // [n_pages] where a page goes; -2 - k: to hole[k]; -1: free
+  int *hole, *mover;         // the k-th move goes from mover[k] to hole[k]
+  int* n_moves;
+};
+
 struct AttnArgs {
   KvArgs kv;
   int64_t Hq, G;

@@ -1,0 +1,254 @@
+// Norms of the heads of queries and keys, with the rotation by position.
+//
+// A head of D elements: y = x w / sqrt(mean x^2 + eps) (w NULL: y = x), then the
+// pairs of the first 2 n_pairs elements, (i, i + n_pairs) or (2 i, 2 i + 1), turn
+// by the angle position[axis(i)][token] freqs[i].  Squares, their sum and the
+// turn are fp32; the angle is reduced to an eighth of a turn in fp64, so
+// positions of any size keep their angle (fp32 would be off by 2^-24 of an angle
+// of many turns), and its sine and cosine are Taylor series of an argument of at
+// most pi / 4 (the first terms left out are below 2^-28 of the result).
+//
+// A wave has one token and a run of its heads.  Each lane finds the sine and
+// cosine of one pair for all of the token's heads and leaves them in LDS.  A head
+// lies in D / (2 W) lanes (rounded up to a power of two), two chunks of W
+// elements each, so that a lane holds both elements of its pairs.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "kv8.hpp"
+
+namespace lowbit {
+namespace {
+
+constexpr int kWaves = 4;       // of a workgroup
+constexpr int kMaxPairs = 128;  // of a head (D <= 256)
+constexpr int kHold = 4;        // heads of a lane read at once
+
+// sin and cos of 2 pi s, |s| <= 1/8
+__device__ __forceinline__ float2 small_turn(float s) {
+  constexpr double t = 6.283185307179586;
+  constexpr double t2 = t * t, t3 = t2 * t, t4 = t2 * t2, t5 = t4 * t, t6 = t3 * t3, t7 = t6 * t, t8 = t4 * t4;
+  const float z = s * s;
+  float p = fmaf(z, (float)(t8 * t / 362880), (float)(-t7 / 5040));
+  p = fmaf(z, p, (float)(t5 / 120));
+  p = fmaf(z, p, (float)(-t3 / 6));
+  float q = fmaf(z, (float)(-t8 * t2 / 3628800), (float)(t8 / 40320));
+  q = fmaf(z, q, (float)(-t6 / 720));
+  q = fmaf(z, q, (float)(t4 / 24));
+  q = fmaf(z, q, (float)(-t2 / 2));
+  return make_float2(fmaf(s * z, p, s * (float)t), fmaf(z, q, 1.f));
+}
+
+// (cos, sin) of position f
+__device__ __forceinline__ float2 turn_of(int position, double f) {
+  double t = (double)position * f * 0.15915494309189535;  // turns
+  t -= rint(t);
+  const double e = rint(4. * t);
+  const float2 v = small_turn((float)(t - 0.25 * e));  // sin, cos
+  const int quarter = (int)e & 3;
+  const float c = quarter & 1 ? v.x : v.y, s = quarter & 1 ? v.y : v.x;
+  return make_float2(quarter == 1 || quarter == 2 ? -c : c, quarter >= 2 ? -s : s);
+}
+
+// W elements as they lie in memory
+template <bool F32, int W>
+struct Chunk {
+  static constexpr int N = W * (F32 ? 4 : 2) / 8;  // words of 8 bytes
+  uint2 w[N];
+  __device__ __forceinline__ void read(const uint8_t* p) {
+    if constexpr (N == 1) {
+      w[0] = *(const uint2*)p;
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; i += 2) {
+        const mx_u4 v = *(const mx_u4*)(p + 8 * i);
+        w[i] = make_uint2(v.x, v.y);
+        w[i + 1] = make_uint2(v.z, v.w);
+      }
+    }
+  }
+  __device__ __forceinline__ float operator[](int e) const {
+    if constexpr (F32) return __uint_as_float(e & 1 ? w[e >> 1].y : w[e >> 1].x);
+    const uint32_t u = e & 2 ? w[e >> 2].y : w[e >> 2].x;
+    return __uint_as_float(e & 1 ? u & 0xFFFF0000u : u << 16);
+  }
+};
+template <bool F32, int W>
+__device__ __forceinline__ void write_chunk(uint8_t* p, const float* y) {
+  uint32_t w[W * (F32 ? 4 : 2) / 4];
+#pragma unroll
+  for (int e = 0; e < W; e += F32 ? 1 : 2) {
+    if constexpr (F32) {
+      w[e] = __float_as_uint(y[e]);
+    } else {
+      v2bf h;
+      h[0] = (__bf16)y[e];
+      h[1] = (__bf16)y[e + 1];
+      w[e / 2] = __builtin_bit_cast(uint32_t, h);
+    }
+  }
+  constexpr int N = W * (F32 ? 4 : 2) / 4;
+  if constexpr (N == 2) {
+    *(uint2*)p = make_uint2(w[0], w[1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) *(mx_u4*)(p + 4 * i) = mx_u4{w[i], w[i + 1], w[i + 2], w[i + 3]};
+  }
+}
+
+template <int CTRL>
+__device__ __forceinline__ float add_dpp(float x) {
+  return x + __uint_as_float((uint32_t)__builtin_amdgcn_mov_dpp((int)__float_as_uint(x), CTRL, 0xF, 0xF, true));
+}
+// sum over the 2^lg neighbouring lanes of a head, the same in all of them
+__device__ __forceinline__ float head_sum(float x, int lg) {
+  if (lg >= 1) x = add_dpp<0xB1>(x);   // lane ^ 1
+  if (lg >= 2) x = add_dpp<0x4E>(x);   // lane ^ 2
+  if (lg >= 3) x = add_dpp<0x141>(x);  // the other four of eight
+  if (lg >= 4) x = add_dpp<0x140>(x);  // the other eight of sixteen
+  if (lg >= 5) x += __shfl_xor(x, 16);
+  return x;
+}
+
+template <bool F32, bool OUT32, int W>
+__global__ __launch_bounds__(64 * kWaves) void qk_norm_rope(RopeArgs a, int lg, int slices, int per) {
+  constexpr int EI = F32 ? 4 : 2, EO = OUT32 ? 4 : 2;
+  __shared__ float2 turn_[kWaves][kMaxPairs];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  float2* turn = turn_[wave];
+  const int team = lane >> lg, at = lane & ((1 << lg) - 1), teams = 64 >> lg;
+  const bool mine = at * 2 * W < a.D;  // lanes behind the head's end idle
+  const bool turns = at * W < a.pairs; // whole chunks: pairs is a multiple of W
+  // first dims of the lane's two chunks
+  const int d0 = turns && !a.adjacent ? at * W : at * 2 * W, d1 = turns && !a.adjacent ? a.pairs + at * W : d0 + W;
+  const int heads = a.Hq + a.Hk;
+  const int64_t items = a.tokens * slices;
+  float wq[2 * W], wk[2 * W];
+#pragma unroll
+  for (int e = 0; e < 2 * W; e++) {
+    const int d = e < W ? d0 + e : d1 + e - W;
+    wq[e] = mine && a.qw ? a.qw[d] : 1.f;
+    wk[e] = mine && a.kw ? a.kw[d] : 1.f;
+  }
+  for (int64_t item = (int64_t)blockIdx.x * kWaves + wave; item < items; item += (int64_t)gridDim.x * kWaves) {
+    int64_t t = item;
+    int slice = 0;
+    if (slices > 1) {
+      t = item / slices;
+      slice = (int)(item - t * slices);
+    }
+    const int h_end = min(heads, (slice + 1) * per);
+    // the first heads' elements are on their way while the angles are found
+    const uint8_t* q = (const uint8_t*)a.q + t * a.q_stride * EI;
+    const uint8_t* k = (const uint8_t*)a.k + t * a.k_stride * EI;
+    uint8_t* qo = (uint8_t*)a.qo + t * a.qo_stride * EO;
+    uint8_t* ko = (uint8_t*)a.ko + t * a.ko_stride * EO;
+    Chunk<F32, W> c0[kHold], c1[kHold];
+    auto read = [&](int h0) {
+#pragma unroll
+      for (int i = 0; i < kHold; i++) {
+        const int h = h0 + i * teams + team;
+        c0[i] = c1[i] = Chunk<F32, W>{};
+        if (h >= h_end || !mine) continue;
+        const uint8_t* p = h < a.Hq ? q + (int64_t)h * a.D * EI : k + (int64_t)(h - a.Hq) * a.D * EI;
+        c0[i].read(p + d0 * EI);
+        c1[i].read(p + d1 * EI);
+      }
+    };
+    int h0 = slice * per;
+    read(h0);
+    for (int i = lane; i < a.pairs; i += 64) {
+      const int axis = a.pair_axis ? a.pair_axis[i] : 0;
+      const int pos = axis >= 0 && axis < a.axes ? a.pos[axis * a.pos_stride + t] : 0;
+      turn[i] = turn_of(pos, a.freqs[i]);
+    }
+    // the wave's own LDS: its writes are done before its reads
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    float2 cs[W];
+#pragma unroll
+    for (int e = 0; e < W; e++) cs[e] = turns && mine ? turn[at * W + e] : make_float2(1.f, 0.f);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    for (;;) {
+#pragma unroll
+      for (int i = 0; i < kHold; i++) {
+        const int h = h0 + i * teams + team;
+        if (h0 + i * teams >= h_end) break;
+        const bool is_q = h < a.Hq;
+        float x[2 * W], sum = 0.f;
+#pragma unroll
+        for (int e = 0; e < W; e++) {
+          x[e] = c0[i][e];
+          x[W + e] = c1[i][e];
+        }
+        if (is_q ? a.qw != nullptr : a.kw != nullptr) {
+          if (mine) {
+#pragma unroll
+            for (int e = 0; e < 2 * W; e++) sum = fmaf(x[e], x[e], sum);
+          }
+        }
+        sum = head_sum(sum, lg);
+        if (h >= h_end || !mine) continue;
+        if (is_q ? a.qw != nullptr : a.kw != nullptr) {
+          const float r = 1.0f / sqrtf(sum * a.inv_d + a.eps);
+#pragma unroll
+          for (int e = 0; e < 2 * W; e++) x[e] = x[e] * r * (is_q ? wq[e] : wk[e]);
+        }
+        float y[2 * W];
+#pragma unroll
+        for (int e = 0; e < 2 * W; e++) y[e] = x[e];
+        if (turns) {
+#pragma unroll
+          for (int e = 0; e < W; e++) {
+            if (a.adjacent) {
+              y[2 * e] = x[2 * e] * cs[e].x - x[2 * e + 1] * cs[e].y;
+              y[2 * e + 1] = x[2 * e + 1] * cs[e].x + x[2 * e] * cs[e].y;
+            } else {
+              y[e] = x[e] * cs[e].x - x[W + e] * cs[e].y;
+              y[W + e] = x[W + e] * cs[e].x + x[e] * cs[e].y;
+            }
+          }
+        }
+        uint8_t* p = is_q ? qo + (int64_t)h * a.D * EO : ko + (int64_t)(h - a.Hq) * a.D * EO;
+        write_chunk<OUT32, W>(p + d0 * EO, y);
+        write_chunk<OUT32, W>(p + d1 * EO, y + W);
+      }
+      h0 += kHold * teams;
+      if (h0 >= h_end) break;
+      read(h0);
+    }
+  }
+}
+
+}  // namespace
+
+hipError_t launch_qk_norm_rope(const RopeArgs& a, bool f32, bool out32, hipStream_t s) {
+  const bool wide = a.D % 16 == 0 && a.pairs % 8 == 0;
+  const int lanes = a.D / (wide ? 16 : 8);
+  int lg = 0;
+  while ((1 << lg) < lanes) lg++;
+  const int teams = 64 >> lg, heads = a.Hq + a.Hk;
+  // A wave takes all heads of a token where there are tokens for the whole chip,
+  // else as few as are read at once, or one each.
+  constexpr int64_t kFill = 8192;
+  int per = heads;
+  if (a.tokens < kFill) {
+    const int64_t slices = std::min<int64_t>(cdiv(heads, teams), cdiv(kFill, a.tokens));
+    per = (int)(cdiv(cdiv(heads, slices), teams) * teams);
+  }
+  const int slices = (int)cdiv(heads, per);
+  const int64_t blocks = std::min<int64_t>(cdiv(a.tokens * slices, kWaves), 1 << 20);
+  const dim3 grid((unsigned)blocks), block(64 * kWaves);
+  auto go = [&](auto in, auto out) {
+    constexpr bool I = decltype(in)::value, O = decltype(out)::value;
+    if (wide) hipLaunchKernelGGL((qk_norm_rope<I, O, 8>), grid, block, 0, s, a, lg, slices, per);
+    else hipLaunchKernelGGL((qk_norm_rope<I, O, 4>), grid, block, 0, s, a, lg, slices, per);
+  };
+  if (f32) out32 ? go(std::true_type{}, std::true_type{}) : go(std::true_type{}, std::false_type{});
+  else out32 ? go(std::false_type{}, std::true_type{}) : go(std::false_type{}, std::false_type{});
+  return hipGetLastError();
+}
+
+}  // namespace lowbit

@@ -27,7 +27,9 @@ EXPORTS = ("lowbit_abi_version", "lowbit_status_str", "lowbit_packed_bytes", "lo
            "lowbit_chain_destroy",
            "lowbit_hbm_read_probe", "lowbit_quantize_weights", "lowbit_rotate_act",
            "lowbit_mxfp4_bytes", "lowbit_pack_mxfp4", "lowbit_quantize_mxfp4", "lowbit_gemm_mxfp4", "lowbit_gemm_mxfp4_workspace",
-           "lowbit_kv8_append", "lowbit_attention_kv8", "lowbit_attention_kv8_workspace")
+           "lowbit_kv8_append", "lowbit_attention_kv8", "lowbit_attention_kv8_workspace",
+           "lowbit_qk_norm_rope", "lowbit_kv8_fork", "lowbit_kv8_fork_workspace", "lowbit_kv8_compact",
+           "lowbit_kv8_compact_workspace")
 
 
 class GemvStage(ctypes.Structure):
@@ -50,6 +52,13 @@ class Kv8Batch(ctypes.Structure):
     _fields_ = [("n_seqs", ctypes.c_int64), ("page_table", ctypes.c_void_p), ("table_width", ctypes.c_int64),
                 ("kv_lens", ctypes.c_void_p), ("q_starts", ctypes.c_void_p), ("total_q", ctypes.c_int64),
                 ("max_q", ctypes.c_int64), ("max_kv", ctypes.c_int64), ("bad_pages", ctypes.c_void_p)]
+
+
+class Rope(ctypes.Structure):
+    """lowbit_rope"""
+    _fields_ = [("tokens", ctypes.c_int64), ("head_dim", ctypes.c_int), ("n_pairs", ctypes.c_int),
+                ("adjacent", ctypes.c_int), ("n_axes", ctypes.c_int), ("positions", ctypes.c_void_p),
+                ("pos_stride", ctypes.c_int64), ("freqs", ctypes.c_void_p), ("pair_axis", ctypes.c_void_p)]
 
 
 class LowbitError(RuntimeError):
@@ -102,6 +111,12 @@ def lib():
         L.lowbit_kv8_append.argtypes = [kvp, kbp, i32, vp, vp, i64, i64, vp]
         L.lowbit_attention_kv8.argtypes = [kvp, kbp, i64, vp, i64, ctypes.c_float, i32, i64, vp, i64, vp, vp]
         L.lowbit_attention_kv8_workspace.argtypes = [kvp, kbp, i64, szp]
+        L.lowbit_qk_norm_rope.argtypes = [ctypes.POINTER(Rope), i32, vp, i64, i64, vp, vp, i64, i64, vp, ctypes.c_float, i32,
+                                          vp, i64, vp, i64, vp]
+        L.lowbit_kv8_fork.argtypes = [kvp, i64, i64, vp, i64, vp, vp, i64, vp, vp, i64, vp, i64, vp, vp, vp, vp]
+        L.lowbit_kv8_fork_workspace.argtypes = [i64, i32, i64, i64, i64, szp]
+        L.lowbit_kv8_compact.argtypes = [kvp, i64, i64, vp, i64, vp, vp, vp, vp, vp, vp, vp]
+        L.lowbit_kv8_compact_workspace.argtypes = [i64, szp]
         for name in EXPORTS[2:]:
             getattr(L, name).restype = i32
         _lib = L
@@ -267,6 +282,7 @@ _FLOAT = {}       # torch type -> lowbit_dtype of the float inputs
 _fast = None      # the same exports with address-only prototypes
 _PACK_KV8 = struct.Struct("@qiiiPPPP").pack        # lowbit_kv8
 _PACK_BATCH = struct.Struct("@qPqPPqqqP").pack     # lowbit_kv8_batch
+_PACK_ROPE = struct.Struct("@qiiiiPqPP").pack      # lowbit_rope
 
 
 class _Fast:
@@ -276,7 +292,11 @@ class _Fast:
                 ("lowbit_quantize_mxfp4", [i64, i64, i32, vp, i64, vp, vp, vp, vp]),
                 ("lowbit_gemm_mxfp4", [i64, i64, i64, vp, vp, i32, vp, i64, vp, i32, vp, vp]),
                 ("lowbit_kv8_append", [vp, vp, i32, vp, vp, i64, i64, vp]),
-                ("lowbit_attention_kv8", [vp, vp, i64, vp, i64, ctypes.c_float, i32, i64, vp, i64, vp, vp])):
+                ("lowbit_attention_kv8", [vp, vp, i64, vp, i64, ctypes.c_float, i32, i64, vp, i64, vp, vp]),
+                ("lowbit_qk_norm_rope", [vp, i32, vp, i64, i64, vp, vp, i64, i64, vp, ctypes.c_float, i32, vp, i64, vp, i64,
+                                         vp]),
+                ("lowbit_kv8_fork", [vp, i64, i64, vp, i64, vp, vp, i64, vp, vp, i64, vp, i64, vp, vp, vp, vp]),
+                ("lowbit_kv8_compact", [vp, i64, i64, vp, i64, vp, vp, vp, vp, vp, vp, vp])):
             f = L[name]  # a function object of its own
             f.argtypes, f.restype = types, i32
             setattr(self, name[7:], f)
@@ -561,6 +581,182 @@ def attention_kv8_workspace(cache, page_table, kv_lens, q_heads, total_q, q_star
            lib().lowbit_attention_kv8_workspace(Kv8.from_buffer_copy(c), Kv8Batch.from_buffer_copy(b), q_heads,
                                                 ctypes.byref(n)))
     return n.value
+
+
+def _weight(T, w, D, what):
+    if w is None:
+        return None
+    if w.dtype != T.float32 or w.shape != (D,) or not w.is_contiguous():
+        raise ValueError(f"{what}: contiguous fp32 [{D}]")
+    return w.data_ptr()
+
+
+def qk_norm_rope(Q, K, positions, freqs, q_weight=None, k_weight=None, eps=1e-6, pair_axis=None, adjacent=False,
+                 y_dtype=None, Q_out=None, K_out=None, stream=None):
+    """Heads of queries [tokens][q_heads][dim] and keys [tokens][kv_heads][dim] (bf16 or fp32, tokens may be
+    strided; K None: queries alone) normalised with the fp32 weights [dim] (None: not) and rotated (see
+    lowbit_qk_norm_rope): positions int32 [tokens] or [axes][tokens], freqs fp64 [pairs] in radians for one step,
+    pair_axis int32 [pairs]; freqs None: no rotation.  y_dtype F32 or BF16 (None: as Q).  Returns (Q_out, K_out);
+    Q_out = Q and K_out = K write in place."""
+    T = _torch or _load()
+    if Q.dim() != 3 or Q.dtype not in _FLOAT:
+        raise ValueError("Q: bf16 or fp32 [tokens][q_heads][dim]")
+    tokens, Hq, D = Q.shape
+    dev = Q.get_device()
+    qs = _heads(Q, Hq, D, "Q")
+    Hk = ks = kos = 0
+    if K is not None:
+        if K.dim() != 3 or K.shape[0] != tokens or K.dtype != Q.dtype:
+            raise ValueError("K: Q's tokens and type")
+        Hk = K.shape[1]
+        ks = _heads(K, Hk, D, "K")
+    elif K_out is not None or k_weight is not None:
+        raise ValueError("K_out or k_weight without K")
+    pairs, axes, pos, ps, fr, pa = 0, 1, None, 0, None, None
+    if freqs is not None:
+        if freqs.dtype != T.float64 or freqs.dim() != 1 or not freqs.is_contiguous():
+            raise ValueError("freqs: contiguous fp64 [pairs]")
+        pairs, fr = freqs.shape[0], freqs.data_ptr()
+        if positions is None or positions.dtype != T.int32 or positions.dim() not in (1, 2) or (
+                positions.shape[-1] != tokens or (tokens > 1 and positions.stride(-1) != 1)):
+            raise ValueError("positions: int32 [tokens] or [axes][tokens]")
+        pos = positions.data_ptr()
+        if positions.dim() == 2:
+            axes = positions.shape[0]
+            ps = positions.stride(0) if axes > 1 else 0
+        if pair_axis is not None:
+            if pair_axis.dtype != T.int32 or pair_axis.shape != (pairs,) or not pair_axis.is_contiguous():
+                raise ValueError("pair_axis: contiguous int32 [pairs]")
+            pa = pair_axis.data_ptr()
+    elif pair_axis is not None:
+        raise ValueError("pair_axis without freqs")
+    qw, kw = _weight(T, q_weight, D, "q_weight"), _weight(T, k_weight, D, "k_weight")
+    if y_dtype is None:
+        y_dtype = _FLOAT.get(Q.dtype if Q_out is None else Q_out.dtype)
+    yt = T.float32 if y_dtype == F32 else T.bfloat16 if y_dtype == BF16 else None
+    if yt is None:
+        raise ValueError("y_dtype: F32 or BF16")
+    for name, x, y in (("Q_out", Q, Q_out), ("K_out", K, K_out)):
+        if y is not None and (y.shape != x.shape or y.dtype != yt):
+            raise ValueError(f"{name}: of y_dtype and its input's shape")
+    _device(T, dev, K, positions if pairs else None, freqs, pair_axis, q_weight, k_weight, Q_out, K_out)
+    if Q_out is None:
+        Q_out, qos = _empty(T, (tokens, Hq, D), yt, Q.device, stream), Hq * D
+    else:
+        qos = _heads(Q_out, Hq, D, "Q_out")
+    if K is not None:
+        if K_out is None:
+            K_out, kos = _empty(T, (tokens, Hk, D), yt, Q.device, stream), Hk * D
+        else:
+            kos = _heads(K_out, Hk, D, "K_out")
+    rc = _fast.qk_norm_rope(_PACK_ROPE(tokens, D, pairs, 1 if adjacent else 0, axes, pos or 0, ps, fr or 0, pa or 0),
+                            _FLOAT[Q.dtype], Q.data_ptr(), Hq, qs, qw, None if K is None else K.data_ptr(), Hk, ks, kw, eps,
+                            y_dtype, Q_out.data_ptr(), qos, None if K is None else K_out.data_ptr(), kos,
+                            _raw_stream(T, dev, stream))
+    if rc:
+        raise LowbitError("lowbit_qk_norm_rope", rc)
+    return Q_out, K_out
+
+
+def _layers(T, cache):
+    """Packed lowbit_kv8 of a cache, or of a list of them (a model's layers), their number, pages, page size and device."""
+    caches = [cache] if hasattr(cache[0], "data_ptr") else cache
+    out = []
+    n, _, P, _ = caches[0][0].shape
+    dev = caches[0][0].get_device()
+    for kc, vc, ks, vs in caches:
+        m, H, Q, D = kc.shape
+        if vc.shape != (m, H, D, Q) or kc.element_size() != 1 or vc.element_size() != 1:
+            raise ValueError("cache: 8-bit codes k [pages][heads][tokens][dim] and v [pages][heads][dim][tokens]")
+        if ks.shape != (m, H) or vs.shape != (m, H) or ks.dtype != T.uint8 or vs.dtype != T.uint8:
+            raise ValueError("cache: uint8 scales [pages][heads]")
+        if not (kc.is_contiguous() and vc.is_contiguous() and ks.is_contiguous() and vs.is_contiguous()):
+            raise ValueError("cache: contiguous tensors")
+        if m != n or Q != P:
+            raise ValueError("caches: the same pages in every layer")
+        _device(T, dev, kc, vc, ks, vs)
+        out.append(_PACK_KV8(m, Q, H, D, kc.data_ptr(), vc.data_ptr(), ks.data_ptr(), vs.data_ptr()))
+    return b"".join(out), len(out), n, P, dev
+
+
+def _ints(T, t, shape, what):
+    """Address of a contiguous int32 tensor of a shape."""
+    if t.dtype != T.int32 or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{what}: contiguous int32 {list(shape)}")
+    return t.data_ptr()
+
+
+def _out_ints(T, out, shapes, names, device, stream):
+    if out is None:
+        return tuple(_empty(T, s, T.int32, device, stream) for s in shapes)
+    out = tuple(out)
+    if len(out) != len(shapes):
+        raise ValueError(f"out: {', '.join(names)}")
+    for t, s, n in zip(out, shapes, names):
+        _ints(T, t, s, n)
+    return out
+
+
+def kv8_fork(cache, page_table, kv_lens, refs, parents, grow=0, width=None, max_grow=None, out=None, stream=None):
+    """The next batch's (page_table [new][width], kv_lens [new], refs [pages], failed [1]) from this one's (see
+    lowbit_kv8_fork): parents int32 [new] on the device; grow: tokens each new sequence is about to append, a
+    number, or int32 [new] on the device with max_grow as its bound.  cache may be a list of a model's layers.
+    width None: page_table's.  out: the four outputs, which overlap no input."""
+    T = _torch or _load()
+    c, n_caches, pages, P, dev = _layers(T, cache)
+    B, w = page_table.shape
+    n = parents.shape[0]
+    width = w if width is None else width
+    if hasattr(grow, "data_ptr"):
+        if max_grow is None:
+            raise ValueError("max_grow: a bound of grow")
+        g = _ints(T, grow, (n,), "grow")
+        _device(T, dev, grow)
+    else:
+        g, max_grow = None, grow
+    pt, ln = _ints(T, page_table, (B, w), "page_table"), _ints(T, kv_lens, (B,), "kv_lens")
+    rf, pr = _ints(T, refs, (pages,), "refs"), _ints(T, parents, (n,), "parents")
+    _device(T, dev, page_table, kv_lens, refs, parents)
+    out = _out_ints(T, out, ((n, width), (n,), (pages,), (1,)), ("page_table", "kv_lens", "refs", "failed"), refs.device, stream)
+    _device(T, dev, *out)
+    rc = _fast.kv8_fork(c, n_caches, B, pt, w, ln, rf, n, pr, g, max_grow, out[0].data_ptr(), width, out[1].data_ptr(),
+                        out[2].data_ptr(), out[3].data_ptr(), _raw_stream(T, dev, stream))
+    if rc:
+        raise LowbitError("lowbit_kv8_fork", rc)
+    return out
+
+
+def kv8_fork_workspace(n_pages, page_tokens, n_seqs, n_new, max_grow):
+    """Workspace bytes lowbit_kv8_fork needs for these sizes (reserve before a capture)."""
+    b = ctypes.c_size_t()
+    _check("lowbit_kv8_fork_workspace",
+           lib().lowbit_kv8_fork_workspace(n_pages, page_tokens, n_seqs, n_new, max_grow, ctypes.byref(b)))
+    return b.value
+
+
+def kv8_compact(cache, page_table, kv_lens, refs, out=None, stream=None):
+    """Moves the pages in use to the front of the cache (see lowbit_kv8_compact; a list of caches: a model's layers).
+    Returns (page_table, refs, remap [pages], live [1]) as they are then."""
+    T = _torch or _load()
+    c, n_caches, pages, P, dev = _layers(T, cache)
+    B, w = page_table.shape
+    pt, ln = _ints(T, page_table, (B, w), "page_table"), _ints(T, kv_lens, (B,), "kv_lens")
+    rf = _ints(T, refs, (pages,), "refs")
+    _device(T, dev, page_table, kv_lens, refs)
+    out = _out_ints(T, out, ((B, w), (pages,), (pages,), (1,)), ("page_table", "refs", "remap", "live"), refs.device, stream)
+    _device(T, dev, *out)
+    rc = _fast.kv8_compact(c, n_caches, B, pt, w, ln, rf, out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(),
+                           out[3].data_ptr(), _raw_stream(T, dev, stream))
+    if rc:
+        raise LowbitError("lowbit_kv8_compact", rc)
+    return out
+
+
+def kv8_compact_workspace(n_pages):
+    """Workspace bytes lowbit_kv8_compact needs for a cache of n_pages."""
+    b = ctypes.c_size_t()
+    _check("lowbit_kv8_compact_workspace", lib().lowbit_kv8_compact_workspace(n_pages, ctypes.byref(b)))
+    return b.value
 
 
 def hbm_read_probe(src, out, stream=None):
