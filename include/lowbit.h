@@ -43,8 +43,9 @@
  * point waits for the GPU except lowbit_chain_status, lowbit_chain_destroy
  * and lowbit_release_workspaces, which say so.
  *
- * Streams, workspaces and graphs.  lowbit_gemv, lowbit_gemm, lowbit_gemm_mxfp4
- * and lowbit_attention_kv8 use a device workspace that the library owns, one
+ * Streams, workspaces and graphs.  lowbit_gemv, lowbit_gemm, lowbit_gemm_mxfp4,
+ * lowbit_attention_kv8, lowbit_attention_kv8_prefix, lowbit_kv8_fork and
+ * lowbit_kv8_compact use a device workspace that the library owns, one
  * per (device, stream).  Calls on one stream are ordered and share it; calls on
  * different streams never share one.  A call that needs more than its stream's workspace holds allocates a
  * larger one (hipMalloc, which may synchronize the device as HIP does) and
@@ -54,7 +55,7 @@
  * cannot grow its workspace: such a call returns LOWBIT_E_NOMEM, so reserve
  * the workspace first (lowbit_workspace_bytes + lowbit_reserve_workspace, or
  * one eager call of the largest captured product on that stream;
- * lowbit_gemm_mxfp4_workspace and lowbit_attention_kv8_workspace for those).
+ * the calls beyond products have a ..._workspace call each).
  * A captured graph keeps the workspace address it was captured with; replaying it is
  * valid until lowbit_release_workspaces.  Replays of graphs captured on one
  * stream must run in order on one stream (they share its workspace).  The
@@ -547,6 +548,47 @@ int lowbit_attention_kv8(const lowbit_kv8* cache, const lowbit_kv8_batch* batch,
                          int64_t window, uint16_t* O_bf16, int64_t o_stride, float* lse, void* stream);
 int lowbit_attention_kv8_workspace(const lowbit_kv8* cache, const lowbit_kv8_batch* batch, int64_t q_heads,
                                    size_t* bytes);
+
+/* Sequences that begin with the same tokens (answers to one prompt, prompts behind
+ * one instruction): group g's sequences are seq_starts[g] .. seq_starts[g + 1] - 1
+ * of the batch, so that its rows lie in order, and the tokens they share are
+ * the first lens[g] of the pages in page_table's row g.  seq_starts NULL: n_seqs
+ * / n_groups each, in order.  max_seqs and max_len bound the sequences of any one
+ * group and its lengths; they size the launch, so keep them close.  Arrays are read
+ * on the device, as those of lowbit_kv8_batch, and can not lead a kernel outside the
+ * buffers either: lengths are cut to max_len, sequences to the batch's, a group's rows to
+ * max_seqs * max_q. */
+typedef struct lowbit_kv8_prefix {
+  int64_t n_groups;
+  const int32_t* page_table; /* device [n_groups][table_width] */
+  int64_t table_width;
+  const int32_t* lens;       /* device [n_groups], 0 allowed */
+  const int32_t* seq_starts; /* device [n_groups + 1], or NULL */
+  int64_t max_seqs;          /* seq_starts NULL: ignored */
+  int64_t max_len;           /* at most table_width * page_tokens */
+} lowbit_kv8_prefix;
+
+/* lowbit_attention_kv8 for sequences behind shared prefixes: every row of a
+ * sequence sees all tokens of its group's prefix, and of its own tokens what a
+ * row of lowbit_attention_kv8 sees (window 0).  The batch describes the own tokens
+ * alone: kv_lens counts them, page_table holds their pages (its table_width is the
+ * distance of two rows, so it may point into rows that begin with the prefix's
+ * pages: page_table + k, kv_lens less k * page_tokens, max_kv at most
+ * (table_width - k) * page_tokens).  A prefix need not end with a page.  Each
+ * prefix is read once for all rows of its group, as a prompt's tokens are (in tiles
+ * of 128 or 256 rows; 16 or 32 where the group has few); one row's sums over prefix
+ * and own tokens are joined in fp32.  Sequences of no group have no
+ * prefix.  Rows of a sequence behind its first max_q are not defined, should
+ * q_starts have more.  Everything else is as lowbit_attention_kv8 says, limits included, for the
+ * groups too (their rows: min(total_q, max_seqs * max_q)); total_q * q_heads * (head_dim + 4) <= 2^38.
+ * Needs workspace in every case (lowbit_attention_kv8_prefix_workspace).
+ * Errors: as lowbit_attention_kv8. */
+int lowbit_attention_kv8_prefix(const lowbit_kv8* cache, const lowbit_kv8_prefix* prefix,
+                                const lowbit_kv8_batch* batch, int64_t q_heads, const uint16_t* Q_bf16,
+                                int64_t q_stride, float softmax_scale, int causal, uint16_t* O_bf16,
+                                int64_t o_stride, float* lse, void* stream);
+int lowbit_attention_kv8_prefix_workspace(const lowbit_kv8* cache, const lowbit_kv8_prefix* prefix,
+                                          const lowbit_kv8_batch* batch, int64_t q_heads, size_t* bytes);
 
 /* =====================  heads of queries and keys  ========================
  * Between a fused q/k/v product and lowbit_kv8_append / lowbit_attention_kv8

@@ -120,3 +120,16 @@ class Pages:
             h = held(self._cut(n, len(row)), P)
             out.append([to[p] if 0 <= p < N else -1 for p in row[:h]] + [-1] * (len(row) - h))
         return out, new, to, L, list(zip(movers, holes))
+
+
+def attention_prefix(q, Kp, Vp, Ko, Vo, first, scale, causal):
+    """q [n][Hq][D] behind Kp, Vp [prefix][H][D], its own tokens Ko, Vo [T][H][D], query i at own position first + i.
+    Returns O, lse and the bound's ingredients, as mx_ref.attention does."""
+    import mx_ref
+    n, Hq, D = q.shape
+    out = []
+    for i in range(n):
+        hi = max(0, min(len(Ko), first + i + 1)) if causal else len(Ko)
+        K, V = np.concatenate((Kp, Ko[:hi])), np.concatenate((Vp, Vo[:hi]))
+        out.append(mx_ref.attention(q[i:i + 1], K, V, 0, scale, False, 0))
+    return tuple(np.concatenate(x) for x in zip(*out))

@@ -603,6 +603,8 @@ int kv8_check(const lowbit_kv8* c, const lowbit_kv8_batch* b, KvArgs* out) {
   out->max_q = b->max_q;
   out->max_kv = b->max_kv;
   out->bad = b->bad_pages;
+  out->members = nullptr;
+  out->member_count = out->n_members = out->member_q = 0;
   return LOWBIT_OK;
 }
 
@@ -674,6 +676,83 @@ int lowbit_attention_kv8(const lowbit_kv8* cache, const lowbit_kv8_batch* batch,
     if (r2) return r2;
   }
   return hip_status(launch_attention(a, ws, (hipStream_t)stream));
+}
+
+namespace {
+
+// checks of what a call behind shared prefixes has in common with its workspace query
+int prefix_check(const lowbit_kv8* cache, const lowbit_kv8_prefix* p, const lowbit_kv8_batch* batch, int64_t q_heads,
+                 AttnArgs* a, KvArgs* out) {
+  if (!p) return LOWBIT_E_NULL;
+  const int rc = kv8_check(cache, batch, &a->kv);
+  if (rc) return rc;
+  if (!p->page_table || !p->lens) return LOWBIT_E_NULL;
+  if (p->n_groups < 1 || p->n_groups > (1 << 20) || p->table_width < 1 || p->table_width > (1 << 26))
+    return LOWBIT_E_SHAPE;
+  if (p->max_len < 1 || p->max_len > (1 << 30) || p->max_len > p->table_width * cache->page_tokens) return LOWBIT_E_SHAPE;
+  if (p->seq_starts ? p->max_seqs < 1 || p->max_seqs > batch->n_seqs : batch->n_seqs % p->n_groups != 0)
+    return LOWBIT_E_SHAPE;
+  if (!aligned(p->page_table, 4) || !aligned(p->lens, 4) || (p->seq_starts && !aligned(p->seq_starts, 4)))
+    return LOWBIT_E_ALIGN;
+  const int64_t each = batch->n_seqs / p->n_groups, seqs = p->seq_starts ? p->max_seqs : each;
+  *out = a->kv;
+  out->n_seqs = p->n_groups;
+  out->table = p->page_table;
+  out->width = p->table_width;
+  out->lens = p->lens;
+  out->max_q = std::min(batch->total_q, seqs * batch->max_q);
+  out->max_kv = p->max_len;
+  out->members = p->seq_starts;
+  out->member_count = each;
+  out->n_members = batch->n_seqs;
+  out->member_q = batch->max_q;
+  if (!attention_heads_ok(a->kv, q_heads) || !attention_heads_ok(*out, q_heads)) return LOWBIT_E_SHAPE;
+  if (a->kv.total_q * q_heads > (int64_t(1) << 38) / (a->kv.D + 4)) return LOWBIT_E_SHAPE;
+  a->Hq = q_heads;
+  a->G = q_heads / a->kv.H;
+  return LOWBIT_OK;
+}
+
+}  // namespace
+
+int lowbit_attention_kv8_prefix_workspace(const lowbit_kv8* cache, const lowbit_kv8_prefix* prefix,
+                                          const lowbit_kv8_batch* batch, int64_t q_heads, size_t* bytes) {
+  if (!bytes) return LOWBIT_E_NULL;
+  *bytes = 0;
+  AttnArgs a = {};
+  KvArgs pk = {};
+  const int rc = prefix_check(cache, prefix, batch, q_heads, &a, &pk);
+  if (rc) return rc;
+  *bytes = attention_prefix_workspace_bytes(a, pk);
+  return LOWBIT_OK;
+}
+
+int lowbit_attention_kv8_prefix(const lowbit_kv8* cache, const lowbit_kv8_prefix* prefix,
+                                const lowbit_kv8_batch* batch, int64_t q_heads, const uint16_t* Q_bf16,
+                                int64_t q_stride, float softmax_scale, int causal, uint16_t* O_bf16,
+                                int64_t o_stride, float* lse, void* stream) {
+  if (!Q_bf16 || !O_bf16) return LOWBIT_E_NULL;
+  AttnArgs a = {};
+  KvArgs pk = {};
+  const int rc = prefix_check(cache, prefix, batch, q_heads, &a, &pk);
+  if (rc) return rc;
+  const int64_t row = q_heads * a.kv.D, most = int64_t(1) << 40;
+  if (q_stride < row || o_stride < row || q_stride > most || o_stride > most) return LOWBIT_E_SHAPE;
+  a.scale2 = softmax_scale * 1.4426950408889634f;
+  if (!(a.scale2 - a.scale2 == 0.0f)) return LOWBIT_E_UNSUPPORTED;  // infinite or NaN
+  if (!aligned(Q_bf16, 16) || !aligned(O_bf16, 16) || q_stride % 8 != 0 || o_stride % 8 != 0 ||
+      (lse && !aligned(lse, 4)))
+    return LOWBIT_E_ALIGN;
+  a.q = Q_bf16;
+  a.q_stride = q_stride;
+  a.causal = causal ? 1 : 0;
+  a.o = O_bf16;
+  a.o_stride = o_stride;
+  a.lse = lse;
+  void* ws = nullptr;
+  const int r2 = workspace((hipStream_t)stream, attention_prefix_workspace_bytes(a, pk), &ws);
+  if (r2) return r2;
+  return hip_status(launch_attention_prefix(a, pk, ws, (hipStream_t)stream));
 }
 
 // ------------------------------------------- heads of queries and keys; pages

@@ -20,6 +20,12 @@
 // products are, rounded once (off by 2^-8 at most, the output's own rounding): a
 // second term would take 2 x 4096 rows, 40 heads over 8, D = 128, from 383 to 497 us
 // and attn_prompt32<64> out of its registers (221 -> 511 us).
+//
+// MODE.  kPlain: a call's rows see one sequence each.  Behind a prefix shared by
+// a group of sequences a call runs in two: kPrefix, where the "sequences" are the
+// groups (the rows of their sequences lie in order) and results go to the
+// workspace as sums; kOwn, each sequence's own tokens, whose results go out as
+// those of kPlain and to the workspace too.  attn_merge adds the two.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -30,8 +36,13 @@
 namespace lowbit {
 namespace {
 
+enum Mode { kPlain, kOwn, kPrefix };
+
 constexpr int kUnit = 64;  // tokens of one step of a wave
 constexpr float kLn2 = 0.6931471805599453f;
+// Results that are still to be joined lie in rows of kPartPad floats more than D:
+// sums of O (before the division), maximum (of base 2), sum of weights.
+constexpr int kPartPad = 4;
 
 // eight codes times the power of two s as bf16 (exact: four significant bits)
 __device__ __forceinline__ v8bf bf16x8_of_e4m3(uint32_t w0, uint32_t w1, float s) {
@@ -190,7 +201,7 @@ __device__ __forceinline__ float2 get2(const float* p) {
 constexpr int kDecWaves = 4;
 constexpr int kBlock = kUnit * kDecWaves;  // tokens of a block: a step of every wave
 
-template <int D, int NC>
+template <int D, int NC, int MODE>
 __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_decode(AttnArgs a) {
   constexpr int DC = D / 64, DT = D / 16;
   __shared__ __attribute__((aligned(16))) float lo_[kDecWaves / 2][NC * 16 * D];  // partial O of half the waves
@@ -208,7 +219,7 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
   };
   auto tiles_of = [&](const SeqSpan& t) -> int64_t { return (t.n * a.G + 16 * NC - 1) / (16 * NC); };
   auto work_of = [&](int64_t i) -> int64_t {
-    const SeqSpan t = seq_span(a.kv, i);
+    const SeqSpan t = seq_span<MODE == kPrefix>(a.kv, i);
     return tiles_of(t) * blocks_of(t);
   };
   ItemScan<64 * kDecWaves, decltype(work_of)> scan(a.kv.n_seqs, work_of, scan_);
@@ -226,7 +237,7 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
   int h = (int)quot(x, per_head);
   int64_t b, item;
   scan.find(x - h * per_head, &b, &item);
-  SeqSpan s = seq_span(a.kv, b);
+  SeqSpan s = seq_span<MODE == kPrefix>(a.kv, b);
   int64_t blocks = blocks_of(s), tiles = tiles_of(s);
   int64_t rt = quot(item, blocks);
   int at = (int)(item - rt * blocks);  // first block of this share in the tile
@@ -522,6 +533,13 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
           if (rho[c] >= R) continue;
           const float inv = lt[c] > 0.f || lt[c] != lt[c] ? 1.0f / lt[c] : 0.f;
           const int64_t tok = s.row0 + rho[c] / a.G, hd = h * a.G + rho[c] % a.G;
+          if constexpr (MODE != kPlain) {
+            float* sums = a.sums + (tok * a.Hq + hd) * (D + kPartPad);
+#pragma unroll
+            for (int d = 0; d < DT; d++) *(v4f*)(sums + 16 * d + 4 * g) = o[c][d];
+            if (g == 0) *(float2*)(sums + D) = make_float2(mt[c], lt[c]);
+          }
+          if constexpr (MODE == kPrefix) continue;
           uint16_t* op = a.o + tok * a.o_stride + hd * D + 4 * g;
 #pragma unroll
           for (int d = 0; d < DT; d++) {
@@ -619,6 +637,12 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
       auto finish = [&](int r, int d, float px, float py) {
         const float L = jl[r], inv = L > 0.f || L != L ? 1.0f / L : 0.f;
         const int64_t rr = rho0 + r, tok = s.row0 + rr / a.G, hd = h * a.G + rr % a.G;
+        if constexpr (MODE != kPlain) {
+          float* sums = a.sums + (tok * a.Hq + hd) * (D + kPartPad);
+          *(float2*)(sums + d) = make_float2(px, py);
+          if (d == 0) *(float2*)(sums + D) = make_float2(jm[r], L);
+        }
+        if constexpr (MODE == kPrefix) return;
         *(uint32_t*)(a.o + tok * a.o_stride + hd * D + d) = bf16_bits(px * inv) | (bf16_bits(py * inv) << 16);
         if (a.lse && d == 0) a.lse[tok * a.Hq + hd] = L == 0.f ? -INFINITY : (jm[r] + __builtin_amdgcn_logf(L)) * kLn2;
       };
@@ -656,7 +680,7 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
           b = 0;
           h++;
         }
-        s = seq_span(a.kv, b);
+        s = seq_span<MODE == kPrefix>(a.kv, b);
         tiles = tiles_of(s);
       } while (tiles == 0);  // some sequence has tiles, as x < total
       blocks = blocks_of(s);
@@ -672,10 +696,6 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
 // heads over 4, D = 256: 593 us (0.70 PFLOP/s).
 // Where the tiles do not fill the chip, a tile's steps are cut into parts, one
 // workgroup each, whose results attn_join puts together.
-//
-// A part's results lie in rows of kPartPad floats more than D: sums of O
-// (before the division), maximum (of base 2), sum of weights.
-constexpr int kPartPad = 4;
 // Parts of a tile of `steps` steps: at most the launch's, which knows only a
 // bound on the length.  A step takes some 1.5 us, a part more to join 0.4: twice
 // the root of the steps is best (40 tokens of 32 heads over 8, D = 128, in 4096
@@ -697,7 +717,7 @@ struct Seen {
 };
 
 // A tile of ROWS rows of one sequence and key head.
-template <int ROWS>
+template <int ROWS, int MODE>
 struct PromptTile {
   int64_t b;     // sequence
   SeqSpan s;
@@ -710,12 +730,12 @@ struct PromptTile {
   // tile number `at` of a head, all sequences in turn; false behind the last
   template <int THREADS>
   __device__ __forceinline__ bool find(const AttnArgs& a, uint32_t at, int64_t* mem) {
-    auto tiles = [&](int64_t i) -> int64_t { return (seq_span(a.kv, i).n * a.G + ROWS - 1) / ROWS; };
+    auto tiles = [&](int64_t i) -> int64_t { return (seq_span<MODE == kPrefix>(a.kv, i).n * a.G + ROWS - 1) / ROWS; };
     ItemScan<THREADS, decltype(tiles)> scan(a.kv.n_seqs, tiles, mem);
     if (at >= scan.total) return false;
     int64_t item;
     scan.find(at, &b, &item);
-    s = seq_span(a.kv, b);
+    s = seq_span<MODE == kPrefix>(a.kv, b);
     R = s.n * (int)a.G;
     wg0 = (R - 1) / ROWS * ROWS - (int)item * ROWS;  // the last, longest tiles of a sequence first
     first = s.len - s.n;
@@ -738,7 +758,7 @@ struct PromptTile {
   }
 };
 
-template <int D, int NC, int WAVES>
+template <int D, int NC, int WAVES, int MODE>
 __global__ __launch_bounds__(64 * WAVES, 2) void attn_prompt(AttnArgs a) {
   constexpr int DS = D / 32, DT = D / 16, HALF = 32 * WAVES, SP = 4 * D / HALF;
   static_assert(SP * HALF == 4 * D, "whole 16-byte pieces per thread");
@@ -752,7 +772,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attn_prompt(AttnArgs a) {
   const uint32_t G = (uint32_t)a.G, H = (uint32_t)a.kv.H, at_part = blockIdx.x / H, tile_at = at_part / (uint32_t)a.parts;
   const int h = (int)(blockIdx.x - at_part * H), part = (int)(at_part - tile_at * a.parts);
   __shared__ int64_t scan_[WAVES + 2];
-  PromptTile<ROWS> t;
+  PromptTile<ROWS, MODE> t;
   if (!t.template find<64 * WAVES>(a, tile_at, scan_) || part >= t.parts) return;
   const SeqSpan s = t.s;
   const int R = t.R, wg0 = t.wg0, len = s.len, first = t.first, P = 1 << a.kv.lp, rho0 = wg0 + wave * 16 * NC;
@@ -1037,7 +1057,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attn_prompt(AttnArgs a) {
 #pragma unroll
       for (int e = 0; e < 4; e++)
         if ((nanned[c] >> (4 * d + e)) & 1) o[c][d][e] = __uint_as_float(0x7FC00000u);
-    if (parts > 1) {
+    if (MODE == kPrefix || parts > 1) {
       float* pp = a.part + ((int64_t)blockIdx.x * ROWS + (rho[c] - wg0)) * (D + kPartPad);
 #pragma unroll
       for (int d = 0; d < DT; d++) *(v4f*)(pp + 16 * d + 4 * g) = o[c][d];
@@ -1047,6 +1067,12 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attn_prompt(AttnArgs a) {
     const float inv = l[c] > 0.f || l[c] != l[c] ? 1.0f / l[c] : 0.f;
     const uint32_t tok = (uint32_t)rho[c] / G;
     const int64_t row = s.row0 + tok, hd = (int64_t)h * G + (rho[c] - tok * G);
+    if constexpr (MODE == kOwn) {
+      float* sums = a.sums + (row * a.Hq + hd) * (D + kPartPad);
+#pragma unroll
+      for (int d = 0; d < DT; d++) *(v4f*)(sums + 16 * d + 4 * g) = o[c][d];
+      if (g == 0) *(float2*)(sums + D) = make_float2(m[c], l[c]);
+    }
     uint16_t* op = a.o + row * a.o_stride + hd * D + 4 * g;
 #pragma unroll
     for (int d = 0; d < DT; d++) {
@@ -1074,7 +1100,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attn_prompt(AttnArgs a) {
 // busy in 24% of the cycles, LDS is active in 20%; vector instructions take 47% at
 // four cycles each and the exponentials' quarter rate some 17% more (2 x 4096 in
 // 4096, 32 heads over 8: 226 us).  One register is spilled.
-template <int D, int NC, int WAVES, int OCC>
+template <int D, int NC, int WAVES, int OCC, int MODE>
 __global__ __launch_bounds__(64 * WAVES, OCC) void attn_prompt32(AttnArgs a) {
   constexpr int DS = D / 16, DT = D / 32, HALF = 32 * WAVES, SP = 4 * D / HALF, PS = WAVES / 4;
   static_assert(SP * HALF == 4 * D, "whole 16-byte pieces per thread");
@@ -1090,7 +1116,7 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void attn_prompt32(AttnArgs a) {
   const uint32_t G = (uint32_t)a.G, H = (uint32_t)a.kv.H, at_part = blockIdx.x / H, tile_at = at_part / (uint32_t)a.parts;
   const int h = (int)(blockIdx.x - at_part * H), part = (int)(at_part - tile_at * a.parts);
   __shared__ int64_t scan_[WAVES + 2];
-  PromptTile<ROWS> t;
+  PromptTile<ROWS, MODE> t;
   if (!t.template find<64 * WAVES>(a, tile_at, scan_) || part >= t.parts) return;
   const SeqSpan s = t.s;
   const int R = t.R, wg0 = t.wg0, len = s.len, first = t.first, P = 1 << a.kv.lp, rho0 = wg0 + wave * 32 * NC;
@@ -1393,23 +1419,25 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void attn_prompt32(AttnArgs a) {
     pg1 = page_of(u + 2, e2);
     if (keys || u < u1) meet();
   }
-  if (parts > 1) {
+  // sums of row c to where they are joined
+  auto write_sums = [&](int c, float* pp) {
+#pragma unroll
+    for (int d = 0; d < DT; d++)
+#pragma unroll
+      for (int x = 0; x < 4; x++) {
+        v4f y;
+#pragma unroll
+        for (int e = 0; e < 4; e++)
+          y[e] = (nanned[c] >> (16 * d + 4 * x + e)) & 1 ? __uint_as_float(0x7FC00000u) : o[c][d][4 * x + e];
+        *(v4f*)(pp + 32 * d + 8 * x + 4 * hf) = y;
+      }
+    if (hf == 0) *(float2*)(pp + D) = make_float2(m[c], l[c]);
+  };
+  if (MODE == kPrefix || parts > 1) {
 #pragma unroll
     for (int c = 0; c < NC; c++) {
       l[c] += __shfl_xor(l[c], 32);
-      if (rho[c] >= R) continue;
-      float* pp = a.part + ((int64_t)blockIdx.x * ROWS + (rho[c] - wg0)) * (D + kPartPad);
-#pragma unroll
-      for (int d = 0; d < DT; d++)
-#pragma unroll
-        for (int x = 0; x < 4; x++) {
-          v4f y;
-#pragma unroll
-          for (int e = 0; e < 4; e++)
-            y[e] = (nanned[c] >> (16 * d + 4 * x + e)) & 1 ? __uint_as_float(0x7FC00000u) : o[c][d][4 * x + e];
-          *(v4f*)(pp + 32 * d + 8 * x + 4 * hf) = y;
-        }
-      if (hf == 0) *(float2*)(pp + D) = make_float2(m[c], l[c]);
+      if (rho[c] < R) write_sums(c, a.part + ((int64_t)blockIdx.x * ROWS + (rho[c] - wg0)) * (D + kPartPad));
     }
     return;
   }
@@ -1419,6 +1447,11 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void attn_prompt32(AttnArgs a) {
 #pragma unroll
   for (int c = 0; c < NC; c++) {
     l[c] += __shfl_xor(l[c], 32);
+    if constexpr (MODE == kOwn) {
+      const uint32_t at = (uint32_t)rho[c] / G;
+      if (rho[c] < R)
+        write_sums(c, a.sums + ((s.row0 + at) * a.Hq + (int64_t)h * G + (rho[c] - at * G)) * (D + kPartPad));
+    }
     const float inv = l[c] > 0.f || l[c] != l[c] ? 1.0f / l[c] : 0.f;
 #pragma unroll
     for (int d = 0; d < DT; d++)
@@ -1452,12 +1485,12 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void attn_prompt32(AttnArgs a) {
 // M the largest m_k, in the order of the parts.  One thread for four dims of a
 // row, rows of ROWS as the tile's workgroups have them.  Eight parts are read at
 // once: the loads' latency bounds it (some 3 us with the launch for 16 parts).
-template <int D, int ROWS>
+template <int D, int ROWS, int MODE>
 __global__ __launch_bounds__(256) void attn_join(AttnArgs a) {
   constexpr int T4 = D / 4, AHEAD = 8;
   const uint32_t G = (uint32_t)a.G, H = (uint32_t)a.kv.H, tile_at = blockIdx.x / H, h = blockIdx.x - tile_at * H;
   __shared__ int64_t scan_[256 / 64 + 2];
-  PromptTile<ROWS> t;
+  PromptTile<ROWS, MODE> t;
   if (!t.template find<256>(a, tile_at, scan_) || t.parts == 1) return;  // one part: its workgroup has written O
   const int parts = t.parts, at = blockIdx.y * 256 + threadIdx.x, r = at / T4, d = at % T4 * 4;
   if (t.wg0 + r >= t.R) return;
@@ -1491,9 +1524,76 @@ __global__ __launch_bounds__(256) void attn_join(AttnArgs a) {
       for (int c = 0; c < 4; c++) o[c] += w * po[e][c];
     }
   }
-  const float inv = L > 0.f || L != L ? 1.0f / L : 0.f;
   const uint32_t rc = t.wg0 + r, tok = rc / G;
   const int64_t row = t.s.row0 + tok, hd = (int64_t)h * G + (rc - tok * G);
+  if constexpr (MODE == kOwn) {
+    float* sums = a.sums + (row * a.Hq + hd) * (D + kPartPad);
+    *(v4f*)(sums + d) = o;
+    if (d == 0) *(float2*)(sums + D) = make_float2(M, L);
+  }
+  const float inv = L > 0.f || L != L ? 1.0f / L : 0.f;
+  uint2 w;
+  w.x = bf16_bits(o[0] * inv) | (bf16_bits(o[1] * inv) << 16);
+  w.y = bf16_bits(o[2] * inv) | (bf16_bits(o[3] * inv) << 16);
+  *(uint2*)(a.o + row * a.o_stride + hd * D + d) = w;
+  if (a.lse && d == 0) a.lse[row * a.Hq + hd] = L == 0.f ? -INFINITY : (M + __builtin_amdgcn_logf(L)) * kLn2;
+}
+
+// A row behind a shared prefix: its sums over its own tokens and over the prefix
+// (of one launch or of its parts), joined as attn_join does.  The tiles are those
+// of the prefixes' rows, so rows without a prefix keep what kOwn wrote.
+struct MergeArgs {
+  AttnArgs a;         // of the prefixes' launch
+  const float* own;   // [total_q][Hq] sums
+  const float* rows;  // the prefixes' likewise; NULL: in a.part, by tiles and parts
+};
+template <int D, int ROWS>
+__global__ __launch_bounds__(256) void attn_merge(MergeArgs args) {
+  constexpr int MODE = kPrefix, T4 = D / 4, AHEAD = 8;
+  const AttnArgs& a = args.a;
+  const uint32_t G = (uint32_t)a.G, H = (uint32_t)a.kv.H, tile_at = blockIdx.x / H, h = blockIdx.x - tile_at * H;
+  __shared__ int64_t scan_[256 / 64 + 2];
+  PromptTile<ROWS, MODE> t;
+  if (!t.template find<256>(a, tile_at, scan_)) return;
+  const int at = blockIdx.y * 256 + threadIdx.x, r = at / T4, d = at % T4 * 4;
+  if (t.wg0 + r >= t.R) return;
+  const uint32_t rc = t.wg0 + r, tok = rc / G;
+  const int64_t row = t.s.row0 + tok, hd = (int64_t)h * G + (rc - tok * G);
+  const float* own = args.own + (row * a.Hq + hd) * (D + kPartPad);
+  const int64_t step = (int64_t)H * ROWS * (D + kPartPad);  // to the next part
+  const float* p = args.rows ? args.rows + (row * a.Hq + hd) * (D + kPartPad)
+                             : a.part + (((int64_t)tile_at * a.parts * H + h) * ROWS + r) * (D + kPartPad);
+  const int parts = args.rows ? 1 : t.parts;
+  v4f o = *(const v4f*)(own + d);
+  const float2 own_ml = *(const float2*)(own + D);
+  float M = own_ml.x, L = own_ml.y;
+  for (int k = 0; k < parts; k += AHEAD) {
+    v4f po[AHEAD];
+    float2 ml[AHEAD];
+#pragma unroll
+    for (int e = 0; e < AHEAD; e++) {
+      const float* q = p + min(k + e, parts - 1) * step;
+      po[e] = *(const v4f*)(q + d);
+      ml[e] = *(const float2*)(q + D);
+    }
+    float mx = M;
+#pragma unroll
+    for (int e = 0; e < AHEAD; e++) mx = fmaxf(mx, ml[e].x);
+    const float mu = mx == -INFINITY ? 0.f : mx, al = __builtin_amdgcn_exp2f(M - mu);
+    M = mx;
+    L *= al;
+#pragma unroll
+    for (int c = 0; c < 4; c++) o[c] *= al;
+#pragma unroll
+    for (int e = 0; e < AHEAD; e++) {
+      if (k + e >= parts) break;
+      const float w = __builtin_amdgcn_exp2f(ml[e].x - mu);
+      L += w * ml[e].y;
+#pragma unroll
+      for (int c = 0; c < 4; c++) o[c] += w * po[e][c];
+    }
+  }
+  const float inv = L > 0.f || L != L ? 1.0f / L : 0.f;
   uint2 w;
   w.x = bf16_bits(o[0] * inv) | (bf16_bits(o[1] * inv) << 16);
   w.y = bf16_bits(o[2] * inv) | (bf16_bits(o[3] * inv) << 16);
@@ -1559,43 +1659,106 @@ Plan plan_attention(const KvArgs& kv, int64_t G, int64_t window) {
   return p;
 }
 
+// bytes behind the counters that a plan's results take until they are joined
+size_t plan_bytes(const Plan& p, int D) {
+  if (p.nc > 0) return (size_t)4 * kMaxShares * 16 * p.nc * (D + 2) * 4;
+  return (size_t)(p.blocks * p.parts * p.rows) * (D + kPartPad) * 4;
+}
+
+// one launch by its plan, and the join of a prompt's parts
+template <int MODE>
+void launch_plan(const Plan& p, AttnArgs a, hipStream_t s) {
+  a.parts = p.parts;
+  const dim3 grid((unsigned)(p.blocks * p.parts));
+  const int D = a.kv.D;
+  if (p.nc == 0) {
+    if (D == 64) hipLaunchKernelGGL((attn_prompt32<64, 1, 4, 3, MODE>), grid, dim3(256), 0, s, a);
+    else if (D == 128 && p.rows == 128) hipLaunchKernelGGL((attn_prompt32<128, 1, 4, 2, MODE>), grid, dim3(256), 0, s, a);
+    else if (D == 128) hipLaunchKernelGGL((attn_prompt32<128, 1, 8, 2, MODE>), grid, dim3(512), 0, s, a);
+    else hipLaunchKernelGGL((attn_prompt<256, 1, 8, MODE>), grid, dim3(512), 0, s, a);
+    if constexpr (MODE != kPrefix) {
+      if (p.parts == 1) return;
+      const dim3 join((unsigned)p.blocks, (unsigned)(p.rows * D / 4 / 256));
+      if (D == 64) hipLaunchKernelGGL((attn_join<64, 128, MODE>), join, dim3(256), 0, s, a);
+      else if (D == 128 && p.rows == 128) hipLaunchKernelGGL((attn_join<128, 128, MODE>), join, dim3(256), 0, s, a);
+      else if (D == 128) hipLaunchKernelGGL((attn_join<128, 256, MODE>), join, dim3(256), 0, s, a);
+      else hipLaunchKernelGGL((attn_join<256, 128, MODE>), join, dim3(256), 0, s, a);
+    }
+    return;
+  }
+#define LOWBIT_DEC(DD, NN) \
+  hipLaunchKernelGGL((attn_decode<DD, NN, MODE>), grid, dim3(64 * kDecWaves), 0, s, a)
+  if (D == 64 && p.nc == 1) LOWBIT_DEC(64, 1);
+  else if (D == 64) LOWBIT_DEC(64, 2);
+  else if (D == 128) LOWBIT_DEC(128, 1);
+  else LOWBIT_DEC(256, 1);
+#undef LOWBIT_DEC
+}
+
+// Of a call behind shared prefixes: the sequences' own launch and the prefixes'.
+struct PrefixPlan {
+  Plan own, prefix;
+  int64_t rows, merge_blocks;  // of a merge tile
+  size_t sums, own_bytes, prefix_bytes;
+};
+PrefixPlan plan_prefix(const AttnArgs& a, const KvArgs& prefix) {
+  PrefixPlan p;
+  p.own = plan_attention(a.kv, a.G, 0);
+  p.prefix = plan_attention(prefix, a.G, 0);
+  p.rows = p.prefix.nc == 0 ? p.prefix.rows : 128;
+  p.merge_blocks = p.prefix.nc == 0 ? p.prefix.blocks
+                                    : std::min<int64_t>(prefix.n_seqs * prefix.H * cdiv(prefix.max_q * a.G, p.rows),
+                                                        prefix.H * (prefix.total_q * a.G / p.rows + prefix.n_seqs));
+  p.sums = (size_t)(a.kv.total_q * a.Hq) * (a.kv.D + kPartPad) * 4;
+  p.own_bytes = p.own.nc == 0 && p.own.parts == 1 ? 0 : plan_bytes(p.own, a.kv.D);
+  p.prefix_bytes = plan_bytes(p.prefix, a.kv.D);
+  return p;
+}
+
 }  // namespace
 
 int64_t attention_blocks(const KvArgs& kv, int64_t G) { return plan_attention(kv, G, 0).blocks; }
 
 size_t attention_workspace_bytes(const KvArgs& kv, int64_t G) {
   const Plan p = plan_attention(kv, G, 0);  // a window takes no more
-  if (p.nc > 0) return (size_t)kCounterBytes + (size_t)4 * kMaxShares * 16 * p.nc * (kv.D + 2) * 4;
-  if (p.parts == 1) return 0;
-  return (size_t)kCounterBytes + (size_t)(p.blocks * p.parts * p.rows) * (kv.D + kPartPad) * 4;
+  if (p.nc == 0 && p.parts == 1) return 0;
+  return (size_t)kCounterBytes + plan_bytes(p, kv.D);
 }
 
 hipError_t launch_attention(AttnArgs a, void* ws, hipStream_t s) {
-  const Plan p = plan_attention(a.kv, a.G, a.causal ? a.window : 0);
   a.cnt = (uint32_t*)ws + 16;
   a.part = (float*)((uint8_t*)ws + kCounterBytes);
-  a.parts = p.parts;
-  const dim3 grid((unsigned)(p.blocks * p.parts));
-  if (p.nc == 0) {
-    if (a.kv.D == 64) hipLaunchKernelGGL((attn_prompt32<64, 1, 4, 3>), grid, dim3(256), 0, s, a);
-    else if (a.kv.D == 128 && p.rows == 128) hipLaunchKernelGGL((attn_prompt32<128, 1, 4, 2>), grid, dim3(256), 0, s, a);
-    else if (a.kv.D == 128) hipLaunchKernelGGL((attn_prompt32<128, 1, 8, 2>), grid, dim3(512), 0, s, a);
-    else hipLaunchKernelGGL((attn_prompt<256, 1, 8>), grid, dim3(512), 0, s, a);
-    if (p.parts == 1) return hipGetLastError();
-    const dim3 join((unsigned)p.blocks, (unsigned)(p.rows * a.kv.D / 4 / 256));
-    if (a.kv.D == 64) hipLaunchKernelGGL((attn_join<64, 128>), join, dim3(256), 0, s, a);
-    else if (a.kv.D == 128 && p.rows == 128) hipLaunchKernelGGL((attn_join<128, 128>), join, dim3(256), 0, s, a);
-    else if (a.kv.D == 128) hipLaunchKernelGGL((attn_join<128, 256>), join, dim3(256), 0, s, a);
-    else hipLaunchKernelGGL((attn_join<256, 128>), join, dim3(256), 0, s, a);
-    return hipGetLastError();
-  }
-#define LOWBIT_DEC(DD, NN) \
-  hipLaunchKernelGGL((attn_decode<DD, NN>), grid, dim3(64 * kDecWaves), 0, s, a)
-  if (a.kv.D == 64 && p.nc == 1) LOWBIT_DEC(64, 1);
-  else if (a.kv.D == 64) LOWBIT_DEC(64, 2);
-  else if (a.kv.D == 128) LOWBIT_DEC(128, 1);
-  else LOWBIT_DEC(256, 1);
-#undef LOWBIT_DEC
+  launch_plan<kPlain>(plan_attention(a.kv, a.G, a.causal ? a.window : 0), a, s);
+  return hipGetLastError();
+}
+
+size_t attention_prefix_workspace_bytes(const AttnArgs& a, const KvArgs& prefix) {
+  const PrefixPlan p = plan_prefix(a, prefix);
+  return (size_t)kCounterBytes + p.sums * (p.prefix.nc > 0 ? 2 : 1) + p.own_bytes + p.prefix_bytes;
+}
+
+hipError_t launch_attention_prefix(AttnArgs a, const KvArgs& prefix, void* ws, hipStream_t s) {
+  const PrefixPlan p = plan_prefix(a, prefix);
+  uint8_t* at = (uint8_t*)ws + kCounterBytes;
+  float *own = (float*)at, *rows = p.prefix.nc > 0 ? (float*)(at + p.sums) : nullptr;
+  at += p.sums * (p.prefix.nc > 0 ? 2 : 1);
+  a.cnt = (uint32_t*)ws + 16;
+  a.sums = own;
+  a.part = (float*)at;
+  launch_plan<kOwn>(p.own, a, s);
+  MergeArgs m{a, own, rows};
+  m.a.kv = prefix;
+  m.a.causal = 0;
+  m.a.cnt += kCounterWords / 2;
+  m.a.sums = rows;
+  m.a.part = (float*)(at + p.own_bytes);
+  m.a.parts = p.prefix.nc == 0 ? p.prefix.parts : 1;
+  launch_plan<kPrefix>(p.prefix, m.a, s);
+  const dim3 grid((unsigned)p.merge_blocks, (unsigned)(p.rows * a.kv.D / 4 / 256));
+  if (a.kv.D == 64) hipLaunchKernelGGL((attn_merge<64, 128>), grid, dim3(256), 0, s, m);
+  else if (a.kv.D == 128 && p.rows == 128) hipLaunchKernelGGL((attn_merge<128, 128>), grid, dim3(256), 0, s, m);
+  else if (a.kv.D == 128) hipLaunchKernelGGL((attn_merge<128, 256>), grid, dim3(256), 0, s, m);
+  else hipLaunchKernelGGL((attn_merge<256, 128>), grid, dim3(256), 0, s, m);
   return hipGetLastError();
 }
 

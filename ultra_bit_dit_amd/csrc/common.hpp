@@ -215,5 +215,8 @@ hipError_t launch_kv8_append(const KvArgs& a, bool f32, const void* K, const voi
 int64_t attention_blocks(const KvArgs& kv, int64_t G);
 size_t attention_workspace_bytes(const KvArgs& kv, int64_t G);
 hipError_t launch_attention(AttnArgs a, void* ws, hipStream_t s);
+// the same behind prefixes that groups of sequences share
+size_t attention_prefix_workspace_bytes(const AttnArgs& a, const KvArgs& prefix);
+hipError_t launch_attention_prefix(AttnArgs a, const KvArgs& prefix, void* ws, hipStream_t s);
 
 }  // namespace lowbit

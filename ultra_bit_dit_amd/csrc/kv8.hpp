@@ -26,6 +26,10 @@ struct KvArgs {
   const int32_t* starts;     // [n_seqs + 1] rows of the new tokens, or NULL: max_q each
   int64_t total_q, max_q, max_kv;
   int32_t* bad;              // counts unreadable pages, or NULL
+  // Groups in the place of sequences: a group's rows are those of its sequences.
+  const int32_t* members;    // [n_seqs + 1] first sequence of each group, or NULL: member_count each
+  int64_t member_count;
+  int64_t n_members, member_q;  // sequences in all, and rows of each where `starts` (theirs) is NULL
 };
 
 // Length and new tokens of sequence b, clamped to what the table and the
@@ -34,13 +38,24 @@ struct SeqSpan {
   int64_t row0;  // first row of its new tokens
   int n, len;    // new tokens, length with them
 };
+template <bool GROUPS = false>
 __device__ __forceinline__ SeqSpan seq_span(const KvArgs& a, int64_t b) {
   SeqSpan s;
   int64_t len = a.lens[b];
   len = len < 0 ? 0 : len;
   len = len < a.max_kv ? len : a.max_kv;  // max_kv <= width * page tokens
-  int64_t r0 = a.starts ? (int64_t)a.starts[b] : b * a.max_q;
-  int64_t r1 = a.starts ? (int64_t)a.starts[b + 1] : r0 + a.max_q;
+  int64_t r0, r1;
+  if constexpr (GROUPS) {
+    int64_t m0 = a.members ? (int64_t)a.members[b] : b * a.member_count;
+    int64_t m1 = a.members ? (int64_t)a.members[b + 1] : m0 + a.member_count;
+    m0 = m0 < 0 ? 0 : m0 < a.n_members ? m0 : a.n_members;
+    m1 = m1 < m0 ? m0 : m1 < a.n_members ? m1 : a.n_members;
+    r0 = a.starts ? (int64_t)a.starts[m0] : m0 * a.member_q;
+    r1 = a.starts ? (int64_t)a.starts[m1] : m1 * a.member_q;
+  } else {
+    r0 = a.starts ? (int64_t)a.starts[b] : b * a.max_q;
+    r1 = a.starts ? (int64_t)a.starts[b + 1] : r0 + a.max_q;
+  }
   r0 = r0 < 0 ? 0 : r0;
   r1 = r1 < a.total_q ? r1 : a.total_q;
   int64_t n = r1 > r0 ? r1 - r0 : 0;
@@ -109,6 +124,7 @@ struct AttnArgs {
   float* lse;                // [total_q][Hq] or NULL
   float* part;               // results of shares: two places each, then of their groups; or of a tile's parts
   int parts;                 // of a prompt tile
+  float* sums;               // [total_q][Hq] sums before the division, for a row that is joined with more tokens
   uint32_t* cnt;             // arrivals: of a group (by the place of its first share), then of a tile
 };
 

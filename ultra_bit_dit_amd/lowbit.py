@@ -28,7 +28,7 @@ EXPORTS = ("lowbit_abi_version", "lowbit_status_str", "lowbit_packed_bytes", "lo
            "lowbit_hbm_read_probe", "lowbit_quantize_weights", "lowbit_rotate_act",
            "lowbit_mxfp4_bytes", "lowbit_pack_mxfp4", "lowbit_quantize_mxfp4", "lowbit_gemm_mxfp4", "lowbit_gemm_mxfp4_workspace",
            "lowbit_kv8_append", "lowbit_attention_kv8", "lowbit_attention_kv8_workspace",
-           "lowbit_qk_norm_rope", "lowbit_kv8_fork", "lowbit_kv8_fork_workspace", "lowbit_kv8_compact",
+           "lowbit_attention_kv8_prefix", "lowbit_attention_kv8_prefix_workspace", "lowbit_qk_norm_rope", "lowbit_kv8_fork", "lowbit_kv8_fork_workspace", "lowbit_kv8_compact",
            "lowbit_kv8_compact_workspace")
 
 
@@ -52,6 +52,13 @@ class Kv8Batch(ctypes.Structure):
     _fields_ = [("n_seqs", ctypes.c_int64), ("page_table", ctypes.c_void_p), ("table_width", ctypes.c_int64),
                 ("kv_lens", ctypes.c_void_p), ("q_starts", ctypes.c_void_p), ("total_q", ctypes.c_int64),
                 ("max_q", ctypes.c_int64), ("max_kv", ctypes.c_int64), ("bad_pages", ctypes.c_void_p)]
+
+
+class Kv8Prefix(ctypes.Structure):
+    """lowbit_kv8_prefix"""
+    _fields_ = [("n_groups", ctypes.c_int64), ("page_table", ctypes.c_void_p), ("table_width", ctypes.c_int64),
+                ("lens", ctypes.c_void_p), ("seq_starts", ctypes.c_void_p), ("max_seqs", ctypes.c_int64),
+                ("max_len", ctypes.c_int64)]
 
 
 class Rope(ctypes.Structure):
@@ -111,6 +118,9 @@ def lib():
         L.lowbit_kv8_append.argtypes = [kvp, kbp, i32, vp, vp, i64, i64, vp]
         L.lowbit_attention_kv8.argtypes = [kvp, kbp, i64, vp, i64, ctypes.c_float, i32, i64, vp, i64, vp, vp]
         L.lowbit_attention_kv8_workspace.argtypes = [kvp, kbp, i64, szp]
+        kpp = ctypes.POINTER(Kv8Prefix)
+        L.lowbit_attention_kv8_prefix.argtypes = [kvp, kpp, kbp, i64, vp, i64, ctypes.c_float, i32, vp, i64, vp, vp]
+        L.lowbit_attention_kv8_prefix_workspace.argtypes = [kvp, kpp, kbp, i64, szp]
         L.lowbit_qk_norm_rope.argtypes = [ctypes.POINTER(Rope), i32, vp, i64, i64, vp, vp, i64, i64, vp, ctypes.c_float, i32,
                                           vp, i64, vp, i64, vp]
         L.lowbit_kv8_fork.argtypes = [kvp, i64, i64, vp, i64, vp, vp, i64, vp, vp, i64, vp, i64, vp, vp, vp, vp]
@@ -282,6 +292,7 @@ _FLOAT = {}       # torch type -> lowbit_dtype of the float inputs
 _fast = None      # the same exports with address-only prototypes
 _PACK_KV8 = struct.Struct("@qiiiPPPP").pack        # lowbit_kv8
 _PACK_BATCH = struct.Struct("@qPqPPqqqP").pack     # lowbit_kv8_batch
+_PACK_PREFIX = struct.Struct("@qPqPPqq").pack      # lowbit_kv8_prefix
 _PACK_ROPE = struct.Struct("@qiiiiPqPP").pack      # lowbit_rope
 
 
@@ -293,6 +304,7 @@ class _Fast:
                 ("lowbit_gemm_mxfp4", [i64, i64, i64, vp, vp, i32, vp, i64, vp, i32, vp, vp]),
                 ("lowbit_kv8_append", [vp, vp, i32, vp, vp, i64, i64, vp]),
                 ("lowbit_attention_kv8", [vp, vp, i64, vp, i64, ctypes.c_float, i32, i64, vp, i64, vp, vp]),
+                ("lowbit_attention_kv8_prefix", [vp, vp, vp, i64, vp, i64, ctypes.c_float, i32, vp, i64, vp, vp]),
                 ("lowbit_qk_norm_rope", [vp, i32, vp, i64, i64, vp, vp, i64, i64, vp, ctypes.c_float, i32, vp, i64, vp, i64,
                                          vp]),
                 ("lowbit_kv8_fork", [vp, i64, i64, vp, i64, vp, vp, i64, vp, vp, i64, vp, i64, vp, vp, vp, vp]),
@@ -580,6 +592,112 @@ def attention_kv8_workspace(cache, page_table, kv_lens, q_heads, total_q, q_star
     _check("lowbit_attention_kv8_workspace",
            lib().lowbit_attention_kv8_workspace(Kv8.from_buffer_copy(c), Kv8Batch.from_buffer_copy(b), q_heads,
                                                 ctypes.byref(n)))
+    return n.value
+
+
+def _rows(T, t, what):
+    """Address and row distance of an int32 [rows][columns] tensor whose rows may be strided."""
+    if t.dtype != T.int32 or t.dim() != 2 or t.shape[0] < 1 or t.shape[1] < 1:
+        raise ValueError(f"{what}: int32 [rows][pages]")
+    rows, cols = t.shape
+    if (cols > 1 and t.stride(1) != 1) or (rows > 1 and t.stride(0) < cols):
+        raise ValueError(f"{what}: a row's entries have to be contiguous")
+    return t.data_ptr(), t.stride(0) if rows > 1 else cols
+
+
+def _prefix(T, cache, prefix_table, prefix_lens, page_table, kv_lens, seq_starts, q_starts, total_q, max_q, max_kv,
+            max_prefix, max_seqs, bad_pages):
+    """Checked and packed lowbit_kv8, lowbit_kv8_prefix and lowbit_kv8_batch, and the tensors' device."""
+    kc, vc, ks, vs = cache
+    n, H, P, D = kc.shape
+    if vc.shape != (n, H, D, P) or kc.element_size() != 1 or vc.element_size() != 1:
+        raise ValueError("cache: 8-bit codes k [pages][heads][tokens][dim] and v [pages][heads][dim][tokens]")
+    if ks.shape != (n, H) or vs.shape != (n, H) or ks.dtype != T.uint8 or vs.dtype != T.uint8:
+        raise ValueError("cache: uint8 scales [pages][heads]")
+    if not (kc.is_contiguous() and vc.is_contiguous() and ks.is_contiguous() and vs.is_contiguous()):
+        raise ValueError("cache: contiguous tensors")
+    pt, stride = _rows(T, page_table, "page_table")
+    qt, qstride = _rows(T, prefix_table, "prefix_table")
+    B, groups = page_table.shape[0], prefix_table.shape[0]
+    ln, pl = _ints(T, kv_lens, (B,), "kv_lens"), _ints(T, prefix_lens, (groups,), "prefix_lens")
+    ss = qs = bad = 0
+    if seq_starts is not None:
+        ss = _ints(T, seq_starts, (groups + 1,), "seq_starts")
+    elif B % groups:
+        raise ValueError("without seq_starts every group has the same number of sequences")
+    if q_starts is not None:
+        qs = _ints(T, q_starts, (B + 1,), "q_starts")
+    elif total_q % B:
+        raise ValueError("without q_starts every sequence has the same number of new tokens")
+    if max_q is None:
+        max_q = total_q // B if q_starts is None else total_q
+    if max_kv is None:
+        max_kv = page_table.shape[1] * P
+    if max_prefix is None:
+        max_prefix = prefix_table.shape[1] * P
+    if max_kv > page_table.shape[1] * P or max_prefix > prefix_table.shape[1] * P:
+        raise ValueError("max_kv, max_prefix: at most what the tables hold")
+    if bad_pages is not None:
+        if bad_pages.dtype != T.int32 or bad_pages.numel() < 1:
+            raise ValueError("bad_pages: int32")
+        bad = bad_pages.data_ptr()
+    dev = kc.get_device()
+    _device(T, dev, vc, ks, vs, page_table, prefix_table, kv_lens, prefix_lens, seq_starts, q_starts, bad_pages)
+    return (_PACK_KV8(n, P, H, D, kc.data_ptr(), vc.data_ptr(), ks.data_ptr(), vs.data_ptr()),
+            _PACK_PREFIX(groups, qt, qstride, pl, ss, B if max_seqs is None else max_seqs, max_prefix),
+            _PACK_BATCH(B, pt, stride, ln, qs, total_q, max_q, max_kv, bad), dev)
+
+
+def attention_kv8_prefix(Q, cache, prefix_table, prefix_lens, page_table, kv_lens, seq_starts=None, q_starts=None,
+                         max_q=None, max_kv=None, max_prefix=None, max_seqs=None, softmax_scale=None, causal=True, O=None,
+                         lse=None, return_lse=False, bad_pages=None, stream=None):
+    """attention_kv8 behind prefixes that groups of sequences share (see lowbit_attention_kv8_prefix): group g's
+    sequences are seq_starts[g] .. seq_starts[g + 1] - 1 (None: equally many each), their common tokens the first
+    prefix_lens[g] of prefix_table's row g; page_table and kv_lens are of each sequence's own tokens behind them.
+    Either table may be a slice of wider rows (page_table[:, k:]).  Returns O, or (O, lse) with return_lse.
+    max_q, max_kv, max_prefix and max_seqs bound a sequence's new tokens and own length, a prefix and a group's
+    sequences; they size the launches and choose the kernels.  Without them: all the tokens (with q_starts), the
+    whole tables, all the sequences (with seq_starts)."""
+    T = _torch or _load()
+    D = cache[0].shape[3]
+    if Q.dim() != 3 or Q.dtype != T.bfloat16:
+        raise ValueError("Q: bf16 [tokens][q_heads][dim]")
+    tokens, Hq, _ = Q.shape
+    qs = _heads(Q, Hq, D, "Q")
+    c, p, b, dev = _prefix(T, cache, prefix_table, prefix_lens, page_table, kv_lens, seq_starts, q_starts, tokens, max_q, max_kv,
+                           max_prefix, max_seqs, bad_pages)
+    if Q.get_device() != dev:
+        raise ValueError("Q lies on another device than the cache")
+    if O is None:
+        O = _empty(T, (tokens, Hq, D), T.bfloat16, Q.device, stream)
+        os = Hq * D
+    else:
+        if O.shape != Q.shape or O.dtype != T.bfloat16 or O.get_device() != dev:
+            raise ValueError("O: bf16 of Q's shape, on its device")
+        os = _heads(O, Hq, D, "O")
+    if lse is None:
+        if return_lse:
+            lse = _empty(T, (tokens, Hq), T.float32, Q.device, stream)
+    elif lse.shape != (tokens, Hq) or lse.dtype != T.float32 or not lse.is_contiguous() or lse.get_device() != dev:
+        raise ValueError("lse: contiguous fp32 [tokens][q_heads] on Q's device")
+    rc = _fast.attention_kv8_prefix(c, p, b, Hq, Q.data_ptr(), qs, D ** -0.5 if softmax_scale is None else softmax_scale,
+                                    1 if causal else 0, O.data_ptr(), os, None if lse is None else lse.data_ptr(),
+                                    _raw_stream(T, dev, stream))
+    if rc:
+        raise LowbitError("lowbit_attention_kv8_prefix", rc)
+    return (O, lse) if return_lse else O
+
+
+def attention_kv8_prefix_workspace(cache, prefix_table, prefix_lens, page_table, kv_lens, q_heads, total_q, seq_starts=None,
+                                   q_starts=None, max_q=None, max_kv=None, max_prefix=None, max_seqs=None):
+    """Workspace bytes lowbit_attention_kv8_prefix needs for these arguments (reserve before a capture)."""
+    T = _torch or _load()
+    c, p, b, _ = _prefix(T, cache, prefix_table, prefix_lens, page_table, kv_lens, seq_starts, q_starts, total_q, max_q, max_kv,
+                         max_prefix, max_seqs, None)
+    n = ctypes.c_size_t()
+    _check("lowbit_attention_kv8_prefix_workspace",
+           lib().lowbit_attention_kv8_prefix_workspace(Kv8.from_buffer_copy(c), Kv8Prefix.from_buffer_copy(p),
+                                                       Kv8Batch.from_buffer_copy(b), q_heads, ctypes.byref(n)))
     return n.value
 
 
