@@ -669,8 +669,8 @@ int lowbit_kv8_fork(const lowbit_kv8* caches, int64_t n_caches, int64_t n_seqs, 
                     int64_t table_width, const int32_t* kv_lens, const int32_t* refs, int64_t n_new,
                     const int32_t* parents, const int32_t* grow, int64_t max_grow, int32_t* new_table,
                     int64_t new_width, int32_t* new_lens, int32_t* new_refs, int32_t* failed, void* stream);
-int lowbit_kv8_fork_workspace(int64_t n_pages, int page_tokens, int64_t n_seqs, int64_t n_new, int64_t max_grow,
-                              size_t* bytes);
+int lowbit_kv8_fork_workspace(int64_t n_pages, int page_tokens, int64_t n_caches, int64_t n_seqs, int64_t n_new,
+                              int64_t max_grow, size_t* bytes);
 
 /* Closes the cache up: with *live pages in use (refs > 0), the k-th page in use
  * at or behind *live moves to the k-th free page before it, so that the pages
@@ -684,7 +684,7 @@ int lowbit_kv8_fork_workspace(int64_t n_pages, int page_tokens, int64_t n_seqs, 
 int lowbit_kv8_compact(const lowbit_kv8* caches, int64_t n_caches, int64_t n_seqs, const int32_t* page_table,
                        int64_t table_width, const int32_t* kv_lens, const int32_t* refs, int32_t* new_table,
                        int32_t* new_refs, int32_t* remap, int32_t* live, void* stream);
-int lowbit_kv8_compact_workspace(int64_t n_pages, size_t* bytes);
+int lowbit_kv8_compact_workspace(int64_t n_pages, int64_t n_caches, size_t* bytes);
 
 #ifdef __cplusplus
 }

@@ -89,10 +89,10 @@ def test_fork_refusals():
         assert fork(**kw) == lb.E_SHAPE, kw
     b = ctypes.c_size_t(7)
     f = lb.lib().lowbit_kv8_fork_workspace
-    assert f(64, 16, 1, 1, 1, None) == lb.E_NULL
-    assert f(64, 17, 1, 1, 1, ctypes.byref(b)) == lb.E_UNSUPPORTED and b.value == 0
-    for bad in ((0, 16, 1, 1, 1), (1 << 27, 16, 1, 1, 1), (64, 16, -1, 1, 1), (64, 16, 1, 1 << 21, 1), (64, 16, 1, 1, -1),
-                (64, 16, 1, 1 << 20, 1 << 20)):
+    assert f(64, 16, 1, 1, 1, 1, None) == lb.E_NULL
+    assert f(64, 17, 1, 1, 1, 1, ctypes.byref(b)) == lb.E_UNSUPPORTED and b.value == 0
+    for bad in ((0, 16, 1, 1, 1, 1), (1 << 27, 16, 1, 1, 1, 1), (64, 16, 1, -1, 1, 1), (64, 16, 1, 1, 1 << 21, 1),
+                (64, 16, 1, 1, 1, -1), (64, 16, 1, 1, 1 << 20, 1 << 20), (64, 16, 0, 1, 1, 1), (64, 16, 4097, 1, 1, 1)):
         assert f(*bad, ctypes.byref(b)) == lb.E_SHAPE
     assert lb.kv8_fork_workspace(64, 16, 0, 0, 0) > 0
     # the free pages' list grows with what can be asked for, never past the pages
@@ -108,9 +108,9 @@ def test_compact_refusals():
         assert compact(**kw) == lb.E_SHAPE, kw
     b = ctypes.c_size_t(7)
     f = lb.lib().lowbit_kv8_compact_workspace
-    assert f(64, None) == lb.E_NULL
-    assert f(0, ctypes.byref(b)) == lb.E_SHAPE and b.value == 0
-    assert f((1 << 26) + 1, ctypes.byref(b)) == lb.E_SHAPE
+    assert f(64, 1, None) == lb.E_NULL
+    assert f(0, 1, ctypes.byref(b)) == lb.E_SHAPE and b.value == 0
+    assert f((1 << 26) + 1, 1, ctypes.byref(b)) == lb.E_SHAPE and f(64, 0, ctypes.byref(b)) == lb.E_SHAPE
 
 
 # ------------------------------------------------------- the plain forms' pins

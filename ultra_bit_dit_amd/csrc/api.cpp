@@ -858,14 +858,16 @@ int no_throw(F&& f) {
 
 }  // namespace
 
-int lowbit_kv8_fork_workspace(int64_t n_pages, int page_tokens, int64_t n_seqs, int64_t n_new, int64_t max_grow,
-                              size_t* bytes) {
+int lowbit_kv8_fork_workspace(int64_t n_pages, int page_tokens, int64_t n_caches, int64_t n_seqs, int64_t n_new,
+                              int64_t max_grow, size_t* bytes) {
   if (!bytes) return LOWBIT_E_NULL;
   *bytes = 0;
   if (log2_page(page_tokens) < 0) return LOWBIT_E_UNSUPPORTED;
+  if (n_caches < 1 || n_caches > kMaxCaches) return LOWBIT_E_SHAPE;
   if (!fork_sizes_ok(n_pages, page_tokens, n_seqs, n_new, max_grow)) return LOWBIT_E_SHAPE;
   ForkArgs a = {};
   a.n_pages = n_pages;
+  a.n_layers = n_caches;
   a.lp = log2_page(page_tokens);
   a.n_seqs = n_seqs;
   a.n_new = n_new;
@@ -894,6 +896,7 @@ int lowbit_kv8_fork(const lowbit_kv8* caches, int64_t n_caches, int64_t n_seqs, 
     if (!aligned(new_refs, 16)) return LOWBIT_E_ALIGN;
     ForkArgs a = {};
     a.n_pages = caches[0].n_pages;
+    a.n_layers = n_caches;
     a.lp = log2_page(P);
     a.n_seqs = n_seqs;
     a.width = n_seqs ? table_width : 1;
@@ -913,16 +916,17 @@ int lowbit_kv8_fork(const lowbit_kv8* caches, int64_t n_caches, int64_t n_seqs, 
     void* ws = nullptr;
     const int r2 = workspace((hipStream_t)stream, fork_workspace_bytes(a), &ws);
     if (r2) return r2;
-    return hip_status(launch_fork(a, layers.data(), n_caches, ws, (hipStream_t)stream));
+    return hip_status(launch_fork(a, layers.data(), ws, (hipStream_t)stream));
   });
 }
 
-int lowbit_kv8_compact_workspace(int64_t n_pages, size_t* bytes) {
+int lowbit_kv8_compact_workspace(int64_t n_pages, int64_t n_caches, size_t* bytes) {
   if (!bytes) return LOWBIT_E_NULL;
   *bytes = 0;
-  if (n_pages < 1 || n_pages > kMaxCachePages) return LOWBIT_E_SHAPE;
+  if (n_pages < 1 || n_pages > kMaxCachePages || n_caches < 1 || n_caches > kMaxCaches) return LOWBIT_E_SHAPE;
   CompactArgs a = {};
   a.n_pages = n_pages;
+  a.n_layers = n_caches;
   *bytes = compact_workspace_bytes(a);
   return LOWBIT_OK;
 }
@@ -942,6 +946,7 @@ int lowbit_kv8_compact(const lowbit_kv8* caches, int64_t n_caches, int64_t n_seq
       if (!aligned(p, 4)) return LOWBIT_E_ALIGN;
     CompactArgs a = {};
     a.n_pages = caches[0].n_pages;
+    a.n_layers = n_caches;
     a.lp = log2_page(caches[0].page_tokens);
     a.n_seqs = n_seqs;
     a.width = n_seqs ? table_width : 1;
@@ -956,6 +961,6 @@ int lowbit_kv8_compact(const lowbit_kv8* caches, int64_t n_caches, int64_t n_seq
     void* ws = nullptr;
     const int r2 = workspace((hipStream_t)stream, compact_workspace_bytes(a), &ws);
     if (r2) return r2;
-    return hip_status(launch_compact(a, layers.data(), n_caches, ws, (hipStream_t)stream));
+    return hip_status(launch_compact(a, layers.data(), ws, (hipStream_t)stream));
   });
 }

@@ -203,8 +203,8 @@ bool fork_fits(const ForkArgs& a);  // one launch holds its workgroups
 bool compact_fits(const CompactArgs& a);
 size_t fork_workspace_bytes(ForkArgs a);
 size_t compact_workspace_bytes(CompactArgs a);
-hipError_t launch_fork(ForkArgs a, const KvLayer* caches, int64_t n_caches, void* ws, hipStream_t s);
-hipError_t launch_compact(CompactArgs a, const KvLayer* caches, int64_t n_caches, void* ws, hipStream_t s);
+hipError_t launch_fork(ForkArgs a, const KvLayer* caches, void* ws, hipStream_t s);
+hipError_t launch_compact(CompactArgs a, const KvLayer* caches, void* ws, hipStream_t s);
 
 struct KvArgs;
 struct AttnArgs;

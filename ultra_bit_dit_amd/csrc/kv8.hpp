@@ -70,8 +70,13 @@ struct KvLayer {
   int H, D;
   uint8_t *kc, *vc, *ks, *vs;
 };
+struct PageLayer {
+  uint8_t *k, *v, *ks, *vs;
+  int64_t bytes;             // of a page's keys
+  int heads;
+};
 struct ForkArgs {
-  int64_t n_pages;
+  int64_t n_pages, n_layers;
   int lp;                    // log2 of a page's tokens
   int64_t n_seqs, width;
   const int32_t* table;      // [n_seqs][width]
@@ -84,10 +89,10 @@ struct ForkArgs {
   int32_t* new_lens;         // [n_new]
   int32_t* new_refs;         // [n_pages]
   int32_t* failed;           // pages that were not found
+  int pieces;                // a page of the largest layer is moved in
   // workspace
+  PageLayer* layers;
   int* children;             // [n_seqs]
-  int* first;                // [n_pages] the first child that will write to the page, and how many will:
-  int* writers;              // [n_pages] set for those pages only
   int* fresh;                // free pages, for the children in turn
   int64_t* start;            // [n_new] twice the place of a child's first one there, and 1 if that is a copy
   int *src, *dst;            // copies: a page, and the place of the one it is copied to
@@ -95,7 +100,7 @@ struct ForkArgs {
   int64_t* found;            // pages in `fresh`
 };
 struct CompactArgs {
-  int64_t n_pages;
+  int64_t n_pages, n_layers;
   int lp;
   int64_t n_seqs, width;
   const int32_t* table;
@@ -105,7 +110,9 @@ struct CompactArgs {
   int32_t* new_refs;
   int32_t* remap;            // [n_pages]
   int32_t* live;             // pages in use
+  int pieces;
   // workspace
+  PageLayer* layers;
   int* count;                // pages in use in each chunk
   int* place;                // [n_pages] where a page goes; -2 - k: to hole[k]; -1: free
   int *hole, *mover;         // the k-th move goes from mover[k] to hole[k]

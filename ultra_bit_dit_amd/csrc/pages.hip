@@ -102,44 +102,135 @@ __global__ void copy_refs(const int32_t* __restrict__ from, int32_t* __restrict_
   if (i < n) to[i] = from[i];
 }
 
+constexpr int kLayers = 32;  // given to a launch
+struct Layers {
+  PageLayer at[kLayers];
+  int n;
+};
+// A table of layers in the workspace: an array among a kernel's arguments that is
+// indexed by a variable would be copied to every lane's private memory (1.5 KB; the
+// moves below took 4 times as long).
+__device__ __forceinline__ void put_layers(PageLayer* to, const Layers& l) {
+#pragma unroll
+  for (int i = 0; i < kLayers; i++)
+    if (i < l.n) to[i] = l.at[i];
+}
+__global__ void more_layers(PageLayer* to, Layers l) { put_layers(to, l); }
+
 // One workgroup: children of each parent, counts of holders, which tail pages
-// are copied, free pages.
-__global__ __launch_bounds__(kPlan) void fork_plan(ForkArgs a) {
+// are copied, free pages.  Bound by the latency of its steps, each of which needs
+// what the one before counted, so the counts lie in LDS where they fit (NEAR).
+//
+// A tail page of r holders, w of which will write to it: with r > w all of them
+// copy and r - w holders stay; with r = w the first one keeps it.  So the writers
+// take themselves off its count, and where that leaves 0, the smallest of them is
+// written in its place.
+constexpr int kNearSeqs = 4096;       // sequences whose children and lengths lie in LDS
+constexpr int kNearPages = 30720;     // pages whose counts do
+constexpr int kFirst = INT32_MIN;     // + child: it keeps the page
+
+template <bool NEAR>
+__global__ __launch_bounds__(kPlan) void fork_plan(ForkArgs a, Layers l) {
   __shared__ int lds[kPlan / 64];
+  __shared__ int near_children[kNearSeqs], near_lens[kNearSeqs];
+  __shared__ __attribute__((aligned(16))) int near_refs[NEAR ? kNearPages : 4];
   const int tid = threadIdx.x;
-  for (int64_t b = tid; b < a.n_seqs; b += kPlan) store_dev(a.children + b, 0);
-  for (int64_t i = tid; i < a.n_new; i += kPlan) {
-    const Child c = child_of(a, i);
-    if (c.tail >= 0) {
-      store_dev(a.first + c.tail, INT32_MAX);
-      store_dev(a.writers + c.tail, 0);
+  const bool near = a.n_seqs <= kNearSeqs;
+  auto add = [&](int64_t p, int d) {
+    if constexpr (NEAR) atomicAdd(near_refs + p, d);
+    else add_dev(a.new_refs + p, d);
+  };
+  auto count = [&](int64_t p) -> int {
+    if constexpr (NEAR) return near_refs[p];
+    else return load_dev(a.new_refs + p);
+  };
+  auto put = [&](int64_t p, int v) {
+    if constexpr (NEAR) near_refs[p] = v;
+    else store_dev(a.new_refs + p, v);
+  };
+  auto step = [&]() {
+    if constexpr (NEAR) __syncthreads();
+    else meet();
+  };
+  if constexpr (NEAR) {
+    constexpr int kRun = 8;
+    for (int p0 = 0; p0 < a.n_pages; p0 += kPlan * kRun) {
+      int r[kRun];
+#pragma unroll
+      for (int e = 0; e < kRun; e++) {
+        const int p = p0 + e * kPlan + tid;
+        r[e] = p < a.n_pages ? a.refs[p] : 0;
+      }
+#pragma unroll
+      for (int e = 0; e < kRun; e++) {
+        const int p = p0 + e * kPlan + tid;
+        if (p < a.n_pages) near_refs[p] = r[e];
+      }
     }
   }
-  meet();
-  for (int64_t i = tid; i < a.n_new; i += kPlan) {
-    const Child c = child_of(a, i);
-    if (c.parent >= 0) add_dev(a.children + c.parent, 1);
-    if (c.tail >= 0) {
-      __hip_atomic_fetch_min(a.first + c.tail, (int)i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      add_dev(a.writers + c.tail, 1);
+  for (int64_t b = tid; b < a.n_seqs; b += kPlan) {
+    if (near) {
+      near_children[b] = 0;
+      near_lens[b] = (int)length_of(a, b);
+    } else {
+      store_dev(a.children + b, 0);
     }
   }
-  meet();
+  // the first children's, which every step wants, stay in registers
+  Child mine;
+  mine.parent = mine.tail = -1;
+  if (tid < a.n_new) mine = child_of(a, tid);
+  auto child = [&](int64_t i) { return i < kPlan ? mine : child_of(a, i); };
+  if (tid == 0) put_layers(a.layers, l);
+  if (near) __syncthreads();
+  else meet();
+  for (int64_t i = tid; i < a.n_new; i += kPlan) {
+    const int64_t b = i < kPlan ? mine.parent : parent_of(a, i);
+    if (b < 0) continue;
+    if (near) atomicAdd(near_children + b, 1);
+    else add_dev(a.children + b, 1);
+  }
+  if (near) __syncthreads();
+  else meet();
   // A page loses its old holders and gains their children: nothing changes for a
-  // sequence that goes on as one.  Teams of threads have a sequence each.
-  int team = 64;
-  while (team < kPlan && team < a.width) team *= 2;
+  // sequence that goes on as one.  Teams of threads have a sequence each, four
+  // entries of a thread on their way at once.
+  constexpr int kAhead = 4;
+  int team = 16;
+  while (team < kPlan && team * kAhead < a.width) team *= 2;
   for (int64_t b = tid / team; b < a.n_seqs; b += kPlan / team) {
-    const int64_t held = pages_of(length_of(a, b), a.lp);
-    const int children = load_dev(a.children + b);
+    const int64_t held = pages_of(near ? near_lens[b] : length_of(a, b), a.lp);
+    const int children = near ? near_children[b] : load_dev(a.children + b);
     if (children == 1 && held <= a.new_width) continue;
-    for (int64_t j = tid & (team - 1); j < held; j += team) {
-      const int64_t p = a.table[b * a.width + j];
-      const int d = (j < a.new_width ? children : 0) - 1;
-      if (d != 0 && p >= 0 && p < a.n_pages) add_dev(a.new_refs + p, d);
+    for (int64_t j0 = tid & (team - 1); j0 < held; j0 += team * kAhead) {
+      int p[kAhead];
+#pragma unroll
+      for (int e = 0; e < kAhead; e++) p[e] = j0 + e * team < held ? a.table[b * a.width + j0 + e * team] : -1;
+#pragma unroll
+      for (int e = 0; e < kAhead; e++) {
+        const int d = (j0 + e * team < a.new_width ? children : 0) - 1;
+        if (d != 0 && p[e] >= 0 && p[e] < a.n_pages) add(p[e], d);
+      }
     }
   }
-  meet();
+  step();
+  for (int64_t i = tid; i < a.n_new; i += kPlan) {
+    const int64_t t = child(i).tail;
+    if (t >= 0) add(t, -1);
+  }
+  step();
+  for (int64_t i = tid; i < a.n_new; i += kPlan) {
+    const int64_t t = child(i).tail;
+    if (t < 0) continue;
+    // 0 until the first child of such a page comes, less from then on
+    if constexpr (NEAR) {
+      if (near_refs[t] <= 0) atomicMin(near_refs + t, kFirst + (int)i);
+    } else {
+      if (load_dev(a.new_refs + t) <= 0)
+        __hip_atomic_fetch_min(a.new_refs + t, kFirst + (int)i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+  }
+  step();
   // pages that the children need, in their order
   int64_t total = 0;
   int copies = 0;
@@ -148,10 +239,8 @@ __global__ __launch_bounds__(kPlan) void fork_plan(ForkArgs a) {
     int need = 0, copy = 0;
     Child c;
     if (i < a.n_new) {
-      c = child_of(a, i);
-      // kept by the first of its writers where nobody else holds it
-      copy = c.tail >= 0 && !(load_dev(a.first + c.tail) == (int)i &&
-                              load_dev(a.new_refs + c.tail) == load_dev(a.writers + c.tail));
+      c = child(i);
+      copy = c.tail >= 0 && count(c.tail) != kFirst + (int)i;
       need = copy + (int)(c.need - c.had);
     }
     int all, all_copies;
@@ -168,74 +257,71 @@ __global__ __launch_bounds__(kPlan) void fork_plan(ForkArgs a) {
     total += all;
     copies += all_copies;
   }
-  // the first `total` free pages; the counts by wide loads, past what L1 may hold of them
+  step();
+  for (int64_t i = tid; i < a.n_new; i += kPlan) {
+    const int64_t t = child(i).tail;
+    if (t >= 0 && count(t) == kFirst + (int)i) put(t, 1);
+  }
+  step();
+  // the first `total` free pages; counts in memory by wide loads, past what L1 may hold of them
   int64_t found = 0;
-  constexpr int kRun = 16;
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+  constexpr int kRun = NEAR ? 4 : 16;
+  if constexpr (!NEAR) __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
   for (int64_t p0 = 0; p0 < a.n_pages && found < total; p0 += kPlan * kRun) {
     const int64_t p = p0 + tid * kRun;
+    const int* counts = NEAR ? near_refs : a.new_refs;
     uint32_t free = 0;
     if (p + kRun <= a.n_pages) {
       mx_u4 r[kRun / 4];
 #pragma unroll
-      for (int e = 0; e < kRun / 4; e++) r[e] = *(const mx_u4*)(a.new_refs + p + 4 * e);
+      for (int e = 0; e < kRun / 4; e++) r[e] = *(const mx_u4*)(counts + p + 4 * e);
 #pragma unroll
       for (int e = 0; e < kRun; e++) free |= r[e / 4][e % 4] == 0 ? 1u << e : 0u;
     } else {
-      for (int e = 0; p + e < a.n_pages; e++) free |= a.new_refs[p + e] == 0 ? 1u << e : 0u;
+      for (int e = 0; p + e < a.n_pages; e++) free |= counts[p + e] == 0 ? 1u << e : 0u;
     }
     int all;
     int64_t at = found + scan_before<kPlan>(__builtin_popcount(free), lds, &all);
     for (; free && at < total; free &= free - 1, at++) {
       const int64_t page = p + __builtin_ctz(free);
       a.fresh[at] = (int)page;
-      a.new_refs[page] = 1;
+      put(page, 1);
     }
     found += all;
   }
-  meet();
-  const bool ok = found >= total;
-  for (int64_t i = tid; ok && i < copies; i += kPlan) add_dev(a.new_refs + a.src[i], -1);
+  if constexpr (NEAR) {
+    __syncthreads();
+    for (int p = tid; p < a.n_pages; p += kPlan) a.new_refs[p] = near_refs[p];
+  }
   if (tid == 0) {
-    *a.n_copies = ok ? copies : 0;
+    *a.n_copies = found >= total ? copies : 0;
     *a.found = min(found, total);
     *a.failed = (int32_t)min(total - min(found, total), (int64_t)INT32_MAX);
   }
 }
 
-struct Layer {
-  uint8_t *k, *v, *ks, *vs;
-  int64_t bytes;  // of a page's keys
-  int heads, pieces;
-};
-constexpr int kLayers = 32;  // of a launch
-struct Layers {
-  Layer at[kLayers];
-  int n, pieces;  // pieces: of a page, all layers
-};
-
-// piece `piece` of page src to page dst
-__device__ __forceinline__ void move_piece(const Layers& l, int piece, int64_t src, int64_t dst) {
-  int i = 0;
-  while (piece >= l.at[i].pieces) piece -= l.at[i++].pieces;
-  const Layer& at = l.at[i];
-  const int half = at.pieces / 2;
+// piece `piece` of the pages of all layers, page src to page dst
+__device__ __forceinline__ void move_piece(const PageLayer* layers, int pieces, int piece, int64_t src, int64_t dst) {
+  const int i = piece / pieces;  // `pieces` of the largest layer
+  piece -= i * pieces;
+  const PageLayer at = layers[i];
+  const int half = (int)((at.bytes + kPiece - 1) / kPiece);
+  if (piece >= 2 * half) return;
   const bool keys = piece < half;
   const int64_t off = (int64_t)(keys ? piece : piece - half) * kPiece;
   uint8_t* base = keys ? at.k : at.v;
   const uint8_t* from = base + src * at.bytes + off;
   uint8_t* to = base + dst * at.bytes + off;
   const int n = (int)min((int64_t)kPiece, at.bytes - off);
-  mx_u4 w[kPiece / (16 * kMoveThreads)];
+  constexpr int kEach = kPiece / (16 * kMoveThreads);
+  mx_u4 w[kEach];
+  if (n == kPiece) {
 #pragma unroll
-  for (int e = 0; e < kPiece / (16 * kMoveThreads); e++) {
-    const int o = (e * kMoveThreads + threadIdx.x) * 16;
-    if (o < n) w[e] = *(const mx_u4*)(from + o);
-  }
+    for (int e = 0; e < kEach; e++) w[e] = *(const mx_u4*)(from + (e * kMoveThreads + threadIdx.x) * 16);
 #pragma unroll
-  for (int e = 0; e < kPiece / (16 * kMoveThreads); e++) {
-    const int o = (e * kMoveThreads + threadIdx.x) * 16;
-    if (o < n) *(mx_u4*)(to + o) = w[e];
+    for (int e = 0; e < kEach; e++) *(mx_u4*)(to + (e * kMoveThreads + threadIdx.x) * 16) = w[e];
+  } else {
+    for (int o = threadIdx.x * 16; o < n; o += kMoveThreads * 16) *(mx_u4*)(to + o) = *(const mx_u4*)(from + o);
   }
   if (off == 0) {
     uint8_t* sc = keys ? at.ks : at.vs;
@@ -244,7 +330,7 @@ __device__ __forceinline__ void move_piece(const Layers& l, int piece, int64_t s
 }
 
 // Table rows of the children, then the copies.
-__global__ __launch_bounds__(kMoveThreads) void fork_apply(ForkArgs a, Layers l, int64_t row_blocks) {
+__global__ __launch_bounds__(kMoveThreads) void fork_apply(ForkArgs a, int64_t row_blocks) {
   if ((int64_t)blockIdx.x < row_blocks) {
     const int64_t per = (a.new_width + kRows - 1) / kRows, i = blockIdx.x / per, j0 = (blockIdx.x - i * per) * kRows;
     const Child c = child_of(a, i);
@@ -264,10 +350,10 @@ __global__ __launch_bounds__(kMoveThreads) void fork_apply(ForkArgs a, Layers l,
     }
     return;
   }
-  const int64_t items = (int64_t)*a.n_copies * l.pieces;
+  const int64_t all = (int64_t)a.n_layers * a.pieces, items = *a.n_copies * all;
   for (int64_t x = blockIdx.x - row_blocks; x < items; x += gridDim.x - row_blocks) {
-    const int64_t i = x / l.pieces;
-    move_piece(l, (int)(x - i * l.pieces), a.src[i], a.fresh[a.dst[i]]);
+    const int64_t i = x / all;
+    move_piece(a.layers, a.pieces, (int)(x - i * all), a.src[i], a.fresh[a.dst[i]]);
   }
 }
 
@@ -276,7 +362,7 @@ constexpr int kChunk = 4096;  // pages of a workgroup
 constexpr int kEach = kChunk / 256;
 
 // pages in use in each chunk
-__global__ __launch_bounds__(256) void compact_count(CompactArgs a) {
+__global__ __launch_bounds__(256) void compact_count(CompactArgs a, Layers l) {
   __shared__ int lds[4];
   const int64_t p0 = blockIdx.x * (int64_t)kChunk;
   int live = 0;
@@ -288,6 +374,7 @@ __global__ __launch_bounds__(256) void compact_count(CompactArgs a) {
   int all;
   (void)scan_before<256>(live, lds, &all);
   if (threadIdx.x == 0) a.count[blockIdx.x] = all;
+  if (blockIdx.x == 0 && threadIdx.x == 64) put_layers(a.layers, l);
 }
 
 // Where each page goes: with L pages in use, the k-th of those at or behind L
@@ -351,7 +438,7 @@ __device__ __forceinline__ int place_of(const CompactArgs& a, int64_t p) {
   return at < -1 ? a.hole[-2 - at] : at;
 }
 
-__global__ __launch_bounds__(kMoveThreads) void compact_apply(CompactArgs a, Layers l, int64_t page_blocks, int64_t row_blocks) {
+__global__ __launch_bounds__(kMoveThreads) void compact_apply(CompactArgs a, int64_t page_blocks, int64_t row_blocks) {
   const int64_t block = blockIdx.x;
   const int moves = *a.n_moves;
   if (block < page_blocks) {
@@ -378,26 +465,36 @@ __global__ __launch_bounds__(kMoveThreads) void compact_apply(CompactArgs a, Lay
     }
     return;
   }
-  const int64_t items = (int64_t)moves * l.pieces, first = page_blocks + row_blocks;
+  const int64_t all = (int64_t)a.n_layers * a.pieces, items = moves * all, first = page_blocks + row_blocks;
   for (int64_t x = block - first; x < items; x += gridDim.x - first) {
-    const int64_t i = x / l.pieces;
-    move_piece(l, (int)(x - i * l.pieces), a.mover[i], a.hole[i]);
+    const int64_t i = x / all;
+    move_piece(a.layers, a.pieces, (int)(x - i * all), a.mover[i], a.hole[i]);
   }
 }
 
 Layers layers_of(const KvLayer* caches, int64_t n, int page_tokens) {
   Layers l;
-  l.n = (int)n;
-  l.pieces = 0;
+  l.n = (int)std::min<int64_t>(kLayers, n);
+  for (int i = 0; i < kLayers; i++) l.at[i] = PageLayer{};
   for (int i = 0; i < l.n; i++) {
-    const int64_t bytes = (int64_t)caches[i].H * page_tokens * caches[i].D;
-    l.at[i] = Layer{caches[i].kc, caches[i].vc, caches[i].ks, caches[i].vs, bytes, caches[i].H, (int)(2 * cdiv(bytes, kPiece))};
-    l.pieces += l.at[i].pieces;
+    const KvLayer& c = caches[i];
+    l.at[i] = PageLayer{c.kc, c.vc, c.ks, c.vs, (int64_t)c.H * page_tokens * c.D, c.H};
   }
   return l;
 }
+// the layers behind those that the first launch has
+void put_more(PageLayer* to, const KvLayer* caches, int64_t n, int page_tokens, hipStream_t s) {
+  for (int64_t c = kLayers; c < n; c += kLayers)
+    hipLaunchKernelGGL(more_layers, dim3(1), dim3(1), 0, s, to + c, layers_of(caches + c, n - c, page_tokens));
+}
+// pieces of a page of the largest layer
+int pieces_of(const KvLayer* caches, int64_t n, int page_tokens) {
+  int64_t most = 0;
+  for (int64_t i = 0; i < n; i++) most = std::max(most, (int64_t)caches[i].H * page_tokens * caches[i].D);
+  return (int)(2 * cdiv(most, kPiece));
+}
 // workgroups that move pages: at most so many pieces, eight workgroups of them a compute unit
-int64_t move_blocks(int64_t pages, const Layers& l) { return std::min<int64_t>(pages * l.pieces, 2048); }
+int64_t move_blocks(int64_t pages, int64_t pieces) { return std::min<int64_t>(pages * pieces, 2048); }
 
 template <class T>
 T* take(uint8_t** at, int64_t n) {
@@ -412,18 +509,18 @@ size_t fork_layout(ForkArgs* a, uint8_t* at) {
   uint8_t* const from = at;
   a->found = take<int64_t>(&at, 1);
   a->n_copies = take<int>(&at, 1);
+  a->layers = take<PageLayer>(&at, a->n_layers);
   a->children = take<int>(&at, a->n_seqs);
   a->start = take<int64_t>(&at, a->n_new);
   a->src = take<int>(&at, a->n_new);
   a->dst = take<int>(&at, a->n_new);
   a->fresh = take<int>(&at, most_fresh(*a));
-  a->first = take<int>(&at, a->n_pages);
-  a->writers = take<int>(&at, a->n_pages);
   return (size_t)(at - from);
 }
 size_t compact_layout(CompactArgs* a, uint8_t* at) {
   uint8_t* const from = at;
   a->n_moves = take<int>(&at, 1);
+  a->layers = take<PageLayer>(&at, a->n_layers);
   a->count = take<int>(&at, cdiv(a->n_pages, kChunk));
   a->place = take<int>(&at, a->n_pages);
   a->hole = take<int>(&at, a->n_pages);
@@ -442,29 +539,37 @@ bool compact_fits(const CompactArgs& a) {
 size_t fork_workspace_bytes(ForkArgs a) { return (size_t)kCounterBytes + fork_layout(&a, nullptr); }
 size_t compact_workspace_bytes(CompactArgs a) { return (size_t)kCounterBytes + compact_layout(&a, nullptr); }
 
-hipError_t launch_fork(ForkArgs a, const KvLayer* caches, int64_t n_caches, void* ws, hipStream_t s) {
+hipError_t launch_fork(ForkArgs a, const KvLayer* caches, void* ws, hipStream_t s) {
   fork_layout(&a, (uint8_t*)ws + kCounterBytes);
-  hipLaunchKernelGGL(copy_refs, dim3((unsigned)cdiv(a.n_pages, 256)), dim3(256), 0, s, a.refs, a.new_refs, a.n_pages);
-  hipLaunchKernelGGL(fork_plan, dim3(1), dim3(kPlan), 0, s, a);
-  for (int64_t c = 0; c < n_caches && a.n_new > 0; c += kLayers) {
-    const Layers l = layers_of(caches + c, std::min<int64_t>(kLayers, n_caches - c), 1 << a.lp);
-    const int64_t rows = c ? 0 : a.n_new * cdiv(a.new_width, kRows);
-    hipLaunchKernelGGL(fork_apply, dim3((unsigned)(rows + move_blocks(a.n_new, l))), dim3(kMoveThreads), 0, s, a, l, rows);
+  const int P = 1 << a.lp;
+  a.pieces = pieces_of(caches, a.n_layers, P);
+  const Layers first = layers_of(caches, a.n_layers, P);
+  if (a.n_pages <= kNearPages) {
+    hipLaunchKernelGGL(fork_plan<true>, dim3(1), dim3(kPlan), 0, s, a, first);
+  } else {
+    hipLaunchKernelGGL(copy_refs, dim3((unsigned)cdiv(a.n_pages, 256)), dim3(256), 0, s, a.refs, a.new_refs, a.n_pages);
+    hipLaunchKernelGGL(fork_plan<false>, dim3(1), dim3(kPlan), 0, s, a, first);
+  }
+  if (a.n_new > 0) {
+    put_more(a.layers, caches, a.n_layers, P, s);
+    const int64_t rows = a.n_new * cdiv(a.new_width, kRows);
+    const dim3 grid((unsigned)(rows + move_blocks(a.n_new, (int64_t)a.pieces * a.n_layers)));
+    hipLaunchKernelGGL(fork_apply, grid, dim3(kMoveThreads), 0, s, a, rows);
   }
   return hipGetLastError();
 }
 
-hipError_t launch_compact(CompactArgs a, const KvLayer* caches, int64_t n_caches, void* ws, hipStream_t s) {
+hipError_t launch_compact(CompactArgs a, const KvLayer* caches, void* ws, hipStream_t s) {
   compact_layout(&a, (uint8_t*)ws + kCounterBytes);
+  const int P = 1 << a.lp;
+  a.pieces = pieces_of(caches, a.n_layers, P);
   const unsigned chunks = (unsigned)cdiv(a.n_pages, kChunk);
-  hipLaunchKernelGGL(compact_count, dim3(chunks), dim3(256), 0, s, a);
+  hipLaunchKernelGGL(compact_count, dim3(chunks), dim3(256), 0, s, a, layers_of(caches, a.n_layers, P));
+  put_more(a.layers, caches, a.n_layers, P, s);
   hipLaunchKernelGGL(compact_plan, dim3(chunks), dim3(256), 0, s, a);
-  for (int64_t c = 0; c < n_caches; c += kLayers) {
-    const Layers l = layers_of(caches + c, std::min<int64_t>(kLayers, n_caches - c), 1 << a.lp);
-    const int64_t pages = c ? 0 : cdiv(a.n_pages, kRows), rows = c ? 0 : a.n_seqs * cdiv(a.width, kRows);
-    hipLaunchKernelGGL(compact_apply, dim3((unsigned)(pages + rows + move_blocks(a.n_pages / 2 + 1, l))), dim3(kMoveThreads), 0,
-                       s, a, l, pages, rows);
-  }
+  const int64_t pages = cdiv(a.n_pages, kRows), rows = a.n_seqs * cdiv(a.width, kRows);
+  const dim3 grid((unsigned)(pages + rows + move_blocks(a.n_pages / 2 + 1, (int64_t)a.pieces * a.n_layers)));
+  hipLaunchKernelGGL(compact_apply, grid, dim3(kMoveThreads), 0, s, a, pages, rows);
   return hipGetLastError();
 }
 

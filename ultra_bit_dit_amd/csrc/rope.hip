@@ -111,90 +111,139 @@ __device__ __forceinline__ float head_sum(float x, int lg) {
   return x;
 }
 
+// 1 / sqrt(v), v >= 0, also where v is subnormal
+__device__ __forceinline__ float inv_root(float v) {
+  const bool small = v < 0x1p-100f;
+  const float r = __builtin_amdgcn_rsqf(small ? v * 0x1p64f : v);
+  return small ? r * 0x1p32f : r;
+}
+
+// slices: parts of a token's heads, `per` of them each.  The wave's heads of all of
+// its tokens are one row of passes (a pass: one head in each team), kHold of them
+// on their way while one is worked on.
 template <bool F32, bool OUT32, int W>
 __global__ __launch_bounds__(64 * kWaves) void qk_norm_rope(RopeArgs a, int lg, int slices, int per) {
   constexpr int EI = F32 ? 4 : 2, EO = OUT32 ? 4 : 2;
   __shared__ float2 turn_[kWaves][kMaxPairs];
+  __shared__ __attribute__((aligned(16))) float weight_[2][2 * kMaxPairs];  // of queries and keys
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   float2* turn = turn_[wave];
   const int team = lane >> lg, at = lane & ((1 << lg) - 1), teams = 64 >> lg;
-  const bool mine = at * 2 * W < a.D;  // lanes behind the head's end idle
-  const bool turns = at * W < a.pairs; // whole chunks: pairs is a multiple of W
+  const bool mine = at * 2 * W < a.D;   // lanes behind the head's end idle
+  const bool turns = at * W < a.pairs;  // whole chunks: pairs is a multiple of W
   // first dims of the lane's two chunks
   const int d0 = turns && !a.adjacent ? at * W : at * 2 * W, d1 = turns && !a.adjacent ? a.pairs + at * W : d0 + W;
-  const int heads = a.Hq + a.Hk;
-  const int64_t items = a.tokens * slices;
-  float wq[2 * W], wk[2 * W];
+  const int heads = a.Hq + a.Hk, passes = (per + teams - 1) / teams;
+  const int64_t items = a.tokens * slices, first = (int64_t)blockIdx.x * kWaves + wave, stride = (int64_t)gridDim.x * kWaves;
+
+  struct Item {
+    int64_t t;
+    int h0, h_end;
+  };
+  auto item_at = [&](int64_t i) {
+    Item x;
+    x.t = slices > 1 ? i / slices : i;
+    x.h0 = slices > 1 ? (int)(i - x.t * slices) * per : 0;
+    x.h_end = min(heads, x.h0 + per);
+    return x;
+  };
+  Chunk<F32, W> c0[kHold], c1[kHold];
+  // what is read next: item and pass
+  int64_t next = first;
+  int next_pass = 0;
+  Item ahead = item_at(next);
+  auto read = [&](int slot) {
+    if (next >= items) return;
+    const int h = ahead.h0 + next_pass * teams + team;
+    if (h < ahead.h_end && mine) {
+      const uint8_t* p = h < a.Hq ? (const uint8_t*)a.q + (ahead.t * a.q_stride + h * a.D) * EI
+                                  : (const uint8_t*)a.k + (ahead.t * a.k_stride + (h - a.Hq) * a.D) * EI;
+      c0[slot].read(p + d0 * EI);
+      c1[slot].read(p + d1 * EI);
+    }
+    if (++next_pass == passes) {
+      next_pass = 0;
+      next += stride;
+      ahead = item_at(next);
+    }
+  };
 #pragma unroll
-  for (int e = 0; e < 2 * W; e++) {
-    const int d = e < W ? d0 + e : d1 + e - W;
-    wq[e] = mine && a.qw ? a.qw[d] : 1.f;
-    wk[e] = mine && a.kw ? a.kw[d] : 1.f;
+  for (int e = 0; e < kHold; e++) {
+    c0[e] = c1[e] = Chunk<F32, W>{};
+    read(e);
   }
-  for (int64_t item = (int64_t)blockIdx.x * kWaves + wave; item < items; item += (int64_t)gridDim.x * kWaves) {
-    int64_t t = item;
-    int slice = 0;
-    if (slices > 1) {
-      t = item / slices;
-      slice = (int)(item - t * slices);
-    }
-    const int h_end = min(heads, (slice + 1) * per);
-    // the first heads' elements are on their way while the angles are found
-    const uint8_t* q = (const uint8_t*)a.q + t * a.q_stride * EI;
-    const uint8_t* k = (const uint8_t*)a.k + t * a.k_stride * EI;
-    uint8_t* qo = (uint8_t*)a.qo + t * a.qo_stride * EO;
-    uint8_t* ko = (uint8_t*)a.ko + t * a.ko_stride * EO;
-    Chunk<F32, W> c0[kHold], c1[kHold];
-    auto read = [&](int h0) {
+  // a lane's pairs are the same for every token
+  constexpr int kMine = kMaxPairs / 64;
+  double freq[kMine];
+  int64_t row[kMine];  // of positions, -1: not rotated
+  int pos[kMine];      // of the item to come
 #pragma unroll
-      for (int i = 0; i < kHold; i++) {
-        const int h = h0 + i * teams + team;
-        c0[i] = c1[i] = Chunk<F32, W>{};
-        if (h >= h_end || !mine) continue;
-        const uint8_t* p = h < a.Hq ? q + (int64_t)h * a.D * EI : k + (int64_t)(h - a.Hq) * a.D * EI;
-        c0[i].read(p + d0 * EI);
-        c1[i].read(p + d1 * EI);
+  for (int k = 0; k < kMine; k++) {
+    const int i = lane + 64 * k;
+    const int axis = i < a.pairs && a.pair_axis ? a.pair_axis[i] : 0;
+    freq[k] = i < a.pairs ? a.freqs[i] : 0.;
+    row[k] = i < a.pairs && axis >= 0 && axis < a.axes ? axis * a.pos_stride : -1;
+  }
+  auto positions = [&](int64_t i) {
+    const int64_t t = item_at(i).t;
+#pragma unroll
+    for (int k = 0; k < kMine; k++) pos[k] = row[k] >= 0 && i < items ? a.pos[row[k] + t] : 0;
+  };
+  positions(first);
+  for (int d = threadIdx.x; d < a.D; d += 64 * kWaves) {
+    weight_[0][d] = a.qw ? a.qw[d] : 1.f;
+    weight_[1][d] = a.kw ? a.kw[d] : 1.f;
+  }
+  __syncthreads();
+
+  float2 cs[W];
+  int pass = 0;
+  Item now;
+  int64_t item = first;
+  while (item < items) {
+#pragma unroll
+    for (int slot = 0; slot < kHold; slot++) {
+      if (item >= items) break;
+      if (pass == 0) {
+        now = item_at(item);
+#pragma unroll
+        for (int k = 0; k < kMine; k++)
+          if (64 * k < a.pairs) turn[lane + 64 * k] = turn_of(pos[k], freq[k]);
+        positions(item + stride);
+        // the wave's own LDS: its writes are done before its reads
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int e = 0; e < W; e++) cs[e] = turns && mine ? turn[at * W + e] : make_float2(1.f, 0.f);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
       }
-    };
-    int h0 = slice * per;
-    read(h0);
-    for (int i = lane; i < a.pairs; i += 64) {
-      const int axis = a.pair_axis ? a.pair_axis[i] : 0;
-      const int pos = axis >= 0 && axis < a.axes ? a.pos[axis * a.pos_stride + t] : 0;
-      turn[i] = turn_of(pos, a.freqs[i]);
-    }
-    // the wave's own LDS: its writes are done before its reads
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    float2 cs[W];
+      const int h = now.h0 + pass * teams + team;
+      const bool is_q = h < a.Hq;
+      float x[2 * W];
 #pragma unroll
-    for (int e = 0; e < W; e++) cs[e] = turns && mine ? turn[at * W + e] : make_float2(1.f, 0.f);
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    for (;;) {
+      for (int e = 0; e < W; e++) {
+        x[e] = c0[slot][e];
+        x[W + e] = c1[slot][e];
+      }
+      read(slot);
+      float sum = 0.f;
 #pragma unroll
-      for (int i = 0; i < kHold; i++) {
-        const int h = h0 + i * teams + team;
-        if (h0 + i * teams >= h_end) break;
-        const bool is_q = h < a.Hq;
-        float x[2 * W], sum = 0.f;
-#pragma unroll
-        for (int e = 0; e < W; e++) {
-          x[e] = c0[i][e];
-          x[W + e] = c1[i][e];
-        }
+      for (int e = 0; e < 2 * W; e++) sum = fmaf(x[e], x[e], sum);
+      sum = head_sum(mine ? sum : 0.f, lg);
+      if (h < now.h_end && mine) {
         if (is_q ? a.qw != nullptr : a.kw != nullptr) {
-          if (mine) {
+          const float r = inv_root(sum * a.inv_d + a.eps);
+          const float* w = weight_[is_q ? 0 : 1];
 #pragma unroll
-            for (int e = 0; e < 2 * W; e++) sum = fmaf(x[e], x[e], sum);
+          for (int e = 0; e < W; e += 4) {
+            const v4f u = *(const v4f*)(w + d0 + e), v = *(const v4f*)(w + d1 + e);
+#pragma unroll
+            for (int f = 0; f < 4; f++) {
+              x[e + f] = x[e + f] * r * u[f];
+              x[W + e + f] = x[W + e + f] * r * v[f];
+            }
           }
-        }
-        sum = head_sum(sum, lg);
-        if (h >= h_end || !mine) continue;
-        if (is_q ? a.qw != nullptr : a.kw != nullptr) {
-          const float r = 1.0f / sqrtf(sum * a.inv_d + a.eps);
-#pragma unroll
-          for (int e = 0; e < 2 * W; e++) x[e] = x[e] * r * (is_q ? wq[e] : wk[e]);
         }
         float y[2 * W];
 #pragma unroll
@@ -211,13 +260,15 @@ __global__ __launch_bounds__(64 * kWaves) void qk_norm_rope(RopeArgs a, int lg, 
             }
           }
         }
-        uint8_t* p = is_q ? qo + (int64_t)h * a.D * EO : ko + (int64_t)(h - a.Hq) * a.D * EO;
+        uint8_t* p = is_q ? (uint8_t*)a.qo + (now.t * a.qo_stride + h * a.D) * EO
+                          : (uint8_t*)a.ko + (now.t * a.ko_stride + (h - a.Hq) * a.D) * EO;
         write_chunk<OUT32, W>(p + d0 * EO, y);
         write_chunk<OUT32, W>(p + d1 * EO, y + W);
       }
-      h0 += kHold * teams;
-      if (h0 >= h_end) break;
-      read(h0);
+      if (++pass == passes) {
+        pass = 0;
+        item += stride;
+      }
     }
   }
 }

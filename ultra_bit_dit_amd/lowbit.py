@@ -124,9 +124,9 @@ def lib():
         L.lowbit_qk_norm_rope.argtypes = [ctypes.POINTER(Rope), i32, vp, i64, i64, vp, vp, i64, i64, vp, ctypes.c_float, i32,
                                           vp, i64, vp, i64, vp]
         L.lowbit_kv8_fork.argtypes = [kvp, i64, i64, vp, i64, vp, vp, i64, vp, vp, i64, vp, i64, vp, vp, vp, vp]
-        L.lowbit_kv8_fork_workspace.argtypes = [i64, i32, i64, i64, i64, szp]
+        L.lowbit_kv8_fork_workspace.argtypes = [i64, i32, i64, i64, i64, i64, szp]
         L.lowbit_kv8_compact.argtypes = [kvp, i64, i64, vp, i64, vp, vp, vp, vp, vp, vp, vp]
-        L.lowbit_kv8_compact_workspace.argtypes = [i64, szp]
+        L.lowbit_kv8_compact_workspace.argtypes = [i64, i64, szp]
         for name in EXPORTS[2:]:
             getattr(L, name).restype = i32
         _lib = L
@@ -288,7 +288,9 @@ def rotate_act(X, signs, stream=None):
 # packed structs straight to the library.
 
 _torch = None     # set by the first call
+_I32 = _U8 = None  # torch's types
 _FLOAT = {}       # torch type -> lowbit_dtype of the float inputs
+_FLOAT_TYPES = {}  # and back
 _fast = None      # the same exports with address-only prototypes
 _PACK_KV8 = struct.Struct("@qiiiPPPP").pack        # lowbit_kv8
 _PACK_BATCH = struct.Struct("@qPqPPqqqP").pack     # lowbit_kv8_batch
@@ -315,9 +317,11 @@ class _Fast:
 
 
 def _load():
-    global _torch, _fast
+    global _torch, _fast, _I32, _U8
     import torch
+    _I32, _U8 = torch.int32, torch.uint8
     _FLOAT.update({torch.bfloat16: BF16, torch.float32: F32})
+    _FLOAT_TYPES.update({v: k for k, v in _FLOAT.items()})
     _fast = _Fast()
     _torch = torch
     return torch
@@ -595,56 +599,76 @@ def attention_kv8_workspace(cache, page_table, kv_lens, q_heads, total_q, q_star
     return n.value
 
 
-def _rows(T, t, what):
-    """Address and row distance of an int32 [rows][columns] tensor whose rows may be strided."""
-    if t.dtype != T.int32 or t.dim() != 2 or t.shape[0] < 1 or t.shape[1] < 1:
+def _rows(t, what):
+    """Address, rows, columns and row distance of an int32 tensor [rows][columns] whose rows may be strided."""
+    if t.dtype is not _I32 or t.dim() != 2:
         raise ValueError(f"{what}: int32 [rows][pages]")
     rows, cols = t.shape
-    if (cols > 1 and t.stride(1) != 1) or (rows > 1 and t.stride(0) < cols):
-        raise ValueError(f"{what}: a row's entries have to be contiguous")
-    return t.data_ptr(), t.stride(0) if rows > 1 else cols
+    s0, s1 = t.stride()
+    if rows < 1 or cols < 1 or (cols > 1 and s1 != 1) or (rows > 1 and s0 < cols):
+        raise ValueError(f"{what}: rows of contiguous entries")
+    return t.data_ptr(), rows, cols, s0 if rows > 1 else cols
 
 
-def _prefix(T, cache, prefix_table, prefix_lens, page_table, kv_lens, seq_starts, q_starts, total_q, max_q, max_kv,
-            max_prefix, max_seqs, bad_pages):
-    """Checked and packed lowbit_kv8, lowbit_kv8_prefix and lowbit_kv8_batch, and the tensors' device."""
+def _ints(t, shape, what):
+    """Address of a contiguous int32 tensor of a shape."""
+    if t.dtype is not _I32 or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{what}: contiguous int32 {list(shape)}")
+    return t.data_ptr()
+
+
+def _cache(cache):
+    """Packed lowbit_kv8 of a cache, its pages, heads, page size and head size."""
     kc, vc, ks, vs = cache
     n, H, P, D = kc.shape
     if vc.shape != (n, H, D, P) or kc.element_size() != 1 or vc.element_size() != 1:
         raise ValueError("cache: 8-bit codes k [pages][heads][tokens][dim] and v [pages][heads][dim][tokens]")
-    if ks.shape != (n, H) or vs.shape != (n, H) or ks.dtype != T.uint8 or vs.dtype != T.uint8:
+    if ks.shape != (n, H) or vs.shape != (n, H) or ks.dtype is not _U8 or vs.dtype is not _U8:
         raise ValueError("cache: uint8 scales [pages][heads]")
     if not (kc.is_contiguous() and vc.is_contiguous() and ks.is_contiguous() and vs.is_contiguous()):
         raise ValueError("cache: contiguous tensors")
-    pt, stride = _rows(T, page_table, "page_table")
-    qt, qstride = _rows(T, prefix_table, "prefix_table")
-    B, groups = page_table.shape[0], prefix_table.shape[0]
-    ln, pl = _ints(T, kv_lens, (B,), "kv_lens"), _ints(T, prefix_lens, (groups,), "prefix_lens")
+    return _PACK_KV8(n, P, H, D, kc.data_ptr(), vc.data_ptr(), ks.data_ptr(), vs.data_ptr()), n, H, P, D
+
+
+def _new(T, like, shape, dtype, stream):
+    """_empty on the device of `like` (dtype None: and of its type)."""
+    if stream is None:
+        return like.new_empty(shape) if dtype is None or dtype is like.dtype else like.new_empty(shape, dtype=dtype)
+    return _empty(T, shape, dtype or like.dtype, like.device, stream)
+
+
+def _prefix(T, cache, prefix_table, prefix_lens, page_table, kv_lens, seq_starts, q_starts, total_q, max_q, max_kv,
+            max_prefix, max_seqs, bad_pages, *more):
+    """Checked and packed lowbit_kv8, lowbit_kv8_prefix and lowbit_kv8_batch, and the device of the tensors (of `more` too)."""
+    c, _, _, P, _ = _cache(cache)
+    pt, B, width, stride = _rows(page_table, "page_table")
+    qt, groups, qwidth, qstride = _rows(prefix_table, "prefix_table")
+    ln, pl = _ints(kv_lens, (B,), "kv_lens"), _ints(prefix_lens, (groups,), "prefix_lens")
     ss = qs = bad = 0
     if seq_starts is not None:
-        ss = _ints(T, seq_starts, (groups + 1,), "seq_starts")
+        ss = _ints(seq_starts, (groups + 1,), "seq_starts")
     elif B % groups:
         raise ValueError("without seq_starts every group has the same number of sequences")
     if q_starts is not None:
-        qs = _ints(T, q_starts, (B + 1,), "q_starts")
+        qs = _ints(q_starts, (B + 1,), "q_starts")
     elif total_q % B:
         raise ValueError("without q_starts every sequence has the same number of new tokens")
     if max_q is None:
         max_q = total_q // B if q_starts is None else total_q
     if max_kv is None:
-        max_kv = page_table.shape[1] * P
+        max_kv = width * P
     if max_prefix is None:
-        max_prefix = prefix_table.shape[1] * P
-    if max_kv > page_table.shape[1] * P or max_prefix > prefix_table.shape[1] * P:
+        max_prefix = qwidth * P
+    if max_kv > width * P or max_prefix > qwidth * P:
         raise ValueError("max_kv, max_prefix: at most what the tables hold")
     if bad_pages is not None:
-        if bad_pages.dtype != T.int32 or bad_pages.numel() < 1:
+        if bad_pages.dtype is not _I32 or bad_pages.numel() < 1:
             raise ValueError("bad_pages: int32")
         bad = bad_pages.data_ptr()
-    dev = kc.get_device()
-    _device(T, dev, vc, ks, vs, page_table, prefix_table, kv_lens, prefix_lens, seq_starts, q_starts, bad_pages)
-    return (_PACK_KV8(n, P, H, D, kc.data_ptr(), vc.data_ptr(), ks.data_ptr(), vs.data_ptr()),
-            _PACK_PREFIX(groups, qt, qstride, pl, ss, B if max_seqs is None else max_seqs, max_prefix),
+    dev = cache[0].get_device()
+    _device(T, dev, cache[1], cache[2], cache[3], page_table, prefix_table, kv_lens, prefix_lens, seq_starts, q_starts, bad_pages,
+            *more)
+    return (c, _PACK_PREFIX(groups, qt, qstride, pl, ss, B if max_seqs is None else max_seqs, max_prefix),
             _PACK_BATCH(B, pt, stride, ln, qs, total_q, max_q, max_kv, bad), dev)
 
 
@@ -659,27 +683,24 @@ def attention_kv8_prefix(Q, cache, prefix_table, prefix_lens, page_table, kv_len
     sequences; they size the launches and choose the kernels.  Without them: all the tokens (with q_starts), the
     whole tables, all the sequences (with seq_starts)."""
     T = _torch or _load()
-    D = cache[0].shape[3]
-    if Q.dim() != 3 or Q.dtype != T.bfloat16:
+    if Q.dim() != 3 or Q.dtype is not T.bfloat16:
         raise ValueError("Q: bf16 [tokens][q_heads][dim]")
-    tokens, Hq, _ = Q.shape
-    qs = _heads(Q, Hq, D, "Q")
+    tokens, Hq, D = Q.shape
+    qs = _heads(Q, Hq, cache[0].shape[3], "Q")
     c, p, b, dev = _prefix(T, cache, prefix_table, prefix_lens, page_table, kv_lens, seq_starts, q_starts, tokens, max_q, max_kv,
-                           max_prefix, max_seqs, bad_pages)
-    if Q.get_device() != dev:
-        raise ValueError("Q lies on another device than the cache")
+                           max_prefix, max_seqs, bad_pages, Q, O, lse)
     if O is None:
-        O = _empty(T, (tokens, Hq, D), T.bfloat16, Q.device, stream)
+        O = _new(T, Q, (tokens, Hq, D), None, stream)
         os = Hq * D
     else:
-        if O.shape != Q.shape or O.dtype != T.bfloat16 or O.get_device() != dev:
-            raise ValueError("O: bf16 of Q's shape, on its device")
+        if O.shape != Q.shape or O.dtype is not T.bfloat16:
+            raise ValueError("O: bf16 of Q's shape")
         os = _heads(O, Hq, D, "O")
     if lse is None:
         if return_lse:
-            lse = _empty(T, (tokens, Hq), T.float32, Q.device, stream)
-    elif lse.shape != (tokens, Hq) or lse.dtype != T.float32 or not lse.is_contiguous() or lse.get_device() != dev:
-        raise ValueError("lse: contiguous fp32 [tokens][q_heads] on Q's device")
+            lse = _new(T, Q, (tokens, Hq), T.float32, stream)
+    elif lse.shape != (tokens, Hq) or lse.dtype is not T.float32 or not lse.is_contiguous():
+        raise ValueError("lse: contiguous fp32 [tokens][q_heads]")
     rc = _fast.attention_kv8_prefix(c, p, b, Hq, Q.data_ptr(), qs, D ** -0.5 if softmax_scale is None else softmax_scale,
                                     1 if causal else 0, O.data_ptr(), os, None if lse is None else lse.data_ptr(),
                                     _raw_stream(T, dev, stream))
@@ -702,9 +723,7 @@ def attention_kv8_prefix_workspace(cache, prefix_table, prefix_lens, page_table,
 
 
 def _weight(T, w, D, what):
-    if w is None:
-        return None
-    if w.dtype != T.float32 or w.shape != (D,) or not w.is_contiguous():
+    if w.dtype is not T.float32 or w.shape != (D,) or not w.is_contiguous():
         raise ValueError(f"{what}: contiguous fp32 [{D}]")
     return w.data_ptr()
 
@@ -717,25 +736,27 @@ def qk_norm_rope(Q, K, positions, freqs, q_weight=None, k_weight=None, eps=1e-6,
     pair_axis int32 [pairs]; freqs None: no rotation.  y_dtype F32 or BF16 (None: as Q).  Returns (Q_out, K_out);
     Q_out = Q and K_out = K write in place."""
     T = _torch or _load()
-    if Q.dim() != 3 or Q.dtype not in _FLOAT:
+    xt = Q.dtype
+    xd = _FLOAT.get(xt)
+    if Q.dim() != 3 or xd is None:
         raise ValueError("Q: bf16 or fp32 [tokens][q_heads][dim]")
     tokens, Hq, D = Q.shape
-    dev = Q.get_device()
     qs = _heads(Q, Hq, D, "Q")
     Hk = ks = kos = 0
+    kp = ko = pos = fr = pa = qw = kw = None
     if K is not None:
-        if K.dim() != 3 or K.shape[0] != tokens or K.dtype != Q.dtype:
+        if K.dim() != 3 or K.shape[0] != tokens or K.dtype is not xt:
             raise ValueError("K: Q's tokens and type")
-        Hk = K.shape[1]
+        Hk, kp = K.shape[1], K.data_ptr()
         ks = _heads(K, Hk, D, "K")
     elif K_out is not None or k_weight is not None:
         raise ValueError("K_out or k_weight without K")
-    pairs, axes, pos, ps, fr, pa = 0, 1, None, 0, None, None
+    pairs, axes, ps = 0, 1, 0
     if freqs is not None:
-        if freqs.dtype != T.float64 or freqs.dim() != 1 or not freqs.is_contiguous():
+        if freqs.dtype is not T.float64 or freqs.dim() != 1 or not freqs.is_contiguous():
             raise ValueError("freqs: contiguous fp64 [pairs]")
         pairs, fr = freqs.shape[0], freqs.data_ptr()
-        if positions is None or positions.dtype != T.int32 or positions.dim() not in (1, 2) or (
+        if positions is None or positions.dtype is not _I32 or positions.dim() not in (1, 2) or (
                 positions.shape[-1] != tokens or (tokens > 1 and positions.stride(-1) != 1)):
             raise ValueError("positions: int32 [tokens] or [axes][tokens]")
         pos = positions.data_ptr()
@@ -743,75 +764,70 @@ def qk_norm_rope(Q, K, positions, freqs, q_weight=None, k_weight=None, eps=1e-6,
             axes = positions.shape[0]
             ps = positions.stride(0) if axes > 1 else 0
         if pair_axis is not None:
-            if pair_axis.dtype != T.int32 or pair_axis.shape != (pairs,) or not pair_axis.is_contiguous():
-                raise ValueError("pair_axis: contiguous int32 [pairs]")
-            pa = pair_axis.data_ptr()
+            pa = _ints(pair_axis, (pairs,), "pair_axis")
     elif pair_axis is not None:
         raise ValueError("pair_axis without freqs")
-    qw, kw = _weight(T, q_weight, D, "q_weight"), _weight(T, k_weight, D, "k_weight")
-    if y_dtype is None:
-        y_dtype = _FLOAT.get(Q.dtype if Q_out is None else Q_out.dtype)
-    yt = T.float32 if y_dtype == F32 else T.bfloat16 if y_dtype == BF16 else None
-    if yt is None:
-        raise ValueError("y_dtype: F32 or BF16")
-    for name, x, y in (("Q_out", Q, Q_out), ("K_out", K, K_out)):
-        if y is not None and (y.shape != x.shape or y.dtype != yt):
-            raise ValueError(f"{name}: of y_dtype and its input's shape")
+    if q_weight is not None:
+        qw = _weight(T, q_weight, D, "q_weight")
+    if k_weight is not None:
+        kw = _weight(T, k_weight, D, "k_weight")
+    dev = Q.get_device()
     _device(T, dev, K, positions if pairs else None, freqs, pair_axis, q_weight, k_weight, Q_out, K_out)
+    yt = xt if y_dtype is None and Q_out is None else Q_out.dtype if y_dtype is None else _FLOAT_TYPES.get(y_dtype)
+    if yt not in _FLOAT:
+        raise ValueError("y_dtype: F32 or BF16")
     if Q_out is None:
-        Q_out, qos = _empty(T, (tokens, Hq, D), yt, Q.device, stream), Hq * D
+        Q_out, qos = _new(T, Q, (tokens, Hq, D), yt, stream), Hq * D
     else:
+        if Q_out.shape != Q.shape or Q_out.dtype is not yt:
+            raise ValueError("Q_out: of y_dtype and Q's shape")
         qos = _heads(Q_out, Hq, D, "Q_out")
     if K is not None:
         if K_out is None:
-            K_out, kos = _empty(T, (tokens, Hk, D), yt, Q.device, stream), Hk * D
+            K_out, kos = _new(T, Q, (tokens, Hk, D), yt, stream), Hk * D
         else:
+            if K_out.shape != K.shape or K_out.dtype is not yt:
+                raise ValueError("K_out: of y_dtype and K's shape")
             kos = _heads(K_out, Hk, D, "K_out")
+        ko = K_out.data_ptr()
     rc = _fast.qk_norm_rope(_PACK_ROPE(tokens, D, pairs, 1 if adjacent else 0, axes, pos or 0, ps, fr or 0, pa or 0),
-                            _FLOAT[Q.dtype], Q.data_ptr(), Hq, qs, qw, None if K is None else K.data_ptr(), Hk, ks, kw, eps,
-                            y_dtype, Q_out.data_ptr(), qos, None if K is None else K_out.data_ptr(), kos,
+                            xd, Q.data_ptr(), Hq, qs, qw, kp, Hk, ks, kw, eps, _FLOAT[yt], Q_out.data_ptr(), qos, ko, kos,
                             _raw_stream(T, dev, stream))
     if rc:
         raise LowbitError("lowbit_qk_norm_rope", rc)
     return Q_out, K_out
 
 
-def _layers(T, cache):
-    """Packed lowbit_kv8 of a cache, or of a list of them (a model's layers), their number, pages, page size and device."""
-    caches = [cache] if hasattr(cache[0], "data_ptr") else cache
-    out = []
-    n, _, P, _ = caches[0][0].shape
-    dev = caches[0][0].get_device()
-    for kc, vc, ks, vs in caches:
-        m, H, Q, D = kc.shape
-        if vc.shape != (m, H, D, Q) or kc.element_size() != 1 or vc.element_size() != 1:
-            raise ValueError("cache: 8-bit codes k [pages][heads][tokens][dim] and v [pages][heads][dim][tokens]")
-        if ks.shape != (m, H) or vs.shape != (m, H) or ks.dtype != T.uint8 or vs.dtype != T.uint8:
-            raise ValueError("cache: uint8 scales [pages][heads]")
-        if not (kc.is_contiguous() and vc.is_contiguous() and ks.is_contiguous() and vs.is_contiguous()):
-            raise ValueError("cache: contiguous tensors")
-        if m != n or Q != P:
-            raise ValueError("caches: the same pages in every layer")
-        _device(T, dev, kc, vc, ks, vs)
-        out.append(_PACK_KV8(m, Q, H, D, kc.data_ptr(), vc.data_ptr(), ks.data_ptr(), vs.data_ptr()))
-    return b"".join(out), len(out), n, P, dev
+def _layers(T, cache, *more):
+    """Packed lowbit_kv8 of a cache, or of a list of them (a model's layers), their number, pages and device (that of
+    `more` too)."""
+    if hasattr(cache[0], "data_ptr"):
+        c, n, _, _, _ = _cache(cache)
+        dev = cache[0].get_device()
+        _device(T, dev, *cache, *more)
+        return c, 1, n, dev
+    dev = cache[0][0].get_device()
+    out, sizes = [], set()
+    for layer in cache:
+        c, n, _, P, _ = _cache(layer)
+        _device(T, dev, *layer)
+        out.append(c)
+        sizes.add((n, P))
+    if len(sizes) != 1:
+        raise ValueError("caches: the same pages in every layer")
+    _device(T, dev, *more)
+    return b"".join(out), len(out), n, dev
 
 
-def _ints(T, t, shape, what):
-    """Address of a contiguous int32 tensor of a shape."""
-    if t.dtype != T.int32 or tuple(t.shape) != shape or not t.is_contiguous():
-        raise ValueError(f"{what}: contiguous int32 {list(shape)}")
-    return t.data_ptr()
-
-
-def _out_ints(T, out, shapes, names, device, stream):
+def _out_ints(T, out, like, shapes, names, stream):
     if out is None:
-        return tuple(_empty(T, s, T.int32, device, stream) for s in shapes)
+        return tuple([_new(T, like, s, None, stream) for s in shapes])
     out = tuple(out)
     if len(out) != len(shapes):
         raise ValueError(f"out: {', '.join(names)}")
     for t, s, n in zip(out, shapes, names):
-        _ints(T, t, s, n)
+        _ints(t, s, n)
+    _device(T, like.get_device(), *out)
     return out
 
 
@@ -821,22 +837,21 @@ def kv8_fork(cache, page_table, kv_lens, refs, parents, grow=0, width=None, max_
     number, or int32 [new] on the device with max_grow as its bound.  cache may be a list of a model's layers.
     width None: page_table's.  out: the four outputs, which overlap no input."""
     T = _torch or _load()
-    c, n_caches, pages, P, dev = _layers(T, cache)
+    c, n_caches, pages, dev = _layers(T, cache, page_table, kv_lens, refs, parents)
     B, w = page_table.shape
     n = parents.shape[0]
     width = w if width is None else width
+    g = None
     if hasattr(grow, "data_ptr"):
         if max_grow is None:
             raise ValueError("max_grow: a bound of grow")
-        g = _ints(T, grow, (n,), "grow")
+        g = _ints(grow, (n,), "grow")
         _device(T, dev, grow)
     else:
-        g, max_grow = None, grow
-    pt, ln = _ints(T, page_table, (B, w), "page_table"), _ints(T, kv_lens, (B,), "kv_lens")
-    rf, pr = _ints(T, refs, (pages,), "refs"), _ints(T, parents, (n,), "parents")
-    _device(T, dev, page_table, kv_lens, refs, parents)
-    out = _out_ints(T, out, ((n, width), (n,), (pages,), (1,)), ("page_table", "kv_lens", "refs", "failed"), refs.device, stream)
-    _device(T, dev, *out)
+        max_grow = grow
+    pt, ln = _ints(page_table, (B, w), "page_table"), _ints(kv_lens, (B,), "kv_lens")
+    rf, pr = _ints(refs, (pages,), "refs"), _ints(parents, (n,), "parents")
+    out = _out_ints(T, out, refs, ((n, width), (n,), (pages,), (1,)), ("page_table", "kv_lens", "refs", "failed"), stream)
     rc = _fast.kv8_fork(c, n_caches, B, pt, w, ln, rf, n, pr, g, max_grow, out[0].data_ptr(), width, out[1].data_ptr(),
                         out[2].data_ptr(), out[3].data_ptr(), _raw_stream(T, dev, stream))
     if rc:
@@ -844,11 +859,11 @@ def kv8_fork(cache, page_table, kv_lens, refs, parents, grow=0, width=None, max_
     return out
 
 
-def kv8_fork_workspace(n_pages, page_tokens, n_seqs, n_new, max_grow):
+def kv8_fork_workspace(n_pages, page_tokens, n_seqs, n_new, max_grow, n_caches=1):
     """Workspace bytes lowbit_kv8_fork needs for these sizes (reserve before a capture)."""
     b = ctypes.c_size_t()
     _check("lowbit_kv8_fork_workspace",
-           lib().lowbit_kv8_fork_workspace(n_pages, page_tokens, n_seqs, n_new, max_grow, ctypes.byref(b)))
+           lib().lowbit_kv8_fork_workspace(n_pages, page_tokens, n_caches, n_seqs, n_new, max_grow, ctypes.byref(b)))
     return b.value
 
 
@@ -856,13 +871,11 @@ def kv8_compact(cache, page_table, kv_lens, refs, out=None, stream=None):
     """Moves the pages in use to the front of the cache (see lowbit_kv8_compact; a list of caches: a model's layers).
     Returns (page_table, refs, remap [pages], live [1]) as they are then."""
     T = _torch or _load()
-    c, n_caches, pages, P, dev = _layers(T, cache)
+    c, n_caches, pages, dev = _layers(T, cache, page_table, kv_lens, refs)
     B, w = page_table.shape
-    pt, ln = _ints(T, page_table, (B, w), "page_table"), _ints(T, kv_lens, (B,), "kv_lens")
-    rf = _ints(T, refs, (pages,), "refs")
-    _device(T, dev, page_table, kv_lens, refs)
-    out = _out_ints(T, out, ((B, w), (pages,), (pages,), (1,)), ("page_table", "refs", "remap", "live"), refs.device, stream)
-    _device(T, dev, *out)
+    pt, ln = _ints(page_table, (B, w), "page_table"), _ints(kv_lens, (B,), "kv_lens")
+    rf = _ints(refs, (pages,), "refs")
+    out = _out_ints(T, out, refs, ((B, w), (pages,), (pages,), (1,)), ("page_table", "refs", "remap", "live"), stream)
     rc = _fast.kv8_compact(c, n_caches, B, pt, w, ln, rf, out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(),
                            out[3].data_ptr(), _raw_stream(T, dev, stream))
     if rc:
@@ -870,10 +883,10 @@ def kv8_compact(cache, page_table, kv_lens, refs, out=None, stream=None):
     return out
 
 
-def kv8_compact_workspace(n_pages):
-    """Workspace bytes lowbit_kv8_compact needs for a cache of n_pages."""
+def kv8_compact_workspace(n_pages, n_caches=1):
+    """Workspace bytes lowbit_kv8_compact needs for caches of n_pages."""
     b = ctypes.c_size_t()
-    _check("lowbit_kv8_compact_workspace", lib().lowbit_kv8_compact_workspace(n_pages, ctypes.byref(b)))
+    _check("lowbit_kv8_compact_workspace", lib().lowbit_kv8_compact_workspace(n_pages, n_caches, ctypes.byref(b)))
     return b.value
 
 
