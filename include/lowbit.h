@@ -580,7 +580,8 @@ typedef struct lowbit_kv8_prefix {
  * and own tokens are joined in fp32.  Sequences of no group have no
  * prefix.  Rows of a sequence behind its first max_q are not defined, should
  * q_starts have more.  Everything else is as lowbit_attention_kv8 says, limits included, for the
- * groups too (their rows: min(total_q, max_seqs * max_q)); total_q * q_heads * (head_dim + 4) <= 2^38.
+ * groups too (their rows: min(total_q, max_seqs * max_q)); max_len + max_kv <=
+ * 2^30; total_q * q_heads * (head_dim + 4) <= 2^38.
  * Needs workspace in every case (lowbit_attention_kv8_prefix_workspace).
  * Errors: as lowbit_attention_kv8. */
 int lowbit_attention_kv8_prefix(const lowbit_kv8* cache, const lowbit_kv8_prefix* prefix,

@@ -682,14 +682,16 @@ namespace {
 
 // checks of what a call behind shared prefixes has in common with its workspace query
 int prefix_check(const lowbit_kv8* cache, const lowbit_kv8_prefix* p, const lowbit_kv8_batch* batch, int64_t q_heads,
-                 AttnArgs* a, KvArgs* out) {
+                 AttnArgs* a) {
+  KvArgs* const out = &a->prefix;
   if (!p) return LOWBIT_E_NULL;
   const int rc = kv8_check(cache, batch, &a->kv);
   if (rc) return rc;
   if (!p->page_table || !p->lens) return LOWBIT_E_NULL;
   if (p->n_groups < 1 || p->n_groups > (1 << 20) || p->table_width < 1 || p->table_width > (1 << 26))
     return LOWBIT_E_SHAPE;
-  if (p->max_len < 1 || p->max_len > (1 << 30) || p->max_len > p->table_width * cache->page_tokens) return LOWBIT_E_SHAPE;
+  if (p->max_len < 1 || p->max_len > p->table_width * cache->page_tokens) return LOWBIT_E_SHAPE;
+  if (p->max_len > (1 << 30) - batch->max_kv) return LOWBIT_E_SHAPE;  // positions behind the prefix are int
   if (p->seq_starts ? p->max_seqs < 1 || p->max_seqs > batch->n_seqs : batch->n_seqs % p->n_groups != 0)
     return LOWBIT_E_SHAPE;
   if (!aligned(p->page_table, 4) || !aligned(p->lens, 4) || (p->seq_starts && !aligned(p->seq_starts, 4)))
@@ -710,7 +712,7 @@ int prefix_check(const lowbit_kv8* cache, const lowbit_kv8_prefix* p, const lowb
   if (a->kv.total_q * q_heads > (int64_t(1) << 38) / (a->kv.D + 4)) return LOWBIT_E_SHAPE;
   a->Hq = q_heads;
   a->G = q_heads / a->kv.H;
-  return LOWBIT_OK;
+  return attention_prefix_fits(*a) ? LOWBIT_OK : LOWBIT_E_SHAPE;
 }
 
 }  // namespace
@@ -720,10 +722,9 @@ int lowbit_attention_kv8_prefix_workspace(const lowbit_kv8* cache, const lowbit_
   if (!bytes) return LOWBIT_E_NULL;
   *bytes = 0;
   AttnArgs a = {};
-  KvArgs pk = {};
-  const int rc = prefix_check(cache, prefix, batch, q_heads, &a, &pk);
+  const int rc = prefix_check(cache, prefix, batch, q_heads, &a);
   if (rc) return rc;
-  *bytes = attention_prefix_workspace_bytes(a, pk);
+  *bytes = attention_prefix_workspace_bytes(a);
   return LOWBIT_OK;
 }
 
@@ -733,8 +734,7 @@ int lowbit_attention_kv8_prefix(const lowbit_kv8* cache, const lowbit_kv8_prefix
                                 int64_t o_stride, float* lse, void* stream) {
   if (!Q_bf16 || !O_bf16) return LOWBIT_E_NULL;
   AttnArgs a = {};
-  KvArgs pk = {};
-  const int rc = prefix_check(cache, prefix, batch, q_heads, &a, &pk);
+  const int rc = prefix_check(cache, prefix, batch, q_heads, &a);
   if (rc) return rc;
   const int64_t row = q_heads * a.kv.D, most = int64_t(1) << 40;
   if (q_stride < row || o_stride < row || q_stride > most || o_stride > most) return LOWBIT_E_SHAPE;
@@ -750,9 +750,9 @@ int lowbit_attention_kv8_prefix(const lowbit_kv8* cache, const lowbit_kv8_prefix
   a.o_stride = o_stride;
   a.lse = lse;
   void* ws = nullptr;
-  const int r2 = workspace((hipStream_t)stream, attention_prefix_workspace_bytes(a, pk), &ws);
+  const int r2 = workspace((hipStream_t)stream, attention_prefix_workspace_bytes(a), &ws);
   if (r2) return r2;
-  return hip_status(launch_attention_prefix(a, pk, ws, (hipStream_t)stream));
+  return hip_status(launch_attention_prefix(a, ws, (hipStream_t)stream));
 }
 
 // ------------------------------------------- heads of queries and keys; pages

@@ -21,11 +21,16 @@
 // second term would take 2 x 4096 rows, 40 heads over 8, D = 128, from 383 to 497 us
 // and attn_prompt32<64> out of its registers (221 -> 511 us).
 //
-// MODE.  kPlain: a call's rows see one sequence each.  Behind a prefix shared by
-// a group of sequences a call runs in two: kPrefix, where the "sequences" are the
-// groups (the rows of their sequences lie in order) and results go to the
-// workspace as sums; kOwn, each sequence's own tokens, whose results go out as
-// those of kPlain and to the workspace too.  attn_merge adds the two.
+// MODE.  kPlain: a call's rows see the tokens of one sequence each.  The others are
+// of calls behind prefixes that groups of sequences share:
+//   kBehind  a row's tokens are its prefix's and then its own, from two tables; the
+//            steps of the prefix come first, and its last one may be partly filled.
+//            For sequences of many rows, which fill tiles by themselves.
+//   kMixed   tiles of the groups' rows (those of their sequences lie in order) see
+//            the prefixes, tiles of the sequences' rows their own tokens, in one launch;
+//            attn_merge adds the two.  For few rows of each sequence.
+//   kUnion   the same for few rows in all: the sequences and behind them the groups are
+//            one list of items for attn_decode.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -36,7 +41,23 @@
 namespace lowbit {
 namespace {
 
-enum Mode { kPlain, kOwn, kPrefix };
+enum Mode { kPlain, kBehind, kMixed, kUnion };
+
+// x or y (field by field: a chosen address would put both into private memory)
+__device__ __forceinline__ KvArgs either(bool first, const KvArgs& x, const KvArgs& y) {
+  KvArgs r = y;
+  r.n_seqs = first ? x.n_seqs : y.n_seqs;
+  r.table = first ? x.table : y.table;
+  r.width = first ? x.width : y.width;
+  r.lens = first ? x.lens : y.lens;
+  r.max_q = first ? x.max_q : y.max_q;
+  r.max_kv = first ? x.max_kv : y.max_kv;
+  r.members = first ? x.members : y.members;
+  r.member_count = first ? x.member_count : y.member_count;
+  r.n_members = first ? x.n_members : y.n_members;
+  r.member_q = first ? x.member_q : y.member_q;
+  return r;
+}
 
 constexpr int kUnit = 64;  // tokens of one step of a wave
 constexpr float kLn2 = 0.6931471805599453f;
@@ -211,6 +232,12 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 15, g = lane >> 4;
   const int P = 1 << a.kv.lp;
+  // items: sequences, and behind them groups
+  const int64_t n_items = MODE == kUnion ? a.kv.n_seqs + a.prefix.n_seqs : a.kv.n_seqs;
+  auto span_of = [&](int64_t i) -> SeqSpan {
+    if (MODE == kUnion && i >= a.kv.n_seqs) return seq_span<true>(a.prefix, i - a.kv.n_seqs);
+    return seq_span(a.kv, i);
+  };
   // blocks of one tile of a sequence (at least one, which writes its rows), and its tiles
   auto blocks_of = [&](const SeqSpan& t) -> int64_t {
     int64_t most = t.len;
@@ -219,10 +246,10 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
   };
   auto tiles_of = [&](const SeqSpan& t) -> int64_t { return (t.n * a.G + 16 * NC - 1) / (16 * NC); };
   auto work_of = [&](int64_t i) -> int64_t {
-    const SeqSpan t = seq_span<MODE == kPrefix>(a.kv, i);
+    const SeqSpan t = span_of(i);
     return tiles_of(t) * blocks_of(t);
   };
-  ItemScan<64 * kDecWaves, decltype(work_of)> scan(a.kv.n_seqs, work_of, scan_);
+  ItemScan<64 * kDecWaves, decltype(work_of)> scan(n_items, work_of, scan_);
   const int64_t per_head = scan.total, total = per_head * a.kv.H;
   // Shares: one for each block while there are workgroups for that, so that none
   // has parts of two tiles, which it would have to begin and join in turn
@@ -237,7 +264,7 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
   int h = (int)quot(x, per_head);
   int64_t b, item;
   scan.find(x - h * per_head, &b, &item);
-  SeqSpan s = seq_span<MODE == kPrefix>(a.kv, b);
+  SeqSpan s = span_of(b);
   int64_t blocks = blocks_of(s), tiles = tiles_of(s);
   int64_t rt = quot(item, blocks);
   int at = (int)(item - rt * blocks);  // first block of this share in the tile
@@ -251,6 +278,8 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
     const int64_t R = (int64_t)s.n * a.G;
     const int64_t rho0 = rt * 16 * NC;
     const int len = s.len, first = len - s.n;  // position of the first new token
+    const bool group = MODE == kUnion && b >= a.kv.n_seqs;
+    const bool causal = a.causal && !group;
 
     // visible tokens of this lane's rows: [vlo, vhi)
     int vlo[NC], vhi[NC];
@@ -258,8 +287,8 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
     {
       const int64_t rlast = rho0 + 16 * NC - 1 < R ? rho0 + 16 * NC - 1 : R - 1;
       const int p0 = first + (int)(rho0 / a.G), p1 = first + (int)(rlast / a.G);
-      hi_max = a.causal ? min(len, p1 + 1) : len;
-      hi_min = a.causal ? min(len, p0 + 1) : len;
+      hi_max = causal ? min(len, p1 + 1) : len;
+      hi_min = causal ? min(len, p0 + 1) : len;
       hi_max = max(hi_max, 0);
       hi_min = max(hi_min, 0);
       if (a.window > 0) {
@@ -273,7 +302,7 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
       rho[c] = rho0 + 16 * c + n;
       const int64_t rc = rho[c] < R ? rho[c] : R - 1;
       const int p = first + (int)(rc / a.G);
-      vhi[c] = a.causal ? min(len, p + 1) : len;
+      vhi[c] = causal ? min(len, p + 1) : len;
       vlo[c] = a.window > 0 ? max(0, p - a.window + 1) : 0;
     }
     const int u0 = lo_min / kUnit + kDecWaves * at, u1 = min(u0 + kDecWaves * count, (hi_max + kUnit - 1) / kUnit);
@@ -301,7 +330,7 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
       for (int d = 0; d < DT; d++) o[c][d] = v4f{0.f, 0.f, 0.f, 0.f};
     }
 
-    const int32_t* table = a.kv.table + b * a.kv.width;
+    const int32_t* table = group ? a.prefix.table + (b - a.kv.n_seqs) * a.prefix.width : a.kv.table + b * a.kv.width;
     const int64_t page_bytes = ((int64_t)D << a.kv.lp);
     // Entry of the 16 tokens from t on, and the page it names: -1 where there are
     // none, -2 where it is unusable.  (Looked at when the page is needed: looked at
@@ -533,13 +562,13 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
           if (rho[c] >= R) continue;
           const float inv = lt[c] > 0.f || lt[c] != lt[c] ? 1.0f / lt[c] : 0.f;
           const int64_t tok = s.row0 + rho[c] / a.G, hd = h * a.G + rho[c] % a.G;
-          if constexpr (MODE != kPlain) {
-            float* sums = a.sums + (tok * a.Hq + hd) * (D + kPartPad);
+          if constexpr (MODE == kUnion) {
+            float* sums = (group ? a.prefix_sums : a.sums) + (tok * a.Hq + hd) * (D + kPartPad);
 #pragma unroll
             for (int d = 0; d < DT; d++) *(v4f*)(sums + 16 * d + 4 * g) = o[c][d];
             if (g == 0) *(float2*)(sums + D) = make_float2(mt[c], lt[c]);
           }
-          if constexpr (MODE == kPrefix) continue;
+          if (group) continue;
           uint16_t* op = a.o + tok * a.o_stride + hd * D + 4 * g;
 #pragma unroll
           for (int d = 0; d < DT; d++) {
@@ -637,12 +666,12 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
       auto finish = [&](int r, int d, float px, float py) {
         const float L = jl[r], inv = L > 0.f || L != L ? 1.0f / L : 0.f;
         const int64_t rr = rho0 + r, tok = s.row0 + rr / a.G, hd = h * a.G + rr % a.G;
-        if constexpr (MODE != kPlain) {
-          float* sums = a.sums + (tok * a.Hq + hd) * (D + kPartPad);
+        if constexpr (MODE == kUnion) {
+          float* sums = (group ? a.prefix_sums : a.sums) + (tok * a.Hq + hd) * (D + kPartPad);
           *(float2*)(sums + d) = make_float2(px, py);
           if (d == 0) *(float2*)(sums + D) = make_float2(jm[r], L);
         }
-        if constexpr (MODE == kPrefix) return;
+        if (group) return;
         *(uint32_t*)(a.o + tok * a.o_stride + hd * D + d) = bf16_bits(px * inv) | (bf16_bits(py * inv) << 16);
         if (a.lse && d == 0) a.lse[tok * a.Hq + hd] = L == 0.f ? -INFINITY : (jm[r] + __builtin_amdgcn_logf(L)) * kLn2;
       };
@@ -676,11 +705,11 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
     if (++rt == tiles) {
       rt = 0;
       do {
-        if (++b == a.kv.n_seqs) {
+        if (++b == n_items) {
           b = 0;
           h++;
         }
-        s = seq_span<MODE == kPrefix>(a.kv, b);
+        s = span_of(b);
         tiles = tiles_of(s);
       } while (tiles == 0);  // some sequence has tiles, as x < total
       blocks = blocks_of(s);
@@ -716,6 +745,42 @@ struct Seen {
   int lo, hi, lo_all, hi_all;
 };
 
+// A workgroup's place in a prompt launch.
+struct Place {
+  bool group;      // its tile is of a group's rows (kMixed)
+  int tile_at, h;  // tile of a head, and that
+  int part, most;  // of the tile's steps, and as how many parts the launch has
+  uint32_t slot;   // of its results in a.part
+};
+// heads run fastest, so that an XCD (bid % 8) keeps few of them in its L2
+template <int MODE>
+__device__ __forceinline__ Place place_of(AttnArgs& a) {
+  Place p;
+  uint32_t bid = blockIdx.x;
+  p.group = MODE == kMixed && bid < a.prefix_wgs;
+  if (MODE == kMixed) {
+    if (!p.group) bid -= a.prefix_wgs;
+    a.kv = either(p.group, a.prefix, a.kv);
+    a.causal = p.group ? 0 : a.causal;
+    a.parts = p.group ? a.parts : 1;
+  }
+  const uint32_t H = (uint32_t)a.kv.H, at = bid / H, parts = (uint32_t)a.parts;
+  p.h = (int)(bid - at * H);
+  p.slot = bid;
+  p.most = a.parts;
+  if (MODE == kBehind && (int)at < a.whole) {
+    p.tile_at = (int)at;
+    p.part = 0;
+    p.most = 1;
+  } else {
+    const uint32_t whole = MODE == kBehind ? (uint32_t)a.whole : 0u, cut = at - whole;
+    p.tile_at = (int)(whole + cut / parts);
+    p.part = (int)(cut % parts);
+    p.slot = bid - whole * H;
+  }
+  return p;
+}
+
 // A tile of ROWS rows of one sequence and key head.
 template <int ROWS, int MODE>
 struct PromptTile {
@@ -726,40 +791,81 @@ struct PromptTile {
   Seen seen;     // by the tile
   int u0, u1;    // steps of 64 tokens that some row sees
   int parts;     // they are cut into
+  // kBehind: tokens and steps of the prefix, its row of the table.  Own token t stands at kUnit * head_steps + t.
+  int head, head_steps;
+  const int32_t* head_table;
 
-  // tile number `at` of a head, all sequences in turn; false behind the last
+  // tile number `at` of a head, all sequences in turn, in at most `most` parts; false behind the last
   template <int THREADS>
-  __device__ __forceinline__ bool find(const AttnArgs& a, uint32_t at, int64_t* mem) {
-    auto tiles = [&](int64_t i) -> int64_t { return (seq_span<MODE == kPrefix>(a.kv, i).n * a.G + ROWS - 1) / ROWS; };
+  __device__ __forceinline__ bool find(const AttnArgs& a, uint32_t at, int most, int64_t* mem) {
+    auto tiles = [&](int64_t i) -> int64_t { return (seq_span<MODE == kMixed>(a.kv, i).n * a.G + ROWS - 1) / ROWS; };
     ItemScan<THREADS, decltype(tiles)> scan(a.kv.n_seqs, tiles, mem);
     if (at >= scan.total) return false;
     int64_t item;
     scan.find(at, &b, &item);
-    s = seq_span<MODE == kPrefix>(a.kv, b);
+    s = seq_span<MODE == kMixed>(a.kv, b);
+    head = head_steps = 0;
+    if constexpr (MODE == kBehind) {
+      // the group that has sequence b: every thread looks at some of them
+      int64_t g = a.prefix.members ? -1 : b / a.prefix.member_count;
+      if (a.prefix.members) {
+        __syncthreads();
+        if (threadIdx.x == 0) mem[0] = -1;
+        __syncthreads();
+        for (int64_t i = threadIdx.x; i < a.prefix.n_seqs; i += THREADS)
+          if (a.prefix.members[i] <= b && b < a.prefix.members[i + 1]) mem[0] = i;
+        __syncthreads();
+        g = uniform64(mem[0]);
+      }
+      if (g >= 0) {
+        const int64_t n = a.prefix.lens[g];
+        head = (int)(n < 0 ? 0 : n < a.prefix.max_kv ? n : a.prefix.max_kv);
+        head_steps = (head + kUnit - 1) / kUnit;
+        head_table = a.prefix.table + g * a.prefix.width;
+      }
+    }
     R = s.n * (int)a.G;
     wg0 = (R - 1) / ROWS * ROWS - (int)item * ROWS;  // the last, longest tiles of a sequence first
+    s.len += head_steps * kUnit;
     first = s.len - s.n;
     seen = of_rows(a, wg0, wg0 + ROWS);
     u0 = seen.lo / kUnit;
     u1 = (seen.hi + kUnit - 1) / kUnit;
-    parts = parts_of(u1 - u0, a.parts);
+    parts = parts_of(u1 - u0, most);
     return true;
+  }
+  // tokens before this one are visible to a row at position p
+  __device__ __forceinline__ int sees_to(const AttnArgs& a, int p) const {
+    return a.causal ? max(head_steps * kUnit, min(s.len, p + 1)) : s.len;
   }
   __device__ __forceinline__ Seen of_rows(const AttnArgs& a, int r0, int r1) const {
     r0 = r0 < R - 1 ? r0 : R - 1;
     r1 = r1 < R ? r1 : R;
     const int p0 = first + (int)((uint32_t)r0 / (uint32_t)a.G), p1 = first + (int)((uint32_t)(r1 - 1) / (uint32_t)a.G);
     Seen v;
-    v.hi = a.causal ? max(0, min(s.len, p1 + 1)) : s.len;
-    v.hi_all = a.causal ? max(0, min(s.len, p0 + 1)) : s.len;
+    v.hi = sees_to(a, p1);
+    v.hi_all = sees_to(a, p0);
     v.lo = a.window > 0 ? max(0, p0 - a.window + 1) : 0;
     v.lo_all = a.window > 0 ? max(0, p1 - a.window + 1) : 0;
     return v;
   }
+  // Step u: the end of its tokens (of the tile's `hi`), the row of the table that has
+  // them, the position of that row's first token.
+  __device__ __forceinline__ int end(int u, int hi) const { return MODE == kBehind && u < head_steps ? head : hi; }
+  __device__ __forceinline__ const int32_t* row(int u, const int32_t* own) const {
+    return MODE == kBehind && u < head_steps ? head_table : own;
+  }
+  __device__ __forceinline__ int origin(int u) const {
+    return MODE == kBehind && u >= head_steps ? head_steps * kUnit : 0;
+  }
+  // some of its tokens are none (kBehind: the end of the prefix)
+  __device__ __forceinline__ bool short_step(int u) const {
+    return MODE == kBehind && u == head_steps - 1 && head < head_steps * kUnit;
+  }
 };
 
 template <int D, int NC, int WAVES, int MODE>
-__global__ __launch_bounds__(64 * WAVES, 2) void attn_prompt(AttnArgs a) {
+__global__ __launch_bounds__(64 * WAVES, 2) void attn_prompt(AttnArgs args) {
   constexpr int DS = D / 32, DT = D / 16, HALF = 32 * WAVES, SP = 4 * D / HALF;
   static_assert(SP * HALF == 4 * D, "whole 16-byte pieces per thread");
   __shared__ __attribute__((aligned(16))) uint8_t k_[2][4 * DS * 1024], v_[2][DT * 2048];
@@ -767,13 +873,14 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attn_prompt(AttnArgs a) {
   const bool keys = __builtin_amdgcn_readfirstlane((int)threadIdx.x) < HALF;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n = lane & 15, g = lane >> 4;
-  // heads run fastest, so that an XCD (bid % 8) keeps few of them in its L2
   constexpr int ROWS = 16 * NC * WAVES;
-  const uint32_t G = (uint32_t)a.G, H = (uint32_t)a.kv.H, at_part = blockIdx.x / H, tile_at = at_part / (uint32_t)a.parts;
-  const int h = (int)(blockIdx.x - at_part * H), part = (int)(at_part - tile_at * a.parts);
+  AttnArgs a = args;
+  const Place at_ = place_of<MODE>(a);
+  const uint32_t G = (uint32_t)a.G;
+  const int h = at_.h, part = at_.part;
   __shared__ int64_t scan_[WAVES + 2];
   PromptTile<ROWS, MODE> t;
-  if (!t.template find<64 * WAVES>(a, tile_at, scan_) || part >= t.parts) return;
+  if (!t.template find<64 * WAVES>(a, at_.tile_at, at_.most, scan_) || part >= t.parts) return;
   const SeqSpan s = t.s;
   const int R = t.R, wg0 = t.wg0, len = s.len, first = t.first, P = 1 << a.kv.lp, rho0 = wg0 + wave * 16 * NC;
   const int lo_min = t.seen.lo, hi_max = t.seen.hi, lo_all = t.seen.lo_all, hi_all = t.seen.hi_all;
@@ -788,7 +895,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attn_prompt(AttnArgs a) {
     rho[c] = rho0 + 16 * c + n;
     const uint32_t rc = rho[c] < R ? rho[c] : R - 1, at = rc / G;
     const int p = first + (int)at;
-    vhi[c] = a.causal ? min(len, p + 1) : len;
+    vhi[c] = MODE == kBehind ? t.sees_to(a, p) : a.causal ? min(len, p + 1) : len;
     vlo[c] = a.window > 0 ? max(0, p - a.window + 1) : 0;
     const uint16_t* qp = a.q + (s.row0 + at) * a.q_stride + ((int64_t)h * G + (rc - at * G)) * D + 16 * g;
 #pragma unroll
@@ -822,9 +929,11 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attn_prompt(AttnArgs a) {
   const int stage_group = keys ? (lane >> 2) & 3 : g;
   // their table entry, and the page it names: -1 where there are none, -2 where it
   // is unusable (looked at a step later: looked at when read, it would be waited for)
-  auto entry_at = [&](int u) -> int { return table[min(u * kUnit + 16 * stage_group, hi_max - 1) >> a.kv.lp]; };
+  auto entry_at = [&](int u) -> int {
+    return t.row(u, table)[(min(u * kUnit + 16 * stage_group, t.end(u, hi_max) - 1) - t.origin(u)) >> a.kv.lp];
+  };
   auto page_of = [&](int u, int entry) -> int {
-    return u * kUnit + 16 * stage_group >= hi_max ? -1 : entry >= 0 && entry < (int)a.kv.n_pages ? entry : -2;
+    return u * kUnit + 16 * stage_group >= t.end(u, hi_max) ? -1 : entry >= 0 && entry < (int)a.kv.n_pages ? entry : -2;
   };
   // This thread's 16-byte pieces of a step: of the keys for the first half of
   // the waves (wave t: the rows of tile t, piece i: dims 64 i + 16 g ..), of the
@@ -839,7 +948,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attn_prompt(AttnArgs a) {
   const uint32_t kat = (uint32_t)((tok & (P - 1)) * D + 16 * g);
   const uint32_t vat = (uint32_t)((16 * w4 + n) * P + ((16 * g) & (P - 1)));
   auto fetch = [&](int u, int pg) {
-    const uint32_t in = (u * kUnit) & (P - 1);  // the step's place in a larger page
+    const uint32_t in = (u * kUnit - t.origin(u)) & (P - 1);  // the step's place in a larger page
     const int64_t ph = (int64_t)(pg < 0 ? 0 : pg) * a.kv.H + h;
     if (keys) {
       const uint8_t* kp = a.kv.kc + (ph << sh) + (kat + in * D);
@@ -854,7 +963,9 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attn_prompt(AttnArgs a) {
     }
   };
   // tokens some row of the workgroup does not see, or that cannot be read
-  auto partial = [&](int u, int pg) { return u * kUnit + kUnit > hi_all || u * kUnit < lo_all || __any(pg < 0); };
+  auto partial = [&](int u, int pg) {
+    return u * kUnit + kUnit > hi_all || u * kUnit < lo_all || t.short_step(u) || __any(pg < 0);
+  };
   // widened and written to the step's buffer
   auto stage = [&](int u, int pg) {
     if (keys) {
@@ -871,7 +982,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attn_prompt(AttnArgs a) {
       if (part) {
         // codes of tokens no row sees become 0; NaN codes too, and are put
         // back beside the products for the rows that see them
-        const int T = u * kUnit + 16 * g, lo = pg < 0 ? 16 : lo_min - T, hi = hi_max - T;
+        const int T = u * kUnit + 16 * g, lo = pg < 0 ? 16 : lo_min - T, hi = t.end(u, hi_max) - T;
         uint32_t nans = 0;
 #pragma unroll
         for (int e = 0; e < 4; e++) {
@@ -933,7 +1044,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attn_prompt(AttnArgs a) {
     if (nan_at_[u & 3] == u) {
       // rare: a NaN code among tokens that not every row of the workgroup sees
       const int T = u * kUnit, vp = __shfl(page_of(u, entry_at(u)), keys ? 4 * g : lane);
-      const uint8_t* vc = a.kv.vc + (((int64_t)(vp < 0 ? 0 : vp) * a.kv.H + h) << sh) + ((T + 16 * g) & (P - 1));
+      const uint8_t* vc = a.kv.vc + (((int64_t)(vp < 0 ? 0 : vp) * a.kv.H + h) << sh) + ((T + 16 * g - t.origin(u)) & (P - 1));
 #pragma unroll 1
       for (int d = 0; d < DT; d++) {
         const mx_u4 w = *(const mx_u4*)(vc + (int64_t)(16 * d + n) * P);
@@ -947,7 +1058,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attn_prompt(AttnArgs a) {
 #pragma unroll
           for (int e = 0; e < 16; e++) {
             const int tok = T + 16 * g + e;
-            vis[e >> 3][e & 7] = (__bf16)(tok >= vlo[c] && tok < vhi[c] ? 1.f : 0.f);
+            vis[e >> 3][e & 7] = (__bf16)(tok >= vlo[c] && tok < t.end(u, vhi[c]) ? 1.f : 0.f);
           }
           v4f hit = v4f{0.f, 0.f, 0.f, 0.f};
           hit = mfma(isn[0], vis[0], hit);
@@ -979,12 +1090,12 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attn_prompt(AttnArgs a) {
   // weights of step u from its scores
   auto softmax = [&](int u, int pg) {
     const int T = u * kUnit;
-    const bool mask = T + kUnit > whi_all || T < wlo_all || __any(pg < 0);
+    const bool mask = T + kUnit > whi_all || T < wlo_all || t.short_step(u) || __any(pg < 0);
     const int page = mask ? __shfl(pg, keys ? 4 * g : lane) : 0;  // of the lane's 16 tokens
 #pragma unroll
     for (int c = 0; c < NC; c++) {
       if (mask) {
-        const int lo = page < 0 ? 16 : vlo[c] - (T + 16 * g), hi = vhi[c] - (T + 16 * g);
+        const int lo = page < 0 ? 16 : vlo[c] - (T + 16 * g), hi = t.end(u, vhi[c]) - (T + 16 * g);
         const uint32_t up = hi >= 16 ? 0xFFFFu : hi <= 0 ? 0u : (1u << hi) - 1u;
         const uint32_t seen = lo >= 16 ? 0u : lo <= 0 ? up : up & ~((1u << lo) - 1u);
 #pragma unroll
@@ -1057,8 +1168,8 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attn_prompt(AttnArgs a) {
 #pragma unroll
       for (int e = 0; e < 4; e++)
         if ((nanned[c] >> (4 * d + e)) & 1) o[c][d][e] = __uint_as_float(0x7FC00000u);
-    if (MODE == kPrefix || parts > 1) {
-      float* pp = a.part + ((int64_t)blockIdx.x * ROWS + (rho[c] - wg0)) * (D + kPartPad);
+    if (at_.group || parts > 1) {
+      float* pp = a.part + ((int64_t)at_.slot * ROWS + (rho[c] - wg0)) * (D + kPartPad);
 #pragma unroll
       for (int d = 0; d < DT; d++) *(v4f*)(pp + 16 * d + 4 * g) = o[c][d];
       if (g == 0) *(float2*)(pp + D) = make_float2(m[c], l[c]);
@@ -1067,7 +1178,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attn_prompt(AttnArgs a) {
     const float inv = l[c] > 0.f || l[c] != l[c] ? 1.0f / l[c] : 0.f;
     const uint32_t tok = (uint32_t)rho[c] / G;
     const int64_t row = s.row0 + tok, hd = (int64_t)h * G + (rho[c] - tok * G);
-    if constexpr (MODE == kOwn) {
+    if constexpr (MODE == kMixed) {
       float* sums = a.sums + (row * a.Hq + hd) * (D + kPartPad);
 #pragma unroll
       for (int d = 0; d < DT; d++) *(v4f*)(sums + 16 * d + 4 * g) = o[c][d];
@@ -1101,7 +1212,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attn_prompt(AttnArgs a) {
 // four cycles each and the exponentials' quarter rate some 17% more (2 x 4096 in
 // 4096, 32 heads over 8: 226 us).  One register is spilled.
 template <int D, int NC, int WAVES, int OCC, int MODE>
-__global__ __launch_bounds__(64 * WAVES, OCC) void attn_prompt32(AttnArgs a) {
+__global__ __launch_bounds__(64 * WAVES, OCC) void attn_prompt32(AttnArgs args) {
   constexpr int DS = D / 16, DT = D / 32, HALF = 32 * WAVES, SP = 4 * D / HALF, PS = WAVES / 4;
   static_assert(SP * HALF == 4 * D, "whole 16-byte pieces per thread");
   constexpr int KB = 2 * DS * 1024, VB = 4 * DT * 1024;  // bytes of a step's operands
@@ -1113,15 +1224,17 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void attn_prompt32(AttnArgs a) {
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n = lane & 31, hf = lane >> 5;
   constexpr int ROWS = 32 * NC * WAVES;
-  const uint32_t G = (uint32_t)a.G, H = (uint32_t)a.kv.H, at_part = blockIdx.x / H, tile_at = at_part / (uint32_t)a.parts;
-  const int h = (int)(blockIdx.x - at_part * H), part = (int)(at_part - tile_at * a.parts);
+  AttnArgs a = args;
+  const Place at_ = place_of<MODE>(a);
+  const uint32_t G = (uint32_t)a.G;
+  const int h = at_.h, part = at_.part;
   __shared__ int64_t scan_[WAVES + 2];
-  PromptTile<ROWS, MODE> t;
-  if (!t.template find<64 * WAVES>(a, tile_at, scan_) || part >= t.parts) return;
-  const SeqSpan s = t.s;
-  const int R = t.R, wg0 = t.wg0, len = s.len, first = t.first, P = 1 << a.kv.lp, rho0 = wg0 + wave * 32 * NC;
-  const int lo_min = t.seen.lo, hi_max = t.seen.hi, lo_all = t.seen.lo_all, hi_all = t.seen.hi_all;
-  const Seen mine = t.of_rows(a, rho0, rho0 + 32 * NC);  // by this wave's rows
+  PromptTile<ROWS, MODE> te;
+  if (!te.template find<64 * WAVES>(a, at_.tile_at, at_.most, scan_) || part >= te.parts) return;
+  const SeqSpan s = te.s;
+  const int R = te.R, wg0 = te.wg0, len = s.len, first = te.first, P = 1 << a.kv.lp, rho0 = wg0 + wave * 32 * NC;
+  const int lo_min = te.seen.lo, hi_max = te.seen.hi, lo_all = te.seen.lo_all, hi_all = te.seen.hi_all;
+  const Seen mine = te.of_rows(a, rho0, rho0 + 32 * NC);  // by this wave's rows
   const int wlo = mine.lo, wlo_all = mine.lo_all, whi_all = mine.hi_all;
   const int whi = __builtin_amdgcn_readfirstlane(rho0 < R ? mine.hi : 0);
   const bool none = a.scale2 == 0.f;  // all scores 0, or NaN
@@ -1132,7 +1245,7 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void attn_prompt32(AttnArgs a) {
     rho[c] = rho0 + 32 * c + n;
     const uint32_t rc = rho[c] < R ? rho[c] : R - 1, at = rc / G;
     const int p = first + (int)at;
-    vhi[c] = a.causal ? min(len, p + 1) : len;
+    vhi[c] = MODE == kBehind ? te.sees_to(a, p) : a.causal ? min(len, p + 1) : len;
     vlo[c] = a.window > 0 ? max(0, p - a.window + 1) : 0;
     const uint16_t* qp = a.q + (s.row0 + at) * a.q_stride + ((int64_t)h * G + (rc - at * G)) * D + 8 * hf;
 #pragma unroll
@@ -1153,10 +1266,10 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void attn_prompt32(AttnArgs a) {
       for (int e = 0; e < 16; e++) o[c][d][e] = 0.f;
   }
 
-  const int parts = t.parts;
-  int u0 = t.u0, u1 = t.u1;
+  const int parts = te.parts;
+  int u0 = te.u0, u1 = te.u1;
   part_steps(part, parts, &u0, &u1);
-  const int32_t* table = a.kv.table + t.b * a.kv.width;
+  const int32_t* table = a.kv.table + te.b * a.kv.width;
   // This thread's 16-byte pieces of a step.  Keys (first half of the waves,
   // tile w4 % 2): 16 dims 16 (2 (w4 / 2 + 2 i) + h) .. of the token of row n.
   // Values (second half): 16 tokens of dim 32 (w4 / 2 + 2 i) + n, tokens
@@ -1166,9 +1279,11 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void attn_prompt32(AttnArgs a) {
   const int stage_group = 2 * tile + (keys ? (lane >> 2) & 1 : hf);  // of 16 tokens
   // their table entry, and the page it names: -1 where there are none, -2 where it
   // is unusable (looked at a step later: looked at when read, it would be waited for)
-  auto entry_at = [&](int u) -> int { return table[min(u * kUnit + 16 * stage_group, hi_max - 1) >> a.kv.lp]; };
+  auto entry_at = [&](int u) -> int {
+    return te.row(u, table)[(min(u * kUnit + 16 * stage_group, te.end(u, hi_max) - 1) - te.origin(u)) >> a.kv.lp];
+  };
   auto page_of = [&](int u, int entry) -> int {
-    return u * kUnit + 16 * stage_group >= hi_max ? -1 : entry >= 0 && entry < (int)a.kv.n_pages ? entry : -2;
+    return u * kUnit + 16 * stage_group >= te.end(u, hi_max) ? -1 : entry >= 0 && entry < (int)a.kv.n_pages ? entry : -2;
   };
   mx_u4 raw[SP];
   uint32_t eb = 0;
@@ -1177,7 +1292,7 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void attn_prompt32(AttnArgs a) {
   const uint32_t kat = (uint32_t)((tok & (P - 1)) * D + 32 * (w4 >> 1) + 16 * hf);
   const uint32_t vat = (uint32_t)((32 * (w4 >> 1) + n) * P + ((16 * stage_group) & (P - 1)));
   auto fetch = [&](int u, int pg) {
-    const uint32_t in = (u * kUnit) & (P - 1);  // the step's place in a larger page
+    const uint32_t in = (u * kUnit - te.origin(u)) & (P - 1);  // the step's place in a larger page
     const int64_t ph = (int64_t)(pg < 0 ? 0 : pg) * a.kv.H + h;
     if (keys) {
       const uint8_t* kp = a.kv.kc + (ph << sh) + (kat + in * D);
@@ -1192,7 +1307,9 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void attn_prompt32(AttnArgs a) {
     }
   };
   // tokens some row of the workgroup does not see, or that cannot be read
-  auto partial = [&](int u, int pg) { return u * kUnit + kUnit > hi_all || u * kUnit < lo_all || __any(pg < 0); };
+  auto partial = [&](int u, int pg) {
+    return u * kUnit + kUnit > hi_all || u * kUnit < lo_all || te.short_step(u) || __any(pg < 0);
+  };
   // widened and written to the step's buffer
   auto stage = [&](int u, int pg) {
     if (keys) {
@@ -1210,7 +1327,7 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void attn_prompt32(AttnArgs a) {
       if (part) {
         // codes of tokens no row sees become 0; NaN codes too, and are put
         // back beside the products for the rows that see them
-        const int T = u * kUnit + 16 * stage_group, lo = pg < 0 ? 16 : lo_min - T, hi = hi_max - T;
+        const int T = u * kUnit + 16 * stage_group, lo = pg < 0 ? 16 : lo_min - T, hi = te.end(u, hi_max) - T;
         uint32_t nans = 0;
 #pragma unroll
         for (int e = 0; e < 4; e++) {
@@ -1297,9 +1414,9 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void attn_prompt32(AttnArgs a) {
 #pragma unroll 1
     for (int t = 0; t < 2; t++) {
       const int T = u * kUnit + 32 * t + 16 * hf;
-      int pg = T < hi_max ? table[T >> a.kv.lp] : -1;
+      int pg = T < te.end(u, hi_max) ? te.row(u, table)[(T - te.origin(u)) >> a.kv.lp] : -1;
       pg = pg >= 0 && pg < a.kv.n_pages ? pg : -1;
-      const uint8_t* vc = a.kv.vc + (((int64_t)(pg < 0 ? 0 : pg) * a.kv.H + h) << sh) + (T & (P - 1));
+      const uint8_t* vc = a.kv.vc + (((int64_t)(pg < 0 ? 0 : pg) * a.kv.H + h) << sh) + ((T - te.origin(u)) & (P - 1));
 #pragma unroll 1
       for (int d = 0; d < DT; d++) {
         const mx_u4 w = *(const mx_u4*)(vc + (int64_t)(32 * d + n) * P);
@@ -1312,7 +1429,7 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void attn_prompt32(AttnArgs a) {
           v8bf vis[2];
 #pragma unroll
           for (int e = 0; e < 16; e++)
-            vis[e >> 3][e & 7] = (__bf16)(T + e >= vlo[c] && T + e < vhi[c] ? 1.f : 0.f);
+            vis[e >> 3][e & 7] = (__bf16)(T + e >= vlo[c] && T + e < te.end(u, vhi[c]) ? 1.f : 0.f);
           v16f hit;
 #pragma unroll
           for (int e = 0; e < 16; e++) hit[e] = 0.f;
@@ -1327,14 +1444,14 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void attn_prompt32(AttnArgs a) {
   // weights of step u from its scores
   auto softmax = [&](int u) {
     const int T = u * kUnit;
-    bool mask = T + kUnit > whi_all || T < wlo_all;
+    bool mask = T + kUnit > whi_all || T < wlo_all || te.short_step(u);
     int unread = 0;  // tiles whose 16 tokens of the lane cannot be read
     if (bad_at_[u & 3] == u) {
       mask = true;
 #pragma unroll
       for (int t = 0; t < 2; t++) {
         const int at = T + 32 * t + 16 * hf;
-        const int pg = at < hi_max ? table[at >> a.kv.lp] : -1;
+        const int pg = at < te.end(u, hi_max) ? te.row(u, table)[(at - te.origin(u)) >> a.kv.lp] : -1;
         unread |= pg >= 0 && pg < a.kv.n_pages ? 0 : 1 << t;
       }
     }
@@ -1344,7 +1461,7 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void attn_prompt32(AttnArgs a) {
 #pragma unroll
         for (int t = 0; t < 2; t++) {
           const int at = T + 32 * t + 16 * hf;
-          const int lo = (unread >> t) & 1 ? 16 : vlo[c] - at, hi = vhi[c] - at;
+          const int lo = (unread >> t) & 1 ? 16 : vlo[c] - at, hi = te.end(u, vhi[c]) - at;
           const uint32_t up = hi >= 16 ? 0xFFFFu : hi <= 0 ? 0u : (1u << hi) - 1u;
           const uint32_t seen = lo >= 16 ? 0u : lo <= 0 ? up : up & ~((1u << lo) - 1u);
 #pragma unroll
@@ -1433,11 +1550,11 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void attn_prompt32(AttnArgs a) {
       }
     if (hf == 0) *(float2*)(pp + D) = make_float2(m[c], l[c]);
   };
-  if (MODE == kPrefix || parts > 1) {
+  if (at_.group || parts > 1) {
 #pragma unroll
     for (int c = 0; c < NC; c++) {
       l[c] += __shfl_xor(l[c], 32);
-      if (rho[c] < R) write_sums(c, a.part + ((int64_t)blockIdx.x * ROWS + (rho[c] - wg0)) * (D + kPartPad));
+      if (rho[c] < R) write_sums(c, a.part + ((int64_t)at_.slot * ROWS + (rho[c] - wg0)) * (D + kPartPad));
     }
     return;
   }
@@ -1447,7 +1564,7 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void attn_prompt32(AttnArgs a) {
 #pragma unroll
   for (int c = 0; c < NC; c++) {
     l[c] += __shfl_xor(l[c], 32);
-    if constexpr (MODE == kOwn) {
+    if constexpr (MODE == kMixed) {
       const uint32_t at = (uint32_t)rho[c] / G;
       if (rho[c] < R)
         write_sums(c, a.sums + ((s.row0 + at) * a.Hq + (int64_t)h * G + (rho[c] - at * G)) * (D + kPartPad));
@@ -1488,14 +1605,15 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void attn_prompt32(AttnArgs a) {
 template <int D, int ROWS, int MODE>
 __global__ __launch_bounds__(256) void attn_join(AttnArgs a) {
   constexpr int T4 = D / 4, AHEAD = 8;
-  const uint32_t G = (uint32_t)a.G, H = (uint32_t)a.kv.H, tile_at = blockIdx.x / H, h = blockIdx.x - tile_at * H;
+  const uint32_t G = (uint32_t)a.G, H = (uint32_t)a.kv.H, cut = blockIdx.x / H, h = blockIdx.x - cut * H;
   __shared__ int64_t scan_[256 / 64 + 2];
   PromptTile<ROWS, MODE> t;
-  if (!t.template find<256>(a, tile_at, scan_) || t.parts == 1) return;  // one part: its workgroup has written O
+  if (!t.template find<256>(a, cut + (MODE == kBehind ? a.whole : 0), a.parts, scan_)) return;
+  if (t.parts == 1) return;  // its workgroup has written O
   const int parts = t.parts, at = blockIdx.y * 256 + threadIdx.x, r = at / T4, d = at % T4 * 4;
   if (t.wg0 + r >= t.R) return;
   const int64_t step = (int64_t)H * ROWS * (D + kPartPad);  // to the next part
-  const float* p = a.part + (((int64_t)tile_at * a.parts * H + h) * ROWS + r) * (D + kPartPad);
+  const float* p = a.part + (((int64_t)cut * a.parts * H + h) * ROWS + r) * (D + kPartPad);
   float M = -INFINITY, L = 0.f;
   v4f o = v4f{0.f, 0.f, 0.f, 0.f};
   for (int k = 0; k < parts; k += AHEAD) {
@@ -1526,11 +1644,6 @@ __global__ __launch_bounds__(256) void attn_join(AttnArgs a) {
   }
   const uint32_t rc = t.wg0 + r, tok = rc / G;
   const int64_t row = t.s.row0 + tok, hd = (int64_t)h * G + (rc - tok * G);
-  if constexpr (MODE == kOwn) {
-    float* sums = a.sums + (row * a.Hq + hd) * (D + kPartPad);
-    *(v4f*)(sums + d) = o;
-    if (d == 0) *(float2*)(sums + D) = make_float2(M, L);
-  }
   const float inv = L > 0.f || L != L ? 1.0f / L : 0.f;
   uint2 w;
   w.x = bf16_bits(o[0] * inv) | (bf16_bits(o[1] * inv) << 16);
@@ -1540,30 +1653,25 @@ __global__ __launch_bounds__(256) void attn_join(AttnArgs a) {
 }
 
 // A row behind a shared prefix: its sums over its own tokens and over the prefix
-// (of one launch or of its parts), joined as attn_join does.  The tiles are those
-// of the prefixes' rows, so rows without a prefix keep what kOwn wrote.
-struct MergeArgs {
-  AttnArgs a;         // of the prefixes' launch
-  const float* own;   // [total_q][Hq] sums
-  const float* rows;  // the prefixes' likewise; NULL: in a.part, by tiles and parts
-};
+// (a.prefix_sums, or its tile's parts where that is NULL), joined as attn_join
+// does.  The tiles are those of the groups' rows (a.kv), so rows without a prefix
+// keep what was written for their own tokens.
 template <int D, int ROWS>
-__global__ __launch_bounds__(256) void attn_merge(MergeArgs args) {
-  constexpr int MODE = kPrefix, T4 = D / 4, AHEAD = 8;
-  const AttnArgs& a = args.a;
+__global__ __launch_bounds__(256) void attn_merge(AttnArgs a) {
+  constexpr int T4 = D / 4, AHEAD = 16;
   const uint32_t G = (uint32_t)a.G, H = (uint32_t)a.kv.H, tile_at = blockIdx.x / H, h = blockIdx.x - tile_at * H;
   __shared__ int64_t scan_[256 / 64 + 2];
-  PromptTile<ROWS, MODE> t;
-  if (!t.template find<256>(a, tile_at, scan_)) return;
+  PromptTile<ROWS, kMixed> t;
+  if (!t.template find<256>(a, tile_at, a.parts, scan_)) return;
   const int at = blockIdx.y * 256 + threadIdx.x, r = at / T4, d = at % T4 * 4;
   if (t.wg0 + r >= t.R) return;
   const uint32_t rc = t.wg0 + r, tok = rc / G;
   const int64_t row = t.s.row0 + tok, hd = (int64_t)h * G + (rc - tok * G);
-  const float* own = args.own + (row * a.Hq + hd) * (D + kPartPad);
+  const float* own = a.sums + (row * a.Hq + hd) * (D + kPartPad);
   const int64_t step = (int64_t)H * ROWS * (D + kPartPad);  // to the next part
-  const float* p = args.rows ? args.rows + (row * a.Hq + hd) * (D + kPartPad)
-                             : a.part + (((int64_t)tile_at * a.parts * H + h) * ROWS + r) * (D + kPartPad);
-  const int parts = args.rows ? 1 : t.parts;
+  const float* p = a.prefix_sums ? a.prefix_sums + (row * a.Hq + hd) * (D + kPartPad)
+                                 : a.part + (((int64_t)tile_at * a.parts * H + h) * ROWS + r) * (D + kPartPad);
+  const int parts = a.prefix_sums ? 1 : t.parts;
   v4f o = *(const v4f*)(own + d);
   const float2 own_ml = *(const float2*)(own + D);
   float M = own_ml.x, L = own_ml.y;
@@ -1659,59 +1767,98 @@ Plan plan_attention(const KvArgs& kv, int64_t G, int64_t window) {
   return p;
 }
 
-// bytes behind the counters that a plan's results take until they are joined
-size_t plan_bytes(const Plan& p, int D) {
-  if (p.nc > 0) return (size_t)4 * kMaxShares * 16 * p.nc * (D + 2) * 4;
-  return (size_t)(p.blocks * p.parts * p.rows) * (D + kPartPad) * 4;
-}
-
-// one launch by its plan, and the join of a prompt's parts
 template <int MODE>
-void launch_plan(const Plan& p, AttnArgs a, hipStream_t s) {
-  a.parts = p.parts;
-  const dim3 grid((unsigned)(p.blocks * p.parts));
-  const int D = a.kv.D;
-  if (p.nc == 0) {
-    if (D == 64) hipLaunchKernelGGL((attn_prompt32<64, 1, 4, 3, MODE>), grid, dim3(256), 0, s, a);
-    else if (D == 128 && p.rows == 128) hipLaunchKernelGGL((attn_prompt32<128, 1, 4, 2, MODE>), grid, dim3(256), 0, s, a);
-    else if (D == 128) hipLaunchKernelGGL((attn_prompt32<128, 1, 8, 2, MODE>), grid, dim3(512), 0, s, a);
-    else hipLaunchKernelGGL((attn_prompt<256, 1, 8, MODE>), grid, dim3(512), 0, s, a);
-    if constexpr (MODE != kPrefix) {
-      if (p.parts == 1) return;
-      const dim3 join((unsigned)p.blocks, (unsigned)(p.rows * D / 4 / 256));
-      if (D == 64) hipLaunchKernelGGL((attn_join<64, 128, MODE>), join, dim3(256), 0, s, a);
-      else if (D == 128 && p.rows == 128) hipLaunchKernelGGL((attn_join<128, 128, MODE>), join, dim3(256), 0, s, a);
-      else if (D == 128) hipLaunchKernelGGL((attn_join<128, 256, MODE>), join, dim3(256), 0, s, a);
-      else hipLaunchKernelGGL((attn_join<256, 128, MODE>), join, dim3(256), 0, s, a);
-    }
-    return;
-  }
-#define LOWBIT_DEC(DD, NN) \
-  hipLaunchKernelGGL((attn_decode<DD, NN, MODE>), grid, dim3(64 * kDecWaves), 0, s, a)
-  if (D == 64 && p.nc == 1) LOWBIT_DEC(64, 1);
-  else if (D == 64) LOWBIT_DEC(64, 2);
-  else if (D == 128) LOWBIT_DEC(128, 1);
-  else LOWBIT_DEC(256, 1);
-#undef LOWBIT_DEC
+void launch_prompt(int rows, unsigned blocks, const AttnArgs& a, hipStream_t s) {
+  const dim3 grid(blocks);
+  if (a.kv.D == 64) hipLaunchKernelGGL((attn_prompt32<64, 1, 4, 3, MODE>), grid, dim3(256), 0, s, a);
+  else if (a.kv.D == 128 && rows == 128) hipLaunchKernelGGL((attn_prompt32<128, 1, 4, 2, MODE>), grid, dim3(256), 0, s, a);
+  else if (a.kv.D == 128) hipLaunchKernelGGL((attn_prompt32<128, 1, 8, 2, MODE>), grid, dim3(512), 0, s, a);
+  else hipLaunchKernelGGL((attn_prompt<256, 1, 8, MODE>), grid, dim3(512), 0, s, a);
+}
+// tiles: of all heads
+template <int MODE>
+void launch_join(int rows, int64_t tiles, const AttnArgs& a, hipStream_t s) {
+  const dim3 grid((unsigned)tiles, (unsigned)(rows * a.kv.D / 4 / 256));
+  if (a.kv.D == 64) hipLaunchKernelGGL((attn_join<64, 128, MODE>), grid, dim3(256), 0, s, a);
+  else if (a.kv.D == 128 && rows == 128) hipLaunchKernelGGL((attn_join<128, 128, MODE>), grid, dim3(256), 0, s, a);
+  else if (a.kv.D == 128) hipLaunchKernelGGL((attn_join<128, 256, MODE>), grid, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((attn_join<256, 128, MODE>), grid, dim3(256), 0, s, a);
+}
+template <int MODE>
+void launch_decode(int nc, unsigned blocks, const AttnArgs& a, hipStream_t s) {
+  const dim3 grid(blocks), block(64 * kDecWaves);
+  if (a.kv.D == 64 && nc == 1) hipLaunchKernelGGL((attn_decode<64, 1, MODE>), grid, block, 0, s, a);
+  else if (a.kv.D == 64) hipLaunchKernelGGL((attn_decode<64, 2, MODE>), grid, block, 0, s, a);
+  else if (a.kv.D == 128) hipLaunchKernelGGL((attn_decode<128, 1, MODE>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((attn_decode<256, 1, MODE>), grid, block, 0, s, a);
 }
 
-// Of a call behind shared prefixes: the sequences' own launch and the prefixes'.
+// bound on the tiles of all heads
+int64_t tiles_of(const KvArgs& kv, int64_t G, int64_t rows) {
+  return std::min<int64_t>(kv.n_seqs * kv.H * cdiv(kv.max_q * G, rows), kv.H * (kv.total_q * G / rows + kv.n_seqs));
+}
+int best_parts(int64_t steps) { return (int)std::max<int64_t>((int64_t)(2.0 * sqrt((double)steps)), 1); }
+
+// Of a call behind shared prefixes.
 struct PrefixPlan {
-  Plan own, prefix;
-  int64_t rows, merge_blocks;  // of a merge tile
-  size_t sums, own_bytes, prefix_bytes;
+  Mode mode;
+  int nc, rows, parts, whole;
+  int64_t tiles;                 // kBehind: of the sequences' rows; kMixed, kUnion: of the groups'
+  int64_t blocks, prefix_wgs;    // of the launch; kMixed: the first of them
+  size_t sums, prefix_sums, part;  // bytes
 };
-PrefixPlan plan_prefix(const AttnArgs& a, const KvArgs& prefix) {
-  PrefixPlan p;
-  p.own = plan_attention(a.kv, a.G, 0);
-  p.prefix = plan_attention(prefix, a.G, 0);
-  p.rows = p.prefix.nc == 0 ? p.prefix.rows : 128;
-  p.merge_blocks = p.prefix.nc == 0 ? p.prefix.blocks
-                                    : std::min<int64_t>(prefix.n_seqs * prefix.H * cdiv(prefix.max_q * a.G, p.rows),
-                                                        prefix.H * (prefix.total_q * a.G / p.rows + prefix.n_seqs));
-  p.sums = (size_t)(a.kv.total_q * a.Hq) * (a.kv.D + kPartPad) * 4;
-  p.own_bytes = p.own.nc == 0 && p.own.parts == 1 ? 0 : plan_bytes(p.own, a.kv.D);
-  p.prefix_bytes = plan_bytes(p.prefix, a.kv.D);
+PrefixPlan plan_prefix(const AttnArgs& a) {
+  const KvArgs &kv = a.kv, &prefix = a.prefix;
+  const int64_t Rs = kv.max_q * a.G, Rg = prefix.max_q * a.G, row_bytes = (kv.D + kPartPad) * 4;
+  PrefixPlan p = {};
+  p.parts = 1;
+  p.sums = (size_t)(kv.total_q * a.Hq * row_bytes);
+  if (Rs > 64) {
+    p.mode = kBehind;
+    p.rows = prompt_rows(kv.D, Rs);
+    p.tiles = tiles_of(kv, a.G, p.rows);
+    const int64_t slots = prompt_slots(kv.D, Rs);
+    const int64_t cut = p.tiles % slots ? cdiv(p.tiles % slots, kv.H) : 0;  // tiles of a head behind the last full round
+    p.whole = (int)(p.tiles / kv.H - cut);
+    p.parts = (int)std::min<int64_t>(cut ? std::max<int64_t>(slots / (cut * kv.H), 1) : 1,
+                                     best_parts(cdiv(prefix.max_kv, kUnit) + cdiv(kv.max_kv, kUnit)));
+    if (p.parts == 1) p.whole = (int)(p.tiles / kv.H);
+    p.blocks = p.whole * kv.H + (p.tiles - p.whole * kv.H) * p.parts;
+    p.sums = 0;
+    p.part = (size_t)((p.blocks - p.whole * kv.H) * p.rows * row_bytes);
+    return p;
+  }
+  if (!many_rows(prefix, Rg)) {
+    p.mode = kUnion;
+    p.nc = std::max(Rs, Rg) > 16 && kv.D == 64 ? 2 : 1;
+    p.blocks = kv.D == 256 ? kMaxShares / 2 : kMaxShares;
+    p.rows = 128;
+    p.tiles = tiles_of(prefix, a.G, p.rows);
+    p.prefix_sums = p.sums;
+    p.part = (size_t)4 * kMaxShares * 16 * p.nc * (kv.D + 2) * 4;
+    return p;
+  }
+  p.mode = kMixed;
+  p.rows = prompt_rows(kv.D, Rg > 512 ? Rg : 128);
+  p.tiles = tiles_of(prefix, a.G, p.rows);
+  const int64_t own = tiles_of(kv, a.G, p.rows), slots = prompt_slots(kv.D, p.rows), best = best_parts(cdiv(prefix.max_kv, kUnit));
+  const int64_t room = std::max(slots - own, slots / 2);
+  if (p.tiles <= room) {
+    p.parts = (int)std::min(room / p.tiles, best);
+  } else {
+    // as many parts as leave the least of the last round idle
+    double least = 1e30;
+    for (int64_t k = 1; k <= std::min<int64_t>(4, best); k++) {
+      const double t = (double)cdiv(p.tiles * k, slots) / k + 0.03 * k;
+      if (t < least) {
+        least = t;
+        p.parts = (int)k;
+      }
+    }
+  }
+  p.prefix_wgs = p.tiles * p.parts;
+  p.blocks = p.prefix_wgs + own;
+  p.part = (size_t)(p.prefix_wgs * p.rows * row_bytes);
   return p;
 }
 
@@ -1721,44 +1868,59 @@ int64_t attention_blocks(const KvArgs& kv, int64_t G) { return plan_attention(kv
 
 size_t attention_workspace_bytes(const KvArgs& kv, int64_t G) {
   const Plan p = plan_attention(kv, G, 0);  // a window takes no more
-  if (p.nc == 0 && p.parts == 1) return 0;
-  return (size_t)kCounterBytes + plan_bytes(p, kv.D);
+  if (p.nc > 0) return (size_t)kCounterBytes + (size_t)4 * kMaxShares * 16 * p.nc * (kv.D + 2) * 4;
+  if (p.parts == 1) return 0;
+  return (size_t)kCounterBytes + (size_t)(p.blocks * p.parts * p.rows) * (kv.D + kPartPad) * 4;
 }
 
 hipError_t launch_attention(AttnArgs a, void* ws, hipStream_t s) {
+  const Plan p = plan_attention(a.kv, a.G, a.causal ? a.window : 0);
   a.cnt = (uint32_t*)ws + 16;
   a.part = (float*)((uint8_t*)ws + kCounterBytes);
-  launch_plan<kPlain>(plan_attention(a.kv, a.G, a.causal ? a.window : 0), a, s);
+  a.parts = p.parts;
+  if (p.nc > 0) {
+    launch_decode<kPlain>(p.nc, (unsigned)p.blocks, a, s);
+  } else {
+    launch_prompt<kPlain>(p.rows, (unsigned)(p.blocks * p.parts), a, s);
+    if (p.parts > 1) launch_join<kPlain>(p.rows, p.blocks, a, s);
+  }
   return hipGetLastError();
 }
 
-size_t attention_prefix_workspace_bytes(const AttnArgs& a, const KvArgs& prefix) {
-  const PrefixPlan p = plan_prefix(a, prefix);
-  return (size_t)kCounterBytes + p.sums * (p.prefix.nc > 0 ? 2 : 1) + p.own_bytes + p.prefix_bytes;
+bool attention_prefix_fits(const AttnArgs& a) {
+  const PrefixPlan p = plan_prefix(a);
+  return p.blocks <= (1 << 22) && p.tiles <= (1 << 22);
 }
 
-hipError_t launch_attention_prefix(AttnArgs a, const KvArgs& prefix, void* ws, hipStream_t s) {
-  const PrefixPlan p = plan_prefix(a, prefix);
+size_t attention_prefix_workspace_bytes(const AttnArgs& a) {
+  const PrefixPlan p = plan_prefix(a);
+  return (size_t)kCounterBytes + p.sums + p.prefix_sums + p.part;
+}
+
+hipError_t launch_attention_prefix(AttnArgs a, void* ws, hipStream_t s) {
+  const PrefixPlan p = plan_prefix(a);
   uint8_t* at = (uint8_t*)ws + kCounterBytes;
-  float *own = (float*)at, *rows = p.prefix.nc > 0 ? (float*)(at + p.sums) : nullptr;
-  at += p.sums * (p.prefix.nc > 0 ? 2 : 1);
   a.cnt = (uint32_t*)ws + 16;
-  a.sums = own;
-  a.part = (float*)at;
-  launch_plan<kOwn>(p.own, a, s);
-  MergeArgs m{a, own, rows};
-  m.a.kv = prefix;
-  m.a.causal = 0;
-  m.a.cnt += kCounterWords / 2;
-  m.a.sums = rows;
-  m.a.part = (float*)(at + p.own_bytes);
-  m.a.parts = p.prefix.nc == 0 ? p.prefix.parts : 1;
-  launch_plan<kPrefix>(p.prefix, m.a, s);
-  const dim3 grid((unsigned)p.merge_blocks, (unsigned)(p.rows * a.kv.D / 4 / 256));
-  if (a.kv.D == 64) hipLaunchKernelGGL((attn_merge<64, 128>), grid, dim3(256), 0, s, m);
-  else if (a.kv.D == 128 && p.rows == 128) hipLaunchKernelGGL((attn_merge<128, 128>), grid, dim3(256), 0, s, m);
-  else if (a.kv.D == 128) hipLaunchKernelGGL((attn_merge<128, 256>), grid, dim3(256), 0, s, m);
-  else hipLaunchKernelGGL((attn_merge<256, 128>), grid, dim3(256), 0, s, m);
+  a.sums = (float*)at;
+  a.prefix_sums = p.prefix_sums ? (float*)(at + p.sums) : nullptr;
+  a.part = (float*)(at + p.sums + p.prefix_sums);
+  a.parts = p.parts;
+  a.whole = p.whole;
+  a.prefix_wgs = (uint32_t)p.prefix_wgs;
+  if (p.mode == kBehind) {
+    launch_prompt<kBehind>(p.rows, (unsigned)p.blocks, a, s);
+    if (p.parts > 1) launch_join<kBehind>(p.rows, p.tiles - p.whole * a.kv.H, a, s);
+    return hipGetLastError();
+  }
+  if (p.mode == kUnion) launch_decode<kUnion>(p.nc, (unsigned)p.blocks, a, s);
+  else launch_prompt<kMixed>(p.rows, (unsigned)p.blocks, a, s);
+  a.kv = a.prefix;
+  a.causal = 0;
+  const dim3 grid((unsigned)p.tiles, (unsigned)(p.rows * a.kv.D / 4 / 256));
+  if (a.kv.D == 64) hipLaunchKernelGGL((attn_merge<64, 128>), grid, dim3(256), 0, s, a);
+  else if (a.kv.D == 128 && p.rows == 128) hipLaunchKernelGGL((attn_merge<128, 128>), grid, dim3(256), 0, s, a);
+  else if (a.kv.D == 128) hipLaunchKernelGGL((attn_merge<128, 256>), grid, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((attn_merge<256, 128>), grid, dim3(256), 0, s, a);
   return hipGetLastError();
 }
 

@@ -216,7 +216,8 @@ int64_t attention_blocks(const KvArgs& kv, int64_t G);
 size_t attention_workspace_bytes(const KvArgs& kv, int64_t G);
 hipError_t launch_attention(AttnArgs a, void* ws, hipStream_t s);
 // the same behind prefixes that groups of sequences share
-size_t attention_prefix_workspace_bytes(const AttnArgs& a, const KvArgs& prefix);
-hipError_t launch_attention_prefix(AttnArgs a, const KvArgs& prefix, void* ws, hipStream_t s);
+bool attention_prefix_fits(const AttnArgs& a);  // its launches hold their workgroups
+size_t attention_prefix_workspace_bytes(const AttnArgs& a);
+hipError_t launch_attention_prefix(AttnArgs a, void* ws, hipStream_t s);
 
 }  // namespace lowbit

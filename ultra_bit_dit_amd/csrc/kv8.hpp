@@ -29,7 +29,7 @@ struct KvArgs {
   // Groups in the place of sequences: a group's rows are those of its sequences.
   const int32_t* members;    // [n_seqs + 1] first sequence of each group, or NULL: member_count each
   int64_t member_count;
-  int64_t n_members, member_q;  // sequences in all, and rows of each where `starts` (theirs) is NULL
+  int64_t n_members, member_q;  // sequences in all (0: no groups), and rows of each where `starts` (theirs) is NULL
 };
 
 // Length and new tokens of sequence b, clamped to what the table and the
@@ -38,6 +38,7 @@ struct SeqSpan {
   int64_t row0;  // first row of its new tokens
   int n, len;    // new tokens, length with them
 };
+// GROUPS: `a` may be of groups.
 template <bool GROUPS = false>
 __device__ __forceinline__ SeqSpan seq_span(const KvArgs& a, int64_t b) {
   SeqSpan s;
@@ -45,7 +46,7 @@ __device__ __forceinline__ SeqSpan seq_span(const KvArgs& a, int64_t b) {
   len = len < 0 ? 0 : len;
   len = len < a.max_kv ? len : a.max_kv;  // max_kv <= width * page tokens
   int64_t r0, r1;
-  if constexpr (GROUPS) {
+  if (GROUPS && a.n_members) {
     int64_t m0 = a.members ? (int64_t)a.members[b] : b * a.member_count;
     int64_t m1 = a.members ? (int64_t)a.members[b + 1] : m0 + a.member_count;
     m0 = m0 < 0 ? 0 : m0 < a.n_members ? m0 : a.n_members;
@@ -131,7 +132,12 @@ struct AttnArgs {
   float* lse;                // [total_q][Hq] or NULL
   float* part;               // results of shares: two places each, then of their groups; or of a tile's parts
   int parts;                 // of a prompt tile
-  float* sums;               // [total_q][Hq] sums before the division, for a row that is joined with more tokens
+  // behind shared prefixes
+  KvArgs prefix;             // their groups
+  float* sums;               // [total_q][Hq] sums of a row over its own tokens, before the division
+  float* prefix_sums;        // and over its prefix, where that is not in parts
+  uint32_t prefix_wgs;       // workgroups of the prefixes' tiles
+  int whole;                 // tiles of a head whose steps are not cut into parts
   uint32_t* cnt;             // arrivals: of a group (by the place of its first share), then of a tile
 };
 
