@@ -23,14 +23,12 @@
 //
 // MODE.  kPlain: a call's rows see the tokens of one sequence each.  The others are
 // of calls behind prefixes that groups of sequences share:
-//   kBehind  a row's tokens are its prefix's and then its own, from two tables; the
-//            steps of the prefix come first, and its last one may be partly filled.
-//            For sequences of many rows, which fill tiles by themselves.
-//   kMixed   tiles of the groups' rows (those of their sequences lie in order) see
-//            the prefixes, tiles of the sequences' rows their own tokens, in one launch;
-//            attn_merge adds the two.  For few rows of each sequence.
-//   kUnion   the same for few rows in all: the sequences and behind them the groups are
-//            one list of items for attn_decode.
+//   kBehind  a row's tokens are its prefix's and then its own, from two tables: steps
+//            of the prefix come first, and the last one may be partly filled.  For
+//            sequences of many rows, which fill tiles by themselves, and for small calls.
+//   kHead    groups in the place of sequences: the rows of a group's sequences, which lie
+//            in order, see its prefix, and leave their sums in the workspace;
+//   kTail    each sequence's rows see its own tokens, and take those sums in.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -41,23 +39,7 @@
 namespace lowbit {
 namespace {
 
-enum Mode { kPlain, kBehind, kMixed, kUnion };
-
-// x or y (field by field: a chosen address would put both into private memory)
-__device__ __forceinline__ KvArgs either(bool first, const KvArgs& x, const KvArgs& y) {
-  KvArgs r = y;
-  r.n_seqs = first ? x.n_seqs : y.n_seqs;
-  r.table = first ? x.table : y.table;
-  r.width = first ? x.width : y.width;
-  r.lens = first ? x.lens : y.lens;
-  r.max_q = first ? x.max_q : y.max_q;
-  r.max_kv = first ? x.max_kv : y.max_kv;
-  r.members = first ? x.members : y.members;
-  r.member_count = first ? x.member_count : y.member_count;
-  r.n_members = first ? x.n_members : y.n_members;
-  r.member_q = first ? x.member_q : y.member_q;
-  return r;
-}
+enum Mode { kPlain, kBehind, kHead, kTail };
 
 constexpr int kUnit = 64;  // tokens of one step of a wave
 constexpr float kLn2 = 0.6931471805599453f;
@@ -120,6 +102,37 @@ __device__ __forceinline__ int64_t quot(int64_t a, int64_t b) {
   if (__builtin_expect((((uint64_t)a | (uint64_t)b) >> 32) == 0, 1)) return (uint32_t)a / (uint32_t)b;
   return a / b;
 }
+
+// The tokens of a sequence's shared prefix (kBehind; else none).  Positions count
+// them first, in whole steps: own token t stands at kUnit * steps + t.
+template <int MODE>
+struct Head {
+  int len = 0, steps = 0;
+  const int32_t* table = nullptr;
+  __device__ __forceinline__ void find(const AttnArgs& a, int64_t b) {
+    len = steps = 0;
+    const int64_t g = group_of(a.prefix, b);
+    if (g < 0) return;
+    const int64_t n = a.prefix.lens[g];
+    len = (int)(n < 0 ? 0 : n < a.prefix.max_kv ? n : a.prefix.max_kv);
+    steps = (len + kUnit - 1) / kUnit;
+    table = a.prefix.table + g * a.prefix.width;
+  }
+  __device__ __forceinline__ int tokens() const { return MODE == kBehind ? steps * kUnit : 0; }
+  __device__ __forceinline__ bool has(int t) const { return MODE == kBehind && t < steps * kUnit; }
+  // Of the tokens around position t: their end (`hi` that of the own ones), the row
+  // of the table that has them, the position of its first token.
+  __device__ __forceinline__ int end(int t, int hi) const { return has(t) ? len : hi; }
+  __device__ __forceinline__ const int32_t* row(int t, const int32_t* own) const { return has(t) ? table : own; }
+  __device__ __forceinline__ int origin(int t) const { return has(t) ? 0 : tokens(); }
+  // the step at T has positions without a token
+  __device__ __forceinline__ bool gap(int T) const { return MODE == kBehind && T + kUnit == steps * kUnit && len < steps * kUnit; }
+  // end of the tokens that a row at position p of `n` sees
+  __device__ __forceinline__ int sees_to(int causal, int p, int n) const {
+    const int e = causal ? min(n, p + 1) : n;
+    return MODE == kBehind ? max(e, steps * kUnit) : e;
+  }
+};
 
 // Work items numbered in the order of the sequences, sequence b having
 // count(b) of them: each thread sums a run of sequences, one scan joins them.
@@ -205,6 +218,15 @@ constexpr int kJoinLoads = 8;   // results of a pair of outputs read at once
 constexpr int kMaxJoin = 32;    // results joined by one workgroup: shares of a tile <= kMaxJoin^2
 constexpr int kMaxShares = 512;
 
+// Parts of a tile of `steps` steps: at most the launch's, which knows only a
+// bound on the length.  A step takes some 1.5 us, a part more to join 0.4: twice
+// the root of the steps is best (40 tokens of 32 heads over 8, D = 128, in 4096
+// tokens: 27 us in 32 parts, 22 in 16, 26 in 8; in 1024 16 us in 8, 19 in 4, 25
+// in 2; in 1000 with a bound of 131072 36 us without this limit).
+__device__ __forceinline__ int parts_of(int steps, int most) {
+  return max(1, min((int)(2.f * __builtin_amdgcn_sqrtf((float)steps)), most));
+}
+
 // two floats, device-coherent
 __device__ __forceinline__ void put2(float* p, float x, float y) {
   __hip_atomic_store((uint64_t*)p, (uint64_t)__float_as_uint(x) | ((uint64_t)__float_as_uint(y) << 32),
@@ -232,11 +254,14 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 15, g = lane >> 4;
   const int P = 1 << a.kv.lp;
-  // items: sequences, and behind them groups
-  const int64_t n_items = MODE == kUnion ? a.kv.n_seqs + a.prefix.n_seqs : a.kv.n_seqs;
   auto span_of = [&](int64_t i) -> SeqSpan {
-    if (MODE == kUnion && i >= a.kv.n_seqs) return seq_span<true>(a.prefix, i - a.kv.n_seqs);
-    return seq_span(a.kv, i);
+    SeqSpan t = seq_span<MODE == kHead>(a.kv, i);
+    if constexpr (MODE == kBehind) {
+      Head<MODE> head;
+      head.find(a, i);
+      t.len += head.tokens();
+    }
+    return t;
   };
   // blocks of one tile of a sequence (at least one, which writes its rows), and its tiles
   auto blocks_of = [&](const SeqSpan& t) -> int64_t {
@@ -245,18 +270,20 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
     return max((most + kBlock - 1) / kBlock, (int64_t)1);
   };
   auto tiles_of = [&](const SeqSpan& t) -> int64_t { return (t.n * a.G + 16 * NC - 1) / (16 * NC); };
+  // many tiles of few blocks: a workgroup has one, so that none has to be joined
+  const bool whole = MODE == kTail && a.whole;
   auto work_of = [&](int64_t i) -> int64_t {
     const SeqSpan t = span_of(i);
-    return tiles_of(t) * blocks_of(t);
+    return tiles_of(t) * (whole ? 1 : blocks_of(t));
   };
-  ItemScan<64 * kDecWaves, decltype(work_of)> scan(n_items, work_of, scan_);
+  ItemScan<64 * kDecWaves, decltype(work_of)> scan(a.kv.n_seqs, work_of, scan_);
   const int64_t per_head = scan.total, total = per_head * a.kv.H;
   // Shares: one for each block while there are workgroups for that, so that none
   // has parts of two tiles, which it would have to begin and join in turn
   const int64_t shares = max(min(total, (int64_t)gridDim.x), (int64_t)1);
   // neighbouring shares on one XCD (bid % 8) where every workgroup has one
   const int64_t per_xcd = gridDim.x / 8, bid = blockIdx.x;
-  const int64_t share = shares == (int64_t)gridDim.x ? (bid % 8) * per_xcd + bid / 8 : bid;
+  const int64_t share = shares == (int64_t)gridDim.x && !whole ? (bid % 8) * per_xcd + bid / 8 : bid;
   if (share >= shares) return;
   int64_t x = quot(total * share, shares);
   const int64_t x_end = quot(total * (share + 1), shares);
@@ -265,7 +292,7 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
   int64_t b, item;
   scan.find(x - h * per_head, &b, &item);
   SeqSpan s = span_of(b);
-  int64_t blocks = blocks_of(s), tiles = tiles_of(s);
+  int64_t blocks = whole ? 1 : blocks_of(s), tiles = tiles_of(s);
   int64_t rt = quot(item, blocks);
   int at = (int)(item - rt * blocks);  // first block of this share in the tile
   for (;;) {
@@ -278,8 +305,8 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
     const int64_t R = (int64_t)s.n * a.G;
     const int64_t rho0 = rt * 16 * NC;
     const int len = s.len, first = len - s.n;  // position of the first new token
-    const bool group = MODE == kUnion && b >= a.kv.n_seqs;
-    const bool causal = a.causal && !group;
+    Head<MODE> head;
+    if constexpr (MODE == kBehind || MODE == kTail) head.find(a, b);
 
     // visible tokens of this lane's rows: [vlo, vhi)
     int vlo[NC], vhi[NC];
@@ -287,8 +314,8 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
     {
       const int64_t rlast = rho0 + 16 * NC - 1 < R ? rho0 + 16 * NC - 1 : R - 1;
       const int p0 = first + (int)(rho0 / a.G), p1 = first + (int)(rlast / a.G);
-      hi_max = causal ? min(len, p1 + 1) : len;
-      hi_min = causal ? min(len, p0 + 1) : len;
+      hi_max = head.sees_to(a.causal, p1, len);
+      hi_min = head.sees_to(a.causal, p0, len);
       hi_max = max(hi_max, 0);
       hi_min = max(hi_min, 0);
       if (a.window > 0) {
@@ -302,10 +329,11 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
       rho[c] = rho0 + 16 * c + n;
       const int64_t rc = rho[c] < R ? rho[c] : R - 1;
       const int p = first + (int)(rc / a.G);
-      vhi[c] = causal ? min(len, p + 1) : len;
+      vhi[c] = head.sees_to(a.causal, p, len);
       vlo[c] = a.window > 0 ? max(0, p - a.window + 1) : 0;
     }
-    const int u0 = lo_min / kUnit + kDecWaves * at, u1 = min(u0 + kDecWaves * count, (hi_max + kUnit - 1) / kUnit);
+    const int u0 = lo_min / kUnit + kDecWaves * at, u_end = (hi_max + kUnit - 1) / kUnit;
+    const int u1 = whole ? u_end : min(u0 + kDecWaves * count, u_end);
 
     // Q: lane (n, g) holds dims 64 c + 16 g + 8 e .. + 7 of its row
     v8bf qf[NC][DC][2];
@@ -330,14 +358,16 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
       for (int d = 0; d < DT; d++) o[c][d] = v4f{0.f, 0.f, 0.f, 0.f};
     }
 
-    const int32_t* table = group ? a.prefix.table + (b - a.kv.n_seqs) * a.prefix.width : a.kv.table + b * a.kv.width;
+    const int32_t* table = a.kv.table + b * a.kv.width;
     const int64_t page_bytes = ((int64_t)D << a.kv.lp);
     // Entry of the 16 tokens from t on, and the page it names: -1 where there are
     // none, -2 where it is unusable.  (Looked at when the page is needed: looked at
     // when read, it would be waited for, and every load before it.)
-    auto entry_at = [&](int t) -> int { return table[min(t, hi_max - 1) >> a.kv.lp]; };
+    auto entry_at = [&](int t) -> int {
+      return head.row(t, table)[(min(t, head.end(t, hi_max) - 1) - head.origin(t)) >> a.kv.lp];
+    };
     auto page_of = [&](int t, int entry) -> int {
-      return t >= hi_max ? -1 : entry >= 0 && entry < (int)a.kv.n_pages ? entry : -2;
+      return t >= head.end(t, hi_max) ? -1 : entry >= 0 && entry < (int)a.kv.n_pages ? entry : -2;
     };
     mx_u4 kr[4][DC], vr[DT];
     int pgv = -1, pkn = 0, pvn = 0;  // this step's values' page, the next step's keys' and values' entries
@@ -349,7 +379,7 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
     auto load_k = [&](int u) {
       const int tk = u * kUnit + 16 * (n >> 2);
       const int64_t ph = (int64_t)max(page_of(tk, pkn), 0) * a.kv.H + h;
-      const uint8_t* kp = a.kv.kc + ph * page_bytes + (int64_t)((tk & (P - 1)) + (n & 3)) * D + 16 * g;
+      const uint8_t* kp = a.kv.kc + ph * page_bytes + (int64_t)(((tk - head.origin(tk)) & (P - 1)) + (n & 3)) * D + 16 * g;
       kb = a.kv.ks[ph];
 #pragma unroll
       for (int t = 0; t < 4; t++)
@@ -360,7 +390,7 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
       const int tv = u * kUnit + 16 * g;
       pgv = page_of(tv, entry);
       const int64_t ph = (int64_t)max(pgv, 0) * a.kv.H + h;
-      const uint8_t* vp = a.kv.vc + ph * page_bytes + (int64_t)n * P + (tv & (P - 1));
+      const uint8_t* vp = a.kv.vc + ph * page_bytes + (int64_t)n * P + ((tv - head.origin(tv)) & (P - 1));
       vb = a.kv.vs[ph];
 #pragma unroll
       for (int d = 0; d < DT; d++) vr[d] = *(const mx_u4*)(vp + (int64_t)16 * d * P);
@@ -381,7 +411,7 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
       const float sk = pow2_byte(kb), sv = gone ? 0.f : pow2_byte(vb);
       if (pgv == -2 && n == 0 && a.kv.bad) atomicAdd(a.kv.bad, 1);
       const int T = u * kUnit;
-      const bool part = T + kUnit > hi_min || T < lo_max || __any(gone);
+      const bool part = T + kUnit > hi_min || T < lo_max || head.gap(T) || __any(gone);
       // scores of tokens T + 16 g + 4 t + j
       v4f sc[NC][4];
 #pragma unroll
@@ -414,7 +444,7 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
 #pragma unroll
           for (int e = 0; e < 16; e++) {
             const int tok = T + 16 * g + e;
-            const bool see = tok >= vlo[c] && tok < vhi[c] && !gone;
+            const bool see = tok >= vlo[c] && tok < head.end(T, vhi[c]) && !gone;
             seen[c] |= see ? 1u << e : 0u;
             sc[c][e >> 2][e & 3] = see ? sc[c][e >> 2][e & 3] * a.scale2 : -INFINITY;
           }
@@ -451,7 +481,7 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
         // A NaN code of a token that only some rows see must reach those rows
         // alone: it becomes 0 too and is put back below.
         uint32_t nans = 0;
-        const int lo = (gone ? 16 : lo_min - (T + 16 * g)), hi = hi_max - (T + 16 * g);
+        const int lo = (gone ? 16 : lo_min - (T + 16 * g)), hi = head.end(T, hi_max) - (T + 16 * g);
         const uint32_t k0 = byte_range(lo, hi), k1 = byte_range(lo - 4, hi - 4);
         const uint32_t k2 = byte_range(lo - 8, hi - 8), k3 = byte_range(lo - 12, hi - 12);
 #pragma unroll
@@ -503,6 +533,30 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
         }
       }
       if (u + kDecWaves < u1) load_v(u + kDecWaves, pvu);
+    }
+
+    if constexpr (MODE == kTail) {
+      // the sums over the prefix, its parts for the waves in turn (the tile's first share takes them in)
+      const int parts = share == share0 && head.len > 0 ? parts_of(head.steps, a.sums_parts) : 0;
+      for (int k = wave; k < parts; k += kDecWaves) {
+#pragma unroll
+        for (int c = 0; c < NC; c++) {
+          const int64_t rc = rho[c] < R ? rho[c] : R - 1;
+          const float* sums = a.sums + ((k * a.kv.total_q + s.row0 + rc / a.G) * a.Hq + h * a.G + rc % a.G) * (D + kPartPad);
+          const float2 ml = *(const float2*)(sums + D);
+          v4f v[DT];
+#pragma unroll
+          for (int d = 0; d < DT; d++) v[d] = *(const v4f*)(sums + 16 * d + 4 * g);
+          const float mn = fmaxf(m[c], ml.x), mu = mn == -INFINITY ? 0.f : mn;
+          const float al = __builtin_amdgcn_exp2f(m[c] - mu), w = __builtin_amdgcn_exp2f(ml.x - mu);
+          m[c] = mn;
+          l[c] = l[c] * al + (g == 0 ? w * ml.y : 0.f);  // the lanes of a row are added below
+#pragma unroll
+          for (int d = 0; d < DT; d++)
+#pragma unroll
+            for (int e = 0; e < 4; e++) o[c][d][e] = o[c][d][e] * al + w * v[d][e];
+        }
+      }
     }
 
     // ---- the waves' results: common maximum, then O added in the order of the waves
@@ -562,13 +616,13 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
           if (rho[c] >= R) continue;
           const float inv = lt[c] > 0.f || lt[c] != lt[c] ? 1.0f / lt[c] : 0.f;
           const int64_t tok = s.row0 + rho[c] / a.G, hd = h * a.G + rho[c] % a.G;
-          if constexpr (MODE == kUnion) {
-            float* sums = (group ? a.prefix_sums : a.sums) + (tok * a.Hq + hd) * (D + kPartPad);
+          if constexpr (MODE == kHead) {
+            float* sums = a.sums + (tok * a.Hq + hd) * (D + kPartPad);
 #pragma unroll
             for (int d = 0; d < DT; d++) *(v4f*)(sums + 16 * d + 4 * g) = o[c][d];
             if (g == 0) *(float2*)(sums + D) = make_float2(mt[c], lt[c]);
+            continue;
           }
-          if (group) continue;
           uint16_t* op = a.o + tok * a.o_stride + hd * D + 4 * g;
 #pragma unroll
           for (int d = 0; d < DT; d++) {
@@ -666,12 +720,12 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
       auto finish = [&](int r, int d, float px, float py) {
         const float L = jl[r], inv = L > 0.f || L != L ? 1.0f / L : 0.f;
         const int64_t rr = rho0 + r, tok = s.row0 + rr / a.G, hd = h * a.G + rr % a.G;
-        if constexpr (MODE == kUnion) {
-          float* sums = (group ? a.prefix_sums : a.sums) + (tok * a.Hq + hd) * (D + kPartPad);
+        if constexpr (MODE == kHead) {
+          float* sums = a.sums + (tok * a.Hq + hd) * (D + kPartPad);
           *(float2*)(sums + d) = make_float2(px, py);
           if (d == 0) *(float2*)(sums + D) = make_float2(jm[r], L);
+          return;
         }
-        if (group) return;
         *(uint32_t*)(a.o + tok * a.o_stride + hd * D + d) = bf16_bits(px * inv) | (bf16_bits(py * inv) << 16);
         if (a.lse && d == 0) a.lse[tok * a.Hq + hd] = L == 0.f ? -INFINITY : (jm[r] + __builtin_amdgcn_logf(L)) * kLn2;
       };
@@ -705,14 +759,14 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
     if (++rt == tiles) {
       rt = 0;
       do {
-        if (++b == n_items) {
+        if (++b == a.kv.n_seqs) {
           b = 0;
           h++;
         }
         s = span_of(b);
         tiles = tiles_of(s);
       } while (tiles == 0);  // some sequence has tiles, as x < total
-      blocks = blocks_of(s);
+      blocks = whole ? 1 : blocks_of(s);
     }
   }
 }
@@ -725,14 +779,6 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
 // heads over 4, D = 256: 593 us (0.70 PFLOP/s).
 // Where the tiles do not fill the chip, a tile's steps are cut into parts, one
 // workgroup each, whose results attn_join puts together.
-// Parts of a tile of `steps` steps: at most the launch's, which knows only a
-// bound on the length.  A step takes some 1.5 us, a part more to join 0.4: twice
-// the root of the steps is best (40 tokens of 32 heads over 8, D = 128, in 4096
-// tokens: 27 us in 32 parts, 22 in 16, 26 in 8; in 1024 16 us in 8, 19 in 4, 25
-// in 2; in 1000 with a bound of 131072 36 us without this limit).
-__device__ __forceinline__ int parts_of(int steps, int most) {
-  return max(1, min((int)(2.f * __builtin_amdgcn_sqrtf((float)steps)), most));
-}
 // steps [u0, u1) of part k of n
 __device__ __forceinline__ void part_steps(int k, int n, int* u0, int* u1) {
   const int each = (*u1 - *u0) / n, more = (*u1 - *u0) - each * n;
@@ -747,36 +793,28 @@ struct Seen {
 
 // A workgroup's place in a prompt launch.
 struct Place {
-  bool group;      // its tile is of a group's rows (kMixed)
   int tile_at, h;  // tile of a head, and that
   int part, most;  // of the tile's steps, and as how many parts the launch has
   uint32_t slot;   // of its results in a.part
 };
 // heads run fastest, so that an XCD (bid % 8) keeps few of them in its L2
 template <int MODE>
-__device__ __forceinline__ Place place_of(AttnArgs& a) {
+__device__ __forceinline__ Place place_of(const AttnArgs& a) {
   Place p;
-  uint32_t bid = blockIdx.x;
-  p.group = MODE == kMixed && bid < a.prefix_wgs;
-  if (MODE == kMixed) {
-    if (!p.group) bid -= a.prefix_wgs;
-    a.kv = either(p.group, a.prefix, a.kv);
-    a.causal = p.group ? 0 : a.causal;
-    a.parts = p.group ? a.parts : 1;
-  }
-  const uint32_t H = (uint32_t)a.kv.H, at = bid / H, parts = (uint32_t)a.parts;
-  p.h = (int)(bid - at * H);
-  p.slot = bid;
-  p.most = a.parts;
-  if (MODE == kBehind && (int)at < a.whole) {
+  const uint32_t H = (uint32_t)a.kv.H, at = blockIdx.x / H, parts = (uint32_t)a.parts;
+  p.h = (int)(blockIdx.x - at * H);
+  const uint32_t whole = MODE == kBehind ? (uint32_t)a.whole : 0u;
+  if (MODE == kBehind && at < whole) {
     p.tile_at = (int)at;
     p.part = 0;
     p.most = 1;
+    p.slot = 0;
   } else {
-    const uint32_t whole = MODE == kBehind ? (uint32_t)a.whole : 0u, cut = at - whole;
-    p.tile_at = (int)(whole + cut / parts);
-    p.part = (int)(cut % parts);
-    p.slot = bid - whole * H;
+    const uint32_t cut = (at - whole) / parts;
+    p.tile_at = (int)(whole + cut);
+    p.part = (int)(at - whole - cut * parts);
+    p.most = a.parts;
+    p.slot = blockIdx.x - whole * H;
   }
   return p;
 }
@@ -791,42 +829,23 @@ struct PromptTile {
   Seen seen;     // by the tile
   int u0, u1;    // steps of 64 tokens that some row sees
   int parts;     // they are cut into
-  // kBehind: tokens and steps of the prefix, its row of the table.  Own token t stands at kUnit * head_steps + t.
-  int head, head_steps;
-  const int32_t* head_table;
+  Head<MODE> head;
 
   // tile number `at` of a head, all sequences in turn, in at most `most` parts; false behind the last
   template <int THREADS>
   __device__ __forceinline__ bool find(const AttnArgs& a, uint32_t at, int most, int64_t* mem) {
-    auto tiles = [&](int64_t i) -> int64_t { return (seq_span<MODE == kMixed>(a.kv, i).n * a.G + ROWS - 1) / ROWS; };
+    auto tiles = [&](int64_t i) -> int64_t { return (seq_span<MODE == kHead>(a.kv, i).n * a.G + ROWS - 1) / ROWS; };
     ItemScan<THREADS, decltype(tiles)> scan(a.kv.n_seqs, tiles, mem);
     if (at >= scan.total) return false;
     int64_t item;
     scan.find(at, &b, &item);
-    s = seq_span<MODE == kMixed>(a.kv, b);
-    head = head_steps = 0;
+    s = seq_span<MODE == kHead>(a.kv, b);
     if constexpr (MODE == kBehind) {
-      // the group that has sequence b: every thread looks at some of them
-      int64_t g = a.prefix.members ? -1 : b / a.prefix.member_count;
-      if (a.prefix.members) {
-        __syncthreads();
-        if (threadIdx.x == 0) mem[0] = -1;
-        __syncthreads();
-        for (int64_t i = threadIdx.x; i < a.prefix.n_seqs; i += THREADS)
-          if (a.prefix.members[i] <= b && b < a.prefix.members[i + 1]) mem[0] = i;
-        __syncthreads();
-        g = uniform64(mem[0]);
-      }
-      if (g >= 0) {
-        const int64_t n = a.prefix.lens[g];
-        head = (int)(n < 0 ? 0 : n < a.prefix.max_kv ? n : a.prefix.max_kv);
-        head_steps = (head + kUnit - 1) / kUnit;
-        head_table = a.prefix.table + g * a.prefix.width;
-      }
+      head.find(a, b);
+      s.len += head.tokens();
     }
     R = s.n * (int)a.G;
     wg0 = (R - 1) / ROWS * ROWS - (int)item * ROWS;  // the last, longest tiles of a sequence first
-    s.len += head_steps * kUnit;
     first = s.len - s.n;
     seen = of_rows(a, wg0, wg0 + ROWS);
     u0 = seen.lo / kUnit;
@@ -834,38 +853,21 @@ struct PromptTile {
     parts = parts_of(u1 - u0, most);
     return true;
   }
-  // tokens before this one are visible to a row at position p
-  __device__ __forceinline__ int sees_to(const AttnArgs& a, int p) const {
-    return a.causal ? max(head_steps * kUnit, min(s.len, p + 1)) : s.len;
-  }
   __device__ __forceinline__ Seen of_rows(const AttnArgs& a, int r0, int r1) const {
     r0 = r0 < R - 1 ? r0 : R - 1;
     r1 = r1 < R ? r1 : R;
     const int p0 = first + (int)((uint32_t)r0 / (uint32_t)a.G), p1 = first + (int)((uint32_t)(r1 - 1) / (uint32_t)a.G);
     Seen v;
-    v.hi = sees_to(a, p1);
-    v.hi_all = sees_to(a, p0);
+    v.hi = max(0, head.sees_to(a.causal, p1, s.len));
+    v.hi_all = max(0, head.sees_to(a.causal, p0, s.len));
     v.lo = a.window > 0 ? max(0, p0 - a.window + 1) : 0;
     v.lo_all = a.window > 0 ? max(0, p1 - a.window + 1) : 0;
     return v;
   }
-  // Step u: the end of its tokens (of the tile's `hi`), the row of the table that has
-  // them, the position of that row's first token.
-  __device__ __forceinline__ int end(int u, int hi) const { return MODE == kBehind && u < head_steps ? head : hi; }
-  __device__ __forceinline__ const int32_t* row(int u, const int32_t* own) const {
-    return MODE == kBehind && u < head_steps ? head_table : own;
-  }
-  __device__ __forceinline__ int origin(int u) const {
-    return MODE == kBehind && u >= head_steps ? head_steps * kUnit : 0;
-  }
-  // some of its tokens are none (kBehind: the end of the prefix)
-  __device__ __forceinline__ bool short_step(int u) const {
-    return MODE == kBehind && u == head_steps - 1 && head < head_steps * kUnit;
-  }
 };
 
 template <int D, int NC, int WAVES, int MODE>
-__global__ __launch_bounds__(64 * WAVES, 2) void attn_prompt(AttnArgs args) {
+__global__ __launch_bounds__(64 * WAVES, 2) void attn_prompt(AttnArgs a) {
   constexpr int DS = D / 32, DT = D / 16, HALF = 32 * WAVES, SP = 4 * D / HALF;
   static_assert(SP * HALF == 4 * D, "whole 16-byte pieces per thread");
   __shared__ __attribute__((aligned(16))) uint8_t k_[2][4 * DS * 1024], v_[2][DT * 2048];
@@ -874,7 +876,6 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attn_prompt(AttnArgs args) {
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n = lane & 15, g = lane >> 4;
   constexpr int ROWS = 16 * NC * WAVES;
-  AttnArgs a = args;
   const Place at_ = place_of<MODE>(a);
   const uint32_t G = (uint32_t)a.G;
   const int h = at_.h, part = at_.part;
@@ -882,6 +883,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attn_prompt(AttnArgs args) {
   PromptTile<ROWS, MODE> t;
   if (!t.template find<64 * WAVES>(a, at_.tile_at, at_.most, scan_) || part >= t.parts) return;
   const SeqSpan s = t.s;
+  const Head<MODE> head = t.head;
   const int R = t.R, wg0 = t.wg0, len = s.len, first = t.first, P = 1 << a.kv.lp, rho0 = wg0 + wave * 16 * NC;
   const int lo_min = t.seen.lo, hi_max = t.seen.hi, lo_all = t.seen.lo_all, hi_all = t.seen.hi_all;
   const Seen mine = t.of_rows(a, rho0, rho0 + 16 * NC);  // by this wave's rows
@@ -895,7 +897,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attn_prompt(AttnArgs args) {
     rho[c] = rho0 + 16 * c + n;
     const uint32_t rc = rho[c] < R ? rho[c] : R - 1, at = rc / G;
     const int p = first + (int)at;
-    vhi[c] = MODE == kBehind ? t.sees_to(a, p) : a.causal ? min(len, p + 1) : len;
+    vhi[c] = head.sees_to(a.causal, p, len);
     vlo[c] = a.window > 0 ? max(0, p - a.window + 1) : 0;
     const uint16_t* qp = a.q + (s.row0 + at) * a.q_stride + ((int64_t)h * G + (rc - at * G)) * D + 16 * g;
 #pragma unroll
@@ -930,10 +932,11 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attn_prompt(AttnArgs args) {
   // their table entry, and the page it names: -1 where there are none, -2 where it
   // is unusable (looked at a step later: looked at when read, it would be waited for)
   auto entry_at = [&](int u) -> int {
-    return t.row(u, table)[(min(u * kUnit + 16 * stage_group, t.end(u, hi_max) - 1) - t.origin(u)) >> a.kv.lp];
+    const int T = u * kUnit;
+    return head.row(T, table)[(min(T + 16 * stage_group, head.end(T, hi_max) - 1) - head.origin(T)) >> a.kv.lp];
   };
   auto page_of = [&](int u, int entry) -> int {
-    return u * kUnit + 16 * stage_group >= t.end(u, hi_max) ? -1 : entry >= 0 && entry < (int)a.kv.n_pages ? entry : -2;
+    return u * kUnit + 16 * stage_group >= head.end(u * kUnit, hi_max) ? -1 : entry >= 0 && entry < (int)a.kv.n_pages ? entry : -2;
   };
   // This thread's 16-byte pieces of a step: of the keys for the first half of
   // the waves (wave t: the rows of tile t, piece i: dims 64 i + 16 g ..), of the
@@ -948,7 +951,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attn_prompt(AttnArgs args) {
   const uint32_t kat = (uint32_t)((tok & (P - 1)) * D + 16 * g);
   const uint32_t vat = (uint32_t)((16 * w4 + n) * P + ((16 * g) & (P - 1)));
   auto fetch = [&](int u, int pg) {
-    const uint32_t in = (u * kUnit - t.origin(u)) & (P - 1);  // the step's place in a larger page
+    const uint32_t in = (u * kUnit - head.origin(u * kUnit)) & (P - 1);  // the step's place in a larger page
     const int64_t ph = (int64_t)(pg < 0 ? 0 : pg) * a.kv.H + h;
     if (keys) {
       const uint8_t* kp = a.kv.kc + (ph << sh) + (kat + in * D);
@@ -964,7 +967,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attn_prompt(AttnArgs args) {
   };
   // tokens some row of the workgroup does not see, or that cannot be read
   auto partial = [&](int u, int pg) {
-    return u * kUnit + kUnit > hi_all || u * kUnit < lo_all || t.short_step(u) || __any(pg < 0);
+    return u * kUnit + kUnit > hi_all || u * kUnit < lo_all || head.gap(u * kUnit) || __any(pg < 0);
   };
   // widened and written to the step's buffer
   auto stage = [&](int u, int pg) {
@@ -982,7 +985,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attn_prompt(AttnArgs args) {
       if (part) {
         // codes of tokens no row sees become 0; NaN codes too, and are put
         // back beside the products for the rows that see them
-        const int T = u * kUnit + 16 * g, lo = pg < 0 ? 16 : lo_min - T, hi = t.end(u, hi_max) - T;
+        const int T = u * kUnit + 16 * g, lo = pg < 0 ? 16 : lo_min - T, hi = head.end(u * kUnit, hi_max) - T;
         uint32_t nans = 0;
 #pragma unroll
         for (int e = 0; e < 4; e++) {
@@ -1044,7 +1047,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attn_prompt(AttnArgs args) {
     if (nan_at_[u & 3] == u) {
       // rare: a NaN code among tokens that not every row of the workgroup sees
       const int T = u * kUnit, vp = __shfl(page_of(u, entry_at(u)), keys ? 4 * g : lane);
-      const uint8_t* vc = a.kv.vc + (((int64_t)(vp < 0 ? 0 : vp) * a.kv.H + h) << sh) + ((T + 16 * g - t.origin(u)) & (P - 1));
+      const uint8_t* vc = a.kv.vc + (((int64_t)(vp < 0 ? 0 : vp) * a.kv.H + h) << sh) + ((T + 16 * g - head.origin(u * kUnit)) & (P - 1));
 #pragma unroll 1
       for (int d = 0; d < DT; d++) {
         const mx_u4 w = *(const mx_u4*)(vc + (int64_t)(16 * d + n) * P);
@@ -1058,7 +1061,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attn_prompt(AttnArgs args) {
 #pragma unroll
           for (int e = 0; e < 16; e++) {
             const int tok = T + 16 * g + e;
-            vis[e >> 3][e & 7] = (__bf16)(tok >= vlo[c] && tok < t.end(u, vhi[c]) ? 1.f : 0.f);
+            vis[e >> 3][e & 7] = (__bf16)(tok >= vlo[c] && tok < head.end(u * kUnit, vhi[c]) ? 1.f : 0.f);
           }
           v4f hit = v4f{0.f, 0.f, 0.f, 0.f};
           hit = mfma(isn[0], vis[0], hit);
@@ -1090,12 +1093,12 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attn_prompt(AttnArgs args) {
   // weights of step u from its scores
   auto softmax = [&](int u, int pg) {
     const int T = u * kUnit;
-    const bool mask = T + kUnit > whi_all || T < wlo_all || t.short_step(u) || __any(pg < 0);
+    const bool mask = T + kUnit > whi_all || T < wlo_all || head.gap(u * kUnit) || __any(pg < 0);
     const int page = mask ? __shfl(pg, keys ? 4 * g : lane) : 0;  // of the lane's 16 tokens
 #pragma unroll
     for (int c = 0; c < NC; c++) {
       if (mask) {
-        const int lo = page < 0 ? 16 : vlo[c] - (T + 16 * g), hi = t.end(u, vhi[c]) - (T + 16 * g);
+        const int lo = page < 0 ? 16 : vlo[c] - (T + 16 * g), hi = head.end(u * kUnit, vhi[c]) - (T + 16 * g);
         const uint32_t up = hi >= 16 ? 0xFFFFu : hi <= 0 ? 0u : (1u << hi) - 1u;
         const uint32_t seen = lo >= 16 ? 0u : lo <= 0 ? up : up & ~((1u << lo) - 1u);
 #pragma unroll
@@ -1168,22 +1171,17 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attn_prompt(AttnArgs args) {
 #pragma unroll
       for (int e = 0; e < 4; e++)
         if ((nanned[c] >> (4 * d + e)) & 1) o[c][d][e] = __uint_as_float(0x7FC00000u);
-    if (at_.group || parts > 1) {
-      float* pp = a.part + ((int64_t)at_.slot * ROWS + (rho[c] - wg0)) * (D + kPartPad);
+    const uint32_t tok = (uint32_t)rho[c] / G;
+    const int64_t row = s.row0 + tok, hd = (int64_t)h * G + (rho[c] - tok * G);
+    if (MODE == kHead || parts > 1) {
+      float* pp = MODE == kHead ? a.sums + ((part * a.kv.total_q + row) * a.Hq + hd) * (D + kPartPad)
+                                : a.part + ((int64_t)at_.slot * ROWS + (rho[c] - wg0)) * (D + kPartPad);
 #pragma unroll
       for (int d = 0; d < DT; d++) *(v4f*)(pp + 16 * d + 4 * g) = o[c][d];
       if (g == 0) *(float2*)(pp + D) = make_float2(m[c], l[c]);
       continue;
     }
     const float inv = l[c] > 0.f || l[c] != l[c] ? 1.0f / l[c] : 0.f;
-    const uint32_t tok = (uint32_t)rho[c] / G;
-    const int64_t row = s.row0 + tok, hd = (int64_t)h * G + (rho[c] - tok * G);
-    if constexpr (MODE == kMixed) {
-      float* sums = a.sums + (row * a.Hq + hd) * (D + kPartPad);
-#pragma unroll
-      for (int d = 0; d < DT; d++) *(v4f*)(sums + 16 * d + 4 * g) = o[c][d];
-      if (g == 0) *(float2*)(sums + D) = make_float2(m[c], l[c]);
-    }
     uint16_t* op = a.o + row * a.o_stride + hd * D + 4 * g;
 #pragma unroll
     for (int d = 0; d < DT; d++) {
@@ -1212,7 +1210,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attn_prompt(AttnArgs args) {
 // four cycles each and the exponentials' quarter rate some 17% more (2 x 4096 in
 // 4096, 32 heads over 8: 226 us).  One register is spilled.
 template <int D, int NC, int WAVES, int OCC, int MODE>
-__global__ __launch_bounds__(64 * WAVES, OCC) void attn_prompt32(AttnArgs args) {
+__global__ __launch_bounds__(64 * WAVES, OCC) void attn_prompt32(AttnArgs a) {
   constexpr int DS = D / 16, DT = D / 32, HALF = 32 * WAVES, SP = 4 * D / HALF, PS = WAVES / 4;
   static_assert(SP * HALF == 4 * D, "whole 16-byte pieces per thread");
   constexpr int KB = 2 * DS * 1024, VB = 4 * DT * 1024;  // bytes of a step's operands
@@ -1224,17 +1222,17 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void attn_prompt32(AttnArgs args) 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n = lane & 31, hf = lane >> 5;
   constexpr int ROWS = 32 * NC * WAVES;
-  AttnArgs a = args;
   const Place at_ = place_of<MODE>(a);
   const uint32_t G = (uint32_t)a.G;
   const int h = at_.h, part = at_.part;
   __shared__ int64_t scan_[WAVES + 2];
-  PromptTile<ROWS, MODE> te;
-  if (!te.template find<64 * WAVES>(a, at_.tile_at, at_.most, scan_) || part >= te.parts) return;
-  const SeqSpan s = te.s;
-  const int R = te.R, wg0 = te.wg0, len = s.len, first = te.first, P = 1 << a.kv.lp, rho0 = wg0 + wave * 32 * NC;
-  const int lo_min = te.seen.lo, hi_max = te.seen.hi, lo_all = te.seen.lo_all, hi_all = te.seen.hi_all;
-  const Seen mine = te.of_rows(a, rho0, rho0 + 32 * NC);  // by this wave's rows
+  PromptTile<ROWS, MODE> t;
+  if (!t.template find<64 * WAVES>(a, at_.tile_at, at_.most, scan_) || part >= t.parts) return;
+  const SeqSpan s = t.s;
+  const Head<MODE> head = t.head;
+  const int R = t.R, wg0 = t.wg0, len = s.len, first = t.first, P = 1 << a.kv.lp, rho0 = wg0 + wave * 32 * NC;
+  const int lo_min = t.seen.lo, hi_max = t.seen.hi, lo_all = t.seen.lo_all, hi_all = t.seen.hi_all;
+  const Seen mine = t.of_rows(a, rho0, rho0 + 32 * NC);  // by this wave's rows
   const int wlo = mine.lo, wlo_all = mine.lo_all, whi_all = mine.hi_all;
   const int whi = __builtin_amdgcn_readfirstlane(rho0 < R ? mine.hi : 0);
   const bool none = a.scale2 == 0.f;  // all scores 0, or NaN
@@ -1245,7 +1243,7 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void attn_prompt32(AttnArgs args) 
     rho[c] = rho0 + 32 * c + n;
     const uint32_t rc = rho[c] < R ? rho[c] : R - 1, at = rc / G;
     const int p = first + (int)at;
-    vhi[c] = MODE == kBehind ? te.sees_to(a, p) : a.causal ? min(len, p + 1) : len;
+    vhi[c] = head.sees_to(a.causal, p, len);
     vlo[c] = a.window > 0 ? max(0, p - a.window + 1) : 0;
     const uint16_t* qp = a.q + (s.row0 + at) * a.q_stride + ((int64_t)h * G + (rc - at * G)) * D + 8 * hf;
 #pragma unroll
@@ -1266,10 +1264,10 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void attn_prompt32(AttnArgs args) 
       for (int e = 0; e < 16; e++) o[c][d][e] = 0.f;
   }
 
-  const int parts = te.parts;
-  int u0 = te.u0, u1 = te.u1;
+  const int parts = t.parts;
+  int u0 = t.u0, u1 = t.u1;
   part_steps(part, parts, &u0, &u1);
-  const int32_t* table = a.kv.table + te.b * a.kv.width;
+  const int32_t* table = a.kv.table + t.b * a.kv.width;
   // This thread's 16-byte pieces of a step.  Keys (first half of the waves,
   // tile w4 % 2): 16 dims 16 (2 (w4 / 2 + 2 i) + h) .. of the token of row n.
   // Values (second half): 16 tokens of dim 32 (w4 / 2 + 2 i) + n, tokens
@@ -1280,10 +1278,11 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void attn_prompt32(AttnArgs args) 
   // their table entry, and the page it names: -1 where there are none, -2 where it
   // is unusable (looked at a step later: looked at when read, it would be waited for)
   auto entry_at = [&](int u) -> int {
-    return te.row(u, table)[(min(u * kUnit + 16 * stage_group, te.end(u, hi_max) - 1) - te.origin(u)) >> a.kv.lp];
+    const int T = u * kUnit;
+    return head.row(T, table)[(min(T + 16 * stage_group, head.end(T, hi_max) - 1) - head.origin(T)) >> a.kv.lp];
   };
   auto page_of = [&](int u, int entry) -> int {
-    return u * kUnit + 16 * stage_group >= te.end(u, hi_max) ? -1 : entry >= 0 && entry < (int)a.kv.n_pages ? entry : -2;
+    return u * kUnit + 16 * stage_group >= head.end(u * kUnit, hi_max) ? -1 : entry >= 0 && entry < (int)a.kv.n_pages ? entry : -2;
   };
   mx_u4 raw[SP];
   uint32_t eb = 0;
@@ -1292,7 +1291,7 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void attn_prompt32(AttnArgs args) 
   const uint32_t kat = (uint32_t)((tok & (P - 1)) * D + 32 * (w4 >> 1) + 16 * hf);
   const uint32_t vat = (uint32_t)((32 * (w4 >> 1) + n) * P + ((16 * stage_group) & (P - 1)));
   auto fetch = [&](int u, int pg) {
-    const uint32_t in = (u * kUnit - te.origin(u)) & (P - 1);  // the step's place in a larger page
+    const uint32_t in = (u * kUnit - head.origin(u * kUnit)) & (P - 1);  // the step's place in a larger page
     const int64_t ph = (int64_t)(pg < 0 ? 0 : pg) * a.kv.H + h;
     if (keys) {
       const uint8_t* kp = a.kv.kc + (ph << sh) + (kat + in * D);
@@ -1308,7 +1307,7 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void attn_prompt32(AttnArgs args) 
   };
   // tokens some row of the workgroup does not see, or that cannot be read
   auto partial = [&](int u, int pg) {
-    return u * kUnit + kUnit > hi_all || u * kUnit < lo_all || te.short_step(u) || __any(pg < 0);
+    return u * kUnit + kUnit > hi_all || u * kUnit < lo_all || head.gap(u * kUnit) || __any(pg < 0);
   };
   // widened and written to the step's buffer
   auto stage = [&](int u, int pg) {
@@ -1327,7 +1326,7 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void attn_prompt32(AttnArgs args) 
       if (part) {
         // codes of tokens no row sees become 0; NaN codes too, and are put
         // back beside the products for the rows that see them
-        const int T = u * kUnit + 16 * stage_group, lo = pg < 0 ? 16 : lo_min - T, hi = te.end(u, hi_max) - T;
+        const int T = u * kUnit + 16 * stage_group, lo = pg < 0 ? 16 : lo_min - T, hi = head.end(u * kUnit, hi_max) - T;
         uint32_t nans = 0;
 #pragma unroll
         for (int e = 0; e < 4; e++) {
@@ -1414,9 +1413,9 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void attn_prompt32(AttnArgs args) 
 #pragma unroll 1
     for (int t = 0; t < 2; t++) {
       const int T = u * kUnit + 32 * t + 16 * hf;
-      int pg = T < te.end(u, hi_max) ? te.row(u, table)[(T - te.origin(u)) >> a.kv.lp] : -1;
+      int pg = T < head.end(u * kUnit, hi_max) ? head.row(u * kUnit, table)[(T - head.origin(u * kUnit)) >> a.kv.lp] : -1;
       pg = pg >= 0 && pg < a.kv.n_pages ? pg : -1;
-      const uint8_t* vc = a.kv.vc + (((int64_t)(pg < 0 ? 0 : pg) * a.kv.H + h) << sh) + ((T - te.origin(u)) & (P - 1));
+      const uint8_t* vc = a.kv.vc + (((int64_t)(pg < 0 ? 0 : pg) * a.kv.H + h) << sh) + ((T - head.origin(u * kUnit)) & (P - 1));
 #pragma unroll 1
       for (int d = 0; d < DT; d++) {
         const mx_u4 w = *(const mx_u4*)(vc + (int64_t)(32 * d + n) * P);
@@ -1429,7 +1428,7 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void attn_prompt32(AttnArgs args) 
           v8bf vis[2];
 #pragma unroll
           for (int e = 0; e < 16; e++)
-            vis[e >> 3][e & 7] = (__bf16)(T + e >= vlo[c] && T + e < te.end(u, vhi[c]) ? 1.f : 0.f);
+            vis[e >> 3][e & 7] = (__bf16)(T + e >= vlo[c] && T + e < head.end(u * kUnit, vhi[c]) ? 1.f : 0.f);
           v16f hit;
 #pragma unroll
           for (int e = 0; e < 16; e++) hit[e] = 0.f;
@@ -1444,14 +1443,14 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void attn_prompt32(AttnArgs args) 
   // weights of step u from its scores
   auto softmax = [&](int u) {
     const int T = u * kUnit;
-    bool mask = T + kUnit > whi_all || T < wlo_all || te.short_step(u);
+    bool mask = T + kUnit > whi_all || T < wlo_all || head.gap(u * kUnit);
     int unread = 0;  // tiles whose 16 tokens of the lane cannot be read
     if (bad_at_[u & 3] == u) {
       mask = true;
 #pragma unroll
       for (int t = 0; t < 2; t++) {
         const int at = T + 32 * t + 16 * hf;
-        const int pg = at < te.end(u, hi_max) ? te.row(u, table)[(at - te.origin(u)) >> a.kv.lp] : -1;
+        const int pg = at < head.end(u * kUnit, hi_max) ? head.row(u * kUnit, table)[(at - head.origin(u * kUnit)) >> a.kv.lp] : -1;
         unread |= pg >= 0 && pg < a.kv.n_pages ? 0 : 1 << t;
       }
     }
@@ -1461,7 +1460,7 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void attn_prompt32(AttnArgs args) 
 #pragma unroll
         for (int t = 0; t < 2; t++) {
           const int at = T + 32 * t + 16 * hf;
-          const int lo = (unread >> t) & 1 ? 16 : vlo[c] - at, hi = te.end(u, vhi[c]) - at;
+          const int lo = (unread >> t) & 1 ? 16 : vlo[c] - at, hi = head.end(u * kUnit, vhi[c]) - at;
           const uint32_t up = hi >= 16 ? 0xFFFFu : hi <= 0 ? 0u : (1u << hi) - 1u;
           const uint32_t seen = lo >= 16 ? 0u : lo <= 0 ? up : up & ~((1u << lo) - 1u);
 #pragma unroll
@@ -1536,25 +1535,26 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void attn_prompt32(AttnArgs args) 
     pg1 = page_of(u + 2, e2);
     if (keys || u < u1) meet();
   }
-  // sums of row c to where they are joined
-  auto write_sums = [&](int c, float* pp) {
-#pragma unroll
-    for (int d = 0; d < DT; d++)
-#pragma unroll
-      for (int x = 0; x < 4; x++) {
-        v4f y;
-#pragma unroll
-        for (int e = 0; e < 4; e++)
-          y[e] = (nanned[c] >> (16 * d + 4 * x + e)) & 1 ? __uint_as_float(0x7FC00000u) : o[c][d][4 * x + e];
-        *(v4f*)(pp + 32 * d + 8 * x + 4 * hf) = y;
-      }
-    if (hf == 0) *(float2*)(pp + D) = make_float2(m[c], l[c]);
-  };
-  if (at_.group || parts > 1) {
+  if (MODE == kHead || parts > 1) {
 #pragma unroll
     for (int c = 0; c < NC; c++) {
       l[c] += __shfl_xor(l[c], 32);
-      if (rho[c] < R) write_sums(c, a.part + ((int64_t)at_.slot * ROWS + (rho[c] - wg0)) * (D + kPartPad));
+      if (rho[c] >= R) continue;
+      const uint32_t at = (uint32_t)rho[c] / G;
+      float* pp = MODE == kHead
+                      ? a.sums + ((part * a.kv.total_q + s.row0 + at) * a.Hq + (int64_t)h * G + (rho[c] - at * G)) * (D + kPartPad)
+                      : a.part + ((int64_t)at_.slot * ROWS + (rho[c] - wg0)) * (D + kPartPad);
+#pragma unroll
+      for (int d = 0; d < DT; d++)
+#pragma unroll
+        for (int x = 0; x < 4; x++) {
+          v4f y;
+#pragma unroll
+          for (int e = 0; e < 4; e++)
+            y[e] = (nanned[c] >> (16 * d + 4 * x + e)) & 1 ? __uint_as_float(0x7FC00000u) : o[c][d][4 * x + e];
+          *(v4f*)(pp + 32 * d + 8 * x + 4 * hf) = y;
+        }
+      if (hf == 0) *(float2*)(pp + D) = make_float2(m[c], l[c]);
     }
     return;
   }
@@ -1564,11 +1564,6 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void attn_prompt32(AttnArgs args) 
 #pragma unroll
   for (int c = 0; c < NC; c++) {
     l[c] += __shfl_xor(l[c], 32);
-    if constexpr (MODE == kMixed) {
-      const uint32_t at = (uint32_t)rho[c] / G;
-      if (rho[c] < R)
-        write_sums(c, a.sums + ((s.row0 + at) * a.Hq + (int64_t)h * G + (rho[c] - at * G)) * (D + kPartPad));
-    }
     const float inv = l[c] > 0.f || l[c] != l[c] ? 1.0f / l[c] : 0.f;
 #pragma unroll
     for (int d = 0; d < DT; d++)
@@ -1644,63 +1639,6 @@ __global__ __launch_bounds__(256) void attn_join(AttnArgs a) {
   }
   const uint32_t rc = t.wg0 + r, tok = rc / G;
   const int64_t row = t.s.row0 + tok, hd = (int64_t)h * G + (rc - tok * G);
-  const float inv = L > 0.f || L != L ? 1.0f / L : 0.f;
-  uint2 w;
-  w.x = bf16_bits(o[0] * inv) | (bf16_bits(o[1] * inv) << 16);
-  w.y = bf16_bits(o[2] * inv) | (bf16_bits(o[3] * inv) << 16);
-  *(uint2*)(a.o + row * a.o_stride + hd * D + d) = w;
-  if (a.lse && d == 0) a.lse[row * a.Hq + hd] = L == 0.f ? -INFINITY : (M + __builtin_amdgcn_logf(L)) * kLn2;
-}
-
-// A row behind a shared prefix: its sums over its own tokens and over the prefix
-// (a.prefix_sums, or its tile's parts where that is NULL), joined as attn_join
-// does.  The tiles are those of the groups' rows (a.kv), so rows without a prefix
-// keep what was written for their own tokens.
-template <int D, int ROWS>
-__global__ __launch_bounds__(256) void attn_merge(AttnArgs a) {
-  constexpr int T4 = D / 4, AHEAD = 16;
-  const uint32_t G = (uint32_t)a.G, H = (uint32_t)a.kv.H, tile_at = blockIdx.x / H, h = blockIdx.x - tile_at * H;
-  __shared__ int64_t scan_[256 / 64 + 2];
-  PromptTile<ROWS, kMixed> t;
-  if (!t.template find<256>(a, tile_at, a.parts, scan_)) return;
-  const int at = blockIdx.y * 256 + threadIdx.x, r = at / T4, d = at % T4 * 4;
-  if (t.wg0 + r >= t.R) return;
-  const uint32_t rc = t.wg0 + r, tok = rc / G;
-  const int64_t row = t.s.row0 + tok, hd = (int64_t)h * G + (rc - tok * G);
-  const float* own = a.sums + (row * a.Hq + hd) * (D + kPartPad);
-  const int64_t step = (int64_t)H * ROWS * (D + kPartPad);  // to the next part
-  const float* p = a.prefix_sums ? a.prefix_sums + (row * a.Hq + hd) * (D + kPartPad)
-                                 : a.part + (((int64_t)tile_at * a.parts * H + h) * ROWS + r) * (D + kPartPad);
-  const int parts = a.prefix_sums ? 1 : t.parts;
-  v4f o = *(const v4f*)(own + d);
-  const float2 own_ml = *(const float2*)(own + D);
-  float M = own_ml.x, L = own_ml.y;
-  for (int k = 0; k < parts; k += AHEAD) {
-    v4f po[AHEAD];
-    float2 ml[AHEAD];
-#pragma unroll
-    for (int e = 0; e < AHEAD; e++) {
-      const float* q = p + min(k + e, parts - 1) * step;
-      po[e] = *(const v4f*)(q + d);
-      ml[e] = *(const float2*)(q + D);
-    }
-    float mx = M;
-#pragma unroll
-    for (int e = 0; e < AHEAD; e++) mx = fmaxf(mx, ml[e].x);
-    const float mu = mx == -INFINITY ? 0.f : mx, al = __builtin_amdgcn_exp2f(M - mu);
-    M = mx;
-    L *= al;
-#pragma unroll
-    for (int c = 0; c < 4; c++) o[c] *= al;
-#pragma unroll
-    for (int e = 0; e < AHEAD; e++) {
-      if (k + e >= parts) break;
-      const float w = __builtin_amdgcn_exp2f(ml[e].x - mu);
-      L += w * ml[e].y;
-#pragma unroll
-      for (int c = 0; c < 4; c++) o[c] += w * po[e][c];
-    }
-  }
   const float inv = L > 0.f || L != L ? 1.0f / L : 0.f;
   uint2 w;
   w.x = bf16_bits(o[0] * inv) | (bf16_bits(o[1] * inv) << 16);
@@ -1799,66 +1737,77 @@ int64_t tiles_of(const KvArgs& kv, int64_t G, int64_t rows) {
 }
 int best_parts(int64_t steps) { return (int)std::max<int64_t>((int64_t)(2.0 * sqrt((double)steps)), 1); }
 
-// Of a call behind shared prefixes.
+// Of a call behind shared prefixes: one launch (kBehind), or the groups' and the
+// sequences' (kHead, kTail).
 struct PrefixPlan {
   Mode mode;
+  // kBehind: of the launch; else of the groups'.  nc 0: prompt tiles of `rows` rows in
+  // `parts` parts, the first `whole` of a head uncut.
   int nc, rows, parts, whole;
-  int64_t tiles;                 // kBehind: of the sequences' rows; kMixed, kUnion: of the groups'
-  int64_t blocks, prefix_wgs;    // of the launch; kMixed: the first of them
-  size_t sums, prefix_sums, part;  // bytes
+  int64_t blocks;
+  int64_t cut;                    // tiles of all heads that are in parts
+  int tail_nc, tail_whole;        // of the sequences'
+  int64_t tail_blocks;
+  size_t sums, part;              // bytes
 };
 PrefixPlan plan_prefix(const AttnArgs& a) {
   const KvArgs &kv = a.kv, &prefix = a.prefix;
   const int64_t Rs = kv.max_q * a.G, Rg = prefix.max_q * a.G, row_bytes = (kv.D + kPartPad) * 4;
+  const int64_t steps = cdiv(prefix.max_kv, kUnit) + cdiv(kv.max_kv, kUnit);
+  auto decode_nc = [&](int64_t R) { return R > 16 && kv.D == 64 ? 2 : 1; };
+  auto decode_part = [&](int nc) { return (size_t)4 * kMaxShares * 16 * nc * (kv.D + 2) * 4; };
+  const int64_t shares = kv.D == 256 ? kMaxShares / 2 : kMaxShares;
   PrefixPlan p = {};
   p.parts = 1;
-  p.sums = (size_t)(kv.total_q * a.Hq * row_bytes);
   if (Rs > 64) {
     p.mode = kBehind;
     p.rows = prompt_rows(kv.D, Rs);
-    p.tiles = tiles_of(kv, a.G, p.rows);
-    const int64_t slots = prompt_slots(kv.D, Rs);
-    const int64_t cut = p.tiles % slots ? cdiv(p.tiles % slots, kv.H) : 0;  // tiles of a head behind the last full round
-    p.whole = (int)(p.tiles / kv.H - cut);
-    p.parts = (int)std::min<int64_t>(cut ? std::max<int64_t>(slots / (cut * kv.H), 1) : 1,
-                                     best_parts(cdiv(prefix.max_kv, kUnit) + cdiv(kv.max_kv, kUnit)));
-    if (p.parts == 1) p.whole = (int)(p.tiles / kv.H);
-    p.blocks = p.whole * kv.H + (p.tiles - p.whole * kv.H) * p.parts;
-    p.sums = 0;
-    p.part = (size_t)((p.blocks - p.whole * kv.H) * p.rows * row_bytes);
+    const int64_t tiles = tiles_of(kv, a.G, p.rows), slots = prompt_slots(kv.D, Rs);
+    const int64_t cut = tiles % slots ? cdiv(tiles % slots, kv.H) : 0;  // tiles of a head behind the last full round
+    if (cut) p.parts = (int)std::min<int64_t>(std::max<int64_t>(slots / (cut * kv.H), 1), best_parts(steps));
+    p.whole = (int)(tiles / kv.H - (p.parts > 1 ? cut : 0));
+    p.cut = tiles - p.whole * kv.H;
+    p.blocks = p.whole * kv.H + p.cut * p.parts;
+    p.part = (size_t)(p.cut * p.parts * p.rows * row_bytes);
     return p;
   }
-  if (!many_rows(prefix, Rg)) {
-    p.mode = kUnion;
-    p.nc = std::max(Rs, Rg) > 16 && kv.D == 64 ? 2 : 1;
-    p.blocks = kv.D == 256 ? kMaxShares / 2 : kMaxShares;
-    p.rows = 128;
-    p.tiles = tiles_of(prefix, a.G, p.rows);
-    p.prefix_sums = p.sums;
-    p.part = (size_t)4 * kMaxShares * 16 * p.nc * (kv.D + 2) * 4;
+  p.tail_nc = decode_nc(Rs);
+  const int64_t tail_tiles = tiles_of(kv, a.G, 16 * p.tail_nc);
+  if (tail_tiles * cdiv(steps, kDecWaves) <= shares) {
+    p.mode = kBehind;
+    p.nc = p.tail_nc;
+    p.blocks = shares;
+    p.part = decode_part(p.nc);
     return p;
   }
-  p.mode = kMixed;
-  p.rows = prompt_rows(kv.D, Rg > 512 ? Rg : 128);
-  p.tiles = tiles_of(prefix, a.G, p.rows);
-  const int64_t own = tiles_of(kv, a.G, p.rows), slots = prompt_slots(kv.D, p.rows), best = best_parts(cdiv(prefix.max_kv, kUnit));
-  const int64_t room = std::max(slots - own, slots / 2);
-  if (p.tiles <= room) {
-    p.parts = (int)std::min(room / p.tiles, best);
-  } else {
-    // as many parts as leave the least of the last round idle
-    double least = 1e30;
-    for (int64_t k = 1; k <= std::min<int64_t>(4, best); k++) {
-      const double t = (double)cdiv(p.tiles * k, slots) / k + 0.03 * k;
-      if (t < least) {
-        least = t;
-        p.parts = (int)k;
+  p.mode = kHead;
+  p.tail_whole = tail_tiles >= shares / 2;
+  p.tail_blocks = p.tail_whole ? tail_tiles : shares;
+  if (!p.tail_whole) p.part = decode_part(p.tail_nc);
+  if (many_rows(prefix, Rg)) {
+    p.rows = prompt_rows(kv.D, Rg > 512 ? Rg : 128);
+    const int64_t tiles = tiles_of(prefix, a.G, p.rows), slots = prompt_slots(kv.D, p.rows);
+    const int64_t best = best_parts(cdiv(prefix.max_kv, kUnit));
+    if (tiles <= slots) {
+      p.parts = (int)std::min(slots / tiles, best);
+    } else {
+      // as many parts as leave the least of the last round idle
+      double least = 1e30;
+      for (int64_t k = 1; k <= std::min<int64_t>(4, best); k++) {
+        const double t = (double)cdiv(tiles * k, slots) / k + 0.03 * k;
+        if (t < least) {
+          least = t;
+          p.parts = (int)k;
+        }
       }
     }
+    p.blocks = tiles * p.parts;
+  } else {
+    p.nc = decode_nc(Rg);
+    p.blocks = shares;
+    p.part = std::max(p.part, decode_part(p.nc));
   }
-  p.prefix_wgs = p.tiles * p.parts;
-  p.blocks = p.prefix_wgs + own;
-  p.part = (size_t)(p.prefix_wgs * p.rows * row_bytes);
+  p.sums = (size_t)(p.parts * kv.total_q * a.Hq * row_bytes);
   return p;
 }
 
@@ -1889,12 +1838,12 @@ hipError_t launch_attention(AttnArgs a, void* ws, hipStream_t s) {
 
 bool attention_prefix_fits(const AttnArgs& a) {
   const PrefixPlan p = plan_prefix(a);
-  return p.blocks <= (1 << 22) && p.tiles <= (1 << 22);
+  return p.blocks <= (1 << 22) && p.tail_blocks <= (1 << 22);
 }
 
 size_t attention_prefix_workspace_bytes(const AttnArgs& a) {
   const PrefixPlan p = plan_prefix(a);
-  return (size_t)kCounterBytes + p.sums + p.prefix_sums + p.part;
+  return (size_t)kCounterBytes + p.sums + p.part;
 }
 
 hipError_t launch_attention_prefix(AttnArgs a, void* ws, hipStream_t s) {
@@ -1902,25 +1851,25 @@ hipError_t launch_attention_prefix(AttnArgs a, void* ws, hipStream_t s) {
   uint8_t* at = (uint8_t*)ws + kCounterBytes;
   a.cnt = (uint32_t*)ws + 16;
   a.sums = (float*)at;
-  a.prefix_sums = p.prefix_sums ? (float*)(at + p.sums) : nullptr;
-  a.part = (float*)(at + p.sums + p.prefix_sums);
-  a.parts = p.parts;
+  a.part = (float*)(at + p.sums);
+  a.parts = a.sums_parts = p.parts;
   a.whole = p.whole;
-  a.prefix_wgs = (uint32_t)p.prefix_wgs;
   if (p.mode == kBehind) {
-    launch_prompt<kBehind>(p.rows, (unsigned)p.blocks, a, s);
-    if (p.parts > 1) launch_join<kBehind>(p.rows, p.tiles - p.whole * a.kv.H, a, s);
+    if (p.nc > 0) {
+      launch_decode<kBehind>(p.nc, (unsigned)p.blocks, a, s);
+    } else {
+      launch_prompt<kBehind>(p.rows, (unsigned)p.blocks, a, s);
+      if (p.parts > 1) launch_join<kBehind>(p.rows, p.cut, a, s);
+    }
     return hipGetLastError();
   }
-  if (p.mode == kUnion) launch_decode<kUnion>(p.nc, (unsigned)p.blocks, a, s);
-  else launch_prompt<kMixed>(p.rows, (unsigned)p.blocks, a, s);
-  a.kv = a.prefix;
-  a.causal = 0;
-  const dim3 grid((unsigned)p.tiles, (unsigned)(p.rows * a.kv.D / 4 / 256));
-  if (a.kv.D == 64) hipLaunchKernelGGL((attn_merge<64, 128>), grid, dim3(256), 0, s, a);
-  else if (a.kv.D == 128 && p.rows == 128) hipLaunchKernelGGL((attn_merge<128, 128>), grid, dim3(256), 0, s, a);
-  else if (a.kv.D == 128) hipLaunchKernelGGL((attn_merge<128, 256>), grid, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((attn_merge<256, 128>), grid, dim3(256), 0, s, a);
+  AttnArgs head = a;
+  head.kv = a.prefix;
+  head.causal = 0;
+  if (p.nc > 0) launch_decode<kHead>(p.nc, (unsigned)p.blocks, head, s);
+  else launch_prompt<kHead>(p.rows, (unsigned)p.blocks, head, s);
+  a.whole = p.tail_whole;
+  launch_decode<kTail>(p.tail_nc, (unsigned)p.tail_blocks, a, s);
   return hipGetLastError();
 }
 

@@ -120,6 +120,17 @@ struct CompactArgs {
   int* n_moves;
 };
 
+// The group that sequence b belongs to, -1: none.
+__device__ __forceinline__ int64_t group_of(const KvArgs& groups, int64_t b) {
+  if (!groups.members) return b / groups.member_count;
+  int64_t lo = 0, hi = groups.n_seqs;  // members[lo] <= b < members[hi] where b has a group
+  while (hi - lo > 1) {
+    const int64_t mid = (lo + hi) / 2;
+    (groups.members[mid] <= b ? lo : hi) = mid;
+  }
+  return groups.members[lo] <= b && b < groups.members[lo + 1] ? lo : -1;
+}
+
 struct AttnArgs {
   KvArgs kv;
   int64_t Hq, G;
@@ -134,10 +145,9 @@ struct AttnArgs {
   int parts;                 // of a prompt tile
   // behind shared prefixes
   KvArgs prefix;             // their groups
-  float* sums;               // [total_q][Hq] sums of a row over its own tokens, before the division
-  float* prefix_sums;        // and over its prefix, where that is not in parts
-  uint32_t prefix_wgs;       // workgroups of the prefixes' tiles
-  int whole;                 // tiles of a head whose steps are not cut into parts
+  float* sums;               // [parts][total_q][Hq] sums of the rows over their prefixes, before the division
+  int sums_parts;            // as how many parts at most
+  int whole;                 // prompts: tiles of a head whose steps are not cut; else: a workgroup has a whole tile
   uint32_t* cnt;             // arrivals: of a group (by the place of its first share), then of a tile
 };
 
