@@ -103,20 +103,43 @@ __device__ __forceinline__ int64_t quot(int64_t a, int64_t b) {
   return a / b;
 }
 
+// The first 64 groups, one a lane, read before the sequence is known.
+struct FirstGroups {
+  int first = 0, last = 0, len = 0;
+  __device__ __forceinline__ void read(const KvArgs& groups) {
+    const int64_t i = threadIdx.x & 63;
+    if (groups.n_seqs > 64 || i >= groups.n_seqs) return;
+    first = groups.members ? groups.members[i] : (int)(i * groups.member_count);
+    last = groups.members ? groups.members[i + 1] : (int)((i + 1) * groups.member_count);
+    len = groups.lens[i];
+  }
+};
+
 // The tokens of a sequence's shared prefix (kBehind; else none).  Positions count
 // them first, in whole steps: own token t stands at kUnit * steps + t.
 template <int MODE>
 struct Head {
   int len = 0, steps = 0;
   const int32_t* table = nullptr;
-  __device__ __forceinline__ void find(const AttnArgs& a, int64_t b) {
-    len = steps = 0;
-    const int64_t g = group_of(a.prefix, b);
-    if (g < 0) return;
-    const int64_t n = a.prefix.lens[g];
+  __device__ __forceinline__ void take(const AttnArgs& a, int64_t g, int64_t n) {
     len = (int)(n < 0 ? 0 : n < a.prefix.max_kv ? n : a.prefix.max_kv);
     steps = (len + kUnit - 1) / kUnit;
     table = a.prefix.table + g * a.prefix.width;
+  }
+  // of sequence b, each lane's own
+  __device__ __forceinline__ void find(const AttnArgs& a, int64_t b) {
+    len = steps = 0;
+    const int64_t g = group_of(a.prefix, b);
+    if (g >= 0) take(a, g, a.prefix.lens[g]);
+  }
+  // of the same sequence for all lanes
+  __device__ __forceinline__ void find(const AttnArgs& a, int64_t b, const FirstGroups& groups) {
+    if (a.prefix.n_seqs > 64) return find(a, b);
+    len = steps = 0;
+    const uint64_t has = __ballot(groups.first <= b && b < groups.last);
+    if (!has) return;
+    const int g = __builtin_ctzll(has);
+    take(a, g, __builtin_amdgcn_readlane(groups.len, g));
   }
   __device__ __forceinline__ int tokens() const { return MODE == kBehind ? steps * kUnit : 0; }
   __device__ __forceinline__ bool has(int t) const { return MODE == kBehind && t < steps * kUnit; }
@@ -254,6 +277,8 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 15, g = lane >> 4;
   const int P = 1 << a.kv.lp;
+  FirstGroups groups;
+  if constexpr (MODE == kBehind || MODE == kTail) groups.read(a.prefix);
   auto span_of = [&](int64_t i) -> SeqSpan {
     SeqSpan t = seq_span<MODE == kHead>(a.kv, i);
     if constexpr (MODE == kBehind) {
@@ -270,11 +295,12 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
     return max((most + kBlock - 1) / kBlock, (int64_t)1);
   };
   auto tiles_of = [&](const SeqSpan& t) -> int64_t { return (t.n * a.G + 16 * NC - 1) / (16 * NC); };
-  // many tiles of few blocks: a workgroup has one, so that none has to be joined
-  const bool whole = MODE == kTail && a.whole;
+  // kTail: a tile is cut into so many pieces at most, one workgroup each (equal shares
+  // of all blocks would often have the end of one tile and the start of the next)
+  const int64_t pieces = MODE == kTail ? a.pieces : 0;
   auto work_of = [&](int64_t i) -> int64_t {
     const SeqSpan t = span_of(i);
-    return tiles_of(t) * (whole ? 1 : blocks_of(t));
+    return tiles_of(t) * (MODE == kTail ? pieces : blocks_of(t));
   };
   ItemScan<64 * kDecWaves, decltype(work_of)> scan(a.kv.n_seqs, work_of, scan_);
   const int64_t per_head = scan.total, total = per_head * a.kv.H;
@@ -283,7 +309,7 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
   const int64_t shares = max(min(total, (int64_t)gridDim.x), (int64_t)1);
   // neighbouring shares on one XCD (bid % 8) where every workgroup has one
   const int64_t per_xcd = gridDim.x / 8, bid = blockIdx.x;
-  const int64_t share = shares == (int64_t)gridDim.x && !whole ? (bid % 8) * per_xcd + bid / 8 : bid;
+  const int64_t share = shares == (int64_t)gridDim.x && MODE != kTail ? (bid % 8) * per_xcd + bid / 8 : bid;
   if (share >= shares) return;
   int64_t x = quot(total * share, shares);
   const int64_t x_end = quot(total * (share + 1), shares);
@@ -292,21 +318,30 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
   int64_t b, item;
   scan.find(x - h * per_head, &b, &item);
   SeqSpan s = span_of(b);
-  int64_t blocks = whole ? 1 : blocks_of(s), tiles = tiles_of(s);
-  int64_t rt = quot(item, blocks);
-  int at = (int)(item - rt * blocks);  // first block of this share in the tile
+  int64_t blocks = blocks_of(s), tiles = tiles_of(s);
+  int64_t rt = quot(item, MODE == kTail ? pieces : blocks);
+  int at = (int)(item - rt * (MODE == kTail ? pieces : blocks));  // first block of this share in the tile
   for (;;) {
-    const int64_t x0 = x - at;     // the tile's first block among all
-    const int count = (int)min(blocks - at, x_end - x);
-    // shares that hold blocks of this tile
-    const int64_t share0 = quot((x0 + 1) * shares + total - 1, total) - 1;
-    const int64_t share1 = quot((x0 + blocks) * shares + total - 1, total) - 1;
-    const int n_parts = (int)(share1 - share0 + 1);
+    int count, n_parts;
+    int64_t share0;  // the first share that holds blocks of this tile
+    if constexpr (MODE == kTail) {
+      n_parts = (int)min(pieces, blocks);
+      share0 = share - at;
+      if (at >= n_parts) return;
+      const int first_block = (int)(blocks * at / n_parts);
+      count = (int)(blocks * (at + 1) / n_parts) - first_block;
+      at = first_block;
+    } else {
+      const int64_t x0 = x - at;  // the tile's first block among all
+      count = (int)min(blocks - at, x_end - x);
+      share0 = quot((x0 + 1) * shares + total - 1, total) - 1;
+      n_parts = (int)(quot((x0 + blocks) * shares + total - 1, total) - 1 - share0 + 1);
+    }
     const int64_t R = (int64_t)s.n * a.G;
     const int64_t rho0 = rt * 16 * NC;
     const int len = s.len, first = len - s.n;  // position of the first new token
     Head<MODE> head;
-    if constexpr (MODE == kBehind || MODE == kTail) head.find(a, b);
+    if constexpr (MODE == kBehind || MODE == kTail) head.find(a, b, groups);
 
     // visible tokens of this lane's rows: [vlo, vhi)
     int vlo[NC], vhi[NC];
@@ -332,8 +367,7 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
       vhi[c] = head.sees_to(a.causal, p, len);
       vlo[c] = a.window > 0 ? max(0, p - a.window + 1) : 0;
     }
-    const int u0 = lo_min / kUnit + kDecWaves * at, u_end = (hi_max + kUnit - 1) / kUnit;
-    const int u1 = whole ? u_end : min(u0 + kDecWaves * count, u_end);
+    const int u0 = lo_min / kUnit + kDecWaves * at, u1 = min(u0 + kDecWaves * count, (hi_max + kUnit - 1) / kUnit);
 
     // Q: lane (n, g) holds dims 64 c + 16 g + 8 e .. + 7 of its row
     v8bf qf[NC][DC][2];
@@ -536,25 +570,48 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
     }
 
     if constexpr (MODE == kTail) {
-      // the sums over the prefix, its parts for the waves in turn (the tile's first share takes them in)
+      // The sums over the prefix, its parts for the waves in turn (the tile's first
+      // share takes them in), kTake of them on their way at once (D = 256: the registers
+      // hold no more).
+      constexpr int kTake = D == 256 ? 1 : 4;
       const int parts = share == share0 && head.len > 0 ? parts_of(head.steps, a.sums_parts) : 0;
-      for (int k = wave; k < parts; k += kDecWaves) {
 #pragma unroll
-        for (int c = 0; c < NC; c++) {
-          const int64_t rc = rho[c] < R ? rho[c] : R - 1;
-          const float* sums = a.sums + ((k * a.kv.total_q + s.row0 + rc / a.G) * a.Hq + h * a.G + rc % a.G) * (D + kPartPad);
-          const float2 ml = *(const float2*)(sums + D);
-          v4f v[DT];
+      for (int c = 0; c < NC; c++) {
+        const int64_t rc = rho[c] < R ? rho[c] : R - 1;
+        const float* sums = a.sums + ((s.row0 + rc / a.G) * a.Hq + h * a.G + rc % a.G) * (D + kPartPad);
+        const int64_t next = a.kv.total_q * a.Hq * (D + kPartPad);  // part
+        for (int k = wave; k < parts; k += kDecWaves * kTake) {
+          float2 ml[kTake];
+          v4f v[kTake][DT];
 #pragma unroll
-          for (int d = 0; d < DT; d++) v[d] = *(const v4f*)(sums + 16 * d + 4 * g);
-          const float mn = fmaxf(m[c], ml.x), mu = mn == -INFINITY ? 0.f : mn;
-          const float al = __builtin_amdgcn_exp2f(m[c] - mu), w = __builtin_amdgcn_exp2f(ml.x - mu);
+          for (int i = 0; i < kTake; i++) {
+            const bool is = k + i * kDecWaves < parts;
+            const float* from = sums + (is ? k + i * kDecWaves : k) * next;
+            ml[i] = *(const float2*)(from + D);
+            ml[i].x = is ? ml[i].x : -INFINITY;
+#pragma unroll
+            for (int d = 0; d < DT; d++) v[i][d] = *(const v4f*)(from + 16 * d + 4 * g);
+          }
+          float mn = m[c];
+#pragma unroll
+          for (int i = 0; i < kTake; i++) mn = fmaxf(mn, ml[i].x);
+          const float mu = mn == -INFINITY ? 0.f : mn, al = __builtin_amdgcn_exp2f(m[c] - mu);
           m[c] = mn;
-          l[c] = l[c] * al + (g == 0 ? w * ml.y : 0.f);  // the lanes of a row are added below
+          l[c] *= al;
 #pragma unroll
           for (int d = 0; d < DT; d++)
 #pragma unroll
-            for (int e = 0; e < 4; e++) o[c][d][e] = o[c][d][e] * al + w * v[d][e];
+            for (int e = 0; e < 4; e++) o[c][d][e] *= al;
+#pragma unroll
+          for (int i = 0; i < kTake; i++) {
+            if (k + i * kDecWaves >= parts) break;
+            const float w = __builtin_amdgcn_exp2f(ml[i].x - mu);
+            l[c] += g == 0 ? w * ml[i].y : 0.f;  // the lanes of a row are added below
+#pragma unroll
+            for (int d = 0; d < DT; d++)
+#pragma unroll
+              for (int e = 0; e < 4; e++) o[c][d][e] += w * v[i][d][e];
+          }
         }
       }
     }
@@ -752,7 +809,7 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
       }
     }
     // ---- the share's next tile
-    x += count;
+    x += MODE == kTail ? 1 : count;  // a share is one piece
     if (x >= x_end) return;
     __syncthreads();  // the LDS is free again
     at = 0;
@@ -766,7 +823,7 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
         s = span_of(b);
         tiles = tiles_of(s);
       } while (tiles == 0);  // some sequence has tiles, as x < total
-      blocks = whole ? 1 : blocks_of(s);
+      blocks = blocks_of(s);
     }
   }
 }
@@ -834,6 +891,8 @@ struct PromptTile {
   // tile number `at` of a head, all sequences in turn, in at most `most` parts; false behind the last
   template <int THREADS>
   __device__ __forceinline__ bool find(const AttnArgs& a, uint32_t at, int most, int64_t* mem) {
+    FirstGroups groups;
+    if constexpr (MODE == kBehind) groups.read(a.prefix);
     auto tiles = [&](int64_t i) -> int64_t { return (seq_span<MODE == kHead>(a.kv, i).n * a.G + ROWS - 1) / ROWS; };
     ItemScan<THREADS, decltype(tiles)> scan(a.kv.n_seqs, tiles, mem);
     if (at >= scan.total) return false;
@@ -841,7 +900,7 @@ struct PromptTile {
     scan.find(at, &b, &item);
     s = seq_span<MODE == kHead>(a.kv, b);
     if constexpr (MODE == kBehind) {
-      head.find(a, b);
+      head.find(a, b, groups);
       s.len += head.tokens();
     }
     R = s.n * (int)a.G;
@@ -1746,7 +1805,7 @@ struct PrefixPlan {
   int nc, rows, parts, whole;
   int64_t blocks;
   int64_t cut;                    // tiles of all heads that are in parts
-  int tail_nc, tail_whole;        // of the sequences'
+  int tail_nc, tail_pieces;       // of the sequences'
   int64_t tail_blocks;
   size_t sums, part;              // bytes
 };
@@ -1762,11 +1821,24 @@ PrefixPlan plan_prefix(const AttnArgs& a) {
   if (Rs > 64) {
     p.mode = kBehind;
     p.rows = prompt_rows(kv.D, Rs);
-    const int64_t tiles = tiles_of(kv, a.G, p.rows), slots = prompt_slots(kv.D, Rs);
-    const int64_t cut = tiles % slots ? cdiv(tiles % slots, kv.H) : 0;  // tiles of a head behind the last full round
-    if (cut) p.parts = (int)std::min<int64_t>(std::max<int64_t>(slots / (cut * kv.H), 1), best_parts(steps));
-    p.whole = (int)(tiles / kv.H - (p.parts > 1 ? cut : 0));
-    p.cut = tiles - p.whole * kv.H;
+    const int64_t slots = prompt_slots(kv.D, Rs), most = tiles_of(kv, a.G, p.rows);
+    // tiles to be expected: each sequence's last one half full
+    const int64_t tiles = std::min(most, kv.H * (kv.total_q * a.G / p.rows + (kv.n_seqs + 1) / 2));
+    p.whole = (int)(tiles / slots * slots / kv.H);
+    const int64_t cut = tiles - p.whole * kv.H;  // behind the last full round
+    // as many parts of those as take the least time (us): steps of 2, 6 for a workgroup's
+    // start and end, the sums written and read at 4.8 TB/s
+    double least = 1e30;
+    for (int64_t k = 1; k <= std::min<int64_t>(best_parts(steps), 64) && (k == 1 || cut * k <= 4 * slots); k++) {
+      const double t = (double)cdiv(cut * k, slots) * (2. * (double)steps / (double)k + 6.) +
+                       (k > 1 ? 3. + (double)(cut * k * p.rows * row_bytes) * 2. / 4.8e6 : 0.);
+      if (t < least) {
+        least = t;
+        p.parts = (int)k;
+      }
+    }
+    if (p.parts == 1) p.whole = (int)(most / kv.H);
+    p.cut = most - p.whole * kv.H;
     p.blocks = p.whole * kv.H + p.cut * p.parts;
     p.part = (size_t)(p.cut * p.parts * p.rows * row_bytes);
     return p;
@@ -1781,9 +1853,10 @@ PrefixPlan plan_prefix(const AttnArgs& a) {
     return p;
   }
   p.mode = kHead;
-  p.tail_whole = tail_tiles >= shares / 2;
-  p.tail_blocks = p.tail_whole ? tail_tiles : shares;
-  if (!p.tail_whole) p.part = decode_part(p.tail_nc);
+  // as many pieces of a tile as fill the chip
+  p.tail_pieces = (int)std::max<int64_t>(std::min(shares / tail_tiles, cdiv(kv.max_kv, kBlock)), 1);
+  p.tail_blocks = tail_tiles * p.tail_pieces;
+  if (p.tail_pieces > 1) p.part = decode_part(p.tail_nc);
   if (many_rows(prefix, Rg)) {
     p.rows = prompt_rows(kv.D, Rg > 512 ? Rg : 128);
     const int64_t tiles = tiles_of(prefix, a.G, p.rows), slots = prompt_slots(kv.D, p.rows);
@@ -1868,7 +1941,7 @@ hipError_t launch_attention_prefix(AttnArgs a, void* ws, hipStream_t s) {
   head.causal = 0;
   if (p.nc > 0) launch_decode<kHead>(p.nc, (unsigned)p.blocks, head, s);
   else launch_prompt<kHead>(p.rows, (unsigned)p.blocks, head, s);
-  a.whole = p.tail_whole;
+  a.pieces = p.tail_pieces;
   launch_decode<kTail>(p.tail_nc, (unsigned)p.tail_blocks, a, s);
   return hipGetLastError();
 }

@@ -147,7 +147,8 @@ struct AttnArgs {
   KvArgs prefix;             // their groups
   float* sums;               // [parts][total_q][Hq] sums of the rows over their prefixes, before the division
   int sums_parts;            // as how many parts at most
-  int whole;                 // prompts: tiles of a head whose steps are not cut; else: a workgroup has a whole tile
+  int whole;                 // tiles of a head whose steps are not cut into parts
+  int pieces;                // of a sequence's tile, a workgroup each
   uint32_t* cnt;             // arrivals: of a group (by the place of its first share), then of a tile
 };
 
