@@ -1809,79 +1809,110 @@ struct PrefixPlan {
   int64_t tail_blocks;
   size_t sums, part;              // bytes
 };
+
+// us of a prompt workgroup over some steps where so many are at work at once
+double wg_time(int D, int64_t rows, int64_t wgs, double steps) {
+  const bool crowded = wgs > 256;
+  const double step = D == 64 ? (crowded ? 2.1 : 1.5) : D == 256 ? 2.0 : rows == 256 ? 1.8 : crowded ? 2.4 : 1.6;
+  return step * steps + (D == 256 ? 10. : 6.);
+}
+// tiles cut into the parts that take the least time; `sums`: us to write and read one
+// part of each, `join`: us that joining takes beside that
+double cut_time(int D, int64_t rows, int64_t tiles, int64_t steps, double sums, double join, int* parts) {
+  double least = 1e30;
+  const int64_t slots = prompt_slots(D, rows);
+  for (int64_t k = 1; k <= best_parts(steps) && (k == 1 || tiles * k <= 4 * slots); k++) {
+    const double t = (double)cdiv(tiles * k, slots) * wg_time(D, rows, std::min(tiles * k, slots), (double)steps / (double)k) +
+                     (k > 1 || join == 0. ? sums * (double)k + join : 0.);
+    if (t < least) {
+      least = t;
+      *parts = (int)k;
+    }
+  }
+  return least;
+}
+// us of attn_decode for tiles of so many rows and blocks
+double decode_time(int D, int64_t rows, int64_t tiles, int64_t blocks) {
+  const double shares = D == 256 ? kMaxShares / 2 : kMaxShares, x = (double)(tiles * blocks) / shares;
+  const double parts = std::min(shares / (double)tiles, (double)blocks);  // of a tile, to be joined
+  const double join = parts > 1. ? 0.08 * (double)std::min<int64_t>(rows, D == 64 ? 32 : 16) * sqrt(parts) : 0.;
+  const double work = D == 256 ? 18. + 3.3 * x : D == 128 ? 13. + 3. * x : rows > 16 ? 18. + 2.8 * x : 11. + 1.9 * x;
+  return work + join;
+}
+
+// The three ways by their expected times.  us, measured, single tokens of 32 heads
+// over 8 behind one prefix (D = 256: 24 over 4), in one attn_decode / in two launches:
+//   D = 64   8 sequences behind 8000 20 / 24, 16 27 / 26, 32 42 / 30, 8 behind 32000 43 / 38
+//   D = 128  4 behind 1000 15 / 21, 8 behind 8000 27 / 31, 16 39 / 33, 32 63 / 38, 8 behind 32000 62 / 43
+//   D = 256  8 behind 8000 32 / 42, 16 45 / 50, 32 70 / 52, 8 behind 32000 72 / 57
+// and more rows of each of 32 sequences behind 16000 / 2000, D = 128, in one prompt launch / in two:
+//   32 rows 292 / 81 and 63 / 44, 64 rows 292 / 124 and 56 / 60, 128 rows 311 / 215 and 69 / 79.
 PrefixPlan plan_prefix(const AttnArgs& a) {
   const KvArgs &kv = a.kv, &prefix = a.prefix;
-  const int64_t Rs = kv.max_q * a.G, Rg = prefix.max_q * a.G, row_bytes = (kv.D + kPartPad) * 4;
-  const int64_t steps = cdiv(prefix.max_kv, kUnit) + cdiv(kv.max_kv, kUnit);
-  auto decode_nc = [&](int64_t R) { return R > 16 && kv.D == 64 ? 2 : 1; };
-  auto decode_part = [&](int nc) { return (size_t)4 * kMaxShares * 16 * nc * (kv.D + 2) * 4; };
-  const int64_t shares = kv.D == 256 ? kMaxShares / 2 : kMaxShares;
-  PrefixPlan p = {};
-  p.parts = 1;
-  if (Rs > 64) {
-    p.mode = kBehind;
-    p.rows = prompt_rows(kv.D, Rs);
-    const int64_t slots = prompt_slots(kv.D, Rs), most = tiles_of(kv, a.G, p.rows);
-    // tiles to be expected: each sequence's last one half full
-    const int64_t tiles = std::min(most, kv.H * (kv.total_q * a.G / p.rows + (kv.n_seqs + 1) / 2));
-    p.whole = (int)(tiles / slots * slots / kv.H);
-    const int64_t cut = tiles - p.whole * kv.H;  // behind the last full round
-    // as many parts of those as take the least time (us): steps of 2, 6 for a workgroup's
-    // start and end, the sums written and read at 4.8 TB/s
-    double least = 1e30;
-    for (int64_t k = 1; k <= std::min<int64_t>(best_parts(steps), 64) && (k == 1 || cut * k <= 4 * slots); k++) {
-      const double t = (double)cdiv(cut * k, slots) * (2. * (double)steps / (double)k + 6.) +
-                       (k > 1 ? 3. + (double)(cut * k * p.rows * row_bytes) * 2. / 4.8e6 : 0.);
-      if (t < least) {
-        least = t;
-        p.parts = (int)k;
-      }
-    }
-    if (p.parts == 1) p.whole = (int)(most / kv.H);
-    p.cut = most - p.whole * kv.H;
-    p.blocks = p.whole * kv.H + p.cut * p.parts;
-    p.part = (size_t)(p.cut * p.parts * p.rows * row_bytes);
-    return p;
-  }
-  p.tail_nc = decode_nc(Rs);
-  const int64_t tail_tiles = tiles_of(kv, a.G, 16 * p.tail_nc);
-  if (tail_tiles * cdiv(steps, kDecWaves) <= shares) {
-    p.mode = kBehind;
-    p.nc = p.tail_nc;
-    p.blocks = shares;
-    p.part = decode_part(p.nc);
-    return p;
-  }
-  p.mode = kHead;
+  const int D = kv.D;
+  const int64_t Rs = kv.max_q * a.G, Rg = prefix.max_q * a.G, row_bytes = (D + kPartPad) * 4;
+  const int64_t head_steps = cdiv(prefix.max_kv, kUnit), own_steps = cdiv(kv.max_kv, kUnit), steps = head_steps + own_steps;
+  constexpr double kRate = 4.8e6;  // bytes a us
+  auto decode_nc = [&](int64_t R) { return R > 16 && D == 64 ? 2 : 1; };
+  auto decode_part = [&](int nc) { return (size_t)4 * kMaxShares * 16 * nc * (D + 2) * 4; };
+  const int64_t shares = D == 256 ? kMaxShares / 2 : kMaxShares;
+
+  // tiles of the sequences' rows, all steps
+  PrefixPlan one = {};
+  one.mode = kBehind;
+  one.rows = prompt_rows(D, Rs);
+  const int64_t slots = prompt_slots(D, Rs), most = tiles_of(kv, a.G, one.rows);
+  // tiles to be expected: each sequence's last one half full
+  const int64_t tiles = std::min(most, kv.H * (kv.total_q * a.G / one.rows + (kv.n_seqs + 1) / 2));
+  one.whole = (int)(tiles / slots * slots / kv.H);
+  const int64_t rest = tiles - one.whole * kv.H;  // behind the last full round
+  one.parts = 1;
+  double one_time = (double)(one.whole * kv.H) / (double)slots * wg_time(D, one.rows, slots, (double)steps);
+  if (rest) one_time += cut_time(D, one.rows, rest, steps, (double)(rest * one.rows * row_bytes) * 2. / kRate, 4., &one.parts);
+  if (one.parts == 1) one.whole = (int)(most / kv.H);
+  one.cut = most - one.whole * kv.H;
+  one.blocks = one.whole * kv.H + one.cut * one.parts;
+  one.part = (size_t)(one.cut * one.parts * one.rows * row_bytes);
+
+  // the same in attn_decode
+  const int nc = decode_nc(Rs);
+  const int64_t few_tiles = tiles_of(kv, a.G, 16 * nc);
+  const double few_time = decode_time(D, Rs, few_tiles, cdiv(steps, kDecWaves));
+
+  // groups, then sequences
+  PrefixPlan two = {};
+  two.mode = kHead;
+  two.parts = 1;
+  two.tail_nc = nc;
   // as many pieces of a tile as fill the chip
-  p.tail_pieces = (int)std::max<int64_t>(std::min(shares / tail_tiles, cdiv(kv.max_kv, kBlock)), 1);
-  p.tail_blocks = tail_tiles * p.tail_pieces;
-  if (p.tail_pieces > 1) p.part = decode_part(p.tail_nc);
+  two.tail_pieces = (int)std::max<int64_t>(std::min(shares / few_tiles, cdiv(kv.max_kv, kBlock)), 1);
+  two.tail_blocks = few_tiles * two.tail_pieces;
+  if (two.tail_pieces > 1) two.part = decode_part(nc);
+  double two_time = 4. + decode_time(D, Rs, few_tiles, cdiv(own_steps, kDecWaves));
   if (many_rows(prefix, Rg)) {
-    p.rows = prompt_rows(kv.D, Rg > 512 ? Rg : 128);
-    const int64_t tiles = tiles_of(prefix, a.G, p.rows), slots = prompt_slots(kv.D, p.rows);
-    const int64_t best = best_parts(cdiv(prefix.max_kv, kUnit));
-    if (tiles <= slots) {
-      p.parts = (int)std::min(slots / tiles, best);
-    } else {
-      // as many parts as leave the least of the last round idle
-      double least = 1e30;
-      for (int64_t k = 1; k <= std::min<int64_t>(4, best); k++) {
-        const double t = (double)cdiv(tiles * k, slots) / k + 0.03 * k;
-        if (t < least) {
-          least = t;
-          p.parts = (int)k;
-        }
-      }
-    }
-    p.blocks = tiles * p.parts;
+    // 256 rows a tile where that is not a fifth more of them than in tiles of 128
+    two.rows = prompt_rows(D, cdiv(Rg, 256) * 256 * 5 < cdiv(Rg, 128) * 128 * 6 ? Rg : 128);
+    const int64_t group_tiles = tiles_of(prefix, a.G, two.rows);
+    two_time += cut_time(D, two.rows, group_tiles, head_steps, (double)(kv.total_q * a.Hq * row_bytes) * 2. / kRate, 0., &two.parts);
+    two.blocks = group_tiles * two.parts;
   } else {
-    p.nc = decode_nc(Rg);
-    p.blocks = shares;
-    p.part = std::max(p.part, decode_part(p.nc));
+    two.nc = decode_nc(Rg);
+    two.blocks = shares;
+    two.part = std::max(two.part, decode_part(two.nc));
+    two_time += decode_time(D, Rg, tiles_of(prefix, a.G, 16 * two.nc), cdiv(head_steps, kDecWaves));
   }
-  p.sums = (size_t)(p.parts * kv.total_q * a.Hq * row_bytes);
-  return p;
+  two.sums = (size_t)(two.parts * kv.total_q * a.Hq * row_bytes);
+
+  if (few_time <= std::min(one_time, two_time)) {
+    PrefixPlan few = {};
+    few.mode = kBehind;
+    few.nc = nc;
+    few.parts = 1;
+    few.blocks = shares;
+    few.part = decode_part(nc);
+    return few;
+  }
+  return one_time <= two_time ? one : two;
 }
 
 }  // namespace
