@@ -159,11 +159,12 @@ def run_compact(caches, P, table, lens, refs, width, what):
 def test_compact_many():
     """Several chunks of pages, the border inside one and at its edge."""
     rng = np.random.default_rng(5)
-    for n_pages, L in ((20000, 9000), (16384, 8192), (4097, 4096), (4096, 4096), (12289, 1)):
+    for n_pages, L in ((20000, 9000), (16384, 8192), (4097, 4096), (4096, 4096), (12289, 1), (30720, 20001), (30721, 16000),
+                       (40960, 8192), (36865, 36864), (45000, 0)):
         refs = np.zeros(n_pages, int)
         refs[rng.permutation(n_pages)[:L]] = rng.integers(1, 5, L)
         use = np.nonzero(refs)[0]
-        table = [[int(x) for x in rng.choice(use, 1500)] for _ in range(3)]
+        table = [[int(x) for x in rng.choice(use, 1500)] if L else [7] * 1500 for _ in range(3)]
         print(f"compact {n_pages} {L}", flush=True)
         run_compact([cache_of(n_pages, 16, 1, 64, 1)], 16, table, [1500 * 16, 1499 * 16, 5], refs.tolist(), 1500, f"{n_pages} {L}")
 
