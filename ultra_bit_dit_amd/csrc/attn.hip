@@ -570,23 +570,22 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
     }
 
     if constexpr (MODE == kTail) {
-      // The sums over the prefix, its parts for the waves in turn (the tile's first
-      // share takes them in), kTake of them on their way at once (D = 256: the registers
-      // hold no more).
-      constexpr int kTake = D == 256 ? 1 : 4;
-      const int parts = share == share0 && head.len > 0 ? parts_of(head.steps, a.sums_parts) : 0;
+      // The sums over the prefix: its parts for the waves of the tile's pieces in turn,
+      // kTake of them on their way at once.
+      constexpr int kTake = 4;
+      const int parts = head.len > 0 ? parts_of(head.steps, a.sums_parts) : 0, takers = kDecWaves * n_parts;
 #pragma unroll
       for (int c = 0; c < NC; c++) {
         const int64_t rc = rho[c] < R ? rho[c] : R - 1;
         const float* sums = a.sums + ((s.row0 + rc / a.G) * a.Hq + h * a.G + rc % a.G) * (D + kPartPad);
         const int64_t next = a.kv.total_q * a.Hq * (D + kPartPad);  // part
-        for (int k = wave; k < parts; k += kDecWaves * kTake) {
+        for (int k = (int)(share - share0) * kDecWaves + wave; k < parts; k += takers * kTake) {
           float2 ml[kTake];
           v4f v[kTake][DT];
 #pragma unroll
           for (int i = 0; i < kTake; i++) {
-            const bool is = k + i * kDecWaves < parts;
-            const float* from = sums + (is ? k + i * kDecWaves : k) * next;
+            const bool is = k + i * takers < parts;
+            const float* from = sums + (is ? k + i * takers : k) * next;
             ml[i] = *(const float2*)(from + D);
             ml[i].x = is ? ml[i].x : -INFINITY;
 #pragma unroll
@@ -604,7 +603,7 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
             for (int e = 0; e < 4; e++) o[c][d][e] *= al;
 #pragma unroll
           for (int i = 0; i < kTake; i++) {
-            if (k + i * kDecWaves >= parts) break;
+            if (k + i * takers >= parts) break;
             const float w = __builtin_amdgcn_exp2f(ml[i].x - mu);
             l[c] += g == 0 ? w * ml[i].y : 0.f;  // the lanes of a row are added below
 #pragma unroll
