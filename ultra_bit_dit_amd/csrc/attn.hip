@@ -103,12 +103,12 @@ __device__ __forceinline__ int64_t quot(int64_t a, int64_t b) {
   return a / b;
 }
 
-// The first 64 groups, one a lane, read before the sequence is known.
+// Up to 16 groups, one a lane, read before the sequences are known.
 struct FirstGroups {
   int first = 0, last = 0, len = 0;
   __device__ __forceinline__ void read(const KvArgs& groups) {
     const int64_t i = threadIdx.x & 63;
-    if (groups.n_seqs > 64 || i >= groups.n_seqs) return;
+    if (groups.n_seqs > 16 || i >= groups.n_seqs) return;
     first = groups.members ? groups.members[i] : (int)(i * groups.member_count);
     last = groups.members ? groups.members[i + 1] : (int)((i + 1) * groups.member_count);
     len = groups.lens[i];
@@ -121,25 +121,25 @@ template <int MODE>
 struct Head {
   int len = 0, steps = 0;
   const int32_t* table = nullptr;
+  int64_t group = -1;
   __device__ __forceinline__ void take(const AttnArgs& a, int64_t g, int64_t n) {
-    len = (int)(n < 0 ? 0 : n < a.prefix.max_kv ? n : a.prefix.max_kv);
+    group = g;
+    len = g < 0 ? 0 : (int)(n < 0 ? 0 : n < a.prefix.max_kv ? n : a.prefix.max_kv);
     steps = (len + kUnit - 1) / kUnit;
-    table = a.prefix.table + g * a.prefix.width;
+    table = a.prefix.table + (g < 0 ? 0 : g) * a.prefix.width;
   }
-  // of sequence b, each lane's own
+  // of sequence b
   __device__ __forceinline__ void find(const AttnArgs& a, int64_t b) {
-    len = steps = 0;
     const int64_t g = group_of(a.prefix, b);
-    if (g >= 0) take(a, g, a.prefix.lens[g]);
+    take(a, g, g < 0 ? 0 : a.prefix.lens[g]);
   }
-  // of the same sequence for all lanes
+  // the same, each lane's own b, where the groups may be at hand
   __device__ __forceinline__ void find(const AttnArgs& a, int64_t b, const FirstGroups& groups) {
-    if (a.prefix.n_seqs > 64) return find(a, b);
-    len = steps = 0;
-    const uint64_t has = __ballot(groups.first <= b && b < groups.last);
-    if (!has) return;
-    const int g = __builtin_ctzll(has);
-    take(a, g, __builtin_amdgcn_readlane(groups.len, g));
+    if (a.prefix.n_seqs > 16) return find(a, b);
+    take(a, -1, 0);
+    for (int g = (int)a.prefix.n_seqs - 1; g >= 0; g--)
+      if (__builtin_amdgcn_readlane(groups.first, g) <= b && b < __builtin_amdgcn_readlane(groups.last, g))
+        take(a, g, __builtin_amdgcn_readlane(groups.len, g));
   }
   __device__ __forceinline__ int tokens() const { return MODE == kBehind ? steps * kUnit : 0; }
   __device__ __forceinline__ bool has(int t) const { return MODE == kBehind && t < steps * kUnit; }
@@ -277,15 +277,35 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 15, g = lane >> 4;
   const int P = 1 << a.kv.lp;
-  FirstGroups groups;
-  if constexpr (MODE == kBehind || MODE == kTail) groups.read(a.prefix);
-  auto span_of = [&](int64_t i) -> SeqSpan {
+  auto span_of = [&](int64_t i, Head<MODE>* head) -> SeqSpan {
     SeqSpan t = seq_span<MODE == kHead>(a.kv, i);
-    if constexpr (MODE == kBehind) {
-      Head<MODE> head;
-      head.find(a, i);
-      t.len += head.tokens();
+    if constexpr (MODE == kBehind || MODE == kTail) {
+      head->find(a, i);
+      t.len += head->tokens();
     }
+    return t;
+  };
+  // a batch of at most 64 (not kPlain): read once, sequence b in lane b
+  const bool near = MODE != kPlain && a.kv.n_seqs <= 64;
+  SeqSpan mine = {0, 0, 0};
+  Head<MODE> my_head;
+  if (near) {
+    FirstGroups groups;
+    if constexpr (MODE == kBehind || MODE == kTail) groups.read(a.prefix);
+    if (lane < a.kv.n_seqs) {
+      mine = seq_span<MODE == kHead>(a.kv, lane);
+      if constexpr (MODE == kBehind || MODE == kTail) my_head.find(a, lane, groups);
+      mine.len += my_head.tokens();
+    }
+  }
+  auto span_for_all = [&](int64_t i, Head<MODE>* head) -> SeqSpan {
+    if (!near) return span_of(i, head);
+    SeqSpan t;
+    t.row0 = uniform64(__shfl((long long)mine.row0, (int)i));
+    t.n = __builtin_amdgcn_readlane(mine.n, (int)i);
+    t.len = __builtin_amdgcn_readlane(mine.len, (int)i);
+    if constexpr (MODE == kBehind || MODE == kTail)
+      head->take(a, __builtin_amdgcn_readlane((int)my_head.group, (int)i), __builtin_amdgcn_readlane(my_head.len, (int)i));
     return t;
   };
   // blocks of one tile of a sequence (at least one, which writes its rows), and its tiles
@@ -299,7 +319,8 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
   // of all blocks would often have the end of one tile and the start of the next)
   const int64_t pieces = MODE == kTail ? a.pieces : 0;
   auto work_of = [&](int64_t i) -> int64_t {
-    const SeqSpan t = span_of(i);
+    Head<MODE> head;
+    const SeqSpan t = near ? mine : span_of(i, &head);  // near: i is the lane
     return tiles_of(t) * (MODE == kTail ? pieces : blocks_of(t));
   };
   ItemScan<64 * kDecWaves, decltype(work_of)> scan(a.kv.n_seqs, work_of, scan_);
@@ -317,7 +338,8 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
   int h = (int)quot(x, per_head);
   int64_t b, item;
   scan.find(x - h * per_head, &b, &item);
-  SeqSpan s = span_of(b);
+  Head<MODE> head;
+  SeqSpan s = span_for_all(b, &head);
   int64_t blocks = blocks_of(s), tiles = tiles_of(s);
   int64_t rt = quot(item, MODE == kTail ? pieces : blocks);
   int at = (int)(item - rt * (MODE == kTail ? pieces : blocks));  // first block of this share in the tile
@@ -340,8 +362,6 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
     const int64_t R = (int64_t)s.n * a.G;
     const int64_t rho0 = rt * 16 * NC;
     const int len = s.len, first = len - s.n;  // position of the first new token
-    Head<MODE> head;
-    if constexpr (MODE == kBehind || MODE == kTail) head.find(a, b, groups);
 
     // visible tokens of this lane's rows: [vlo, vhi)
     int vlo[NC], vhi[NC];
@@ -819,7 +839,7 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
           b = 0;
           h++;
         }
-        s = span_of(b);
+        s = span_for_all(b, &head);
         tiles = tiles_of(s);
       } while (tiles == 0);  // some sequence has tiles, as x < total
       blocks = blocks_of(s);
@@ -890,8 +910,6 @@ struct PromptTile {
   // tile number `at` of a head, all sequences in turn, in at most `most` parts; false behind the last
   template <int THREADS>
   __device__ __forceinline__ bool find(const AttnArgs& a, uint32_t at, int most, int64_t* mem) {
-    FirstGroups groups;
-    if constexpr (MODE == kBehind) groups.read(a.prefix);
     auto tiles = [&](int64_t i) -> int64_t { return (seq_span<MODE == kHead>(a.kv, i).n * a.G + ROWS - 1) / ROWS; };
     ItemScan<THREADS, decltype(tiles)> scan(a.kv.n_seqs, tiles, mem);
     if (at >= scan.total) return false;
@@ -899,7 +917,7 @@ struct PromptTile {
     scan.find(at, &b, &item);
     s = seq_span<MODE == kHead>(a.kv, b);
     if constexpr (MODE == kBehind) {
-      head.find(a, b, groups);
+      head.find(a, b);
       s.len += head.tokens();
     }
     R = s.n * (int)a.G;
