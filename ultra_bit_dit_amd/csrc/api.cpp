@@ -682,7 +682,7 @@ namespace {
 
 // checks of what a call behind shared prefixes has in common with its workspace query
 int prefix_check(const lowbit_kv8* cache, const lowbit_kv8_prefix* p, const lowbit_kv8_batch* batch, int64_t q_heads,
-                 AttnArgs* a) {
+                 AttnArgs* a, PrefixPlan* plan) {
   KvArgs* const out = &a->prefix;
   if (!p) return LOWBIT_E_NULL;
   const int rc = kv8_check(cache, batch, &a->kv);
@@ -712,7 +712,8 @@ int prefix_check(const lowbit_kv8* cache, const lowbit_kv8_prefix* p, const lowb
   if (a->kv.total_q * q_heads > (int64_t(1) << 38) / (a->kv.D + 4)) return LOWBIT_E_SHAPE;
   a->Hq = q_heads;
   a->G = q_heads / a->kv.H;
-  return attention_prefix_fits(*a) ? LOWBIT_OK : LOWBIT_E_SHAPE;
+  *plan = plan_prefix(*a);
+  return plan->blocks <= (1 << 22) ? LOWBIT_OK : LOWBIT_E_SHAPE;
 }
 
 }  // namespace
@@ -722,9 +723,10 @@ int lowbit_attention_kv8_prefix_workspace(const lowbit_kv8* cache, const lowbit_
   if (!bytes) return LOWBIT_E_NULL;
   *bytes = 0;
   AttnArgs a = {};
-  const int rc = prefix_check(cache, prefix, batch, q_heads, &a);
+  PrefixPlan plan;
+  const int rc = prefix_check(cache, prefix, batch, q_heads, &a, &plan);
   if (rc) return rc;
-  *bytes = attention_prefix_workspace_bytes(a);
+  *bytes = attention_prefix_workspace_bytes(plan);
   return LOWBIT_OK;
 }
 
@@ -734,7 +736,8 @@ int lowbit_attention_kv8_prefix(const lowbit_kv8* cache, const lowbit_kv8_prefix
                                 int64_t o_stride, float* lse, void* stream) {
   if (!Q_bf16 || !O_bf16) return LOWBIT_E_NULL;
   AttnArgs a = {};
-  const int rc = prefix_check(cache, prefix, batch, q_heads, &a);
+  PrefixPlan plan;
+  const int rc = prefix_check(cache, prefix, batch, q_heads, &a, &plan);
   if (rc) return rc;
   const int64_t row = q_heads * a.kv.D, most = int64_t(1) << 40;
   if (q_stride < row || o_stride < row || q_stride > most || o_stride > most) return LOWBIT_E_SHAPE;
@@ -750,9 +753,9 @@ int lowbit_attention_kv8_prefix(const lowbit_kv8* cache, const lowbit_kv8_prefix
   a.o_stride = o_stride;
   a.lse = lse;
   void* ws = nullptr;
-  const int r2 = workspace((hipStream_t)stream, attention_prefix_workspace_bytes(a), &ws);
+  const int r2 = workspace((hipStream_t)stream, attention_prefix_workspace_bytes(plan), &ws);
   if (r2) return r2;
-  return hip_status(launch_attention_prefix(a, ws, (hipStream_t)stream));
+  return hip_status(launch_attention_prefix(a, plan, ws, (hipStream_t)stream));
 }
 
 // ------------------------------------------- heads of queries and keys; pages

@@ -1813,33 +1813,25 @@ int64_t tiles_of(const KvArgs& kv, int64_t G, int64_t rows) {
 }
 int best_parts(int64_t steps) { return (int)std::max<int64_t>((int64_t)(2.0 * sqrt((double)steps)), 1); }
 
-// Of a call behind shared prefixes: one launch (kBehind), or the groups' and the
-// sequences' (kHead, kTail).
-struct PrefixPlan {
-  Mode mode;
-  // kBehind: of the launch; else of the groups'.  nc 0: prompt tiles of `rows` rows in
-  // `parts` parts, the first `whole` of a head uncut.
-  int nc, rows, parts, whole;
-  int64_t blocks;
-  int64_t cut;                    // tiles of all heads that are in parts
-  int tail_nc, tail_pieces;       // of the sequences'
-  int64_t tail_blocks;
-  size_t sums, part;              // bytes
-};
-
-// us of a prompt workgroup over some steps where so many are at work at once
-double wg_time(int D, int64_t rows, int64_t wgs, double steps) {
+// us of a prompt workgroup over some steps, `wgs` of them at work at once, `fill` of
+// its rows used
+double wg_time(int D, int64_t rows, double fill, int64_t wgs, double steps) {
   const bool crowded = wgs > 256;
-  const double step = D == 64 ? (crowded ? 2.1 : 1.5) : D == 256 ? 2.0 : rows == 256 ? 1.8 : crowded ? 2.4 : 1.6;
+  const double step = D == 64     ? (crowded ? 1.4 + 0.8 * fill : 1.3 + 0.2 * fill)
+                      : D == 256  ? 1.6 + 1.1 * fill
+                      : rows == 256 ? 1.4 + 0.45 * fill
+                      : crowded   ? 1.5 + 0.9 * fill
+                                  : 1.4 + 0.2 * fill;
   return step * steps + (D == 256 ? 10. : 6.);
 }
-// tiles cut into the parts that take the least time; `sums`: us to write and read one
-// part of each, `join`: us that joining takes beside that
-double cut_time(int D, int64_t rows, int64_t tiles, int64_t steps, double sums, double join, int* parts) {
+// tiles (of at most `most`, for which there is to be room) cut into the parts that take
+// the least time; `sums`: us to write and read one part of each, `join`: us that
+// joining takes beside that
+double cut_time(int D, int64_t rows, double fill, int64_t tiles, int64_t most, int64_t steps, double sums, double join, int* parts) {
   double least = 1e30;
   const int64_t slots = prompt_slots(D, rows);
-  for (int64_t k = 1; k <= best_parts(steps) && (k == 1 || tiles * k <= 4 * slots); k++) {
-    const double t = (double)cdiv(tiles * k, slots) * wg_time(D, rows, std::min(tiles * k, slots), (double)steps / (double)k) +
+  for (int64_t k = 1; k <= best_parts(steps) && (k == 1 || most * k <= 4 * slots); k++) {
+    const double t = (double)cdiv(tiles * k, slots) * wg_time(D, rows, fill, std::min(tiles * k, slots), (double)steps / (double)k) +
                      (k > 1 || join == 0. ? sums * (double)k + join : 0.);
     if (t < least) {
       least = t;
@@ -1864,7 +1856,8 @@ double decode_time(int D, int64_t rows, int64_t tiles, int64_t blocks) {
 //   D = 256  8 behind 8000 32 / 42, 16 45 / 50, 32 70 / 52, 8 behind 32000 72 / 57
 // and more rows of each of 32 sequences behind 16000 / 2000, D = 128, in one prompt launch / in two:
 //   32 rows 292 / 81 and 63 / 44, 64 rows 292 / 124 and 56 / 60, 128 rows 311 / 215 and 69 / 79.
-PrefixPlan plan_prefix(const AttnArgs& a) {
+constexpr int64_t kMostBlocks = 1 << 22;  // of a launch
+PrefixPlan plan_prefix_of(const AttnArgs& a) {
   const KvArgs &kv = a.kv, &prefix = a.prefix;
   const int D = kv.D;
   const int64_t Rs = kv.max_q * a.G, Rg = prefix.max_q * a.G, row_bytes = (D + kPartPad) * 4;
@@ -1876,16 +1869,20 @@ PrefixPlan plan_prefix(const AttnArgs& a) {
 
   // tiles of the sequences' rows, all steps
   PrefixPlan one = {};
-  one.mode = kBehind;
+  one.behind = true;
   one.rows = prompt_rows(D, Rs);
   const int64_t slots = prompt_slots(D, Rs), most = tiles_of(kv, a.G, one.rows);
-  // tiles to be expected: each sequence's last one half full
-  const int64_t tiles = std::min(most, kv.H * (kv.total_q * a.G / one.rows + (kv.n_seqs + 1) / 2));
+  // tiles to be expected: each sequence's last one half full, but one of each
+  const int64_t tiles =
+      std::min(most, kv.H * std::max(kv.n_seqs, kv.total_q * a.G / one.rows + (kv.n_seqs + 1) / 2));
   one.whole = (int)(tiles / slots * slots / kv.H);
   const int64_t rest = tiles - one.whole * kv.H;  // behind the last full round
   one.parts = 1;
-  double one_time = (double)(one.whole * kv.H) / (double)slots * wg_time(D, one.rows, slots, (double)steps);
-  if (rest) one_time += cut_time(D, one.rows, rest, steps, (double)(rest * one.rows * row_bytes) * 2. / kRate, 4., &one.parts);
+  const double one_fill = (double)std::min<int64_t>(Rs, one.rows) / (double)one.rows;
+  double one_time = (double)(one.whole * kv.H) / (double)slots * wg_time(D, one.rows, one_fill, slots, (double)steps);
+  if (rest)
+    one_time += cut_time(D, one.rows, one_fill, rest, most - one.whole * kv.H, steps,
+                         one_fill * (double)(rest * one.rows * row_bytes) * 2. / kRate, 4. + 0.03 * (double)rest, &one.parts);
   if (one.parts == 1) one.whole = (int)(most / kv.H);
   one.cut = most - one.whole * kv.H;
   one.blocks = one.whole * kv.H + one.cut * one.parts;
@@ -1898,8 +1895,7 @@ PrefixPlan plan_prefix(const AttnArgs& a) {
 
   // groups, then sequences
   PrefixPlan two = {};
-  two.mode = kHead;
-  two.parts = 1;
+    two.parts = 1;
   two.tail_nc = nc;
   // as many pieces of a tile as fill the chip
   two.tail_pieces = (int)std::max<int64_t>(std::min(shares / few_tiles, cdiv(kv.max_kv, kBlock)), 1);
@@ -1910,7 +1906,8 @@ PrefixPlan plan_prefix(const AttnArgs& a) {
     // 256 rows a tile where that is not a fifth more of them than in tiles of 128
     two.rows = prompt_rows(D, cdiv(Rg, 256) * 256 * 5 < cdiv(Rg, 128) * 128 * 6 ? Rg : 128);
     const int64_t group_tiles = tiles_of(prefix, a.G, two.rows);
-    two_time += cut_time(D, two.rows, group_tiles, head_steps, (double)(kv.total_q * a.Hq * row_bytes) * 2. / kRate, 0., &two.parts);
+    two_time += cut_time(D, two.rows, (double)std::min<int64_t>(Rg, two.rows) / (double)two.rows, group_tiles, group_tiles, head_steps,
+                         (double)(kv.total_q * a.Hq * row_bytes) * 2. / kRate, 0., &two.parts);
     two.blocks = group_tiles * two.parts;
   } else {
     two.nc = decode_nc(Rg);
@@ -1920,9 +1917,11 @@ PrefixPlan plan_prefix(const AttnArgs& a) {
   }
   two.sums = (size_t)(two.parts * kv.total_q * a.Hq * row_bytes);
 
+  // sequences of 256 rows and more fill their tiles without a group, and need no sums
+  if (Rs > 256 || two.blocks > kMostBlocks || two.tail_blocks > kMostBlocks) two_time = 1e30;
   if (few_time <= std::min(one_time, two_time)) {
     PrefixPlan few = {};
-    few.mode = kBehind;
+    few.behind = true;
     few.nc = nc;
     few.parts = 1;
     few.blocks = shares;
@@ -1957,25 +1956,18 @@ hipError_t launch_attention(AttnArgs a, void* ws, hipStream_t s) {
   return hipGetLastError();
 }
 
-bool attention_prefix_fits(const AttnArgs& a) {
-  const PrefixPlan p = plan_prefix(a);
-  return p.blocks <= (1 << 22) && p.tail_blocks <= (1 << 22);
-}
+PrefixPlan plan_prefix(const AttnArgs& a) { return plan_prefix_of(a); }
 
-size_t attention_prefix_workspace_bytes(const AttnArgs& a) {
-  const PrefixPlan p = plan_prefix(a);
-  return (size_t)kCounterBytes + p.sums + p.part;
-}
+size_t attention_prefix_workspace_bytes(const PrefixPlan& p) { return (size_t)kCounterBytes + p.sums + p.part; }
 
-hipError_t launch_attention_prefix(AttnArgs a, void* ws, hipStream_t s) {
-  const PrefixPlan p = plan_prefix(a);
+hipError_t launch_attention_prefix(AttnArgs a, const PrefixPlan& p, void* ws, hipStream_t s) {
   uint8_t* at = (uint8_t*)ws + kCounterBytes;
   a.cnt = (uint32_t*)ws + 16;
   a.sums = (float*)at;
   a.part = (float*)(at + p.sums);
   a.parts = a.sums_parts = p.parts;
   a.whole = p.whole;
-  if (p.mode == kBehind) {
+  if (p.behind) {
     if (p.nc > 0) {
       launch_decode<kBehind>(p.nc, (unsigned)p.blocks, a, s);
     } else {

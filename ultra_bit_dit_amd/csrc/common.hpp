@@ -216,8 +216,9 @@ int64_t attention_blocks(const KvArgs& kv, int64_t G);
 size_t attention_workspace_bytes(const KvArgs& kv, int64_t G);
 hipError_t launch_attention(AttnArgs a, void* ws, hipStream_t s);
 // the same behind prefixes that groups of sequences share
-bool attention_prefix_fits(const AttnArgs& a);  // its launches hold their workgroups
-size_t attention_prefix_workspace_bytes(const AttnArgs& a);
-hipError_t launch_attention_prefix(AttnArgs a, void* ws, hipStream_t s);
+struct PrefixPlan;
+PrefixPlan plan_prefix(const AttnArgs& a);
+size_t attention_prefix_workspace_bytes(const PrefixPlan& p);
+hipError_t launch_attention_prefix(AttnArgs a, const PrefixPlan& p, void* ws, hipStream_t s);
 
 }  // namespace lowbit

@@ -152,4 +152,17 @@ struct AttnArgs {
   uint32_t* cnt;             // arrivals: of a group (by the place of its first share), then of a tile
 };
 
+// Of a call behind shared prefixes: one launch, or the groups' and the sequences'.
+struct PrefixPlan {
+  bool behind;               // one launch
+  // of that, else of the groups'.  nc 0: prompt tiles of `rows` rows in `parts` parts, the
+  // first `whole` of a head uncut; else attn_decode with nc column tiles.
+  int nc, rows, parts, whole;
+  int64_t blocks;
+  int64_t cut;               // tiles of all heads that are in parts
+  int tail_nc, tail_pieces;  // of the sequences' launch
+  int64_t tail_blocks;
+  size_t sums, part;         // bytes
+};
+
 }  // namespace lowbit
