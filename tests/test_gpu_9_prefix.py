@@ -39,13 +39,13 @@ class Call:
         a = self.args(O=O, lse=lse, **kw)
         return lb.attention_kv8_prefix(self.q, self.c.gpu, self.prefix_table, i32(self.prefix), self.table, i32(self.own), **a)
 
-    def check(self, out, what, causal=True, scale=None, rows=None):
+    def check(self, out, what, causal=True, scale=None, rows=None, some=None):
         O, lse = f64(out[0]), f64(out[1])
         assert np.all(O[self.rows[-1]:] == 7) and np.all(lse[self.rows[-1]:] == 7), f"{what}: rows behind the last sequence"
         scale = self.D ** -0.5 if scale is None else scale
         q = f64(self.q)
         for b in range(self.B):
-            if self.new[b] == 0:
+            if self.new[b] == 0 or (some and b % max(1, self.B // some) and b != self.B - 1):
                 continue
             g = int(np.searchsorted(self.starts, b, side="right")) - 1
             Kp, Vp = self.c.read(g, self.prefix[g]) if 0 <= g < self.G else (np.zeros((0, self.H, self.D)),) * 2
@@ -99,6 +99,43 @@ def test_sizes_of_plans(Hq, H, D, P, B, n, L):
     k.check(k.run(), "plans", rows=2)
     # loose bounds choose other kernels and parts; the same within the bound
     k.check(k.run(max_q=None, max_seqs=None, max_kv=None, max_prefix=None), "loose bounds", rows=2)
+
+
+OWN = lambda n, first=30: [first + 11 * (i % 9) for i in range(n)]
+LAUNCHES = {
+    # one attn_decode: above.  One prompt launch, its tiles in parts, uncut, or cut in the last round:
+    "parts, 64": dict(prefix=[700, 90], count=[3, 2], new=[70, 100, 3, 90, 61], own=[70, 150, 30, 90, 300], Hq=8, H=2, D=64, P=16),
+    "parts, 128": dict(prefix=[700, 90], count=[3, 2], new=[30, 20, 3, 30, 31], own=[70, 150, 30, 90, 300], Hq=8, H=2, D=128, P=16),
+    "parts, 256": dict(prefix=[500, 90], count=[3, 1], new=[60, 20, 3, 30], own=[70, 150, 30, 90], Hq=4, H=4, D=256, P=64),
+    "uncut, 64": dict(prefix=[300], count=[100], new=[130] * 100, own=[130] * 100, Hq=8, H=8, D=64, P=64),
+    "uncut, 128": dict(prefix=[150], count=[40], new=[120] * 40, own=[120] * 40, Hq=32, H=8, D=128, P=64),
+    "uncut, 256": dict(prefix=[300], count=[40], new=[130] * 40, own=[130] * 40, Hq=8, H=8, D=256, P=64),
+    "last round, 128": dict(prefix=[300, 400], count=[10, 30], new=[130] * 40, own=[130] * 40, Hq=32, H=8, D=128, P=64),
+    # the groups in prompt tiles of 128 and 256 rows, then the sequences, in pieces or whole
+    "groups, 64": dict(prefix=[8000], count=[60], new=[2] * 60, own=OWN(60), Hq=16, H=4, D=64, P=64),
+    "groups, pieces": dict(prefix=[20000], count=[24], new=[1] * 24, own=OWN(24, 300), Hq=4, H=4, D=64, P=64),
+    "groups, 128": dict(prefix=[9000, 3000], count=[30, 3], new=[1] * 33, own=OWN(33), Hq=16, H=4, D=128, P=64),
+    "groups, 256 rows": dict(prefix=[9000, 3000], count=[60, 3], new=[1] * 63, own=OWN(63), Hq=16, H=4, D=128, P=64),
+    "groups, 256": dict(prefix=[9000, 500], count=[40, 2], new=[1] * 42, own=OWN(42), Hq=12, H=2, D=256, P=128),
+    # the groups in attn_decode too
+    "few, 64": dict(prefix=[20000], count=[16], new=[1] * 16, own=OWN(16), Hq=8, H=8, D=64, P=64),
+    "few, 64, 32 rows a wave": dict(prefix=[24000], count=[16], new=[1] * 16, own=OWN(16), Hq=32, H=8, D=64, P=64),
+    "few, 128": dict(prefix=[30000], count=[16], new=[1] * 16, own=OWN(16, 300), Hq=8, H=8, D=128, P=64),
+    "few, 256": dict(prefix=[20000], count=[14], new=[1] * 14, own=OWN(14, 300), Hq=4, H=4, D=256, P=128),
+}
+
+
+@pytest.mark.parametrize("name", LAUNCHES)
+def test_every_launch(name):
+    """Sizes that take each of the launches by the expected times; softmax scales of both signs and 0; some rows of some
+    sequences against the plain form, all of them the same twice."""
+    print(f"launch {name}", flush=True)
+    k = Call(**LAUNCHES[name])
+    for scale in (None, -0.3, 0.0):
+        out = k.run(softmax_scale=scale)
+        again = k.run(softmax_scale=scale)
+        assert torch.equal(out[0], again[0]) and torch.equal(out[1], again[1])
+        k.check(out, f"{name} scale {scale}", scale=scale, rows=2, some=6)
 
 
 def test_equal_groups_without_starts():
