@@ -623,8 +623,8 @@ typedef struct lowbit_rope {
  * All of Q, K, Q_out, K_out 16-byte aligned, strides multiples of 8; freqs 8 bytes,
  * positions, pair_axis and weights 4.  tokens <= 2^30, q_heads, kv_heads <= 2^16.
  * eps finite, >= 0.
- * Errors: E_NULL, E_UNSUPPORTED (types, head_dim, n_pairs, eps), E_SHAPE, E_ALIGN,
- * E_HIP. */
+ * Errors: E_NULL, E_UNSUPPORTED (types, head_dim, n_pairs, eps, an output at an
+ * input's or the other output's address otherwise), E_SHAPE, E_ALIGN, E_HIP. */
 int lowbit_qk_norm_rope(const lowbit_rope* rope, int x_dtype, const void* Q, int64_t q_heads, int64_t q_stride,
                         const float* q_weight, const void* K, int64_t kv_heads, int64_t k_stride,
                         const float* k_weight, float eps, int y_dtype, void* Q_out, int64_t qo_stride, void* K_out,
@@ -658,14 +658,15 @@ int lowbit_qk_norm_rope(const lowbit_rope* rope, int x_dtype, const void* Q, int
  * is written, and the other outputs do not stand: the inputs do.  A child that
  * has more than new_width pages, or 2^30 tokens, is cut to them.
  * n_seqs 0 (nothing yet: parents are none) and n_new 0 (everything freed) are
- * fine, their arrays may be NULL.  Outputs overlap no input; new_refs 16-byte
- * aligned.  n_pages <= 2^26; n_seqs, n_new <= 2^20; table widths <= 2^26; max_grow <= 2^30, n_new
- * (max_grow / page_tokens + 2) <= 2^30, n_new * ceil(new_width / 1024) < 2^24 - 2048;
+ * fine, their arrays may be NULL.  Outputs overlap no input and not each other
+ * (refused); new_refs 16-byte aligned.
+ * n_pages <= 2^26; n_seqs, n_new <= 2^20; table widths <= 2^26; max_grow <= 2^30;
+ * n_new * (max_grow / page_tokens + 2) <= 2^30, n_new * ceil(new_width / 1024) < 2^24 - 2048;
  * n_caches <= 4096.  One workgroup plans: time grows with n_new and with the
  * entries of the sequences that do not go on as one.  Uses the stream's workspace
  * (lowbit_kv8_fork_workspace bytes); reserve it before a capture.
- * Errors: E_NULL, E_UNSUPPORTED (page_tokens, head_dim), E_SHAPE, E_ALIGN, E_NOMEM,
- * E_HIP. */
+ * Errors: E_NULL, E_UNSUPPORTED (page_tokens, head_dim, overlaps), E_SHAPE, E_ALIGN,
+ * E_NOMEM, E_HIP. */
 int lowbit_kv8_fork(const lowbit_kv8* caches, int64_t n_caches, int64_t n_seqs, const int32_t* page_table,
                     int64_t table_width, const int32_t* kv_lens, const int32_t* refs, int64_t n_new,
                     const int32_t* parents, const int32_t* grow, int64_t max_grow, int32_t* new_table,
@@ -678,7 +679,7 @@ int lowbit_kv8_fork_workspace(int64_t n_pages, int page_tokens, int64_t n_caches
  * from *live on are free (in all layers).  remap [n_pages] receives where each
  * page is now (-1: it was free), for tables that are not in the call; new_table
  * is page_table so rewritten (-1 behind a sequence's pages), new_refs the counts.
- * n_seqs may be 0 (the tables then NULL).  Outputs overlap no input.  Limits as
+ * n_seqs may be 0 (the tables then NULL).  Outputs as lowbit_kv8_fork's.  Limits as
  * lowbit_kv8_fork, and ceil(n_pages / 1024) + n_seqs * ceil(table_width / 1024) <
  * 2^24 - 2048.  Uses the stream's workspace (lowbit_kv8_compact_workspace bytes).
  * Errors as lowbit_kv8_fork. */

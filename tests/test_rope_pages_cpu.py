@@ -45,6 +45,14 @@ def test_rope_refusals(kw, status):
     assert call(**kw) == status
 
 
+def test_rope_outputs_elsewhere_or_in_place():
+    """In place: the same type and strides.  Never over the other input, or both outputs in one place."""
+    B, C, D = (ctypes.c_void_p(k) for k in (0x40000, 0x50000, 0x60000))
+    bad = lb.E_UNSUPPORTED
+    assert call(K=B, Ko=C, qos=512) == bad and call(K=B, Ko=C, yd=lb.F32) == bad and call(K=B, Qo=D, Ko=B, kos=256) == bad
+    assert call(K=B, Qo=B, Ko=C) == bad and call(K=B, Qo=C, Ko=A16) == bad and call(K=B, Qo=D, Ko=D) == bad
+
+
 def kv(**over):
     c = dict(n_pages=64, page_tokens=16, kv_heads=2, head_dim=64, k_codes=0x10000, v_codes=0x20000, k_scales=0x30000,
              v_scales=0x40000)
@@ -98,6 +106,23 @@ def test_fork_refusals():
     # the free pages' list grows with what can be asked for, never past the pages
     assert lb.kv8_fork_workspace(1 << 20, 16, 8, 1 << 10, 1) < lb.kv8_fork_workspace(1 << 20, 16, 8, 1 << 10, 1 << 12)
     assert lb.kv8_fork_workspace(1 << 20, 16, 8, 1 << 10, 1 << 16) == lb.kv8_fork_workspace(1 << 20, 16, 8, 1 << 10, 1 << 17)
+
+
+def test_page_outputs_overlap_nothing():
+    """Refused where one integer is shared."""
+    at = {k: 0x100000 * (i + 1) for i, k in enumerate(("pt", "ln", "refs", "par", "grow", "nt", "nl", "nr", "fl", "rm", "lv"))}
+    size = dict(pt=8, ln=2, refs=64, par=3, grow=3, nt=12, nl=3, nr=64, fl=1, rm=64, lv=1)
+    for f, ins, outs in ((fork, ("pt", "ln", "refs", "par", "grow"), ("nt", "nl", "nr", "fl")),
+                         (compact, ("pt", "ln", "refs"), ("nt", "nr", "rm", "lv"))):
+        base = {k: ctypes.c_void_p(at[k]) for k in ins + outs}
+        n = dict(size, nt=8) if f is compact else size
+        for o in outs:
+            for i in ins + outs:
+                if i == o:
+                    continue
+                if o != "nr" or f is compact:  # the last integer of i
+                    assert f(**dict(base, **{o: ctypes.c_void_p(at[i] + 4 * n[i] - 4)})) == lb.E_UNSUPPORTED, (o, i)
+                assert f(**dict(base, **{o: ctypes.c_void_p(at[i])})) == lb.E_UNSUPPORTED, (o, i)
 
 
 def test_compact_refusals():

@@ -6,6 +6,7 @@
 #include <map>
 #include <mutex>
 #include <utility>
+#include <initializer_list>
 #include <vector>
 
 #include "../../include/lowbit.h"
@@ -785,6 +786,12 @@ int lowbit_qk_norm_rope(const lowbit_rope* rope, int x_dtype, const void* Q, int
   if (r.n_pairs && (!aligned(r.positions, 4) || !aligned(r.freqs, 8) || (r.pair_axis && !aligned(r.pair_axis, 4))))
     return LOWBIT_E_ALIGN;
   if ((q_weight && !aligned(q_weight, 4)) || (k_weight && !aligned(k_weight, 4))) return LOWBIT_E_ALIGN;
+  auto not_in_place = [&](int64_t stride, int64_t o_stride) {
+    return x_dtype != y_dtype || (r.tokens > 1 && stride != o_stride);
+  };
+  if (Q_out == Q && not_in_place(q_stride, qo_stride)) return LOWBIT_E_UNSUPPORTED;
+  if (kv_heads && ((K_out == K && not_in_place(k_stride, ko_stride)) || Q_out == K || K_out == Q || K_out == Q_out))
+    return LOWBIT_E_UNSUPPORTED;
   RopeArgs a;
   a.tokens = r.tokens;
   a.D = r.head_dim;
@@ -845,6 +852,25 @@ bool fork_sizes_ok(int64_t n_pages, int page_tokens, int64_t n_seqs, int64_t n_n
          n_new <= (1 << 20) && max_grow >= 0 && max_grow <= (1 << 30) &&
          n_new * (max_grow / page_tokens + 2) <= (1 << 30);
 }
+// whether an output shares a byte with an input or with another output
+struct Span {
+  const void* p;
+  int64_t ints;
+};
+bool outputs_overlap(std::initializer_list<Span> in, std::initializer_list<Span> out) {
+  auto meet = [](const Span& a, const Span& b) {
+    const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
+    return a.p && b.p && a.ints && b.ints && x < y + 4 * (uintptr_t)b.ints && y < x + 4 * (uintptr_t)a.ints;
+  };
+  for (const Span* o = out.begin(); o != out.end(); o++) {
+    for (const Span& i : in)
+      if (meet(*o, i)) return true;
+    for (const Span* q = out.begin(); q != o; q++)
+      if (meet(*o, *q)) return true;
+  }
+  return false;
+}
+
 bool table_ok(int64_t n_seqs, int64_t width) {
   return n_seqs == 0 || (width >= 1 && width <= kMaxWidth);
 }
@@ -916,6 +942,9 @@ int lowbit_kv8_fork(const lowbit_kv8* caches, int64_t n_caches, int64_t n_seqs, 
     a.new_refs = new_refs;
     a.failed = failed;
     if (!fork_fits(a)) return LOWBIT_E_SHAPE;
+    if (outputs_overlap({{page_table, n_seqs * a.width}, {kv_lens, n_seqs}, {refs, a.n_pages}, {parents, n_new}, {grow, n_new}},
+                        {{new_table, n_new * a.new_width}, {new_lens, n_new}, {new_refs, a.n_pages}, {failed, 1}}))
+      return LOWBIT_E_UNSUPPORTED;
     void* ws = nullptr;
     const int r2 = workspace((hipStream_t)stream, fork_workspace_bytes(a), &ws);
     if (r2) return r2;
@@ -961,6 +990,9 @@ int lowbit_kv8_compact(const lowbit_kv8* caches, int64_t n_caches, int64_t n_seq
     a.remap = remap;
     a.live = live;
     if (!compact_fits(a)) return LOWBIT_E_SHAPE;
+    if (outputs_overlap({{page_table, n_seqs * a.width}, {kv_lens, n_seqs}, {refs, a.n_pages}},
+                        {{new_table, n_seqs * a.width}, {new_refs, a.n_pages}, {remap, a.n_pages}, {live, 1}}))
+      return LOWBIT_E_UNSUPPORTED;
     void* ws = nullptr;
     const int r2 = workspace((hipStream_t)stream, compact_workspace_bytes(a), &ws);
     if (r2) return r2;
