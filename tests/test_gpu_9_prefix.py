@@ -103,7 +103,7 @@ def test_sizes_of_plans(Hq, H, D, P, B, n, L):
 
 OWN = lambda n, first=30: [first + 11 * (i % 9) for i in range(n)]
 LAUNCHES = {
-    # one attn_decode: above.  One prompt launch, its tiles in parts, uncut, or cut in the last round:
+    # one prompt launch, its tiles in parts, uncut, or cut in the last round
     "parts, 64": dict(prefix=[700, 90], count=[3, 2], new=[70, 100, 3, 90, 61], own=[70, 150, 30, 90, 300], Hq=8, H=2, D=64, P=16),
     "parts, 128": dict(prefix=[700, 90], count=[3, 2], new=[30, 20, 3, 30, 31], own=[70, 150, 30, 90, 300], Hq=8, H=2, D=128, P=16),
     "parts, 256": dict(prefix=[500, 90], count=[3, 1], new=[60, 20, 3, 30], own=[70, 150, 30, 90], Hq=4, H=4, D=256, P=64),
@@ -122,6 +122,24 @@ LAUNCHES = {
     "few, 64, 32 rows a wave": dict(prefix=[24000], count=[16], new=[1] * 16, own=OWN(16), Hq=32, H=8, D=64, P=64),
     "few, 128": dict(prefix=[30000], count=[16], new=[1] * 16, own=OWN(16, 300), Hq=8, H=8, D=128, P=64),
     "few, 256": dict(prefix=[20000], count=[14], new=[1] * 14, own=OWN(14, 300), Hq=4, H=4, D=256, P=128),
+    # again parts and uncut tiles of prompts
+    "parts, 64, again": dict(prefix=[3000, 90], count=[3, 2], new=[70, 100, 30, 90, 61], own=[70, 150, 30, 90, 300], Hq=32, H=2, D=64, P=16),
+    "parts, 128, again": dict(prefix=[3000, 90], count=[3, 2], new=[32, 32, 3, 32, 31], own=[70, 150, 40, 90, 300], Hq=24, H=6, D=128, P=16),
+    "parts, 128, 256 rows": dict(prefix=[1000, 90], count=[3, 2], new=[70, 100, 3, 90, 61], own=[70, 150, 30, 90, 300], Hq=32, H=4, D=128, P=16),
+    "uncut, 128, 128 rows": dict(prefix=[100, 90], count=[30, 30], new=[40] * 60, own=[50] * 60, Hq=24, H=8, D=128, P=16),
+    # one attn_decode: a workgroup for each tile or several for each, and equal shares
+    "tiles, 64": dict(prefix=[900, 90], count=[9, 5], new=[1] * 14, own=OWN(14), Hq=16, H=8, D=64, P=16),
+    "pieces, 64": dict(prefix=[2900, 90], count=[9, 5], new=[1] * 14, own=OWN(14), Hq=16, H=8, D=64, P=16),
+    "tiles, 64, 32 rows a wave": dict(prefix=[900, 1500], count=[9, 50], new=[5] * 59, own=OWN(59), Hq=32, H=8, D=64, P=32),
+    "pieces, 64, 32 rows a wave": dict(prefix=[3000, 800], count=[9, 1], new=[5] * 10, own=OWN(10), Hq=20, H=5, D=64, P=16),
+    "tiles, 128": dict(prefix=[700, 800], count=[19, 60], new=[2] * 79, own=OWN(79), Hq=20, H=4, D=128, P=16),
+    "pieces, 128": dict(prefix=[3000, 800], count=[9, 1], new=[2] * 10, own=OWN(10), Hq=20, H=4, D=128, P=16),
+    "tiles, 256": dict(prefix=[300, 200], count=[19, 30], new=[1] * 49, own=OWN(49), Hq=12, H=4, D=256, P=16),
+    "pieces, 256": dict(prefix=[1500, 800], count=[9, 1], new=[1] * 10, own=OWN(10), Hq=4, H=4, D=256, P=16),
+    "shares, 64": dict(prefix=[300, 200], count=[100, 130], new=[1] * 230, own=OWN(230), Hq=12, H=4, D=64, P=16),
+    "shares, 64, 32 rows a wave": dict(prefix=[60000, 90, 700], count=[2, 1, 3], new=[5] * 6, own=OWN(6), Hq=32, H=8, D=64, P=128),
+    "shares, 128": dict(prefix=[300, 200], count=[100, 130], new=[1] * 230, own=OWN(230), Hq=12, H=4, D=128, P=16),
+    "shares, 256": dict(prefix=[40000, 90], count=[2, 1], new=[1] * 3, own=OWN(3), Hq=8, H=8, D=256, P=128),
 }
 
 

@@ -315,22 +315,30 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
     return max((most + kBlock - 1) / kBlock, (int64_t)1);
   };
   auto tiles_of = [&](const SeqSpan& t) -> int64_t { return (t.n * a.G + 16 * NC - 1) / (16 * NC); };
-  // kTail: a tile is cut into so many pieces at most, one workgroup each (equal shares
-  // of all blocks would often have the end of one tile and the start of the next)
-  const int64_t pieces = MODE == kTail ? a.pieces : 0;
+  // kTail, and kBehind where a.pieces is set: a tile is cut into so many pieces at most, one
+  // workgroup each (equal shares of all blocks would often have the end of one tile and the
+  // start of the next)
+  const int64_t pieces = MODE == kTail || MODE == kBehind ? a.pieces : 0;
+  const bool in_pieces = MODE == kTail || (MODE == kBehind && pieces > 0);
   auto work_of = [&](int64_t i) -> int64_t {
     Head<MODE> head;
     const SeqSpan t = near ? mine : span_of(i, &head);  // near: i is the lane
-    return tiles_of(t) * (MODE == kTail ? pieces : blocks_of(t));
+    return tiles_of(t) * (in_pieces ? pieces : blocks_of(t));
   };
   ItemScan<64 * kDecWaves, decltype(work_of)> scan(a.kv.n_seqs, work_of, scan_);
   const int64_t per_head = scan.total, total = per_head * a.kv.H;
   // Shares: one for each block while there are workgroups for that, so that none
   // has parts of two tiles, which it would have to begin and join in turn
   const int64_t shares = max(min(total, (int64_t)gridDim.x), (int64_t)1);
-  // neighbouring shares on one XCD (bid % 8) where every workgroup has one
-  const int64_t per_xcd = gridDim.x / 8, bid = blockIdx.x;
-  const int64_t share = shares == (int64_t)gridDim.x && MODE != kTail ? (bid % 8) * per_xcd + bid / 8 : bid;
+  // Neighbouring shares on one XCD (bid % 8): where every workgroup has one; and pieces behind
+  // prefixes, so that sequences of a group find its codes in their L2 (a grid of whole eights)
+  const int64_t per_xcd = MODE == kBehind && in_pieces ? (shares + 7) / 8 : gridDim.x / 8, bid = blockIdx.x;
+  int64_t share = bid;
+  if (MODE == kBehind && in_pieces) {
+    share = bid / 8 < per_xcd ? (bid % 8) * per_xcd + bid / 8 : shares;
+  } else if (MODE != kTail && shares == (int64_t)gridDim.x) {
+    share = (bid % 8) * per_xcd + bid / 8;
+  }
   if (share >= shares) return;
   int64_t x = quot(total * share, shares);
   const int64_t x_end = quot(total * (share + 1), shares);
@@ -341,12 +349,12 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
   Head<MODE> head;
   SeqSpan s = span_for_all(b, &head);
   int64_t blocks = blocks_of(s), tiles = tiles_of(s);
-  int64_t rt = quot(item, MODE == kTail ? pieces : blocks);
-  int at = (int)(item - rt * (MODE == kTail ? pieces : blocks));  // first block of this share in the tile
+  int64_t rt = quot(item, in_pieces ? pieces : blocks);
+  int at = (int)(item - rt * (in_pieces ? pieces : blocks));  // first block of this share in the tile
   for (;;) {
     int count, n_parts;
     int64_t share0;  // the first share that holds blocks of this tile
-    if constexpr (MODE == kTail) {
+    if (in_pieces) {
       n_parts = (int)min(pieces, blocks);
       share0 = share - at;
       if (at >= n_parts) return;
@@ -828,7 +836,7 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
       }
     }
     // ---- the share's next tile
-    x += MODE == kTail ? 1 : count;  // a share is one piece
+    x += in_pieces ? 1 : count;  // a share is one piece
     if (x >= x_end) return;
     __syncthreads();  // the LDS is free again
     at = 0;
@@ -1840,7 +1848,7 @@ double cut_time(int D, int64_t rows, double fill, int64_t tiles, int64_t most, i
   }
   return least;
 }
-// us of attn_decode for tiles of so many rows and blocks
+// us of attn_decode over the groups' rows, in equal shares of all blocks
 double decode_time(int D, int64_t rows, int64_t tiles, int64_t blocks) {
   const double shares = D == 256 ? kMaxShares / 2 : kMaxShares, x = (double)(tiles * blocks) / shares;
   const double parts = std::min(shares / (double)tiles, (double)blocks);  // of a tile, to be joined
@@ -1848,14 +1856,44 @@ double decode_time(int D, int64_t rows, int64_t tiles, int64_t blocks) {
   const double work = D == 256 ? 18. + 3.3 * x : D == 128 ? 13. + 3. * x : rows > 16 ? 18. + 2.8 * x : 11. + 1.9 * x;
   return work + join;
 }
+// us of joining the pieces of a tile
+double join_time(int D, int64_t rows, int64_t pieces) {
+  const double each = D == 64 ? 0.05 : D == 128 ? 0.13 : 0.25;
+  return pieces > 1 ? 1.4 + each * (double)std::min<int64_t>(rows, D == 64 ? 32 : 16) * sqrt((double)pieces) : 0.;
+}
+// us of attn_decode over sequences and their prefixes, `pieces` a tile (0: equal shares of all blocks)
+double few_time_of(int D, int64_t rows, int64_t tiles, int64_t blocks, int64_t pieces) {
+  const double shares = D == 256 ? kMaxShares / 2 : kMaxShares, t = (double)tiles / shares, x = t * (double)blocks;
+  if (pieces == 0) {
+    if (D == 64) return rows > 16 ? 22.5 + 1.9 * x + 3. * t : 12.9 + 1.6 * x + 4.2 * t;
+    return D == 128 ? 15.3 + 2.7 * x + 4.3 * t : 11.8 + 3.1 * x + 8.4 * t;
+  }
+  const double join = join_time(D, rows, pieces);
+  if (D == 64) return (rows > 16 ? 12.5 + 2.6 * x : 9.6 + 2.3 * x) + join;
+  return (D == 128 ? 10.8 + 3.2 * x : 12.5 + 0.6 * x + 3.4 * (double)cdiv(blocks, pieces)) + join;
+}
+// us of the sequences' launch behind the groups', beside what it takes for a block of each: `t` times the tiles
+// and pieces that the chip holds
+double tail_time(int D, int64_t rows, int64_t tiles, int64_t blocks, int64_t pieces) {
+  const double t = (double)(tiles * pieces) / (D == 256 ? kMaxShares / 2 : kMaxShares), full = std::max(t, 1.);
+  const double each = (double)cdiv(blocks, pieces);
+  const double time = D == 64 ? 2.5 * t + 2.1 * full * each + 4. * (full - 1.) : D == 128 ? 6. * t + 4. * full * each
+                                                                                         : 6. * t + 3.3 * full * each + 5. * (full - 1.);
+  return time + join_time(D, rows, pieces);
+}
 
-// The three ways by their expected times.  us, measured, single tokens of 32 heads
-// over 8 behind one prefix (D = 256: 24 over 4), in one attn_decode / in two launches:
+// The three ways by their expected times, whose numbers are fitted to 450 random calls (1 to 8 groups of 2 to 64
+// sequences, 1 to 700 new tokens, prefixes of 10 to 60000); 300 others took 1.2% longer than with always the best of
+// the three.  us, measured, single tokens of 32 heads over 8 behind one prefix (D = 256: 24 over 4), in one attn_decode /
+// in two launches:
 //   D = 64   8 sequences behind 8000 20 / 24, 16 27 / 26, 32 42 / 30, 8 behind 32000 43 / 38
 //   D = 128  4 behind 1000 15 / 21, 8 behind 8000 27 / 31, 16 39 / 33, 32 63 / 38, 8 behind 32000 62 / 43
 //   D = 256  8 behind 8000 32 / 42, 16 45 / 50, 32 70 / 52, 8 behind 32000 72 / 57
 // and more rows of each of 32 sequences behind 16000 / 2000, D = 128, in one prompt launch / in two:
 //   32 rows 292 / 81 and 63 / 44, 64 rows 292 / 124 and 56 / 60, 128 rows 311 / 215 and 69 / 79.
+// attn_decode over sequences and prefixes in pieces rather than equal shares where there are no more than 8 blocks a
+// workgroup (of the 450 calls those with 2 to 4 took 0.72 to 0.87 of the time, with 4 to 8 0.9, with more 1.0 to 1.25,
+// as sequences differ in length).
 constexpr int64_t kMostBlocks = 1 << 22;  // of a launch
 PrefixPlan plan_prefix_of(const AttnArgs& a) {
   const KvArgs &kv = a.kv, &prefix = a.prefix;
@@ -1887,21 +1925,25 @@ PrefixPlan plan_prefix_of(const AttnArgs& a) {
   one.cut = most - one.whole * kv.H;
   one.blocks = one.whole * kv.H + one.cut * one.parts;
   one.part = (size_t)(one.cut * one.parts * one.rows * row_bytes);
+  one_time = 0.92 * one_time + (D == 64 ? 3.7 : D == 256 ? 1.9 : one.rows == 128 ? 4.9 : 10.3);
 
   // the same in attn_decode
   const int nc = decode_nc(Rs);
-  const int64_t few_tiles = tiles_of(kv, a.G, 16 * nc);
-  const double few_time = decode_time(D, Rs, few_tiles, cdiv(steps, kDecWaves));
+  const int64_t few_tiles = tiles_of(kv, a.G, 16 * nc), few_blocks = cdiv(steps, kDecWaves);
+  const bool in_pieces = few_tiles <= shares && few_tiles * few_blocks <= 8 * shares;
+  const int64_t few_pieces = in_pieces ? std::min(shares / few_tiles, few_blocks) : 0;
+  const double few_time = few_time_of(D, Rs, few_tiles, few_blocks, few_pieces);
 
   // groups, then sequences
   PrefixPlan two = {};
-    two.parts = 1;
+  two.parts = 1;
   two.tail_nc = nc;
   // as many pieces of a tile as fill the chip
-  two.tail_pieces = (int)std::max<int64_t>(std::min(shares / few_tiles, cdiv(kv.max_kv, kBlock)), 1);
-  two.tail_blocks = few_tiles * two.tail_pieces;
-  if (two.tail_pieces > 1) two.part = decode_part(nc);
-  double two_time = 4. + decode_time(D, Rs, few_tiles, cdiv(own_steps, kDecWaves));
+  two.pieces = (int)std::max<int64_t>(std::min(shares / few_tiles, cdiv(kv.max_kv, kBlock)), 1);
+  two.tail_blocks = few_tiles * two.pieces;
+  if (two.pieces > 1) two.part = decode_part(nc);
+  double two_time = D == 256 ? 10.7 : 8.4;
+  two_time += tail_time(D, Rs, few_tiles, cdiv(own_steps, kDecWaves), two.pieces);
   if (many_rows(prefix, Rg)) {
     // 256 rows a tile where that is not a fifth more of them than in tiles of 128
     two.rows = prompt_rows(D, cdiv(Rg, 256) * 256 * 5 < cdiv(Rg, 128) * 128 * 6 ? Rg : 128);
@@ -1924,7 +1966,8 @@ PrefixPlan plan_prefix_of(const AttnArgs& a) {
     few.behind = true;
     few.nc = nc;
     few.parts = 1;
-    few.blocks = shares;
+    few.pieces = (int)few_pieces;
+    few.blocks = in_pieces ? cdiv(few_tiles * few_pieces, 8) * 8 : shares;
     few.part = decode_part(nc);
     return few;
   }
@@ -1967,6 +2010,7 @@ hipError_t launch_attention_prefix(AttnArgs a, const PrefixPlan& p, void* ws, hi
   a.part = (float*)(at + p.sums);
   a.parts = a.sums_parts = p.parts;
   a.whole = p.whole;
+  a.pieces = p.pieces;
   if (p.behind) {
     if (p.nc > 0) {
       launch_decode<kBehind>(p.nc, (unsigned)p.blocks, a, s);
@@ -1981,7 +2025,6 @@ hipError_t launch_attention_prefix(AttnArgs a, const PrefixPlan& p, void* ws, hi
   head.causal = 0;
   if (p.nc > 0) launch_decode<kHead>(p.nc, (unsigned)p.blocks, head, s);
   else launch_prompt<kHead>(p.rows, (unsigned)p.blocks, head, s);
-  a.pieces = p.tail_pieces;
   launch_decode<kTail>(p.tail_nc, (unsigned)p.tail_blocks, a, s);
   return hipGetLastError();
 }

@@ -148,7 +148,7 @@ struct AttnArgs {
   float* sums;               // [parts][total_q][Hq] sums of the rows over their prefixes, before the division
   int sums_parts;            // as how many parts at most
   int whole;                 // tiles of a head whose steps are not cut into parts
-  int pieces;                // of a sequence's tile, a workgroup each
+  int pieces;                // of a sequence's tile, a workgroup each; kBehind: 0 for equal shares
   uint32_t* cnt;             // arrivals: of a group (by the place of its first share), then of a tile
 };
 
@@ -160,8 +160,9 @@ struct PrefixPlan {
   int nc, rows, parts, whole;
   int64_t blocks;
   int64_t cut;               // tiles of all heads that are in parts
-  int tail_nc, tail_pieces;  // of the sequences' launch
+  int tail_nc;               // of the sequences' launch
   int64_t tail_blocks;
+  int pieces;                // that a tile of attn_decode over the sequences is cut into, 0: equal shares
   size_t sums, part;         // bytes
 };
 
