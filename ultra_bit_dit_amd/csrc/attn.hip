@@ -270,7 +270,7 @@ constexpr int kBlock = kUnit * kDecWaves;  // tokens of a block: a step of every
 template <int D, int NC, int MODE>
 __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_decode(AttnArgs a) {
   constexpr int DC = D / 64, DT = D / 16;
-  __shared__ __attribute__((aligned(16))) float lo_[kDecWaves / 2][NC * 16 * D];  // partial O of half the waves
+  __shared__ __attribute__((aligned(16))) float lo_[kDecWaves][NC * 16 * D];  // the waves' O
   __shared__ float lm_[kDecWaves][NC * 16], ll_[kDecWaves][NC * 16];
   __shared__ int64_t scan_[kDecWaves + 2];
   __shared__ uint32_t s_last;
@@ -654,70 +654,72 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
       }
     }
     __syncthreads();
-    float f[NC], mt[NC], lt[NC];
+    // maximum and sum of weights of a row of the tile
+    auto stats_of = [&](int row, float* mt, float* lt) {
+      float mm = -INFINITY, L = 0.f;
+#pragma unroll
+      for (int w = 0; w < kDecWaves; w++) mm = fmaxf(mm, lm_[w][row]);
+      const float mu = mm == -INFINITY ? 0.f : mm;
+#pragma unroll
+      for (int w = 0; w < kDecWaves; w++) L += ll_[w][row] * __builtin_amdgcn_exp2f(lm_[w][row] - mu);
+      *mt = mm;
+      *lt = L;
+    };
 #pragma unroll
     for (int c = 0; c < NC; c++) {
-      mt[c] = -INFINITY;
-      lt[c] = 0.f;
+      float mm = -INFINITY;
 #pragma unroll
-      for (int w = 0; w < kDecWaves; w++) mt[c] = fmaxf(mt[c], lm_[w][16 * c + n]);
-      const float mu = mt[c] == -INFINITY ? 0.f : mt[c];
+      for (int w = 0; w < kDecWaves; w++) mm = fmaxf(mm, lm_[w][16 * c + n]);
+      const float f = __builtin_amdgcn_exp2f(m[c] - (mm == -INFINITY ? 0.f : mm));
 #pragma unroll
-      for (int w = 0; w < kDecWaves; w++) lt[c] += ll_[w][16 * c + n] * __builtin_amdgcn_exp2f(lm_[w][16 * c + n] - mu);
-      f[c] = __builtin_amdgcn_exp2f(m[c] - mu);
+      for (int d = 0; d < DT; d++) {
 #pragma unroll
-      for (int d = 0; d < DT; d++)
-#pragma unroll
-        for (int e = 0; e < 4; e++) o[c][d][e] *= f[c];
-    }
-    // a tree over the waves: the upper half hands its O to the lower half
-#pragma unroll
-    for (int half = kDecWaves / 2; half >= 1; half >>= 1) {
-      if (wave >= half && wave < 2 * half) {
-#pragma unroll
-        for (int c = 0; c < NC; c++)
-#pragma unroll
-          for (int d = 0; d < DT; d++) *(v4f*)&lo_[wave - half][((c * DT + d) * 64 + lane) * 4] = o[c][d];
+        for (int e = 0; e < 4; e++) o[c][d][e] *= f;
+        *(v4f*)&lo_[wave][((c * DT + d) * 64 + lane) * 4] = o[c][d];
       }
-      __syncthreads();
-      if (wave < half) {
-#pragma unroll
-        for (int c = 0; c < NC; c++)
-#pragma unroll
-          for (int d = 0; d < DT; d++) {
-            const v4f v = *(const v4f*)&lo_[wave][((c * DT + d) * 64 + lane) * 4];
-#pragma unroll
-            for (int e = 0; e < 4; e++) o[c][d][e] += v[e];
-          }
-      }
-      __syncthreads();
     }
+    __syncthreads();
+    // every thread adds eight dims of a row, rows fastest: put(row, dims 8 q .., O)
+    auto add_up = [&](int rows, auto&& put) {
+      for (int i = threadIdx.x; i < NC * 2 * D; i += 64 * kDecWaves) {
+        const int c = i / (2 * D), q = i / 16 % (D / 8), row = 16 * c + (i & 15);
+        if (row >= rows) continue;
+        const float* at = &lo_[0][((c * DT + q / 2) * 64 + 32 * (q & 1) + (i & 15)) * 4];
+        v4f y[2];
+#pragma unroll
+        for (int k = 0; k < 2; k++) {
+          v4f v[kDecWaves];
+#pragma unroll
+          for (int w = 0; w < kDecWaves; w++) v[w] = *(const v4f*)(at + w * (NC * 16 * D) + 64 * k);
+#pragma unroll
+          for (int e = 0; e < 4; e++) y[k][e] = (v[0][e] + v[2][e]) + (v[1][e] + v[3][e]);
+        }
+        put(row, q, y);
+      }
+    };
+    static_assert(kDecWaves == 4, "the sum above");
+    const int rows = (int)(R - rho0 < 16 * NC ? R - rho0 : 16 * NC);
 
     if (n_parts == 1) {
-      if (wave == 0) {
-#pragma unroll
-        for (int c = 0; c < NC; c++) {
-          if (rho[c] >= R) continue;
-          const float inv = lt[c] > 0.f || lt[c] != lt[c] ? 1.0f / lt[c] : 0.f;
-          const int64_t tok = s.row0 + rho[c] / a.G, hd = h * a.G + rho[c] % a.G;
-          if constexpr (MODE == kHead) {
-            float* sums = a.sums + (tok * a.Hq + hd) * (D + kPartPad);
-#pragma unroll
-            for (int d = 0; d < DT; d++) *(v4f*)(sums + 16 * d + 4 * g) = o[c][d];
-            if (g == 0) *(float2*)(sums + D) = make_float2(mt[c], lt[c]);
-            continue;
-          }
-          uint16_t* op = a.o + tok * a.o_stride + hd * D + 4 * g;
-#pragma unroll
-          for (int d = 0; d < DT; d++) {
-            uint2 w;
-            w.x = bf16_bits(o[c][d][0] * inv) | (bf16_bits(o[c][d][1] * inv) << 16);
-            w.y = bf16_bits(o[c][d][2] * inv) | (bf16_bits(o[c][d][3] * inv) << 16);
-            *(uint2*)(op + 16 * d) = w;
-          }
-          if (a.lse && g == 0) a.lse[tok * a.Hq + hd] = lt[c] == 0.f ? -INFINITY : (mt[c] + __builtin_amdgcn_logf(lt[c])) * kLn2;
+      add_up(rows, [&](int row, int q, const v4f* y) {
+        float mt, lt;
+        stats_of(row, &mt, &lt);
+        const uint32_t rr = (uint32_t)rho0 + row, at = rr / (uint32_t)a.G;
+        const int64_t tok = s.row0 + at, hd = h * a.G + (rr - at * (uint32_t)a.G);
+        if constexpr (MODE == kHead) {
+          float* sums = a.sums + (tok * a.Hq + hd) * (D + kPartPad);
+          *(v4f*)(sums + 8 * q) = y[0];
+          *(v4f*)(sums + 8 * q + 4) = y[1];
+          if (q == 0) *(float2*)(sums + D) = make_float2(mt, lt);
+          return;
         }
-      }
+        const float inv = lt > 0.f || lt != lt ? 1.0f / lt : 0.f;
+        mx_u4 w;
+#pragma unroll
+        for (int k = 0; k < 4; k++) w[k] = bf16_bits(y[k / 2][2 * (k & 1)] * inv) | (bf16_bits(y[k / 2][2 * (k & 1) + 1] * inv) << 16);
+        *(mx_u4*)(a.o + tok * a.o_stride + hd * D + 8 * q) = w;
+        if (a.lse && q == 0) a.lse[tok * a.Hq + hd] = lt == 0.f ? -INFINITY : (mt + __builtin_amdgcn_logf(lt)) * kLn2;
+      });
     } else {
       // ---- Several shares: results to the workspace with device-coherent stores
       // that complete before the arrival is counted.  A share has at most two
@@ -726,7 +728,6 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
       // order of the shares in groups, by the last of a group to arrive, then the
       // groups by the last of them: one workgroup reading every result of a long
       // context would take longer than reading the context.
-      const int rows = (int)(R - rho0 < 16 * NC ? R - rho0 : 16 * NC);
       constexpr int PR = D + 2;                      // floats of one row: O, m, l
       constexpr int64_t PS = (int64_t)16 * NC * PR;  // of one place
       const int group = n_parts <= 64 ? 8 : kMaxJoin, groups = (n_parts + group - 1) / group;
@@ -736,30 +737,26 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
       float* joined = a.part + 2 * (int64_t)kMaxShares * PS;  // a group's result, at the place of its first share
       uint32_t* group_cnt = a.cnt + place(grp * group);
       uint32_t* tile_cnt = a.cnt + 2 * kMaxShares + share0;
-      if (wave == 0) {
-        float* mine = a.part + place(part_no) * PS;
+      add_up(rows, [&](int row, int q, const v4f* y) {
+        float* to = a.part + place(part_no) * PS + row * PR;
 #pragma unroll
-        for (int c = 0; c < NC; c++) {
-          if (16 * c + n < rows) {
-            float* row = mine + (16 * c + n) * PR;
-#pragma unroll
-            for (int d = 0; d < DT; d++) {
-              put2(row + 16 * d + 4 * g, o[c][d][0], o[c][d][1]);
-              put2(row + 16 * d + 4 * g + 2, o[c][d][2], o[c][d][3]);
-            }
-            if (g == 0) put2(row + D, mt[c], lt[c]);
-          }
+        for (int k = 0; k < 4; k++) put2(to + 8 * q + 2 * k, y[k / 2][2 * (k & 1)], y[k / 2][2 * (k & 1) + 1]);
+        if (q == 0) {
+          float mt, lt;
+          stats_of(row, &mt, &lt);
+          put2(to + D, mt, lt);
         }
-        __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        if (lane == 0) s_last = __hip_atomic_fetch_add(group_cnt, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      }
+      });
+      __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      __syncthreads();  // every wave's stores are complete
+      if (threadIdx.x == 0) s_last = __hip_atomic_fetch_add(group_cnt, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       __syncthreads();
       // in the LDS of the waves' results: [row][kMaxJoin] maxima, then weights; sums; joined m and l
       float* jw = &lo_[0][0];
       float* js = jw + 16 * NC * kMaxJoin;
       float* jm = js + 16 * NC * kMaxJoin;
       float* jl = jm + 16 * NC;
-      static_assert(16 * NC * (2 * kMaxJoin + 2) <= (kDecWaves / 2) * 16 * NC * D, "fits the waves' O");
+      static_assert(16 * NC * (2 * kMaxJoin + 2) <= kDecWaves * 16 * NC * D, "fits the waves' O");
       // joins the results at from(0 .. count - 1); each pair of outputs goes to put(row, dim, O, O)
       auto join = [&](auto&& from, int count, auto&& put) {
         for (int i = threadIdx.x; i < rows * count; i += 64 * kDecWaves) {
