@@ -315,6 +315,10 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
     return max((most + kBlock - 1) / kBlock, (int64_t)1);
   };
   auto tiles_of = [&](const SeqSpan& t) -> int64_t { return (t.n * a.G + 16 * NC - 1) / (16 * NC); };
+  // new token and head of row r of a sequence and key head (less than 2^31 rows, checked at the entry)
+  const uint32_t G = (uint32_t)a.G;
+  auto token_of = [&](int64_t r) -> int { return (int)((uint32_t)r / G); };
+  auto head_of = [&](int64_t r) -> int { return (int)((uint32_t)r % G); };
   // kTail, and kBehind where a.pieces is set: a tile is cut into so many pieces at most, one
   // workgroup each (equal shares of all blocks would often have the end of one tile and the
   // start of the next)
@@ -376,7 +380,7 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
     int hi_max = 0, hi_min = len, lo_min = 0, lo_max = 0;
     {
       const int64_t rlast = rho0 + 16 * NC - 1 < R ? rho0 + 16 * NC - 1 : R - 1;
-      const int p0 = first + (int)(rho0 / a.G), p1 = first + (int)(rlast / a.G);
+      const int p0 = first + token_of(rho0), p1 = first + token_of(rlast);
       hi_max = head.sees_to(a.causal, p1, len);
       hi_min = head.sees_to(a.causal, p0, len);
       hi_max = max(hi_max, 0);
@@ -391,7 +395,7 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
     for (int c = 0; c < NC; c++) {
       rho[c] = rho0 + 16 * c + n;
       const int64_t rc = rho[c] < R ? rho[c] : R - 1;
-      const int p = first + (int)(rc / a.G);
+      const int p = first + token_of(rc);
       vhi[c] = head.sees_to(a.causal, p, len);
       vlo[c] = a.window > 0 ? max(0, p - a.window + 1) : 0;
     }
@@ -402,7 +406,7 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
 #pragma unroll
     for (int c = 0; c < NC; c++) {
       const int64_t rc = rho[c] < R ? rho[c] : R - 1;
-      const uint16_t* qp = a.q + (s.row0 + rc / a.G) * a.q_stride + (h * a.G + rc % a.G) * D + 16 * g;
+      const uint16_t* qp = a.q + (s.row0 + token_of(rc)) * a.q_stride + (h * a.G + head_of(rc)) * D + 16 * g;
 #pragma unroll
       for (int d = 0; d < DC; d++) {
         qf[c][d][0] = __builtin_bit_cast(v8bf, *(const mx_u4*)(qp + 64 * d));
@@ -605,7 +609,7 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
 #pragma unroll
       for (int c = 0; c < NC; c++) {
         const int64_t rc = rho[c] < R ? rho[c] : R - 1;
-        const float* sums = a.sums + ((s.row0 + rc / a.G) * a.Hq + h * a.G + rc % a.G) * (D + kPartPad);
+        const float* sums = a.sums + ((s.row0 + token_of(rc)) * a.Hq + h * a.G + head_of(rc)) * (D + kPartPad);
         const int64_t next = a.kv.total_q * a.Hq * (D + kPartPad);  // part
         for (int k = (int)(share - share0) * kDecWaves + wave; k < parts; k += takers * kTake) {
           float2 ml[kTake];
@@ -704,8 +708,7 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
       add_up(rows, [&](int row, int q, const v4f* y) {
         float mt, lt;
         stats_of(row, &mt, &lt);
-        const uint32_t rr = (uint32_t)rho0 + row, at = rr / (uint32_t)a.G;
-        const int64_t tok = s.row0 + at, hd = h * a.G + (rr - at * (uint32_t)a.G);
+        const int64_t tok = s.row0 + token_of(rho0 + row), hd = h * a.G + head_of(rho0 + row);
         if constexpr (MODE == kHead) {
           float* sums = a.sums + (tok * a.Hq + hd) * (D + kPartPad);
           *(v4f*)(sums + 8 * q) = y[0];
@@ -800,7 +803,7 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
       };
       auto finish = [&](int r, int d, float px, float py) {
         const float L = jl[r], inv = L > 0.f || L != L ? 1.0f / L : 0.f;
-        const int64_t rr = rho0 + r, tok = s.row0 + rr / a.G, hd = h * a.G + rr % a.G;
+        const int64_t tok = s.row0 + token_of(rho0 + r), hd = h * a.G + head_of(rho0 + r);
         if constexpr (MODE == kHead) {
           float* sums = a.sums + (tok * a.Hq + hd) * (D + kPartPad);
           *(float2*)(sums + d) = make_float2(px, py);
