@@ -612,8 +612,8 @@ typedef struct lowbit_rope {
  * [D] (x_dtype F32 or BF16): y = x w / sqrt(mean of x^2 + eps) with w =
  * q_weight / k_weight [D] (fp32; NULL: y = x, w of 1 + v is the caller's to
  * add); then each pair (a, b) becomes (a cos t - b sin t, b cos t + a sin t),
- * t = positions[axis][token] freqs[pair], reduced in fp64 (exact enough for any
- * position).  Everything else is fp32 (squares beyond its range overflow),
+ * t = positions[axis][token] freqs[pair], reduced in fp64 (off by 2^-51 of the
+ * angle).  Everything else is fp32 (squares beyond its range overflow),
  * rounded once to y_dtype F32 or BF16.  Q, K and the outputs lie with tokens
  * the given strides (in elements) apart, heads contiguous: a fused projection's
  * output as it is.  Q_out may be Q and K_out may be K where x_dtype = y_dtype

@@ -29,6 +29,10 @@
 //   kHead    groups in the place of sequences: the rows of a group's sequences, which lie
 //            in order, see its prefix, and leave their sums in the workspace;
 //   kTail    each sequence's rows see its own tokens, and take those sums in.
+// 64 single tokens behind 32760, 40 heads over 8, D = 128: 91 us (kHead 76, 43 GFLOP in tiles that
+// five heads fill to 0.83; kTail 21, its chain of length, page, codes, sums); 16 behind two prefixes of
+// 65000, 24 heads over 4, D = 256: 100 (74 + 28); 45 x 5 tokens behind six of 8000, D = 64: 41 (21 + 21); 8
+// prompts of 777 behind 6001, 32 heads over 8, D = 128, in one kBehind launch: 470 to 510 by card (0.9 PFLOP/s).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -235,8 +239,9 @@ struct ItemScan {
 // ragged contexts up to 16384, 40 heads over 8, D = 128, 135 us (695 MB, 5.1
 // TB/s); one in 131071, 24 heads over 4, D = 256, 65 us (268 MB, 4.1 TB/s; 57 us
 // where the same cache was read just before and part of it lies in the last-level
-// cache); 64 in 8192, 16 heads over 4, D = 64, 58 us (268 MB, 4.6 TB/s); one in 512,
-// 32 heads over 8, 10.9 us: start, one block a workgroup, the join.
+// cache); 64 in 8192, 16 heads over 4, D = 64, 58 us (268 MB, 4.6 TB/s); one in 77, 40
+// heads over 8, 8.3 us: start, one block a workgroup, the sums of the waves (10.0 us
+// where the waves handed their O down in turn and one of them wrote all rows).
 constexpr int kJoinLoads = 8;   // results of a pair of outputs read at once
 constexpr int kMaxJoin = 32;    // results joined by one workgroup: shares of a tile <= kMaxJoin^2
 constexpr int kMaxShares = 512;
@@ -261,9 +266,8 @@ __device__ __forceinline__ float2 get2(const float* p) {
 }
 
 // Four waves, so that two workgroups share a compute unit where a wave fits
-// 256 registers and one starts or ends while the other reads.  D = 128 fills them:
-// one is spilled, written before the first tile and read back behind a tile's
-// steps; some 110 scalars of every variant lie in lanes of vector registers.
+// 256 registers and one starts or ends while the other reads.  D = 128 fills them; some
+// 110 scalars of every variant lie in lanes of vector registers.
 constexpr int kDecWaves = 4;
 constexpr int kBlock = kUnit * kDecWaves;  // tokens of a block: a step of every wave
 
@@ -1743,7 +1747,8 @@ struct Plan {
 // for all rows, but widens it for 128 or 256 of them and joins its parts by
 // another launch.  So the choice goes by the rows of a head and the steps of all
 // heads.  us, attn_decode / attn_prompt, 32 heads over 8 (D = 256: 24 over 4):
-// (attn_decode with one bf16 term of the weights; the second takes 0.2 to 0.4 us more)
+// (attn_decode with one bf16 term of the weights, whose second takes 0.2 to 0.4 us, and before
+// all threads added its waves' sums, which saves 0.3 to 1.7)
 //   D = 64   4 rows, 1 x 1024 9.4 / 10.3; 16 rows 11.1 / 10.9, 1 x 4096 13.9 / 14.6
 //            20 rows, 1 x 4096 17.4 / 14.6, 16 x 2048 19.4 / 20.8
 //            40 rows, 1 x 4096 19.6 / 14.9, 64 x 2048 53 / 58, 1 x 32768 26 / 41
@@ -1886,11 +1891,11 @@ double tail_time(int D, int64_t rows, int64_t tiles, int64_t blocks, int64_t pie
 // sequences, 1 to 700 new tokens, prefixes of 10 to 60000); 300 others took 1.2% longer than with always the best of
 // the three.  us, measured, single tokens of 32 heads over 8 behind one prefix (D = 256: 24 over 4), in one attn_decode /
 // in two launches:
-//   D = 64   8 sequences behind 8000 20 / 24, 16 27 / 26, 32 42 / 30, 8 behind 32000 43 / 38
-//   D = 128  4 behind 1000 15 / 21, 8 behind 8000 27 / 31, 16 39 / 33, 32 63 / 38, 8 behind 32000 62 / 43
-//   D = 256  8 behind 8000 32 / 42, 16 45 / 50, 32 70 / 52, 8 behind 32000 72 / 57
+//   D = 64   8 sequences behind 8000 20 / 23, 16 30 / 25, 32 44 / 29, 8 behind 32000 43 / 37
+//   D = 128  4 behind 1000 12 / 20, 8 behind 8000 27 / 29, 16 41 / 31, 32 65 / 36, 8 behind 32000 61 / 41
+//   D = 256  8 behind 8000 32 / 40, 16 49 / 47, 32 76 / 50, 8 behind 32000 68 / 54
 // and more rows of each of 32 sequences behind 16000 / 2000, D = 128, in one prompt launch / in two:
-//   32 rows 292 / 81 and 63 / 44, 64 rows 292 / 124 and 56 / 60, 128 rows 311 / 215 and 69 / 79.
+//   32 rows 227 / 78 and 46 / 39, 64 rows 260 / 120 and 53 / 54, 128 rows 312 / 215 and 75 / 71.
 // attn_decode over sequences and prefixes in pieces rather than equal shares where there are no more than 8 blocks a
 // workgroup (of the 450 calls those with 2 to 4 took 0.72 to 0.87 of the time, with 4 to 8 0.9, with more 1.0 to 1.25,
 // as sequences differ in length).

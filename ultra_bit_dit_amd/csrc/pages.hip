@@ -7,6 +7,9 @@
 // Pages are chosen by one small kernel (fork) or by chunks of 4096 pages
 // (compact); their bytes are moved by a launch that fills the chip, a page's keys
 // or values being one run of heads * tokens * dims bytes.
+// In a graph, 64 sequences of 33 pages forked 10.8 us (plan 8.6 alone, rows and copies 4.1 alone),
+// 200 of 2048 pages 13.9; 700 pages compacted 7.2 us, 6000 of 128 KiB with some 1000 moves 63
+// (plan 7.4; moves 45, 132 MB read and written, 5.8 TB/s).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
