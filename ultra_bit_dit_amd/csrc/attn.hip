@@ -334,7 +334,10 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
     return tiles_of(t) * (in_pieces ? pieces : blocks_of(t));
   };
   ItemScan<64 * kDecWaves, decltype(work_of)> scan(a.kv.n_seqs, work_of, scan_);
-  const int64_t per_head = scan.total, total = per_head * a.kv.H;
+  // in pieces: the tiles that the launch has workgroups for; starts that overlap could name more, and a
+  // workgroup has one piece
+  const int64_t per_head = scan.total, all = per_head * a.kv.H;
+  const int64_t total = in_pieces ? min(all, quot(gridDim.x, pieces) * pieces) : all;
   // Shares: one for each block while there are workgroups for that, so that none
   // has parts of two tiles, which it would have to begin and join in turn
   const int64_t shares = max(min(total, (int64_t)gridDim.x), (int64_t)1);
