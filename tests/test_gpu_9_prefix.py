@@ -299,6 +299,40 @@ def test_in_a_graph():
             call()
 
 
+@pytest.mark.parametrize("name", ["groups, pieces", "few, 256", "parts, 64, again", "pieces, 128", "shares, 128"])
+def test_launches_in_a_graph_beside_another_stream(name):
+    """Two launches, parts with their join, pieces and shares: replayed on one stream while another call runs on
+    a second, shorter lengths from replay to replay."""
+    k, other = Call(**LAUNCHES[name]), Call(**LAUNCHES["tiles, 64"], seed=3)
+    pl, ow, a = i32(k.prefix), i32(k.own), k.args()
+    call = lambda **kw: lb.attention_kv8_prefix(k.q, k.c.gpu, k.prefix_table, pl, k.table, ow, **{**a, **kw})
+    O, lse = (torch.zeros_like(x) for x in call())
+    want_other = other.run()
+    s, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        call()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        call(O=O, lse=lse)
+    print(f"graph {name}", flush=True)
+    used = int(k.rows[-1])  # rows behind the last sequence are left as they were
+    for i in range(4):
+        pl.copy_(i32([max(n - 777 * i, i) for n in k.prefix]))
+        ow.copy_(i32([max(n - 5 * i, m) for n, m in zip(k.own, k.new)]))
+        torch.cuda.synchronize()
+        want = call()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            g.replay()
+        with torch.cuda.stream(s2):
+            out = other.run()
+        torch.cuda.synchronize()
+        assert torch.equal(O[:used], want[0][:used]) and torch.equal(lse[:used], want[1][:used]), i
+        assert torch.equal(out[0], want_other[0]) and torch.equal(out[1], want_other[1]), i
+
+
 def test_argument_errors():
     k = Call(prefix=[20], count=[2], new=[1, 1], own=[5, 5], Hq=4, H=2, D=64, P=16)
     base = dict(Q=k.q, cache=k.c.gpu, prefix_table=k.prefix_table, prefix_lens=i32([20]), page_table=k.table, kv_lens=i32([5, 5]))
