@@ -159,7 +159,7 @@ def run_compact(caches, P, table, lens, refs, width, what):
 def test_compact_many():
     """Several chunks of pages, the border inside one and at its edge."""
     rng = np.random.default_rng(5)
-    for n_pages, L in ((20000, 9000), (16384, 8192), (4097, 4096), (4096, 4096), (12289, 1), (30720, 20001), (30721, 16000),
+    for n_pages, L in ((20000, 9000), (16384, 8192), (4097, 4096), (4096, 4096), (12289, 1), (28672, 20001), (28673, 16000),
                        (40960, 8192), (36865, 36864), (45000, 0)):
         refs = np.zeros(n_pages, int)
         refs[rng.permutation(n_pages)[:L]] = rng.integers(1, 5, L)

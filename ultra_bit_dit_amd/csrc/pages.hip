@@ -129,7 +129,7 @@ __global__ void more_layers(PageLayer* to, Layers l) { put_layers(to, l); }
 // take themselves off its count, and where that leaves 0, the smallest of them is
 // written in its place.
 constexpr int kNearSeqs = 4096;       // sequences whose children and lengths lie in LDS
-constexpr int kNearPages = 30720;     // pages whose counts do
+constexpr int kNearPages = 28672;     // pages whose counts do
 constexpr int kFirst = INT32_MIN;     // + child: it keeps the page
 
 template <bool NEAR>
