@@ -577,7 +577,9 @@ typedef struct lowbit_kv8_prefix {
  * (table_width - k) * page_tokens).  A prefix need not end with a page.  Each
  * prefix is read once for all rows of its group, as a prompt's tokens are (in tiles
  * of 128 or 256 rows; 16 or 32 where the group has few); one row's sums over prefix
- * and own tokens are joined in fp32.  Sequences of no group have no
+ * and own tokens are joined in fp32.  Weights enter the second product in two bf16
+ * terms wherever max_q * q_heads / kv_heads is at most 64; with more rows they may be
+ * rounded once.  Sequences of no group have no
  * prefix.  Rows of a sequence behind its first max_q are not defined, should
  * q_starts have more.  Everything else is as lowbit_attention_kv8 says, limits included, for the
  * groups too (their rows: min(total_q, max_seqs * max_q)); max_len + max_kv <=

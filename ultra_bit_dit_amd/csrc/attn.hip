@@ -19,7 +19,10 @@
 // wave: 16 x 5 tokens in 2048, D = 64, 19.2 -> 20.1 us); with many rows, where the
 // products are, rounded once (off by 2^-8 at most, the output's own rounding): a
 // second term would take 2 x 4096 rows, 40 heads over 8, D = 128, from 383 to 497 us
-// and attn_prompt32<64> out of its registers (221 -> 511 us).
+// and attn_prompt32<64> out of its registers (221 -> 511 us).  Behind prefixes few rows
+// of many sequences fill prompt tiles too: where a sequence has at most kFineRows of a
+// key head, those have two terms as well (FINE; the batch of 64 below 93 -> 109 us, 45 x
+// 5 tokens 41 -> 50, 16 with D = 256 100 -> 109).
 //
 // MODE.  kPlain: a call's rows see the tokens of one sequence each.  The others are
 // of calls behind prefixes that groups of sequences share:
@@ -29,9 +32,9 @@
 //   kHead    groups in the place of sequences: the rows of a group's sequences, which lie
 //            in order, see its prefix, and leave their sums in the workspace;
 //   kTail    each sequence's rows see its own tokens, and take those sums in.
-// 64 single tokens behind 32760, 40 heads over 8, D = 128: 91 us (kHead 76, 43 GFLOP in tiles that
-// five heads fill to 0.83; kTail 21, its chain of length, page, codes, sums); 16 behind two prefixes of
-// 65000, 24 heads over 4, D = 256: 100 (74 + 28); 45 x 5 tokens behind six of 8000, D = 64: 41 (21 + 21); 8
+// 64 single tokens behind 32760, 40 heads over 8, D = 128: 109 us (43 GFLOP in tiles that
+// five heads fill to 0.83; kTail 21 of it, its chain of length, page, codes, sums); 16 behind two prefixes of
+// 65000, 24 heads over 4, D = 256: 109; 45 x 5 tokens behind six of 8000, D = 64: 50; 8
 // prompts of 777 behind 6001, 32 heads over 8, D = 128, in one kBehind launch: 470 to 510 by card (0.9 PFLOP/s).
 #include <hip/hip_runtime.h>
 
@@ -957,7 +960,7 @@ struct PromptTile {
   }
 };
 
-template <int D, int NC, int WAVES, int MODE>
+template <int D, int NC, int WAVES, int MODE, bool FINE>
 __global__ __launch_bounds__(64 * WAVES, 2) void attn_prompt(AttnArgs a) {
   constexpr int DS = D / 32, DT = D / 16, HALF = 32 * WAVES, SP = 4 * D / HALF;
   static_assert(SP * HALF == 4 * D, "whole 16-byte pieces per thread");
@@ -1108,7 +1111,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attn_prompt(AttnArgs a) {
 
   const int at = 16 * lane;
   v4f sc[NC][4];
-  v8bf pf[NC][2];
+  v8bf pf[NC][2], pl[FINE ? NC : 1][2];  // weights; FINE: and what their rounding left
   auto sees = [&](int u) { return u * kUnit < whi && u * kUnit + kUnit > wlo; };
   // scores of step u
   auto scores = [&](int u) {
@@ -1177,7 +1180,10 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attn_prompt(AttnArgs a) {
 #pragma unroll
         for (int e = f; e < 4; e += 2)
 #pragma unroll
-          for (int c = 0; c < NC; c++) o[c][d + (e >> 1)] = mfma(vf[(d >> 1) & 1][e], pf[c][f], o[c][d + (e >> 1)]);
+          for (int c = 0; c < NC; c++) {
+            o[c][d + (e >> 1)] = mfma(vf[(d >> 1) & 1][e], pf[c][f], o[c][d + (e >> 1)]);
+            if constexpr (FINE) o[c][d + (e >> 1)] = mfma(vf[(d >> 1) & 1][e], pl[c][f], o[c][d + (e >> 1)]);
+          }
       __builtin_amdgcn_sched_barrier(0);
     }
   };
@@ -1217,7 +1223,9 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attn_prompt(AttnArgs a) {
       for (int e = 0; e < 16; e++) {
         const float p = __builtin_amdgcn_exp2f(fmaf(sc[c][e >> 2][e & 3], scale, -mu));  // masked: 2^-inf = 0
         sum[e & 3] += p;
-        pf[c][e >> 3][e & 7] = (__bf16)p;
+        const __bf16 hi = (__bf16)p;
+        pf[c][e >> 3][e & 7] = hi;
+        if constexpr (FINE) pl[c][e >> 3][e & 7] = (__bf16)(p - (float)hi);
       }
       l[c] += (sum[0] + sum[1]) + (sum[2] + sum[3]);
     }
@@ -1300,7 +1308,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attn_prompt(AttnArgs a) {
 // busy in 24% of the cycles, LDS is active in 20%; vector instructions take 47% at
 // four cycles each and the exponentials' quarter rate some 17% more (2 x 4096 in
 // 4096, 32 heads over 8: 226 us).  One register is spilled.
-template <int D, int NC, int WAVES, int OCC, int MODE>
+template <int D, int NC, int WAVES, int OCC, int MODE, bool FINE>
 __global__ __launch_bounds__(64 * WAVES, OCC) void attn_prompt32(AttnArgs a) {
   constexpr int DS = D / 16, DT = D / 32, HALF = 32 * WAVES, SP = 4 * D / HALF, PS = WAVES / 4;
   static_assert(SP * HALF == 4 * D, "whole 16-byte pieces per thread");
@@ -1450,7 +1458,8 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void attn_prompt32(AttnArgs a) {
   };
 
   v16f sc[NC][2];
-  v8bf pf[NC][4];  // weights of 8 tokens: tile, first or second eight of the lane's 16
+  // weights of 8 tokens: tile, first or second eight of the lane's 16; FINE: and what their rounding left
+  v8bf pf[NC][4], pl[FINE ? NC : 1][4];
   auto sees = [&](int u) { return u * kUnit < whi && u * kUnit + kUnit > wlo; };
   auto mul = [](const v8bf& x, const v8bf& y, const v16f& z) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, y, z, 0, 0, 0);
@@ -1477,6 +1486,7 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void attn_prompt32(AttnArgs a) {
         } else {         // operand 4 (st - KST) + e: tokens / DT, dims % DT
           const int i = 4 * (st - KST) + e;
           o[c][i % DT] = mul(f[st & 1][e], pf[c][i / DT], o[c][i % DT]);
+          if constexpr (FINE) o[c][i % DT] = mul(f[st & 1][e], pl[c][i / DT], o[c][i % DT]);
         }
       }
   };
@@ -1581,7 +1591,9 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void attn_prompt32(AttnArgs a) {
       for (int e = 0; e < 32; e++) {
         const float p = __builtin_amdgcn_exp2f(fmaf(sc[c][e >> 4][e & 15], scale, -mu));  // masked: 2^-inf = 0
         sum[e & 3] += p;
-        pf[c][e >> 3][e & 7] = (__bf16)p;
+        const __bf16 hi = (__bf16)p;
+        pf[c][e >> 3][e & 7] = hi;
+        if constexpr (FINE) pl[c][e >> 3][e & 7] = (__bf16)(p - (float)hi);
       }
       l[c] += (sum[0] + sum[1]) + (sum[2] + sum[3]);
     }
@@ -1775,7 +1787,10 @@ bool many_rows(const KvArgs& kv, int64_t R) {
 // waves; 2 x 4096 in 4096, 40 heads over 8, 411 us with 128 rows and 376 with 256,
 // 16 x 64 in 1024 50 and 42, 16 x 5 in 2048, 32 heads, 26 and 35).
 int prompt_rows(int D, int64_t R) { return D == 128 && R > 128 ? 256 : 128; }
-int prompt_slots(int D, int64_t R) { return D == 64 ? 768 : D == 128 && R <= 128 ? 512 : 256; }
+// fine: weights in two terms, whose registers leave two workgroups of D = 64 (three spill 16 to 66 of them).
+int prompt_slots(int D, int64_t R, bool fine = false) {
+  return D == 64 ? (fine ? 512 : 768) : D == 128 && R <= 128 ? 512 : 256;
+}
 
 // window: 0 where rows see everything before them or more
 Plan plan_attention(const KvArgs& kv, int64_t G, int64_t window) {
@@ -1797,13 +1812,14 @@ Plan plan_attention(const KvArgs& kv, int64_t G, int64_t window) {
   return p;
 }
 
-template <int MODE>
+template <int MODE, bool FINE = false>
 void launch_prompt(int rows, unsigned blocks, const AttnArgs& a, hipStream_t s) {
   const dim3 grid(blocks);
-  if (a.kv.D == 64) hipLaunchKernelGGL((attn_prompt32<64, 1, 4, 3, MODE>), grid, dim3(256), 0, s, a);
-  else if (a.kv.D == 128 && rows == 128) hipLaunchKernelGGL((attn_prompt32<128, 1, 4, 2, MODE>), grid, dim3(256), 0, s, a);
-  else if (a.kv.D == 128) hipLaunchKernelGGL((attn_prompt32<128, 1, 8, 2, MODE>), grid, dim3(512), 0, s, a);
-  else hipLaunchKernelGGL((attn_prompt<256, 1, 8, MODE>), grid, dim3(512), 0, s, a);
+  if (a.kv.D == 64) hipLaunchKernelGGL((attn_prompt32<64, 1, 4, FINE ? 2 : 3, MODE, FINE>), grid, dim3(256), 0, s, a);
+  else if (a.kv.D == 256) hipLaunchKernelGGL((attn_prompt<256, 1, 8, MODE, FINE>), grid, dim3(512), 0, s, a);
+  else if (rows == 128) hipLaunchKernelGGL((attn_prompt32<128, 1, 4, 2, MODE, FINE>), grid, dim3(256), 0, s, a);
+  else if constexpr (MODE != kBehind || !FINE)  // of sequences with few rows the tiles have 128
+    hipLaunchKernelGGL((attn_prompt32<128, 1, 8, 2, MODE, FINE>), grid, dim3(512), 0, s, a);
 }
 // tiles: of all heads
 template <int MODE>
@@ -1843,9 +1859,10 @@ double wg_time(int D, int64_t rows, double fill, int64_t wgs, double steps) {
 // tiles (of at most `most`, for which there is to be room) cut into the parts that take
 // the least time; `sums`: us to write and read one part of each, `join`: us that
 // joining takes beside that
-double cut_time(int D, int64_t rows, double fill, int64_t tiles, int64_t most, int64_t steps, double sums, double join, int* parts) {
+double cut_time(int D, int64_t rows, bool fine, double fill, int64_t tiles, int64_t most, int64_t steps, double sums, double join,
+                int* parts) {
   double least = 1e30;
-  const int64_t slots = prompt_slots(D, rows);
+  const int64_t slots = prompt_slots(D, rows, fine);
   for (int64_t k = 1; k <= best_parts(steps) && (k == 1 || most * k <= 4 * slots); k++) {
     const double t = (double)cdiv(tiles * k, slots) * wg_time(D, rows, fill, std::min(tiles * k, slots), (double)steps / (double)k) +
                      (k > 1 || join == 0. ? sums * (double)k + join : 0.);
@@ -1903,6 +1920,7 @@ double tail_time(int D, int64_t rows, int64_t tiles, int64_t blocks, int64_t pie
 // workgroup (of the 450 calls those with 2 to 4 took 0.72 to 0.87 of the time, with 4 to 8 0.9, with more 1.0 to 1.25,
 // as sequences differ in length).
 constexpr int64_t kMostBlocks = 1 << 22;  // of a launch
+constexpr int64_t kFineRows = 64;         // of a sequence and key head: eight tokens of eight heads
 PrefixPlan plan_prefix_of(const AttnArgs& a) {
   const KvArgs &kv = a.kv, &prefix = a.prefix;
   const int D = kv.D;
@@ -1916,8 +1934,9 @@ PrefixPlan plan_prefix_of(const AttnArgs& a) {
   // tiles of the sequences' rows, all steps
   PrefixPlan one = {};
   one.behind = true;
+  one.fine = Rs <= kFineRows;
   one.rows = prompt_rows(D, Rs);
-  const int64_t slots = prompt_slots(D, Rs), most = tiles_of(kv, a.G, one.rows);
+  const int64_t slots = prompt_slots(D, Rs, one.fine), most = tiles_of(kv, a.G, one.rows);
   // tiles to be expected: each sequence's last one half full, but one of each
   const int64_t tiles =
       std::min(most, kv.H * std::max(kv.n_seqs, kv.total_q * a.G / one.rows + (kv.n_seqs + 1) / 2));
@@ -1927,13 +1946,15 @@ PrefixPlan plan_prefix_of(const AttnArgs& a) {
   const double one_fill = (double)std::min<int64_t>(Rs, one.rows) / (double)one.rows;
   double one_time = (double)(one.whole * kv.H) / (double)slots * wg_time(D, one.rows, one_fill, slots, (double)steps);
   if (rest)
-    one_time += cut_time(D, one.rows, one_fill, rest, most - one.whole * kv.H, steps,
+    one_time += cut_time(D, one.rows, one.fine, one_fill, rest, most - one.whole * kv.H, steps,
                          one_fill * (double)(rest * one.rows * row_bytes) * 2. / kRate, 4. + 0.03 * (double)rest, &one.parts);
   if (one.parts == 1) one.whole = (int)(most / kv.H);
   one.cut = most - one.whole * kv.H;
   one.blocks = one.whole * kv.H + one.cut * one.parts;
   one.part = (size_t)(one.cut * one.parts * one.rows * row_bytes);
   one_time = 0.92 * one_time + (D == 64 ? 3.7 : D == 256 ? 1.9 : one.rows == 128 ? 4.9 : 10.3);
+  if (one.fine && D == 128) one_time *= 1.15;  // the second terms; with other heads the times' spread is larger
+  if (Rs <= 8) one_time = 1e30;  // tiles filled to a sixteenth: of 252 such calls none took less than 0.98 of the others' time
 
   // the same in attn_decode
   const int nc = decode_nc(Rs);
@@ -1944,6 +1965,7 @@ PrefixPlan plan_prefix_of(const AttnArgs& a) {
 
   // groups, then sequences
   PrefixPlan two = {};
+  two.fine = Rs <= kFineRows;
   two.parts = 1;
   two.tail_nc = nc;
   // as many pieces of a tile as fill the chip
@@ -1956,7 +1978,7 @@ PrefixPlan plan_prefix_of(const AttnArgs& a) {
     // 256 rows a tile where that is not a fifth more of them than in tiles of 128
     two.rows = prompt_rows(D, cdiv(Rg, 256) * 256 * 5 < cdiv(Rg, 128) * 128 * 6 ? Rg : 128);
     const int64_t group_tiles = tiles_of(prefix, a.G, two.rows);
-    two_time += cut_time(D, two.rows, (double)std::min<int64_t>(Rg, two.rows) / (double)two.rows, group_tiles, group_tiles, head_steps,
+    two_time += cut_time(D, two.rows, two.fine, (double)std::min<int64_t>(Rg, two.rows) / (double)two.rows, group_tiles, group_tiles, head_steps,
                          (double)(kv.total_q * a.Hq * row_bytes) * 2. / kRate, 0., &two.parts);
     two.blocks = group_tiles * two.parts;
   } else {
@@ -2023,7 +2045,8 @@ hipError_t launch_attention_prefix(AttnArgs a, const PrefixPlan& p, void* ws, hi
     if (p.nc > 0) {
       launch_decode<kBehind>(p.nc, (unsigned)p.blocks, a, s);
     } else {
-      launch_prompt<kBehind>(p.rows, (unsigned)p.blocks, a, s);
+      if (p.fine) launch_prompt<kBehind, true>(p.rows, (unsigned)p.blocks, a, s);
+      else launch_prompt<kBehind>(p.rows, (unsigned)p.blocks, a, s);
       if (p.parts > 1) launch_join<kBehind>(p.rows, p.cut, a, s);
     }
     return hipGetLastError();
@@ -2032,6 +2055,7 @@ hipError_t launch_attention_prefix(AttnArgs a, const PrefixPlan& p, void* ws, hi
   head.kv = a.prefix;
   head.causal = 0;
   if (p.nc > 0) launch_decode<kHead>(p.nc, (unsigned)p.blocks, head, s);
+  else if (p.fine) launch_prompt<kHead, true>(p.rows, (unsigned)p.blocks, head, s);
   else launch_prompt<kHead>(p.rows, (unsigned)p.blocks, head, s);
   launch_decode<kTail>(p.tail_nc, (unsigned)p.tail_blocks, a, s);
   return hipGetLastError();

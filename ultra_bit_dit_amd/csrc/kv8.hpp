@@ -155,6 +155,7 @@ struct AttnArgs {
 // Of a call behind shared prefixes: one launch, or the groups' and the sequences'.
 struct PrefixPlan {
   bool behind;               // one launch
+  bool fine;                 // prompt tiles take weights in two terms
   // of that, else of the groups'.  nc 0: prompt tiles of `rows` rows in `parts` parts, the
   // first `whole` of a head uncut; else attn_decode with nc column tiles.
   int nc, rows, parts, whole;
