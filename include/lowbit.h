@@ -556,8 +556,9 @@ int lowbit_attention_kv8_workspace(const lowbit_kv8* cache, const lowbit_kv8_bat
  * / n_groups each, in order.  max_seqs and max_len bound the sequences of any one
  * group and its lengths; they size the launch, so keep them close.  Arrays are read
  * on the device, as those of lowbit_kv8_batch, and can not lead a kernel outside the
- * buffers either: lengths are cut to max_len, sequences to the batch's, a group's rows to
- * max_seqs * max_q. */
+ * buffers either: lengths are cut to max_len, sequences to the batch's.  q_starts may
+ * leave rows between the sequences (more than max_q for one: its first max_q are its
+ * tokens); such rows, and sequences beyond max_seqs, cost time and change no result. */
 typedef struct lowbit_kv8_prefix {
   int64_t n_groups;
   const int32_t* page_table; /* device [n_groups][table_width] */
@@ -580,8 +581,8 @@ typedef struct lowbit_kv8_prefix {
  * and own tokens are joined in fp32.  Weights enter the second product in two bf16
  * terms wherever max_q * q_heads / kv_heads is at most 64; with more rows they may be
  * rounded once.  Sequences of no group have no
- * prefix.  Rows of a sequence behind its first max_q are not defined, should
- * q_starts have more.  Everything else is as lowbit_attention_kv8 says, limits included, for the
+ * prefix.  Rows of a sequence behind its first max_q are left as they were,
+ * should q_starts have more.  Everything else is as lowbit_attention_kv8 says, limits included, for the
  * groups too (their rows: min(total_q, max_seqs * max_q)); max_len + max_kv <=
  * 2^30; total_q * q_heads * (head_dim + 4) <= 2^38.
  * Needs workspace in every case (lowbit_attention_kv8_prefix_workspace).

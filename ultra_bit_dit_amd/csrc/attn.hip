@@ -1840,9 +1840,10 @@ void launch_decode(int nc, unsigned blocks, const AttnArgs& a, hipStream_t s) {
 }
 
 // bound on the tiles of all heads
-int64_t tiles_of(const KvArgs& kv, int64_t G, int64_t rows) {
-  return std::min<int64_t>(kv.n_seqs * kv.H * cdiv(kv.max_q * G, rows), kv.H * (kv.total_q * G / rows + kv.n_seqs));
+int64_t tiles_of(const KvArgs& kv, int64_t G, int64_t rows, int64_t max_q) {
+  return std::min<int64_t>(kv.n_seqs * kv.H * cdiv(max_q * G, rows), kv.H * (kv.total_q * G / rows + kv.n_seqs));
 }
+int64_t tiles_of(const KvArgs& kv, int64_t G, int64_t rows) { return tiles_of(kv, G, rows, kv.max_q); }
 int best_parts(int64_t steps) { return (int)std::max<int64_t>((int64_t)(2.0 * sqrt((double)steps)), 1); }
 
 // us of a prompt workgroup over some steps, `wgs` of them at work at once, `fill` of
@@ -1924,7 +1925,7 @@ constexpr int64_t kFineRows = 64;         // of a sequence and key head: eight t
 PrefixPlan plan_prefix_of(const AttnArgs& a) {
   const KvArgs &kv = a.kv, &prefix = a.prefix;
   const int D = kv.D;
-  const int64_t Rs = kv.max_q * a.G, Rg = prefix.max_q * a.G, row_bytes = (D + kPartPad) * 4;
+  const int64_t Rs = kv.max_q * a.G, Rg = a.group_q * a.G, row_bytes = (D + kPartPad) * 4;
   const int64_t head_steps = cdiv(prefix.max_kv, kUnit), own_steps = cdiv(kv.max_kv, kUnit), steps = head_steps + own_steps;
   constexpr double kRate = 4.8e6;  // bytes a us
   auto decode_nc = [&](int64_t R) { return R > 16 && D == 64 ? 2 : 1; };
@@ -1977,15 +1978,15 @@ PrefixPlan plan_prefix_of(const AttnArgs& a) {
   if (many_rows(prefix, Rg)) {
     // 256 rows a tile where that is not a fifth more of them than in tiles of 128
     two.rows = prompt_rows(D, cdiv(Rg, 256) * 256 * 5 < cdiv(Rg, 128) * 128 * 6 ? Rg : 128);
-    const int64_t group_tiles = tiles_of(prefix, a.G, two.rows);
-    two_time += cut_time(D, two.rows, two.fine, (double)std::min<int64_t>(Rg, two.rows) / (double)two.rows, group_tiles, group_tiles, head_steps,
+    const int64_t group_tiles = tiles_of(prefix, a.G, two.rows, a.group_q), room = tiles_of(prefix, a.G, two.rows);
+    two_time += cut_time(D, two.rows, two.fine, (double)std::min<int64_t>(Rg, two.rows) / (double)two.rows, group_tiles, room, head_steps,
                          (double)(kv.total_q * a.Hq * row_bytes) * 2. / kRate, 0., &two.parts);
-    two.blocks = group_tiles * two.parts;
+    two.blocks = room * two.parts;
   } else {
     two.nc = decode_nc(Rg);
     two.blocks = shares;
     two.part = std::max(two.part, decode_part(two.nc));
-    two_time += decode_time(D, Rg, tiles_of(prefix, a.G, 16 * two.nc), cdiv(head_steps, kDecWaves));
+    two_time += decode_time(D, Rg, tiles_of(prefix, a.G, 16 * two.nc, a.group_q), cdiv(head_steps, kDecWaves));
   }
   two.sums = (size_t)(two.parts * kv.total_q * a.Hq * row_bytes);
 

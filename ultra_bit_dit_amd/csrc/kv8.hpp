@@ -145,6 +145,7 @@ struct AttnArgs {
   int parts;                 // of a prompt tile
   // behind shared prefixes
   KvArgs prefix;             // their groups
+  int64_t group_q;           // rows of each of them to be expected; at most prefix.max_q
   float* sums;               // [parts][total_q][Hq] sums of the rows over their prefixes, before the division
   int sums_parts;            // as how many parts at most
   int whole;                 // tiles of a head whose steps are not cut into parts
