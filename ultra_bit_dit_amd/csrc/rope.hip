@@ -11,7 +11,7 @@
 // Bound by memory: 8191 x 28 heads of 256, fp32 to bf16, 73 us (4.8 TB/s, as a 4 GiB copy);
 // 18432 x 40 heads of 128, bf16, three axes, adjacent pairs, 79 us (4.8 TB/s); one token,
 // 48 heads of 128, 4.8 us (the launch, a load, the sums, a store).  Heads whose lanes are no
-// power of two leave some idle: 16384 x 25 heads of 96 3.9 TB/s, of 72 2.4 TB/s (more
+// power of two leave some idle: 16384 x 25 heads of 96 3.9 TB/s, of 72 3.2 TB/s (more
 // loads on their way at once made those 5 to 25% slower).
 //
 // A wave has one token and a run of its heads.  Each lane finds the sine and
@@ -145,6 +145,8 @@ __global__ __launch_bounds__(64 * kWaves) void qk_norm_rope(RopeArgs a, int lg, 
   const int d0 = a.adjacent || half ? at * W : at * 2 * W;
   const int d1 = a.adjacent ? a.D / 2 + at * W : half ? a.pairs + at * W : d0 + W;
   const bool turn0 = half || (a.adjacent && d0 < 2 * a.pairs), turn1 = half || (a.adjacent && d1 < 2 * a.pairs);
+  // the pair whose elements the lane has: e and W + e, or 2 e and 2 e + 1 of its 2 W
+  auto pair_at = [&](int e) -> int { return !a.adjacent ? at * W + e : e < W / 2 ? d0 / 2 + e : d1 / 2 + e - W / 2; };
   const int heads = a.Hq + a.Hk, passes = (per + teams - 1) / teams;
   const int64_t items = a.tokens * slices, first = (int64_t)blockIdx.x * kWaves + wave, stride = (int64_t)gridDim.x * kWaves;
 
@@ -196,6 +198,18 @@ __global__ __launch_bounds__(64 * kWaves) void qk_norm_rope(RopeArgs a, int lg, 
     freq[k] = i < a.pairs ? a.freqs[i] : 0.;
     row[k] = i < a.pairs && axis >= 0 && axis < a.axes ? axis * a.pos_stride : -1;
   }
+  // Bit e: its pair has no axis.  It is left out rather than turned by nothing: 0 times
+  // an infinity would be NaN.
+  uint32_t stay = 0;
+  bool some_stay = false;
+  if (a.pair_axis) {
+#pragma unroll
+    for (int e = 0; e < W; e++) {
+      const int axis = mine && (e < W / 2 ? turn0 : turn1) ? a.pair_axis[pair_at(e)] : 0;
+      stay |= axis >= 0 && axis < a.axes ? 0u : 1u << e;
+    }
+    some_stay = __any(stay != 0);
+  }
   auto positions = [&](int64_t i) {
     const int64_t t = item_at(i).t;
 #pragma unroll
@@ -227,9 +241,7 @@ __global__ __launch_bounds__(64 * kWaves) void qk_norm_rope(RopeArgs a, int lg, 
         __builtin_amdgcn_wave_barrier();
 #pragma unroll
         for (int e = 0; e < W; e++) {
-          // of the pair whose elements the lane has: e and W + e, or 2 e and 2 e + 1 of its 2 W
-          const int i = !a.adjacent ? at * W + e : e < W / 2 ? d0 / 2 + e : d1 / 2 + e - W / 2;
-          cs[e] = mine && (e < W / 2 ? turn0 : turn1) ? turn[i] : make_float2(1.f, 0.f);
+          cs[e] = mine && (e < W / 2 ? turn0 : turn1) ? turn[pair_at(e)] : make_float2(1.f, 0.f);
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
@@ -266,13 +278,38 @@ __global__ __launch_bounds__(64 * kWaves) void qk_norm_rope(RopeArgs a, int lg, 
         for (int e = 0; e < 2 * W; e++) y[e] = x[e];
         if (turn0) {
 #pragma unroll
-          for (int e = 0; e < W; e++) {
+          for (int e = 0; e < W / 2; e++) {
             if (a.adjacent) {
               y[2 * e] = x[2 * e] * cs[e].x - x[2 * e + 1] * cs[e].y;
               y[2 * e + 1] = x[2 * e + 1] * cs[e].x + x[2 * e] * cs[e].y;
             } else {
               y[e] = x[e] * cs[e].x - x[W + e] * cs[e].y;
               y[W + e] = x[W + e] * cs[e].x + x[e] * cs[e].y;
+            }
+          }
+        }
+        if (turn1) {
+#pragma unroll
+          for (int e = W / 2; e < W; e++) {
+            if (a.adjacent) {
+              y[2 * e] = x[2 * e] * cs[e].x - x[2 * e + 1] * cs[e].y;
+              y[2 * e + 1] = x[2 * e + 1] * cs[e].x + x[2 * e] * cs[e].y;
+            } else {
+              y[e] = x[e] * cs[e].x - x[W + e] * cs[e].y;
+              y[W + e] = x[W + e] * cs[e].x + x[e] * cs[e].y;
+            }
+          }
+        }
+        if (some_stay) {
+#pragma unroll
+          for (int e = 0; e < W; e++) {
+            const bool is = (stay >> e) & 1u;
+            if (a.adjacent) {
+              y[2 * e] = is ? x[2 * e] : y[2 * e];
+              y[2 * e + 1] = is ? x[2 * e + 1] : y[2 * e + 1];
+            } else {
+              y[e] = is ? x[e] : y[e];
+              y[W + e] = is ? x[W + e] : y[W + e];
             }
           }
         }
