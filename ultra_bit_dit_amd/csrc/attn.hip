@@ -140,13 +140,16 @@ struct Head {
     const int64_t g = group_of(a.prefix, b);
     take(a, g, g < 0 ? 0 : a.prefix.lens[g]);
   }
-  // the same, each lane's own b, where the groups may be at hand
+  // the same, each lane's own b, where the groups may be at hand; all lanes call it, as any of
+  // them may have a group that others ask for
   __device__ __forceinline__ void find(const AttnArgs& a, int64_t b, const FirstGroups& groups) {
     if (a.prefix.n_seqs > 16) return find(a, b);
     take(a, -1, 0);
-    for (int g = (int)a.prefix.n_seqs - 1; g >= 0; g--)
-      if (__builtin_amdgcn_readlane(groups.first, g) <= b && b < __builtin_amdgcn_readlane(groups.last, g))
-        take(a, g, __builtin_amdgcn_readlane(groups.len, g));
+    for (int g = (int)a.prefix.n_seqs - 1; g >= 0; g--) {
+      const int from = __builtin_amdgcn_readlane(groups.first, g), to = __builtin_amdgcn_readlane(groups.last, g);
+      const int n = __builtin_amdgcn_readlane(groups.len, g);
+      if (from <= b && b < to) take(a, g, n);
+    }
   }
   __device__ __forceinline__ int tokens() const { return MODE == kBehind ? steps * kUnit : 0; }
   __device__ __forceinline__ bool has(int t) const { return MODE == kBehind && t < steps * kUnit; }
@@ -299,11 +302,10 @@ __global__ __launch_bounds__(64 * kDecWaves, D * NC <= 128 ? 2 : 1) void attn_de
   if (near) {
     FirstGroups groups;
     if constexpr (MODE == kBehind || MODE == kTail) groups.read(a.prefix);
-    if (lane < a.kv.n_seqs) {
-      mine = seq_span<MODE == kHead>(a.kv, lane);
-      if constexpr (MODE == kBehind || MODE == kTail) my_head.find(a, lane, groups);
-      mine.len += my_head.tokens();
-    }
+    const int64_t b = min((int64_t)lane, a.kv.n_seqs - 1);
+    mine = seq_span<MODE == kHead>(a.kv, b);
+    if constexpr (MODE == kBehind || MODE == kTail) my_head.find(a, b, groups);
+    mine.len += my_head.tokens();
   }
   auto span_for_all = [&](int64_t i, Head<MODE>* head) -> SeqSpan {
     if (!near) return span_of(i, head);
