@@ -594,6 +594,20 @@ int lowbit_attention_kv8_prefix(const lowbit_kv8* cache, const lowbit_kv8_prefix
 int lowbit_attention_kv8_prefix_workspace(const lowbit_kv8* cache, const lowbit_kv8_prefix* prefix,
                                           const lowbit_kv8_batch* batch, int64_t q_heads, size_t* bytes);
 
+/* What lowbit_attention_kv8_prefix runs for these arguments (host-only): the
+ * bounds decide, so this shows what a loose one costs. */
+typedef struct lowbit_kv8_prefix_plan {
+  int launches;     /* 1: prefix and own tokens together; 2: the groups over their prefixes, then the sequences */
+  int tile_rows;    /* of the first: 16 or 32 read by each wave from the cache, or 128 or 256 of a workgroup */
+  int tile_parts;   /* that a tile's tokens are cut into at most; 0: as equal shares of all tokens fall */
+  int whole_tiles;  /* of a key head that are not cut (launches 1, tile_rows from 128) */
+  int own_rows;     /* launches 2: tile_rows and tile_parts of the second; else 0 */
+  int own_parts;
+  int weight_terms; /* bf16 terms of a weight, 1 or 2 */
+} lowbit_kv8_prefix_plan;
+int lowbit_attention_kv8_prefix_launches(const lowbit_kv8* cache, const lowbit_kv8_prefix* prefix,
+                                         const lowbit_kv8_batch* batch, int64_t q_heads, lowbit_kv8_prefix_plan* plan);
+
 /* =====================  heads of queries and keys  ========================
  * Between a fused q/k/v product and lowbit_kv8_append / lowbit_attention_kv8
  * (or a diffusion transformer's attention): each head's norm and its rotation

@@ -734,6 +734,25 @@ int lowbit_attention_kv8_prefix_workspace(const lowbit_kv8* cache, const lowbit_
   return LOWBIT_OK;
 }
 
+int lowbit_attention_kv8_prefix_launches(const lowbit_kv8* cache, const lowbit_kv8_prefix* prefix,
+                                         const lowbit_kv8_batch* batch, int64_t q_heads, lowbit_kv8_prefix_plan* plan) {
+  if (!plan) return LOWBIT_E_NULL;
+  *plan = {};
+  AttnArgs a = {};
+  PrefixPlan p;
+  const int rc = prefix_check(cache, prefix, batch, q_heads, &a, &p);
+  if (rc) return rc;
+  const bool few = p.nc > 0;
+  plan->launches = p.behind ? 1 : 2;
+  plan->tile_rows = few ? 16 * p.nc : p.rows;
+  plan->tile_parts = !few ? p.parts : p.behind ? p.pieces : 0;
+  plan->whole_tiles = p.behind && !few ? p.whole : 0;
+  plan->own_rows = p.behind ? 0 : 16 * p.tail_nc;
+  plan->own_parts = p.behind ? 0 : p.pieces;
+  plan->weight_terms = few || p.fine ? 2 : 1;
+  return LOWBIT_OK;
+}
+
 int lowbit_attention_kv8_prefix(const lowbit_kv8* cache, const lowbit_kv8_prefix* prefix,
                                 const lowbit_kv8_batch* batch, int64_t q_heads, const uint16_t* Q_bf16,
                                 int64_t q_stride, float softmax_scale, int causal, uint16_t* O_bf16,

@@ -28,7 +28,8 @@ EXPORTS = ("lowbit_abi_version", "lowbit_status_str", "lowbit_packed_bytes", "lo
            "lowbit_hbm_read_probe", "lowbit_quantize_weights", "lowbit_rotate_act",
            "lowbit_mxfp4_bytes", "lowbit_pack_mxfp4", "lowbit_quantize_mxfp4", "lowbit_gemm_mxfp4", "lowbit_gemm_mxfp4_workspace",
            "lowbit_kv8_append", "lowbit_attention_kv8", "lowbit_attention_kv8_workspace",
-           "lowbit_attention_kv8_prefix", "lowbit_attention_kv8_prefix_workspace", "lowbit_qk_norm_rope", "lowbit_kv8_fork", "lowbit_kv8_fork_workspace", "lowbit_kv8_compact",
+           "lowbit_attention_kv8_prefix", "lowbit_attention_kv8_prefix_workspace", "lowbit_attention_kv8_prefix_launches",
+           "lowbit_qk_norm_rope", "lowbit_kv8_fork", "lowbit_kv8_fork_workspace", "lowbit_kv8_compact",
            "lowbit_kv8_compact_workspace")
 
 
@@ -59,6 +60,12 @@ class Kv8Prefix(ctypes.Structure):
     _fields_ = [("n_groups", ctypes.c_int64), ("page_table", ctypes.c_void_p), ("table_width", ctypes.c_int64),
                 ("lens", ctypes.c_void_p), ("seq_starts", ctypes.c_void_p), ("max_seqs", ctypes.c_int64),
                 ("max_len", ctypes.c_int64)]
+
+
+class Kv8PrefixPlan(ctypes.Structure):
+    """lowbit_kv8_prefix_plan"""
+    _fields_ = [(n, ctypes.c_int) for n in ("launches", "tile_rows", "tile_parts", "whole_tiles", "own_rows", "own_parts",
+                                            "weight_terms")]
 
 
 class Rope(ctypes.Structure):
@@ -121,6 +128,7 @@ def lib():
         kpp = ctypes.POINTER(Kv8Prefix)
         L.lowbit_attention_kv8_prefix.argtypes = [kvp, kpp, kbp, i64, vp, i64, ctypes.c_float, i32, vp, i64, vp, vp]
         L.lowbit_attention_kv8_prefix_workspace.argtypes = [kvp, kpp, kbp, i64, szp]
+        L.lowbit_attention_kv8_prefix_launches.argtypes = [kvp, kpp, kbp, i64, ctypes.POINTER(Kv8PrefixPlan)]
         L.lowbit_qk_norm_rope.argtypes = [ctypes.POINTER(Rope), i32, vp, i64, i64, vp, vp, i64, i64, vp, ctypes.c_float, i32,
                                           vp, i64, vp, i64, vp]
         L.lowbit_kv8_fork.argtypes = [kvp, i64, i64, vp, i64, vp, vp, i64, vp, vp, i64, vp, i64, vp, vp, vp, vp]
@@ -720,6 +728,19 @@ def attention_kv8_prefix_workspace(cache, prefix_table, prefix_lens, page_table,
            lib().lowbit_attention_kv8_prefix_workspace(Kv8.from_buffer_copy(c), Kv8Prefix.from_buffer_copy(p),
                                                        Kv8Batch.from_buffer_copy(b), q_heads, ctypes.byref(n)))
     return n.value
+
+
+def attention_kv8_prefix_launches(cache, prefix_table, prefix_lens, page_table, kv_lens, q_heads, total_q, seq_starts=None,
+                                  q_starts=None, max_q=None, max_kv=None, max_prefix=None, max_seqs=None):
+    """What lowbit_attention_kv8_prefix runs for these arguments: the fields of lowbit_kv8_prefix_plan by name."""
+    T = _torch or _load()
+    c, p, b, _ = _prefix(T, cache, prefix_table, prefix_lens, page_table, kv_lens, seq_starts, q_starts, total_q, max_q, max_kv,
+                         max_prefix, max_seqs, None)
+    plan = Kv8PrefixPlan()
+    _check("lowbit_attention_kv8_prefix_launches",
+           lib().lowbit_attention_kv8_prefix_launches(Kv8.from_buffer_copy(c), Kv8Prefix.from_buffer_copy(p),
+                                                      Kv8Batch.from_buffer_copy(b), q_heads, ctypes.byref(plan)))
+    return {n: getattr(plan, n) for n, _ in plan._fields_}
 
 
 def _weight(T, w, D, what):
