@@ -64,17 +64,3 @@ def test_weight_terms():
                         p = launches(2 * G, 2, D, 64, told, 1, seqs, seqs, seqs * q, q, q + 100)
                         assert p["weight_terms"] == 2 or q * G > 64
     assert launches(8, 2, 128, 64, 3000, 1, 8, 8, 8 * 300, 300, 400)["weight_terms"] == 1
-
-
-def test_through_the_binding():
-    """The plan's fields by name; a loose bound on the new tokens costs the shared prefix."""
-    import torch
-    cache = lb.empty_kv8(8, 64, 2, 128, device="cpu")
-    i32 = lambda *x: torch.zeros(x, dtype=torch.int32)
-    args = (cache, i32(1, 500), i32(1), i32(64, 8), i32(64), 8, 64)
-    tight = lb.attention_kv8_prefix_launches(*args, q_starts=i32(65), max_q=1, max_kv=500)
-    assert tight == launches(8, 2, 128, 64, 500 * 64, 1, 64, 64, 64, 1, 500)
-    assert set(tight) == {n for n, _ in lb.Kv8PrefixPlan._fields_} and tight["launches"] == 2 and tight["weight_terms"] == 2
-    assert lb.attention_kv8_prefix_launches(*args, q_starts=i32(65), max_kv=500)["launches"] == 1
-    with pytest.raises(lb.LowbitError):
-        lb.attention_kv8_prefix_launches(*args[:5], 7, 64)
