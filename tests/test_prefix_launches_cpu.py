@@ -64,3 +64,22 @@ def test_weight_terms():
                         p = launches(2 * G, 2, D, 64, told, 1, seqs, seqs, seqs * q, q, q + 100)
                         assert p["weight_terms"] == 2 or q * G > 64
     assert launches(8, 2, 128, 64, 3000, 1, 8, 8, 8 * 300, 300, 400)["weight_terms"] == 1
+
+
+@pytest.mark.parametrize("D,G", [(64, 4), (128, 5), (256, 6)])
+def test_rows_between_sequences_are_reckoned_with(D, G):
+    """A batch padded to many rows a sequence fills as many tiles as one that has them."""
+    args = dict(Hq=8 * G, H=8, D=D, P=64, max_prefix=20000, groups=2, max_seqs=32, seqs=64, max_q=1, max_kv=100)
+    tight, loose = launches(total_q=64, **args), launches(total_q=64 * 64, **args)
+    assert tight["launches"] == 2 and (loose["launches"] == 1 or loose["tile_parts"] < tight["tile_parts"])
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_groups_of_more_rows_than_int_counts(D):
+    """More than 2^30 rows of a key head in the batch: a padded group could have them all, so it is not asked for."""
+    for H, G, groups, seqs in ((1, 64, 4, 1 << 10), (1, 8, 1, 2), (2, 16, 1 << 10, 1 << 20), (1, 64, 1, 1)):
+        for told in (1000, 1 << 28):
+            total = (1 << 30) // G + 1
+            p = launches(Hq=H * G, H=H, D=D, P=128, max_prefix=told, groups=groups, max_seqs=seqs // groups, seqs=seqs, max_q=1,
+                         max_kv=100, total_q=total)
+            assert p is None or p["launches"] == 1

@@ -703,7 +703,7 @@ int prefix_check(const lowbit_kv8* cache, const lowbit_kv8_prefix* p, const lowb
   out->table = p->page_table;
   out->width = p->table_width;
   out->lens = p->lens;
-  out->max_q = std::min(batch->total_q, seqs * batch->max_q);  // rows to be expected of a group
+  out->max_q = std::min(batch->total_q, seqs * batch->max_q);
   out->max_kv = p->max_len;
   out->members = p->seq_starts;
   out->member_count = each;
@@ -713,9 +713,11 @@ int prefix_check(const lowbit_kv8* cache, const lowbit_kv8_prefix* p, const lowb
   if (a->kv.total_q * q_heads > (int64_t(1) << 38) / (a->kv.D + 4)) return LOWBIT_E_SHAPE;
   a->Hq = q_heads;
   a->G = q_heads / a->kv.H;
-  a->group_q = out->max_q;
-  // and what it may have: starts may name more rows for a sequence than max_q, which only its own launch cuts
-  out->max_q = std::min(batch->total_q, std::max(out->max_q, (int64_t(1) << 30) / a->G));
+  // Starts may name more rows for a sequence than max_q, which only its own launch cuts: rows of a
+  // group to be expected, and those that it may have.  (Of a key head int counts them: more than
+  // 2^30 would take more workgroups than a launch has, so such calls go by their sequences.)
+  a->group_q = std::max(out->max_q, batch->total_q / batch->n_seqs * seqs);
+  out->max_q = batch->total_q;
   *plan = plan_prefix(*a);
   return plan->blocks <= (1 << 22) ? LOWBIT_OK : LOWBIT_E_SHAPE;
 }
