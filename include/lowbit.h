@@ -634,14 +634,15 @@ typedef struct lowbit_rope {
  * rounded once to y_dtype F32 or BF16.  Q, K and the outputs lie with tokens
  * the given strides (in elements) apart, heads contiguous: a fused projection's
  * output as it is.  Q_out may be Q and K_out may be K where x_dtype = y_dtype
- * and the strides agree; otherwise outputs overlap nothing.  K NULL (kv_heads 0):
+ * and the strides agree; otherwise outputs share no byte with an input or each
+ * other (refused; rows may lie between another tensor's).  K NULL (kv_heads 0):
  * queries alone.
  * Several axes (time, height, width): each pair turns by one of them.
  * All of Q, K, Q_out, K_out 16-byte aligned, strides multiples of 8; freqs 8 bytes,
  * positions, pair_axis and weights 4.  tokens <= 2^30, q_heads, kv_heads <= 2^16.
  * eps finite, >= 0.
- * Errors: E_NULL, E_UNSUPPORTED (types, head_dim, n_pairs, eps, an output at an
- * input's or the other output's address otherwise), E_SHAPE, E_ALIGN, E_HIP. */
+ * Errors: E_NULL, E_UNSUPPORTED (types, head_dim, n_pairs, eps, overlaps),
+ * E_SHAPE, E_ALIGN, E_HIP. */
 int lowbit_qk_norm_rope(const lowbit_rope* rope, int x_dtype, const void* Q, int64_t q_heads, int64_t q_stride,
                         const float* q_weight, const void* K, int64_t kv_heads, int64_t k_stride,
                         const float* k_weight, float eps, int y_dtype, void* Q_out, int64_t qo_stride, void* K_out,

@@ -4,6 +4,7 @@
 
 #include <algorithm>
 #include <map>
+#include <numeric>
 #include <mutex>
 #include <utility>
 #include <initializer_list>
@@ -785,6 +786,35 @@ int lowbit_attention_kv8_prefix(const lowbit_kv8* cache, const lowbit_kv8_prefix
 
 // ------------------------------------------- heads of queries and keys; pages
 
+namespace {
+
+// n runs of bytes, `stride` apart (at least `bytes`)
+struct Rows {
+  uintptr_t at;
+  int64_t bytes, stride, n;
+};
+// whether some run of a and some run of b share a byte
+bool rows_meet(Rows a, Rows b) {
+  if (!a.at || !b.at) return false;
+  if (a.stride < b.stride) std::swap(a, b);
+  auto end = [](const Rows& r) { return r.at + (uintptr_t)((r.n - 1) * r.stride + r.bytes); };
+  if (end(a) <= b.at || end(b) <= a.at) return false;
+  // Runs of a from the first that ends behind b's begin.  One that lies over b's begin or end meets it; of
+  // the others the places between b's runs come again after stride / gcd runs.
+  const int64_t gap = (int64_t)(b.at - a.at);
+  const int64_t first = gap < a.bytes ? 0 : (gap - a.bytes) / a.stride + 1;
+  const int64_t last = std::min(a.n, first + b.stride / std::gcd(a.stride, b.stride) + 2);
+  for (int64_t i = first; i < last; i++) {
+    const int64_t x = i * a.stride - gap;  // from b's begin
+    const int64_t j = x < 0 ? 0 : std::min(x / b.stride, b.n - 1);
+    if (j * b.stride < x + a.bytes && x < j * b.stride + b.bytes) return true;
+    if (j + 1 < b.n && (j + 1) * b.stride < x + a.bytes) return true;
+  }
+  return false;
+}
+
+}  // namespace
+
 int lowbit_qk_norm_rope(const lowbit_rope* rope, int x_dtype, const void* Q, int64_t q_heads, int64_t q_stride,
                         const float* q_weight, const void* K, int64_t kv_heads, int64_t k_stride,
                         const float* k_weight, float eps, int y_dtype, void* Q_out, int64_t qo_stride, void* K_out,
@@ -810,12 +840,28 @@ int lowbit_qk_norm_rope(const lowbit_rope* rope, int x_dtype, const void* Q, int
   if (r.n_pairs && (!aligned(r.positions, 4) || !aligned(r.freqs, 8) || (r.pair_axis && !aligned(r.pair_axis, 4))))
     return LOWBIT_E_ALIGN;
   if ((q_weight && !aligned(q_weight, 4)) || (k_weight && !aligned(k_weight, 4))) return LOWBIT_E_ALIGN;
-  auto not_in_place = [&](int64_t stride, int64_t o_stride) {
-    return x_dtype != y_dtype || (r.tokens > 1 && stride != o_stride);
+  // Outputs share no byte with an input or each other, but for an output that is its input.
+  const int xb = x_dtype == LOWBIT_F32 ? 4 : 2, yb = y_dtype == LOWBIT_F32 ? 4 : 2;
+  auto rows = [&](const void* p, int64_t heads, int64_t stride, int bytes) {
+    const int64_t row = heads * r.head_dim * bytes;
+    return Rows{(uintptr_t)p, row, r.tokens > 1 ? stride * bytes : row, r.tokens};
   };
-  if (Q_out == Q && not_in_place(q_stride, qo_stride)) return LOWBIT_E_UNSUPPORTED;
-  if (kv_heads && ((K_out == K && not_in_place(k_stride, ko_stride)) || Q_out == K || K_out == Q || K_out == Q_out))
+  auto run = [](const void* p, int64_t bytes) { return Rows{(uintptr_t)p, bytes, bytes, 1}; };
+  const Rows none = {0, 0, 0, 0}, q = rows(Q, q_heads, q_stride, xb), qo = rows(Q_out, q_heads, qo_stride, yb);
+  const Rows k = kv_heads ? rows(K, kv_heads, k_stride, xb) : none, ko = kv_heads ? rows(K_out, kv_heads, ko_stride, yb) : none;
+  auto in_place = [&](const Rows& x, const Rows& y) { return x.at == y.at && xb == yb && x.stride == y.stride; };
+  if ((!in_place(q, qo) && rows_meet(q, qo)) || (!in_place(k, ko) && rows_meet(k, ko)) || rows_meet(q, ko) || rows_meet(k, qo) ||
+      rows_meet(qo, ko))
     return LOWBIT_E_UNSUPPORTED;
+  for (const Rows& y : {qo, ko}) {
+    for (const float* w : {q_weight, k_weight})
+      if (rows_meet(y, run(w, 4 * (int64_t)r.head_dim))) return LOWBIT_E_UNSUPPORTED;
+    if (r.n_pairs == 0) continue;
+    const Rows positions = {(uintptr_t)r.positions, 4 * r.tokens, r.n_axes > 1 ? 4 * r.pos_stride : 4 * r.tokens, r.n_axes};
+    if (rows_meet(y, positions) || rows_meet(y, run(r.freqs, 8 * (int64_t)r.n_pairs)) ||
+        rows_meet(y, run(r.pair_axis, 4 * (int64_t)r.n_pairs)))
+      return LOWBIT_E_UNSUPPORTED;
+  }
   RopeArgs a;
   a.tokens = r.tokens;
   a.D = r.head_dim;
