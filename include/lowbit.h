@@ -674,7 +674,11 @@ int lowbit_qk_norm_rope(const lowbit_rope* rope, int x_dtype, const void* Q, int
  *     0 .. n_pages - 1 in a row becomes -1 and counts for nobody.
  * Where pages do not suffice, *failed is the number that lacks (else 0), no page
  * is written, and the other outputs do not stand: the inputs do.  A child that
- * has more than new_width pages, or 2^30 tokens, is cut to them.
+ * has more than new_width pages, or 2^30 tokens, is cut to them: its new_lens is less
+ * than its parent's and grow together, and appending as many tokens as it asked for
+ * would overwrite its last ones, in pages that others may hold.
+ * lowbit_kv8_fork_cut is the same call and counts the children that were cut in
+ * *cut (device int32, set, not added; NULL to skip).
  * n_seqs 0 (nothing yet: parents are none) and n_new 0 (everything freed) are
  * fine, their arrays may be NULL.  Outputs overlap no input and not each other
  * (refused); new_refs 16-byte aligned.
@@ -689,6 +693,11 @@ int lowbit_kv8_fork(const lowbit_kv8* caches, int64_t n_caches, int64_t n_seqs, 
                     int64_t table_width, const int32_t* kv_lens, const int32_t* refs, int64_t n_new,
                     const int32_t* parents, const int32_t* grow, int64_t max_grow, int32_t* new_table,
                     int64_t new_width, int32_t* new_lens, int32_t* new_refs, int32_t* failed, void* stream);
+int lowbit_kv8_fork_cut(const lowbit_kv8* caches, int64_t n_caches, int64_t n_seqs, const int32_t* page_table,
+                        int64_t table_width, const int32_t* kv_lens, const int32_t* refs, int64_t n_new,
+                        const int32_t* parents, const int32_t* grow, int64_t max_grow, int32_t* new_table,
+                        int64_t new_width, int32_t* new_lens, int32_t* new_refs, int32_t* failed, int32_t* cut,
+                        void* stream);
 int lowbit_kv8_fork_workspace(int64_t n_pages, int page_tokens, int64_t n_caches, int64_t n_seqs, int64_t n_new,
                               int64_t max_grow, size_t* bytes);
 

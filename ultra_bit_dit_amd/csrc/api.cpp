@@ -975,10 +975,11 @@ int lowbit_kv8_fork_workspace(int64_t n_pages, int page_tokens, int64_t n_caches
   return LOWBIT_OK;
 }
 
-int lowbit_kv8_fork(const lowbit_kv8* caches, int64_t n_caches, int64_t n_seqs, const int32_t* page_table,
-                    int64_t table_width, const int32_t* kv_lens, const int32_t* refs, int64_t n_new,
-                    const int32_t* parents, const int32_t* grow, int64_t max_grow, int32_t* new_table,
-                    int64_t new_width, int32_t* new_lens, int32_t* new_refs, int32_t* failed, void* stream) {
+int lowbit_kv8_fork_cut(const lowbit_kv8* caches, int64_t n_caches, int64_t n_seqs, const int32_t* page_table,
+                        int64_t table_width, const int32_t* kv_lens, const int32_t* refs, int64_t n_new,
+                        const int32_t* parents, const int32_t* grow, int64_t max_grow, int32_t* new_table,
+                        int64_t new_width, int32_t* new_lens, int32_t* new_refs, int32_t* failed, int32_t* cut,
+                        void* stream) {
   return no_throw([&]() -> int {
     std::vector<KvLayer> layers;
     const int rc = caches_check(caches, n_caches, &layers);
@@ -990,7 +991,8 @@ int lowbit_kv8_fork(const lowbit_kv8* caches, int64_t n_caches, int64_t n_seqs, 
     if (!fork_sizes_ok(caches[0].n_pages, P, n_seqs, n_new, max_grow)) return LOWBIT_E_SHAPE;
     if (!table_ok(n_seqs, table_width) || !table_ok(n_new, new_width)) return LOWBIT_E_SHAPE;
     for (const void* p : {(const void*)page_table, (const void*)kv_lens, (const void*)refs, (const void*)parents,
-                          (const void*)grow, (const void*)new_table, (const void*)new_lens, (const void*)failed})
+                          (const void*)grow, (const void*)new_table, (const void*)new_lens, (const void*)failed,
+                          (const void*)cut})
       if (!aligned(p, 4)) return LOWBIT_E_ALIGN;
     if (!aligned(new_refs, 16)) return LOWBIT_E_ALIGN;
     ForkArgs a = {};
@@ -1011,15 +1013,24 @@ int lowbit_kv8_fork(const lowbit_kv8* caches, int64_t n_caches, int64_t n_seqs, 
     a.new_lens = new_lens;
     a.new_refs = new_refs;
     a.failed = failed;
+    a.cut = cut;
     if (!fork_fits(a)) return LOWBIT_E_SHAPE;
     if (outputs_overlap({{page_table, n_seqs * a.width}, {kv_lens, n_seqs}, {refs, a.n_pages}, {parents, n_new}, {grow, n_new}},
-                        {{new_table, n_new * a.new_width}, {new_lens, n_new}, {new_refs, a.n_pages}, {failed, 1}}))
+                        {{new_table, n_new * a.new_width}, {new_lens, n_new}, {new_refs, a.n_pages}, {failed, 1}, {cut, 1}}))
       return LOWBIT_E_UNSUPPORTED;
     void* ws = nullptr;
     const int r2 = workspace((hipStream_t)stream, fork_workspace_bytes(a), &ws);
     if (r2) return r2;
     return hip_status(launch_fork(a, layers.data(), ws, (hipStream_t)stream));
   });
+}
+
+int lowbit_kv8_fork(const lowbit_kv8* caches, int64_t n_caches, int64_t n_seqs, const int32_t* page_table,
+                    int64_t table_width, const int32_t* kv_lens, const int32_t* refs, int64_t n_new,
+                    const int32_t* parents, const int32_t* grow, int64_t max_grow, int32_t* new_table,
+                    int64_t new_width, int32_t* new_lens, int32_t* new_refs, int32_t* failed, void* stream) {
+  return lowbit_kv8_fork_cut(caches, n_caches, n_seqs, page_table, table_width, kv_lens, refs, n_new, parents, grow, max_grow,
+                             new_table, new_width, new_lens, new_refs, failed, nullptr, stream);
 }
 
 int lowbit_kv8_compact_workspace(int64_t n_pages, int64_t n_caches, size_t* bytes) {

@@ -90,6 +90,7 @@ struct ForkArgs {
   int32_t* new_lens;         // [n_new]
   int32_t* new_refs;         // [n_pages]
   int32_t* failed;           // pages that were not found
+  int32_t* cut;              // children with less room than they asked for, or NULL
   int pieces;                // a page of the largest layer is moved in
   // workspace
   PageLayer* layers;

@@ -70,6 +70,7 @@ struct Child {
   int64_t had;     // pages taken over
   int64_t need;    // with the tokens to come
   int64_t len;     // with them
+  bool cut;        // fewer tokens than the parent's and those to come
   int64_t tail;    // partly filled page that will be written to, -1: none
 };
 __device__ __forceinline__ int64_t parent_of(const ForkArgs& a, int64_t i) {
@@ -86,10 +87,11 @@ __device__ __forceinline__ Child child_of(const ForkArgs& a, int64_t i) {
   Child c;
   c.parent = parent_of(a, i);
   const int64_t most = most_tokens(a.new_width, a.lp);
-  const int64_t n = c.parent < 0 ? 0 : min(length_of(a, c.parent), most);
+  const int64_t all = c.parent < 0 ? 0 : length_of(a, c.parent), n = min(all, most);
   int64_t grow = a.grow ? (int64_t)a.grow[i] : a.max_grow;
   grow = grow < 0 ? 0 : grow < a.max_grow ? grow : a.max_grow;
   c.len = min(n + grow, most);
+  c.cut = all + grow > c.len;
   c.had = pages_of(n, a.lp);
   c.need = pages_of(c.len, a.lp);
   c.tail = -1;
@@ -180,7 +182,7 @@ __global__ __launch_bounds__(kPlan) void fork_plan(ForkArgs a, Layers l) {
     }
   }
   // the first children's, which every step wants, stay in registers
-  Child mine;
+  Child mine = {};
   mine.parent = mine.tail = -1;
   if (tid < a.n_new) mine = child_of(a, tid);
   auto child = [&](int64_t i) { return i < kPlan ? mine : child_of(a, i); };
@@ -236,7 +238,7 @@ __global__ __launch_bounds__(kPlan) void fork_plan(ForkArgs a, Layers l) {
   step();
   // pages that the children need, in their order
   int64_t total = 0;
-  int copies = 0;
+  int copies = 0, cut = 0;
   for (int64_t i0 = 0; i0 < a.n_new; i0 += kPlan) {
     const int64_t i = i0 + tid;
     int need = 0, copy = 0;
@@ -256,6 +258,7 @@ __global__ __launch_bounds__(kPlan) void fork_plan(ForkArgs a, Layers l) {
         a.dst[copies + nth] = (int)(total + before);  // the place of its page among the free ones
       }
       a.new_lens[i] = (int32_t)c.len;
+      cut += c.cut;
     }
     total += all;
     copies += all_copies;
@@ -295,6 +298,11 @@ __global__ __launch_bounds__(kPlan) void fork_plan(ForkArgs a, Layers l) {
   if constexpr (NEAR) {
     __syncthreads();
     for (int p = tid; p < a.n_pages; p += kPlan) a.new_refs[p] = near_refs[p];
+  }
+  if (a.cut) {
+    int all;
+    (void)scan_before<kPlan>(cut, lds, &all);
+    if (tid == 0) *a.cut = all;
   }
   if (tid == 0) {
     *a.n_copies = found >= total ? copies : 0;

@@ -29,7 +29,7 @@ EXPORTS = ("lowbit_abi_version", "lowbit_status_str", "lowbit_packed_bytes", "lo
            "lowbit_mxfp4_bytes", "lowbit_pack_mxfp4", "lowbit_quantize_mxfp4", "lowbit_gemm_mxfp4", "lowbit_gemm_mxfp4_workspace",
            "lowbit_kv8_append", "lowbit_attention_kv8", "lowbit_attention_kv8_workspace",
            "lowbit_attention_kv8_prefix", "lowbit_attention_kv8_prefix_workspace", "lowbit_attention_kv8_prefix_launches",
-           "lowbit_qk_norm_rope", "lowbit_kv8_fork", "lowbit_kv8_fork_workspace", "lowbit_kv8_compact",
+           "lowbit_qk_norm_rope", "lowbit_kv8_fork", "lowbit_kv8_fork_cut", "lowbit_kv8_fork_workspace", "lowbit_kv8_compact",
            "lowbit_kv8_compact_workspace")
 
 
@@ -132,6 +132,7 @@ def lib():
         L.lowbit_qk_norm_rope.argtypes = [ctypes.POINTER(Rope), i32, vp, i64, i64, vp, vp, i64, i64, vp, ctypes.c_float, i32,
                                           vp, i64, vp, i64, vp]
         L.lowbit_kv8_fork.argtypes = [kvp, i64, i64, vp, i64, vp, vp, i64, vp, vp, i64, vp, i64, vp, vp, vp, vp]
+        L.lowbit_kv8_fork_cut.argtypes = L.lowbit_kv8_fork.argtypes[:-1] + [vp, vp]
         L.lowbit_kv8_fork_workspace.argtypes = [i64, i32, i64, i64, i64, i64, szp]
         L.lowbit_kv8_compact.argtypes = [kvp, i64, i64, vp, i64, vp, vp, vp, vp, vp, vp, vp]
         L.lowbit_kv8_compact_workspace.argtypes = [i64, i64, szp]
@@ -317,7 +318,7 @@ class _Fast:
                 ("lowbit_attention_kv8_prefix", [vp, vp, vp, i64, vp, i64, ctypes.c_float, i32, vp, i64, vp, vp]),
                 ("lowbit_qk_norm_rope", [vp, i32, vp, i64, i64, vp, vp, i64, i64, vp, ctypes.c_float, i32, vp, i64, vp, i64,
                                          vp]),
-                ("lowbit_kv8_fork", [vp, i64, i64, vp, i64, vp, vp, i64, vp, vp, i64, vp, i64, vp, vp, vp, vp]),
+                ("lowbit_kv8_fork_cut", [vp, i64, i64, vp, i64, vp, vp, i64, vp, vp, i64, vp, i64, vp, vp, vp, vp, vp]),
                 ("lowbit_kv8_compact", [vp, i64, i64, vp, i64, vp, vp, vp, vp, vp, vp, vp])):
             f = L[name]  # a function object of its own
             f.argtypes, f.restype = types, i32
@@ -852,11 +853,12 @@ def _out_ints(T, out, like, shapes, names, stream):
     return out
 
 
-def kv8_fork(cache, page_table, kv_lens, refs, parents, grow=0, width=None, max_grow=None, out=None, stream=None):
+def kv8_fork(cache, page_table, kv_lens, refs, parents, grow=0, width=None, max_grow=None, out=None, cut=None, stream=None):
     """The next batch's (page_table [new][width], kv_lens [new], refs [pages], failed [1]) from this one's (see
     lowbit_kv8_fork): parents int32 [new] on the device; grow: tokens each new sequence is about to append, a
     number, or int32 [new] on the device with max_grow as its bound.  cache may be a list of a model's layers.
-    width None: page_table's.  out: the four outputs, which overlap no input."""
+    width None: page_table's; a sequence whose tokens and grow need more pages is cut to them, as its new length shows, and
+    counted in cut, an int32 [1] on the device (None: not).  out: the four outputs, which overlap no input."""
     T = _torch or _load()
     c, n_caches, pages, dev = _layers(T, cache, page_table, kv_lens, refs, parents)
     B, w = page_table.shape
@@ -873,8 +875,13 @@ def kv8_fork(cache, page_table, kv_lens, refs, parents, grow=0, width=None, max_
     pt, ln = _ints(page_table, (B, w), "page_table"), _ints(kv_lens, (B,), "kv_lens")
     rf, pr = _ints(refs, (pages,), "refs"), _ints(parents, (n,), "parents")
     out = _out_ints(T, out, refs, ((n, width), (n,), (pages,), (1,)), ("page_table", "kv_lens", "refs", "failed"), stream)
-    rc = _fast.kv8_fork(c, n_caches, B, pt, w, ln, rf, n, pr, g, max_grow, out[0].data_ptr(), width, out[1].data_ptr(),
-                        out[2].data_ptr(), out[3].data_ptr(), _raw_stream(T, dev, stream))
+    if cut is not None:
+        ct = _ints(cut, (1,), "cut")
+        _device(T, dev, cut)
+    else:
+        ct = None
+    rc = _fast.kv8_fork_cut(c, n_caches, B, pt, w, ln, rf, n, pr, g, max_grow, out[0].data_ptr(), width, out[1].data_ptr(),
+                        out[2].data_ptr(), out[3].data_ptr(), ct, _raw_stream(T, dev, stream))
     if rc:
         raise LowbitError("lowbit_kv8_fork", rc)
     return out
