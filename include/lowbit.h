@@ -540,7 +540,8 @@ int lowbit_kv8_append(const lowbit_kv8* cache, const lowbit_kv8_batch* batch, in
  * Q or the cache.  Keys and values below 2^-126 in magnitude may count as 0.
  * Q, O 16-byte aligned, strides multiples of 8.  Uses the stream's workspace
  * (lowbit_attention_kv8_workspace bytes) as lowbit_gemv does; reserve it
- * before a capture.
+ * before a capture.  A smaller call may need more, as its tiles are cut into more
+ * parts: ask for each shape that is captured.
  * Errors: E_NULL, E_UNSUPPORTED (page_tokens, head_dim, softmax_scale
  * log2(e) not finite), E_SHAPE, E_ALIGN, E_NOMEM, E_HIP. */
 int lowbit_attention_kv8(const lowbit_kv8* cache, const lowbit_kv8_batch* batch, int64_t q_heads,
@@ -585,7 +586,8 @@ typedef struct lowbit_kv8_prefix {
  * should q_starts have more.  Everything else is as lowbit_attention_kv8 says, limits included, for the
  * groups too (their rows: min(total_q, max_seqs * max_q)); max_len + max_kv <=
  * 2^30; total_q * q_heads * (head_dim + 4) <= 2^38.
- * Needs workspace in every case (lowbit_attention_kv8_prefix_workspace).
+ * Needs workspace in every case (lowbit_attention_kv8_prefix_workspace: with the
+ * same heads no more for a call with smaller bounds, sequences, groups or rows).
  * Errors: as lowbit_attention_kv8. */
 int lowbit_attention_kv8_prefix(const lowbit_kv8* cache, const lowbit_kv8_prefix* prefix,
                                 const lowbit_kv8_batch* batch, int64_t q_heads, const uint16_t* Q_bf16,

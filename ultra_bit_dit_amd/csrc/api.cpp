@@ -733,7 +733,7 @@ int lowbit_attention_kv8_prefix_workspace(const lowbit_kv8* cache, const lowbit_
   PrefixPlan plan;
   const int rc = prefix_check(cache, prefix, batch, q_heads, &a, &plan);
   if (rc) return rc;
-  *bytes = attention_prefix_workspace_bytes(plan);
+  *bytes = attention_prefix_workspace_bytes(a);
   return LOWBIT_OK;
 }
 
@@ -779,7 +779,7 @@ int lowbit_attention_kv8_prefix(const lowbit_kv8* cache, const lowbit_kv8_prefix
   a.o_stride = o_stride;
   a.lse = lse;
   void* ws = nullptr;
-  const int r2 = workspace((hipStream_t)stream, attention_prefix_workspace_bytes(plan), &ws);
+  const int r2 = workspace((hipStream_t)stream, attention_prefix_workspace_bytes(a), &ws);
   if (r2) return r2;
   return hip_status(launch_attention_prefix(a, plan, ws, (hipStream_t)stream));
 }

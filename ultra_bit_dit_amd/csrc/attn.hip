@@ -1923,6 +1923,7 @@ double tail_time(int D, int64_t rows, int64_t tiles, int64_t blocks, int64_t pie
 // workgroup (of the 450 calls those with 2 to 4 took 0.72 to 0.87 of the time, with 4 to 8 0.9, with more 1.0 to 1.25,
 // as sequences differ in length).
 constexpr int64_t kMostBlocks = 1 << 22;  // of a launch
+constexpr int64_t kNoTile = 8;            // rows of a sequence and key head that do not take a prompt tile of their own
 constexpr int64_t kFineRows = 64;         // of a sequence and key head: eight tokens of eight heads
 PrefixPlan plan_prefix_of(const AttnArgs& a) {
   const KvArgs &kv = a.kv, &prefix = a.prefix;
@@ -1957,7 +1958,7 @@ PrefixPlan plan_prefix_of(const AttnArgs& a) {
   one.part = (size_t)(one.cut * one.parts * one.rows * row_bytes);
   one_time = 0.92 * one_time + (D == 64 ? 3.7 : D == 256 ? 1.9 : one.rows == 128 ? 4.9 : 10.3);
   if (one.fine && D == 128) one_time *= 1.15;  // the second terms; with other heads the times' spread is larger
-  if (Rs <= 8) one_time = 1e30;  // tiles filled to a sixteenth: of 252 such calls none took less than 0.98 of the others' time
+  if (Rs <= kNoTile) one_time = 1e30;  // tiles filled to a sixteenth: of 252 such calls none took less than 0.98 of the others' time
 
   // the same in attn_decode
   const int nc = decode_nc(Rs);
@@ -2034,7 +2035,22 @@ hipError_t launch_attention(AttnArgs a, void* ws, hipStream_t s) {
 
 PrefixPlan plan_prefix(const AttnArgs& a) { return plan_prefix_of(a); }
 
-size_t attention_prefix_workspace_bytes(const PrefixPlan& p) { return (size_t)kCounterBytes + p.sums + p.part; }
+// For every plan within the bounds of `a`, which does not fall as any of them rises: plans do not grow with their
+// calls, as a smaller call may be cut into more parts.
+size_t attention_prefix_workspace_bytes(const AttnArgs& a) {
+  const KvArgs& kv = a.kv;
+  const int D = kv.D;
+  const int64_t row_bytes = (D + kPartPad) * 4, total = kv.total_q * a.Hq;
+  // Tiles in parts, of 128 rows or for D = 128 of 256, are at most four times those that the chip holds, and
+  // a tile has at most best_parts of them.
+  const int64_t rows = D == 128 ? 256 : 128, most = 4 * prompt_slots(D, rows) * rows;
+  const int64_t head_steps = cdiv(a.prefix.max_kv, kUnit), steps = head_steps + cdiv(kv.max_kv, kUnit);
+  const int64_t decode = (int64_t)4 * kMaxShares * 16 * (D == 64 ? 2 : 1) * (D + 2) * 4;
+  const int64_t sums = std::max(total, std::min(best_parts(head_steps) * total, most)) * row_bytes;
+  const int64_t tiles = tiles_of(kv, a.G, rows) * rows;
+  const int64_t own = kv.max_q * a.G > kNoTile ? std::min(best_parts(steps) * tiles, most) * row_bytes : 0;
+  return (size_t)(kCounterBytes + std::max(sums + decode, own));
+}
 
 hipError_t launch_attention_prefix(AttnArgs a, const PrefixPlan& p, void* ws, hipStream_t s) {
   uint8_t* at = (uint8_t*)ws + kCounterBytes;

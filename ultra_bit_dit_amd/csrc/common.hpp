@@ -218,7 +218,7 @@ hipError_t launch_attention(AttnArgs a, void* ws, hipStream_t s);
 // the same behind prefixes that groups of sequences share
 struct PrefixPlan;
 PrefixPlan plan_prefix(const AttnArgs& a);
-size_t attention_prefix_workspace_bytes(const PrefixPlan& p);
+size_t attention_prefix_workspace_bytes(const AttnArgs& a);
 hipError_t launch_attention_prefix(AttnArgs a, const PrefixPlan& p, void* ws, hipStream_t s);
 
 }  // namespace lowbit
