@@ -1631,8 +1631,21 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void attn_prompt32(AttnArgs a) {
       using Middle = std::integral_constant<int, KST>;
       using Last = std::integral_constant<int, KST + VST>;
       if (w_now && nan_at_[(u - 1) & 3] == u - 1) mark_nans(u - 1);
-      if (s_now) products(First{}, Middle{}, kb, vb);
-      if (w_now) products(Middle{}, Last{}, kb, vb);
+      if constexpr (FINE) {
+        // Weights first, which then live no longer than scores do: with both terms of them beside the
+        // scores 66 registers were spilled (D = 64)
+        if (w_now) products(Middle{}, Last{}, kb, vb);
+#pragma unroll
+        for (int c = 0; c < NC; c++) {
+          sc[c][0] = sc[c][1] = v16f{};
+#pragma unroll
+          for (int e = 0; e < 4; e++) pf[c][e] = pl[c][e] = v8bf{};
+        }
+        if (s_now) products(First{}, Middle{}, kb, vb);
+      } else {
+        if (s_now) products(First{}, Middle{}, kb, vb);
+        if (w_now) products(Middle{}, Last{}, kb, vb);
+      }
     }
     meet();
     if (u < u1 && sees(u)) softmax(u);
@@ -1789,10 +1802,7 @@ bool many_rows(const KvArgs& kv, int64_t R) {
 // waves; 2 x 4096 in 4096, 40 heads over 8, 411 us with 128 rows and 376 with 256,
 // 16 x 64 in 1024 50 and 42, 16 x 5 in 2048, 32 heads, 26 and 35).
 int prompt_rows(int D, int64_t R) { return D == 128 && R > 128 ? 256 : 128; }
-// fine: weights in two terms, whose registers leave two workgroups of D = 64 (three spill 16 to 66 of them).
-int prompt_slots(int D, int64_t R, bool fine = false) {
-  return D == 64 ? (fine ? 512 : 768) : D == 128 && R <= 128 ? 512 : 256;
-}
+int prompt_slots(int D, int64_t R) { return D == 64 ? 768 : D == 128 && R <= 128 ? 512 : 256; }
 
 // window: 0 where rows see everything before them or more
 Plan plan_attention(const KvArgs& kv, int64_t G, int64_t window) {
@@ -1817,7 +1827,7 @@ Plan plan_attention(const KvArgs& kv, int64_t G, int64_t window) {
 template <int MODE, bool FINE = false>
 void launch_prompt(int rows, unsigned blocks, const AttnArgs& a, hipStream_t s) {
   const dim3 grid(blocks);
-  if (a.kv.D == 64) hipLaunchKernelGGL((attn_prompt32<64, 1, 4, FINE ? 2 : 3, MODE, FINE>), grid, dim3(256), 0, s, a);
+  if (a.kv.D == 64) hipLaunchKernelGGL((attn_prompt32<64, 1, 4, 3, MODE, FINE>), grid, dim3(256), 0, s, a);
   else if (a.kv.D == 256) hipLaunchKernelGGL((attn_prompt<256, 1, 8, MODE, FINE>), grid, dim3(512), 0, s, a);
   else if (rows == 128) hipLaunchKernelGGL((attn_prompt32<128, 1, 4, 2, MODE, FINE>), grid, dim3(256), 0, s, a);
   else if constexpr (MODE != kBehind || !FINE)  // of sequences with few rows the tiles have 128
@@ -1862,10 +1872,9 @@ double wg_time(int D, int64_t rows, double fill, int64_t wgs, double steps) {
 // tiles (of at most `most`, for which there is to be room) cut into the parts that take
 // the least time; `sums`: us to write and read one part of each, `join`: us that
 // joining takes beside that
-double cut_time(int D, int64_t rows, bool fine, double fill, int64_t tiles, int64_t most, int64_t steps, double sums, double join,
-                int* parts) {
+double cut_time(int D, int64_t rows, double fill, int64_t tiles, int64_t most, int64_t steps, double sums, double join, int* parts) {
   double least = 1e30;
-  const int64_t slots = prompt_slots(D, rows, fine);
+  const int64_t slots = prompt_slots(D, rows);
   for (int64_t k = 1; k <= best_parts(steps) && (k == 1 || most * k <= 4 * slots); k++) {
     const double t = (double)cdiv(tiles * k, slots) * wg_time(D, rows, fill, std::min(tiles * k, slots), (double)steps / (double)k) +
                      (k > 1 || join == 0. ? sums * (double)k + join : 0.);
@@ -1940,7 +1949,7 @@ PrefixPlan plan_prefix_of(const AttnArgs& a) {
   one.behind = true;
   one.fine = Rs <= kFineRows;
   one.rows = prompt_rows(D, Rs);
-  const int64_t slots = prompt_slots(D, Rs, one.fine), most = tiles_of(kv, a.G, one.rows);
+  const int64_t slots = prompt_slots(D, Rs), most = tiles_of(kv, a.G, one.rows);
   // tiles to be expected: each sequence's last one half full, but one of each
   const int64_t tiles =
       std::min(most, kv.H * std::max(kv.n_seqs, kv.total_q * a.G / one.rows + (kv.n_seqs + 1) / 2));
@@ -1950,7 +1959,7 @@ PrefixPlan plan_prefix_of(const AttnArgs& a) {
   const double one_fill = (double)std::min<int64_t>(Rs, one.rows) / (double)one.rows;
   double one_time = (double)(one.whole * kv.H) / (double)slots * wg_time(D, one.rows, one_fill, slots, (double)steps);
   if (rest)
-    one_time += cut_time(D, one.rows, one.fine, one_fill, rest, most - one.whole * kv.H, steps,
+    one_time += cut_time(D, one.rows, one_fill, rest, most - one.whole * kv.H, steps,
                          one_fill * (double)(rest * one.rows * row_bytes) * 2. / kRate, 4. + 0.03 * (double)rest, &one.parts);
   if (one.parts == 1) one.whole = (int)(most / kv.H);
   one.cut = most - one.whole * kv.H;
@@ -1982,7 +1991,7 @@ PrefixPlan plan_prefix_of(const AttnArgs& a) {
     // 256 rows a tile where that is not a fifth more of them than in tiles of 128
     two.rows = prompt_rows(D, cdiv(Rg, 256) * 256 * 5 < cdiv(Rg, 128) * 128 * 6 ? Rg : 128);
     const int64_t group_tiles = tiles_of(prefix, a.G, two.rows, a.group_q), room = tiles_of(prefix, a.G, two.rows);
-    two_time += cut_time(D, two.rows, two.fine, (double)std::min<int64_t>(Rg, two.rows) / (double)two.rows, group_tiles, room, head_steps,
+    two_time += cut_time(D, two.rows, (double)std::min<int64_t>(Rg, two.rows) / (double)two.rows, group_tiles, room, head_steps,
                          (double)(kv.total_q * a.Hq * row_bytes) * 2. / kRate, 0., &two.parts);
     two.blocks = room * two.parts;
   } else {
