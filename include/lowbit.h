@@ -529,7 +529,8 @@ int lowbit_kv8_append(const lowbit_kv8* cache, const lowbit_kv8_batch* batch, in
  * encoder's states) of its own length.  Sums and
  * statistics are fp32.  Weights enter the second product as bf16: in two terms
  * (16 bits) in calls of few rows a sequence and key head, such as single
- * tokens, rounded once (8 bits, as O) in calls of many.  Results do not depend
+ * tokens, rounded once (8 bits, as O) in calls of many (with heads of 256 and at
+ * most 16 rows also where n_seqs * kv_heads * ceil(max_kv / 64) <= 512).  Results do not depend
  * on the order in which workgroups run.  Rows of sequences behind the last
  * q_starts entry are not written.
  * One call runs one kernel for all its sequences, chosen by max_q * q_heads /
@@ -552,7 +553,7 @@ int lowbit_attention_kv8_workspace(const lowbit_kv8* cache, const lowbit_kv8_bat
 
 /* Sequences that begin with the same tokens (answers to one prompt, prompts behind
  * one instruction): group g's sequences are seq_starts[g] .. seq_starts[g + 1] - 1
- * of the batch, so that its rows lie in order, and the tokens they share are
+ * of the batch (no sequence in two groups), so that its rows lie in order, and the tokens they share are
  * the first lens[g] of the pages in page_table's row g.  seq_starts NULL: n_seqs
  * / n_groups each, in order.  max_seqs and max_len bound the sequences of any one
  * group and its lengths; they size the launch, so keep them close.  Arrays are read
@@ -632,7 +633,7 @@ typedef struct lowbit_rope {
  * q_weight / k_weight [D] (fp32; NULL: y = x, w of 1 + v is the caller's to
  * add); then each pair (a, b) becomes (a cos t - b sin t, b cos t + a sin t),
  * t = positions[axis][token] freqs[pair], reduced in fp64 (off by 2^-51 of the
- * angle).  Everything else is fp32 (squares beyond its range overflow),
+ * angle).  Everything else is fp32 (squares beyond its range overflow, below it they are 0),
  * rounded once to y_dtype F32 or BF16.  Q, K and the outputs lie with tokens
  * the given strides (in elements) apart, heads contiguous: a fused projection's
  * output as it is.  Q_out may be Q and K_out may be K where x_dtype = y_dtype
@@ -683,7 +684,7 @@ int lowbit_qk_norm_rope(const lowbit_rope* rope, int x_dtype, const void* Q, int
  * *cut (device int32, set, not added; NULL to skip).
  * n_seqs 0 (nothing yet: parents are none) and n_new 0 (everything freed) are
  * fine, their arrays may be NULL.  Outputs overlap no input and not each other
- * (refused); new_refs 16-byte aligned.
+ * (refused; that they lie outside the caches is the caller's care); new_refs 16-byte aligned.
  * n_pages <= 2^26; n_seqs, n_new <= 2^20; table widths <= 2^26; max_grow <= 2^30;
  * n_new * (max_grow / page_tokens + 2) <= 2^30, n_new * ceil(new_width / 1024) < 2^24 - 2048;
  * n_caches <= 4096.  One workgroup plans: time grows with n_new and with the

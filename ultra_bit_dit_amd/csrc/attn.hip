@@ -21,8 +21,8 @@
 // second term would take 2 x 4096 rows, 40 heads over 8, D = 128, from 383 to 497 us
 // and attn_prompt32<64> out of its registers (221 -> 511 us).  Behind prefixes few rows
 // of many sequences fill prompt tiles too: where a sequence has at most kFineRows of a
-// key head, those have two terms as well (FINE; the batch of 64 below 93 -> 109 us, 45 x
-// 5 tokens 41 -> 50, 16 with D = 256 100 -> 109).
+// key head, those have two terms as well (FINE; the batch of 64 below 90 -> 108 us, 45 x
+// 5 tokens 42 -> 45, 16 with D = 256 101 -> 109).
 //
 // MODE.  kPlain: a call's rows see the tokens of one sequence each.  The others are
 // of calls behind prefixes that groups of sequences share:
@@ -32,10 +32,11 @@
 //   kHead    groups in the place of sequences: the rows of a group's sequences, which lie
 //            in order, see its prefix, and leave their sums in the workspace;
 //   kTail    each sequence's rows see its own tokens, and take those sums in.
-// 64 single tokens behind 32760, 40 heads over 8, D = 128: 109 us (43 GFLOP in tiles that
-// five heads fill to 0.83; kTail 21 of it, its chain of length, page, codes, sums); 16 behind two prefixes of
-// 65000, 24 heads over 4, D = 256: 109; 45 x 5 tokens behind six of 8000, D = 64: 50; 8
-// prompts of 777 behind 6001, 32 heads over 8, D = 128, in one kBehind launch: 470 to 510 by card (0.9 PFLOP/s).
+// 64 single tokens behind 32760, 40 heads over 8, D = 128: 107 to 121 us by card and clock (kHead 97, 43 GFLOP
+// and half as many again for the second terms, in tiles that five heads fill to 0.83; kTail 21, its chain of length,
+// page, codes, sums); 16 behind two prefixes of 65000, 24 heads over 4, D = 256: 109 (86 + 29 alone); 45 x 5 tokens
+// behind six of 8000, D = 64: 45 (25 + 21); 8 prompts of 777 behind 6001, 32 heads over 8, D = 128, in one kBehind
+// launch and its join: 476 to 515 by card and clock (0.86 to 0.93 PFLOP/s).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -272,8 +273,8 @@ __device__ __forceinline__ float2 get2(const float* p) {
 }
 
 // Four waves, so that two workgroups share a compute unit where a wave fits
-// 256 registers and one starts or ends while the other reads.  D = 128 fills them; some
-// 110 scalars of every variant lie in lanes of vector registers.
+// 256 registers and one starts or ends while the other reads.  D = 128 fills them; 96 to
+// 116 scalars lie in lanes of vector registers, 131 to 159 of kBehind.
 constexpr int kDecWaves = 4;
 constexpr int kBlock = kUnit * kDecWaves;  // tokens of a block: a step of every wave
 
@@ -1309,7 +1310,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attn_prompt(AttnArgs a) {
 // workgroups a compute unit: more waves hide latency.  Its products keep the MFMA
 // busy in 24% of the cycles, LDS is active in 20%; vector instructions take 47% at
 // four cycles each and the exponentials' quarter rate some 17% more (2 x 4096 in
-// 4096, 32 heads over 8: 226 us).  One register is spilled.
+// 4096, 32 heads over 8: 226 us).  One register is spilled (kBehind: two).
 template <int D, int NC, int WAVES, int OCC, int MODE, bool FINE>
 __global__ __launch_bounds__(64 * WAVES, OCC) void attn_prompt32(AttnArgs a) {
   constexpr int DS = D / 16, DT = D / 32, HALF = 32 * WAVES, SP = 4 * D / HALF, PS = WAVES / 4;
@@ -1776,19 +1777,17 @@ struct Plan {
 // the registers) and every tile reads the cache again; attn_prompt reads it once
 // for all rows, but widens it for 128 or 256 of them and joins its parts by
 // another launch.  So the choice goes by the rows of a head and the steps of all
-// heads.  us, attn_decode / attn_prompt, 32 heads over 8 (D = 256: 24 over 4):
-// (attn_decode with one bf16 term of the weights, whose second takes 0.2 to 0.4 us, and before
-// all threads added its waves' sums, which saves 0.3 to 1.7)
-//   D = 64   4 rows, 1 x 1024 9.4 / 10.3; 16 rows 11.1 / 10.9, 1 x 4096 13.9 / 14.6
-//            20 rows, 1 x 4096 17.4 / 14.6, 16 x 2048 19.4 / 20.8
-//            40 rows, 1 x 4096 19.6 / 14.9, 64 x 2048 53 / 58, 1 x 32768 26 / 41
-//            80 rows, 16 x 2048 35 / 29
-//   D = 128  8 rows, 1 x 1024 12.7 / 12.2, 1 x 4096 15.6 / 16.6, 8 x 1000 13.2 / 14.1
-//            16 rows, 1 x 1024 14.8 / 12.2, 1 x 8192 20.5 / 20.8, 16 x 2048 24 / 26
-//            20 rows (of 32 a wave), 1 x 4096 23 / 16, 64 x 2048 65 / 64, 1 x 131071 80 / 86
-//            40 rows, 1 x 32768 62 / 47, 64 x 2048 115 / 74
-//   D = 256  6 rows, 1 x 1024 16.4 / 13.9, 8 x 1024 16.8 / 14.8, 32 x 1024 24 / 28, 1 x 16384 22 / 32
-//            18 rows, 1 x 1024 21 / 14, 64 x 2048 93 / 66
+// heads.  us in a graph over two caches in turn, attn_decode / attn_prompt, 32 heads over 8 (D = 256: 24 over 4):
+//   D = 64   4 rows, 1 x 1024 9.3 / 10.9; 16 rows 10.8 / 11.5, 1 x 4096 14.6 / 15.1
+//            20 rows, 1 x 4096 18.1 / 15.1, 16 x 2048 21.2 / 21.1
+//            40 rows, 1 x 4096 20.3 / 15.3, 64 x 2048 61 / 56, 1 x 32768 29 / 41
+//            80 rows, 16 x 2048 36 / 29
+//   D = 128  8 rows, 1 x 1024 12.1 / 12.4, 1 x 4096 15.7 / 16.8, 8 x 1000 13.8 / 15.0
+//            16 rows, 1 x 1024 14.2 / 12.6, 1 x 8192 21.9 / 21.2, 16 x 2048 25.0 / 25.8
+//            20 rows, 1 x 4096 20 / 17, 64 x 2048 88 / 66, 1 x 131071 83 / 83
+//            40 rows, 1 x 32768 43 / 47, 64 x 2048 124 / 74
+//   D = 256  6 rows, 1 x 1024 15.5 / 14.6, 8 x 1024 17.3 / 16.2, 32 x 1024 23 / 29, 1 x 16384 23 / 33
+//            18 rows, 1 x 1024 21 / 15, 64 x 2048 97 / 69
 bool many_rows(const KvArgs& kv, int64_t R) {
   constexpr int64_t kAny = INT64_MAX;
   int64_t most;  // steps up to which attn_prompt is the faster one
@@ -1920,14 +1919,14 @@ double tail_time(int D, int64_t rows, int64_t tiles, int64_t blocks, int64_t pie
 }
 
 // The three ways by their expected times, whose numbers are fitted to 450 random calls (1 to 8 groups of 2 to 64
-// sequences, 1 to 700 new tokens, prefixes of 10 to 60000); 300 others took 1.2% longer than with always the best of
-// the three.  us, measured, single tokens of 32 heads over 8 behind one prefix (D = 256: 24 over 4), in one attn_decode /
-// in two launches:
-//   D = 64   8 sequences behind 8000 20 / 23, 16 30 / 25, 32 44 / 29, 8 behind 32000 43 / 37
-//   D = 128  4 behind 1000 12 / 20, 8 behind 8000 27 / 29, 16 41 / 31, 32 65 / 36, 8 behind 32000 61 / 41
-//   D = 256  8 behind 8000 32 / 40, 16 49 / 47, 32 76 / 50, 8 behind 32000 68 / 54
+// sequences, 1 to 700 new tokens, prefixes of 10 to 60000; outside of that they are extrapolation); 450 others took
+// 1.1% longer than with always the best of the three.  us, measured, single tokens of 32 heads over 8 behind one prefix
+// (D = 256: 24 over 4), 100 own tokens, in one attn_decode / in two launches:
+//   D = 64   8 sequences behind 8000 18 / 25, 16 26 / 27, 32 40 / 32, 8 behind 32000 40 / 37
+//   D = 128  4 behind 1000 12 / 20, 8 behind 8000 25 / 32, 16 37 / 34, 32 60 / 39, 8 behind 32000 59 / 46
+//   D = 256  8 behind 8000 31 / 40, 16 44 / 49, 32 69 / 52, 8 behind 32000 69 / 56
 // and more rows of each of 32 sequences behind 16000 / 2000, D = 128, in one prompt launch / in two:
-//   32 rows 227 / 78 and 46 / 39, 64 rows 260 / 120 and 53 / 54, 128 rows 312 / 215 and 75 / 71.
+//   32 rows 281 / 119 and 54 / 47, 64 rows 328 / 210 and 80 / 63, 128 rows 330 / 294 and 73 / 89.
 // attn_decode over sequences and prefixes in pieces rather than equal shares where there are no more than 8 blocks a
 // workgroup (of the 450 calls those with 2 to 4 took 0.72 to 0.87 of the time, with 4 to 8 0.9, with more 1.0 to 1.25,
 // as sequences differ in length).

@@ -7,9 +7,11 @@
 // Pages are chosen by one small kernel (fork) or by chunks of 4096 pages
 // (compact); their bytes are moved by a launch that fills the chip, a page's keys
 // or values being one run of heads * tokens * dims bytes.
-// In a graph, 64 sequences of 33 pages forked 10.8 us (plan 8.6 alone, rows and copies 4.1 alone),
-// 200 of 2048 pages 13.9; 700 pages compacted 7.2 us, 6000 of 128 KiB with some 1000 moves 63
-// (plan 7.4; moves 45, 132 MB read and written, 5.8 TB/s).
+// In a graph, 64 sequences of 33 pages forked 11 us (plan 8.7 alone, rows and copies 4.4 alone; 47
+// with 32 layers, whose copies are 33 MB), 200 of 2048 pages 14; 700 pages compacted 7.3 us, 6000 of
+// 128 KiB with some 1000 moves 66 (plan 7.3; moves 46, 132 MB read and written, 5.8 TB/s).  Pools of
+// more than kNearPages are planned by the same one workgroup over counts in memory: 40 prompts of 8
+// beams, 30000 tokens in pages of 16 (600000 entries, 78100 pages) 626 us.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -131,7 +133,9 @@ __global__ void more_layers(PageLayer* to, Layers l) { put_layers(to, l); }
 // take themselves off its count, and where that leaves 0, the smallest of them is
 // written in its place.
 constexpr int kNearSeqs = 4096;       // sequences whose children and lengths lie in LDS
-constexpr int kNearPages = 28672;     // pages whose counts do
+// Pages whose counts do: with the sequences' 32 KiB 147 KB of a compute unit's 160; whole turns of
+// the workgroup's free pages (4 to a thread).
+constexpr int kNearPages = 28672;
 constexpr int kFirst = INT32_MIN;     // + child: it keeps the page
 
 template <bool NEAR>

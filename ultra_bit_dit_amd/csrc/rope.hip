@@ -8,9 +8,10 @@
 // of many turns), and its sine and cosine are Taylor series of an argument of at
 // most pi / 4 (the first terms left out are below 2^-28 of the result).
 //
-// Bound by memory: 8191 x 28 heads of 256, fp32 to bf16, 73 us (4.8 TB/s, as a 4 GiB copy);
-// 18432 x 40 heads of 128, bf16, three axes, adjacent pairs, 79 us (4.8 TB/s); one token,
-// 48 heads of 128, 4.8 us (the launch, a load, the sums, a store).  Heads whose lanes are no
+// Bound by memory: 8191 x 28 heads of 256, fp32 to bf16, 76 us over two sets of inputs in
+// turn (4.6 TB/s; a 4 GiB copy 4.7) and 74 over one, part of which the last-level cache
+// keeps; 18432 x 40 heads of 128, bf16, three axes, adjacent pairs, 84.5 us (4.5 TB/s) and
+// 79; one token, 48 heads of 128, 4.8 us (the launch, a load, the sums, a store).  Heads whose lanes are no
 // power of two leave some idle: 16384 x 25 heads of 96 3.9 TB/s, of 72 3.2 TB/s (more
 // loads on their way at once made those 5 to 25% slower).
 //
@@ -345,7 +346,7 @@ hipError_t launch_qk_norm_rope(const RopeArgs& a, bool f32, bool out32, hipStrea
   const int slices = (int)cdiv(heads, per);
   // What the chip holds at once (three workgroups a compute unit; six with the
   // smaller chunks): a wave with several tokens reads ahead from one to the next.
-  // 8191 x 28 heads of 256, fp32 to bf16: 72 us, with a wave for each token 86.
+  // 8191 x 28 heads of 256, fp32 to bf16, one set of inputs: 74 us, with a wave for each token 86.
   const int64_t blocks = std::min<int64_t>(cdiv(a.tokens * slices, kWaves), wide ? 768 : 1536);
   const dim3 grid((unsigned)blocks), block(64 * kWaves);
   auto go = [&](auto in, auto out) {
