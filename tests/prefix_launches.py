@@ -57,7 +57,7 @@ def every_kind(draws=30000, least=3):
         g, new, P = some(1, 40), some(1, 600), rng.choice((16, 32, 64, 128))
         seqs, own, told = g * some(1, 40), new + some(1, 1000), some(1, 60000)
         cost = (seqs + g) * max(own, 300) * H * D + seqs * new * H * G * D * 4
-        if cost > 6e7:
+        if cost > 4e7:
             continue
         case = ragged(g, seqs, new, own, told, Hq=H * G, H=H, D=D, P=P)
         plan = launches_of(case)

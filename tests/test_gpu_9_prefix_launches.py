@@ -13,7 +13,7 @@ pytestmark = pytest.mark.gpu
 @pytest.mark.parametrize("kind", list(every_kind()))
 def test_every_kind_of_launch(kind):
     print(kind, flush=True)
-    k = Told(**every_kind()[kind], short=290)
+    k = Told(**every_kind()[kind], short=270)
     out = k.run()
     k.check(out, kind, rows=2, some=6)
     again = k.run()

@@ -13,7 +13,7 @@ pytestmark = pytest.mark.gpu
 @pytest.mark.parametrize("Hq,H,D,new", [(40, 8, 128, 1), (16, 4, 64, 2), (12, 2, 256, 1)])
 def test_the_largest_batch_reserves_for_all(Hq, H, D, new):
     """One reservation, then graphs of smaller batches behind shorter prefixes on the same stream; each replayed twice."""
-    largest = dict(prefix=[32760], count=[80], new=[new] * 80, own=OWN(80, 60))
+    largest = dict(prefix=[32760], count=[80], new=[new] * 80, own=OWN(80, 20))
     k = Told(**largest, Hq=Hq, H=H, D=D, P=64)
     a = k.args()
     a.pop("return_lse")
@@ -26,7 +26,7 @@ def test_the_largest_batch_reserves_for_all(Hq, H, D, new):
     torch.cuda.synchronize()
     for B, told in ((80, 32760), (64, 32760), (32, 32760), (24, 8000), (64, 1000), (3, 8000), (1, 32760), (1, 1)):
         print(f"captured B={B} prefix={told} D={D}", flush=True)
-        k = Told(prefix=[told], count=[B], new=[new] * B, own=OWN(B, 60), Hq=Hq, H=H, D=D, P=64)
+        k = Told(prefix=[told], count=[B], new=[new] * B, own=OWN(B, 20), Hq=Hq, H=H, D=D, P=64)
         pl, ow, a = i32(k.prefix), i32(k.own), k.args()
         call = lambda **kw: lb.attention_kv8_prefix(k.q, k.c.gpu, k.prefix_table, pl, k.table, ow, **{**a, **kw})
         want = [x.clone() for x in call()]  # on the current stream, which has a workspace of its own

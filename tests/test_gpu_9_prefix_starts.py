@@ -14,8 +14,8 @@ class Told(Call):
     """Prefixes of `short` tokens and fewer, told to be as long as `prefix` says (which sizes the launches), sequence b's
     rows from b * spacing on (0: one after the other)."""
 
-    def __init__(self, prefix, spacing=0, short=150, **kw):
-        super().__init__(prefix=[min(n, short - 11 * (g % 8)) for g, n in enumerate(prefix)], **kw)
+    def __init__(self, prefix, spacing=0, short=100, **kw):
+        super().__init__(prefix=[min(n, short - 7 * (g % 8)) for g, n in enumerate(prefix)], **kw)
         self.told = max(prefix)
         wide = torch.full((self.G, -(-self.told // self.P)), -77, dtype=torch.int32, device="cuda")
         n = min(self.prefix_table.shape[1], wide.shape[1])
