@@ -72,6 +72,8 @@ def test_rows_between_sequences_are_reckoned_with(D, G):
     args = dict(Hq=8 * G, H=8, D=D, P=64, max_prefix=20000, groups=2, max_seqs=32, seqs=64, max_q=1, max_kv=100)
     tight, loose = launches(total_q=64, **args), launches(total_q=64 * 64, **args)
     assert tight["launches"] == 2 and (loose["launches"] == 1 or loose["tile_parts"] < tight["tile_parts"])
+    # more than 256 rows of a sequence go by the sequences, which skip those between
+    assert launches(total_q=64 * (256 // G + 1), **args)["launches"] == 1
 
 
 @pytest.mark.parametrize("D", [64, 128, 256])

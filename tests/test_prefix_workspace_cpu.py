@@ -39,3 +39,10 @@ def test_one_prefix_of_a_server():
     assert sizes == sorted(sizes) and sizes[-1] < 200 << 20
     sizes = [at(64, n) for n in (10, 1000, 8000, 32760)]
     assert sizes == sorted(sizes)
+
+
+@pytest.mark.parametrize("D,H,G", [(64, 8, 4), (128, 8, 5), (256, 4, 6)])
+def test_long_prompts_keep_no_sums(D, H, G):
+    """Rows that go by their sequences alone leave no sums: the bytes do not grow with them, padded or not."""
+    for seqs, q, padded in ((8, 4096, 4096), (64, 1000, 1000), (64, 1, 1000), (1, 1 << 20, 1 << 20)):
+        assert need(D, H, G, 1, seqs, seqs, seqs * padded, q, q, 6001) < 200 << 20

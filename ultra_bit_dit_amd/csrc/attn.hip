@@ -1932,6 +1932,7 @@ double tail_time(int D, int64_t rows, int64_t tiles, int64_t blocks, int64_t pie
 // as sequences differ in length).
 constexpr int64_t kMostBlocks = 1 << 22;  // of a launch
 constexpr int64_t kNoTile = 8;            // rows of a sequence and key head that do not take a prompt tile of their own
+constexpr int64_t kSpaced = 256;          // rows of a sequence and key head, with those before the next, that groups take
 constexpr int64_t kFineRows = 64;         // of a sequence and key head: eight tokens of eight heads
 PrefixPlan plan_prefix_of(const AttnArgs& a) {
   const KvArgs &kv = a.kv, &prefix = a.prefix;
@@ -2001,8 +2002,10 @@ PrefixPlan plan_prefix_of(const AttnArgs& a) {
   }
   two.sums = (size_t)(two.parts * kv.total_q * a.Hq * row_bytes);
 
-  // sequences of 256 rows and more fill their tiles without a group, and need no sums
-  if (Rs > 256 || two.blocks > kMostBlocks || two.tail_blocks > kMostBlocks) two_time = 1e30;
+  // sequences of more than 256 rows fill their tiles without a group, and need no sums; rows
+  // between them would be the groups' work too
+  const int64_t spaced = std::max(kv.max_q, kv.total_q / kv.n_seqs) * a.G;
+  if (spaced > kSpaced || two.blocks > kMostBlocks || two.tail_blocks > kMostBlocks) two_time = 1e30;
   if (few_time <= std::min(one_time, two_time)) {
     PrefixPlan few = {};
     few.behind = true;
@@ -2048,7 +2051,8 @@ PrefixPlan plan_prefix(const AttnArgs& a) { return plan_prefix_of(a); }
 size_t attention_prefix_workspace_bytes(const AttnArgs& a) {
   const KvArgs& kv = a.kv;
   const int D = kv.D;
-  const int64_t row_bytes = (D + kPartPad) * 4, total = kv.total_q * a.Hq;
+  const int64_t row_bytes = (D + kPartPad) * 4;
+  const int64_t total = std::min(kv.total_q, kv.n_seqs * (kSpaced / a.G + 1)) * a.Hq;  // rows that may have sums
   // Tiles in parts, of 128 rows or for D = 128 of 256, are at most four times those that the chip holds, and
   // a tile has at most best_parts of them.
   const int64_t rows = D == 128 ? 256 : 128, most = 4 * prompt_slots(D, rows) * rows;
