@@ -642,7 +642,8 @@ typedef struct lowbit_rope {
  * queries alone.
  * Several axes (time, height, width): each pair turns by one of them.
  * All of Q, K, Q_out, K_out 16-byte aligned, strides multiples of 8; freqs 8 bytes,
- * positions, pair_axis and weights 4.  tokens <= 2^30, q_heads, kv_heads <= 2^16.
+ * positions, pair_axis and weights 4.  tokens <= 2^30, q_heads, kv_heads <= 2^16,
+ * tokens * stride <= 2^46.
  * eps finite, >= 0.
  * Errors: E_NULL, E_UNSUPPORTED (types, head_dim, n_pairs, eps, overlaps),
  * E_SHAPE, E_ALIGN, E_HIP. */

@@ -75,3 +75,13 @@ def test_rows_against_bytes():
         r = rope(tokens=T, head_dim=8, n_pairs=4, positions=0x2000, freqs=0x3000, pos_stride=T)
         assert call(r=r, Q=at(0, 1 << 28), hq=hq, qs=64, K=at(0, 1 << 29), hk=hk, ks=64, Qo=P(q), qos=qos, Ko=P(k), kos=kos) == BAD
     assert refused > 500
+
+
+@pytest.mark.parametrize("name", ["qs", "ks", "qos", "kos"])
+def test_rows_that_no_memory_has(name):
+    """tokens * stride up to 2^46; the places of rows are counted in 64 bits."""
+    r = rope(tokens=1 << 30, positions=0x2000, freqs=0x3000, pos_stride=1 << 30)
+    strides = dict(qs=512, ks=512, qos=512, kos=512)
+    assert call(**{**FUSED, "r": r, **strides, name: (1 << 16) + 8}) == lb.E_SHAPE
+    # one less is looked at further: this address is misplaced
+    assert call(**{**FUSED, "r": r, "Qo": P(BASE + 8), "Ko": at(1 << 40), **strides, name: 1 << 16}) == lb.E_ALIGN

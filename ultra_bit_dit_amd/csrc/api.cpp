@@ -831,7 +831,10 @@ int lowbit_qk_norm_rope(const lowbit_rope* rope, int x_dtype, const void* Q, int
   const int64_t most = int64_t(1) << 40;
   if (r.n_axes > 1 && r.n_pairs != 0 && (r.pos_stride < r.tokens || r.pos_stride > most)) return LOWBIT_E_SHAPE;
   if (q_heads < 1 || q_heads > (1 << 16) || kv_heads < 0 || kv_heads > (1 << 16)) return LOWBIT_E_SHAPE;
-  auto bad_stride = [&](int64_t stride, int64_t heads) { return stride < heads * r.head_dim || stride > most; };
+  const int64_t far = (int64_t(1) << 46) / r.tokens;  // rows beyond that lie in no address space
+  auto bad_stride = [&](int64_t stride, int64_t heads) {
+    return stride < heads * r.head_dim || stride > most || (r.tokens > 1 && stride > far);
+  };
   if (bad_stride(q_stride, q_heads) || bad_stride(qo_stride, q_heads)) return LOWBIT_E_SHAPE;
   if (kv_heads && (bad_stride(k_stride, kv_heads) || bad_stride(ko_stride, kv_heads))) return LOWBIT_E_SHAPE;
   if (!aligned(Q, 16) || !aligned(Q_out, 16) || q_stride % 8 != 0 || qo_stride % 8 != 0) return LOWBIT_E_ALIGN;
